@@ -31,6 +31,7 @@ MB_AUTO, MB_ALGO, MB_TASK, MB_SEGMENT = 0, 1, 2, 3
 LINK_FIFO, LINK_DIRECT = 0, 1
 PROTO_SIMPLE, PROTO_LL = 0, 1
 ENGINE_PIPELINED, ENGINE_SEQUENTIAL = 0, 1
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_SILU = range(4)
 KIND_NAMES = ["copy", "reduce", "send", "recv", "rrc", "rcs", "fwd", "rrs", "rrcs", "copy_send", "copy2", "rrc2",
               "rrs3", "rrc3", "rrcs3", "rsend", "rcsend", "rrc3d", "reduce2", "copy3"]
 DTYPE_NAMES = {F32: "f32", BF16: "bf16", F16: "f16", I32: "i32"}
@@ -112,6 +113,34 @@ class TuneRow(ctypes.Structure):
     _fields_ = [("chunk_elems", ctypes.c_int64), ("best", PlanOpts), ("report", TuneReport)]
 
 
+class Linear(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("act", ctypes.c_int32), ("experts", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("x", ctypes.c_void_p), ("w", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("residual", ctypes.c_void_p), ("offsets", ctypes.c_void_p), ("y", ctypes.c_void_p),
+                ("z", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("ldw", ctypes.c_int64), ("ldr", ctypes.c_int64),
+                ("ldy", ctypes.c_int64), ("ldz", ctypes.c_int64), ("w_stride", ctypes.c_int64),
+                ("bias_stride", ctypes.c_int64)]
+
+
+class LinearGrad(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("act", ctypes.c_int32), ("experts", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("dy", ctypes.c_void_p), ("x", ctypes.c_void_p), ("w", ctypes.c_void_p), ("z", ctypes.c_void_p),
+                ("offsets", ctypes.c_void_p), ("dx", ctypes.c_void_p), ("dw", ctypes.c_void_p),
+                ("db", ctypes.c_void_p), ("lddy", ctypes.c_int64), ("ldx", ctypes.c_int64), ("ldw", ctypes.c_int64),
+                ("ldz", ctypes.c_int64), ("lddx", ctypes.c_int64), ("lddw", ctypes.c_int64),
+                ("w_stride", ctypes.c_int64), ("dw_stride", ctypes.c_int64), ("db_stride", ctypes.c_int64)]
+
+
+class Ortho(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("p", ctypes.c_int64), ("q", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("steps", ctypes.c_int32), ("a", ctypes.c_float),
+                ("b", ctypes.c_float), ("c", ctypes.c_float), ("eps", ctypes.c_float), ("scale", ctypes.c_float),
+                ("g", ctypes.c_void_p), ("out", ctypes.c_void_p), ("ldg", ctypes.c_int64), ("ldo", ctypes.c_int64),
+                ("g_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64)]
+
+
 PROBE_FN = ctypes.CFUNCTYPE(ctypes.c_double, ctypes.c_void_p, ctypes.POINTER(PlanOpts))
 
 
@@ -156,6 +185,13 @@ def _load():
         "ccl_schedule_write_json": [P, ctypes.c_char_p],
         "ccl_plan_codegen_source": [P, I64_, I32_, ctypes.POINTER(PlanOpts), ctypes.c_char_p, ctypes.c_size_t,
                                     ctypes.POINTER(ctypes.c_size_t), I32_, ctypes.POINTER(ctypes.c_int64)],
+        "ccl_linear_workspace": [ctypes.POINTER(Linear), ctypes.POINTER(I64_)],
+        "ccl_linear": [ctypes.POINTER(Linear), P, I64_, P],
+        "ccl_linear_grad_workspace": [ctypes.POINTER(LinearGrad), ctypes.POINTER(I64_)],
+        "ccl_linear_grad": [ctypes.POINTER(LinearGrad), P, I64_, P],
+        "ccl_orthogonalize_workspace": [ctypes.POINTER(Ortho), ctypes.POINTER(I64_)],
+        "ccl_orthogonalize": [ctypes.POINTER(Ortho), P, I64_, P],
+        "ccl_tensor_status": [],
         "ccl_schedule_read_json": [ctypes.c_char_p, ctypes.POINTER(P)],
     }
     for name, args in sig.items():
@@ -471,6 +507,190 @@ def tune_search(probe, start: PlanOpts | None = None, max_rounds=3, min_gain=0.0
     _check(lib.ccl_tune_search(ctypes.byref(start) if start is not None else None, ctypes.byref(to), cb, None,
                                ctypes.byref(best), ctypes.byref(bw), ctypes.byref(n)))
     return best, bw.value, n.value
+
+
+# ------------------------------------------------------- tensor products
+def _dtype_of(t):
+    import torch
+    codes = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
+    if t.dtype not in codes:
+        raise ValueError(f"unsupported tensor type {t.dtype}")
+    return codes[t.dtype]
+
+
+def _matrix(name, t, shape, like=None):
+    """Address and row stride of a CUDA matrix of this shape; (None, 0) for None."""
+    if t is None:
+        return None, 0
+    if not t.is_cuda:
+        raise ValueError(f"{name} is not a CUDA tensor")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+        raise ValueError(f"{name} is {t.dtype} on {t.device}, not {like.dtype} on {like.device}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} needs rows of consecutive elements")
+    if t.dim() > 1 and t.shape[-2] > 1 and t.stride(-2) < t.shape[-1]:
+        raise ValueError(f"{name} has overlapping rows (an expanded tensor: make it contiguous)")
+    return t.data_ptr(), (t.stride(-2) if t.dim() > 1 and t.shape[-2] > 1 else 0)
+
+
+def _stacked(name, t):
+    """Stride between the matrices of a stack (0: a single one)."""
+    if t is None or t.shape[0] <= 1:
+        return 0
+    if t.stride(0) < (t.shape[1] - 1) * t.stride(1) + (t.shape[2] if t.dim() > 2 else 1):
+        raise ValueError(f"{name} has overlapping matrices (an expanded tensor: make it contiguous)")
+    return t.stride(0)
+
+
+class _On:
+    """The stream a call runs on.  New tensors (outputs, workspaces) are
+    allocated while it is current, so the allocator ties them to it."""
+
+    def __init__(self, t, stream):
+        import torch
+        if not t.is_cuda:
+            raise ValueError("tensor products need CUDA tensors")
+        if t.device.index != torch.cuda.current_device():
+            raise ValueError(f"tensors on {t.device}, but device {torch.cuda.current_device()} is current")
+        self.ctx = None
+        if stream is None:
+            self.handle = torch.cuda.current_stream().cuda_stream
+            return
+        s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) and stream else stream
+        if isinstance(s, int):
+            s = torch.cuda.default_stream()
+        self.handle = s.cuda_stream
+        self.ctx = torch.cuda.stream(s)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _call(name, args, device, handle):
+    """Run a tensor product with the workspace it asks for."""
+    import torch
+    need = ctypes.c_int64()
+    _check(getattr(lib, name + "_workspace")(ctypes.byref(args), ctypes.byref(need)))
+    ws = torch.empty(need.value, dtype=torch.uint8, device=device) if need.value else None
+    _check(getattr(lib, name)(ctypes.byref(args), ws.data_ptr() if ws is not None else None, need.value, handle))
+
+
+def _offsets(offsets, w):
+    import torch
+    if offsets.dtype != torch.int32 or offsets.shape != (w.shape[0] + 1,) or not offsets.is_contiguous():
+        raise ValueError(f"offsets must be {w.shape[0] + 1} consecutive int32 (one more than experts)")
+    if offsets.device != w.device:
+        raise ValueError(f"offsets on {offsets.device}, not {w.device}")
+    return offsets.data_ptr()
+
+
+def _forward(x, w, offsets, bias, residual, act, preact, out, stream):
+    import torch
+    if x.dim() != 2 or w.dim() != (2 if offsets is None else 3):
+        raise ValueError("x must be rows x k and w n x k (experts x n x k with offsets)")
+    (rows, k), n = x.shape, w.shape[-2]
+    with _On(x, stream) as handle:
+        y = out if out is not None else torch.empty((rows, n), dtype=x.dtype, device=x.device)
+        z = torch.empty((rows, n), dtype=x.dtype, device=x.device) if preact else None
+        px, ldx = _matrix("x", x, (rows, k))
+        pw, ldw = _matrix("w", w, (*w.shape[:-2], n, k), x)
+        pb, _ = _matrix("bias", bias, (*w.shape[:-2], n), x)
+        pr, ldr = _matrix("residual", residual, (rows, n), x)
+        py, ldy = _matrix("out", y, (rows, n), x)
+        pz, ldz = _matrix("z", z, (rows, n), x)
+        grouped = offsets is not None
+        a = Linear(rows, n, k, _dtype_of(x), act, w.shape[0] if grouped else 0, 0, px, pw, pb, pr,
+                   _offsets(offsets, w) if grouped else None, py, pz, ldx, ldw, ldr, ldy, ldz,
+                   _stacked("w", w) if grouped else 0,
+                   bias.stride(0) if grouped and bias is not None and bias.shape[0] > 1 else 0)
+        _call("ccl_linear", a, x.device, handle)
+    return (y, z) if preact else y
+
+
+def _backward(dy, x, w, offsets, preact, act, bias, need_dx, need_dw, stream):
+    import torch
+    if x.dim() != 2 or w.dim() != (2 if offsets is None else 3):
+        raise ValueError("x must be rows x k and w n x k (experts x n x k with offsets)")
+    (rows, k), n = x.shape, w.shape[-2]
+    if act != ACT_NONE and preact is None:
+        raise ValueError("the gradient of an activation needs the pre-activation kept by the forward pass")
+    with _On(x, stream) as handle:
+        new = dict(dtype=x.dtype, device=x.device)
+        dx = torch.empty((rows, k), **new) if need_dx else None
+        dw = torch.empty((*w.shape[:-2], n, k), **new) if need_dw else None
+        db = torch.empty((*w.shape[:-2], n), **new) if bias else None
+        pdy, lddy = _matrix("dy", dy, (rows, n), x)
+        px, ldx = _matrix("x", x, (rows, k))
+        pw, ldw = _matrix("w", w, (*w.shape[:-2], n, k), x)
+        pz, ldz = _matrix("preact", preact if act != ACT_NONE else None, (rows, n), x)
+        grouped = offsets is not None
+        ptr = [t.data_ptr() if t is not None else None for t in (dx, dw, db)]
+        a = LinearGrad(rows, n, k, _dtype_of(x), act, w.shape[0] if grouped else 0, 0, pdy, px, pw, pz,
+                       _offsets(offsets, w) if grouped else None, *ptr, lddy, ldx, ldw, ldz, 0, 0,
+                       _stacked("w", w) if grouped else 0, 0, 0)
+        _call("ccl_linear_grad", a, x.device, handle)
+    return dx, dw, db
+
+
+def linear(x, w, bias=None, residual=None, act=ACT_NONE, preact=False, out=None, stream=None):
+    """act(x w^T + bias) + residual (``ccl_linear``) for x (rows, k) and w
+    (n, k), bf16 or f16.  With ``preact`` also the values before the
+    activation, which ``linear_backward`` needs: (y, z)."""
+    return _forward(x, w, None, bias, residual, act, preact, out, stream)
+
+
+def linear_backward(dy, x, w, preact=None, act=ACT_NONE, bias=False, need_dx=True, need_dw=True, stream=None):
+    """(dx, dw, db) of ``linear`` (``ccl_linear_grad``); an output that is not
+    asked for is None.  The residual's gradient is dy itself."""
+    return _backward(dy, x, w, None, preact, act, bias, need_dx, need_dw, stream)
+
+
+def grouped_linear(x, w, offsets, bias=None, act=ACT_NONE, preact=False, out=None, stream=None):
+    """``linear`` with a weight (and bias) per expert: w (experts, n, k), rows
+    of x sorted by expert, rows offsets[e] .. offsets[e + 1] - 1 (int32, on the
+    device) for expert e.  Rows that no expert owns are not written."""
+    return _forward(x, w, offsets, bias, None, act, preact, out, stream)
+
+
+def grouped_linear_backward(dy, x, w, offsets, preact=None, act=ACT_NONE, bias=False, need_dx=True, need_dw=True,
+                            stream=None):
+    """(dx, dw, db) of ``grouped_linear``; experts without rows get zeros."""
+    return _backward(dy, x, w, offsets, preact, act, bias, need_dx, need_dw, stream)
+
+
+def orthogonalize(g, steps=5, coeffs=(3.4445, -4.7750, 2.0315), eps=1e-7, scale=1.0, out=None, stream=None):
+    """Newton-Schulz orthogonalisation of a gradient matrix (p, q) or a stack
+    (batch, p, q) of them, f32, bf16 or f16 (``ccl_orthogonalize``).  The
+    update is bf16 unless ``out`` is a given f16 matrix."""
+    import torch
+    if g.dim() not in (2, 3):
+        raise ValueError("g must be a matrix or a stack of matrices")
+    a, b, c = coeffs
+    with _On(g, stream) as handle:
+        if out is None:
+            out = torch.empty(g.shape, dtype=torch.bfloat16, device=g.device)
+        pg, ldg = _matrix("g", g, g.shape)
+        po, ldo = _matrix("out", out, g.shape)
+        stack = g.dim() == 3
+        args = Ortho(g.shape[0] if stack else 1, g.shape[-2], g.shape[-1], _dtype_of(g), _dtype_of(out), steps, a, b,
+                     c, eps, scale, pg, po, ldg, ldo, _stacked("g", g) if stack else 0,
+                     _stacked("out", out) if stack else 0)
+        _call("ccl_orthogonalize", args, g.device, handle)
+    return out
+
+
+def tensor_status():
+    """Raise what went wrong inside the tensor products launched since the
+    last call (``ccl_tensor_status``; synchronizes the device)."""
+    _check(lib.ccl_tensor_status())
 
 
 def version() -> str:

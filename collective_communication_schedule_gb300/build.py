@@ -17,11 +17,11 @@ LIB = os.path.join(HERE, "libccl.so")
 ROOT = os.path.dirname(HERE)
 INCLUDE = os.path.join(ROOT, "include")
 
-SOURCES = ["ccl_runtime.cu", "ccl_static.cu", "ccl_compiler.cpp", "ccl_builtin.cpp", "ccl_planner.cpp",
-           "ccl_tuner.cpp", "ccl_persist.cpp", "ccl_codegen.cpp"]
+SOURCES = ["ccl_runtime.cu", "ccl_static.cu", "ccl_tensor.cu", "ccl_compiler.cpp", "ccl_builtin.cpp",
+           "ccl_planner.cpp", "ccl_tuner.cpp", "ccl_persist.cpp", "ccl_codegen.cpp"]
 # device headers the run-time compiler of generated kernels receives as text
 EMBEDDED = ["ccl_layout.h", "ccl_core.cuh"]
-HEADERS = ["ccl_internal.h", "ccl_plan.h", "ccl_layout.h", "ccl_core.cuh"]
+HEADERS = ["ccl_internal.h", "ccl_plan.h", "ccl_layout.h", "ccl_core.cuh", "ccl_tensor.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",

@@ -1,0 +1,1161 @@
+// Tensor products of language-model layers: dense products with a fused
+// epilogue, products grouped by expert over ragged rows, and the
+// Newton-Schulz orthogonalisation of gradient matrices.  C ABI in
+// include/ccl.h; PTX building blocks in ccl_tensor.cuh.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <mutex>
+#include <string>
+
+#include <cuda_runtime.h>
+
+#include "ccl_internal.h"
+#include "ccl_tensor.cuh"
+
+namespace ccl {
+namespace tensor {
+
+// ======================================================================
+// The product kernel
+//
+//   out[n, m] = act(alpha * sum_k A[m, k] B[n, k] + bias[m]) + beta * C[n, m]
+//
+// m runs along the contiguous axis of the output (features), n along its
+// rows (tokens), so a thread that owns accumulator lane m writes neighbours
+// of its warp's other lanes.  A and B are 16-bit matrices in either storage
+// order; a leading index g selects the matrix of a batch or an expert.
+// Ragged forms: RAGGED_ROWS (rows n of all experts in one matrix, offsets
+// give every expert's range) and RAGGED_REDUCE (the reduction runs over an
+// expert's rows).
+//
+// A threadblock owns one output tile at a time: 128 features x bn rows.
+// Warp 0 streams 64-wide slices of the reduction axis into a ring of
+// shared-memory stages with TMA, warp 1 issues tcgen05 matrix instructions
+// into one of two accumulators in tensor memory, warps 4..7 drain the other
+// one through the epilogue, so that an epilogue costs nothing as long as it
+// is shorter than the next tile's products.
+// ======================================================================
+constexpr int kTileM = 128;
+constexpr int kSliceK = 64;
+constexpr int kMaxStages = 12;
+constexpr int kMaxGroups = 1024;
+constexpr int kThreads = 256;
+constexpr int kStagePitch = 36;                 // floats; rows 4 banks apart: conflict-free 16-byte reads
+constexpr int kStagingBytes = 4 * 32 * kStagePitch * 4;
+constexpr int kSmemBudget = 227 * 1024 - 6 * 1024;   // dynamic part; the rest is static
+
+enum { DENSE = 0, RAGGED_ROWS = 1, RAGGED_REDUCE = 2 };
+
+struct Product {
+    CUtensorMap ma, mb;
+    uint16_t *out, *pre;           // pre: the sum before the activation (may be null)
+    const uint16_t *c, *bias;
+    const float *alpha_of, *beta_of;   // device factors per batch entry (may be null)
+    const int32_t* offsets;
+    int64_t ld_out, bs_out, ld_pre, ld_c, bs_c, bs_bias;
+    float alpha, beta;
+    int32_t m, n, k, groups;
+    int32_t bn, stages, tiles_m, tiles_n;
+    int32_t ragged, symmetric, act;
+    int32_t in_bf, out_bf, a_mn, b_mn;
+    int32_t vec_out, vec_pre, vec_c, vec_bias;
+};
+
+// [0]: a ccl_status_t of a failed launch on this device, 0 if none
+__device__ int g_status[4];
+
+struct TileAt {
+    int g, za, zb;          // group, and its index in the operand maps
+    int m0, n0;             // first feature, first row within the group
+    int rows;               // rows of the group (n)
+    int row0;               // row of the group's first row in the matrices
+    int k0, klen;           // reduction range
+};
+
+struct Shared {
+    uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
+    uint32_t tmem;
+    int failed;
+    int total;
+    int seg_end[kMaxGroups];
+};
+
+__device__ __forceinline__ void group_range(const Product& P, int g, int limit, int& lo, int& len)
+{
+    lo = min(max(P.offsets[g], 0), limit);
+    len = min(max(P.offsets[g + 1], lo), limit) - lo;
+}
+
+// Tiles of a segment: all tiles of an expert (ragged rows), or the tiles of
+// one column of tiles that touch the lower triangle (symmetric outputs).
+__device__ __forceinline__ int segment_tiles(const Product& P, int s)
+{
+    if (P.symmetric) return P.tiles_n - s * kTileM / P.bn;
+    int lo, len;
+    group_range(P, s, P.n, lo, len);
+    return P.tiles_m * ((len + P.bn - 1) / P.bn);
+}
+
+__device__ __forceinline__ int find_segment(const Shared* sh, int n, int t)
+{
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (t < sh->seg_end[mid])
+            hi = mid;
+        else
+            lo = mid + 1;
+    }
+    return lo;
+}
+
+__device__ __forceinline__ TileAt tile_at(const Product& P, const Shared* sh, int t)
+{
+    TileAt q;
+    q.row0 = 0;
+    q.rows = P.n;
+    q.k0 = 0;
+    q.klen = P.k;
+    if (P.ragged == RAGGED_ROWS) {
+        q.g = find_segment(sh, P.groups, t);
+        const int l = t - (q.g ? sh->seg_end[q.g - 1] : 0);
+        group_range(P, q.g, P.n, q.row0, q.rows);
+        // an expert's row tiles of one feature tile are neighbours: they share its weights
+        const int tn = (q.rows + P.bn - 1) / P.bn;
+        q.m0 = l / tn * kTileM;
+        q.n0 = l % tn * P.bn;
+        q.za = q.g;
+        q.zb = 0;
+        return q;
+    }
+    if (P.symmetric) {
+        const int per = sh->seg_end[P.tiles_m - 1];
+        q.g = t / per;
+        const int l = t % per, s = find_segment(sh, P.tiles_m, l);
+        q.m0 = s * kTileM;
+        q.n0 = (s * kTileM / P.bn + l - (s ? sh->seg_end[s - 1] : 0)) * P.bn;
+    } else {
+        // bands of 16 feature tiles, row tiles inside: the tiles in flight
+        // at one time form a compact block of the output
+        const int per = P.tiles_m * P.tiles_n;
+        q.g = t / per;
+        const int l = t % per, band = l / (16 * P.tiles_n), r = l % (16 * P.tiles_n);
+        const int width = min(16, P.tiles_m - band * 16);
+        q.m0 = (band * 16 + r % width) * kTileM;
+        q.n0 = r / width * P.bn;
+    }
+    q.za = q.zb = q.g;
+    if (P.ragged == RAGGED_REDUCE) {
+        group_range(P, q.g, P.k, q.k0, q.klen);
+        q.za = q.zb = 0;
+    }
+    return q;
+}
+
+// 32 rows x 32 features, staged as st[row][feature], through the epilogue
+// into global memory; 8 features per thread and step.  side: 0 = every
+// element; 1 = only feature <= row (the tile of a symmetric output), -1 =
+// only feature > row (its mirror image), so that each element is written
+// once and the result is symmetric bit for bit.
+__device__ __forceinline__ void write_block(const Product& P, const float* st, int lane, int g, int64_t row, int nrows,
+                                            int feat, int nfeat, int side, float alpha, float beta)
+{
+#pragma unroll
+    for (int pass = 0; pass < 4; ++pass) {
+        const int r = pass * 8 + (lane >> 2), c = (lane & 3) * 8, f = feat + c;
+        const int64_t n = row + r;
+        int lo = 0, hi = min(8, nfeat - c);
+        if (side > 0) hi = (int)min((int64_t)hi, n - f + 1);
+        if (side < 0) lo = (int)max((int64_t)0, n - f + 1);
+        if (r >= nrows || lo >= hi) continue;
+        float v[8], w[8];
+        const float4 a = *reinterpret_cast<const float4*>(st + r * kStagePitch + c);
+        const float4 b = *reinterpret_cast<const float4*>(st + r * kStagePitch + c + 4);
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= alpha;
+        if (P.bias) {
+            load8(P.bias + g * P.bs_bias + f, P.in_bf, P.vec_bias, lo, hi, w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += w[i];
+        }
+        if (P.pre) store8(P.pre + n * P.ld_pre + f, P.in_bf, P.vec_pre, lo, hi, v);
+        if (P.act) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = activate(v[i], P.act);
+        }
+        if (P.c) {
+            load8(P.c + g * P.bs_c + n * P.ld_c + f, P.in_bf, P.vec_c, lo, hi, w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += beta * w[i];
+        }
+        store8(P.out + g * P.bs_out + n * P.ld_out + f, P.out_bf, P.vec_out, lo, hi, v);
+    }
+}
+
+__global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ Product P)
+{
+    __shared__ __align__(8) Shared sh;
+    extern __shared__ unsigned char raw[];
+    unsigned char* dyn = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t bytes_a = kTileM * kSliceK * 2, bytes_b = P.bn * kSliceK * 2, bytes = bytes_a + bytes_b;
+    float* staging = reinterpret_cast<float*>(dyn + (size_t)P.stages * bytes);
+    uint32_t tcols = 64;
+    while (tcols < 2u * P.bn) tcols *= 2;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < P.stages; ++i) {
+            bar_init(smem_addr(&sh.full[i]), 1);
+            bar_init(smem_addr(&sh.empty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            bar_init(smem_addr(&sh.acc_full[i]), 1);
+            bar_init(smem_addr(&sh.acc_empty[i]), 4);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        sh.failed = 0;
+        tma_prefetch(&P.ma);
+        tma_prefetch(&P.mb);
+    }
+    if (warp == 2) tmem_alloc(smem_addr(&sh.tmem), tcols);
+    wait_for_previous();
+    const int nseg = P.ragged == RAGGED_ROWS ? P.groups : P.symmetric ? P.tiles_m : 0;
+    for (int s = threadIdx.x; s < nseg; s += kThreads) sh.seg_end[s] = segment_tiles(P, s);
+    if (P.offsets && blockIdx.x == 0) {
+        const int limit = P.ragged == RAGGED_ROWS ? P.n : P.k;
+        for (int s = threadIdx.x; s < P.groups; s += kThreads)
+            if (P.offsets[s] < 0 || P.offsets[s + 1] < P.offsets[s] || P.offsets[s + 1] > limit)
+                atomicCAS(&g_status[0], 0, (int)CCL_ERR_INVALID_ARG);
+    }
+    __syncthreads();
+    if (nseg && warp == 0) {
+        int base = 0;
+        for (int s = 0; s < nseg; s += 32) {
+            int v = s + lane < nseg ? sh.seg_end[s + lane] : 0;
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {
+                const int u = __shfl_up_sync(~0u, v, d);
+                if (lane >= d) v += u;
+            }
+            if (s + lane < nseg) sh.seg_end[s + lane] = base + v;
+            base += __shfl_sync(~0u, v, 31);
+        }
+        if (lane == 0) sh.total = P.symmetric ? base * P.groups : base;
+    } else if (!nseg && threadIdx.x == 0) {
+        sh.total = P.tiles_m * P.tiles_n * P.groups;
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const int total = sh.total;
+    const uint32_t tmem = sh.tmem;
+    volatile int* failed = &sh.failed;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int it = 0;
+            for (int t = blockIdx.x; t < total; t += gridDim.x) {
+                const TileAt q = tile_at(P, &sh, t);
+                for (int k = 0; k < q.klen; k += kSliceK, ++it) {
+                    const int s = it % P.stages;
+                    if (!bar_wait(smem_addr(&sh.empty[s]), ((it / P.stages) & 1) ^ 1, failed)) goto drain;
+                    const uint32_t bar = smem_addr(&sh.full[s]);
+                    const uint32_t a = smem_addr(dyn + (size_t)s * bytes), b = a + bytes_a;
+                    bar_expect(bar, bytes);
+                    if (P.a_mn) {
+                        tma_load(a, &P.ma, bar, q.m0, q.k0 + k, q.za);
+                        tma_load(a + kSliceK * 128, &P.ma, bar, q.m0 + 64, q.k0 + k, q.za);
+                    } else {
+                        tma_load(a, &P.ma, bar, k, q.m0, q.za);
+                    }
+                    if (P.b_mn) {
+                        for (int i = 0; i < P.bn; i += 64)
+                            tma_load(b + i * 128, &P.mb, bar, q.n0 + i, q.k0 + k, q.zb);
+                    } else {
+                        tma_load(b, &P.mb, bar, k, q.row0 + q.n0, q.zb);
+                    }
+                }
+            }
+        drain:
+            // copies in flight write this threadblock's shared memory: see
+            // the last one of every stage land before leaving
+            int none = 0;
+            for (int i = max(0, it - P.stages); i < it; ++i)
+                bar_wait(smem_addr(&sh.full[i % P.stages]), (i / P.stages) & 1, &none);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        const uint32_t idesc = mma_desc(P.in_bf, P.a_mn, P.b_mn, kTileM, P.bn);
+        const uint32_t lead = kSliceK * 128, step_a = P.a_mn ? 2048 : 32, step_b = P.b_mn ? 2048 : 32;
+        int it = 0, done = 0;
+        bool ok = true;
+        for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
+            const TileAt q = tile_at(P, &sh, t);
+            if (q.klen <= 0) continue;
+            const int acc = done & 1;
+            ok = __all_sync(~0u, bar_wait(smem_addr(&sh.acc_empty[acc]), ((done >> 1) & 1) ^ 1, failed));
+            if (!ok) break;
+            fence_after();
+            for (int k = 0; k < q.klen; k += kSliceK, ++it) {
+                const int s = it % P.stages;
+                ok = __all_sync(~0u, bar_wait(smem_addr(&sh.full[s]), (it / P.stages) & 1, failed));
+                if (!ok) break;
+                const uint32_t a = smem_addr(dyn + (size_t)s * bytes), b = a + bytes_a;
+                if (P.ragged == RAGGED_REDUCE && q.klen - k < kSliceK) {
+                    // the slice runs into the next expert's rows: zero them in
+                    // both operands (0 x Inf or NaN would not be 0)
+                    const int live = q.klen - k, dead = kSliceK - live;
+                    const int blocks = (kTileM + P.bn) / 64;
+                    for (int i = lane; i < blocks * dead * 8; i += 32) {
+                        const int blk = i / (dead * 8), o = i % (dead * 8);
+                        *reinterpret_cast<uint4*>(dyn + (size_t)s * bytes + blk * (kSliceK * 128) + live * 128 + o * 16) =
+                            make_uint4(0, 0, 0, 0);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                }
+                if (lane == 0) {
+                    fence_after();
+#pragma unroll
+                    for (int j = 0; j < kSliceK / 16; ++j)
+                        mma_f16(tmem + acc * P.bn, operand_desc(a + j * step_a, lead, 1024),
+                                operand_desc(b + j * step_b, lead, 1024), idesc, k > 0 || j > 0);
+                    mma_commit(smem_addr(&sh.empty[s]));
+                }
+                __syncwarp();
+            }
+            if (!ok) break;
+            if (lane == 0) mma_commit(smem_addr(&sh.acc_full[acc]));
+            __syncwarp();
+            ++done;
+        }
+        if (!ok && lane == 0 && it > 0) {
+            // matrix instructions still in flight read shared memory and
+            // write tensor memory: wait (bounded) until all have finished
+            int none = 0;
+            const int s = (it - 1) % P.stages;
+            bar_wait(smem_addr(&sh.empty[s]), ((it - 1) / P.stages) & 1, &none);
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        const int quad = warp & 3;
+        float* st = staging + quad * 32 * kStagePitch;
+        int done = 0;
+        for (int t = blockIdx.x; t < total; t += gridDim.x) {
+            const TileAt q = tile_at(P, &sh, t);
+            const bool some = q.klen > 0;
+            const int acc = done & 1;
+            if (some) {
+                if (!__all_sync(~0u, bar_wait(smem_addr(&sh.acc_full[acc]), (done >> 1) & 1, failed))) break;
+                fence_after();
+            }
+            const float alpha = P.alpha * (P.alpha_of ? P.alpha_of[q.g] : 1.f);
+            const float beta = P.beta * (P.beta_of ? P.beta_of[q.g] : 1.f);
+            const int live = min(P.bn, q.rows - q.n0), feat = q.m0 + quad * 32;
+            for (int c = 0; c < live; c += 32) {
+                float v[32];
+                if (some) {
+                    tmem_load32(tmem + ((uint32_t)(quad * 32) << 16) + acc * P.bn + c, v);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = 0.f;
+                }
+#pragma unroll
+                for (int i = 0; i < 32; ++i) st[i * kStagePitch + lane] = v[i];
+                __syncwarp();
+                write_block(P, st, lane, q.g, (int64_t)q.row0 + q.n0 + c, min(32, live - c), feat, P.m - feat,
+                            P.symmetric ? 1 : 0, alpha, beta);
+                __syncwarp();
+                if (P.symmetric && q.n0 + c + 31 > feat) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) st[lane * kStagePitch + i] = v[i];
+                    __syncwarp();
+                    write_block(P, st, lane, q.g, feat, min(32, P.m - feat), q.n0 + c, live - c, -1, alpha, beta);
+                    __syncwarp();
+                }
+            }
+            if (some) {
+                fence_before();
+                if (lane == 0) bar_arrive(smem_addr(&sh.acc_empty[acc]));
+                ++done;
+            }
+        }
+        fence_before();
+    }
+    __syncthreads();
+    if (sh.failed && threadIdx.x == 0) atomicCAS(&g_status[0], 0, (int)CCL_ERR_TIMEOUT);
+    if (warp == 2) {
+        fence_after();
+        tmem_free(tmem, tcols);
+    }
+}
+
+// ======================================================================
+// Elementwise passes
+// ======================================================================
+
+// dz = dy * act'(z), and the column sums of dz that make the bias gradient.
+// A threadblock takes 256 columns of up to kGradRows rows of one expert
+// (dense: one expert with all rows); 32 threads cover the columns, 8 each,
+// and 8 groups of threads take the rows in turn.  The sums go, in 32 bits
+// and a fixed order, to partial[chunk][column]; bias_grad_kernel adds an
+// expert's chunks up in order.  Chunks of expert e start at
+// offsets[e] / kGradRows + e, which leaves every expert room for its rows.
+constexpr int kGradRows = 64;
+
+struct GradPass {
+    const uint16_t *dy, *z;
+    uint16_t* dz;                  // may be null (sums only)
+    float* partial;                // may be null (no bias gradient)
+    uint16_t* db;
+    const int32_t* offsets;        // null: one expert with all rows
+    int64_t ld_dy, ld_z, ld_dz, bs_db;
+    int64_t ld_part;
+    int32_t rows, n, groups, act, bf, vec;
+};
+
+__device__ __forceinline__ int64_t chunk_base(const GradPass& G, int e, int lo) { return lo / kGradRows + e; }
+
+__device__ __forceinline__ void grad_range(const GradPass& G, int e, int& lo, int& len)
+{
+    lo = 0;
+    len = G.rows;
+    if (G.offsets) {
+        lo = min(max(G.offsets[e], 0), G.rows);
+        len = min(max(G.offsets[e + 1], lo), G.rows) - lo;
+    }
+}
+
+__global__ void __launch_bounds__(256) act_grad_kernel(const GradPass G)
+{
+    __shared__ float sums[8][256 + 8];
+    wait_for_previous();
+    // the last expert whose first chunk is at or before this one (first chunks strictly increase)
+    const int chunk = blockIdx.x;
+    int e = 0, lo, len;
+    if (G.offsets) {
+        int a = 0, b = G.groups - 1;
+        while (a < b) {
+            const int mid = (a + b + 1) >> 1;
+            grad_range(G, mid, lo, len);
+            if (chunk_base(G, mid, lo) <= chunk)
+                a = mid;
+            else
+                b = mid - 1;
+        }
+        e = a;
+    }
+    grad_range(G, e, lo, len);
+    const int64_t first = (chunk - chunk_base(G, e, lo)) * kGradRows;
+    if (first < 0 || first >= len) return;
+    const int nrows = (int)min((int64_t)kGradRows, len - first);
+    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+    const int col = blockIdx.y * 256 + tx * 8;
+    const int hi = min(8, G.n - col);
+    float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (hi > 0) {
+        for (int r = ty; r < nrows; r += 8) {
+            const int64_t row = lo + first + r;
+            float v[8];
+            load8(G.dy + row * G.ld_dy + col, G.bf, G.vec & 1, 0, hi, v);
+            if (G.act) {
+                float z[8];
+                load8(G.z + row * G.ld_z + col, G.bf, G.vec & 2, 0, hi, z);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] *= activate_grad(z[i], G.act);
+            }
+            if (G.dz) store8(G.dz + row * G.ld_dz + col, G.bf, G.vec & 4, 0, hi, v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum[i] += v[i];
+        }
+    }
+    if (!G.partial) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sums[ty][tx * 8 + i] = sum[i];
+    __syncthreads();
+    const int c = blockIdx.y * 256 + threadIdx.x;
+    if (c < G.n) {
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += sums[i][threadIdx.x];
+        G.partial[(int64_t)chunk * G.ld_part + c] = s;
+    }
+}
+
+__global__ void __launch_bounds__(256) bias_grad_kernel(const GradPass G)
+{
+    wait_for_previous();
+    const int e = blockIdx.y, c = blockIdx.x * 256 + threadIdx.x;
+    if (c >= G.n) return;
+    int lo, len;
+    grad_range(G, e, lo, len);
+    const float* p = G.partial + chunk_base(G, e, lo) * G.ld_part + c;
+    float s = 0.f;
+    for (int i = 0; i < len; i += kGradRows, p += G.ld_part) s += *p;
+    store1(G.db + e * G.bs_db + c, s, G.bf);
+}
+
+// ---------------------------------------------- orthogonalisation passes
+// The iteration keeps x, A and B in f16: 11 bits instead of bf16's 8, at the
+// same matrix rate, and their range is known (singular values of x stay
+// near 1), so fixed powers of two keep the entries clear of both ends.
+constexpr float kScaleX = 4096.f, kScaleA = 1024.f;
+constexpr int kNormBlocks = 64;
+
+struct NormPass {
+    const void* g;
+    __half* x;
+    float *partial, *kappa, *kappa2;
+    int64_t ld_g, bs_g, ld_x, bs_x;
+    int32_t p, q, type;
+    float eps;
+};
+
+__device__ __forceinline__ float load_any(const void* p, int64_t i, int type)
+{
+    if (type == CCL_F32) return ((const float*)p)[i];
+    return load1((const uint16_t*)p + i, type == CCL_BF16);
+}
+
+__device__ __forceinline__ float block_sum(float v, float* sm)
+{
+#pragma unroll
+    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(~0u, v, d);
+    if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
+    __syncthreads();
+    float s = 0.f;
+    for (int i = 0; i < (int)blockDim.x / 32; ++i) s += sm[i];
+    return s;
+}
+
+__global__ void __launch_bounds__(256) norm_kernel(const NormPass N)
+{
+    __shared__ float sm[8];
+    wait_for_previous();
+    float s = 0.f;
+    for (int r = blockIdx.x; r < N.p; r += gridDim.x) {
+        const int64_t base = blockIdx.y * N.bs_g + r * N.ld_g;
+        float line = 0.f;
+        for (int c = threadIdx.x; c < N.q; c += 256) {
+            const float v = load_any(N.g, base + c, N.type);
+            line += v * v;
+        }
+        s += line;
+    }
+    s = block_sum(s, sm);
+    if (threadIdx.x == 0) N.partial[blockIdx.y * kNormBlocks + blockIdx.x] = s;
+}
+
+// x0 = g * 2^e in f16 (exact for bf16 gradients) with the power of two that
+// brings the norm to kScaleX / 2 .. kScaleX; the remaining factor kappa of
+// x0 = kScaleX * g / (norm + eps) is applied in 32 bits by the epilogues of
+// the first step.
+__global__ void __launch_bounds__(256) scale_kernel(const NormPass N)
+{
+    wait_for_previous();
+    float s = 0.f;
+    for (int i = 0; i < kNormBlocks; ++i) s += N.partial[blockIdx.y * kNormBlocks + i];
+    const float norm = sqrtf(s);
+    int e = 0;
+    if (norm > 0.f && norm <= 3.4e38f) {
+        int x;
+        frexpf(norm, &x);            // norm in [2^(x-1), 2^x)
+        e = 12 - x;                  // kScaleX = 2^12
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        const float kappa = ldexpf(1.f, 12 - e) / (norm + N.eps);
+        N.kappa[blockIdx.y] = kappa;
+        N.kappa2[blockIdx.y] = kappa * kappa;
+    }
+    for (int r = blockIdx.x; r < N.p; r += gridDim.x) {
+        const int64_t base = blockIdx.y * N.bs_g + r * N.ld_g;
+        __half* d = N.x + blockIdx.y * N.bs_x + r * N.ld_x;
+        for (int c = threadIdx.x; c < N.q; c += 256) d[c] = __float2half_rn(ldexpf(load_any(N.g, base + c, N.type), e));
+    }
+}
+
+// ======================================================================
+// Host side
+// ======================================================================
+#define TRY_CUDA(call, what)                                                                                   \
+    do {                                                                                                       \
+        cudaError_t e_ = (call);                                                                               \
+        if (e_ != cudaSuccess)                                                                                 \
+            return fail(e_ == cudaErrorMemoryAllocation ? CCL_ERR_OOM : CCL_ERR_CUDA,                          \
+                        std::string(what) + ": " + cudaGetErrorString(e_));                                    \
+    } while (0)
+#define TRY(call)                                 \
+    do {                                          \
+        ccl_status_t s_ = (call);                 \
+        if (s_ != CCL_OK) return s_;              \
+    } while (0)
+
+static int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
+static bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                             const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// What the launches need to know of a device, looked up once per device.
+struct Device {
+    bool ready = false;
+    int sms = 0;
+    EncodeFn encode = nullptr;
+};
+
+static ccl_status_t device(const Device** out)
+{
+    static std::mutex mu;
+    static Device all[64];
+    int d = 0;
+    TRY_CUDA(cudaGetDevice(&d), "cudaGetDevice");
+    if (d < 0 || d >= 64) return fail(CCL_ERR_UNSUPPORTED, "device index above 63");
+    std::lock_guard<std::mutex> lock(mu);
+    if (!all[d].ready) {
+        TRY_CUDA(cudaDeviceGetAttribute(&all[d].sms, cudaDevAttrMultiProcessorCount, d), "SM count");
+        void* fn = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        TRY_CUDA(cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q),
+                 "cuTensorMapEncodeTiled");
+        if (q != cudaDriverEntryPointSuccess || !fn) return fail(CCL_ERR_CUDA, "the driver has no tensor maps");
+        all[d].encode = (EncodeFn)fn;
+        TRY_CUDA(cudaFuncSetAttribute(product_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBudget),
+                 "shared memory of the product kernel");
+        all[d].ready = true;
+    }
+    *out = &all[d];
+    return CCL_OK;
+}
+
+template <typename Arg>
+static ccl_status_t launch(void (*kernel)(Arg), dim3 grid, int threads, size_t smem, cudaStream_t stream, const Arg& arg)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    TRY_CUDA(cudaLaunchKernelEx(&cfg, kernel, arg), "launch");
+    return CCL_OK;
+}
+
+// A 16-bit matrix (or a stack of them): rows of `cols` consecutive elements.
+struct Matrix {
+    const void* p = nullptr;
+    int64_t rows = 0, cols = 0, ld = 0, count = 1, stride = 0;
+    bool loadable() const
+    {
+        return aligned16(p) && ld % 8 == 0 && (count <= 1 || stride % 8 == 0);
+    }
+    int64_t packed_ld() const { return round_up(cols, 8); }
+    int64_t packed_bytes() const { return loadable() ? 0 : round_up(count * rows * packed_ld() * 2, 256); }
+};
+
+// Bump allocation from the caller's workspace (a null base only measures).
+struct Arena {
+    char* base;
+    int64_t used = 0;
+    template <typename T>
+    T* take(int64_t bytes)
+    {
+        T* p = base ? reinterpret_cast<T*>(base + used) : nullptr;
+        used += round_up(bytes, 256);
+        return p;
+    }
+};
+
+struct PackArgs {
+    uint16_t* dst;
+    const uint16_t* src;
+    int64_t ld_dst, bs_dst, ld_src, bs_src, rows, cols;
+};
+// Copy a matrix whose base or row stride TMA cannot address (not a multiple
+// of 16 bytes) into rows padded to 8 elements.
+__global__ void __launch_bounds__(256) pack_rows_kernel(const PackArgs a)
+{
+    wait_for_previous();
+    for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+        const uint16_t* s = a.src + blockIdx.y * a.bs_src + r * a.ld_src;
+        uint16_t* d = a.dst + blockIdx.y * a.bs_dst + r * a.ld_dst;
+        for (int64_t i = threadIdx.x; i < a.cols; i += blockDim.x) d[i] = s[i];
+    }
+}
+
+// The matrix itself, or a copy in the workspace that TMA can address.
+static ccl_status_t loadable(Matrix* m, Arena* ws, cudaStream_t stream)
+{
+    if (m->loadable()) return CCL_OK;
+    uint16_t* d = ws->take<uint16_t>(m->packed_bytes());
+    PackArgs a = {d, (const uint16_t*)m->p, m->packed_ld(), m->rows * m->packed_ld(), m->ld, m->stride, m->rows, m->cols};
+    m->p = d;
+    m->ld = a.ld_dst;
+    m->stride = a.bs_dst;
+    if (!ws->base) return CCL_OK;
+    return launch(pack_rows_kernel, dim3((unsigned)std::min<int64_t>(a.rows, 4096), (unsigned)m->count), 256, 0, stream, a);
+}
+
+static ccl_status_t encode(const Device* dev, CUtensorMap* map, const Matrix& m, int box_cols, int box_rows)
+{
+    const cuuint64_t dims[3] = {(cuuint64_t)m.cols, (cuuint64_t)m.rows, (cuuint64_t)m.count};
+    const cuuint64_t strides[2] = {(cuuint64_t)m.ld * 2, (cuuint64_t)(m.count > 1 ? m.stride : m.ld * m.rows) * 2};
+    const cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1};
+    const cuuint32_t unit[3] = {1, 1, 1};
+    const CUresult r = dev->encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(m.p), dims, strides, box,
+                                   unit, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(CCL_ERR_INVALID_ARG, "a matrix cannot be described to TMA (size or stride)");
+    return CCL_OK;
+}
+
+// Complete a product (operands, tile, stages) and launch it.
+static ccl_status_t run(Product P, Matrix a, Matrix b, cudaStream_t stream)
+{
+    const Device* dev = nullptr;
+    TRY(device(&dev));
+    P.tiles_m = (P.m + kTileM - 1) / kTileM;
+    // Rows per tile: the width whose waves of tiles cost least.  Per 64-wide
+    // slice a tile takes 2 clocks per row of matrix instructions, or the
+    // time its operands take from L2 at about 70 bytes a clock; about 1500
+    // clocks per tile go to filling and draining.
+    static const int widths[] = {256, 192, 128, 64, 32};
+    double best = 0;
+    for (int w : widths) {
+        if (P.b_mn && w % 64) continue;
+        const double rows = P.ragged == RAGGED_ROWS ? std::max(1.0, (double)P.n / P.groups) : (double)P.n;
+        const double groups = P.ragged == RAGGED_ROWS ? std::min(P.n, P.groups) : P.groups;
+        const double reduce = P.ragged == RAGGED_REDUCE ? (double)P.k / P.groups : P.k;
+        double tiles = groups * P.tiles_m * std::ceil(rows / w);
+        if (P.symmetric) tiles *= 0.5 + 0.5 / P.tiles_m;
+        const double slice = std::max(2.0 * w, (kTileM + w) * 128.0 / 70);
+        const double cost = std::ceil(tiles / dev->sms) * (std::ceil(reduce / kSliceK) * slice + 1500 + 8 * w);
+        if (best == 0 || cost < best) {
+            best = cost;
+            P.bn = w;
+        }
+    }
+    P.tiles_n = (int)((P.n + (int64_t)P.bn - 1) / P.bn);
+    const int bytes = (kTileM + P.bn) * kSliceK * 2;
+    P.stages = std::min(kMaxStages, (kSmemBudget - 1024 - kStagingBytes) / bytes);
+    const int64_t most = P.ragged == RAGGED_ROWS ? (int64_t)P.tiles_m * ((int64_t)P.tiles_n + P.groups)
+                                                 : (int64_t)P.tiles_m * P.tiles_n * P.groups;
+    if (most > INT32_MAX) return fail(CCL_ERR_UNSUPPORTED, "too many tiles");
+    TRY(encode(dev, &P.ma, a, 64, P.a_mn ? kSliceK : kTileM));
+    TRY(encode(dev, &P.mb, b, 64, P.b_mn ? kSliceK : P.bn));
+    const size_t smem = 1024 + (size_t)P.stages * bytes + kStagingBytes;
+    return launch(product_kernel, dim3((unsigned)std::min<int64_t>(most, dev->sms)), kThreads, smem, stream, P);
+}
+
+static void set_out(Product* P, void* out, int64_t ld, int64_t bs, bool bf)
+{
+    P->out = (uint16_t*)out;
+    P->ld_out = ld;
+    P->bs_out = bs;
+    P->out_bf = bf;
+    P->vec_out = aligned16(out) && ld % 8 == 0 && bs % 8 == 0;
+}
+static void set_c(Product* P, const void* c, int64_t ld, int64_t bs, float beta)
+{
+    P->c = (const uint16_t*)c;
+    P->ld_c = ld;
+    P->bs_c = bs;
+    P->beta = beta;
+    P->vec_c = aligned16(c) && ld % 8 == 0 && bs % 8 == 0;
+}
+
+// --------------------------------------------------------- linear layers
+static std::string dims(int64_t rows, int64_t n, int64_t k)
+{
+    return "rows " + std::to_string(rows) + ", n " + std::to_string(n) + ", k " + std::to_string(k);
+}
+
+static ccl_status_t check_shape(const char* who, int64_t rows, int64_t n, int64_t k, int32_t dtype, int32_t act,
+                                int32_t experts, const void* offsets)
+{
+    const std::string w = std::string(who) + ": ";
+    if (dtype != CCL_BF16 && dtype != CCL_F16)
+        return fail(CCL_ERR_UNSUPPORTED, w + "products take bf16 and f16 (dtype " + std::to_string(dtype) + ")");
+    const int64_t top = (int64_t)1 << 30;
+    if (rows < 0 || n < 1 || k < 1 || rows > top || n > top || k > top)
+        return fail(CCL_ERR_INVALID_ARG, w + "sizes out of range (" + dims(rows, n, k) + ")");
+    if (act < CCL_ACT_NONE || act > CCL_ACT_SILU)
+        return fail(CCL_ERR_INVALID_ARG, w + "unknown activation " + std::to_string(act));
+    if (experts < 0 || experts > kMaxGroups)
+        return fail(CCL_ERR_INVALID_ARG, w + "experts outside 0.." + std::to_string(kMaxGroups));
+    if (experts > 0 && !offsets) return fail(CCL_ERR_INVALID_ARG, w + "experts without offsets");
+    return CCL_OK;
+}
+
+// A stride given as 0 means packed; one below the row's length would make rows overlap.
+static ccl_status_t stride(const char* what, int64_t given, int64_t least, int64_t* out)
+{
+    if (given != 0 && given < least)
+        return fail(CCL_ERR_INVALID_ARG, std::string(what) + " stride " + std::to_string(given) + " below " +
+                                             std::to_string(least));
+    *out = given ? given : least;
+    return CCL_OK;
+}
+
+static ccl_status_t pointer(const char* what, const void* p, bool needed)
+{
+    if (needed && !p) return fail(CCL_ERR_INVALID_ARG, std::string(what) + " is null");
+    if ((uintptr_t)p & 1) return fail(CCL_ERR_INVALID_ARG, std::string(what) + " is not aligned to its elements");
+    return CCL_OK;
+}
+
+static ccl_status_t linear(const ccl_linear_t* a, char* base, int64_t* need, cudaStream_t stream)
+{
+    if (!a) return fail(CCL_ERR_INVALID_ARG, "ccl_linear: null arguments");
+    TRY(check_shape("ccl_linear", a->rows, a->n, a->k, a->dtype, a->act, a->experts, a->offsets));
+    int64_t ldx, ldw, ldr, ldy, ldz, sw, sb;
+    TRY(stride("x", a->ldx, a->k, &ldx));
+    TRY(stride("w", a->ldw, a->k, &ldw));
+    TRY(stride("residual", a->ldr, a->n, &ldr));
+    TRY(stride("y", a->ldy, a->n, &ldy));
+    TRY(stride("z", a->ldz, a->n, &ldz));
+    TRY(stride("w expert", a->w_stride, (a->n - 1) * ldw + a->k, &sw));
+    if (!a->w_stride) sw = a->n * ldw;
+    TRY(stride("bias expert", a->bias_stride, a->n, &sb));
+    Arena ws = {base};
+    const int64_t count = a->experts > 0 ? a->experts : 1;
+    Matrix w = {a->w, a->n, a->k, ldw, count, sw}, x = {a->x, a->rows, a->k, ldx};
+    if (!need) {
+        const bool some = a->rows > 0;
+        TRY(pointer("x", a->x, some));
+        TRY(pointer("w", a->w, some));
+        TRY(pointer("y", a->y, some));
+        TRY(pointer("z", a->z, false));
+        TRY(pointer("bias", a->bias, false));
+        TRY(pointer("residual", a->residual, false));
+        if (some && (a->y == a->x || a->y == a->w || (a->z && a->z == a->y)))
+            return fail(CCL_ERR_INVALID_ARG, "ccl_linear: an output is also an operand");
+        if (!some) return CCL_OK;
+    }
+    if (need) {
+        *need = w.packed_bytes() + x.packed_bytes();
+        return CCL_OK;
+    }
+    TRY(loadable(&w, &ws, stream));
+    TRY(loadable(&x, &ws, stream));
+    Product P = {};
+    P.m = (int32_t)a->n;
+    P.n = (int32_t)a->rows;
+    P.k = (int32_t)a->k;
+    P.groups = (int32_t)count;
+    P.ragged = a->experts > 0 ? RAGGED_ROWS : DENSE;
+    P.offsets = a->experts > 0 ? a->offsets : nullptr;
+    P.alpha = 1.f;
+    P.act = a->act;
+    P.in_bf = a->dtype == CCL_BF16;
+    set_out(&P, a->y, ldy, 0, P.in_bf);
+    if (a->residual) set_c(&P, a->residual, ldr, 0, 1.f);
+    if (a->z) {
+        P.pre = (uint16_t*)a->z;
+        P.ld_pre = ldz;
+        P.vec_pre = aligned16(a->z) && ldz % 8 == 0;
+    }
+    if (a->bias) {
+        P.bias = (const uint16_t*)a->bias;
+        P.bs_bias = sb;
+        P.vec_bias = aligned16(a->bias) && (count == 1 || sb % 8 == 0);
+    }
+    return run(P, w, x, stream);
+}
+
+static ccl_status_t linear_grad(const ccl_linear_grad_t* a, char* base, int64_t* need, cudaStream_t stream)
+{
+    if (!a) return fail(CCL_ERR_INVALID_ARG, "ccl_linear_grad: null arguments");
+    TRY(check_shape("ccl_linear_grad", a->rows, a->n, a->k, a->dtype, a->act, a->experts, a->offsets));
+    int64_t lddy, ldx, ldw, ldz, lddx, lddw, sw, sdw, sdb;
+    TRY(stride("dy", a->lddy, a->n, &lddy));
+    TRY(stride("x", a->ldx, a->k, &ldx));
+    TRY(stride("w", a->ldw, a->k, &ldw));
+    TRY(stride("z", a->ldz, a->n, &ldz));
+    TRY(stride("dx", a->lddx, a->k, &lddx));
+    TRY(stride("dw", a->lddw, a->k, &lddw));
+    TRY(stride("w expert", a->w_stride, (a->n - 1) * ldw + a->k, &sw));
+    if (!a->w_stride) sw = a->n * ldw;
+    TRY(stride("dw expert", a->dw_stride, (a->n - 1) * lddw + a->k, &sdw));
+    if (!a->dw_stride) sdw = a->n * lddw;
+    TRY(stride("db expert", a->db_stride, a->n, &sdb));
+    const int64_t count = a->experts > 0 ? a->experts : 1;
+    if (!need) {
+        const bool some = a->rows > 0;
+        TRY(pointer("dy", a->dy, some));
+        TRY(pointer("x", a->x, some && a->dw));
+        TRY(pointer("w", a->w, some && a->dx));
+        TRY(pointer("z", a->z, some && a->act != CCL_ACT_NONE));
+        TRY(pointer("dx", a->dx, false));
+        TRY(pointer("dw", a->dw, false));
+        TRY(pointer("db", a->db, false));
+        if ((a->dx && (a->dx == a->dy || a->dx == a->w)) || (a->dw && (a->dw == a->dy || a->dw == a->x)))
+            return fail(CCL_ERR_INVALID_ARG, "ccl_linear_grad: an output is also an operand");
+        if (!some) {
+            if (a->dw)
+                for (int64_t e = 0; e < count; ++e)
+                    TRY_CUDA(cudaMemset2DAsync((uint16_t*)a->dw + e * sdw, lddw * 2, 0, a->k * 2, a->n, stream), "dw");
+            if (a->db)
+                TRY_CUDA(cudaMemset2DAsync(a->db, sdb * 2, 0, a->n * 2, count, stream), "db");
+            return CCL_OK;
+        }
+    }
+    // dz: dy itself where there is no activation and TMA can read it
+    const bool own_dz = a->act != CCL_ACT_NONE || !aligned16(a->dy) || lddy % 8 != 0;
+    Arena ws = {base};
+    Matrix dz = {a->dy, a->rows, a->n, lddy}, x = {a->x, a->rows, a->k, ldx}, w = {a->w, a->n, a->k, ldw, count, sw};
+    if (!a->dx) w.p = nullptr, w.ld = 8;
+    if (!a->dw) x.p = nullptr, x.ld = 8;
+    GradPass G = {};
+    const int64_t chunks = a->rows / kGradRows + count;
+    G.ld_part = round_up(a->n, 64);
+    G.ld_dz = round_up(a->n, 8);
+    if (own_dz) {
+        G.dz = ws.take<uint16_t>(a->rows * G.ld_dz * 2);
+        dz.p = G.dz;
+        dz.ld = G.ld_dz;
+    }
+    if (a->db) G.partial = ws.take<float>(chunks * G.ld_part * 4);
+    if (need) {
+        *need = ws.used + w.packed_bytes() + x.packed_bytes();
+        return CCL_OK;
+    }
+    const bool bf = a->dtype == CCL_BF16;
+    if (own_dz || a->db) {
+        G.dy = (const uint16_t*)a->dy;
+        G.z = (const uint16_t*)a->z;
+        G.db = (uint16_t*)a->db;
+        G.offsets = a->experts > 0 ? a->offsets : nullptr;
+        G.ld_dy = lddy;
+        G.ld_z = ldz;
+        G.bs_db = sdb;
+        G.rows = (int32_t)a->rows;
+        G.n = (int32_t)a->n;
+        G.groups = (int32_t)count;
+        G.act = a->act;
+        G.bf = bf;
+        G.vec = (aligned16(a->dy) && lddy % 8 == 0 ? 1 : 0) | (aligned16(a->z) && ldz % 8 == 0 ? 2 : 0) | 4;
+        TRY(launch(act_grad_kernel, dim3((unsigned)chunks, (unsigned)((a->n + 255) / 256)), 256, 0, stream, G));
+        if (a->db)
+            TRY(launch(bias_grad_kernel, dim3((unsigned)((a->n + 255) / 256), (unsigned)count), 256, 0, stream, G));
+    }
+    Product P = {};
+    P.groups = (int32_t)count;
+    P.offsets = a->experts > 0 ? a->offsets : nullptr;
+    P.alpha = 1.f;
+    P.in_bf = bf;
+    if (a->dx) {   // dx[t, k] = sum_n w[n, k] dz[t, n]
+        TRY(loadable(&w, &ws, stream));
+        P.m = (int32_t)a->k;
+        P.n = (int32_t)a->rows;
+        P.k = (int32_t)a->n;
+        P.ragged = a->experts > 0 ? RAGGED_ROWS : DENSE;
+        P.a_mn = 1;
+        set_out(&P, a->dx, lddx, 0, bf);
+        TRY(run(P, w, dz, stream));
+    }
+    if (a->dw) {   // dw[n, k] = sum_t x[t, k] dz[t, n]
+        TRY(loadable(&x, &ws, stream));
+        P.m = (int32_t)a->k;
+        P.n = (int32_t)a->n;
+        P.k = (int32_t)a->rows;
+        P.ragged = a->experts > 0 ? RAGGED_REDUCE : DENSE;
+        P.a_mn = P.b_mn = 1;
+        set_out(&P, a->dw, lddw, sdw, bf);
+        TRY(run(P, x, dz, stream));
+    }
+    return CCL_OK;
+}
+
+// ------------------------------------------------------ orthogonalisation
+static ccl_status_t orthogonalize(const ccl_ortho_t* a, char* base, int64_t* need, cudaStream_t stream)
+{
+    const std::string who = "ccl_orthogonalize: ";
+    if (!a) return fail(CCL_ERR_INVALID_ARG, who + "null arguments");
+    if (a->dtype != CCL_F32 && a->dtype != CCL_BF16 && a->dtype != CCL_F16)
+        return fail(CCL_ERR_UNSUPPORTED, who + "gradients are f32, bf16 or f16");
+    if (a->out_dtype != CCL_BF16 && a->out_dtype != CCL_F16)
+        return fail(CCL_ERR_UNSUPPORTED, who + "the update is bf16 or f16");
+    if (a->batch < 0 || a->batch > 65535 || a->p < 1 || a->q < 1 || a->p > (1 << 30) || a->q > (1 << 30) ||
+        std::min(a->p, a->q) > kMaxGroups * kTileM)
+        return fail(CCL_ERR_INVALID_ARG, who + "sizes out of range (batch " + std::to_string(a->batch) + ", " +
+                                             std::to_string(a->p) + " x " + std::to_string(a->q) + ")");
+    if (a->steps < 1 || a->steps > 64) return fail(CCL_ERR_INVALID_ARG, who + "steps outside 1..64");
+    if (!(a->eps >= 0.f)) return fail(CCL_ERR_INVALID_ARG, who + "eps is negative");
+    int64_t ldg, ldo, sg, so;
+    TRY(stride("g", a->ldg, a->q, &ldg));
+    TRY(stride("out", a->ldo, a->q, &ldo));
+    TRY(stride("g matrix", a->g_stride, (a->p - 1) * ldg + a->q, &sg));
+    if (!a->g_stride) sg = a->p * ldg;
+    TRY(stride("out matrix", a->out_stride, (a->p - 1) * ldo + a->q, &so));
+    if (!a->out_stride) so = a->p * ldo;
+    const int64_t r = std::min(a->p, a->q);
+    const bool tall = a->p > a->q;
+    Arena ws = {base};
+    Matrix x[2], A, B;
+    const int64_t ldx = round_up(a->q, 8), lda = round_up(r, 8);
+    for (int i = 0; i < 2; ++i) {
+        x[i] = {nullptr, a->p, a->q, ldx, a->batch, a->p * ldx};
+        x[i].p = ws.take<void>(a->batch * a->p * ldx * 2);
+    }
+    A = B = {nullptr, r, r, lda, a->batch, r * lda};
+    A.p = ws.take<void>(a->batch * r * lda * 2);
+    B.p = ws.take<void>(a->batch * r * lda * 2);
+    NormPass N = {};
+    N.partial = ws.take<float>(a->batch * kNormBlocks * 4);
+    N.kappa = ws.take<float>(a->batch * 4);
+    N.kappa2 = ws.take<float>(a->batch * 4);
+    if (need) {
+        *need = ws.used;
+        return CCL_OK;
+    }
+    if (a->batch == 0) return CCL_OK;
+    if (!a->g || !a->out) return fail(CCL_ERR_INVALID_ARG, who + "null matrix");
+    if ((uintptr_t)a->g % (a->dtype == CCL_F32 ? 4 : 2) || (uintptr_t)a->out % 2)
+        return fail(CCL_ERR_INVALID_ARG, who + "a matrix is not aligned to its elements");
+    N.g = a->g;
+    N.x = (__half*)x[0].p;
+    N.ld_g = ldg;
+    N.bs_g = sg;
+    N.ld_x = ldx;
+    N.bs_x = a->p * ldx;
+    N.p = (int32_t)a->p;
+    N.q = (int32_t)a->q;
+    N.type = a->dtype;
+    N.eps = a->eps;
+    TRY(launch(norm_kernel, dim3(kNormBlocks, (unsigned)a->batch), 256, 0, stream, N));
+    TRY(launch(scale_kernel, dim3((unsigned)std::min<int64_t>(a->p, 1024), (unsigned)a->batch), 256, 0, stream, N));
+    for (int i = 0; i < a->steps; ++i) {
+        Matrix &from = x[i & 1], &to = x[(i & 1) ^ 1];
+        const bool first = i == 0, last = i + 1 == a->steps;
+        Product P = {};
+        P.groups = (int32_t)a->batch;
+        P.m = P.n = (int32_t)r;
+        // A = x x^T (or x^T x of a tall x): symmetric
+        P.k = (int32_t)(tall ? a->p : a->q);
+        P.a_mn = P.b_mn = tall;
+        P.symmetric = 1;
+        P.alpha = kScaleA / (kScaleX * kScaleX);
+        P.alpha_of = first ? N.kappa2 : nullptr;
+        set_out(&P, const_cast<void*>(A.p), lda, r * lda, false);
+        TRY(run(P, from, from, stream));
+        // B = b A + c A A: symmetric
+        P.k = (int32_t)r;
+        P.a_mn = P.b_mn = 0;
+        P.alpha = a->c / kScaleA;
+        P.alpha_of = nullptr;
+        set_c(&P, A.p, lda, r * lda, a->b);
+        set_out(&P, const_cast<void*>(B.p), lda, r * lda, false);
+        TRY(run(P, A, A, stream));
+        // x <- a x + B x (or a x + x B)
+        P.symmetric = 0;
+        P.m = (int32_t)a->q;
+        P.n = (int32_t)a->p;
+        P.k = (int32_t)r;
+        const float unscale = last ? a->scale / kScaleX : 1.f;
+        P.alpha = unscale / kScaleA;
+        P.alpha_of = P.beta_of = first ? N.kappa : nullptr;
+        set_c(&P, from.p, ldx, a->p * ldx, a->a * unscale);
+        if (last)
+            set_out(&P, a->out, ldo, so, a->out_dtype == CCL_BF16);
+        else
+            set_out(&P, const_cast<void*>(to.p), ldx, a->p * ldx, false);
+        if (tall) {   // out[p, q] = sum_r B[q, r] x[p, r], B symmetric
+            P.a_mn = 0;
+            P.b_mn = 0;
+            TRY(run(P, B, from, stream));
+        } else {      // out[p, q] = sum_r x[r, q] B[p, r]
+            P.a_mn = 1;
+            P.b_mn = 0;
+            TRY(run(P, from, B, stream));
+        }
+    }
+    return CCL_OK;
+}
+
+template <typename Args>
+static ccl_status_t guarded(ccl_status_t (*fn)(const Args*, char*, int64_t*, cudaStream_t), const Args* a, void* ws,
+                            int64_t ws_bytes, void* stream)
+{
+    int64_t need = 0;
+    TRY(fn(a, nullptr, &need, nullptr));
+    if (need > 0 && (!ws || ws_bytes < need))
+        return fail(CCL_ERR_INVALID_ARG, "workspace of " + std::to_string(need) + " bytes needed, " +
+                                             std::to_string(ws ? ws_bytes : 0) + " given");
+    if (need > 0 && ((uintptr_t)ws & 255)) return fail(CCL_ERR_INVALID_ARG, "workspace not aligned to 256 bytes");
+    return fn(a, (char*)ws, nullptr, (cudaStream_t)stream);
+}
+
+template <typename Args>
+static ccl_status_t measured(ccl_status_t (*fn)(const Args*, char*, int64_t*, cudaStream_t), const Args* a, int64_t* out)
+{
+    if (!out) return fail(CCL_ERR_INVALID_ARG, "null size");
+    int64_t need = 0;
+    TRY(fn(a, nullptr, &need, nullptr));
+    *out = need;
+    return CCL_OK;
+}
+
+}  // namespace tensor
+}  // namespace ccl
+
+using namespace ccl;
+
+// no exception leaves the library
+#define C_ENTRY(...)                                                     \
+    try {                                                                \
+        return (__VA_ARGS__);                                            \
+    } catch (const std::bad_alloc&) {                                    \
+        return CCL_ERR_OOM;                                              \
+    } catch (...) {                                                      \
+        return CCL_ERR_INTERNAL;                                         \
+    }
+
+extern "C" {
+
+ccl_status_t ccl_linear_workspace(const ccl_linear_t* a, int64_t* bytes)
+{
+    C_ENTRY(tensor::measured(tensor::linear, a, bytes));
+}
+ccl_status_t ccl_linear(const ccl_linear_t* a, void* ws, int64_t ws_bytes, void* stream)
+{
+    C_ENTRY(tensor::guarded(tensor::linear, a, ws, ws_bytes, stream));
+}
+ccl_status_t ccl_linear_grad_workspace(const ccl_linear_grad_t* a, int64_t* bytes)
+{
+    C_ENTRY(tensor::measured(tensor::linear_grad, a, bytes));
+}
+ccl_status_t ccl_linear_grad(const ccl_linear_grad_t* a, void* ws, int64_t ws_bytes, void* stream)
+{
+    C_ENTRY(tensor::guarded(tensor::linear_grad, a, ws, ws_bytes, stream));
+}
+ccl_status_t ccl_orthogonalize_workspace(const ccl_ortho_t* a, int64_t* bytes)
+{
+    C_ENTRY(tensor::measured(tensor::orthogonalize, a, bytes));
+}
+ccl_status_t ccl_orthogonalize(const ccl_ortho_t* a, void* ws, int64_t ws_bytes, void* stream)
+{
+    C_ENTRY(tensor::guarded(tensor::orthogonalize, a, ws, ws_bytes, stream));
+}
+
+ccl_status_t ccl_tensor_status(void)
+{
+    C_ENTRY([]() -> ccl_status_t {
+        int st[4] = {0, 0, 0, 0};
+        TRY_CUDA(cudaDeviceSynchronize(), "cudaDeviceSynchronize");
+        TRY_CUDA(cudaMemcpyFromSymbol(st, tensor::g_status, sizeof(st)), "status word");
+        if (st[0] == 0) return CCL_OK;
+        const int zero[4] = {0, 0, 0, 0};
+        TRY_CUDA(cudaMemcpyToSymbol(tensor::g_status, zero, sizeof(zero)), "status word");
+        return fail((ccl_status_t)st[0], st[0] == CCL_ERR_TIMEOUT ? "a wait inside a tensor product ran out of time"
+                                                                  : "expert offsets decrease or leave the rows");
+    }());
+}
+
+}  // extern "C"

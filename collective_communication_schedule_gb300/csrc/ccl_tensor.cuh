@@ -1,0 +1,257 @@
+// Device-side building blocks of the tensor products: shared-memory barriers
+// with bounded waits, TMA tile loads, tcgen05 matrix instructions on tensor
+// memory, and the descriptors they take.  sm_103a only.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cstdint>
+
+namespace ccl {
+namespace tensor {
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p)
+{
+    return (uint32_t)__cvta_generic_to_shared(p);
+}
+
+__device__ __forceinline__ unsigned long long now_ns()
+{
+    unsigned long long t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
+
+// Every kernel here may be launched before the one ahead of it on the stream
+// has ended: let the next one in early, and touch no global memory before
+// the previous one is complete.
+__device__ __forceinline__ void wait_for_previous()
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// ------------------------------------------------------------- barriers
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count)
+{
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.b32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    return ok != 0;
+}
+
+// Limit of every wait: no step of a product takes anywhere near this long,
+// so a wait that reaches it means a lost signal.
+constexpr unsigned long long kWaitNs = 4000000000ull;
+constexpr int kWaitSpins = 1 << 26;
+
+// Bounded wait for the completion of the phase with this parity.  Gives up
+// when the limit passes or another warp of the threadblock has given up.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* failed)
+{
+    if (bar_try(bar, parity)) return true;
+    const unsigned long long t0 = now_ns();
+    for (int i = 1; i < kWaitSpins; ++i) {
+        if (bar_try(bar, parity)) return true;
+        if ((i & 63) == 0) {
+            if (*failed) return false;
+            if (now_ns() - t0 > kWaitNs) break;
+        }
+    }
+    *failed = 1;
+    return false;
+}
+
+// ------------------------------------------------------------------ TMA
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z)
+{
+    asm volatile("cp.async.bulk.tensor.3d.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];"
+                 ::"r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_prefetch(const CUtensorMap* map)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
+// ------------------------------------------------------- tensor memory
+__device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t cols)
+{
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols)
+{
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void fence_after()
+{
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void fence_before()
+{
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+// 32 lanes x 32 columns of 32-bit accumulators, one lane per thread
+__device__ __forceinline__ void tmem_load32(uint32_t addr, float v[32])
+{
+    uint32_t* r = reinterpret_cast<uint32_t*>(v);
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+                   "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+                   "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+                   "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+                 : "r"(addr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// ------------------------------------------------- matrix instructions
+// Shared-memory operand descriptor, 128-byte swizzle.  Operand tiles are
+// stacks of 1024-byte atoms (8 rows of 128 bytes):
+//   reduction-major (rows of 64 reduction elements): `stride` is the step
+//     between atoms of 8 rows; `lead` is not used;
+//   row-major (rows of 64 consecutive M or N elements, one row per reduction
+//     index): `stride` is the step between atoms of 8 reduction indexes,
+//     `lead` the step to the next 64 M or N elements.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, uint32_t lead, uint32_t stride)
+{
+    return (uint64_t)((addr & 0x3ffff) >> 4) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(stride >> 4) << 32) |
+           (1ull << 46) | (2ull << 61);
+}
+// Instruction descriptor: f32 accumulators, both operands bf16 or both f16.
+__host__ __device__ constexpr uint32_t mma_desc(bool bf16, bool a_mn, bool b_mn, int m, int n)
+{
+    return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((a_mn ? 1u : 0u) << 15) |
+           ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+                 : "memory");
+}
+// the barrier is arrived on once every matrix instruction this thread issued so far has finished
+__device__ __forceinline__ void mma_commit(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// ------------------------------------------------------- element types
+template <bool BF>
+__device__ __forceinline__ float2 unpack2(uint32_t u)
+{
+    if (BF) return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+    return __half22float2(*reinterpret_cast<const __half2*>(&u));
+}
+template <bool BF>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi)
+{
+    uint32_t r;
+    if (BF)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float load1(const uint16_t* p, bool bf)
+{
+    const uint16_t u = *p;
+    return bf ? __uint_as_float((uint32_t)u << 16) : __half2float(*reinterpret_cast<const __half*>(&u));
+}
+__device__ __forceinline__ void store1(uint16_t* p, float v, bool bf)
+{
+    if (bf) {
+        const __nv_bfloat16 h = __float2bfloat16_rn(v);
+        *p = *reinterpret_cast<const uint16_t*>(&h);
+    } else {
+        const __half h = __float2half_rn(v);
+        *p = *reinterpret_cast<const uint16_t*>(&h);
+    }
+}
+// elements [lo, hi) of 8 consecutive ones; the others read as 0 and are not
+// touched.  vec: the address is 16-byte aligned
+__device__ __forceinline__ void load8(const uint16_t* p, bool bf, bool vec, int lo, int hi, float v[8])
+{
+    if (vec && lo == 0 && hi == 8) {
+        const uint4 u = *reinterpret_cast<const uint4*>(p);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = bf ? unpack2<true>(w[i]) : unpack2<false>(w[i]);
+            v[2 * i] = f.x;
+            v[2 * i + 1] = f.y;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = i >= lo && i < hi ? load1(p + i, bf) : 0.f;
+    }
+}
+__device__ __forceinline__ void store8(uint16_t* p, bool bf, bool vec, int lo, int hi, const float v[8])
+{
+    if (vec && lo == 0 && hi == 8) {
+        uint4 u;
+        if (bf)
+            u = make_uint4(pack2<true>(v[0], v[1]), pack2<true>(v[2], v[3]), pack2<true>(v[4], v[5]),
+                           pack2<true>(v[6], v[7]));
+        else
+            u = make_uint4(pack2<false>(v[0], v[1]), pack2<false>(v[2], v[3]), pack2<false>(v[4], v[5]),
+                           pack2<false>(v[6], v[7]));
+        *reinterpret_cast<uint4*>(p) = u;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i >= lo && i < hi) store1(p + i, v[i], bf);
+    }
+}
+
+// ---------------------------------------------------------- activations
+// gelu is the tanh form, 0.5 z (1 + tanh u) = z sigmoid(2 u),
+// u = sqrt(2/pi) (z + 0.044715 z^3); silu is z sigmoid(z).  In 32 bits.
+enum { ACT_NONE = 0, ACT_RELU = 1, ACT_GELU = 2, ACT_SILU = 3 };
+
+__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+
+__device__ __forceinline__ float activate(float z, int act)
+{
+    if (act == ACT_RELU) return z < 0.f ? 0.f : z;   // keeps NaN
+    if (act == ACT_SILU) return z * sigmoid(z);
+    if (act == ACT_GELU) return z * sigmoid(1.5957691216057308f * (z + 0.044715f * z * z * z));
+    return z;
+}
+__device__ __forceinline__ float activate_grad(float z, int act)
+{
+    if (act == ACT_RELU) return z > 0.f ? 1.f : 0.f;
+    if (act == ACT_SILU) {
+        const float s = sigmoid(z);
+        return s * (1.f + z * (1.f - s));
+    }
+    if (act == ACT_GELU) {
+        const float s = sigmoid(1.5957691216057308f * (z + 0.044715f * z * z * z));
+        return s + z * s * (1.f - s) * 1.5957691216057308f * (1.f + 0.134145f * z * z);
+    }
+    return 1.f;
+}
+
+}  // namespace tensor
+}  // namespace ccl

@@ -728,6 +728,117 @@ ccl_status_t ccl_tune_table_lookup(const ccl_tune_row_t* rows, int32_t n, int64_
 ccl_status_t ccl_schedule_write_json(ccl_schedule_t s, const char* path);
 ccl_status_t ccl_schedule_read_json(const char* path, ccl_schedule_t* out);
 
+/* ======================================================================
+ * Tensor products of language-model layers
+ *
+ * The work between the collectives of a training or serving step: the dense
+ * and expert products whose inputs an AllGather or AllToAll brings and whose
+ * gradients an AllReduce or ReduceScatter takes away, and the orthogonalised
+ * update computed from the reduced gradient.  One tcgen05 product kernel
+ * (csrc/ccl_tensor.cu) serves all of them.
+ *
+ * Conventions, besides those at the top of this file: calls are
+ * asynchronous on `stream`, allocate nothing, keep nothing between calls and
+ * can be captured in a CUDA graph (after one call on the device outside
+ * capture).  A call that needs scratch memory takes it from the caller
+ * (*_workspace gives the size, which may be 0; 256-byte aligned; free for
+ * other use once the call's work on `stream` is done).  Matrices are stored
+ * by rows with consecutive elements; strides are in elements, 0 = packed.
+ * Any stride and alignment is accepted; operands whose base or row stride is
+ * no multiple of 16 bytes are first copied into the workspace.  Sums are
+ * held in 32 bits and rounded once per output; the order of every sum is
+ * fixed by the sizes, so equal calls give equal bits.
+ * ====================================================================== */
+
+/* Activations.  GELU is the tanh form, 0.5 z (1 + tanh(sqrt(2/pi) (z +
+ * 0.044715 z^3))); SILU is z / (1 + exp(-z)). */
+#define CCL_ACT_NONE 0
+#define CCL_ACT_RELU 1
+#define CCL_ACT_GELU 2
+#define CCL_ACT_SILU 3
+
+/*
+ * z = x w^T + bias,  y = act(z) + residual.
+ *   experts = 0: x is rows x k, w is n x k.
+ *   experts > 0 (at most 1024): row t of x meets the weight of its expert.
+ *     Rows are sorted by expert; expert e owns rows offsets[e] ..
+ *     offsets[e + 1] - 1 (device array of experts + 1 int32, may repeat:
+ *     experts without rows).  Rows outside [offsets[0], offsets[experts])
+ *     are not written.  Offsets are read on the device, clamped to the rows;
+ *     ones that decrease or leave the rows are reported by
+ *     ccl_tensor_status.  w is experts matrices w_stride apart, bias experts
+ *     vectors bias_stride apart.
+ * bias, residual (rows x n) and z (output, rows x n, the values before the
+ * activation, for the backward pass) may be null.  y may be residual (same
+ * stride), no other operand.
+ */
+typedef struct {
+    int64_t rows, n, k;
+    int32_t dtype;               /* CCL_BF16 or CCL_F16: of x, w, bias, residual, y, z */
+    int32_t act;                 /* CCL_ACT_* */
+    int32_t experts;
+    int32_t reserved;
+    const void *x, *w, *bias, *residual;
+    const int32_t* offsets;
+    void *y, *z;
+    int64_t ldx, ldw, ldr, ldy, ldz;
+    int64_t w_stride, bias_stride;
+} ccl_linear_t;
+
+/*
+ * Gradients of ccl_linear from dy (rows x n):
+ *   dz = dy * act'(z),  dx = dz w,  dw = dz^T x,  db = sum over rows of dz
+ * (by expert where experts > 0; an expert without rows gets dw = db = 0).
+ * The gradient of the residual is dy itself.  z is needed when act is not
+ * CCL_ACT_NONE.  dx, dw, db may be null (not computed; then w, x are not
+ * read).  dz is rounded to the element type between the two products, as z
+ * and y are between layers; db sums it unrounded.
+ */
+typedef struct {
+    int64_t rows, n, k;
+    int32_t dtype, act, experts;
+    int32_t reserved;
+    const void *dy, *x, *w, *z;
+    const int32_t* offsets;
+    void *dx, *dw, *db;
+    int64_t lddy, ldx, ldw, ldz, lddx, lddw;
+    int64_t w_stride, dw_stride, db_stride;
+} ccl_linear_grad_t;
+
+/*
+ * Orthogonalised updates (Newton-Schulz, as the Muon optimiser takes them):
+ * for each of `batch` p x q matrices g_stride apart
+ *   x = g / (|g|_F + eps);  `steps` times:  A = x x^T,
+ *   x <- a x + (b A + c A A) x;   out = scale * x
+ * (x^T x on the other side for p > q, which is the same matrix).  g is f32,
+ * bf16 or f16; out (may be g where type and strides agree) is bf16 or f16.
+ * Intermediate matrices are f16 with fixed power-of-two scales, which holds
+ * for coefficients that keep the singular values of x below 8 and the
+ * entries of b A + c A A below 63 in magnitude.
+ */
+typedef struct {
+    int64_t batch, p, q;
+    int32_t dtype, out_dtype;
+    int32_t steps;
+    float a, b, c, eps, scale;
+    const void* g;
+    void* out;
+    int64_t ldg, ldo, g_stride, out_stride;
+} ccl_ortho_t;
+
+ccl_status_t ccl_linear_workspace(const ccl_linear_t* a, int64_t* bytes);
+ccl_status_t ccl_linear(const ccl_linear_t* a, void* ws, int64_t ws_bytes, void* stream);
+ccl_status_t ccl_linear_grad_workspace(const ccl_linear_grad_t* a, int64_t* bytes);
+ccl_status_t ccl_linear_grad(const ccl_linear_grad_t* a, void* ws, int64_t ws_bytes, void* stream);
+ccl_status_t ccl_orthogonalize_workspace(const ccl_ortho_t* a, int64_t* bytes);
+ccl_status_t ccl_orthogonalize(const ccl_ortho_t* a, void* ws, int64_t ws_bytes, void* stream);
+
+/* Synchronize the device and report (once) what went wrong inside the tensor
+ * products launched on it since the last call: CCL_ERR_TIMEOUT (a wait on the
+ * device ran out; the outputs are incomplete) or CCL_ERR_INVALID_ARG (expert
+ * offsets that decrease or leave the rows). */
+ccl_status_t ccl_tensor_status(void);
+
 const char* ccl_error_string(ccl_status_t s);
 const char* ccl_last_error_detail(void);
 const char* ccl_version(void);

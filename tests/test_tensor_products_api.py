@@ -1,0 +1,134 @@
+"""Refusals, workspace sizes and struct layouts of the tensor products (no GPU
+needed: arguments are checked before any device is touched)."""
+import ctypes
+import os
+import shutil
+import subprocess
+
+import pytest
+
+import collective_communication_schedule_gb300 as ccl
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+A = 1 << 20                # stands for device addresses: never read here
+
+
+def linear(**kw):
+    a = ccl.Linear(rows=4, n=16, k=32, dtype=ccl.BF16, x=A, w=2 * A, y=3 * A)
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+def grad(**kw):
+    a = ccl.LinearGrad(rows=4, n=16, k=32, dtype=ccl.F16, dy=A, x=2 * A, w=3 * A, dx=4 * A, dw=5 * A)
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+def ortho(**kw):
+    a = ccl.Ortho(batch=1, p=16, q=32, dtype=ccl.F32, out_dtype=ccl.BF16, steps=5, a=3.4, b=-4.7, c=2.0, eps=1e-7,
+                  scale=1.0, g=A, out=2 * A)
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+def code(name, a, ws=64 * A, size=1 << 40):
+    return getattr(ccl.lib, name)(ctypes.byref(a), ws, size, None)
+
+
+INVALID, UNSUPPORTED = 1, 5
+
+
+@pytest.mark.parametrize("name,a,want,word", [
+    ("ccl_linear", linear(dtype=ccl.F32), UNSUPPORTED, "bf16 and f16"),
+    ("ccl_linear", linear(dtype=ccl.I32), UNSUPPORTED, "bf16 and f16"),
+    ("ccl_linear", linear(rows=-1), INVALID, "sizes"),
+    ("ccl_linear", linear(k=0), INVALID, "sizes"),
+    ("ccl_linear", linear(n=0), INVALID, "sizes"),
+    ("ccl_linear", linear(rows=1 << 31), INVALID, "sizes"),
+    ("ccl_linear", linear(act=4), INVALID, "activation"),
+    ("ccl_linear", linear(act=-1), INVALID, "activation"),
+    ("ccl_linear", linear(ldx=31), INVALID, "x stride"),
+    ("ccl_linear", linear(ldw=-32), INVALID, "w stride"),
+    ("ccl_linear", linear(ldy=15), INVALID, "y stride"),
+    ("ccl_linear", linear(x=None), INVALID, "x is null"),
+    ("ccl_linear", linear(y=None), INVALID, "y is null"),
+    ("ccl_linear", linear(w=A + 1), INVALID, "not aligned"),
+    ("ccl_linear", linear(y=A), INVALID, "also an operand"),
+    ("ccl_linear", linear(experts=3), INVALID, "offsets"),
+    ("ccl_linear", linear(experts=1025, offsets=A), INVALID, "experts outside"),
+    ("ccl_linear", linear(experts=3, offsets=A, w_stride=100), INVALID, "w expert stride"),
+    ("ccl_linear_grad", grad(dtype=ccl.F32), UNSUPPORTED, "bf16 and f16"),
+    ("ccl_linear_grad", grad(act=ccl.ACT_GELU), INVALID, "z is null"),
+    ("ccl_linear_grad", grad(dy=None), INVALID, "dy is null"),
+    ("ccl_linear_grad", grad(lddx=8), INVALID, "dx stride"),
+    ("ccl_linear_grad", grad(dx=A), INVALID, "also an operand"),
+    ("ccl_orthogonalize", ortho(dtype=ccl.I32), UNSUPPORTED, "gradients"),
+    ("ccl_orthogonalize", ortho(out_dtype=ccl.F32), UNSUPPORTED, "update"),
+    ("ccl_orthogonalize", ortho(p=0), INVALID, "sizes"),
+    ("ccl_orthogonalize", ortho(batch=-1), INVALID, "sizes"),
+    ("ccl_orthogonalize", ortho(steps=0), INVALID, "steps"),
+    ("ccl_orthogonalize", ortho(eps=-1.0), INVALID, "eps"),
+    ("ccl_orthogonalize", ortho(eps=float("nan")), INVALID, "eps"),
+    ("ccl_orthogonalize", ortho(g=None), INVALID, "null"),
+    ("ccl_orthogonalize", ortho(ldg=31), INVALID, "g stride"),
+    ("ccl_orthogonalize", ortho(g=A + 2), INVALID, "not aligned"),
+])
+def test_refusals(name, a, want, word):
+    assert code(name, a) == want
+    assert word in ccl.lib.ccl_last_error_detail().decode()
+
+
+def test_workspaces_are_asked_for_and_checked():
+    def need(name, a):
+        n = ctypes.c_int64(-1)
+        assert getattr(ccl.lib, name + "_workspace")(ctypes.byref(a), ctypes.byref(n)) == 0
+        return n.value
+
+    assert need("ccl_linear", linear()) == 0
+    assert need("ccl_linear", linear(k=33)) >= (4 + 16) * 40 * 2        # both operands copied to padded rows
+    assert need("ccl_linear", linear(x=A + 2)) >= 4 * 32 * 2
+    assert need("ccl_linear_grad", grad()) == 0
+    assert need("ccl_linear_grad", grad(act=ccl.ACT_RELU, z=A)) >= 4 * 16 * 2
+    assert need("ccl_orthogonalize", ortho()) > 2 * 16 * 32 * 2
+    assert code("ccl_linear", linear(k=33), ws=None, size=0) == INVALID
+    assert "workspace" in ccl.lib.ccl_last_error_detail().decode()
+    assert code("ccl_orthogonalize", ortho(), ws=64 * A, size=16) == INVALID
+    assert code("ccl_orthogonalize", ortho(), ws=64 * A + 16) == INVALID
+    assert ccl.lib.ccl_linear_workspace(None, ctypes.byref(ctypes.c_int64())) == INVALID
+    assert ccl.lib.ccl_linear_workspace(ctypes.byref(linear()), None) == INVALID
+
+
+def test_empty_calls_need_no_device():
+    assert code("ccl_linear", linear(rows=0, x=None, w=None, y=None)) == 0
+    assert code("ccl_orthogonalize", ortho(batch=0)) == 0
+
+
+def test_structs_match_the_header_layout(tmp_path):
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if not cc:
+        pytest.skip("no C compiler")
+    pairs = [(ccl.Linear, "ccl_linear_t"), (ccl.LinearGrad, "ccl_linear_grad_t"), (ccl.Ortho, "ccl_ortho_t")]
+    lines, want = ["#include <stddef.h>", "#include <stdio.h>", '#include "ccl.h"', "int main(void) {"], []
+    for cls, name in pairs:
+        lines.append(f'    printf("%zu\\n", sizeof({name}));')
+        want.append(ctypes.sizeof(cls))
+        for f in cls._fields_:
+            lines.append(f'    printf("%zu\\n", offsetof({name}, {f[0]}));')
+            want.append(getattr(cls, f[0]).offset)
+    (tmp_path / "l.c").write_text("\n".join(lines + ["    return 0;", "}"]) + "\n")
+    exe = str(tmp_path / "l")
+    subprocess.run([cc, "-std=c11", "-I", os.path.join(ROOT, "include"), str(tmp_path / "l.c"), "-o", exe], check=True)
+    assert [int(v) for v in subprocess.run([exe], check=True, capture_output=True, text=True).stdout.split()] == want
+
+
+def test_python_refusals():
+    torch = pytest.importorskip("torch")
+    x, w = torch.zeros(4, 8, dtype=torch.bfloat16), torch.zeros(6, 8, dtype=torch.bfloat16)
+    for call in (lambda: ccl.linear(x, w), lambda: ccl.orthogonalize(x), lambda: ccl.linear(x[0], w),
+                 lambda: ccl.linear_backward(x, x, w, act=ccl.ACT_GELU), lambda: ccl.orthogonalize(x[0])):
+        with pytest.raises(ValueError):
+            call()
