@@ -29,20 +29,30 @@ namespace tensor {
 // give every expert's range) and RAGGED_REDUCE (the reduction runs over an
 // expert's rows).
 //
-// A threadblock owns one output tile at a time: 128 features x bn rows.
-// Warp 0 streams 64-wide slices of the reduction axis into a ring of
-// shared-memory stages with TMA, warp 1 issues tcgen05 matrix instructions
-// into one of two accumulators in tensor memory, warps 4..7 drain the other
-// one through the epilogue, so that an epilogue costs nothing as long as it
-// is shorter than the next tile's products.
+// A threadblock owns 128 features x bn rows of the output at a time.  Warp 0
+// streams 64-wide slices of the reduction axis into a ring of shared-memory
+// stages with TMA, warp 1 issues tcgen05 matrix instructions into one of two
+// accumulators in tensor memory, warps 4..11 drain the other one through the
+// epilogue, so that an epilogue costs nothing as long as it is shorter than
+// the next tile's products.  Warp 3 clears what a ragged reduction must not
+// see.  Two ways to use a cluster:
+//   CG = 2: a pair of threadblocks on neighbouring SMs works on 256 features
+//     x bn rows with one matrix instruction stream (cta_group::2); each
+//     loads its 128 features and half of the rows, so an operand byte taken
+//     from L2 feeds twice the products.  For large outputs.
+//   split > 1 (CG = 1): the reduction of one tile is cut over the cluster's
+//     threadblocks; each then sums its share of the tile's rows, sent by the
+//     others through distributed shared memory, in rank order.  For outputs
+//     with fewer tiles than SMs.
 // ======================================================================
 constexpr int kTileM = 128;
 constexpr int kSliceK = 64;
-constexpr int kMaxStages = 12;
+constexpr int kMaxStages = 10;
 constexpr int kMaxGroups = 1024;
-constexpr int kThreads = 256;
+constexpr int kEpilogueWarps = 8;
+constexpr int kThreads = 128 + 32 * kEpilogueWarps;
 constexpr int kStagePitch = 36;                 // floats; rows 4 banks apart: conflict-free 16-byte reads
-constexpr int kStagingBytes = 4 * 32 * kStagePitch * 4;
+constexpr int kStagingBytes = kEpilogueWarps * 32 * kStagePitch * 4;
 constexpr int kSmemBudget = 227 * 1024 - 6 * 1024;   // dynamic part; the rest is static
 
 enum { DENSE = 0, RAGGED_ROWS = 1, RAGGED_REDUCE = 2 };
@@ -56,10 +66,10 @@ struct Product {
     int64_t ld_out, bs_out, ld_pre, ld_c, bs_c, bs_bias;
     float alpha, beta;
     int32_t m, n, k, groups;
-    int32_t bn, stages, tiles_m, tiles_n;
+    int32_t bn, stages, split, tiles_m, tiles_n;
     int32_t ragged, symmetric, act;
     int32_t in_bf, out_bf, a_mn, b_mn;
-    int32_t vec_out, vec_pre, vec_c, vec_bias;
+    int32_t vec;                   // rows of out, pre, c and bias allow 16-byte accesses
 };
 
 // [0]: a ccl_status_t of a failed launch on this device, 0 if none
@@ -68,13 +78,15 @@ __device__ int g_status[4];
 struct TileAt {
     int g, za, zb;          // group, and its index in the operand maps
     int m0, n0;             // first feature, first row within the group
-    int rows;               // rows of the group (n)
+    int live;               // rows of this tile
     int row0;               // row of the group's first row in the matrices
     int k0, klen;           // reduction range
 };
 
 struct Shared {
     uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
+    uint64_t land[kMaxStages], fixed[kMaxStages];   // a ragged reduction's last slice: loaded, cleared
+    uint64_t got, taken;           // split: every share has arrived here, every share sent has been read
     uint32_t tmem;
     int failed;
     int total;
@@ -89,9 +101,10 @@ __device__ __forceinline__ void group_range(const Product& P, int g, int limit, 
 
 // Tiles of a segment: all tiles of an expert (ragged rows), or the tiles of
 // one column of tiles that touch the lower triangle (symmetric outputs).
+template <int CG>
 __device__ __forceinline__ int segment_tiles(const Product& P, int s)
 {
-    if (P.symmetric) return P.tiles_n - s * kTileM / P.bn;
+    if (P.symmetric) return P.tiles_n - s * (CG * kTileM) / P.bn;
     int lo, len;
     group_range(P, s, P.n, lo, len);
     return P.tiles_m * ((len + P.bn - 1) / P.bn);
@@ -110,98 +123,167 @@ __device__ __forceinline__ int find_segment(const Shared* sh, int n, int t)
     return lo;
 }
 
+// Position of tile t; tiles are CG * 128 features x bn rows.
+template <int CG>
 __device__ __forceinline__ TileAt tile_at(const Product& P, const Shared* sh, int t)
 {
     TileAt q;
+    int rows = P.n;
     q.row0 = 0;
-    q.rows = P.n;
     q.k0 = 0;
     q.klen = P.k;
     if (P.ragged == RAGGED_ROWS) {
         q.g = find_segment(sh, P.groups, t);
         const int l = t - (q.g ? sh->seg_end[q.g - 1] : 0);
-        group_range(P, q.g, P.n, q.row0, q.rows);
+        group_range(P, q.g, P.n, q.row0, rows);
         // an expert's row tiles of one feature tile are neighbours: they share its weights
-        const int tn = (q.rows + P.bn - 1) / P.bn;
-        q.m0 = l / tn * kTileM;
+        const int tn = (rows + P.bn - 1) / P.bn;
+        q.m0 = l / tn * (CG * kTileM);
         q.n0 = l % tn * P.bn;
         q.za = q.g;
         q.zb = 0;
-        return q;
-    }
-    if (P.symmetric) {
-        const int per = sh->seg_end[P.tiles_m - 1];
-        q.g = t / per;
-        const int l = t % per, s = find_segment(sh, P.tiles_m, l);
-        q.m0 = s * kTileM;
-        q.n0 = (s * kTileM / P.bn + l - (s ? sh->seg_end[s - 1] : 0)) * P.bn;
     } else {
-        // bands of 16 feature tiles, row tiles inside: the tiles in flight
-        // at one time form a compact block of the output
-        const int per = P.tiles_m * P.tiles_n;
-        q.g = t / per;
-        const int l = t % per, band = l / (16 * P.tiles_n), r = l % (16 * P.tiles_n);
-        const int width = min(16, P.tiles_m - band * 16);
-        q.m0 = (band * 16 + r % width) * kTileM;
-        q.n0 = r / width * P.bn;
+        if (P.symmetric) {
+            const int per = sh->seg_end[P.tiles_m - 1];
+            q.g = t / per;
+            const int l = t % per, s = find_segment(sh, P.tiles_m, l);
+            q.m0 = s * (CG * kTileM);
+            q.n0 = (s * (CG * kTileM) / P.bn + l - (s ? sh->seg_end[s - 1] : 0)) * P.bn;
+        } else {
+            // bands of feature tiles (2048 features), row tiles inside: the
+            // tiles in flight at one time form a compact block of the output
+            const int band_w = 16 / CG, per = P.tiles_m * P.tiles_n;
+            q.g = t / per;
+            const int l = t % per, band = l / (band_w * P.tiles_n), r = l % (band_w * P.tiles_n);
+            const int width = min(band_w, P.tiles_m - band * band_w);
+            q.m0 = (band * band_w + r % width) * (CG * kTileM);
+            q.n0 = r / width * P.bn;
+        }
+        q.za = q.zb = q.g;
+        if (P.ragged == RAGGED_REDUCE) {
+            group_range(P, q.g, P.k, q.k0, q.klen);
+            q.za = q.zb = 0;
+        }
     }
-    q.za = q.zb = q.g;
-    if (P.ragged == RAGGED_REDUCE) {
-        group_range(P, q.g, P.k, q.k0, q.klen);
-        q.za = q.zb = 0;
-    }
+    q.live = min(P.bn, rows - q.n0);
     return q;
 }
 
-// 32 rows x 32 features, staged as st[row][feature], through the epilogue
-// into global memory; 8 features per thread and step.  side: 0 = every
-// element; 1 = only feature <= row (the tile of a symmetric output), -1 =
-// only feature > row (its mirror image), so that each element is written
-// once and the result is symmetric bit for bit.
-__device__ __forceinline__ void write_block(const Product& P, const float* st, int lane, int g, int64_t row, int nrows,
-                                            int feat, int nfeat, int side, float alpha, float beta)
+// The part of the epilogue after alpha, for elements [lo, hi) of 8
+// consecutive features f.. of row n; c: their values of C, if any.
+__device__ __forceinline__ void finish8(const Product& P, float v[8], int g, int64_t n, int f, int lo, int hi,
+                                        float beta, const uint4* c)
 {
+    float w[8];
+    if (P.bias) {
+        load8(P.bias + g * P.bs_bias + f, P.in_bf, true, lo, hi, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += w[i];
+    }
+    if (P.pre) store8(P.pre + n * P.ld_pre + f, P.in_bf, true, lo, hi, v);
+    if (P.act) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = activate(v[i], P.act);
+    }
+    if (P.c) {
+        if (c)
+            unpack8(*c, P.in_bf, w);
+        else
+            load8(P.c + g * P.bs_c + n * P.ld_c + f, P.in_bf, true, lo, hi, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += beta * w[i];
+    }
+    store8(P.out + g * P.bs_out + n * P.ld_out + f, P.out_bf, true, lo, hi, v);
+}
+
+__device__ __forceinline__ void finish1(const Product& P, float v, int g, int64_t n, int f, float beta, float bias,
+                                        float c)
+{
+    v += bias;
+    if (P.pre) store1(P.pre + n * P.ld_pre + f, v, P.in_bf);
+    if (P.act) v = activate(v, P.act);
+    store1(P.out + g * P.bs_out + n * P.ld_out + f, v + beta * c, P.out_bf);
+}
+
+// 8 features f.. of row n: which of them this side of a symmetric output
+// writes.  side: 0 = all; 1 = only feature <= row (the tile itself), -1 =
+// only feature > row (its mirror image): each element is written once and
+// the result is symmetric bit for bit.
+__device__ __forceinline__ void side_range(int side, int64_t n, int f, int nfeat, int& lo, int& hi)
+{
+    lo = 0;
+    hi = min(8, nfeat);
+    if (side > 0) hi = (int)min((int64_t)hi, n - f + 1);
+    if (side < 0) lo = (int)max((int64_t)0, n - f + 1);
+}
+
+// C of a thread's four groups of 8 in a block of 32 rows x 32 features
+__device__ __forceinline__ void fetch_c(const Product& P, int lane, int g, int64_t row, int nrows, int feat, int nfeat,
+                                        uint4 c[4])
+{
+    const int k = (lane & 3) * 8;
 #pragma unroll
     for (int pass = 0; pass < 4; ++pass) {
-        const int r = pass * 8 + (lane >> 2), c = (lane & 3) * 8, f = feat + c;
-        const int64_t n = row + r;
-        int lo = 0, hi = min(8, nfeat - c);
-        if (side > 0) hi = (int)min((int64_t)hi, n - f + 1);
-        if (side < 0) lo = (int)max((int64_t)0, n - f + 1);
-        if (r >= nrows || lo >= hi) continue;
-        float v[8], w[8];
-        const float4 a = *reinterpret_cast<const float4*>(st + r * kStagePitch + c);
-        const float4 b = *reinterpret_cast<const float4*>(st + r * kStagePitch + c + 4);
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= alpha;
-        if (P.bias) {
-            load8(P.bias + g * P.bs_bias + f, P.in_bf, P.vec_bias, lo, hi, w);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] += w[i];
-        }
-        if (P.pre) store8(P.pre + n * P.ld_pre + f, P.in_bf, P.vec_pre, lo, hi, v);
-        if (P.act) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = activate(v[i], P.act);
-        }
-        if (P.c) {
-            load8(P.c + g * P.bs_c + n * P.ld_c + f, P.in_bf, P.vec_c, lo, hi, w);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] += beta * w[i];
-        }
-        store8(P.out + g * P.bs_out + n * P.ld_out + f, P.out_bf, P.vec_out, lo, hi, v);
+        const int r = pass * 8 + (lane >> 2);
+        if (r < nrows && k + 8 <= nfeat)
+            c[pass] = *reinterpret_cast<const uint4*>(P.c + g * P.bs_c + (row + r) * P.ld_c + feat + k);
     }
 }
 
+// 32 rows x 32 features, staged as st[row][feature], through the epilogue
+// into global memory; 8 features per thread and step.
+__device__ __forceinline__ void write_block(const Product& P, const float* st, int lane, int g, int64_t row, int nrows,
+                                            int feat, int nfeat, int side, float alpha, float beta, const uint4* c)
+{
+#pragma unroll
+    for (int pass = 0; pass < 4; ++pass) {
+        const int r = pass * 8 + (lane >> 2), k = (lane & 3) * 8;
+        int lo, hi;
+        side_range(side, row + r, feat + k, nfeat - k, lo, hi);
+        if (r >= nrows || lo >= hi) continue;
+        float v[8];
+        const float4 a = *reinterpret_cast<const float4*>(st + r * kStagePitch + k);
+        const float4 b = *reinterpret_cast<const float4*>(st + r * kStagePitch + k + 4);
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= alpha;
+        finish8(P, v, g, row + r, feat + k, lo, hi, beta, c && k + 8 <= nfeat ? c + pass : nullptr);
+    }
+}
+
+// Rows that 16-byte accesses cannot address: every lane writes its own
+// feature, so a warp still writes 32 neighbours at a time.
+__device__ __forceinline__ void write_lanes(const Product& P, const uint32_t acc[32], int g, int64_t row, int nrows,
+                                            int f, int side, float alpha, float beta)
+{
+    if (f >= P.m) return;
+    const float bias = P.bias ? load1(P.bias + g * P.bs_bias + f, P.in_bf) : 0.f;
+#pragma unroll
+    for (int i0 = 0; i0 < 32; i0 += 16) {
+        float c[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            c[i] = P.c && i0 + i < nrows ? load1(P.c + g * P.bs_c + (row + i0 + i) * P.ld_c + f, P.in_bf) : 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (i0 + i < nrows && (!side || f <= row + i0 + i))
+                finish1(P, alpha * __uint_as_float(acc[i0 + i]), g, row + i0 + i, f, beta, bias, c[i]);
+    }
+}
+
+template <int CG>
 __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ Product P)
 {
     __shared__ __align__(8) Shared sh;
     extern __shared__ unsigned char raw[];
     unsigned char* dyn = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t bytes_a = kTileM * kSliceK * 2, bytes_b = P.bn * kSliceK * 2, bytes = bytes_a + bytes_b;
+    const int size = CG == 2 ? 2 : P.split;             // threadblocks of the cluster
+    const int rank = size > 1 ? (int)cluster_rank() : 0;
+    const int cluster = blockIdx.x / size, clusters = gridDim.x / size;
+    const uint32_t bytes_a = kTileM * kSliceK * 2, bytes_b = P.bn / CG * kSliceK * 2, bytes = bytes_a + bytes_b;
     float* staging = reinterpret_cast<float*>(dyn + (size_t)P.stages * bytes);
+    float* shares = staging + kStagingBytes / 4;        // split: [source][row][feature] of this threadblock's rows
     uint32_t tcols = 64;
     while (tcols < 2u * P.bn) tcols *= 2;
 
@@ -209,20 +291,24 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         for (int i = 0; i < P.stages; ++i) {
             bar_init(smem_addr(&sh.full[i]), 1);
             bar_init(smem_addr(&sh.empty[i]), 1);
+            bar_init(smem_addr(&sh.land[i]), 1);
+            bar_init(smem_addr(&sh.fixed[i]), CG);
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(smem_addr(&sh.acc_full[i]), 1);
-            bar_init(smem_addr(&sh.acc_empty[i]), 4);
+            bar_init(smem_addr(&sh.acc_empty[i]), CG * kEpilogueWarps);
         }
+        bar_init(smem_addr(&sh.got), size * kEpilogueWarps);
+        bar_init(smem_addr(&sh.taken), size * kEpilogueWarps);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         sh.failed = 0;
         tma_prefetch(&P.ma);
         tma_prefetch(&P.mb);
     }
-    if (warp == 2) tmem_alloc(smem_addr(&sh.tmem), tcols);
+    if (warp == 2) tmem_alloc<CG>(smem_addr(&sh.tmem), tcols);
     wait_for_previous();
     const int nseg = P.ragged == RAGGED_ROWS ? P.groups : P.symmetric ? P.tiles_m : 0;
-    for (int s = threadIdx.x; s < nseg; s += kThreads) sh.seg_end[s] = segment_tiles(P, s);
+    for (int s = threadIdx.x; s < nseg; s += kThreads) sh.seg_end[s] = segment_tiles<CG>(P, s);
     if (P.offsets && blockIdx.x == 0) {
         const int limit = P.ragged == RAGGED_ROWS ? P.n : P.k;
         for (int s = threadIdx.x; s < P.groups; s += kThreads)
@@ -247,34 +333,75 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         sh.total = P.tiles_m * P.tiles_n * P.groups;
     }
     fence_before();
-    __syncthreads();
+    if (size > 1)
+        cluster_sync();
+    else
+        __syncthreads();
     fence_after();
     const int total = sh.total;
     const uint32_t tmem = sh.tmem;
     volatile int* failed = &sh.failed;
 
+    // this threadblock's slices of a tile's reduction: [first, last) of ns
+    auto slices = [&](const TileAt& q, int& first, int& last) {
+        const int ns = (q.klen + kSliceK - 1) / kSliceK;
+        const int parts = CG == 2 ? 1 : size;
+        first = CG == 2 ? 0 : (int)((int64_t)ns * rank / parts);
+        last = CG == 2 ? ns : (int)((int64_t)ns * (rank + 1) / parts);
+    };
+    // a slice that runs into the next expert's rows has to be cleared there
+    auto partial = [&](const TileAt& q, int s) {
+        return P.ragged == RAGGED_REDUCE && q.klen - s * kSliceK < kSliceK;
+    };
+    // rows of a tile that are worth multiplying: a multiple of what one instruction takes
+    auto used_rows = [&](const TileAt& q) {
+        return P.ragged == RAGGED_ROWS ? min(P.bn, (q.live + 16 * CG - 1) / (16 * CG) * (16 * CG)) : P.bn;
+    };
+
     if (warp == 0) {
         if (lane == 0) {
             int it = 0;
-            for (int t = blockIdx.x; t < total; t += gridDim.x) {
-                const TileAt q = tile_at(P, &sh, t);
-                for (int k = 0; k < q.klen; k += kSliceK, ++it) {
-                    const int s = it % P.stages;
+            uint32_t flips = 0, used = 0;      // per stage: parity of its uses for cleared slices, whether any
+            for (int t = cluster; t < total; t += clusters) {
+                const TileAt q = tile_at<CG>(P, &sh, t);
+                const int m0 = q.m0 + (CG == 2 ? rank * kTileM : 0);
+                const int n0 = q.n0 + (CG == 2 ? rank * (used_rows(q) / 2) : 0);
+                int first, last;
+                slices(q, first, last);
+                for (int j = first; j < last; ++j, ++it) {
+                    const int s = it % P.stages, k = j * kSliceK;
                     if (!bar_wait(smem_addr(&sh.empty[s]), ((it / P.stages) & 1) ^ 1, failed)) goto drain;
-                    const uint32_t bar = smem_addr(&sh.full[s]);
                     const uint32_t a = smem_addr(dyn + (size_t)s * bytes), b = a + bytes_a;
-                    bar_expect(bar, bytes);
-                    if (P.a_mn) {
-                        tma_load(a, &P.ma, bar, q.m0, q.k0 + k, q.za);
-                        tma_load(a + kSliceK * 128, &P.ma, bar, q.m0 + 64, q.k0 + k, q.za);
+                    uint32_t bar = smem_addr(&sh.full[s]);
+                    if (partial(q, j)) {
+                        // lands on a barrier of this threadblock, for warp 3
+                        if (rank == 0 || CG == 1) bar_arrive(bar);
+                        bar = smem_addr(&sh.land[s]);
+                        bar_expect(bar, bytes);
+                        flips ^= 1u << s;
+                        used |= 1u << s;
+                    } else if (CG == 1) {
+                        bar_expect(bar, bytes);
                     } else {
-                        tma_load(a, &P.ma, bar, k, q.m0, q.za);
+                        if (rank == 0) bar_expect(bar, 2 * bytes);
+                        bar = cluster_addr(bar, 0);
+                    }
+                    auto load = [&](uint32_t dst, const CUtensorMap* map, int x, int y, int z) {
+                        if (CG == 1)
+                            tma_load(dst, map, bar, x, y, z);
+                        else
+                            tma_load_pair(dst, map, bar, x, y, z);
+                    };
+                    if (P.a_mn) {
+                        load(a, &P.ma, m0, q.k0 + k, q.za);
+                        load(a + kSliceK * 128, &P.ma, m0 + 64, q.k0 + k, q.za);
+                    } else {
+                        load(a, &P.ma, k, m0, q.za);
                     }
                     if (P.b_mn) {
-                        for (int i = 0; i < P.bn; i += 64)
-                            tma_load(b + i * 128, &P.mb, bar, q.n0 + i, q.k0 + k, q.zb);
+                        for (int i = 0; i < P.bn / CG; i += 64) load(b + i * 128, &P.mb, n0 + i, q.k0 + k, q.zb);
                     } else {
-                        tma_load(b, &P.mb, bar, k, q.row0 + q.n0, q.zb);
+                        load(b, &P.mb, k, q.row0 + n0, q.zb);
                     }
                 }
             }
@@ -282,52 +409,49 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             // copies in flight write this threadblock's shared memory: see
             // the last one of every stage land before leaving
             int none = 0;
-            for (int i = max(0, it - P.stages); i < it; ++i)
-                bar_wait(smem_addr(&sh.full[i % P.stages]), (i / P.stages) & 1, &none);
+            if (CG == 1 || rank == 0)
+                for (int i = max(0, it - P.stages); i < it; ++i)
+                    bar_wait(smem_addr(&sh.full[i % P.stages]), (i / P.stages) & 1, &none);
+            for (int i = 0; i < P.stages; ++i)
+                if (used >> i & 1) bar_wait(smem_addr(&sh.land[i]), (flips >> i & 1) ^ 1, &none);
         }
         __syncwarp();
-    } else if (warp == 1) {
-        const uint32_t idesc = mma_desc(P.in_bf, P.a_mn, P.b_mn, kTileM, P.bn);
+    } else if (warp == 1 && (CG == 1 || rank == 0)) {
         const uint32_t lead = kSliceK * 128, step_a = P.a_mn ? 2048 : 32, step_b = P.b_mn ? 2048 : 32;
         int it = 0, done = 0;
+        uint32_t flips = 0;
         bool ok = true;
-        for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
-            const TileAt q = tile_at(P, &sh, t);
-            if (q.klen <= 0) continue;
+        for (int t = cluster; ok && t < total; t += clusters) {
+            const TileAt q = tile_at<CG>(P, &sh, t);
+            int first, last;
+            slices(q, first, last);
+            if (first >= last) continue;
+            const uint32_t idesc = mma_desc(P.in_bf, P.a_mn, P.b_mn, CG * kTileM, used_rows(q));
             const int acc = done & 1;
             ok = __all_sync(~0u, bar_wait(smem_addr(&sh.acc_empty[acc]), ((done >> 1) & 1) ^ 1, failed));
             if (!ok) break;
             fence_after();
-            for (int k = 0; k < q.klen; k += kSliceK, ++it) {
+            for (int j = first; j < last; ++j, ++it) {
                 const int s = it % P.stages;
-                ok = __all_sync(~0u, bar_wait(smem_addr(&sh.full[s]), (it / P.stages) & 1, failed));
-                if (!ok) break;
-                const uint32_t a = smem_addr(dyn + (size_t)s * bytes), b = a + bytes_a;
-                if (P.ragged == RAGGED_REDUCE && q.klen - k < kSliceK) {
-                    // the slice runs into the next expert's rows: zero them in
-                    // both operands (0 x Inf or NaN would not be 0)
-                    const int live = q.klen - k, dead = kSliceK - live;
-                    const int blocks = (kTileM + P.bn) / 64;
-                    for (int i = lane; i < blocks * dead * 8; i += 32) {
-                        const int blk = i / (dead * 8), o = i % (dead * 8);
-                        *reinterpret_cast<uint4*>(dyn + (size_t)s * bytes + blk * (kSliceK * 128) + live * 128 + o * 16) =
-                            make_uint4(0, 0, 0, 0);
-                    }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();
+                ok = bar_wait(smem_addr(&sh.full[s]), (it / P.stages) & 1, failed);
+                if (partial(q, j)) {
+                    ok = ok && bar_wait(smem_addr(&sh.fixed[s]), flips >> s & 1, failed);
+                    flips ^= 1u << s;
                 }
+                if (!(ok = __all_sync(~0u, ok))) break;
+                const uint32_t a = smem_addr(dyn + (size_t)s * bytes), b = a + bytes_a;
                 if (lane == 0) {
                     fence_after();
 #pragma unroll
-                    for (int j = 0; j < kSliceK / 16; ++j)
-                        mma_f16(tmem + acc * P.bn, operand_desc(a + j * step_a, lead, 1024),
-                                operand_desc(b + j * step_b, lead, 1024), idesc, k > 0 || j > 0);
-                    mma_commit(smem_addr(&sh.empty[s]));
+                    for (int i = 0; i < kSliceK / 16; ++i)
+                        mma_f16<CG>(tmem + acc * P.bn, operand_desc(a + i * step_a, lead, 1024),
+                                    operand_desc(b + i * step_b, lead, 1024), idesc, j > first || i > 0);
+                    mma_commit<CG>(smem_addr(&sh.empty[s]));
                 }
                 __syncwarp();
             }
             if (!ok) break;
-            if (lane == 0) mma_commit(smem_addr(&sh.acc_full[acc]));
+            if (lane == 0) mma_commit<CG>(smem_addr(&sh.acc_full[acc]));
             __syncwarp();
             ++done;
         }
@@ -339,56 +463,194 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             bar_wait(smem_addr(&sh.empty[s]), ((it - 1) / P.stages) & 1, &none);
         }
         __syncwarp();
+    } else if (warp == 3 && P.ragged == RAGGED_REDUCE) {
+        // 0 x Inf or NaN would not be 0: both operands are cleared
+        int it = 0;
+        uint32_t flips = 0;
+        for (int t = cluster; t < total; t += clusters) {
+            const TileAt q = tile_at<CG>(P, &sh, t);
+            int first, last;
+            slices(q, first, last);
+            if (first >= last) continue;
+            it += last - first;
+            if (!partial(q, last - 1)) continue;
+            const int s = (it - 1) % P.stages;
+            if (!__all_sync(~0u, bar_wait(smem_addr(&sh.land[s]), flips >> s & 1, failed))) break;
+            flips ^= 1u << s;
+            unsigned char* at = dyn + (size_t)s * bytes;
+            const int left = q.klen - (last - 1) * kSliceK, dead = kSliceK - left;
+            for (int i = lane; i < (int)(bytes / (kSliceK * 128)) * dead * 8; i += 32) {
+                const int blk = i / (dead * 8), o = i % (dead * 8);
+                *reinterpret_cast<uint4*>(at + blk * (kSliceK * 128) + left * 128 + o * 16) = make_uint4(0, 0, 0, 0);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+                if (CG == 2)
+                    bar_arrive_cluster(cluster_addr(smem_addr(&sh.fixed[s]), 0));
+                else
+                    bar_arrive(smem_addr(&sh.fixed[s]));
+            }
+        }
+        __syncwarp();
     } else if (warp >= 4) {
-        const int quad = warp & 3;
-        float* st = staging + quad * 32 * kStagePitch;
-        int done = 0;
-        for (int t = blockIdx.x; t < total; t += gridDim.x) {
-            const TileAt q = tile_at(P, &sh, t);
-            const bool some = q.klen > 0;
+        const int quad = warp & 3, half = (warp - 4) >> 2;
+        float* st = staging + (warp - 4) * 32 * kStagePitch;
+        const int side = P.symmetric ? 1 : 0;
+        uint32_t release[2];
+        for (int i = 0; i < 2; ++i)
+            release[i] = CG == 2 ? cluster_addr(smem_addr(&sh.acc_empty[i]), 0) : smem_addr(&sh.acc_empty[i]);
+        int done = 0, round = 0;
+        for (int t = cluster; t < total; t += clusters) {
+            const TileAt q = tile_at<CG>(P, &sh, t);
+            int first, last;
+            slices(q, first, last);
+            const bool some = first < last;
             const int acc = done & 1;
+            const int feat = q.m0 + (CG == 2 ? rank * kTileM : 0) + quad * 32, nfeat = P.m - feat;
+            const int64_t row = (int64_t)q.row0 + q.n0;
+            const float alpha = P.alpha * (P.alpha_of ? P.alpha_of[q.g] : 1.f);
+            const float beta = P.beta * (P.beta_of ? P.beta_of[q.g] : 1.f);
+            const bool ahead = P.c && P.vec && size == CG;     // C is fetched a block ahead
+            uint4 next[4];
+            if (ahead) fetch_c(P, lane, q.g, row + half * 32, q.live - half * 32, feat, nfeat, next);
             if (some) {
                 if (!__all_sync(~0u, bar_wait(smem_addr(&sh.acc_full[acc]), (done >> 1) & 1, failed))) break;
                 fence_after();
             }
-            const float alpha = P.alpha * (P.alpha_of ? P.alpha_of[q.g] : 1.f);
-            const float beta = P.beta * (P.beta_of ? P.beta_of[q.g] : 1.f);
-            const int live = min(P.bn, q.rows - q.n0), feat = q.m0 + quad * 32;
-            for (int c = 0; c < live; c += 32) {
-                float v[32];
+            if (size > CG) {
+                // shares of the last tile have been read by their owners
+                if (!__all_sync(~0u, bar_wait(smem_addr(&sh.taken), (round & 1) ^ 1, failed))) break;
+            }
+            for (int c = half * 32; c < q.live; c += 64) {
+                uint32_t v[32];
                 if (some) {
                     tmem_load32(tmem + ((uint32_t)(quad * 32) << 16) + acc * P.bn + c, v);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = 0.f;
+                    for (int i = 0; i < 32; ++i) v[i] = 0;
                 }
+                if (size > CG) {
+                    const int own = P.bn / size;
+                    const uint32_t at = smem_addr(shares + (size_t)rank * own * kTileM + quad * 32 + lane);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) st[i * kStagePitch + lane] = v[i];
-                __syncwarp();
-                write_block(P, st, lane, q.g, (int64_t)q.row0 + q.n0 + c, min(32, live - c), feat, P.m - feat,
-                            P.symmetric ? 1 : 0, alpha, beta);
-                __syncwarp();
-                if (P.symmetric && q.n0 + c + 31 > feat) {
+                    for (int i = 0; i < 32; ++i) {
+                        const int r = c + i;
+                        if (r < q.live)
+                            store_cluster(cluster_addr(at + (r % own) * (kTileM * 4), r / own), __uint_as_float(v[i]));
+                    }
+                    continue;
+                }
+                if (!P.vec) {
+                    write_lanes(P, v, q.g, row + c, q.live - c, feat + lane, side, alpha, beta);
+                } else {
+                    uint4 now[4];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) st[lane * kStagePitch + i] = v[i];
+                    for (int i = 0; i < 4; ++i) now[i] = next[i];
+                    if (ahead && c + 64 < q.live)
+                        fetch_c(P, lane, q.g, row + c + 64, q.live - c - 64, feat, nfeat, next);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) st[i * kStagePitch + lane] = __uint_as_float(v[i]);
                     __syncwarp();
-                    write_block(P, st, lane, q.g, feat, min(32, P.m - feat), q.n0 + c, live - c, -1, alpha, beta);
+                    write_block(P, st, lane, q.g, row + c, q.live - c, feat, nfeat, side, alpha, beta,
+                                ahead ? now : nullptr);
+                    __syncwarp();
+                }
+                if (side && q.n0 + c + 31 > feat) {
+                    // the mirror image: rows are features, features are rows
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) st[lane * kStagePitch + i] = __uint_as_float(v[i]);
+                    __syncwarp();
+                    write_block(P, st, lane, q.g, feat, nfeat, q.n0 + c, q.live - c, -1, alpha, beta, nullptr);
                     __syncwarp();
                 }
             }
             if (some) {
                 fence_before();
-                if (lane == 0) bar_arrive(smem_addr(&sh.acc_empty[acc]));
+                if (lane == 0) {
+                    if (CG == 2)
+                        bar_arrive_cluster(release[acc]);
+                    else
+                        bar_arrive(release[acc]);
+                }
                 ++done;
+            }
+            if (size > CG) {
+                __syncwarp();
+                if (lane < size) bar_arrive_cluster(cluster_addr(smem_addr(&sh.got), lane));
+                if (!__all_sync(~0u, bar_wait(smem_addr(&sh.got), round & 1, failed))) break;
+                // sum the shares of this threadblock's rows in rank order
+                const int own = P.bn / size, base = rank * own, mine = min(own, q.live - base);
+                const int id = (warp - 4) * 32 + lane;
+                const int left = P.m - q.m0;
+                if (P.vec) {
+                    for (int i = id; i < mine * (kTileM / 8); i += 32 * kEpilogueWarps) {
+                        const int r = i / (kTileM / 8), f = i % (kTileM / 8) * 8;
+                        int lo, hi;
+                        side_range(side, row + base + r, q.m0 + f, left - f, lo, hi);
+                        if (lo >= hi) continue;
+                        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                        for (int s = 0; s < size; ++s) {
+                            const float4* p =
+                                reinterpret_cast<const float4*>(shares + ((size_t)s * own + r) * kTileM + f);
+                            const float4 a = p[0], b = p[1];
+                            v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
+                            v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+                        }
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[e] *= alpha;
+                        finish8(P, v, q.g, row + base + r, q.m0 + f, lo, hi, beta, nullptr);
+                    }
+                } else {
+                    for (int i = id; i < mine * kTileM; i += 32 * kEpilogueWarps) {
+                        const int r = i / kTileM, f = q.m0 + i % kTileM;
+                        const int64_t n = row + base + r;
+                        if (f >= P.m || (side && f > n)) continue;
+                        float v = 0.f;
+                        for (int s = 0; s < size; ++s) v += shares[((size_t)s * own + r) * kTileM + i % kTileM];
+                        finish1(P, alpha * v, q.g, n, f, beta,
+                                P.bias ? load1(P.bias + q.g * P.bs_bias + f, P.in_bf) : 0.f,
+                                P.c ? load1(P.c + q.g * P.bs_c + n * P.ld_c + f, P.in_bf) : 0.f);
+                    }
+                }
+                if (side) {
+                    // the mirror image: 8 of this threadblock's rows at a time for one feature
+                    const int parts = (mine + 7) / 8;
+                    for (int i = id; i < parts * kTileM; i += 32 * kEpilogueWarps) {
+                        const int f = i % kTileM, r0 = i / kTileM * 8, n = q.n0 + base + r0;
+                        int lo, hi;
+                        side_range(-1, q.m0 + f, n, mine - r0, lo, hi);
+                        if (f >= left || lo >= hi) continue;
+                        float v[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            v[e] = 0.f;
+                            if (e >= lo && e < hi)
+                                for (int s = 0; s < size; ++s)
+                                    v[e] += shares[((size_t)s * own + r0 + e) * kTileM + f];
+                            v[e] *= alpha;
+                        }
+                        finish8(P, v, q.g, q.m0 + f, n, lo, hi, beta, nullptr);
+                    }
+                }
+                __syncwarp();
+                if (lane < size) bar_arrive_cluster(cluster_addr(smem_addr(&sh.taken), lane));
+                ++round;
             }
         }
         fence_before();
     }
-    __syncthreads();
-    if (sh.failed && threadIdx.x == 0) atomicCAS(&g_status[0], 0, (int)CCL_ERR_TIMEOUT);
+    if (sh.failed && lane == 0) atomicCAS(&g_status[0], 0, (int)CCL_ERR_TIMEOUT);
+    __syncwarp();
+    // no threadblock leaves while another one of its cluster may still reach
+    // its memory or its barriers
+    if (size > 1)
+        cluster_sync();
+    else
+        __syncthreads();
     if (warp == 2) {
         fence_after();
-        tmem_free(tmem, tcols);
+        tmem_free<CG>(tmem, tcols);
     }
 }
 
@@ -622,8 +884,9 @@ static ccl_status_t device(const Device** out)
                  "cuTensorMapEncodeTiled");
         if (q != cudaDriverEntryPointSuccess || !fn) return fail(CCL_ERR_CUDA, "the driver has no tensor maps");
         all[d].encode = (EncodeFn)fn;
-        TRY_CUDA(cudaFuncSetAttribute(product_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBudget),
-                 "shared memory of the product kernel");
+        for (auto kernel : {product_kernel<1>, product_kernel<2>})
+            TRY_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBudget),
+                     "shared memory of the product kernel");
         all[d].ready = true;
     }
     *out = &all[d];
@@ -631,18 +894,22 @@ static ccl_status_t device(const Device** out)
 }
 
 template <typename Arg>
-static ccl_status_t launch(void (*kernel)(Arg), dim3 grid, int threads, size_t smem, cudaStream_t stream, const Arg& arg)
+static ccl_status_t launch(void (*kernel)(Arg), dim3 grid, int threads, size_t smem, cudaStream_t stream, const Arg& arg,
+                           int cluster = 1)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     TRY_CUDA(cudaLaunchKernelEx(&cfg, kernel, arg), "launch");
     return CCL_OK;
 }
@@ -715,43 +982,7 @@ static ccl_status_t encode(const Device* dev, CUtensorMap* map, const Matrix& m,
     return CCL_OK;
 }
 
-// Complete a product (operands, tile, stages) and launch it.
-static ccl_status_t run(Product P, Matrix a, Matrix b, cudaStream_t stream)
-{
-    const Device* dev = nullptr;
-    TRY(device(&dev));
-    P.tiles_m = (P.m + kTileM - 1) / kTileM;
-    // Rows per tile: the width whose waves of tiles cost least.  Per 64-wide
-    // slice a tile takes 2 clocks per row of matrix instructions, or the
-    // time its operands take from L2 at about 70 bytes a clock; about 1500
-    // clocks per tile go to filling and draining.
-    static const int widths[] = {256, 192, 128, 64, 32};
-    double best = 0;
-    for (int w : widths) {
-        if (P.b_mn && w % 64) continue;
-        const double rows = P.ragged == RAGGED_ROWS ? std::max(1.0, (double)P.n / P.groups) : (double)P.n;
-        const double groups = P.ragged == RAGGED_ROWS ? std::min(P.n, P.groups) : P.groups;
-        const double reduce = P.ragged == RAGGED_REDUCE ? (double)P.k / P.groups : P.k;
-        double tiles = groups * P.tiles_m * std::ceil(rows / w);
-        if (P.symmetric) tiles *= 0.5 + 0.5 / P.tiles_m;
-        const double slice = std::max(2.0 * w, (kTileM + w) * 128.0 / 70);
-        const double cost = std::ceil(tiles / dev->sms) * (std::ceil(reduce / kSliceK) * slice + 1500 + 8 * w);
-        if (best == 0 || cost < best) {
-            best = cost;
-            P.bn = w;
-        }
-    }
-    P.tiles_n = (int)((P.n + (int64_t)P.bn - 1) / P.bn);
-    const int bytes = (kTileM + P.bn) * kSliceK * 2;
-    P.stages = std::min(kMaxStages, (kSmemBudget - 1024 - kStagingBytes) / bytes);
-    const int64_t most = P.ragged == RAGGED_ROWS ? (int64_t)P.tiles_m * ((int64_t)P.tiles_n + P.groups)
-                                                 : (int64_t)P.tiles_m * P.tiles_n * P.groups;
-    if (most > INT32_MAX) return fail(CCL_ERR_UNSUPPORTED, "too many tiles");
-    TRY(encode(dev, &P.ma, a, 64, P.a_mn ? kSliceK : kTileM));
-    TRY(encode(dev, &P.mb, b, 64, P.b_mn ? kSliceK : P.bn));
-    const size_t smem = 1024 + (size_t)P.stages * bytes + kStagingBytes;
-    return launch(product_kernel, dim3((unsigned)std::min<int64_t>(most, dev->sms)), kThreads, smem, stream, P);
-}
+static bool vectors(const void* p, int64_t ld, int64_t bs) { return aligned16(p) && ld % 8 == 0 && bs % 8 == 0; }
 
 static void set_out(Product* P, void* out, int64_t ld, int64_t bs, bool bf)
 {
@@ -759,7 +990,6 @@ static void set_out(Product* P, void* out, int64_t ld, int64_t bs, bool bf)
     P->ld_out = ld;
     P->bs_out = bs;
     P->out_bf = bf;
-    P->vec_out = aligned16(out) && ld % 8 == 0 && bs % 8 == 0;
 }
 static void set_c(Product* P, const void* c, int64_t ld, int64_t bs, float beta)
 {
@@ -767,7 +997,76 @@ static void set_c(Product* P, const void* c, int64_t ld, int64_t bs, float beta)
     P->ld_c = ld;
     P->bs_c = bs;
     P->beta = beta;
-    P->vec_c = aligned16(c) && ld % 8 == 0 && bs % 8 == 0;
+}
+// how the epilogue may access its matrices (once all of them are set)
+static void set_vec(Product* P)
+{
+    P->vec = vectors(P->out, P->ld_out, P->bs_out) && (!P->pre || vectors(P->pre, P->ld_pre, 0)) &&
+             (!P->c || vectors(P->c, P->ld_c, P->bs_c)) && (!P->bias || vectors(P->bias, 0, P->bs_bias));
+}
+
+// How a product is cut up.
+struct Shape {
+    int cg, bn, split;
+    double cost;
+};
+
+// The cheapest way by an estimate in clocks: waves of tiles over the SMs (or
+// pairs, or clusters), each tile the longer of its products with their loads
+// and of its epilogue.  Per 64-wide slice a threadblock's matrix
+// instructions take 2 clocks per row (128 features, either form), its loads
+// come from L2 at about 70 bytes a clock.
+static Shape choose(const Product& P, int sms)
+{
+    const double rows = P.ragged == RAGGED_ROWS ? std::max(1.0, (double)P.n / P.groups) : (double)P.n;
+    const double groups = P.ragged == RAGGED_ROWS ? std::min(P.n, P.groups) : P.groups;
+    const double reduce = P.ragged == RAGGED_REDUCE ? std::max(1.0, (double)P.k / P.groups) : P.k;
+    const double slices = std::ceil(reduce / kSliceK);
+    Shape best = {0, 0, 0, 0};
+    for (int cg = 1; cg <= 2; ++cg) {
+        for (int bn : {256, 192, 128, 64, 32}) {
+            if (bn / cg % (P.b_mn ? 64 : 16)) continue;
+            for (int split = 1; split <= (cg == 2 || bn > 128 || bn * 8 < rows ? 1 : 8); split *= 2) {
+                if (split > 1 && split * 2 > slices) continue;
+                const double tiles_m = std::ceil((double)P.m / (cg * kTileM)), tiles_n = std::ceil(rows / bn);
+                double tiles = groups * tiles_m * tiles_n;
+                if (P.symmetric) tiles = groups * (tiles_m * tiles_n + std::max(tiles_m, tiles_n)) / 2;
+                const double slice = std::max(2.0 * bn, (kTileM + bn / cg) * 128.0 / 70);
+                const double main = std::ceil(slices / split) * slice;
+                const double epilogue = 400 + 8.0 * std::min((double)bn, rows) / split + (split > 1 ? 12.0 * bn + 1500 : 0);
+                const double waves = std::ceil(tiles / (sms / (cg * split)));
+                const double cost = waves * std::max(main, epilogue) + std::min(main, epilogue) + 1500;
+                if (best.cg == 0 || cost < best.cost) best = {cg, bn, split, cost};
+            }
+        }
+    }
+    return best;
+}
+
+// Complete a product (operands, tile, stages) and launch it.
+static ccl_status_t run(Product P, Matrix a, Matrix b, cudaStream_t stream)
+{
+    set_vec(&P);
+    const Device* dev = nullptr;
+    TRY(device(&dev));
+    const Shape sh = choose(P, dev->sms);
+    const int size = sh.cg == 2 ? 2 : sh.split;
+    P.bn = sh.bn;
+    P.split = sh.split;
+    P.tiles_m = (int)((P.m + (int64_t)sh.cg * kTileM - 1) / (sh.cg * kTileM));
+    P.tiles_n = (int)((P.n + (int64_t)P.bn - 1) / P.bn);
+    const int bytes = (kTileM + P.bn / sh.cg) * kSliceK * 2;
+    const int fixed = 1024 + kStagingBytes + (sh.split > 1 ? P.bn * kTileM * 4 : 0);
+    P.stages = std::min(kMaxStages, (kSmemBudget - fixed) / bytes);
+    const int64_t most = P.ragged == RAGGED_ROWS ? (int64_t)P.tiles_m * ((int64_t)P.tiles_n + P.groups)
+                                                 : (int64_t)P.tiles_m * P.tiles_n * P.groups;
+    if (most > INT32_MAX) return fail(CCL_ERR_UNSUPPORTED, "too many tiles");
+    TRY(encode(dev, &P.ma, a, 64, P.a_mn ? kSliceK : kTileM));
+    TRY(encode(dev, &P.mb, b, 64, P.b_mn ? kSliceK : P.bn / sh.cg));
+    const size_t smem = fixed + (size_t)P.stages * bytes;
+    const int64_t clusters = std::min<int64_t>(most, dev->sms / size);
+    return launch(sh.cg == 2 ? product_kernel<2> : product_kernel<1>, dim3((unsigned)(clusters * size)), kThreads, smem,
+                  stream, P, size);
 }
 
 // --------------------------------------------------------- linear layers
@@ -859,12 +1158,10 @@ static ccl_status_t linear(const ccl_linear_t* a, char* base, int64_t* need, cud
     if (a->z) {
         P.pre = (uint16_t*)a->z;
         P.ld_pre = ldz;
-        P.vec_pre = aligned16(a->z) && ldz % 8 == 0;
     }
     if (a->bias) {
         P.bias = (const uint16_t*)a->bias;
-        P.bs_bias = sb;
-        P.vec_bias = aligned16(a->bias) && (count == 1 || sb % 8 == 0);
+        P.bs_bias = count > 1 ? sb : 0;
     }
     return run(P, w, x, stream);
 }

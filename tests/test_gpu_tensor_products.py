@@ -308,6 +308,29 @@ def test_grouped_backward(ccl, counts, n, k, act, dtype):
     check_grads(got, dy, x, w, z, act, list(zip(offs[:-1], offs[1:])), dtype)
 
 
+@pytest.mark.parametrize("counts", [[3, 70, 0, 65, 1, 127, 200, 33] * 5, [900, 1, 1300, 77], [64] * 24],
+                         ids=lambda c: f"{len(c)}x{sum(c)}")
+def test_grouped_backward_with_many_tiles_per_threadblock(ccl, counts):
+    """Several experts' tiles pass through each threadblock's ring of stages,
+    with the cleared last slices of more than one in flight."""
+    offs = offsets_of(counts)
+    rows, e, n, k, dtype = offs[-1], len(counts), 1032, 1288, torch.bfloat16
+    g = gen(rows)
+    dy, x = rnd(g, rows, n, dtype=dtype), rnd(g, rows, k, dtype=dtype)
+    w = rnd(g, e, n, k, dtype=dtype)
+    o = torch.tensor(offs, dtype=torch.int32, device="cuda")
+    got = ccl.grouped_linear_backward(dy, x, w, o, bias=True)
+    ccl.tensor_status()
+    check_grads(got, dy, x, w, None, 0, list(zip(offs[:-1], offs[1:])), dtype)
+
+
+@pytest.mark.parametrize("rows,n,k", [(4100, 4104, 520), (16, 5000, 4096), (1, 3000, 6000), (300, 512, 8192),
+                                      (2048, 2048, 2056)])
+def test_linear_large_and_split(ccl, rows, n, k):
+    check_linear(ccl, rows, n, k, torch.bfloat16, ccl.ACT_NONE, True, True, False)
+    ccl.tensor_status()
+
+
 def test_grouped_with_one_expert_equals_the_dense_product(ccl):
     g = gen(11)
     x, w = rnd(g, 77, 96, dtype=torch.bfloat16), rnd(g, 1, 200, 96, dtype=torch.bfloat16)
