@@ -51,14 +51,13 @@ constexpr int kMaxStages = 10;
 constexpr int kMaxGroups = 1024;
 constexpr int kEpilogueWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpilogueWarps;
-constexpr int kStagePitch = 36;                 // floats; rows 4 banks apart: conflict-free 16-byte reads
-constexpr int kStagingBytes = kEpilogueWarps * 32 * kStagePitch * 4;
+constexpr int kStagingBytes = kEpilogueWarps * 2 * 2048;   // two blocks of 32 x 32 outputs per epilogue warp
 constexpr int kSmemBudget = 227 * 1024 - 6 * 1024;   // dynamic part; the rest is static
 
 enum { DENSE = 0, RAGGED_ROWS = 1, RAGGED_REDUCE = 2 };
 
 struct Product {
-    CUtensorMap ma, mb;
+    CUtensorMap ma, mb, mo, mp;    // operands; out and pre where TMA can store them
     uint16_t *out, *pre;           // pre: the sum before the activation (may be null)
     const uint16_t *c, *bias;
     const float *alpha_of, *beta_of;   // device factors per batch entry (may be null)
@@ -69,6 +68,7 @@ struct Product {
     int32_t bn, stages, split, tiles_m, tiles_n;
     int32_t ragged, symmetric, act;
     int32_t in_bf, out_bf, a_mn, b_mn;
+    int32_t tma_out, tma_pre;
     int32_t vec;                   // rows of out, pre, c and bias allow 16-byte accesses
 };
 
@@ -217,57 +217,48 @@ __device__ __forceinline__ void side_range(int side, int64_t n, int f, int nfeat
     if (side < 0) lo = (int)max((int64_t)0, n - f + 1);
 }
 
-// C of a thread's four groups of 8 in a block of 32 rows x 32 features
-__device__ __forceinline__ void fetch_c(const Product& P, int lane, int g, int64_t row, int nrows, int feat, int nfeat,
-                                        uint4 c[4])
+// 32 rows of C at one feature per lane: 64 neighbouring bytes a row and warp,
+// whatever the alignment
+__device__ __forceinline__ void fetch_c(const Product& P, uint16_t c[32], int g, int64_t row, int nrows, int f)
 {
-    const int k = (lane & 3) * 8;
+    const uint16_t* p = P.c + g * P.bs_c + row * P.ld_c + f;
+    if (f < P.m && nrows >= 32) {
 #pragma unroll
-    for (int pass = 0; pass < 4; ++pass) {
-        const int r = pass * 8 + (lane >> 2);
-        if (r < nrows && k + 8 <= nfeat)
-            c[pass] = *reinterpret_cast<const uint4*>(P.c + g * P.bs_c + (row + r) * P.ld_c + feat + k);
+        for (int i = 0; i < 32; ++i, p += P.ld_c) c[i] = *p;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i, p += P.ld_c) c[i] = f < P.m && i < nrows ? *p : (uint16_t)0;
     }
 }
 
-// 32 rows x 32 features, staged as st[row][feature], through the epilogue
-// into global memory; 8 features per thread and step.
-__device__ __forceinline__ void write_block(const Product& P, const float* st, int lane, int g, int64_t row, int nrows,
-                                            int feat, int nfeat, int side, float alpha, float beta, const uint4* c)
+// A block of 32 rows x 32 features (one feature per lane) to global memory:
+// through shared memory and a TMA store where the whole block may be
+// written (the parts of it outside the matrix are cut off by TMA), else 64
+// neighbouring bytes of a row at a time.  side: symmetric outputs, only
+// feature <= row.  buf: this warp's two 2 KB buffers, used in turn.
+template <bool BF>
+__device__ __forceinline__ void store_block(const CUtensorMap* map, uint16_t* p, int64_t ld, const float v[32],
+                                            unsigned char* buf, int& turn, bool tma, int lane, int x, int y, int z,
+                                            int nrows, int nfeat, int below)
 {
+    if (tma && nfeat > 0) {
+        if (lane == 0) tma_stores_read<1>();
+        __syncwarp();
+        uint16_t* b = reinterpret_cast<uint16_t*>(buf + (turn & 1) * 2048) + lane;
 #pragma unroll
-    for (int pass = 0; pass < 4; ++pass) {
-        const int r = pass * 8 + (lane >> 2), k = (lane & 3) * 8;
-        int lo, hi;
-        side_range(side, row + r, feat + k, nfeat - k, lo, hi);
-        if (r >= nrows || lo >= hi) continue;
-        float v[8];
-        const float4 a = *reinterpret_cast<const float4*>(st + r * kStagePitch + k);
-        const float4 b = *reinterpret_cast<const float4*>(st + r * kStagePitch + k + 4);
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        for (int i = 0; i < 32; i += 2) {
+            const uint32_t u = pack2<BF>(v[i], v[i + 1]);
+            b[i * 32] = (uint16_t)u;
+            b[i * 32 + 32] = (uint16_t)(u >> 16);
+        }
+        fence_async();
+        __syncwarp();
+        if (lane == 0) tma_store(map, smem_addr(buf + (turn & 1) * 2048), x, y, z);
+        ++turn;
+    } else if (lane < nfeat) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= alpha;
-        finish8(P, v, g, row + r, feat + k, lo, hi, beta, c && k + 8 <= nfeat ? c + pass : nullptr);
-    }
-}
-
-// Rows that 16-byte accesses cannot address: every lane writes its own
-// feature, so a warp still writes 32 neighbours at a time.
-__device__ __forceinline__ void write_lanes(const Product& P, const uint32_t acc[32], int g, int64_t row, int nrows,
-                                            int f, int side, float alpha, float beta)
-{
-    if (f >= P.m) return;
-    const float bias = P.bias ? load1(P.bias + g * P.bs_bias + f, P.in_bf) : 0.f;
-#pragma unroll
-    for (int i0 = 0; i0 < 32; i0 += 16) {
-        float c[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            c[i] = P.c && i0 + i < nrows ? load1(P.c + g * P.bs_c + (row + i0 + i) * P.ld_c + f, P.in_bf) : 0.f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (i0 + i < nrows && (!side || f <= row + i0 + i))
-                finish1(P, alpha * __uint_as_float(acc[i0 + i]), g, row + i0 + i, f, beta, bias, c[i]);
+        for (int i = 0; i < 32; ++i, p += ld)
+            if (i < nrows && i >= below) store1(p, v[i], BF);
     }
 }
 
@@ -282,8 +273,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     const int rank = size > 1 ? (int)cluster_rank() : 0;
     const int cluster = blockIdx.x / size, clusters = gridDim.x / size;
     const uint32_t bytes_a = kTileM * kSliceK * 2, bytes_b = P.bn / CG * kSliceK * 2, bytes = bytes_a + bytes_b;
-    float* staging = reinterpret_cast<float*>(dyn + (size_t)P.stages * bytes);
-    float* shares = staging + kStagingBytes / 4;        // split: [source][row][feature] of this threadblock's rows
+    unsigned char* staging = dyn + (size_t)P.stages * bytes;
+    float* shares = reinterpret_cast<float*>(staging + kStagingBytes);   // split: [source][row][feature], own rows
     uint32_t tcols = 64;
     while (tcols < 2u * P.bn) tcols *= 2;
 
@@ -305,7 +296,6 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         tma_prefetch(&P.ma);
         tma_prefetch(&P.mb);
     }
-    if (warp == 2) tmem_alloc<CG>(smem_addr(&sh.tmem), tcols);
     wait_for_previous();
     const int nseg = P.ragged == RAGGED_ROWS ? P.groups : P.symmetric ? P.tiles_m : 0;
     for (int s = threadIdx.x; s < nseg; s += kThreads) sh.seg_end[s] = segment_tiles<CG>(P, s);
@@ -332,22 +322,27 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     } else if (!nseg && threadIdx.x == 0) {
         sh.total = P.tiles_m * P.tiles_n * P.groups;
     }
-    fence_before();
     if (size > 1)
         cluster_sync();
     else
         __syncthreads();
-    fence_after();
     const int total = sh.total;
-    const uint32_t tmem = sh.tmem;
     volatile int* failed = &sh.failed;
+    // loads start while tensor memory is being allocated
+    uint32_t tmem = 0;
+    if (warp == 2) tmem_alloc<CG>(smem_addr(&sh.tmem), tcols);
+    if (warp != 0 && warp != 3) {
+        fence_before();
+        named_sync(1, 64 + 32 * kEpilogueWarps);
+        fence_after();
+        tmem = sh.tmem;
+    }
 
     // this threadblock's slices of a tile's reduction: [first, last) of ns
     auto slices = [&](const TileAt& q, int& first, int& last) {
         const int ns = (q.klen + kSliceK - 1) / kSliceK;
-        const int parts = CG == 2 ? 1 : size;
-        first = CG == 2 ? 0 : (int)((int64_t)ns * rank / parts);
-        last = CG == 2 ? ns : (int)((int64_t)ns * (rank + 1) / parts);
+        first = CG == 2 || size == 1 ? 0 : (int)((int64_t)ns * rank / size);
+        last = CG == 2 || size == 1 ? ns : (int)((int64_t)ns * (rank + 1) / size);
     };
     // a slice that runs into the next expert's rows has to be cleared there
     auto partial = [&](const TileAt& q, int s) {
@@ -360,7 +355,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 
     if (warp == 0) {
         if (lane == 0) {
-            int it = 0;
+            int s = 0, loaded = 0;
+            uint32_t phase = 0;                // of the current stage
             uint32_t flips = 0, used = 0;      // per stage: parity of its uses for cleared slices, whether any
             for (int t = cluster; t < total; t += clusters) {
                 const TileAt q = tile_at<CG>(P, &sh, t);
@@ -368,10 +364,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                 const int n0 = q.n0 + (CG == 2 ? rank * (used_rows(q) / 2) : 0);
                 int first, last;
                 slices(q, first, last);
-                for (int j = first; j < last; ++j, ++it) {
-                    const int s = it % P.stages, k = j * kSliceK;
-                    if (!bar_wait(smem_addr(&sh.empty[s]), ((it / P.stages) & 1) ^ 1, failed)) goto drain;
-                    const uint32_t a = smem_addr(dyn + (size_t)s * bytes), b = a + bytes_a;
+                for (int j = first; j < last; ++j) {
+                    const int k = j * kSliceK;
+                    if (!bar_wait(smem_addr(&sh.empty[s]), phase ^ 1, failed)) goto drain;
+                    const uint32_t a = smem_addr(dyn) + s * bytes, b = a + bytes_a;
                     uint32_t bar = smem_addr(&sh.full[s]);
                     if (partial(q, j)) {
                         // lands on a barrier of this threadblock, for warp 3
@@ -403,6 +399,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                     } else {
                         load(b, &P.mb, k, q.row0 + n0, q.zb);
                     }
+                    ++loaded;
+                    if (++s == P.stages) s = 0, phase ^= 1;
                 }
             }
         drain:
@@ -410,57 +408,57 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             // the last one of every stage land before leaving
             int none = 0;
             if (CG == 1 || rank == 0)
-                for (int i = max(0, it - P.stages); i < it; ++i)
-                    bar_wait(smem_addr(&sh.full[i % P.stages]), (i / P.stages) & 1, &none);
+                for (int i = 0; i < min(loaded, P.stages); ++i) {
+                    if (--s < 0) s = P.stages - 1, phase ^= 1;
+                    bar_wait(smem_addr(&sh.full[s]), phase, &none);
+                }
             for (int i = 0; i < P.stages; ++i)
                 if (used >> i & 1) bar_wait(smem_addr(&sh.land[i]), (flips >> i & 1) ^ 1, &none);
         }
         __syncwarp();
-    } else if (warp == 1 && (CG == 1 || rank == 0)) {
-        const uint32_t lead = kSliceK * 128, step_a = P.a_mn ? 2048 : 32, step_b = P.b_mn ? 2048 : 32;
-        int it = 0, done = 0;
-        uint32_t flips = 0;
-        bool ok = true;
-        for (int t = cluster; ok && t < total; t += clusters) {
-            const TileAt q = tile_at<CG>(P, &sh, t);
-            int first, last;
-            slices(q, first, last);
-            if (first >= last) continue;
-            const uint32_t idesc = mma_desc(P.in_bf, P.a_mn, P.b_mn, CG * kTileM, used_rows(q));
-            const int acc = done & 1;
-            ok = __all_sync(~0u, bar_wait(smem_addr(&sh.acc_empty[acc]), ((done >> 1) & 1) ^ 1, failed));
-            if (!ok) break;
-            fence_after();
-            for (int j = first; j < last; ++j, ++it) {
-                const int s = it % P.stages;
-                ok = bar_wait(smem_addr(&sh.full[s]), (it / P.stages) & 1, failed);
-                if (partial(q, j)) {
-                    ok = ok && bar_wait(smem_addr(&sh.fixed[s]), flips >> s & 1, failed);
-                    flips ^= 1u << s;
-                }
-                if (!(ok = __all_sync(~0u, ok))) break;
-                const uint32_t a = smem_addr(dyn + (size_t)s * bytes), b = a + bytes_a;
-                if (lane == 0) {
+    } else if (warp == 1) {
+        if (lane == 0 && (CG == 1 || rank == 0)) {
+            const uint32_t lead = kSliceK * 128, step_a = P.a_mn ? 2048 : 32, step_b = P.b_mn ? 2048 : 32;
+            const uint64_t base = operand_desc(0, lead, 1024);
+            int s = 0, issued = 0, done = 0;
+            uint32_t phase = 0, flips = 0;
+            for (int t = cluster; t < total; t += clusters) {
+                const TileAt q = tile_at<CG>(P, &sh, t);
+                int first, last;
+                slices(q, first, last);
+                if (first >= last) continue;
+                const uint32_t idesc = mma_desc(P.in_bf, P.a_mn, P.b_mn, CG * kTileM, used_rows(q));
+                const int acc = done & 1;
+                if (!bar_wait(smem_addr(&sh.acc_empty[acc]), ((done >> 1) & 1) ^ 1, failed)) goto stop;
+                fence_after();
+                for (int j = first; j < last; ++j) {
+                    if (!bar_wait(smem_addr(&sh.full[s]), phase, failed)) goto stop;
+                    if (partial(q, j)) {
+                        if (!bar_wait<CG == 2>(smem_addr(&sh.fixed[s]), flips >> s & 1, failed)) goto stop;
+                        flips ^= 1u << s;
+                    }
                     fence_after();
+                    // (in a cluster the upper bits of a shared-memory address tell the threadblock)
+                    const uint32_t a = (smem_addr(dyn) & 0x3ffff) + s * bytes, b = a + bytes_a;
 #pragma unroll
                     for (int i = 0; i < kSliceK / 16; ++i)
-                        mma_f16<CG>(tmem + acc * P.bn, operand_desc(a + i * step_a, lead, 1024),
-                                    operand_desc(b + i * step_b, lead, 1024), idesc, j > first || i > 0);
+                        mma_f16<CG>(tmem + acc * P.bn, base | ((a + i * step_a) >> 4), base | ((b + i * step_b) >> 4),
+                                    idesc, j > first || i > 0);
                     mma_commit<CG>(smem_addr(&sh.empty[s]));
+                    ++issued;
+                    if (++s == P.stages) s = 0, phase ^= 1;
                 }
-                __syncwarp();
+                mma_commit<CG>(smem_addr(&sh.acc_full[acc]));
+                ++done;
             }
-            if (!ok) break;
-            if (lane == 0) mma_commit<CG>(smem_addr(&sh.acc_full[acc]));
-            __syncwarp();
-            ++done;
-        }
-        if (!ok && lane == 0 && it > 0) {
-            // matrix instructions still in flight read shared memory and
-            // write tensor memory: wait (bounded) until all have finished
-            int none = 0;
-            const int s = (it - 1) % P.stages;
-            bar_wait(smem_addr(&sh.empty[s]), ((it - 1) / P.stages) & 1, &none);
+        stop:
+            if (*failed && issued) {
+                // matrix instructions still in flight read shared memory and
+                // write tensor memory: wait (bounded) until all have finished
+                int none = 0;
+                if (--s < 0) s = P.stages - 1, phase ^= 1;
+                bar_wait(smem_addr(&sh.empty[s]), phase, &none);
+            }
         }
         __syncwarp();
     } else if (warp == 3 && P.ragged == RAGGED_REDUCE) {
@@ -483,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                 const int blk = i / (dead * 8), o = i % (dead * 8);
                 *reinterpret_cast<uint4*>(at + blk * (kSliceK * 128) + left * 128 + o * 16) = make_uint4(0, 0, 0, 0);
             }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            fence_async();
             __syncwarp();
             if (lane == 0) {
                 if (CG == 2)
@@ -495,74 +493,108 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         __syncwarp();
     } else if (warp >= 4) {
         const int quad = warp & 3, half = (warp - 4) >> 2;
-        float* st = staging + (warp - 4) * 32 * kStagePitch;
+        unsigned char* st = staging + (warp - 4) * 4096;
         const int side = P.symmetric ? 1 : 0;
         uint32_t release[2];
         for (int i = 0; i < 2; ++i)
             release[i] = CG == 2 ? cluster_addr(smem_addr(&sh.acc_empty[i]), 0) : smem_addr(&sh.acc_empty[i]);
-        int done = 0, round = 0;
+        int done = 0, round = 0, turn = 0;
         for (int t = cluster; t < total; t += clusters) {
             const TileAt q = tile_at<CG>(P, &sh, t);
             int first, last;
             slices(q, first, last);
             const bool some = first < last;
             const int acc = done & 1;
-            const int feat = q.m0 + (CG == 2 ? rank * kTileM : 0) + quad * 32, nfeat = P.m - feat;
+            const int feat = q.m0 + (CG == 2 ? rank * kTileM : 0) + quad * 32, nfeat = P.m - feat, f = feat + lane;
             const int64_t row = (int64_t)q.row0 + q.n0;
             const float alpha = P.alpha * (P.alpha_of ? P.alpha_of[q.g] : 1.f);
             const float beta = P.beta * (P.beta_of ? P.beta_of[q.g] : 1.f);
-            const bool ahead = P.c && P.vec && size == CG;     // C is fetched a block ahead
-            uint4 next[4];
-            if (ahead) fetch_c(P, lane, q.g, row + half * 32, q.live - half * 32, feat, nfeat, next);
+            const float bias = P.bias && f < P.m ? load1(P.bias + q.g * P.bs_bias + f, P.in_bf) : 0.f;
+            const bool whole = P.ragged != RAGGED_ROWS;    // TMA may cut rows off at the end of the matrix only
+            const int zo = P.ragged == RAGGED_ROWS ? 0 : q.g;
+            uint16_t cv[32];
+            // C is read a block ahead of its use
+            if (P.c && size == CG) fetch_c(P, cv, q.g, row + half * 32, q.live - half * 32, f);
             if (some) {
                 if (!__all_sync(~0u, bar_wait(smem_addr(&sh.acc_full[acc]), (done >> 1) & 1, failed))) break;
                 fence_after();
             }
             if (size > CG) {
                 // shares of the last tile have been read by their owners
-                if (!__all_sync(~0u, bar_wait(smem_addr(&sh.taken), (round & 1) ^ 1, failed))) break;
+                if (!__all_sync(~0u, bar_wait<true>(smem_addr(&sh.taken), (round & 1) ^ 1, failed))) break;
             }
             for (int c = half * 32; c < q.live; c += 64) {
-                uint32_t v[32];
+                uint32_t u[32];
                 if (some) {
-                    tmem_load32(tmem + ((uint32_t)(quad * 32) << 16) + acc * P.bn + c, v);
+                    tmem_load32(tmem + ((uint32_t)(quad * 32) << 16) + acc * P.bn + c, u);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = 0;
+                    for (int i = 0; i < 32; ++i) u[i] = 0;
                 }
+                const int nrows = q.live - c;
                 if (size > CG) {
                     const int own = P.bn / size;
                     const uint32_t at = smem_addr(shares + (size_t)rank * own * kTileM + quad * 32 + lane);
+                    // own is a power of two from 4 up: 4 rows at a time go to one owner
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
+                    for (int i = 0; i < 32; i += 4) {
                         const int r = c + i;
-                        if (r < q.live)
-                            store_cluster(cluster_addr(at + (r % own) * (kTileM * 4), r / own), __uint_as_float(v[i]));
+                        const uint32_t to = cluster_addr(at + r % own * (kTileM * 4), r / own);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (i + e < nrows) store_cluster(to + e * (kTileM * 4), __uint_as_float(u[i + e]));
                     }
                     continue;
                 }
-                if (!P.vec) {
-                    write_lanes(P, v, q.g, row + c, q.live - c, feat + lane, side, alpha, beta);
-                } else {
-                    uint4 now[4];
+                float v[32];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) now[i] = next[i];
-                    if (ahead && c + 64 < q.live)
-                        fetch_c(P, lane, q.g, row + c + 64, q.live - c - 64, feat, nfeat, next);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) st[i * kStagePitch + lane] = __uint_as_float(v[i]);
-                    __syncwarp();
-                    write_block(P, st, lane, q.g, row + c, q.live - c, feat, nfeat, side, alpha, beta,
-                                ahead ? now : nullptr);
-                    __syncwarp();
+                for (int i = 0; i < 32; ++i) v[i] = fmaf(alpha, __uint_as_float(u[i]), bias);
+                if (P.pre) {
+                    const bool tma = P.tma_pre && (whole || nrows >= 32);
+                    uint16_t* p = P.pre + (row + c) * P.ld_pre + f;
+                    if (P.in_bf)
+                        store_block<true>(&P.mp, p, P.ld_pre, v, st, turn, tma, lane, feat, (int)row + c, 0, nrows, nfeat, 0);
+                    else
+                        store_block<false>(&P.mp, p, P.ld_pre, v, st, turn, tma, lane, feat, (int)row + c, 0, nrows, nfeat, 0);
                 }
-                if (side && q.n0 + c + 31 > feat) {
-                    // the mirror image: rows are features, features are rows
+                if (P.act == ACT_RELU) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) st[lane * kStagePitch + i] = __uint_as_float(v[i]);
-                    __syncwarp();
-                    write_block(P, st, lane, q.g, feat, nfeat, q.n0 + c, q.live - c, -1, alpha, beta, nullptr);
-                    __syncwarp();
+                    for (int i = 0; i < 32; ++i) v[i] = activate(v[i], ACT_RELU);
+                } else if (P.act == ACT_GELU) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = activate(v[i], ACT_GELU);
+                } else if (P.act == ACT_SILU) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = activate(v[i], ACT_SILU);
+                }
+                if (P.c) {
+                    if (P.in_bf) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] += beta * __uint_as_float((uint32_t)cv[i] << 16);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] += beta * __half2float(__ushort_as_half(cv[i]));
+                    }
+                    if (c + 64 < q.live) fetch_c(P, cv, q.g, row + c + 64, nrows - 64, f);
+                }
+                const int over = feat + 31 - (q.n0 + c);      // symmetric: > 0 where the block reaches above the diagonal
+                if (side && over >= 63) continue;             // nothing of it on this side
+                {
+                    const bool tma = P.tma_out && (whole || nrows >= 32) && !(side && over > 0);
+                    uint16_t* p = P.out + q.g * P.bs_out + (row + c) * P.ld_out + f;
+                    const int below = side ? f - (q.n0 + c) : 0;   // first row this lane writes
+                    if (P.out_bf)
+                        store_block<true>(&P.mo, p, P.ld_out, v, st, turn, tma, lane, feat, (int)row + c, zo, nrows, nfeat, below);
+                    else
+                        store_block<false>(&P.mo, p, P.ld_out, v, st, turn, tma, lane, feat, (int)row + c, zo, nrows, nfeat, below);
+                }
+                if (side && lane < nfeat) {
+                    // the mirror image: a lane's 32 values are neighbours in row f (symmetric outputs are f16
+                    // and start rows at multiples of 16 bytes)
+                    uint16_t* p = P.out + q.g * P.bs_out + (int64_t)f * P.ld_out + q.n0 + c;
+                    const int from = f + 1 - (q.n0 + c);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8) store8(p + i, false, true, max(0, min(8, from - i)), min(8, nrows - i), v + i);
                 }
             }
             if (some) {
@@ -578,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             if (size > CG) {
                 __syncwarp();
                 if (lane < size) bar_arrive_cluster(cluster_addr(smem_addr(&sh.got), lane));
-                if (!__all_sync(~0u, bar_wait(smem_addr(&sh.got), round & 1, failed))) break;
+                if (!__all_sync(~0u, bar_wait<true>(smem_addr(&sh.got), round & 1, failed))) break;
                 // sum the shares of this threadblock's rows in rank order
                 const int own = P.bn / size, base = rank * own, mine = min(own, q.live - base);
                 const int id = (warp - 4) * 32 + lane;
@@ -638,6 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                 ++round;
             }
         }
+        if (lane == 0) tma_stores_done();
         fence_before();
     }
     if (sh.failed && lane == 0) atomicCAS(&g_status[0], 0, (int)CCL_ERR_TIMEOUT);
@@ -969,14 +1002,15 @@ static ccl_status_t loadable(Matrix* m, Arena* ws, cudaStream_t stream)
     return launch(pack_rows_kernel, dim3((unsigned)std::min<int64_t>(a.rows, 4096), (unsigned)m->count), 256, 0, stream, a);
 }
 
-static ccl_status_t encode(const Device* dev, CUtensorMap* map, const Matrix& m, int box_cols, int box_rows)
+static ccl_status_t encode(const Device* dev, CUtensorMap* map, const Matrix& m, int box_cols, int box_rows,
+                           CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B)
 {
     const cuuint64_t dims[3] = {(cuuint64_t)m.cols, (cuuint64_t)m.rows, (cuuint64_t)m.count};
     const cuuint64_t strides[2] = {(cuuint64_t)m.ld * 2, (cuuint64_t)(m.count > 1 ? m.stride : m.ld * m.rows) * 2};
     const cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1};
     const cuuint32_t unit[3] = {1, 1, 1};
     const CUresult r = dev->encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(m.p), dims, strides, box,
-                                   unit, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                   unit, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(CCL_ERR_INVALID_ARG, "a matrix cannot be described to TMA (size or stride)");
     return CCL_OK;
@@ -1061,8 +1095,22 @@ static ccl_status_t run(Product P, Matrix a, Matrix b, cudaStream_t stream)
     const int64_t most = P.ragged == RAGGED_ROWS ? (int64_t)P.tiles_m * ((int64_t)P.tiles_n + P.groups)
                                                  : (int64_t)P.tiles_m * P.tiles_n * P.groups;
     if (most > INT32_MAX) return fail(CCL_ERR_UNSUPPORTED, "too many tiles");
+    // one tile each: no more stages than it has slices, so that the next
+    // kernel's threadblocks find room beside this one's
+    if (most <= dev->sms / size)
+        P.stages = (int)std::min<int64_t>(P.stages, ((P.k + kSliceK - 1) / kSliceK + P.split - 1) / P.split);
     TRY(encode(dev, &P.ma, a, 64, P.a_mn ? kSliceK : kTileM));
     TRY(encode(dev, &P.mb, b, 64, P.b_mn ? kSliceK : P.bn / sh.cg));
+    if (sh.split == 1) {
+        const int64_t count = P.ragged == RAGGED_ROWS ? 1 : P.groups;
+        P.tma_out = vectors(P.out, P.ld_out, P.bs_out);
+        if (P.tma_out)
+            TRY(encode(dev, &P.mo, Matrix{P.out, P.n, P.m, P.ld_out, count, P.bs_out}, 32, 32,
+                       CU_TENSOR_MAP_SWIZZLE_NONE));
+        P.tma_pre = P.pre && vectors(P.pre, P.ld_pre, 0);
+        if (P.tma_pre)
+            TRY(encode(dev, &P.mp, Matrix{P.pre, P.n, P.m, P.ld_pre}, 32, 32, CU_TENSOR_MAP_SWIZZLE_NONE));
+    }
     const size_t smem = fixed + (size_t)P.stages * bytes;
     const int64_t clusters = std::min<int64_t>(most, dev->sms / size);
     return launch(sh.cg == 2 ? product_kernel<2> : product_kernel<1>, dim3((unsigned)(clusters * size)), kThreads, smem,

@@ -71,15 +71,25 @@ __device__ __forceinline__ void store_cluster(uint32_t addr, float v)
 {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
+// CLUSTER: also acquire what other threadblocks of the cluster released (dearer)
+template <bool CLUSTER>
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity)
 {
     uint32_t ok;
-    asm volatile("{\n\t.reg .pred p;\n\t"
-                 "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-                 "selp.b32 %0, 1, 0, p;\n\t}"
-                 : "=r"(ok)
-                 : "r"(bar), "r"(parity)
-                 : "memory");
+    if (CLUSTER)
+        asm volatile("{\n\t.reg .pred p;\n\t"
+                     "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                     "selp.b32 %0, 1, 0, p;\n\t}"
+                     : "=r"(ok)
+                     : "r"(bar), "r"(parity)
+                     : "memory");
+    else
+        asm volatile("{\n\t.reg .pred p;\n\t"
+                     "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                     "selp.b32 %0, 1, 0, p;\n\t}"
+                     : "=r"(ok)
+                     : "r"(bar), "r"(parity)
+                     : "memory");
     return ok != 0;
 }
 
@@ -88,14 +98,12 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity)
 constexpr unsigned long long kWaitNs = 4000000000ull;
 constexpr int kWaitSpins = 1 << 26;
 
-// Bounded wait for the completion of the phase with this parity.  Gives up
-// when the limit passes or another warp of the threadblock has given up.
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* failed)
+template <bool CLUSTER>
+__device__ __noinline__ bool bar_wait_long(uint32_t bar, uint32_t parity, volatile int* failed)
 {
-    if (bar_try(bar, parity)) return true;
     const unsigned long long t0 = now_ns();
     for (int i = 1; i < kWaitSpins; ++i) {
-        if (bar_try(bar, parity)) return true;
+        if (bar_try<CLUSTER>(bar, parity)) return true;
         if ((i & 63) == 0) {
             if (*failed) return false;
             if (now_ns() - t0 > kWaitNs) break;
@@ -103,6 +111,14 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
     }
     *failed = 1;
     return false;
+}
+// Bounded wait for the completion of the phase with this parity.  Gives up
+// when the limit passes or another warp of the threadblock has given up.
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* failed)
+{
+    if (bar_try<CLUSTER>(bar, parity)) return true;
+    return bar_wait_long<CLUSTER>(bar, parity, failed);
 }
 
 // ------------------------------------------------------------------ TMA
@@ -120,6 +136,21 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* m
                  "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
                  : "memory");
 }
+// a tile from shared memory to global; parts outside the matrix are not written
+__device__ __forceinline__ void tma_store(const CUtensorMap* map, uint32_t src, int x, int y, int z)
+{
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map),
+                 "r"(src), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+template <int LEFT>
+__device__ __forceinline__ void tma_stores_read()   // all but the last LEFT stores of this thread have read their source
+{
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(LEFT) : "memory");
+}
+__device__ __forceinline__ void tma_stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void tma_prefetch(const CUtensorMap* map)
 {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
@@ -217,6 +248,16 @@ __device__ __forceinline__ void mma_commit(uint32_t bar)
         asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
                      ::"r"(bar), "h"((uint16_t)3)
                      : "memory");
+}
+
+// ------------------------------------------------------- named barriers
+__device__ __forceinline__ void named_sync(int id, int threads)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ void named_arrive(int id, int threads)
+{
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
 // ------------------------------------------------------- element types
