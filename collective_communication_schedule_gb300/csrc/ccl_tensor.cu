@@ -353,29 +353,35 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         return P.ragged == RAGGED_ROWS ? min(P.bn, (q.live + 16 * CG - 1) / (16 * CG) * (16 * CG)) : P.bn;
     };
 
+    const int stages = P.stages, bn = P.bn;
+    const bool a_mn = P.a_mn, b_mn = P.b_mn, reduce_rows = P.ragged == RAGGED_REDUCE;
+    const uint32_t ring = smem_addr(dyn), full0 = smem_addr(sh.full), empty0 = smem_addr(sh.empty);
+
+    // A wait that fails does not change the way through these loops: it only
+    // keeps them from issuing anything more, and later waits return at once.
     if (warp == 0) {
-        if (lane == 0) {
-            int s = 0, loaded = 0;
-            uint32_t phase = 0;                // of the current stage
-            uint32_t flips = 0, used = 0;      // per stage: parity of its uses for cleared slices, whether any
-            for (int t = cluster; t < total; t += clusters) {
-                const TileAt q = tile_at<CG>(P, &sh, t);
-                const int m0 = q.m0 + (CG == 2 ? rank * kTileM : 0);
-                const int n0 = q.n0 + (CG == 2 ? rank * (used_rows(q) / 2) : 0);
-                int first, last;
-                slices(q, first, last);
-                for (int j = first; j < last; ++j) {
-                    const int k = j * kSliceK;
-                    if (!bar_wait(smem_addr(&sh.empty[s]), phase ^ 1, failed)) goto drain;
-                    const uint32_t a = smem_addr(dyn) + s * bytes, b = a + bytes_a;
-                    uint32_t bar = smem_addr(&sh.full[s]);
-                    if (partial(q, j)) {
+        int s = 0, loaded = 0;
+        uint32_t phase = 0;                // of the current stage
+        uint32_t flips = 0, used = 0;      // per stage: parity of its uses for cleared slices, whether any
+        bool good = true;
+        for (int t = cluster; t < total; t += clusters) {
+            const TileAt q = tile_at<CG>(P, &sh, t);
+            const int m0 = q.m0 + (CG == 2 ? rank * kTileM : 0);
+            const int n0 = q.n0 + (CG == 2 ? rank * (used_rows(q) / 2) : 0);
+            int first, last;
+            slices(q, first, last);
+            for (int j = first; j < last; ++j) {
+                const int k = j * kSliceK;
+                if (good) good = bar_wait(empty0 + s * 8, phase ^ 1, failed);
+                const uint32_t a = ring + s * bytes, b = a + bytes_a;
+                uint32_t bar = full0 + s * 8;
+                const bool clear = reduce_rows && partial(q, j);
+                if (elect_one() && good) {
+                    if (clear) {
                         // lands on a barrier of this threadblock, for warp 3
                         if (rank == 0 || CG == 1) bar_arrive(bar);
                         bar = smem_addr(&sh.land[s]);
                         bar_expect(bar, bytes);
-                        flips ^= 1u << s;
-                        used |= 1u << s;
                     } else if (CG == 1) {
                         bar_expect(bar, bytes);
                     } else {
@@ -388,76 +394,77 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                         else
                             tma_load_pair(dst, map, bar, x, y, z);
                     };
-                    if (P.a_mn) {
+                    if (a_mn) {
                         load(a, &P.ma, m0, q.k0 + k, q.za);
                         load(a + kSliceK * 128, &P.ma, m0 + 64, q.k0 + k, q.za);
                     } else {
                         load(a, &P.ma, k, m0, q.za);
                     }
-                    if (P.b_mn) {
-                        for (int i = 0; i < P.bn / CG; i += 64) load(b + i * 128, &P.mb, n0 + i, q.k0 + k, q.zb);
+                    if (b_mn) {
+                        for (int i = 0; i < bn / CG; i += 64) load(b + i * 128, &P.mb, n0 + i, q.k0 + k, q.zb);
                     } else {
                         load(b, &P.mb, k, q.row0 + n0, q.zb);
                     }
-                    ++loaded;
-                    if (++s == P.stages) s = 0, phase ^= 1;
                 }
+                if (clear && good) flips ^= 1u << s, used |= 1u << s;
+                if (good) ++loaded;
+                if (++s == stages) s = 0, phase ^= 1;
             }
-        drain:
-            // copies in flight write this threadblock's shared memory: see
-            // the last one of every stage land before leaving
-            int none = 0;
-            if (CG == 1 || rank == 0)
-                for (int i = 0; i < min(loaded, P.stages); ++i) {
-                    if (--s < 0) s = P.stages - 1, phase ^= 1;
-                    bar_wait(smem_addr(&sh.full[s]), phase, &none);
-                }
-            for (int i = 0; i < P.stages; ++i)
-                if (used >> i & 1) bar_wait(smem_addr(&sh.land[i]), (flips >> i & 1) ^ 1, &none);
         }
+        // copies in flight write this threadblock's shared memory: see the
+        // last one of every stage land before leaving
+        int none = 0;
+        if (CG == 1 || rank == 0)
+            for (int i = max(0, loaded - stages); i < loaded; ++i)
+                bar_wait(full0 + i % stages * 8, i / stages & 1, &none);
+        for (int i = 0; i < stages; ++i)
+            if (used >> i & 1) bar_wait(smem_addr(&sh.land[i]), (flips >> i & 1) ^ 1, &none);
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0 && (CG == 1 || rank == 0)) {
-            const uint32_t lead = kSliceK * 128, step_a = P.a_mn ? 2048 : 32, step_b = P.b_mn ? 2048 : 32;
+        if (CG == 1 || rank == 0) {
+            const uint32_t lead = kSliceK * 128;
+            const uint32_t step_a = (a_mn ? 2048 : 32) >> 4, step_b = (b_mn ? 2048 : 32) >> 4;
             const uint64_t base = operand_desc(0, lead, 1024);
+            // (in a cluster the upper bits of a shared-memory address tell the threadblock)
+            const uint32_t ring_at = (ring & 0x3ffff) >> 4;
+            const uint32_t acc_full0 = smem_addr(sh.acc_full), acc_empty0 = smem_addr(sh.acc_empty);
             int s = 0, issued = 0, done = 0;
             uint32_t phase = 0, flips = 0;
+            bool good = true;
             for (int t = cluster; t < total; t += clusters) {
                 const TileAt q = tile_at<CG>(P, &sh, t);
                 int first, last;
                 slices(q, first, last);
                 if (first >= last) continue;
-                const uint32_t idesc = mma_desc(P.in_bf, P.a_mn, P.b_mn, CG * kTileM, used_rows(q));
+                const uint32_t idesc = mma_desc(P.in_bf, a_mn, b_mn, CG * kTileM, used_rows(q));
                 const int acc = done & 1;
-                if (!bar_wait(smem_addr(&sh.acc_empty[acc]), ((done >> 1) & 1) ^ 1, failed)) goto stop;
+                const uint32_t d = tmem + acc * bn;
+                if (good) good = bar_wait(acc_empty0 + acc * 8, ((done >> 1) & 1) ^ 1, failed);
                 fence_after();
                 for (int j = first; j < last; ++j) {
-                    if (!bar_wait(smem_addr(&sh.full[s]), phase, failed)) goto stop;
-                    if (partial(q, j)) {
-                        if (!bar_wait<CG == 2>(smem_addr(&sh.fixed[s]), flips >> s & 1, failed)) goto stop;
+                    if (good) good = bar_wait(full0 + s * 8, phase, failed);
+                    if (reduce_rows && partial(q, j)) {
+                        if (good) good = bar_wait<CG == 2>(smem_addr(&sh.fixed[s]), flips >> s & 1, failed);
                         flips ^= 1u << s;
                     }
-                    fence_after();
-                    // (in a cluster the upper bits of a shared-memory address tell the threadblock)
-                    const uint32_t a = (smem_addr(dyn) & 0x3ffff) + s * bytes, b = a + bytes_a;
+                    const uint32_t a = ring_at + s * (bytes >> 4), b = a + (bytes_a >> 4);
+                    if (elect_one() && good) {
 #pragma unroll
-                    for (int i = 0; i < kSliceK / 16; ++i)
-                        mma_f16<CG>(tmem + acc * P.bn, base | ((a + i * step_a) >> 4), base | ((b + i * step_b) >> 4),
-                                    idesc, j > first || i > 0);
-                    mma_commit<CG>(smem_addr(&sh.empty[s]));
-                    ++issued;
-                    if (++s == P.stages) s = 0, phase ^= 1;
+                        for (int i = 0; i < kSliceK / 16; ++i)
+                            mma_f16<CG>(d, base | (a + i * step_a), base | (b + i * step_b), idesc, j > first || i > 0);
+                        mma_commit<CG>(empty0 + s * 8);
+                        if (j + 1 == last) mma_commit<CG>(acc_full0 + acc * 8);
+                    }
+                    if (good) ++issued;
+                    if (++s == stages) s = 0, phase ^= 1;
                 }
-                mma_commit<CG>(smem_addr(&sh.acc_full[acc]));
                 ++done;
             }
-        stop:
-            if (*failed && issued) {
+            if (!good && issued) {
                 // matrix instructions still in flight read shared memory and
                 // write tensor memory: wait (bounded) until all have finished
                 int none = 0;
-                if (--s < 0) s = P.stages - 1, phase ^= 1;
-                bar_wait(smem_addr(&sh.empty[s]), phase, &none);
+                bar_wait(empty0 + (issued - 1) % stages * 8, (issued - 1) / stages & 1, &none);
             }
         }
         __syncwarp();

@@ -101,12 +101,16 @@ constexpr int kWaitSpins = 1 << 26;
 template <bool CLUSTER>
 __device__ __noinline__ bool bar_wait_long(uint32_t bar, uint32_t parity, volatile int* failed)
 {
-    const unsigned long long t0 = now_ns();
+    if (*failed) return false;
+    // reading the timer is slow: not before the wait has proved long
+    unsigned long long t0 = 0;
     for (int i = 1; i < kWaitSpins; ++i) {
         if (bar_try<CLUSTER>(bar, parity)) return true;
-        if ((i & 63) == 0) {
+        if ((i & 255) == 0) {
             if (*failed) return false;
-            if (now_ns() - t0 > kWaitNs) break;
+            const unsigned long long t = now_ns();
+            if (!t0) t0 = t;
+            if (t - t0 > kWaitNs) break;
         }
     }
     *failed = 1;
@@ -119,6 +123,16 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
 {
     if (bar_try<CLUSTER>(bar, parity)) return true;
     return bar_wait_long<CLUSTER>(bar, parity, failed);
+}
+
+// One lane of a converged warp.  The loops that issue copies and matrix
+// instructions are run by the whole warp, so that the compiler keeps their
+// addresses in uniform registers, and only the issue is left to one lane.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 // ------------------------------------------------------------------ TMA
