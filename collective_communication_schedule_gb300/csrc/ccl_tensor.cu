@@ -30,7 +30,7 @@ namespace tensor {
 // expert's rows).
 //
 // A threadblock owns 128 features x bn rows of the output at a time.  Warp 0
-// streams 64-wide slices of the reduction axis into a ring of shared-memory
+// streams 128-wide slices of the reduction axis into a ring of shared-memory
 // stages with TMA, warp 1 issues tcgen05 matrix instructions into one of two
 // accumulators in tensor memory, warps 4..11 drain the other one through the
 // epilogue, so that an epilogue costs nothing as long as it is shorter than
@@ -46,12 +46,12 @@ namespace tensor {
 //     with fewer tiles than SMs.
 // ======================================================================
 constexpr int kTileM = 128;
-constexpr int kSliceK = 64;
-constexpr int kMaxStages = 10;
+constexpr int kSliceK = 128;      // reduction elements per stage: two swizzled rows of 64, or 128 rows
+constexpr int kMaxStages = 6;
 constexpr int kMaxGroups = 1024;
 constexpr int kEpilogueWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpilogueWarps;
-constexpr int kStagingBytes = kEpilogueWarps * 2 * 2048;   // two blocks of 32 x 32 outputs per epilogue warp
+constexpr int kStagingBytes = kEpilogueWarps * 2048;   // a block of 32 x 32 outputs per epilogue warp
 constexpr int kSmemBudget = 227 * 1024 - 6 * 1024;   // dynamic part; the rest is static
 
 enum { DENSE = 0, RAGGED_ROWS = 1, RAGGED_REDUCE = 2 };
@@ -67,7 +67,9 @@ struct Product {
     int32_t m, n, k, groups;
     int32_t bn, stages, split, tiles_m, tiles_n;
     int32_t ragged, symmetric, act;
-    int32_t in_bf, out_bf, a_mn, b_mn;
+    int32_t in_bf, out_bf;
+    int32_t a_mn, b_mn;            // stored with consecutive rows (features, or rows of the output) instead of
+                                   // consecutive reduction elements
     int32_t tma_out, tma_pre;
     int32_t vec;                   // rows of out, pre, c and bias allow 16-byte accesses
 };
@@ -235,16 +237,16 @@ __device__ __forceinline__ void fetch_c(const Product& P, uint16_t c[32], int g,
 // through shared memory and a TMA store where the whole block may be
 // written (the parts of it outside the matrix are cut off by TMA), else 64
 // neighbouring bytes of a row at a time.  side: symmetric outputs, only
-// feature <= row.  buf: this warp's two 2 KB buffers, used in turn.
+// feature <= row.  buf: this warp's 2 KB of shared memory.
 template <bool BF>
 __device__ __forceinline__ void store_block(const CUtensorMap* map, uint16_t* p, int64_t ld, const float v[32],
-                                            unsigned char* buf, int& turn, bool tma, int lane, int x, int y, int z,
+                                            unsigned char* buf, bool tma, int lane, int x, int y, int z,
                                             int nrows, int nfeat, int below)
 {
     if (tma && nfeat > 0) {
-        if (lane == 0) tma_stores_read<1>();
+        if (lane == 0) tma_stores_read<0>();
         __syncwarp();
-        uint16_t* b = reinterpret_cast<uint16_t*>(buf + (turn & 1) * 2048) + lane;
+        uint16_t* b = reinterpret_cast<uint16_t*>(buf) + lane;
 #pragma unroll
         for (int i = 0; i < 32; i += 2) {
             const uint32_t u = pack2<BF>(v[i], v[i + 1]);
@@ -253,8 +255,7 @@ __device__ __forceinline__ void store_block(const CUtensorMap* map, uint16_t* p,
         }
         fence_async();
         __syncwarp();
-        if (lane == 0) tma_store(map, smem_addr(buf + (turn & 1) * 2048), x, y, z);
-        ++turn;
+        if (lane == 0) tma_store(map, smem_addr(buf), x, y, z);
     } else if (lane < nfeat) {
 #pragma unroll
         for (int i = 0; i < 32; ++i, p += ld)
@@ -262,7 +263,10 @@ __device__ __forceinline__ void store_block(const CUtensorMap* map, uint16_t* p,
     }
 }
 
-template <int CG>
+// FORM: storage of the operands
+enum { BOTH_K = 0, A_MN = 1, BOTH_MN = 2 };
+
+template <int CG, int FORM>
 __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ Product P)
 {
     __shared__ __align__(8) Shared sh;
@@ -278,20 +282,21 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     uint32_t tcols = 64;
     while (tcols < 2u * P.bn) tcols *= 2;
 
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < P.stages; ++i) {
-            bar_init(smem_addr(&sh.full[i]), 1);
-            bar_init(smem_addr(&sh.empty[i]), 1);
-            bar_init(smem_addr(&sh.land[i]), 1);
-            bar_init(smem_addr(&sh.fixed[i]), CG);
-        }
-        for (int i = 0; i < 2; ++i) {
+    if (threadIdx.x < kMaxStages) {
+        const int i = threadIdx.x;
+        bar_init(smem_addr(&sh.full[i]), 1);
+        bar_init(smem_addr(&sh.empty[i]), 1);
+        bar_init(smem_addr(&sh.land[i]), 1);
+        bar_init(smem_addr(&sh.fixed[i]), CG);
+        if (i < 2) {
             bar_init(smem_addr(&sh.acc_full[i]), 1);
             bar_init(smem_addr(&sh.acc_empty[i]), CG * kEpilogueWarps);
         }
-        bar_init(smem_addr(&sh.got), size * kEpilogueWarps);
-        bar_init(smem_addr(&sh.taken), size * kEpilogueWarps);
+        if (i == 2) bar_init(smem_addr(&sh.got), size * kEpilogueWarps);
+        if (i == 3) bar_init(smem_addr(&sh.taken), size * kEpilogueWarps);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (threadIdx.x == 32) {
         sh.failed = 0;
         tma_prefetch(&P.ma);
         tma_prefetch(&P.mb);
@@ -346,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     };
     // a slice that runs into the next expert's rows has to be cleared there
     auto partial = [&](const TileAt& q, int s) {
-        return P.ragged == RAGGED_REDUCE && q.klen - s * kSliceK < kSliceK;
+        return q.klen - s * kSliceK < kSliceK;
     };
     // rows of a tile that are worth multiplying: a multiple of what one instruction takes
     auto used_rows = [&](const TileAt& q) {
@@ -354,7 +359,9 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     };
 
     const int stages = P.stages, bn = P.bn;
-    const bool a_mn = P.a_mn, b_mn = P.b_mn, reduce_rows = P.ragged == RAGGED_REDUCE;
+    constexpr bool a_mn = FORM != BOTH_K, b_mn = FORM == BOTH_MN;
+    const bool reduce_rows = b_mn && P.ragged == RAGGED_REDUCE;
+    const uint32_t part_b = bytes_b / 2;      // one of a slice's two halves of B (reduction 0..63, 64..127)
     const uint32_t ring = smem_addr(dyn), full0 = smem_addr(sh.full), empty0 = smem_addr(sh.empty);
 
     // A wait that fails does not change the way through these loops: it only
@@ -399,11 +406,14 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                         load(a + kSliceK * 128, &P.ma, m0 + 64, q.k0 + k, q.za);
                     } else {
                         load(a, &P.ma, k, m0, q.za);
+                        load(a + kTileM * 128, &P.ma, k + 64, m0, q.za);
                     }
                     if (b_mn) {
-                        for (int i = 0; i < bn / CG; i += 64) load(b + i * 128, &P.mb, n0 + i, q.k0 + k, q.zb);
+                        for (int i = 0; i < bn / CG; i += 64)
+                            load(b + i * (kSliceK * 2), &P.mb, n0 + i, q.k0 + k, q.zb);
                     } else {
                         load(b, &P.mb, k, q.row0 + n0, q.zb);
+                        load(b + part_b, &P.mb, k + 64, q.row0 + n0, q.zb);
                     }
                 }
                 if (clear && good) flips ^= 1u << s, used |= 1u << s;
@@ -423,7 +433,6 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     } else if (warp == 1) {
         if (CG == 1 || rank == 0) {
             const uint32_t lead = kSliceK * 128;
-            const uint32_t step_a = (a_mn ? 2048 : 32) >> 4, step_b = (b_mn ? 2048 : 32) >> 4;
             const uint64_t base = operand_desc(0, lead, 1024);
             // (in a cluster the upper bits of a shared-memory address tell the threadblock)
             const uint32_t ring_at = (ring & 0x3ffff) >> 4;
@@ -450,8 +459,12 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                     const uint32_t a = ring_at + s * (bytes >> 4), b = a + (bytes_a >> 4);
                     if (elect_one() && good) {
 #pragma unroll
-                        for (int i = 0; i < kSliceK / 16; ++i)
-                            mma_f16<CG>(d, base | (a + i * step_a), base | (b + i * step_b), idesc, j > first || i > 0);
+                        for (int i = 0; i < kSliceK / 16; ++i) {
+                            // 16 reduction elements: 16 rows of 128 bytes, or 32 bytes along a row of 64
+                            const uint32_t at_a = a + ((a_mn ? i * 2048 : i / 4 * (kTileM * 128) + i % 4 * 32) >> 4);
+                            const uint32_t at_b = b + (b_mn ? i * 2048 >> 4 : (i / 4) * (part_b >> 4) + (i % 4 * 32 >> 4));
+                            mma_f16<CG>(d, base | at_a, base | at_b, idesc, j > first || i > 0);
+                        }
                         mma_commit<CG>(empty0 + s * 8);
                         if (j + 1 == last) mma_commit<CG>(acc_full0 + acc * 8);
                     }
@@ -468,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             }
         }
         __syncwarp();
-    } else if (warp == 3 && P.ragged == RAGGED_REDUCE) {
+    } else if (warp == 3 && reduce_rows) {
         // 0 x Inf or NaN would not be 0: both operands are cleared
         int it = 0;
         uint32_t flips = 0;
@@ -500,12 +513,12 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         __syncwarp();
     } else if (warp >= 4) {
         const int quad = warp & 3, half = (warp - 4) >> 2;
-        unsigned char* st = staging + (warp - 4) * 4096;
+        unsigned char* st = staging + (warp - 4) * 2048;
         const int side = P.symmetric ? 1 : 0;
         uint32_t release[2];
         for (int i = 0; i < 2; ++i)
             release[i] = CG == 2 ? cluster_addr(smem_addr(&sh.acc_empty[i]), 0) : smem_addr(&sh.acc_empty[i]);
-        int done = 0, round = 0, turn = 0;
+        int done = 0, round = 0;
         for (int t = cluster; t < total; t += clusters) {
             const TileAt q = tile_at<CG>(P, &sh, t);
             int first, last;
@@ -560,9 +573,9 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                     const bool tma = P.tma_pre && (whole || nrows >= 32);
                     uint16_t* p = P.pre + (row + c) * P.ld_pre + f;
                     if (P.in_bf)
-                        store_block<true>(&P.mp, p, P.ld_pre, v, st, turn, tma, lane, feat, (int)row + c, 0, nrows, nfeat, 0);
+                        store_block<true>(&P.mp, p, P.ld_pre, v, st, tma, lane, feat, (int)row + c, 0, nrows, nfeat, 0);
                     else
-                        store_block<false>(&P.mp, p, P.ld_pre, v, st, turn, tma, lane, feat, (int)row + c, 0, nrows, nfeat, 0);
+                        store_block<false>(&P.mp, p, P.ld_pre, v, st, tma, lane, feat, (int)row + c, 0, nrows, nfeat, 0);
                 }
                 if (P.act == ACT_RELU) {
 #pragma unroll
@@ -591,9 +604,9 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                     uint16_t* p = P.out + q.g * P.bs_out + (row + c) * P.ld_out + f;
                     const int below = side ? f - (q.n0 + c) : 0;   // first row this lane writes
                     if (P.out_bf)
-                        store_block<true>(&P.mo, p, P.ld_out, v, st, turn, tma, lane, feat, (int)row + c, zo, nrows, nfeat, below);
+                        store_block<true>(&P.mo, p, P.ld_out, v, st, tma, lane, feat, (int)row + c, zo, nrows, nfeat, below);
                     else
-                        store_block<false>(&P.mo, p, P.ld_out, v, st, turn, tma, lane, feat, (int)row + c, zo, nrows, nfeat, below);
+                        store_block<false>(&P.mo, p, P.ld_out, v, st, tma, lane, feat, (int)row + c, zo, nrows, nfeat, below);
                 }
                 if (side && lane < nfeat) {
                     // the mirror image: a lane's 32 values are neighbours in row f (symmetric outputs are f16
@@ -901,6 +914,10 @@ typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void
                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
+static void (*const kKernels[2][3])(Product) = {
+    {product_kernel<1, BOTH_K>, product_kernel<1, A_MN>, product_kernel<1, BOTH_MN>},
+    {product_kernel<2, BOTH_K>, product_kernel<2, A_MN>, product_kernel<2, BOTH_MN>}};
+
 // What the launches need to know of a device, looked up once per device.
 struct Device {
     bool ready = false;
@@ -924,9 +941,10 @@ static ccl_status_t device(const Device** out)
                  "cuTensorMapEncodeTiled");
         if (q != cudaDriverEntryPointSuccess || !fn) return fail(CCL_ERR_CUDA, "the driver has no tensor maps");
         all[d].encode = (EncodeFn)fn;
-        for (auto kernel : {product_kernel<1>, product_kernel<2>})
-            TRY_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBudget),
-                     "shared memory of the product kernel");
+        for (auto& forms : kKernels)
+            for (auto kernel : forms)
+                TRY_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBudget),
+                         "shared memory of the product kernel");
         all[d].ready = true;
     }
     *out = &all[d];
@@ -934,7 +952,7 @@ static ccl_status_t device(const Device** out)
 }
 
 template <typename Arg>
-static ccl_status_t launch(void (*kernel)(Arg), dim3 grid, int threads, size_t smem, cudaStream_t stream, const Arg& arg,
+static ccl_status_t launch(void (*kernel)(const Arg), dim3 grid, int threads, size_t smem, cudaStream_t stream, const Arg& arg,
                            int cluster = 1)
 {
     cudaLaunchConfig_t cfg = {};
@@ -1054,7 +1072,7 @@ struct Shape {
 
 // The cheapest way by an estimate in clocks: waves of tiles over the SMs (or
 // pairs, or clusters), each tile the longer of its products with their loads
-// and of its epilogue.  Per 64-wide slice a threadblock's matrix
+// and of its epilogue.  Per 64 reduction elements a threadblock's matrix
 // instructions take 2 clocks per row (128 features, either form), its loads
 // come from L2 at about 70 bytes a clock.
 static Shape choose(const Product& P, int sms)
@@ -1062,13 +1080,13 @@ static Shape choose(const Product& P, int sms)
     const double rows = P.ragged == RAGGED_ROWS ? std::max(1.0, (double)P.n / P.groups) : (double)P.n;
     const double groups = P.ragged == RAGGED_ROWS ? std::min(P.n, P.groups) : P.groups;
     const double reduce = P.ragged == RAGGED_REDUCE ? std::max(1.0, (double)P.k / P.groups) : P.k;
-    const double slices = std::ceil(reduce / kSliceK);
+    const double slices = std::ceil(reduce / kSliceK) * 2;
     Shape best = {0, 0, 0, 0};
     for (int cg = 1; cg <= 2; ++cg) {
         for (int bn : {256, 192, 128, 64, 32}) {
             if (bn / cg % (P.b_mn ? 64 : 16)) continue;
             for (int split = 1; split <= (cg == 2 || bn > 128 || bn * 8 < rows ? 1 : 8); split *= 2) {
-                if (split > 1 && split * 2 > slices) continue;
+                if (split > 1 && split * 4 > slices) continue;
                 const double tiles_m = std::ceil((double)P.m / (cg * kTileM)), tiles_n = std::ceil(rows / bn);
                 double tiles = groups * tiles_m * tiles_n;
                 if (P.symmetric) tiles = groups * (tiles_m * tiles_n + std::max(tiles_m, tiles_n)) / 2;
@@ -1120,7 +1138,7 @@ static ccl_status_t run(Product P, Matrix a, Matrix b, cudaStream_t stream)
     }
     const size_t smem = fixed + (size_t)P.stages * bytes;
     const int64_t clusters = std::min<int64_t>(most, dev->sms / size);
-    return launch(sh.cg == 2 ? product_kernel<2> : product_kernel<1>, dim3((unsigned)(clusters * size)), kThreads, smem,
+    return launch(kKernels[sh.cg - 1][P.b_mn ? BOTH_MN : P.a_mn ? A_MN : BOTH_K], dim3((unsigned)(clusters * size)), kThreads, smem,
                   stream, P, size);
 }
 
