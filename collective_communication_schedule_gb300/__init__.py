@@ -510,77 +510,77 @@ def tune_search(probe, start: PlanOpts | None = None, max_rounds=3, min_gain=0.0
 
 
 # ------------------------------------------------------- tensor products
+_TYPES = {}           # torch dtype -> CCL_*, filled on first use (torch is imported lazily)
+
+
 def _dtype_of(t):
-    import torch
-    codes = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
-    if t.dtype not in codes:
+    if not _TYPES:
+        import torch
+        _TYPES.update({torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16})
+    code = _TYPES.get(t.dtype)
+    if code is None:
         raise ValueError(f"unsupported tensor type {t.dtype}")
-    return codes[t.dtype]
+    return code
 
 
-def _matrix(name, t, shape, like=None):
-    """Address and row stride of a CUDA matrix of this shape; (None, 0) for None."""
-    if t is None:
-        return None, 0
-    if not t.is_cuda:
-        raise ValueError(f"{name} is not a CUDA tensor")
-    if tuple(t.shape) != tuple(shape):
+def _matrix(name, t, shape, like):
+    """Address and row stride (0: packed) of a tensor of this shape, on the
+    device and (unless None) of the type of ``like``."""
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
-    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+    if t.dtype != like.dtype or t.device != like.device:
         raise ValueError(f"{name} is {t.dtype} on {t.device}, not {like.dtype} on {like.device}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    if t.is_contiguous():
+        return t.data_ptr(), 0
+    st = t.stride()
+    if shape[-1] > 1 and st[-1] != 1:
         raise ValueError(f"{name} needs rows of consecutive elements")
-    if t.dim() > 1 and t.shape[-2] > 1 and t.stride(-2) < t.shape[-1]:
+    if len(shape) == 1 or shape[-2] <= 1:
+        return t.data_ptr(), 0
+    if st[-2] < shape[-1]:
         raise ValueError(f"{name} has overlapping rows (an expanded tensor: make it contiguous)")
-    return t.data_ptr(), (t.stride(-2) if t.dim() > 1 and t.shape[-2] > 1 else 0)
+    return t.data_ptr(), st[-2]
 
 
 def _stacked(name, t):
-    """Stride between the matrices of a stack (0: a single one)."""
-    if t is None or t.shape[0] <= 1:
+    """Stride between the matrices (or vectors) of a stack (0: packed)."""
+    if t.is_contiguous() or t.shape[0] <= 1:
         return 0
-    if t.stride(0) < (t.shape[1] - 1) * t.stride(1) + (t.shape[2] if t.dim() > 2 else 1):
+    extent = t.shape[-1] + ((t.shape[1] - 1) * t.stride(1) if t.dim() > 2 else 0)
+    if t.stride(0) < extent:
         raise ValueError(f"{name} has overlapping matrices (an expanded tensor: make it contiguous)")
     return t.stride(0)
 
 
-class _On:
-    """The stream a call runs on.  New tensors (outputs, workspaces) are
-    allocated while it is current, so the allocator ties them to it."""
-
-    def __init__(self, t, stream):
-        import torch
-        if not t.is_cuda:
-            raise ValueError("tensor products need CUDA tensors")
-        if t.device.index != torch.cuda.current_device():
-            raise ValueError(f"tensors on {t.device}, but device {torch.cuda.current_device()} is current")
-        self.ctx = None
-        if stream is None:
-            self.handle = torch.cuda.current_stream().cuda_stream
-            return
-        s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) and stream else stream
-        if isinstance(s, int):
-            s = torch.cuda.default_stream()
-        self.handle = s.cuda_stream
-        self.ctx = torch.cuda.stream(s)
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return self.handle
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
-
-
-def _call(name, args, device, handle):
-    """Run a tensor product with the workspace it asks for."""
+def _on(t, stream):
+    """(stream handle, context) of a call on the device of ``t``.  New tensors
+    (outputs, workspaces) are allocated inside the context, so that the
+    allocator ties them to the stream the call runs on."""
     import torch
+    if not t.is_cuda:
+        raise ValueError("tensor products need CUDA tensors")
+    device = t.device.index
+    if device != torch._C._cuda_getDevice():
+        raise ValueError(f"tensors on {t.device}, but device {torch.cuda.current_device()} is current")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device), None
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    return stream.cuda_stream, torch.cuda.stream(stream)
+
+
+def _run(name, args, device, handle):
+    """Run a tensor product with the workspace it asks for."""
+    ref = ctypes.byref(args)
     need = ctypes.c_int64()
-    _check(getattr(lib, name + "_workspace")(ctypes.byref(args), ctypes.byref(need)))
-    ws = torch.empty(need.value, dtype=torch.uint8, device=device) if need.value else None
-    _check(getattr(lib, name)(ctypes.byref(args), ws.data_ptr() if ws is not None else None, need.value, handle))
+    _check(getattr(lib, name + "_workspace")(ref, ctypes.byref(need)))
+    size = need.value
+    if size:
+        import torch
+        ws = torch.empty(size, dtype=torch.uint8, device=device)
+        _check(getattr(lib, name)(ref, ws.data_ptr(), size, handle))
+    else:
+        _check(getattr(lib, name)(ref, None, 0, handle))
 
 
 def _offsets(offsets, w):
@@ -592,51 +592,73 @@ def _offsets(offsets, w):
     return offsets.data_ptr()
 
 
-def _forward(x, w, offsets, bias, residual, act, preact, out, stream):
-    import torch
+def _operands(x, w, offsets):
+    """rows, k, n, experts and the shape of a vector per output feature."""
     if x.dim() != 2 or w.dim() != (2 if offsets is None else 3):
         raise ValueError("x must be rows x k and w n x k (experts x n x k with offsets)")
-    (rows, k), n = x.shape, w.shape[-2]
-    with _On(x, stream) as handle:
-        y = out if out is not None else torch.empty((rows, n), dtype=x.dtype, device=x.device)
-        z = torch.empty((rows, n), dtype=x.dtype, device=x.device) if preact else None
-        px, ldx = _matrix("x", x, (rows, k))
-        pw, ldw = _matrix("w", w, (*w.shape[:-2], n, k), x)
-        pb, _ = _matrix("bias", bias, (*w.shape[:-2], n), x)
-        pr, ldr = _matrix("residual", residual, (rows, n), x)
-        py, ldy = _matrix("out", y, (rows, n), x)
-        pz, ldz = _matrix("z", z, (rows, n), x)
-        grouped = offsets is not None
-        a = Linear(rows, n, k, _dtype_of(x), act, w.shape[0] if grouped else 0, 0, px, pw, pb, pr,
-                   _offsets(offsets, w) if grouped else None, py, pz, ldx, ldw, ldr, ldy, ldz,
-                   _stacked("w", w) if grouped else 0,
-                   bias.stride(0) if grouped and bias is not None and bias.shape[0] > 1 else 0)
-        _call("ccl_linear", a, x.device, handle)
+    rows, k = x.shape
+    shape = w.shape
+    if offsets is None:
+        return rows, k, shape[0], 0, shape[:1]
+    return rows, k, shape[1], shape[0], shape[:2]
+
+
+def _forward(x, w, offsets, bias, residual, act, preact, out, stream):
+    rows, k, n, experts, vector = _operands(x, w, offsets)
+    handle, ctx = _on(x, stream)
+    if ctx is not None:
+        with ctx:
+            return _forward(x, w, offsets, bias, residual, act, preact, out, None)
+    y = x.new_empty((rows, n)) if out is None else out
+    a = Linear(rows, n, k, _dtype_of(x), act, experts)
+    a.x, a.ldx = _matrix("x", x, x.shape, x)
+    a.w, a.ldw = _matrix("w", w, (*vector, k), x)
+    a.y, a.ldy = (y.data_ptr(), 0) if out is None else _matrix("out", y, (rows, n), x)
+    if bias is not None:
+        a.bias, _ = _matrix("bias", bias, vector, x)
+        if experts:
+            a.bias_stride = _stacked("bias", bias)
+    if residual is not None:
+        a.residual, a.ldr = _matrix("residual", residual, (rows, n), x)
+    if experts:
+        a.offsets = _offsets(offsets, w)
+        a.w_stride = _stacked("w", w)
+    z = None
+    if preact:
+        z = x.new_empty((rows, n))
+        a.z = z.data_ptr()
+    _run("ccl_linear", a, x.device, handle)
     return (y, z) if preact else y
 
 
 def _backward(dy, x, w, offsets, preact, act, bias, need_dx, need_dw, stream):
-    import torch
-    if x.dim() != 2 or w.dim() != (2 if offsets is None else 3):
-        raise ValueError("x must be rows x k and w n x k (experts x n x k with offsets)")
-    (rows, k), n = x.shape, w.shape[-2]
+    rows, k, n, experts, vector = _operands(x, w, offsets)
     if act != ACT_NONE and preact is None:
         raise ValueError("the gradient of an activation needs the pre-activation kept by the forward pass")
-    with _On(x, stream) as handle:
-        new = dict(dtype=x.dtype, device=x.device)
-        dx = torch.empty((rows, k), **new) if need_dx else None
-        dw = torch.empty((*w.shape[:-2], n, k), **new) if need_dw else None
-        db = torch.empty((*w.shape[:-2], n), **new) if bias else None
-        pdy, lddy = _matrix("dy", dy, (rows, n), x)
-        px, ldx = _matrix("x", x, (rows, k))
-        pw, ldw = _matrix("w", w, (*w.shape[:-2], n, k), x)
-        pz, ldz = _matrix("preact", preact if act != ACT_NONE else None, (rows, n), x)
-        grouped = offsets is not None
-        ptr = [t.data_ptr() if t is not None else None for t in (dx, dw, db)]
-        a = LinearGrad(rows, n, k, _dtype_of(x), act, w.shape[0] if grouped else 0, 0, pdy, px, pw, pz,
-                       _offsets(offsets, w) if grouped else None, *ptr, lddy, ldx, ldw, ldz, 0, 0,
-                       _stacked("w", w) if grouped else 0, 0, 0)
-        _call("ccl_linear_grad", a, x.device, handle)
+    handle, ctx = _on(x, stream)
+    if ctx is not None:
+        with ctx:
+            return _backward(dy, x, w, offsets, preact, act, bias, need_dx, need_dw, None)
+    a = LinearGrad(rows, n, k, _dtype_of(x), act, experts)
+    a.dy, a.lddy = _matrix("dy", dy, (rows, n), x)
+    a.x, a.ldx = _matrix("x", x, x.shape, x)
+    a.w, a.ldw = _matrix("w", w, (*vector, k), x)
+    if act != ACT_NONE:
+        a.z, a.ldz = _matrix("preact", preact, (rows, n), x)
+    if experts:
+        a.offsets = _offsets(offsets, w)
+        a.w_stride = _stacked("w", w)
+    dx = dw = db = None
+    if need_dx:
+        dx = x.new_empty((rows, k))
+        a.dx = dx.data_ptr()
+    if need_dw:
+        dw = x.new_empty((*vector, k))
+        a.dw = dw.data_ptr()
+    if bias:
+        db = x.new_empty(vector)
+        a.db = db.data_ptr()
+    _run("ccl_linear_grad", a, x.device, handle)
     return dx, dw, db
 
 
@@ -673,17 +695,22 @@ def orthogonalize(g, steps=5, coeffs=(3.4445, -4.7750, 2.0315), eps=1e-7, scale=
     import torch
     if g.dim() not in (2, 3):
         raise ValueError("g must be a matrix or a stack of matrices")
-    a, b, c = coeffs
-    with _On(g, stream) as handle:
-        if out is None:
-            out = torch.empty(g.shape, dtype=torch.bfloat16, device=g.device)
-        pg, ldg = _matrix("g", g, g.shape)
-        po, ldo = _matrix("out", out, g.shape)
-        stack = g.dim() == 3
-        args = Ortho(g.shape[0] if stack else 1, g.shape[-2], g.shape[-1], _dtype_of(g), _dtype_of(out), steps, a, b,
-                     c, eps, scale, pg, po, ldg, ldo, _stacked("g", g) if stack else 0,
-                     _stacked("out", out) if stack else 0)
-        _call("ccl_orthogonalize", args, g.device, handle)
+    handle, ctx = _on(g, stream)
+    if ctx is not None:
+        with ctx:
+            return orthogonalize(g, steps, coeffs, eps, scale, out, None)
+    if out is None:
+        out = torch.empty(g.shape, dtype=torch.bfloat16, device=g.device)
+    stack = g.dim() == 3
+    args = Ortho(g.shape[0] if stack else 1, g.shape[-2], g.shape[-1], _dtype_of(g), _dtype_of(out), steps, *coeffs,
+                 eps, scale)
+    args.g, args.ldg = _matrix("g", g, g.shape, g)
+    args.out, args.ldo = _matrix("out", out, g.shape, out)
+    if out.device != g.device:
+        raise ValueError(f"out on {out.device}, not {g.device}")
+    if stack:
+        args.g_stride, args.out_stride = _stacked("g", g), _stacked("out", out)
+    _run("ccl_orthogonalize", args, g.device, handle)
     return out
 
 

@@ -457,13 +457,14 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                         flips ^= 1u << s;
                     }
                     const uint32_t a = ring_at + s * (bytes >> 4), b = a + (bytes_a >> 4);
+                    const int steps = min(kSliceK / 16, (q.klen - j * kSliceK + 15) / 16);   // of 16 reduction elements
                     if (elect_one() && good) {
 #pragma unroll
                         for (int i = 0; i < kSliceK / 16; ++i) {
                             // 16 reduction elements: 16 rows of 128 bytes, or 32 bytes along a row of 64
                             const uint32_t at_a = a + ((a_mn ? i * 2048 : i / 4 * (kTileM * 128) + i % 4 * 32) >> 4);
                             const uint32_t at_b = b + (b_mn ? i * 2048 >> 4 : (i / 4) * (part_b >> 4) + (i % 4 * 32 >> 4));
-                            mma_f16<CG>(d, base | at_a, base | at_b, idesc, j > first || i > 0);
+                            if (i < steps) mma_f16<CG>(d, base | at_a, base | at_b, idesc, j > first || i > 0);
                         }
                         mma_commit<CG>(empty0 + s * 8);
                         if (j + 1 == last) mma_commit<CG>(acc_full0 + acc * 8);
@@ -496,7 +497,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             if (!__all_sync(~0u, bar_wait(smem_addr(&sh.land[s]), flips >> s & 1, failed))) break;
             flips ^= 1u << s;
             unsigned char* at = dyn + (size_t)s * bytes;
-            const int left = q.klen - (last - 1) * kSliceK, dead = kSliceK - left;
+            // only as far as the matrix instructions reach: 16 rows at a time
+            const int left = q.klen - (last - 1) * kSliceK, dead = -left & 15;
             for (int i = lane; i < (int)(bytes / (kSliceK * 128)) * dead * 8; i += 32) {
                 const int blk = i / (dead * 8), o = i % (dead * 8);
                 *reinterpret_cast<uint4*>(at + blk * (kSliceK * 128) + left * 128 + o * 16) = make_uint4(0, 0, 0, 0);
@@ -1072,30 +1074,38 @@ struct Shape {
 
 // The cheapest way by an estimate in clocks: waves of tiles over the SMs (or
 // pairs, or clusters), each tile the longer of its products with their loads
-// and of its epilogue.  Per 64 reduction elements a threadblock's matrix
-// instructions take 2 clocks per row (128 features, either form), its loads
-// come from L2 at about 70 bytes a clock.
+// and of its epilogue, and never less than DRAM takes for the operands.  The
+// constants are fits to measured times (bf16, 1.9 GHz, 4096 x 4096 x 4096
+// unless noted).  Per 64 reduction elements: pairs 620, 540, 378 and 278
+// clocks for 256, 192, 128 and 64 rows; single threadblocks 864, 476 and 300
+// for 256, 128 and 64; and no SM gets more than about 68 bytes a clock from
+// L2.  An exchange of shares costs about 5000 clocks (1 x 4096 x 4096: 15.1,
+// 12.9, 11.7 and 19 us cut in 1, 2, 4 and 8), and clusters of 4 and 8 leave
+// SMs unused.
 static Shape choose(const Product& P, int sms)
 {
     const double rows = P.ragged == RAGGED_ROWS ? std::max(1.0, (double)P.n / P.groups) : (double)P.n;
     const double groups = P.ragged == RAGGED_ROWS ? std::min(P.n, P.groups) : P.groups;
     const double reduce = P.ragged == RAGGED_REDUCE ? std::max(1.0, (double)P.k / P.groups) : P.k;
-    const double slices = std::ceil(reduce / kSliceK) * 2;
+    const double slices = std::ceil(reduce / kSliceK);
+    const double least = 2.0 * P.k * ((double)P.m * (P.ragged == RAGGED_REDUCE ? 1 : groups) + P.n) / 3400;
     Shape best = {0, 0, 0, 0};
     for (int cg = 1; cg <= 2; ++cg) {
         for (int bn : {256, 192, 128, 64, 32}) {
             if (bn / cg % (P.b_mn ? 64 : 16)) continue;
-            for (int split = 1; split <= (cg == 2 || bn > 128 || bn * 8 < rows ? 1 : 8); split *= 2) {
-                if (split > 1 && split * 4 > slices) continue;
+            for (int split = 1; split <= (cg == 2 || bn > 128 ? 1 : 8); split *= 2) {
+                if (split > 1 && split * 2 > slices) continue;
                 const double tiles_m = std::ceil((double)P.m / (cg * kTileM)), tiles_n = std::ceil(rows / bn);
                 double tiles = groups * tiles_m * tiles_n;
                 if (P.symmetric) tiles = groups * (tiles_m * tiles_n + std::max(tiles_m, tiles_n)) / 2;
-                const double slice = std::max(2.0 * bn, (kTileM + bn / cg) * 128.0 / 70);
-                const double main = std::ceil(slices / split) * slice;
-                const double epilogue = 400 + 8.0 * std::min((double)bn, rows) / split + (split > 1 ? 12.0 * bn + 1500 : 0);
-                const double waves = std::ceil(tiles / (sms / (cg * split)));
-                const double cost = waves * std::max(main, epilogue) + std::min(main, epilogue) + 1500;
-                if (best.cg == 0 || cost < best.cost) best = {cg, bn, split, cost};
+                const double slice = std::max(cg == 2 ? 150 + 1.85 * bn : 130 + 2.8 * bn, (kTileM + bn / cg) * 128.0 / 68);
+                const double main = std::ceil(slices / split) * 2 * slice;
+                const double exchange = split > 1 ? 5000 + 10 * bn : 0;
+                const double epilogue = 400 + 16 * std::min((double)bn, rows) / split + exchange;
+                const int places = cg == 2 ? sms / 2 : split == 4 ? sms / 4 - 2 : split == 8 ? sms / 8 - 3 : sms / split;
+                const double cost = std::ceil(tiles / places) * std::max(main, epilogue) + std::min(main, epilogue);
+                const double total = std::max(cost, least) + 0.1 * cost;
+                if (best.cg == 0 || total < best.cost) best = {cg, bn, split, total};
             }
         }
     }
