@@ -301,7 +301,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         tma_prefetch(&P.ma);
         tma_prefetch(&P.mb);
     }
-    wait_for_previous();
+    let_next_in();
+    if (P.offsets) wait_for_previous();
     const int nseg = P.ragged == RAGGED_ROWS ? P.groups : P.symmetric ? P.tiles_m : 0;
     for (int s = threadIdx.x; s < nseg; s += kThreads) sh.seg_end[s] = segment_tiles<CG>(P, s);
     if (P.offsets && blockIdx.x == 0) {
@@ -333,9 +334,11 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         __syncthreads();
     const int total = sh.total;
     volatile int* failed = &sh.failed;
-    // loads start while tensor memory is being allocated
+    // loads start while tensor memory is being allocated; everything up to
+    // here overlaps the end of the kernel before this one
     uint32_t tmem = 0;
     if (warp == 2) tmem_alloc<CG>(smem_addr(&sh.tmem), tcols);
+    if (warp == 0 || warp >= 4) wait_for_previous();
     if (warp != 0 && warp != 3) {
         fence_before();
         named_sync(1, 64 + 32 * kEpilogueWarps);
@@ -692,8 +695,15 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                 ++round;
             }
         }
-        if (lane == 0) tma_stores_done();
         fence_before();
+        if (CG == 1) named_arrive(2, 32 + 32 * kEpilogueWarps);
+        if (lane == 0) tma_stores_read<0>();
+    }
+    if (CG == 1 && warp == 2) {
+        // tensor memory is free as soon as the last accumulator has been read
+        named_sync(2, 32 + 32 * kEpilogueWarps);
+        fence_after();
+        tmem_free<1>(tmem, tcols);
     }
     if (sh.failed && lane == 0) atomicCAS(&g_status[0], 0, (int)CCL_ERR_TIMEOUT);
     __syncwarp();
@@ -703,9 +713,9 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         cluster_sync();
     else
         __syncthreads();
-    if (warp == 2) {
+    if (CG == 2 && warp == 2) {
         fence_after();
-        tmem_free<CG>(tmem, tcols);
+        tmem_free<2>(tmem, tcols);
     }
 }
 
@@ -716,9 +726,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 // dz = dy * act'(z), and the column sums of dz that make the bias gradient.
 // A threadblock takes 256 columns of up to kGradRows rows of one expert
 // (dense: one expert with all rows); 32 threads cover the columns, 8 each,
-// and 8 groups of threads take the rows in turn.  The sums go, in 32 bits
-// and a fixed order, to partial[chunk][column]; bias_grad_kernel adds an
-// expert's chunks up in order.  Chunks of expert e start at
+// and 8 groups of threads take the rows in turn, two at a time to keep more
+// loads in flight (bound by DRAM: 6 bytes an element).  The sums go, in 32
+// bits and a fixed order, to partial[chunk][column]; bias_grad_kernel adds
+// an expert's chunks up in order.  Chunks of expert e start at
 // offsets[e] / kGradRows + e, which leaves every expert room for its rows.
 constexpr int kGradRows = 64;
 
@@ -748,6 +759,7 @@ __device__ __forceinline__ void grad_range(const GradPass& G, int e, int& lo, in
 __global__ void __launch_bounds__(256) act_grad_kernel(const GradPass G)
 {
     __shared__ float sums[8][256 + 8];
+    let_next_in();
     wait_for_previous();
     // the last expert whose first chunk is at or before this one (first chunks strictly increase)
     const int chunk = blockIdx.x;
@@ -773,19 +785,27 @@ __global__ void __launch_bounds__(256) act_grad_kernel(const GradPass G)
     const int hi = min(8, G.n - col);
     float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (hi > 0) {
-        for (int r = ty; r < nrows; r += 8) {
+        for (int r = ty; r < nrows; r += 16) {
             const int64_t row = lo + first + r;
-            float v[8];
-            load8(G.dy + row * G.ld_dy + col, G.bf, G.vec & 1, 0, hi, v);
-            if (G.act) {
-                float z[8];
-                load8(G.z + row * G.ld_z + col, G.bf, G.vec & 2, 0, hi, z);
+            const int n = r + 8 < nrows ? 2 : 1;
+            float v[2][8], z[2][8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] *= activate_grad(z[i], G.act);
-            }
-            if (G.dz) store8(G.dz + row * G.ld_dz + col, G.bf, G.vec & 4, 0, hi, v);
+            for (int j = 0; j < 2; ++j)
+                if (j < n) {
+                    load8(G.dy + (row + 8 * j) * G.ld_dy + col, G.bf, G.vec & 1, 0, hi, v[j]);
+                    if (G.act) load8(G.z + (row + 8 * j) * G.ld_z + col, G.bf, G.vec & 2, 0, hi, z[j]);
+                }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum[i] += v[i];
+            for (int j = 0; j < 2; ++j)
+                if (j < n) {
+                    if (G.act) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[j][i] *= activate_grad(z[j][i], G.act);
+                    }
+                    if (G.dz) store8(G.dz + (row + 8 * j) * G.ld_dz + col, G.bf, true, 0, hi, v[j]);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) sum[i] += v[j][i];
+                }
         }
     }
     if (!G.partial) return;
@@ -801,17 +821,30 @@ __global__ void __launch_bounds__(256) act_grad_kernel(const GradPass G)
     }
 }
 
+// 32 columns per threadblock; 8 groups of threads take an expert's chunks in
+// turn, and their sums are added in order.
 __global__ void __launch_bounds__(256) bias_grad_kernel(const GradPass G)
 {
+    __shared__ float sums[8][32];
+    let_next_in();
     wait_for_previous();
-    const int e = blockIdx.y, c = blockIdx.x * 256 + threadIdx.x;
-    if (c >= G.n) return;
+    const int e = blockIdx.y, tx = threadIdx.x & 31, ty = threadIdx.x >> 5, c = blockIdx.x * 32 + tx;
     int lo, len;
     grad_range(G, e, lo, len);
-    const float* p = G.partial + chunk_base(G, e, lo) * G.ld_part + c;
+    const int chunks = (len + kGradRows - 1) / kGradRows;
     float s = 0.f;
-    for (int i = 0; i < len; i += kGradRows, p += G.ld_part) s += *p;
-    store1(G.db + e * G.bs_db + c, s, G.bf);
+    if (c < G.n) {
+        const float* p = G.partial + chunk_base(G, e, lo) * G.ld_part + c;
+#pragma unroll 4
+        for (int i = ty; i < chunks; i += 8) s += p[i * G.ld_part];
+    }
+    sums[ty][tx] = s;
+    __syncthreads();
+    if (ty == 0 && c < G.n) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i) s += sums[i][tx];
+        store1(G.db + e * G.bs_db + c, s, G.bf);
+    }
 }
 
 // ---------------------------------------------- orthogonalisation passes
@@ -819,14 +852,15 @@ __global__ void __launch_bounds__(256) bias_grad_kernel(const GradPass G)
 // same matrix rate, and their range is known (singular values of x stay
 // near 1), so fixed powers of two keep the entries clear of both ends.
 constexpr float kScaleX = 4096.f, kScaleA = 1024.f;
-constexpr int kNormBlocks = 64;
+constexpr int kNormBlocks = 256;
 
 struct NormPass {
     const void* g;
     __half* x;
     float *partial, *kappa, *kappa2;
     int64_t ld_g, bs_g, ld_x, bs_x;
-    int32_t p, q, type;
+    int64_t run;                   // elements of a run of consecutive ones: a row, or the whole matrix
+    int32_t p, q, type, runs, blocks;
     float eps;
 };
 
@@ -834,6 +868,24 @@ __device__ __forceinline__ float load_any(const void* p, int64_t i, int type)
 {
     if (type == CCL_F32) return ((const float*)p)[i];
     return load1((const uint16_t*)p + i, type == CCL_BF16);
+}
+
+// 8 elements from i on, i any index
+__device__ __forceinline__ void load_any8(const void* p, int64_t i, int type, float v[8])
+{
+    if (type == CCL_F32) {
+        const float* f = (const float*)p + i;
+        if (((uintptr_t)f & 15) == 0) {
+            const float4 a = ((const float4*)f)[0], b = ((const float4*)f)[1];
+            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = f[e];
+        }
+    } else {
+        const uint16_t* h = (const uint16_t*)p + i;
+        load8(h, type == CCL_BF16, ((uintptr_t)h & 15) == 0, 0, 8, v);
+    }
 }
 
 __device__ __forceinline__ float block_sum(float v, float* sm)
@@ -847,19 +899,29 @@ __device__ __forceinline__ float block_sum(float v, float* sm)
     return s;
 }
 
+// Sums of squares: threadblocks take groups of 8 elements of all runs in
+// turn (one run where the matrix is packed), so the order is fixed.
 __global__ void __launch_bounds__(256) norm_kernel(const NormPass N)
 {
     __shared__ float sm[8];
+    let_next_in();
     wait_for_previous();
+    const int64_t base = blockIdx.y * N.bs_g, per = (N.run + 7) / 8, all = per * N.runs;
     float s = 0.f;
-    for (int r = blockIdx.x; r < N.p; r += gridDim.x) {
-        const int64_t base = blockIdx.y * N.bs_g + r * N.ld_g;
-        float line = 0.f;
-        for (int c = threadIdx.x; c < N.q; c += 256) {
-            const float v = load_any(N.g, base + c, N.type);
-            line += v * v;
+#pragma unroll 4
+    for (int64_t i = blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
+        const int64_t r = N.runs == 1 ? 0 : i / per, c = (i - r * per) * 8, at = base + r * N.ld_g + c;
+        float v[8];
+        if (c + 8 <= N.run) {
+            load_any8(N.g, at, N.type, v);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = c + e < N.run ? load_any(N.g, at + e, N.type) : 0.f;
         }
-        s += line;
+        float t = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) t = fmaf(v[e], v[e], t);
+        s += t;
     }
     s = block_sum(s, sm);
     if (threadIdx.x == 0) N.partial[blockIdx.y * kNormBlocks + blockIdx.x] = s;
@@ -869,27 +931,48 @@ __global__ void __launch_bounds__(256) norm_kernel(const NormPass N)
 // brings the norm to kScaleX / 2 .. kScaleX; the remaining factor kappa of
 // x0 = kScaleX * g / (norm + eps) is applied in 32 bits by the epilogues of
 // the first step.
-__global__ void __launch_bounds__(256) scale_kernel(const NormPass N)
+__device__ __forceinline__ void norm_scale(float sum, float eps, float& kappa, float& f1, float& f2)
 {
-    wait_for_previous();
-    float s = 0.f;
-    for (int i = 0; i < kNormBlocks; ++i) s += N.partial[blockIdx.y * kNormBlocks + i];
-    const float norm = sqrtf(s);
+    const float norm = sqrtf(sum);
     int e = 0;
     if (norm > 0.f && norm <= 3.4e38f) {
         int x;
         frexpf(norm, &x);            // norm in [2^(x-1), 2^x)
         e = 12 - x;                  // kScaleX = 2^12
     }
+    kappa = ldexpf(1.f, 12 - e) / (norm + eps);
+    f1 = ldexpf(1.f, e / 2);         // 2^e may leave the range of 32 bits: in two factors
+    f2 = ldexpf(1.f, e - e / 2);
+}
+
+__global__ void __launch_bounds__(256) scale_kernel(const NormPass N)
+{
+    __shared__ float sm[8];
+    let_next_in();
+    wait_for_previous();
+    float s = (int)threadIdx.x < N.blocks ? N.partial[blockIdx.y * kNormBlocks + threadIdx.x] : 0.f;
+    s = block_sum(s, sm);
+    float kappa, f1, f2;
+    norm_scale(s, N.eps, kappa, f1, f2);
     if (blockIdx.x == 0 && threadIdx.x == 0) {
-        const float kappa = ldexpf(1.f, 12 - e) / (norm + N.eps);
         N.kappa[blockIdx.y] = kappa;
         N.kappa2[blockIdx.y] = kappa * kappa;
     }
-    for (int r = blockIdx.x; r < N.p; r += gridDim.x) {
-        const int64_t base = blockIdx.y * N.bs_g + r * N.ld_g;
-        __half* d = N.x + blockIdx.y * N.bs_x + r * N.ld_x;
-        for (int c = threadIdx.x; c < N.q; c += 256) d[c] = __float2half_rn(ldexpf(load_any(N.g, base + c, N.type), e));
+    const int per = (N.q + 7) / 8;
+    const int64_t all = (int64_t)per * N.p;
+#pragma unroll 2
+    for (int64_t i = blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
+        const int64_t r = i / per, c = (i - r * per) * 8, at = blockIdx.y * N.bs_g + r * N.ld_g + c;
+        float v[8];
+        if (c + 8 <= N.q) {
+            load_any8(N.g, at, N.type, v);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = c + e < N.q ? load_any(N.g, at + e, N.type) : 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = v[e] * f1 * f2;
+        store8((uint16_t*)N.x + blockIdx.y * N.bs_x + r * N.ld_x + c, false, true, 0, 8, v);   // rows are padded to 8
     }
 }
 
@@ -1008,6 +1091,7 @@ struct PackArgs {
 // of 16 bytes) into rows padded to 8 elements.
 __global__ void __launch_bounds__(256) pack_rows_kernel(const PackArgs a)
 {
+    let_next_in();
     wait_for_previous();
     for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
         const uint16_t* s = a.src + blockIdx.y * a.bs_src + r * a.ld_src;
@@ -1320,10 +1404,10 @@ static ccl_status_t linear_grad(const ccl_linear_grad_t* a, char* base, int64_t*
         G.groups = (int32_t)count;
         G.act = a->act;
         G.bf = bf;
-        G.vec = (aligned16(a->dy) && lddy % 8 == 0 ? 1 : 0) | (aligned16(a->z) && ldz % 8 == 0 ? 2 : 0) | 4;
+        G.vec = (aligned16(a->dy) && lddy % 8 == 0 ? 1 : 0) | (aligned16(a->z) && ldz % 8 == 0 ? 2 : 0);
         TRY(launch(act_grad_kernel, dim3((unsigned)chunks, (unsigned)((a->n + 255) / 256)), 256, 0, stream, G));
         if (a->db)
-            TRY(launch(bias_grad_kernel, dim3((unsigned)((a->n + 255) / 256), (unsigned)count), 256, 0, stream, G));
+            TRY(launch(bias_grad_kernel, dim3((unsigned)((a->n + 31) / 32), (unsigned)count), 256, 0, stream, G));
     }
     Product P = {};
     P.groups = (int32_t)count;
@@ -1409,8 +1493,13 @@ static ccl_status_t orthogonalize(const ccl_ortho_t* a, char* base, int64_t* nee
     N.q = (int32_t)a->q;
     N.type = a->dtype;
     N.eps = a->eps;
-    TRY(launch(norm_kernel, dim3(kNormBlocks, (unsigned)a->batch), 256, 0, stream, N));
-    TRY(launch(scale_kernel, dim3((unsigned)std::min<int64_t>(a->p, 1024), (unsigned)a->batch), 256, 0, stream, N));
+    N.runs = ldg == a->q ? 1 : (int32_t)a->p;
+    N.run = N.runs == 1 ? a->p * a->q : a->q;
+    const int64_t groups = a->p * ((a->q + 7) / 8);   // of 8 elements
+    N.blocks = (int32_t)std::min<int64_t>(kNormBlocks, (groups + 1023) / 1024);
+    TRY(launch(norm_kernel, dim3(N.blocks, (unsigned)a->batch), 256, 0, stream, N));
+    TRY(launch(scale_kernel, dim3((unsigned)std::min<int64_t>(1216, (groups + 511) / 512), (unsigned)a->batch), 256, 0,
+               stream, N));
     for (int i = 0; i < a->steps; ++i) {
         Matrix &from = x[i & 1], &to = x[(i & 1) ^ 1];
         const bool first = i == 0, last = i + 1 == a->steps;

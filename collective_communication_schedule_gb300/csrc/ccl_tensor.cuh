@@ -24,13 +24,10 @@ __device__ __forceinline__ unsigned long long now_ns()
 }
 
 // Every kernel here may be launched before the one ahead of it on the stream
-// has ended: let the next one in early, and touch no global memory before
-// the previous one is complete.
-__device__ __forceinline__ void wait_for_previous()
-{
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-}
+// has ended: each lets the next one in early, and touches no global memory
+// before the previous one is complete.
+__device__ __forceinline__ void let_next_in() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // ------------------------------------------------------------- barriers
 __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count)
@@ -163,7 +160,6 @@ __device__ __forceinline__ void tma_stores_read()   // all but the last LEFT sto
 {
     asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(LEFT) : "memory");
 }
-__device__ __forceinline__ void tma_stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void tma_prefetch(const CUtensorMap* map)
 {
