@@ -57,21 +57,38 @@ constexpr int kSmemBudget = 227 * 1024 - 6 * 1024;   // dynamic part; the rest i
 enum { DENSE = 0, RAGGED_ROWS = 1, RAGGED_REDUCE = 2 };
 
 struct Product {
-    CUtensorMap ma, mb, mo, mp;    // operands; out and pre where TMA can store them
-    uint16_t *out, *pre;           // pre: the sum before the activation (may be null)
-    const uint16_t *c, *bias;
-    const float *alpha_of, *beta_of;   // device factors per batch entry (may be null)
-    const int32_t* offsets;
-    int64_t ld_out, bs_out, ld_pre, ld_c, bs_c, bs_bias;
-    float alpha, beta;
     int32_t m, n, k, groups;
     int32_t bn, stages, split, tiles_m, tiles_n;
+    int32_t per, total;            // tiles of a batch entry, of all (RAGGED_ROWS: counted on the device)
     int32_t ragged, symmetric, act;
     int32_t in_bf, out_bf;
     int32_t a_mn, b_mn;            // stored with consecutive rows (features, or rows of the output) instead of
                                    // consecutive reduction elements
     int32_t tma_out, tma_pre;
     int32_t vec;                   // rows of out, pre, c and bias allow 16-byte accesses
+    float alpha, beta;
+    const int32_t* offsets;
+    uint16_t *out, *pre;           // pre: the sum before the activation (may be null)
+    const uint16_t *c, *bias;
+    const float *alpha_of, *beta_of;   // device factors per batch entry (may be null)
+    int64_t ld_out, bs_out, ld_pre, ld_c, bs_c, bs_bias;
+    CUtensorMap ma, mb, mo, mp;    // operands; out and pre where TMA can store them
+};
+
+// Products one after the other in one launch, each reading what the ones
+// before it wrote: the steps of the Newton-Schulz iteration.  `p` holds each
+// different product once; phase() tells which one comes when.
+struct Chain {
+    int32_t steps, width, stages;  // width: the widest tile's rows; stages of that width
+    uint32_t* arrived;             // threadblocks that have finished a phase, in all phases so far
+    Product p[8];
+    __device__ int phase(int i) const
+    {
+        const int s = i / 3, kind = i % 3;
+        if (kind == 0) return s == 0 ? 0 : s & 1 ? 2 : 1;
+        if (kind == 1) return 3;
+        return s + 1 == steps ? 7 : s == 0 ? 4 : s & 1 ? 6 : 5;
+    }
 };
 
 // [0]: a ccl_status_t of a failed launch on this device, 0 if none
@@ -101,15 +118,37 @@ __device__ __forceinline__ void group_range(const Product& P, int g, int limit, 
     len = min(max(P.offsets[g + 1], lo), limit) - lo;
 }
 
-// Tiles of a segment: all tiles of an expert (ragged rows), or the tiles of
-// one column of tiles that touch the lower triangle (symmetric outputs).
+// Tiles of the experts before and up to each one, for RAGGED_ROWS.
 template <int CG>
-__device__ __forceinline__ int segment_tiles(const Product& P, int s)
+__device__ __forceinline__ void prepare_tiles(const Product& P, Shared* sh)
 {
-    if (P.symmetric) return P.tiles_n - s * (CG * kTileM) / P.bn;
-    int lo, len;
-    group_range(P, s, P.n, lo, len);
-    return P.tiles_m * ((len + P.bn - 1) / P.bn);
+    if (!P.offsets) return;
+    const int lane = threadIdx.x & 31;
+    if (blockIdx.x == 0) {
+        const int limit = P.ragged == RAGGED_ROWS ? P.n : P.k;
+        for (int s = threadIdx.x; s < P.groups; s += kThreads)
+            if (P.offsets[s] < 0 || P.offsets[s + 1] < P.offsets[s] || P.offsets[s + 1] > limit)
+                atomicCAS(&g_status[0], 0, (int)CCL_ERR_INVALID_ARG);
+    }
+    if (P.ragged == RAGGED_ROWS && threadIdx.x < 32) {
+        int base = 0;
+        for (int s = 0; s < P.groups; s += 32) {
+            int v = 0;
+            if (s + lane < P.groups) {
+                int lo, len;
+                group_range(P, s + lane, P.n, lo, len);
+                v = P.tiles_m * ((len + P.bn - 1) / P.bn);
+            }
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {
+                const int u = __shfl_up_sync(~0u, v, d);
+                if (lane >= d) v += u;
+            }
+            if (s + lane < P.groups) sh->seg_end[s + lane] = base + v;
+            base += __shfl_sync(~0u, v, 31);
+        }
+        if (lane == 0) sh->total = base;
+    }
 }
 
 __device__ __forceinline__ int find_segment(const Shared* sh, int n, int t)
@@ -145,21 +184,26 @@ __device__ __forceinline__ TileAt tile_at(const Product& P, const Shared* sh, in
         q.za = q.g;
         q.zb = 0;
     } else {
+        q.g = P.groups == 1 ? 0 : t / P.per;
+        int l = t - q.g * P.per;
         if (P.symmetric) {
-            const int per = sh->seg_end[P.tiles_m - 1];
-            q.g = t / per;
-            const int l = t % per, s = find_segment(sh, P.tiles_m, l);
+            // columns of tiles, each from the diagonal on
+            int s = 0, first = 0;
+            while (l >= P.tiles_n - first) {
+                l -= P.tiles_n - first;
+                ++s;
+                first = s * (CG * kTileM) / P.bn;
+            }
             q.m0 = s * (CG * kTileM);
-            q.n0 = (s * (CG * kTileM) / P.bn + l - (s ? sh->seg_end[s - 1] : 0)) * P.bn;
+            q.n0 = (first + l) * P.bn;
         } else {
             // bands of feature tiles (2048 features), row tiles inside: the
             // tiles in flight at one time form a compact block of the output
-            const int band_w = 16 / CG, per = P.tiles_m * P.tiles_n;
-            q.g = t / per;
-            const int l = t % per, band = l / (band_w * P.tiles_n), r = l % (band_w * P.tiles_n);
-            const int width = min(band_w, P.tiles_m - band * band_w);
-            q.m0 = (band * band_w + r % width) * (CG * kTileM);
-            q.n0 = r / width * P.bn;
+            const int band_w = 16 / CG, area = band_w * P.tiles_n;
+            const int band = P.tiles_m <= band_w ? 0 : l / area, r = l - band * area;
+            const int width = min(band_w, P.tiles_m - band * band_w), x = r / width;
+            q.m0 = (band * band_w + r - x * width) * (CG * kTileM);
+            q.n0 = x * P.bn;
         }
         q.za = q.zb = q.g;
         if (P.ragged == RAGGED_REDUCE) {
@@ -169,6 +213,22 @@ __device__ __forceinline__ TileAt tile_at(const Product& P, const Shared* sh, in
     }
     q.live = min(P.bn, rows - q.n0);
     return q;
+}
+
+// A threadblock's slices of a tile's reduction: [first, last) of all of them.
+__device__ __forceinline__ void slices(const TileAt& q, int parts, int rank, int& first, int& last)
+{
+    const int ns = (q.klen + kSliceK - 1) / kSliceK;
+    first = parts == 1 ? 0 : (int)((int64_t)ns * rank / parts);
+    last = parts == 1 ? ns : (int)((int64_t)ns * (rank + 1) / parts);
+}
+// a slice that runs into the next expert's rows has to be cleared there
+__device__ __forceinline__ bool partial(const TileAt& q, int s) { return q.klen - s * kSliceK < kSliceK; }
+// rows of a tile that are worth multiplying: a multiple of what one instruction takes
+template <int CG>
+__device__ __forceinline__ int used_rows(const Product& P, const TileAt& q)
+{
+    return P.ragged == RAGGED_ROWS ? min(P.bn, (q.live + 16 * CG - 1) / (16 * CG) * (16 * CG)) : P.bn;
 }
 
 // The part of the epilogue after alpha, for elements [lo, hi) of 8
@@ -220,16 +280,16 @@ __device__ __forceinline__ void side_range(int side, int64_t n, int f, int nfeat
 }
 
 // 32 rows of C at one feature per lane: 64 neighbouring bytes a row and warp,
-// whatever the alignment
+// whatever the alignment (past L1: in a chain other SMs write C)
 __device__ __forceinline__ void fetch_c(const Product& P, uint16_t c[32], int g, int64_t row, int nrows, int f)
 {
     const uint16_t* p = P.c + g * P.bs_c + row * P.ld_c + f;
     if (f < P.m && nrows >= 32) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i, p += P.ld_c) c[i] = *p;
+        for (int i = 0; i < 32; ++i, p += P.ld_c) c[i] = __ldcg(p);
     } else {
 #pragma unroll
-        for (int i = 0; i < 32; ++i, p += P.ld_c) c[i] = f < P.m && i < nrows ? *p : (uint16_t)0;
+        for (int i = 0; i < 32; ++i, p += P.ld_c) c[i] = f < P.m && i < nrows ? __ldcg(p) : (uint16_t)0;
     }
 }
 
@@ -263,24 +323,53 @@ __device__ __forceinline__ void store_block(const CUtensorMap* map, uint16_t* p,
     }
 }
 
-// FORM: storage of the operands
-enum { BOTH_K = 0, A_MN = 1, BOTH_MN = 2 };
+// FORM: storage of the operands, or ANY_FORM (looked up)
+enum { BOTH_K = 0, A_MN = 1, BOTH_MN = 2, ANY_FORM = 3 };
 
-template <int CG, int FORM>
-__global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ Product P)
+// Wait (bounded) until all threadblocks have finished `phases` phases, and
+// let this thread's loads see what they wrote.
+__device__ __noinline__ bool phases_done(const uint32_t* arrived, uint32_t phases, volatile int* failed)
+{
+    const uint32_t want = phases * gridDim.x;
+    unsigned long long t0 = 0;
+    for (int i = 0; i < kWaitSpins; ++i) {
+        uint32_t v;
+        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(arrived) : "memory");
+        if (v >= want) {
+            asm volatile("fence.proxy.async;" ::: "memory");
+            return true;
+        }
+        if ((i & 255) == 255) {
+            if (*failed) return false;
+            const unsigned long long t = now_ns();
+            if (!t0) t0 = t;
+            if (t - t0 > kWaitNs) break;
+        }
+    }
+    *failed = 1;
+    return false;
+}
+
+// The products list[0 .. count) (CHAIN: those of a Chain, in its order, with
+// all threadblocks of the grid in step) on this threadblock's share of tiles.
+template <int CG, int FORM, bool CHAIN>
+__device__ __forceinline__ void products(const Product* list, const Chain* chain)
 {
     __shared__ __align__(8) Shared sh;
     extern __shared__ unsigned char raw[];
     unsigned char* dyn = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int size = CG == 2 ? 2 : P.split;             // threadblocks of the cluster
+    const int size = CG == 2 ? 2 : CHAIN ? 1 : list->split;            // threadblocks of the cluster
     const int rank = size > 1 ? (int)cluster_rank() : 0;
     const int cluster = blockIdx.x / size, clusters = gridDim.x / size;
-    const uint32_t bytes_a = kTileM * kSliceK * 2, bytes_b = P.bn / CG * kSliceK * 2, bytes = bytes_a + bytes_b;
-    unsigned char* staging = dyn + (size_t)P.stages * bytes;
+    const int width = CHAIN ? chain->width : list->bn, stages = CHAIN ? chain->stages : list->stages;
+    const int phases = CHAIN ? 3 * chain->steps : 1;
+    const uint32_t bytes_a = kTileM * kSliceK * 2;
+    const uint32_t step = bytes_a + width / CG * kSliceK * 2;          // from one stage to the next
+    unsigned char* staging = dyn + (size_t)stages * step;
     float* shares = reinterpret_cast<float*>(staging + kStagingBytes);   // split: [source][row][feature], own rows
     uint32_t tcols = 64;
-    while (tcols < 2u * P.bn) tcols *= 2;
+    while (tcols < 2u * width) tcols *= 2;
 
     if (threadIdx.x < kMaxStages) {
         const int i = threadIdx.x;
@@ -298,41 +387,16 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     }
     if (threadIdx.x == 32) {
         sh.failed = 0;
-        tma_prefetch(&P.ma);
-        tma_prefetch(&P.mb);
+        tma_prefetch(&list->ma);
+        tma_prefetch(&list->mb);
     }
     let_next_in();
-    if (P.offsets) wait_for_previous();
-    const int nseg = P.ragged == RAGGED_ROWS ? P.groups : P.symmetric ? P.tiles_m : 0;
-    for (int s = threadIdx.x; s < nseg; s += kThreads) sh.seg_end[s] = segment_tiles<CG>(P, s);
-    if (P.offsets && blockIdx.x == 0) {
-        const int limit = P.ragged == RAGGED_ROWS ? P.n : P.k;
-        for (int s = threadIdx.x; s < P.groups; s += kThreads)
-            if (P.offsets[s] < 0 || P.offsets[s + 1] < P.offsets[s] || P.offsets[s + 1] > limit)
-                atomicCAS(&g_status[0], 0, (int)CCL_ERR_INVALID_ARG);
-    }
-    __syncthreads();
-    if (nseg && warp == 0) {
-        int base = 0;
-        for (int s = 0; s < nseg; s += 32) {
-            int v = s + lane < nseg ? sh.seg_end[s + lane] : 0;
-#pragma unroll
-            for (int d = 1; d < 32; d *= 2) {
-                const int u = __shfl_up_sync(~0u, v, d);
-                if (lane >= d) v += u;
-            }
-            if (s + lane < nseg) sh.seg_end[s + lane] = base + v;
-            base += __shfl_sync(~0u, v, 31);
-        }
-        if (lane == 0) sh.total = P.symmetric ? base * P.groups : base;
-    } else if (!nseg && threadIdx.x == 0) {
-        sh.total = P.tiles_m * P.tiles_n * P.groups;
-    }
+    if (list->offsets) wait_for_previous();
+    if (!CHAIN) prepare_tiles<CG>(*list, &sh);
     if (size > 1)
         cluster_sync();
     else
         __syncthreads();
-    const int total = sh.total;
     volatile int* failed = &sh.failed;
     // loads start while tensor memory is being allocated; everything up to
     // here overlaps the end of the kernel before this one
@@ -346,25 +410,6 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         tmem = sh.tmem;
     }
 
-    // this threadblock's slices of a tile's reduction: [first, last) of ns
-    auto slices = [&](const TileAt& q, int& first, int& last) {
-        const int ns = (q.klen + kSliceK - 1) / kSliceK;
-        first = CG == 2 || size == 1 ? 0 : (int)((int64_t)ns * rank / size);
-        last = CG == 2 || size == 1 ? ns : (int)((int64_t)ns * (rank + 1) / size);
-    };
-    // a slice that runs into the next expert's rows has to be cleared there
-    auto partial = [&](const TileAt& q, int s) {
-        return q.klen - s * kSliceK < kSliceK;
-    };
-    // rows of a tile that are worth multiplying: a multiple of what one instruction takes
-    auto used_rows = [&](const TileAt& q) {
-        return P.ragged == RAGGED_ROWS ? min(P.bn, (q.live + 16 * CG - 1) / (16 * CG) * (16 * CG)) : P.bn;
-    };
-
-    const int stages = P.stages, bn = P.bn;
-    constexpr bool a_mn = FORM != BOTH_K, b_mn = FORM == BOTH_MN;
-    const bool reduce_rows = b_mn && P.ragged == RAGGED_REDUCE;
-    const uint32_t part_b = bytes_b / 2;      // one of a slice's two halves of B (reduction 0..63, 64..127)
     const uint32_t ring = smem_addr(dyn), full0 = smem_addr(sh.full), empty0 = smem_addr(sh.empty);
 
     // A wait that fails does not change the way through these loops: it only
@@ -374,54 +419,64 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         uint32_t phase = 0;                // of the current stage
         uint32_t flips = 0, used = 0;      // per stage: parity of its uses for cleared slices, whether any
         bool good = true;
-        for (int t = cluster; t < total; t += clusters) {
-            const TileAt q = tile_at<CG>(P, &sh, t);
-            const int m0 = q.m0 + (CG == 2 ? rank * kTileM : 0);
-            const int n0 = q.n0 + (CG == 2 ? rank * (used_rows(q) / 2) : 0);
-            int first, last;
-            slices(q, first, last);
-            for (int j = first; j < last; ++j) {
-                const int k = j * kSliceK;
-                if (good) good = bar_wait(empty0 + s * 8, phase ^ 1, failed);
-                const uint32_t a = ring + s * bytes, b = a + bytes_a;
-                uint32_t bar = full0 + s * 8;
-                const bool clear = reduce_rows && partial(q, j);
-                if (elect_one() && good) {
-                    if (clear) {
-                        // lands on a barrier of this threadblock, for warp 3
-                        if (rank == 0 || CG == 1) bar_arrive(bar);
-                        bar = smem_addr(&sh.land[s]);
-                        bar_expect(bar, bytes);
-                    } else if (CG == 1) {
-                        bar_expect(bar, bytes);
-                    } else {
-                        if (rank == 0) bar_expect(bar, 2 * bytes);
-                        bar = cluster_addr(bar, 0);
+        for (int ph = 0; ph < phases; ++ph) {
+            const Product& P = CHAIN ? list[chain->phase(ph)] : *list;
+            const bool a_mn = FORM == ANY_FORM ? P.a_mn : FORM != BOTH_K, b_mn = FORM == ANY_FORM ? P.b_mn : FORM == BOTH_MN;
+            const uint32_t bytes_b = P.bn / CG * kSliceK * 2;
+            const uint32_t part_b = bytes_b / 2;      // one of a slice's two halves of B (reduction 0..63, 64..127)
+            const uint32_t bytes = bytes_a + bytes_b;
+            const bool reduce_rows = b_mn && P.ragged == RAGGED_REDUCE;
+            const int total = P.ragged == RAGGED_ROWS ? sh.total : P.total, bn = P.bn;
+            if (CHAIN && ph && good) good = phases_done(chain->arrived, ph, failed);
+            for (int t = cluster; t < total; t += clusters) {
+                const TileAt q = tile_at<CG>(P, &sh, t);
+                const int m0 = q.m0 + (CG == 2 ? rank * kTileM : 0);
+                const int n0 = q.n0 + (CG == 2 ? rank * (used_rows<CG>(P, q) / 2) : 0);
+                int first, last;
+                slices(q, CG == 2 ? 1 : size, rank, first, last);
+                for (int j = first; j < last; ++j) {
+                    const int k = j * kSliceK;
+                    if (good) good = bar_wait(empty0 + s * 8, phase ^ 1, failed);
+                    const uint32_t a = ring + s * step, b = a + bytes_a;
+                    uint32_t bar = full0 + s * 8;
+                    const bool clear = reduce_rows && partial(q, j);
+                    if (elect_one() && good) {
+                        if (clear) {
+                            // lands on a barrier of this threadblock, for warp 3
+                            if (rank == 0 || CG == 1) bar_arrive(bar);
+                            bar = smem_addr(&sh.land[s]);
+                            bar_expect(bar, bytes);
+                        } else if (CG == 1) {
+                            bar_expect(bar, bytes);
+                        } else {
+                            if (rank == 0) bar_expect(bar, 2 * bytes);
+                            bar = cluster_addr(bar, 0);
+                        }
+                        auto load = [&](uint32_t dst, const CUtensorMap* map, int x, int y, int z) {
+                            if (CG == 1)
+                                tma_load(dst, map, bar, x, y, z);
+                            else
+                                tma_load_pair(dst, map, bar, x, y, z);
+                        };
+                        if (a_mn) {
+                            load(a, &P.ma, m0, q.k0 + k, q.za);
+                            load(a + kSliceK * 128, &P.ma, m0 + 64, q.k0 + k, q.za);
+                        } else {
+                            load(a, &P.ma, k, m0, q.za);
+                            load(a + kTileM * 128, &P.ma, k + 64, m0, q.za);
+                        }
+                        if (b_mn) {
+                            for (int i = 0; i < bn / CG; i += 64)
+                                load(b + i * (kSliceK * 2), &P.mb, n0 + i, q.k0 + k, q.zb);
+                        } else {
+                            load(b, &P.mb, k, q.row0 + n0, q.zb);
+                            load(b + part_b, &P.mb, k + 64, q.row0 + n0, q.zb);
+                        }
                     }
-                    auto load = [&](uint32_t dst, const CUtensorMap* map, int x, int y, int z) {
-                        if (CG == 1)
-                            tma_load(dst, map, bar, x, y, z);
-                        else
-                            tma_load_pair(dst, map, bar, x, y, z);
-                    };
-                    if (a_mn) {
-                        load(a, &P.ma, m0, q.k0 + k, q.za);
-                        load(a + kSliceK * 128, &P.ma, m0 + 64, q.k0 + k, q.za);
-                    } else {
-                        load(a, &P.ma, k, m0, q.za);
-                        load(a + kTileM * 128, &P.ma, k + 64, m0, q.za);
-                    }
-                    if (b_mn) {
-                        for (int i = 0; i < bn / CG; i += 64)
-                            load(b + i * (kSliceK * 2), &P.mb, n0 + i, q.k0 + k, q.zb);
-                    } else {
-                        load(b, &P.mb, k, q.row0 + n0, q.zb);
-                        load(b + part_b, &P.mb, k + 64, q.row0 + n0, q.zb);
-                    }
+                    if (clear && good) flips ^= 1u << s, used |= 1u << s;
+                    if (good) ++loaded;
+                    if (++s == stages) s = 0, phase ^= 1;
                 }
-                if (clear && good) flips ^= 1u << s, used |= 1u << s;
-                if (good) ++loaded;
-                if (++s == stages) s = 0, phase ^= 1;
             }
         }
         // copies in flight write this threadblock's shared memory: see the
@@ -443,39 +498,47 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             int s = 0, issued = 0, done = 0;
             uint32_t phase = 0, flips = 0;
             bool good = true;
-            for (int t = cluster; t < total; t += clusters) {
-                const TileAt q = tile_at<CG>(P, &sh, t);
-                int first, last;
-                slices(q, first, last);
-                if (first >= last) continue;
-                const uint32_t idesc = mma_desc(P.in_bf, a_mn, b_mn, CG * kTileM, used_rows(q));
-                const int acc = done & 1;
-                const uint32_t d = tmem + acc * bn;
-                if (good) good = bar_wait(acc_empty0 + acc * 8, ((done >> 1) & 1) ^ 1, failed);
-                fence_after();
-                for (int j = first; j < last; ++j) {
-                    if (good) good = bar_wait(full0 + s * 8, phase, failed);
-                    if (reduce_rows && partial(q, j)) {
-                        if (good) good = bar_wait<CG == 2>(smem_addr(&sh.fixed[s]), flips >> s & 1, failed);
-                        flips ^= 1u << s;
-                    }
-                    const uint32_t a = ring_at + s * (bytes >> 4), b = a + (bytes_a >> 4);
-                    const int steps = min(kSliceK / 16, (q.klen - j * kSliceK + 15) / 16);   // of 16 reduction elements
-                    if (elect_one() && good) {
-#pragma unroll
-                        for (int i = 0; i < kSliceK / 16; ++i) {
-                            // 16 reduction elements: 16 rows of 128 bytes, or 32 bytes along a row of 64
-                            const uint32_t at_a = a + ((a_mn ? i * 2048 : i / 4 * (kTileM * 128) + i % 4 * 32) >> 4);
-                            const uint32_t at_b = b + (b_mn ? i * 2048 >> 4 : (i / 4) * (part_b >> 4) + (i % 4 * 32 >> 4));
-                            if (i < steps) mma_f16<CG>(d, base | at_a, base | at_b, idesc, j > first || i > 0);
+            for (int ph = 0; ph < phases; ++ph) {
+                const Product& P = CHAIN ? list[chain->phase(ph)] : *list;
+                const bool a_mn = FORM == ANY_FORM ? P.a_mn : FORM != BOTH_K, b_mn = FORM == ANY_FORM ? P.b_mn : FORM == BOTH_MN;
+                const uint32_t bytes_b = P.bn / CG * kSliceK * 2;
+                const uint32_t part_b = bytes_b / 2;      // one of a slice's two halves of B (reduction 0..63, 64..127)
+                const bool reduce_rows = b_mn && P.ragged == RAGGED_REDUCE;
+                const int total = P.ragged == RAGGED_ROWS ? sh.total : P.total;
+                for (int t = cluster; t < total; t += clusters) {
+                    const TileAt q = tile_at<CG>(P, &sh, t);
+                    int first, last;
+                    slices(q, CG == 2 ? 1 : size, rank, first, last);
+                    if (first >= last) continue;
+                    const uint32_t idesc = mma_desc(P.in_bf, a_mn, b_mn, CG * kTileM, used_rows<CG>(P, q));
+                    const int acc = done & 1;
+                    const uint32_t d = tmem + acc * width;
+                    if (good) good = bar_wait(acc_empty0 + acc * 8, ((done >> 1) & 1) ^ 1, failed);
+                    fence_after();
+                    for (int j = first; j < last; ++j) {
+                        if (good) good = bar_wait(full0 + s * 8, phase, failed);
+                        if (reduce_rows && partial(q, j)) {
+                            if (good) good = bar_wait<CG == 2>(smem_addr(&sh.fixed[s]), flips >> s & 1, failed);
+                            flips ^= 1u << s;
                         }
-                        mma_commit<CG>(empty0 + s * 8);
-                        if (j + 1 == last) mma_commit<CG>(acc_full0 + acc * 8);
+                        const uint32_t a = ring_at + s * (step >> 4), b = a + (bytes_a >> 4);
+                        const int steps = min(kSliceK / 16, (q.klen - j * kSliceK + 15) / 16);   // of 16 reduction elements
+                        if (elect_one() && good) {
+    #pragma unroll
+                            for (int i = 0; i < kSliceK / 16; ++i) {
+                                // 16 reduction elements: 16 rows of 128 bytes, or 32 bytes along a row of 64
+                                const uint32_t at_a = a + ((a_mn ? i * 2048 : i / 4 * (kTileM * 128) + i % 4 * 32) >> 4);
+                                const uint32_t at_b = b + (b_mn ? i * 2048 >> 4 : (i / 4) * (part_b >> 4) + (i % 4 * 32 >> 4));
+                                if (i < steps) mma_f16<CG>(d, base | at_a, base | at_b, idesc, j > first || i > 0);
+                            }
+                            mma_commit<CG>(empty0 + s * 8);
+                            if (j + 1 == last) mma_commit<CG>(acc_full0 + acc * 8);
+                        }
+                        if (good) ++issued;
+                        if (++s == stages) s = 0, phase ^= 1;
                     }
-                    if (good) ++issued;
-                    if (++s == stages) s = 0, phase ^= 1;
+                    ++done;
                 }
-                ++done;
             }
             if (!good && issued) {
                 // matrix instructions still in flight read shared memory and
@@ -485,24 +548,25 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             }
         }
         __syncwarp();
-    } else if (warp == 3 && reduce_rows) {
+    } else if (warp == 3 && !CHAIN && FORM == BOTH_MN && list->ragged == RAGGED_REDUCE) {
         // 0 x Inf or NaN would not be 0: both operands are cleared
+        const Product& P = *list;
         int it = 0;
         uint32_t flips = 0;
-        for (int t = cluster; t < total; t += clusters) {
+        for (int t = cluster; t < P.total; t += clusters) {
             const TileAt q = tile_at<CG>(P, &sh, t);
             int first, last;
-            slices(q, first, last);
+            slices(q, CG == 2 ? 1 : size, rank, first, last);
             if (first >= last) continue;
             it += last - first;
             if (!partial(q, last - 1)) continue;
-            const int s = (it - 1) % P.stages;
+            const int s = (it - 1) % stages;
             if (!__all_sync(~0u, bar_wait(smem_addr(&sh.land[s]), flips >> s & 1, failed))) break;
             flips ^= 1u << s;
-            unsigned char* at = dyn + (size_t)s * bytes;
+            unsigned char* at = dyn + (size_t)s * step;
             // only as far as the matrix instructions reach: 16 rows at a time
             const int left = q.klen - (last - 1) * kSliceK, dead = -left & 15;
-            for (int i = lane; i < (int)(bytes / (kSliceK * 128)) * dead * 8; i += 32) {
+            for (int i = lane; i < (int)(P.bn / CG + kTileM) / 64 * dead * 8; i += 32) {
                 const int blk = i / (dead * 8), o = i % (dead * 8);
                 *reinterpret_cast<uint4*>(at + blk * (kSliceK * 128) + left * 128 + o * 16) = make_uint4(0, 0, 0, 0);
             }
@@ -519,180 +583,195 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     } else if (warp >= 4) {
         const int quad = warp & 3, half = (warp - 4) >> 2;
         unsigned char* st = staging + (warp - 4) * 2048;
-        const int side = P.symmetric ? 1 : 0;
         uint32_t release[2];
         for (int i = 0; i < 2; ++i)
             release[i] = CG == 2 ? cluster_addr(smem_addr(&sh.acc_empty[i]), 0) : smem_addr(&sh.acc_empty[i]);
         int done = 0, round = 0;
-        for (int t = cluster; t < total; t += clusters) {
-            const TileAt q = tile_at<CG>(P, &sh, t);
-            int first, last;
-            slices(q, first, last);
-            const bool some = first < last;
-            const int acc = done & 1;
-            const int feat = q.m0 + (CG == 2 ? rank * kTileM : 0) + quad * 32, nfeat = P.m - feat, f = feat + lane;
-            const int64_t row = (int64_t)q.row0 + q.n0;
-            const float alpha = P.alpha * (P.alpha_of ? P.alpha_of[q.g] : 1.f);
-            const float beta = P.beta * (P.beta_of ? P.beta_of[q.g] : 1.f);
-            const float bias = P.bias && f < P.m ? load1(P.bias + q.g * P.bs_bias + f, P.in_bf) : 0.f;
-            const bool whole = P.ragged != RAGGED_ROWS;    // TMA may cut rows off at the end of the matrix only
-            const int zo = P.ragged == RAGGED_ROWS ? 0 : q.g;
-            uint16_t cv[32];
-            // C is read a block ahead of its use
-            if (P.c && size == CG) fetch_c(P, cv, q.g, row + half * 32, q.live - half * 32, f);
-            if (some) {
-                if (!__all_sync(~0u, bar_wait(smem_addr(&sh.acc_full[acc]), (done >> 1) & 1, failed))) break;
-                fence_after();
-            }
-            if (size > CG) {
-                // shares of the last tile have been read by their owners
-                if (!__all_sync(~0u, bar_wait<true>(smem_addr(&sh.taken), (round & 1) ^ 1, failed))) break;
-            }
-            for (int c = half * 32; c < q.live; c += 64) {
-                uint32_t u[32];
+        for (int ph = 0; ph < phases; ++ph) {
+            const Product& P = CHAIN ? list[chain->phase(ph)] : *list;
+            const int side = P.symmetric ? 1 : 0;
+            const int total = P.ragged == RAGGED_ROWS ? sh.total : P.total;
+            if (CHAIN && ph) phases_done(chain->arrived, ph, failed);
+            for (int t = cluster; t < total; t += clusters) {
+                const TileAt q = tile_at<CG>(P, &sh, t);
+                int first, last;
+                slices(q, CG == 2 ? 1 : size, rank, first, last);
+                const bool some = first < last;
+                const int acc = done & 1;
+                const int feat = q.m0 + (CG == 2 ? rank * kTileM : 0) + quad * 32, nfeat = P.m - feat, f = feat + lane;
+                const int64_t row = (int64_t)q.row0 + q.n0;
+                const float alpha = P.alpha * (P.alpha_of ? P.alpha_of[q.g] : 1.f);
+                const float beta = P.beta * (P.beta_of ? P.beta_of[q.g] : 1.f);
+                const float bias = P.bias && f < P.m ? load1(P.bias + q.g * P.bs_bias + f, P.in_bf) : 0.f;
+                const bool whole = P.ragged != RAGGED_ROWS;    // TMA may cut rows off at the end of the matrix only
+                const int zo = P.ragged == RAGGED_ROWS ? 0 : q.g;
+                uint16_t cv[32];
+                // C is read a block ahead of its use
+                if (P.c && size == CG) fetch_c(P, cv, q.g, row + half * 32, q.live - half * 32, f);
                 if (some) {
-                    tmem_load32(tmem + ((uint32_t)(quad * 32) << 16) + acc * P.bn + c, u);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) u[i] = 0;
+                    if (!__all_sync(~0u, bar_wait(smem_addr(&sh.acc_full[acc]), (done >> 1) & 1, failed))) break;
+                    fence_after();
                 }
-                const int nrows = q.live - c;
                 if (size > CG) {
-                    const int own = P.bn / size;
-                    const uint32_t at = smem_addr(shares + (size_t)rank * own * kTileM + quad * 32 + lane);
-                    // own is a power of two from 4 up: 4 rows at a time go to one owner
-#pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        const int r = c + i;
-                        const uint32_t to = cluster_addr(at + r % own * (kTileM * 4), r / own);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (i + e < nrows) store_cluster(to + e * (kTileM * 4), __uint_as_float(u[i + e]));
-                    }
-                    continue;
+                    // shares of the last tile have been read by their owners
+                    if (!__all_sync(~0u, bar_wait<true>(smem_addr(&sh.taken), (round & 1) ^ 1, failed))) break;
                 }
-                float v[32];
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = fmaf(alpha, __uint_as_float(u[i]), bias);
-                if (P.pre) {
-                    const bool tma = P.tma_pre && (whole || nrows >= 32);
-                    uint16_t* p = P.pre + (row + c) * P.ld_pre + f;
-                    if (P.in_bf)
-                        store_block<true>(&P.mp, p, P.ld_pre, v, st, tma, lane, feat, (int)row + c, 0, nrows, nfeat, 0);
-                    else
-                        store_block<false>(&P.mp, p, P.ld_pre, v, st, tma, lane, feat, (int)row + c, 0, nrows, nfeat, 0);
-                }
-                if (P.act == ACT_RELU) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = activate(v[i], ACT_RELU);
-                } else if (P.act == ACT_GELU) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = activate(v[i], ACT_GELU);
-                } else if (P.act == ACT_SILU) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = activate(v[i], ACT_SILU);
-                }
-                if (P.c) {
-                    if (P.in_bf) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] += beta * __uint_as_float((uint32_t)cv[i] << 16);
+                for (int c = half * 32; c < q.live; c += 64) {
+                    uint32_t u[32];
+                    if (some) {
+                        tmem_load32(tmem + ((uint32_t)(quad * 32) << 16) + acc * width + c, u);
                     } else {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] += beta * __half2float(__ushort_as_half(cv[i]));
+    #pragma unroll
+                        for (int i = 0; i < 32; ++i) u[i] = 0;
                     }
-                    if (c + 64 < q.live) fetch_c(P, cv, q.g, row + c + 64, nrows - 64, f);
+                    const int nrows = q.live - c;
+                    if (size > CG) {
+                        const int own = P.bn / size;
+                        const uint32_t at = smem_addr(shares + (size_t)rank * own * kTileM + quad * 32 + lane);
+                        // own is a power of two from 4 up: 4 rows at a time go to one owner
+    #pragma unroll
+                        for (int i = 0; i < 32; i += 4) {
+                            const int r = c + i;
+                            const uint32_t to = cluster_addr(at + r % own * (kTileM * 4), r / own);
+    #pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (i + e < nrows) store_cluster(to + e * (kTileM * 4), __uint_as_float(u[i + e]));
+                        }
+                        continue;
+                    }
+                    float v[32];
+    #pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = fmaf(alpha, __uint_as_float(u[i]), bias);
+                    if (P.pre) {
+                        const bool tma = P.tma_pre && (whole || nrows >= 32);
+                        uint16_t* p = P.pre + (row + c) * P.ld_pre + f;
+                        if (P.in_bf)
+                            store_block<true>(&P.mp, p, P.ld_pre, v, st, tma, lane, feat, (int)row + c, 0, nrows, nfeat, 0);
+                        else
+                            store_block<false>(&P.mp, p, P.ld_pre, v, st, tma, lane, feat, (int)row + c, 0, nrows, nfeat, 0);
+                    }
+                    if (P.act == ACT_RELU) {
+    #pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = activate(v[i], ACT_RELU);
+                    } else if (P.act == ACT_GELU) {
+    #pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = activate(v[i], ACT_GELU);
+                    } else if (P.act == ACT_SILU) {
+    #pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = activate(v[i], ACT_SILU);
+                    }
+                    if (P.c) {
+                        if (P.in_bf) {
+    #pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] += beta * __uint_as_float((uint32_t)cv[i] << 16);
+                        } else {
+    #pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] += beta * __half2float(__ushort_as_half(cv[i]));
+                        }
+                        if (c + 64 < q.live) fetch_c(P, cv, q.g, row + c + 64, nrows - 64, f);
+                    }
+                    const int over = feat + 31 - (q.n0 + c);      // symmetric: > 0 where the block reaches above the diagonal
+                    if (side && over >= 63) continue;             // nothing of it on this side
+                    {
+                        const bool tma = P.tma_out && (whole || nrows >= 32) && !(side && over > 0);
+                        uint16_t* p = P.out + q.g * P.bs_out + (row + c) * P.ld_out + f;
+                        const int below = side ? f - (q.n0 + c) : 0;   // first row this lane writes
+                        if (P.out_bf)
+                            store_block<true>(&P.mo, p, P.ld_out, v, st, tma, lane, feat, (int)row + c, zo, nrows, nfeat, below);
+                        else
+                            store_block<false>(&P.mo, p, P.ld_out, v, st, tma, lane, feat, (int)row + c, zo, nrows, nfeat, below);
+                    }
+                    if (side && lane < nfeat) {
+                        // the mirror image: a lane's 32 values are neighbours in row f (symmetric outputs are f16
+                        // and start rows at multiples of 16 bytes)
+                        uint16_t* p = P.out + q.g * P.bs_out + (int64_t)f * P.ld_out + q.n0 + c;
+                        const int from = f + 1 - (q.n0 + c);
+    #pragma unroll
+                        for (int i = 0; i < 32; i += 8) store8(p + i, false, true, max(0, min(8, from - i)), min(8, nrows - i), v + i);
+                    }
                 }
-                const int over = feat + 31 - (q.n0 + c);      // symmetric: > 0 where the block reaches above the diagonal
-                if (side && over >= 63) continue;             // nothing of it on this side
-                {
-                    const bool tma = P.tma_out && (whole || nrows >= 32) && !(side && over > 0);
-                    uint16_t* p = P.out + q.g * P.bs_out + (row + c) * P.ld_out + f;
-                    const int below = side ? f - (q.n0 + c) : 0;   // first row this lane writes
-                    if (P.out_bf)
-                        store_block<true>(&P.mo, p, P.ld_out, v, st, tma, lane, feat, (int)row + c, zo, nrows, nfeat, below);
-                    else
-                        store_block<false>(&P.mo, p, P.ld_out, v, st, tma, lane, feat, (int)row + c, zo, nrows, nfeat, below);
+                if (some) {
+                    fence_before();
+                    if (lane == 0) {
+                        if (CG == 2)
+                            bar_arrive_cluster(release[acc]);
+                        else
+                            bar_arrive(release[acc]);
+                    }
+                    ++done;
                 }
-                if (side && lane < nfeat) {
-                    // the mirror image: a lane's 32 values are neighbours in row f (symmetric outputs are f16
-                    // and start rows at multiples of 16 bytes)
-                    uint16_t* p = P.out + q.g * P.bs_out + (int64_t)f * P.ld_out + q.n0 + c;
-                    const int from = f + 1 - (q.n0 + c);
-#pragma unroll
-                    for (int i = 0; i < 32; i += 8) store8(p + i, false, true, max(0, min(8, from - i)), min(8, nrows - i), v + i);
+                if (size > CG) {
+                    __syncwarp();
+                    if (lane < size) bar_arrive_cluster(cluster_addr(smem_addr(&sh.got), lane));
+                    if (!__all_sync(~0u, bar_wait<true>(smem_addr(&sh.got), round & 1, failed))) break;
+                    // sum the shares of this threadblock's rows in rank order
+                    const int own = P.bn / size, base = rank * own, mine = min(own, q.live - base);
+                    const int id = (warp - 4) * 32 + lane;
+                    const int left = P.m - q.m0;
+                    if (P.vec) {
+                        for (int i = id; i < mine * (kTileM / 8); i += 32 * kEpilogueWarps) {
+                            const int r = i / (kTileM / 8), f = i % (kTileM / 8) * 8;
+                            int lo, hi;
+                            side_range(side, row + base + r, q.m0 + f, left - f, lo, hi);
+                            if (lo >= hi) continue;
+                            float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                            for (int s = 0; s < size; ++s) {
+                                const float4* p =
+                                    reinterpret_cast<const float4*>(shares + ((size_t)s * own + r) * kTileM + f);
+                                const float4 a = p[0], b = p[1];
+                                v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
+                                v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+                            }
+    #pragma unroll
+                            for (int e = 0; e < 8; ++e) v[e] *= alpha;
+                            finish8(P, v, q.g, row + base + r, q.m0 + f, lo, hi, beta, nullptr);
+                        }
+                    } else {
+                        for (int i = id; i < mine * kTileM; i += 32 * kEpilogueWarps) {
+                            const int r = i / kTileM, f = q.m0 + i % kTileM;
+                            const int64_t n = row + base + r;
+                            if (f >= P.m || (side && f > n)) continue;
+                            float v = 0.f;
+                            for (int s = 0; s < size; ++s) v += shares[((size_t)s * own + r) * kTileM + i % kTileM];
+                            finish1(P, alpha * v, q.g, n, f, beta,
+                                    P.bias ? load1(P.bias + q.g * P.bs_bias + f, P.in_bf) : 0.f,
+                                    P.c ? load1(P.c + q.g * P.bs_c + n * P.ld_c + f, P.in_bf) : 0.f);
+                        }
+                    }
+                    if (side) {
+                        // the mirror image: 8 of this threadblock's rows at a time for one feature
+                        const int parts = (mine + 7) / 8;
+                        for (int i = id; i < parts * kTileM; i += 32 * kEpilogueWarps) {
+                            const int f = i % kTileM, r0 = i / kTileM * 8, n = q.n0 + base + r0;
+                            int lo, hi;
+                            side_range(-1, q.m0 + f, n, mine - r0, lo, hi);
+                            if (f >= left || lo >= hi) continue;
+                            float v[8];
+    #pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                v[e] = 0.f;
+                                if (e >= lo && e < hi)
+                                    for (int s = 0; s < size; ++s)
+                                        v[e] += shares[((size_t)s * own + r0 + e) * kTileM + f];
+                                v[e] *= alpha;
+                            }
+                            finish8(P, v, q.g, q.m0 + f, n, lo, hi, beta, nullptr);
+                        }
+                    }
+                    __syncwarp();
+                    if (lane < size) bar_arrive_cluster(cluster_addr(smem_addr(&sh.taken), lane));
+                    ++round;
                 }
             }
-            if (some) {
-                fence_before();
-                if (lane == 0) {
-                    if (CG == 2)
-                        bar_arrive_cluster(release[acc]);
-                    else
-                        bar_arrive(release[acc]);
-                }
-                ++done;
-            }
-            if (size > CG) {
+            if (CHAIN) {
+                // everything this threadblock wrote, by either route, is visible before it arrives
+                if (lane == 0) tma_stores_done();
                 __syncwarp();
-                if (lane < size) bar_arrive_cluster(cluster_addr(smem_addr(&sh.got), lane));
-                if (!__all_sync(~0u, bar_wait<true>(smem_addr(&sh.got), round & 1, failed))) break;
-                // sum the shares of this threadblock's rows in rank order
-                const int own = P.bn / size, base = rank * own, mine = min(own, q.live - base);
-                const int id = (warp - 4) * 32 + lane;
-                const int left = P.m - q.m0;
-                if (P.vec) {
-                    for (int i = id; i < mine * (kTileM / 8); i += 32 * kEpilogueWarps) {
-                        const int r = i / (kTileM / 8), f = i % (kTileM / 8) * 8;
-                        int lo, hi;
-                        side_range(side, row + base + r, q.m0 + f, left - f, lo, hi);
-                        if (lo >= hi) continue;
-                        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                        for (int s = 0; s < size; ++s) {
-                            const float4* p =
-                                reinterpret_cast<const float4*>(shares + ((size_t)s * own + r) * kTileM + f);
-                            const float4 a = p[0], b = p[1];
-                            v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
-                            v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
-                        }
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) v[e] *= alpha;
-                        finish8(P, v, q.g, row + base + r, q.m0 + f, lo, hi, beta, nullptr);
-                    }
-                } else {
-                    for (int i = id; i < mine * kTileM; i += 32 * kEpilogueWarps) {
-                        const int r = i / kTileM, f = q.m0 + i % kTileM;
-                        const int64_t n = row + base + r;
-                        if (f >= P.m || (side && f > n)) continue;
-                        float v = 0.f;
-                        for (int s = 0; s < size; ++s) v += shares[((size_t)s * own + r) * kTileM + i % kTileM];
-                        finish1(P, alpha * v, q.g, n, f, beta,
-                                P.bias ? load1(P.bias + q.g * P.bs_bias + f, P.in_bf) : 0.f,
-                                P.c ? load1(P.c + q.g * P.bs_c + n * P.ld_c + f, P.in_bf) : 0.f);
-                    }
-                }
-                if (side) {
-                    // the mirror image: 8 of this threadblock's rows at a time for one feature
-                    const int parts = (mine + 7) / 8;
-                    for (int i = id; i < parts * kTileM; i += 32 * kEpilogueWarps) {
-                        const int f = i % kTileM, r0 = i / kTileM * 8, n = q.n0 + base + r0;
-                        int lo, hi;
-                        side_range(-1, q.m0 + f, n, mine - r0, lo, hi);
-                        if (f >= left || lo >= hi) continue;
-                        float v[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            v[e] = 0.f;
-                            if (e >= lo && e < hi)
-                                for (int s = 0; s < size; ++s)
-                                    v[e] += shares[((size_t)s * own + r0 + e) * kTileM + f];
-                            v[e] *= alpha;
-                        }
-                        finish8(P, v, q.g, q.m0 + f, n, lo, hi, beta, nullptr);
-                    }
-                }
-                __syncwarp();
-                if (lane < size) bar_arrive_cluster(cluster_addr(smem_addr(&sh.taken), lane));
-                ++round;
+                asm volatile("fence.proxy.async;" ::: "memory");
+                named_sync(3, 32 * kEpilogueWarps);
+                if (threadIdx.x == 128)
+                    asm volatile("fence.acq_rel.gpu;\n\tred.release.gpu.global.add.u32 [%0], 1;" ::"l"(chain->arrived)
+                                 : "memory");
             }
         }
         fence_before();
@@ -717,6 +796,16 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         fence_after();
         tmem_free<2>(tmem, tcols);
     }
+}
+
+template <int CG, int FORM>
+__global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ Product P)
+{
+    products<CG, FORM, false>(&P, nullptr);
+}
+__global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constant__ Chain C)
+{
+    products<1, ANY_FORM, true>(C.p, &C);
 }
 
 // ======================================================================
@@ -858,6 +947,7 @@ struct NormPass {
     const void* g;
     __half* x;
     float *partial, *kappa, *kappa2;
+    uint32_t* arrived;             // the chain's counter, set to 0 here
     int64_t ld_g, bs_g, ld_x, bs_x;
     int64_t run;                   // elements of a run of consecutive ones: a row, or the whole matrix
     int32_t p, q, type, runs, blocks;
@@ -955,6 +1045,7 @@ __global__ void __launch_bounds__(256) scale_kernel(const NormPass N)
     float kappa, f1, f2;
     norm_scale(s, N.eps, kappa, f1, f2);
     if (blockIdx.x == 0 && threadIdx.x == 0) {
+        if (blockIdx.y == 0) *N.arrived = 0;
         N.kappa[blockIdx.y] = kappa;
         N.kappa2[blockIdx.y] = kappa * kappa;
     }
@@ -1030,12 +1121,16 @@ static ccl_status_t device(const Device** out)
             for (auto kernel : forms)
                 TRY_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBudget),
                          "shared memory of the product kernel");
+        TRY_CUDA(cudaFuncSetAttribute(chain_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBudget),
+                 "shared memory of the chain kernel");
         all[d].ready = true;
     }
     *out = &all[d];
     return CCL_OK;
 }
 
+// cluster > 1: in clusters of that many threadblocks; 0: all threadblocks
+// resident at once, as ones that wait for each other have to be
 template <typename Arg>
 static ccl_status_t launch(void (*kernel)(const Arg), dim3 grid, int threads, size_t smem, cudaStream_t stream, const Arg& arg,
                            int cluster = 1)
@@ -1046,8 +1141,13 @@ static ccl_status_t launch(void (*kernel)(const Arg), dim3 grid, int threads, si
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
+    if (cluster == 0) {
+        at[0].id = cudaLaunchAttributeCooperative;
+        at[0].val.cooperative = 1;
+    } else {
+        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[0].val.programmaticStreamSerializationAllowed = 1;
+    }
     at[1].id = cudaLaunchAttributeClusterDimension;
     at[1].val.clusterDim.x = (unsigned)cluster;
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
@@ -1165,8 +1265,8 @@ struct Shape {
 // for 256, 128 and 64; and no SM gets more than about 68 bytes a clock from
 // L2.  An exchange of shares costs about 5000 clocks (1 x 4096 x 4096: 15.1,
 // 12.9, 11.7 and 19 us cut in 1, 2, 4 and 8), and clusters of 4 and 8 leave
-// SMs unused.
-static Shape choose(const Product& P, int sms)
+// SMs unused.  chain: only what the phases of a chain can take.
+static Shape choose(const Product& P, int sms, bool chain)
 {
     const double rows = P.ragged == RAGGED_ROWS ? std::max(1.0, (double)P.n / P.groups) : (double)P.n;
     const double groups = P.ragged == RAGGED_ROWS ? std::min(P.n, P.groups) : P.groups;
@@ -1174,10 +1274,10 @@ static Shape choose(const Product& P, int sms)
     const double slices = std::ceil(reduce / kSliceK);
     const double least = 2.0 * P.k * ((double)P.m * (P.ragged == RAGGED_REDUCE ? 1 : groups) + P.n) / 3400;
     Shape best = {0, 0, 0, 0};
-    for (int cg = 1; cg <= 2; ++cg) {
+    for (int cg = 1; cg <= (chain ? 1 : 2); ++cg) {
         for (int bn : {256, 192, 128, 64, 32}) {
             if (bn / cg % (P.b_mn ? 64 : 16)) continue;
-            for (int split = 1; split <= (cg == 2 || bn > 128 ? 1 : 8); split *= 2) {
+            for (int split = 1; split <= (chain || cg == 2 || bn > 128 ? 1 : 8); split *= 2) {
                 if (split > 1 && split * 2 > slices) continue;
                 const double tiles_m = std::ceil((double)P.m / (cg * kTileM)), tiles_n = std::ceil(rows / bn);
                 double tiles = groups * tiles_m * tiles_n;
@@ -1196,44 +1296,60 @@ static Shape choose(const Product& P, int sms)
     return best;
 }
 
-// Complete a product (operands, tile, stages) and launch it.
-static ccl_status_t run(Product P, Matrix a, Matrix b, cudaStream_t stream)
+// Complete a product for a shape: tiles and maps.
+static ccl_status_t complete(const Device* dev, Product* P, const Shape& sh, const Matrix& a, const Matrix& b)
 {
-    set_vec(&P);
+    set_vec(P);
+    P->bn = sh.bn;
+    P->split = sh.split;
+    const int64_t tiles_m = (P->m + (int64_t)sh.cg * kTileM - 1) / (sh.cg * kTileM);
+    const int64_t tiles_n = (P->n + (int64_t)P->bn - 1) / P->bn;
+    int64_t per = tiles_m * tiles_n;
+    if (P->symmetric) {
+        per = 0;
+        for (int64_t s = 0; s < tiles_m; ++s) per += tiles_n - s * sh.cg * kTileM / P->bn;
+    }
+    // ragged rows: at most one more row tile per expert than full tiles
+    const int64_t most = P->ragged == RAGGED_ROWS ? tiles_m * (tiles_n + P->groups) : per * P->groups;
+    if (most > INT32_MAX) return fail(CCL_ERR_UNSUPPORTED, "too many tiles");
+    P->tiles_m = (int32_t)tiles_m;
+    P->tiles_n = (int32_t)tiles_n;
+    P->per = (int32_t)per;
+    P->total = (int32_t)most;
+    TRY(encode(dev, &P->ma, a, 64, P->a_mn ? kSliceK : kTileM));
+    TRY(encode(dev, &P->mb, b, 64, P->b_mn ? kSliceK : P->bn / sh.cg));
+    if (sh.split == 1) {
+        const int64_t count = P->ragged == RAGGED_ROWS ? 1 : P->groups;
+        P->tma_out = vectors(P->out, P->ld_out, P->bs_out);
+        if (P->tma_out)
+            TRY(encode(dev, &P->mo, Matrix{P->out, P->n, P->m, P->ld_out, count, P->bs_out}, 32, 32,
+                       CU_TENSOR_MAP_SWIZZLE_NONE));
+        P->tma_pre = P->pre && vectors(P->pre, P->ld_pre, 0);
+        if (P->tma_pre)
+            TRY(encode(dev, &P->mp, Matrix{P->pre, P->n, P->m, P->ld_pre}, 32, 32, CU_TENSOR_MAP_SWIZZLE_NONE));
+    }
+    return CCL_OK;
+}
+
+// Complete a product and launch it.
+static ccl_status_t run(Product P, const Matrix& a, const Matrix& b, cudaStream_t stream)
+{
     const Device* dev = nullptr;
     TRY(device(&dev));
-    const Shape sh = choose(P, dev->sms);
+    const Shape sh = choose(P, dev->sms, false);
+    TRY(complete(dev, &P, sh, a, b));
     const int size = sh.cg == 2 ? 2 : sh.split;
-    P.bn = sh.bn;
-    P.split = sh.split;
-    P.tiles_m = (int)((P.m + (int64_t)sh.cg * kTileM - 1) / (sh.cg * kTileM));
-    P.tiles_n = (int)((P.n + (int64_t)P.bn - 1) / P.bn);
     const int bytes = (kTileM + P.bn / sh.cg) * kSliceK * 2;
     const int fixed = 1024 + kStagingBytes + (sh.split > 1 ? P.bn * kTileM * 4 : 0);
     P.stages = std::min(kMaxStages, (kSmemBudget - fixed) / bytes);
-    const int64_t most = P.ragged == RAGGED_ROWS ? (int64_t)P.tiles_m * ((int64_t)P.tiles_n + P.groups)
-                                                 : (int64_t)P.tiles_m * P.tiles_n * P.groups;
-    if (most > INT32_MAX) return fail(CCL_ERR_UNSUPPORTED, "too many tiles");
     // one tile each: no more stages than it has slices, so that the next
     // kernel's threadblocks find room beside this one's
-    if (most <= dev->sms / size)
+    if (P.total <= dev->sms / size)
         P.stages = (int)std::min<int64_t>(P.stages, ((P.k + kSliceK - 1) / kSliceK + P.split - 1) / P.split);
-    TRY(encode(dev, &P.ma, a, 64, P.a_mn ? kSliceK : kTileM));
-    TRY(encode(dev, &P.mb, b, 64, P.b_mn ? kSliceK : P.bn / sh.cg));
-    if (sh.split == 1) {
-        const int64_t count = P.ragged == RAGGED_ROWS ? 1 : P.groups;
-        P.tma_out = vectors(P.out, P.ld_out, P.bs_out);
-        if (P.tma_out)
-            TRY(encode(dev, &P.mo, Matrix{P.out, P.n, P.m, P.ld_out, count, P.bs_out}, 32, 32,
-                       CU_TENSOR_MAP_SWIZZLE_NONE));
-        P.tma_pre = P.pre && vectors(P.pre, P.ld_pre, 0);
-        if (P.tma_pre)
-            TRY(encode(dev, &P.mp, Matrix{P.pre, P.n, P.m, P.ld_pre}, 32, 32, CU_TENSOR_MAP_SWIZZLE_NONE));
-    }
     const size_t smem = fixed + (size_t)P.stages * bytes;
-    const int64_t clusters = std::min<int64_t>(most, dev->sms / size);
-    return launch(kKernels[sh.cg - 1][P.b_mn ? BOTH_MN : P.a_mn ? A_MN : BOTH_K], dim3((unsigned)(clusters * size)), kThreads, smem,
-                  stream, P, size);
+    const int clusters = std::min(P.total, dev->sms / size);
+    return launch(kKernels[sh.cg - 1][P.b_mn ? BOTH_MN : P.a_mn ? A_MN : BOTH_K], dim3((unsigned)(clusters * size)),
+                  kThreads, smem, stream, P, size);
 }
 
 // --------------------------------------------------------- linear layers
@@ -1475,6 +1591,7 @@ static ccl_status_t orthogonalize(const ccl_ortho_t* a, char* base, int64_t* nee
     N.partial = ws.take<float>(a->batch * kNormBlocks * 4);
     N.kappa = ws.take<float>(a->batch * 4);
     N.kappa2 = ws.take<float>(a->batch * 4);
+    N.arrived = ws.take<uint32_t>(4);
     if (need) {
         *need = ws.used;
         return CCL_OK;
@@ -1500,50 +1617,88 @@ static ccl_status_t orthogonalize(const ccl_ortho_t* a, char* base, int64_t* nee
     TRY(launch(norm_kernel, dim3(N.blocks, (unsigned)a->batch), 256, 0, stream, N));
     TRY(launch(scale_kernel, dim3((unsigned)std::min<int64_t>(1216, (groups + 511) / 512), (unsigned)a->batch), 256, 0,
                stream, N));
-    for (int i = 0; i < a->steps; ++i) {
-        Matrix &from = x[i & 1], &to = x[(i & 1) ^ 1];
-        const bool first = i == 0, last = i + 1 == a->steps;
-        Product P = {};
+    // The products of a step, by the place their operands are in: kind 0 is
+    // A = x x^T (or x^T x of a tall x), kind 1 is B = b A + c A A, kind 2 is
+    // x <- a x + B x (or a x + x B).
+    struct Step {
+        Product p;
+        const Matrix *a, *b;
+    };
+    auto product = [&](int kind, int from, bool first, bool last) {
+        Step s = {};
+        Product& P = s.p;
         P.groups = (int32_t)a->batch;
         P.m = P.n = (int32_t)r;
-        // A = x x^T (or x^T x of a tall x): symmetric
-        P.k = (int32_t)(tall ? a->p : a->q);
-        P.a_mn = P.b_mn = tall;
-        P.symmetric = 1;
-        P.alpha = kScaleA / (kScaleX * kScaleX);
-        P.alpha_of = first ? N.kappa2 : nullptr;
-        set_out(&P, const_cast<void*>(A.p), lda, r * lda, false);
-        TRY(run(P, from, from, stream));
-        // B = b A + c A A: symmetric
-        P.k = (int32_t)r;
-        P.a_mn = P.b_mn = 0;
-        P.alpha = a->c / kScaleA;
-        P.alpha_of = nullptr;
-        set_c(&P, A.p, lda, r * lda, a->b);
-        set_out(&P, const_cast<void*>(B.p), lda, r * lda, false);
-        TRY(run(P, A, A, stream));
-        // x <- a x + B x (or a x + x B)
-        P.symmetric = 0;
-        P.m = (int32_t)a->q;
-        P.n = (int32_t)a->p;
-        P.k = (int32_t)r;
-        const float unscale = last ? a->scale / kScaleX : 1.f;
-        P.alpha = unscale / kScaleA;
-        P.alpha_of = P.beta_of = first ? N.kappa : nullptr;
-        set_c(&P, from.p, ldx, a->p * ldx, a->a * unscale);
-        if (last)
-            set_out(&P, a->out, ldo, so, a->out_dtype == CCL_BF16);
-        else
-            set_out(&P, const_cast<void*>(to.p), ldx, a->p * ldx, false);
-        if (tall) {   // out[p, q] = sum_r B[q, r] x[p, r], B symmetric
-            P.a_mn = 0;
-            P.b_mn = 0;
-            TRY(run(P, B, from, stream));
-        } else {      // out[p, q] = sum_r x[r, q] B[p, r]
-            P.a_mn = 1;
-            P.b_mn = 0;
-            TRY(run(P, from, B, stream));
+        if (kind == 0) {
+            P.k = (int32_t)(tall ? a->p : a->q);
+            P.a_mn = P.b_mn = tall;
+            P.symmetric = 1;
+            P.alpha = kScaleA / (kScaleX * kScaleX);
+            P.alpha_of = first ? N.kappa2 : nullptr;
+            set_out(&P, const_cast<void*>(A.p), lda, r * lda, false);
+            s.a = s.b = &x[from];
+        } else if (kind == 1) {
+            P.k = (int32_t)r;
+            P.symmetric = 1;
+            P.alpha = a->c / kScaleA;
+            set_c(&P, A.p, lda, r * lda, a->b);
+            set_out(&P, const_cast<void*>(B.p), lda, r * lda, false);
+            s.a = s.b = &A;
+        } else {
+            P.m = (int32_t)a->q;
+            P.n = (int32_t)a->p;
+            P.k = (int32_t)r;
+            const float unscale = last ? a->scale / kScaleX : 1.f;
+            P.alpha = unscale / kScaleA;
+            P.alpha_of = P.beta_of = first ? N.kappa : nullptr;
+            set_c(&P, x[from].p, ldx, a->p * ldx, a->a * unscale);
+            if (last)
+                set_out(&P, a->out, ldo, so, a->out_dtype == CCL_BF16);
+            else
+                set_out(&P, const_cast<void*>(x[from ^ 1].p), ldx, a->p * ldx, false);
+            P.a_mn = !tall;            // wide: out[p, q] = sum_r x[r, q] B[p, r]
+            s.a = tall ? &B : &x[from];   // tall: out[p, q] = sum_r B[q, r] x[p, r], B symmetric
+            s.b = tall ? &x[from] : &B;
         }
+        return s;
+    };
+    const Device* dev = nullptr;
+    TRY(device(&dev));
+    // One launch for all steps where the products are small: a launch of its
+    // own costs a product about 9500 clocks before and after its work (cold
+    // instructions, descriptors, the launch itself), a phase of the chain
+    // about 4500 (waiting for all SMs); the chain runs tiles of single
+    // threadblocks only.
+    double apart = 0, chained = 0;
+    for (int kind = 0; kind < 3; ++kind) {
+        const Step s = product(kind, 0, false, false);
+        apart += choose(s.p, dev->sms, false).cost + 9500;
+        chained += choose(s.p, dev->sms, true).cost + 4500;
+    }
+    if (chained < apart) {
+        Chain C = {};
+        C.steps = a->steps;
+        C.arrived = N.arrived;
+        int most = 0;
+        for (int i = 0; i < 8; ++i) {
+            // the order that Chain::phase() expects
+            const int kind = i < 3 ? 0 : i == 3 ? 1 : 2, last = i == 7;
+            const int from = last ? (a->steps - 1) & 1 : i == 2 || i == 6;
+            const Step s = product(kind, from, kind == 0 ? i == 0 : kind == 2 && (i == 4 || (last && a->steps == 1)), last);
+            C.p[i] = s.p;
+            const Shape sh = choose(s.p, dev->sms, true);
+            TRY(complete(dev, &C.p[i], sh, *s.a, *s.b));
+            C.width = std::max(C.width, sh.bn);
+            most = std::max(most, C.p[i].total);
+        }
+        const int bytes = (kTileM + C.width) * kSliceK * 2, fixed = 1024 + kStagingBytes;
+        C.stages = std::min(kMaxStages, (kSmemBudget - fixed) / bytes);
+        return launch(chain_kernel, dim3((unsigned)std::min(most, dev->sms)), kThreads,
+                      fixed + (size_t)C.stages * bytes, stream, C, 0);
+    }
+    for (int i = 0; i < 3 * a->steps; ++i) {
+        const Step s = product(i % 3, i / 3 & 1, i < 3, i / 3 + 1 == a->steps);
+        TRY(run(s.p, *s.a, *s.b, stream));
     }
     return CCL_OK;
 }
