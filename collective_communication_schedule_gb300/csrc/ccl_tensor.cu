@@ -56,7 +56,9 @@ constexpr int kSmemBudget = 227 * 1024 - 6 * 1024;   // dynamic part; the rest i
 
 enum { DENSE = 0, RAGGED_ROWS = 1, RAGGED_REDUCE = 2 };
 
-struct Product {
+// What a product is, but for its maps: loops keep a copy in registers, since
+// a parameter read again after every barrier costs more than it.
+struct Scalars {
     int32_t m, n, k, groups;
     int32_t bn, stages, split, tiles_m, tiles_n;
     int32_t per, total;            // tiles of a batch entry, of all (RAGGED_ROWS: counted on the device)
@@ -72,6 +74,9 @@ struct Product {
     const uint16_t *c, *bias;
     const float *alpha_of, *beta_of;   // device factors per batch entry (may be null)
     int64_t ld_out, bs_out, ld_pre, ld_c, bs_c, bs_bias;
+};
+
+struct Product : Scalars {
     CUtensorMap ma, mb, mo, mp;    // operands; out and pre where TMA can store them
 };
 
@@ -112,7 +117,7 @@ struct Shared {
     int seg_end[kMaxGroups];
 };
 
-__device__ __forceinline__ void group_range(const Product& P, int g, int limit, int& lo, int& len)
+__device__ __forceinline__ void group_range(const Scalars& P, int g, int limit, int& lo, int& len)
 {
     lo = min(max(P.offsets[g], 0), limit);
     len = min(max(P.offsets[g + 1], lo), limit) - lo;
@@ -120,7 +125,7 @@ __device__ __forceinline__ void group_range(const Product& P, int g, int limit, 
 
 // Tiles of the experts before and up to each one, for RAGGED_ROWS.
 template <int CG>
-__device__ __forceinline__ void prepare_tiles(const Product& P, Shared* sh)
+__device__ __forceinline__ void prepare_tiles(const Scalars& P, Shared* sh)
 {
     if (!P.offsets) return;
     const int lane = threadIdx.x & 31;
@@ -166,7 +171,7 @@ __device__ __forceinline__ int find_segment(const Shared* sh, int n, int t)
 
 // Position of tile t; tiles are CG * 128 features x bn rows.
 template <int CG>
-__device__ __forceinline__ TileAt tile_at(const Product& P, const Shared* sh, int t)
+__device__ __forceinline__ TileAt tile_at(const Scalars& P, const Shared* sh, int t)
 {
     TileAt q;
     int rows = P.n;
@@ -226,14 +231,14 @@ __device__ __forceinline__ void slices(const TileAt& q, int parts, int rank, int
 __device__ __forceinline__ bool partial(const TileAt& q, int s) { return q.klen - s * kSliceK < kSliceK; }
 // rows of a tile that are worth multiplying: a multiple of what one instruction takes
 template <int CG>
-__device__ __forceinline__ int used_rows(const Product& P, const TileAt& q)
+__device__ __forceinline__ int used_rows(const Scalars& P, const TileAt& q)
 {
     return P.ragged == RAGGED_ROWS ? min(P.bn, (q.live + 16 * CG - 1) / (16 * CG) * (16 * CG)) : P.bn;
 }
 
 // The part of the epilogue after alpha, for elements [lo, hi) of 8
 // consecutive features f.. of row n; c: their values of C, if any.
-__device__ __forceinline__ void finish8(const Product& P, float v[8], int g, int64_t n, int f, int lo, int hi,
+__device__ __forceinline__ void finish8(const Scalars& P, float v[8], int g, int64_t n, int f, int lo, int hi,
                                         float beta, const uint4* c)
 {
     float w[8];
@@ -258,7 +263,7 @@ __device__ __forceinline__ void finish8(const Product& P, float v[8], int g, int
     store8(P.out + g * P.bs_out + n * P.ld_out + f, P.out_bf, true, lo, hi, v);
 }
 
-__device__ __forceinline__ void finish1(const Product& P, float v, int g, int64_t n, int f, float beta, float bias,
+__device__ __forceinline__ void finish1(const Scalars& P, float v, int g, int64_t n, int f, float beta, float bias,
                                         float c)
 {
     v += bias;
@@ -281,7 +286,7 @@ __device__ __forceinline__ void side_range(int side, int64_t n, int f, int nfeat
 
 // 32 rows of C at one feature per lane: 64 neighbouring bytes a row and warp,
 // whatever the alignment (past L1: in a chain other SMs write C)
-__device__ __forceinline__ void fetch_c(const Product& P, uint16_t c[32], int g, int64_t row, int nrows, int f)
+__device__ __forceinline__ void fetch_c(const Scalars& P, uint16_t c[32], int g, int64_t row, int nrows, int f)
 {
     const uint16_t* p = P.c + g * P.bs_c + row * P.ld_c + f;
     if (f < P.m && nrows >= 32) {
@@ -293,25 +298,24 @@ __device__ __forceinline__ void fetch_c(const Product& P, uint16_t c[32], int g,
     }
 }
 
-// A block of 32 rows x 32 features (one feature per lane) to global memory:
-// through shared memory and a TMA store where the whole block may be
-// written (the parts of it outside the matrix are cut off by TMA), else 64
-// neighbouring bytes of a row at a time.  side: symmetric outputs, only
-// feature <= row.  buf: this warp's 2 KB of shared memory.
-template <bool BF>
-__device__ __forceinline__ void store_block(const CUtensorMap* map, uint16_t* p, int64_t ld, const float v[32],
-                                            unsigned char* buf, bool tma, int lane, int x, int y, int z,
-                                            int nrows, int nfeat, int below)
+// A block of 32 rows x 32 features (one feature per lane, two rows per word)
+// to global memory: through shared memory and a TMA store where the whole
+// block may be written (the parts of it outside the matrix are cut off by
+// TMA), else 64 neighbouring bytes of a row at a time.  below: the first row
+// this lane writes (symmetric outputs: feature <= row).  buf: this warp's
+// 2 KB of shared memory.
+__device__ __forceinline__ void store_block(const CUtensorMap* map, uint16_t* p, int64_t ld, const uint32_t w[16],
+                                            unsigned char* buf, bool tma, int lane, int x, int y, int z, int nrows,
+                                            int nfeat, int below)
 {
     if (tma && nfeat > 0) {
         if (lane == 0) tma_stores_read<0>();
         __syncwarp();
         uint16_t* b = reinterpret_cast<uint16_t*>(buf) + lane;
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-            const uint32_t u = pack2<BF>(v[i], v[i + 1]);
-            b[i * 32] = (uint16_t)u;
-            b[i * 32 + 32] = (uint16_t)(u >> 16);
+        for (int i = 0; i < 16; ++i) {
+            b[i * 64] = (uint16_t)w[i];
+            b[i * 64 + 32] = (uint16_t)(w[i] >> 16);
         }
         fence_async();
         __syncwarp();
@@ -319,8 +323,31 @@ __device__ __forceinline__ void store_block(const CUtensorMap* map, uint16_t* p,
     } else if (lane < nfeat) {
 #pragma unroll
         for (int i = 0; i < 32; ++i, p += ld)
-            if (i < nrows && i >= below) store1(p, v[i], BF);
+            if (i < nrows && i >= below) *p = (uint16_t)(w[i / 2] >> (i & 1) * 16);
     }
+}
+
+// Its mirror image in a symmetric output: a lane's 32 values are neighbours
+// in row `feature`, from the first one above the diagonal on (rows start at
+// multiples of 16 bytes).
+__device__ __forceinline__ void store_mirror(uint16_t* p, const uint32_t w[16], int from, int nrows)
+{
+    if (from <= 0 && nrows >= 32) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            reinterpret_cast<uint4*>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i >= from && i < nrows) p[i] = (uint16_t)(w[i / 2] >> (i & 1) * 16);
+    }
+}
+
+template <bool BF>
+__device__ __forceinline__ void pack32(const float v[32], uint32_t w[16])
+{
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = pack2<BF>(v[2 * i], v[2 * i + 1]);
 }
 
 // FORM: storage of the operands, or ANY_FORM (looked up)
@@ -402,7 +429,6 @@ __device__ __forceinline__ void products(const Product* list, const Chain* chain
     // here overlaps the end of the kernel before this one
     uint32_t tmem = 0;
     if (warp == 2) tmem_alloc<CG>(smem_addr(&sh.tmem), tcols);
-    if (warp == 0 || warp >= 4) wait_for_previous();
     if (warp != 0 && warp != 3) {
         fence_before();
         named_sync(1, 64 + 32 * kEpilogueWarps);
@@ -420,16 +446,26 @@ __device__ __forceinline__ void products(const Product* list, const Chain* chain
         uint32_t flips = 0, used = 0;      // per stage: parity of its uses for cleared slices, whether any
         bool good = true;
         for (int ph = 0; ph < phases; ++ph) {
-            const Product& P = CHAIN ? list[chain->phase(ph)] : *list;
+            const Product& maps = CHAIN ? list[chain->phase(ph)] : *list;
+            const Scalars P = maps;
+            if (CHAIN && ph + 1 < phases && lane == 0) {
+                const Product& next = list[chain->phase(ph + 1)];
+                tma_prefetch(&next.ma);
+                tma_prefetch(&next.mb);
+            }
             const bool a_mn = FORM == ANY_FORM ? P.a_mn : FORM != BOTH_K, b_mn = FORM == ANY_FORM ? P.b_mn : FORM == BOTH_MN;
             const uint32_t bytes_b = P.bn / CG * kSliceK * 2;
             const uint32_t part_b = bytes_b / 2;      // one of a slice's two halves of B (reduction 0..63, 64..127)
             const uint32_t bytes = bytes_a + bytes_b;
             const bool reduce_rows = b_mn && P.ragged == RAGGED_REDUCE;
             const int total = P.ragged == RAGGED_ROWS ? sh.total : P.total, bn = P.bn;
+            // the first tile is found before the wait for what it reads
+            TileAt q;
+            if (cluster < total) q = tile_at<CG>(P, &sh, cluster);
+            if (ph == 0) wait_for_previous();
             if (CHAIN && ph && good) good = phases_done(chain->arrived, ph, failed);
             for (int t = cluster; t < total; t += clusters) {
-                const TileAt q = tile_at<CG>(P, &sh, t);
+                if (t != cluster) q = tile_at<CG>(P, &sh, t);
                 const int m0 = q.m0 + (CG == 2 ? rank * kTileM : 0);
                 const int n0 = q.n0 + (CG == 2 ? rank * (used_rows<CG>(P, q) / 2) : 0);
                 int first, last;
@@ -459,18 +495,18 @@ __device__ __forceinline__ void products(const Product* list, const Chain* chain
                                 tma_load_pair(dst, map, bar, x, y, z);
                         };
                         if (a_mn) {
-                            load(a, &P.ma, m0, q.k0 + k, q.za);
-                            load(a + kSliceK * 128, &P.ma, m0 + 64, q.k0 + k, q.za);
+                            load(a, &maps.ma, m0, q.k0 + k, q.za);
+                            load(a + kSliceK * 128, &maps.ma, m0 + 64, q.k0 + k, q.za);
                         } else {
-                            load(a, &P.ma, k, m0, q.za);
-                            load(a + kTileM * 128, &P.ma, k + 64, m0, q.za);
+                            load(a, &maps.ma, k, m0, q.za);
+                            load(a + kTileM * 128, &maps.ma, k + 64, m0, q.za);
                         }
                         if (b_mn) {
                             for (int i = 0; i < bn / CG; i += 64)
-                                load(b + i * (kSliceK * 2), &P.mb, n0 + i, q.k0 + k, q.zb);
+                                load(b + i * (kSliceK * 2), &maps.mb, n0 + i, q.k0 + k, q.zb);
                         } else {
-                            load(b, &P.mb, k, q.row0 + n0, q.zb);
-                            load(b + part_b, &P.mb, k + 64, q.row0 + n0, q.zb);
+                            load(b, &maps.mb, k, q.row0 + n0, q.zb);
+                            load(b + part_b, &maps.mb, k + 64, q.row0 + n0, q.zb);
                         }
                     }
                     if (clear && good) flips ^= 1u << s, used |= 1u << s;
@@ -499,7 +535,7 @@ __device__ __forceinline__ void products(const Product* list, const Chain* chain
             uint32_t phase = 0, flips = 0;
             bool good = true;
             for (int ph = 0; ph < phases; ++ph) {
-                const Product& P = CHAIN ? list[chain->phase(ph)] : *list;
+                const Scalars P = CHAIN ? list[chain->phase(ph)] : *list;
                 const bool a_mn = FORM == ANY_FORM ? P.a_mn : FORM != BOTH_K, b_mn = FORM == ANY_FORM ? P.b_mn : FORM == BOTH_MN;
                 const uint32_t bytes_b = P.bn / CG * kSliceK * 2;
                 const uint32_t part_b = bytes_b / 2;      // one of a slice's two halves of B (reduction 0..63, 64..127)
@@ -550,7 +586,7 @@ __device__ __forceinline__ void products(const Product* list, const Chain* chain
         __syncwarp();
     } else if (warp == 3 && !CHAIN && FORM == BOTH_MN && list->ragged == RAGGED_REDUCE) {
         // 0 x Inf or NaN would not be 0: both operands are cleared
-        const Product& P = *list;
+        const Scalars P = *list;
         int it = 0;
         uint32_t flips = 0;
         for (int t = cluster; t < P.total; t += clusters) {
@@ -588,12 +624,16 @@ __device__ __forceinline__ void products(const Product* list, const Chain* chain
             release[i] = CG == 2 ? cluster_addr(smem_addr(&sh.acc_empty[i]), 0) : smem_addr(&sh.acc_empty[i]);
         int done = 0, round = 0;
         for (int ph = 0; ph < phases; ++ph) {
-            const Product& P = CHAIN ? list[chain->phase(ph)] : *list;
+            const Product& maps = CHAIN ? list[chain->phase(ph)] : *list;
+            const Scalars P = maps;
             const int side = P.symmetric ? 1 : 0;
             const int total = P.ragged == RAGGED_ROWS ? sh.total : P.total;
+            TileAt q;
+            if (cluster < total) q = tile_at<CG>(P, &sh, cluster);
+            if (ph == 0) wait_for_previous();
             if (CHAIN && ph) phases_done(chain->arrived, ph, failed);
             for (int t = cluster; t < total; t += clusters) {
-                const TileAt q = tile_at<CG>(P, &sh, t);
+                if (t != cluster) q = tile_at<CG>(P, &sh, t);
                 int first, last;
                 slices(q, CG == 2 ? 1 : size, rank, first, last);
                 const bool some = first < last;
@@ -642,13 +682,14 @@ __device__ __forceinline__ void products(const Product* list, const Chain* chain
                     float v[32];
     #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] = fmaf(alpha, __uint_as_float(u[i]), bias);
+                    uint32_t w[16];
                     if (P.pre) {
-                        const bool tma = P.tma_pre && (whole || nrows >= 32);
-                        uint16_t* p = P.pre + (row + c) * P.ld_pre + f;
                         if (P.in_bf)
-                            store_block<true>(&P.mp, p, P.ld_pre, v, st, tma, lane, feat, (int)row + c, 0, nrows, nfeat, 0);
+                            pack32<true>(v, w);
                         else
-                            store_block<false>(&P.mp, p, P.ld_pre, v, st, tma, lane, feat, (int)row + c, 0, nrows, nfeat, 0);
+                            pack32<false>(v, w);
+                        store_block(&maps.mp, P.pre + (row + c) * P.ld_pre + f, P.ld_pre, w, st,
+                                    P.tma_pre && (whole || nrows >= 32), lane, feat, (int)row + c, 0, nrows, nfeat, 0);
                     }
                     if (P.act == ACT_RELU) {
     #pragma unroll
@@ -672,23 +713,16 @@ __device__ __forceinline__ void products(const Product* list, const Chain* chain
                     }
                     const int over = feat + 31 - (q.n0 + c);      // symmetric: > 0 where the block reaches above the diagonal
                     if (side && over >= 63) continue;             // nothing of it on this side
-                    {
-                        const bool tma = P.tma_out && (whole || nrows >= 32) && !(side && over > 0);
-                        uint16_t* p = P.out + q.g * P.bs_out + (row + c) * P.ld_out + f;
-                        const int below = side ? f - (q.n0 + c) : 0;   // first row this lane writes
-                        if (P.out_bf)
-                            store_block<true>(&P.mo, p, P.ld_out, v, st, tma, lane, feat, (int)row + c, zo, nrows, nfeat, below);
-                        else
-                            store_block<false>(&P.mo, p, P.ld_out, v, st, tma, lane, feat, (int)row + c, zo, nrows, nfeat, below);
-                    }
-                    if (side && lane < nfeat) {
-                        // the mirror image: a lane's 32 values are neighbours in row f (symmetric outputs are f16
-                        // and start rows at multiples of 16 bytes)
-                        uint16_t* p = P.out + q.g * P.bs_out + (int64_t)f * P.ld_out + q.n0 + c;
-                        const int from = f + 1 - (q.n0 + c);
-    #pragma unroll
-                        for (int i = 0; i < 32; i += 8) store8(p + i, false, true, max(0, min(8, from - i)), min(8, nrows - i), v + i);
-                    }
+                    if (P.out_bf)
+                        pack32<true>(v, w);
+                    else
+                        pack32<false>(v, w);
+                    const int below = side ? f - (q.n0 + c) : 0;   // first row this lane writes
+                    store_block(&maps.mo, P.out + q.g * P.bs_out + (row + c) * P.ld_out + f, P.ld_out, w, st,
+                                P.tma_out && (whole || nrows >= 32) && !(side && over > 0), lane, feat, (int)row + c, zo,
+                                nrows, nfeat, below);
+                    if (side && lane < nfeat)
+                        store_mirror(P.out + q.g * P.bs_out + (int64_t)f * P.ld_out + q.n0 + c, w, below + 1, nrows);
                 }
                 if (some) {
                     fence_before();
