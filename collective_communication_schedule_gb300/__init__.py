@@ -510,36 +510,46 @@ def tune_search(probe, start: PlanOpts | None = None, max_rounds=3, min_gain=0.0
 
 
 # ------------------------------------------------------- tensor products
-_TYPES = {}           # torch dtype -> CCL_*, filled on first use (torch is imported lazily)
+# The calls below are short on the GPU (10 us and up), so their Python side is
+# kept lean: plain checks first, messages only when one fails.
+_torch = None
+_TYPES = {}           # torch dtype -> CCL_*
 
 
-def _dtype_of(t):
-    if not _TYPES:
+def _lazy_torch():
+    """torch, imported on first use (the collectives need no torch)."""
+    global _torch
+    if _torch is None:
         import torch
         _TYPES.update({torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16})
-    code = _TYPES.get(t.dtype)
+        _torch = torch
+    return _torch
+
+
+def _type_code(dtype):
+    code = _TYPES.get(dtype)
     if code is None:
-        raise ValueError(f"unsupported tensor type {t.dtype}")
+        raise ValueError(f"unsupported tensor type {dtype}")
     return code
 
 
-def _matrix(name, t, shape, like):
-    """Address and row stride (0: packed) of a tensor of this shape, on the
-    device and (unless None) of the type of ``like``."""
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
-    if t.dtype != like.dtype or t.device != like.device:
-        raise ValueError(f"{name} is {t.dtype} on {t.device}, not {like.dtype} on {like.device}")
-    if t.is_contiguous():
-        return t.data_ptr(), 0
-    st = t.stride()
+def _row_stride(name, t):
+    """Stride between the rows of a matrix that is not packed (0: one row)."""
+    shape, st = t.shape, t.stride()
     if shape[-1] > 1 and st[-1] != 1:
         raise ValueError(f"{name} needs rows of consecutive elements")
     if len(shape) == 1 or shape[-2] <= 1:
-        return t.data_ptr(), 0
+        return 0
     if st[-2] < shape[-1]:
         raise ValueError(f"{name} has overlapping rows (an expanded tensor: make it contiguous)")
-    return t.data_ptr(), st[-2]
+    return st[-2]
+
+
+def _matrix(name, t, shape, dtype, device):
+    """Address and row stride (0: packed) of a tensor that must be this."""
+    if t.shape != shape or t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name} is {tuple(t.shape)} {t.dtype} on {t.device}, not {tuple(shape)} {dtype} on {device}")
+    return t.data_ptr(), 0 if t.is_contiguous() else _row_stride(name, t)
 
 
 def _stacked(name, t):
@@ -552,113 +562,128 @@ def _stacked(name, t):
     return t.stride(0)
 
 
-def _on(t, stream):
-    """(stream handle, context) of a call on the device of ``t``.  New tensors
-    (outputs, workspaces) are allocated inside the context, so that the
-    allocator ties them to the stream the call runs on."""
-    import torch
-    if not t.is_cuda:
+def _handle(device):
+    """The current stream's handle, on the device of the operands."""
+    if device.type != "cuda":
         raise ValueError("tensor products need CUDA tensors")
-    device = t.device.index
-    if device != torch._C._cuda_getDevice():
-        raise ValueError(f"tensors on {t.device}, but device {torch.cuda.current_device()} is current")
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device), None
+    if device.index != _torch._C._cuda_getDevice():
+        raise ValueError(f"tensors on {device}, but device {_torch.cuda.current_device()} is current")
+    return _torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _on_stream(stream):
+    """A context in which ``stream`` is current: tensors allocated inside (the
+    outputs and workspaces of a call) belong to it."""
+    torch = _lazy_torch()
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
-    return stream.cuda_stream, torch.cuda.stream(stream)
+    return torch.cuda.stream(stream)
 
 
-def _run(name, args, device, handle):
-    """Run a tensor product with the workspace it asks for."""
+def _run(call, workspace, args, device, handle, need=None):
+    """Run a tensor product with the workspace it asks for (``need``: its size
+    where the caller knows it)."""
     ref = ctypes.byref(args)
-    need = ctypes.c_int64()
-    _check(getattr(lib, name + "_workspace")(ref, ctypes.byref(need)))
-    size = need.value
-    if size:
-        import torch
-        ws = torch.empty(size, dtype=torch.uint8, device=device)
-        _check(getattr(lib, name)(ref, ws.data_ptr(), size, handle))
+    if need is None:
+        size = ctypes.c_int64()
+        _check(workspace(ref, ctypes.byref(size)))
+        need = size.value
+    if need:
+        ws = _torch.empty(need, dtype=_torch.uint8, device=device)
+        _check(call(ref, ws.data_ptr(), need, handle))
     else:
-        _check(getattr(lib, name)(ref, None, 0, handle))
+        _check(call(ref, None, 0, handle))
 
 
-def _offsets(offsets, w):
-    import torch
-    if offsets.dtype != torch.int32 or offsets.shape != (w.shape[0] + 1,) or not offsets.is_contiguous():
-        raise ValueError(f"offsets must be {w.shape[0] + 1} consecutive int32 (one more than experts)")
-    if offsets.device != w.device:
-        raise ValueError(f"offsets on {offsets.device}, not {w.device}")
+def _operands(x, w, grouped):
+    """rows, k, n, experts and the shape of a vector per output feature."""
+    shape, of = x.shape, w.shape
+    if len(shape) != 2 or len(of) != (3 if grouped else 2):
+        raise ValueError("x must be rows x k and w n x k (experts x n x k with offsets)")
+    return shape[0], shape[1], of[-2], of[0] if grouped else 0, of[:-1]
+
+
+def _offsets(offsets, experts, device):
+    if offsets.dtype != _torch.int32 or offsets.shape != (experts + 1,) or not offsets.is_contiguous():
+        raise ValueError(f"offsets must be {experts + 1} consecutive int32 (one more than experts)")
+    if offsets.device != device:
+        raise ValueError(f"offsets on {offsets.device}, not {device}")
     return offsets.data_ptr()
 
 
-def _operands(x, w, offsets):
-    """rows, k, n, experts and the shape of a vector per output feature."""
-    if x.dim() != 2 or w.dim() != (2 if offsets is None else 3):
-        raise ValueError("x must be rows x k and w n x k (experts x n x k with offsets)")
-    rows, k = x.shape
-    shape = w.shape
-    if offsets is None:
-        return rows, k, shape[0], 0, shape[:1]
-    return rows, k, shape[1], shape[0], shape[:2]
-
-
 def _forward(x, w, offsets, bias, residual, act, preact, out, stream):
-    rows, k, n, experts, vector = _operands(x, w, offsets)
-    handle, ctx = _on(x, stream)
-    if ctx is not None:
-        with ctx:
+    if stream is not None:
+        with _on_stream(stream):
             return _forward(x, w, offsets, bias, residual, act, preact, out, None)
-    y = x.new_empty((rows, n)) if out is None else out
-    a = Linear(rows, n, k, _dtype_of(x), act, experts)
-    a.x, a.ldx = _matrix("x", x, x.shape, x)
-    a.w, a.ldw = _matrix("w", w, (*vector, k), x)
-    a.y, a.ldy = (y.data_ptr(), 0) if out is None else _matrix("out", y, (rows, n), x)
+    torch = _torch or _lazy_torch()
+    rows, k, n, experts, vector = _operands(x, w, offsets is not None)
+    device, dtype = x.device, x.dtype
+    handle = _handle(device)
+    a = Linear(rows, n, k, _type_code(dtype), act, experts)
+    a.x = px = x.data_ptr()
+    a.w = pw = w.data_ptr()
+    plain = x.is_contiguous() and w.is_contiguous()
+    if not plain:
+        a.ldx = _row_stride("x", x)
+        a.ldw = _row_stride("w", w)
+        if experts:
+            a.w_stride = _stacked("w", w)
+    if w.shape[-1] != k or w.dtype != dtype or w.device != device:
+        _matrix("w", w, (*vector, k), dtype, device)
+    if out is None:
+        y = torch.empty((rows, n), dtype=dtype, device=device)
+        a.y = y.data_ptr()
+    else:
+        y = out
+        a.y, a.ldy = _matrix("out", y, (rows, n), dtype, device)
     if bias is not None:
-        a.bias, _ = _matrix("bias", bias, vector, x)
+        a.bias, _ = _matrix("bias", bias, vector, dtype, device)
         if experts:
             a.bias_stride = _stacked("bias", bias)
     if residual is not None:
-        a.residual, a.ldr = _matrix("residual", residual, (rows, n), x)
+        a.residual, a.ldr = _matrix("residual", residual, (rows, n), dtype, device)
     if experts:
-        a.offsets = _offsets(offsets, w)
-        a.w_stride = _stacked("w", w)
+        a.offsets = _offsets(offsets, experts, device)
     z = None
     if preact:
-        z = x.new_empty((rows, n))
+        z = torch.empty((rows, n), dtype=dtype, device=device)
         a.z = z.data_ptr()
-    _run("ccl_linear", a, x.device, handle)
+    # operands that start and step by 16 bytes are used where they are
+    none = 0 if plain and not ((px | pw) & 15 or k & 7) else None
+    _run(lib.ccl_linear, lib.ccl_linear_workspace, a, device, handle, none)
     return (y, z) if preact else y
 
 
 def _backward(dy, x, w, offsets, preact, act, bias, need_dx, need_dw, stream):
-    rows, k, n, experts, vector = _operands(x, w, offsets)
+    if stream is not None:
+        with _on_stream(stream):
+            return _backward(dy, x, w, offsets, preact, act, bias, need_dx, need_dw, None)
+    torch = _torch or _lazy_torch()
+    rows, k, n, experts, vector = _operands(x, w, offsets is not None)
     if act != ACT_NONE and preact is None:
         raise ValueError("the gradient of an activation needs the pre-activation kept by the forward pass")
-    handle, ctx = _on(x, stream)
-    if ctx is not None:
-        with ctx:
-            return _backward(dy, x, w, offsets, preact, act, bias, need_dx, need_dw, None)
-    a = LinearGrad(rows, n, k, _dtype_of(x), act, experts)
-    a.dy, a.lddy = _matrix("dy", dy, (rows, n), x)
-    a.x, a.ldx = _matrix("x", x, x.shape, x)
-    a.w, a.ldw = _matrix("w", w, (*vector, k), x)
+    device, dtype = x.device, x.dtype
+    handle = _handle(device)
+    a = LinearGrad(rows, n, k, _type_code(dtype), act, experts)
+    a.dy, a.lddy = _matrix("dy", dy, (rows, n), dtype, device)
+    a.x, a.ldx = _matrix("x", x, x.shape, dtype, device)
+    a.w, a.ldw = _matrix("w", w, (*vector, k), dtype, device)
     if act != ACT_NONE:
-        a.z, a.ldz = _matrix("preact", preact, (rows, n), x)
+        a.z, a.ldz = _matrix("preact", preact, (rows, n), dtype, device)
     if experts:
-        a.offsets = _offsets(offsets, w)
+        a.offsets = _offsets(offsets, experts, device)
         a.w_stride = _stacked("w", w)
     dx = dw = db = None
     if need_dx:
-        dx = x.new_empty((rows, k))
+        dx = torch.empty((rows, k), dtype=dtype, device=device)
         a.dx = dx.data_ptr()
     if need_dw:
-        dw = x.new_empty((*vector, k))
+        dw = torch.empty((*vector, k), dtype=dtype, device=device)
         a.dw = dw.data_ptr()
     if bias:
-        db = x.new_empty(vector)
+        db = torch.empty(vector, dtype=dtype, device=device)
         a.db = db.data_ptr()
-    _run("ccl_linear_grad", a, x.device, handle)
+    _run(lib.ccl_linear_grad, lib.ccl_linear_grad_workspace, a, device, handle)
     return dx, dw, db
 
 
@@ -692,25 +717,24 @@ def orthogonalize(g, steps=5, coeffs=(3.4445, -4.7750, 2.0315), eps=1e-7, scale=
     """Newton-Schulz orthogonalisation of a gradient matrix (p, q) or a stack
     (batch, p, q) of them, f32, bf16 or f16 (``ccl_orthogonalize``).  The
     update is bf16 unless ``out`` is a given f16 matrix."""
-    import torch
-    if g.dim() not in (2, 3):
-        raise ValueError("g must be a matrix or a stack of matrices")
-    handle, ctx = _on(g, stream)
-    if ctx is not None:
-        with ctx:
+    if stream is not None:
+        with _on_stream(stream):
             return orthogonalize(g, steps, coeffs, eps, scale, out, None)
+    torch = _torch or _lazy_torch()
+    shape, device = g.shape, g.device
+    if len(shape) not in (2, 3):
+        raise ValueError("g must be a matrix or a stack of matrices")
+    handle = _handle(device)
     if out is None:
-        out = torch.empty(g.shape, dtype=torch.bfloat16, device=g.device)
-    stack = g.dim() == 3
-    args = Ortho(g.shape[0] if stack else 1, g.shape[-2], g.shape[-1], _dtype_of(g), _dtype_of(out), steps, *coeffs,
-                 eps, scale)
-    args.g, args.ldg = _matrix("g", g, g.shape, g)
-    args.out, args.ldo = _matrix("out", out, g.shape, out)
-    if out.device != g.device:
-        raise ValueError(f"out on {out.device}, not {g.device}")
+        out = torch.empty(shape, dtype=torch.bfloat16, device=device)
+    stack = len(shape) == 3
+    a = Ortho(shape[0] if stack else 1, shape[-2], shape[-1], _type_code(g.dtype), _type_code(out.dtype), steps, *coeffs,
+              eps, scale)
+    a.g, a.ldg = _matrix("g", g, shape, g.dtype, device)
+    a.out, a.ldo = _matrix("out", out, shape, out.dtype, device)
     if stack:
-        args.g_stride, args.out_stride = _stacked("g", g), _stacked("out", out)
-    _run("ccl_orthogonalize", args, g.device, handle)
+        a.g_stride, a.out_stride = _stacked("g", g), _stacked("out", out)
+    _run(lib.ccl_orthogonalize, lib.ccl_orthogonalize_workspace, a, device, handle)
     return out
 
 

@@ -1310,7 +1310,7 @@ static Shape choose(const Product& P, int sms, bool chain)
     Shape best = {0, 0, 0, 0};
     for (int cg = 1; cg <= (chain ? 1 : 2); ++cg) {
         for (int bn : {256, 192, 128, 64, 32}) {
-            if (bn / cg % (P.b_mn ? 64 : 16)) continue;
+            if (bn / cg % (P.b_mn ? 64 : 16) || (bn > 64 && bn / 2 >= rows)) continue;
             for (int split = 1; split <= (chain || cg == 2 || bn > 128 ? 1 : 8); split *= 2) {
                 if (split > 1 && split * 2 > slices) continue;
                 const double tiles_m = std::ceil((double)P.m / (cg * kTileM)), tiles_n = std::ceil(rows / bn);
@@ -1395,17 +1395,17 @@ static std::string dims(int64_t rows, int64_t n, int64_t k)
 static ccl_status_t check_shape(const char* who, int64_t rows, int64_t n, int64_t k, int32_t dtype, int32_t act,
                                 int32_t experts, const void* offsets)
 {
-    const std::string w = std::string(who) + ": ";
+    auto refuse = [&](ccl_status_t st, const std::string& why) { return fail(st, std::string(who) + ": " + why); };
     if (dtype != CCL_BF16 && dtype != CCL_F16)
-        return fail(CCL_ERR_UNSUPPORTED, w + "products take bf16 and f16 (dtype " + std::to_string(dtype) + ")");
+        return refuse(CCL_ERR_UNSUPPORTED, "products take bf16 and f16 (dtype " + std::to_string(dtype) + ")");
     const int64_t top = (int64_t)1 << 30;
     if (rows < 0 || n < 1 || k < 1 || rows > top || n > top || k > top)
-        return fail(CCL_ERR_INVALID_ARG, w + "sizes out of range (" + dims(rows, n, k) + ")");
+        return refuse(CCL_ERR_INVALID_ARG, "sizes out of range (" + dims(rows, n, k) + ")");
     if (act < CCL_ACT_NONE || act > CCL_ACT_SILU)
-        return fail(CCL_ERR_INVALID_ARG, w + "unknown activation " + std::to_string(act));
+        return refuse(CCL_ERR_INVALID_ARG, "unknown activation " + std::to_string(act));
     if (experts < 0 || experts > kMaxGroups)
-        return fail(CCL_ERR_INVALID_ARG, w + "experts outside 0.." + std::to_string(kMaxGroups));
-    if (experts > 0 && !offsets) return fail(CCL_ERR_INVALID_ARG, w + "experts without offsets");
+        return refuse(CCL_ERR_INVALID_ARG, "experts outside 0.." + std::to_string(kMaxGroups));
+    if (experts > 0 && !offsets) return refuse(CCL_ERR_INVALID_ARG, "experts without offsets");
     return CCL_OK;
 }
 
