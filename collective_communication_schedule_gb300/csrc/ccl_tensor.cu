@@ -1101,6 +1101,317 @@ __global__ void __launch_bounds__(256) scale_kernel(const NormPass N)
     }
 }
 
+// All of the iteration for matrices with a side of at most 128, in one launch
+// and without leaving the SM: x, A and B live in shared memory in the layout
+// the matrix instructions read, accumulators in tensor memory, and a step is
+// three products with a threadblock barrier after each.  A long side is cut
+// over the threadblocks of a cluster, `width` columns of x each: they add up
+// their parts of A = x x^T through distributed shared memory (each sums 128 /
+// size rows, in rank order, and hands them to all), the rest of the step
+// stays within a threadblock.  A tall matrix is transposed as it is loaded
+// and stored.  Bound by the latency of the chain of 3 x steps products.
+//
+// Rows of 64 elements (128 bytes) in 1024-byte atoms of 8 rows, 16-byte pieces
+// exchanged by the row's index: element (i, j) of x is at piece (j / 8 % 8) ^
+// (i % 8) of row i of block j / 64.  The same bytes are x with the reduction
+// along its columns (x x^T) and along its rows (B x).
+constexpr int kSmallSide = 128;
+constexpr int kSmallThreads = 512;
+constexpr int kSmallBlock = kSmallSide * 128;          // bytes of a block of 64 columns
+constexpr int kSharePitch = kSmallSide + 4;            // floats; rows 4 banks apart
+
+struct Small {
+    const void* g;
+    uint16_t* out;
+    int64_t ld_g, bs_g, ld_out, bs_out;
+    int32_t side, length;          // short and long side
+    int32_t tall, type, out_bf, steps;
+    int32_t size, width, vec_out;
+    float a, b, c, eps, scale;
+};
+
+__device__ __forceinline__ uint32_t small_at(int i, int j)
+{
+    return (uint32_t)(j >> 6) * kSmallBlock + i * 128 + (((j >> 3) & 7) ^ (i & 7)) * 16;
+}
+
+__device__ __forceinline__ void store_cluster16(uint32_t addr, uint4 v)
+{
+    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+
+__global__ void __launch_bounds__(kSmallThreads, 1) small_ortho_kernel(const __grid_constant__ Small S)
+{
+    __shared__ __align__(8) uint64_t done;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int failed;
+    __shared__ float sm[16], norms[8];
+    extern __shared__ unsigned char raw[];
+    unsigned char* dyn = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = warp & 3, group = warp >> 2;
+    const int rank = S.size > 1 ? (int)cluster_rank() : 0, entry = blockIdx.x / S.size;
+    const int width = S.width, col0 = rank * width, cols = max(0, min(width, S.length - col0));
+    unsigned char *x = dyn, *A = x + (size_t)width / 64 * kSmallBlock, *B = A + 2 * kSmallBlock;
+    float* shares = reinterpret_cast<float*>(B + 2 * kSmallBlock);   // size > 1: [source][own row][column of A]
+    const uint32_t bar = smem_addr(&done);
+    if (threadIdx.x == 0) {
+        bar_init(bar, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        failed = 0;
+    }
+    if (warp == 1) tmem_alloc<1>(smem_addr(&tmem_slot), 512);
+    let_next_in();
+    wait_for_previous();
+
+    // 8 columns j.. of row i of g (or of its transpose)
+    const int64_t base = (int64_t)entry * S.bs_g;
+    auto fetch = [&](int i, int j, float v[8]) {
+        if (i >= S.side || j >= cols) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = 0.f;
+        } else if (S.tall) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[e] = j + e < cols ? load_any(S.g, base + (int64_t)(col0 + j + e) * S.ld_g + i, S.type) : 0.f;
+        } else if (j + 8 <= cols) {
+            load_any8(S.g, base + i * S.ld_g + col0 + j, S.type, v);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[e] = j + e < cols ? load_any(S.g, base + i * S.ld_g + col0 + j + e, S.type) : 0.f;
+        }
+    };
+    // neighbouring threads take neighbouring elements in memory
+    const int pieces = width / 8, items = pieces * kSmallSide;
+    auto place = [&](int n, int& i, int& j) {
+        if (S.tall) {
+            i = n % kSmallSide;
+            j = n / kSmallSide * 8;
+        } else {
+            i = n / pieces;
+            j = n % pieces * 8;
+        }
+    };
+    float sum = 0.f;
+#pragma unroll 2
+    for (int n = threadIdx.x; n < items; n += kSmallThreads) {
+        int i, j;
+        place(n, i, j);
+        float v[8], t = 0.f;
+        fetch(i, j, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) t = fmaf(v[e], v[e], t);
+        sum += t;
+    }
+    sum = block_sum(sum, sm);
+    if (S.size > 1) {
+        cluster_sync();            // the others' shared memory is live from here on
+        if ((int)threadIdx.x < S.size) store_cluster(cluster_addr(smem_addr(&norms[rank]), threadIdx.x), sum);
+        cluster_sync();
+        sum = 0.f;
+        for (int i = 0; i < S.size; ++i) sum += norms[i];
+    }
+    float kappa, f1, f2;
+    norm_scale(sum, S.eps, kappa, f1, f2);
+#pragma unroll 2
+    for (int n = threadIdx.x; n < items; n += kSmallThreads) {
+        int i, j;
+        place(n, i, j);
+        float v[8];
+        fetch(i, j, v);
+        uint4 u;
+        uint32_t* w = &u.x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = pack2<false>(v[2 * e] * f1 * f2, v[2 * e + 1] * f1 * f2);
+        *reinterpret_cast<uint4*>(x + small_at(i, j)) = u;
+    }
+    fence_async();
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = tmem_slot, lanes = (uint32_t)(quad * 32) << 16;
+    const uint32_t x_at = (smem_addr(x) & 0x3ffff) >> 4, a_at = (smem_addr(A) & 0x3ffff) >> 4,
+                   b_at = (smem_addr(B) & 0x3ffff) >> 4;
+    const uint64_t along = operand_desc(0, 0, 1024), across = operand_desc(0, kSmallBlock, 1024);
+    const uint32_t square = mma_desc(false, false, false, kSmallSide, kSmallSide);
+    constexpr uint32_t to_x = kSmallSide;       // tensor memory: columns 0.. A or B, 128.. x
+    const int row = quad * 32 + lane;
+    uint32_t parity = 0;
+    // an accumulator's 32 columns from `col` of this thread's row, once all products issued so far are done
+    auto finish = [&]() {
+        if (!bar_wait(bar, parity, &failed)) failed = 1;
+        parity ^= 1;
+        fence_after();
+    };
+
+    for (int step = 0; step < S.steps; ++step) {
+        const bool first = step == 0, last = step + 1 == S.steps;
+        // A = x x^T
+        if (warp == 0) {
+            if (elect_one()) {
+                for (int k = 0; k < width / 16; ++k) {
+                    const uint32_t at = x_at + ((k >> 2) * kSmallBlock + (k & 3) * 32 >> 4);
+                    mma_f16<1>(tmem, along | at, along | at, square, k > 0);
+                }
+                mma_commit<1>(bar);
+            }
+            __syncwarp();
+        }
+        finish();
+        const float alpha = kScaleA / (kScaleX * kScaleX) * (first ? kappa * kappa : 1.f);
+        {
+            uint32_t u[32];
+            tmem_load32(tmem + lanes + group * 32, u);
+            if (S.size == 1) {
+#pragma unroll
+                for (int c = 0; c < 32; c += 8) {
+                    uint4 h;
+                    uint32_t* w = &h.x;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        w[e] = pack2<false>(alpha * __uint_as_float(u[c + 2 * e]), alpha * __uint_as_float(u[c + 2 * e + 1]));
+                    *reinterpret_cast<uint4*>(A + small_at(row, group * 32 + c)) = h;
+                }
+            } else {
+                const int own = kSmallSide / S.size, to = row / own;
+                const uint32_t at = cluster_addr(
+                    smem_addr(shares + ((size_t)rank * own + row % own) * kSharePitch + group * 32), to);
+#pragma unroll
+                for (int c = 0; c < 32; c += 4) store_cluster16(at + c * 4, make_uint4(u[c], u[c + 1], u[c + 2], u[c + 3]));
+            }
+        }
+        if (S.size > 1) {
+            cluster_sync();
+            const int own = kSmallSide / S.size;
+            for (int n = threadIdx.x; n < own * (kSmallSide / 8); n += kSmallThreads) {
+                const int r = n / (kSmallSide / 8), c = n % (kSmallSide / 8) * 8;
+                float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                for (int s = 0; s < S.size; ++s) {
+                    const float4* p = reinterpret_cast<const float4*>(shares + ((size_t)s * own + r) * kSharePitch + c);
+                    const float4 l = p[0], h = p[1];
+                    v[0] += l.x, v[1] += l.y, v[2] += l.z, v[3] += l.w;
+                    v[4] += h.x, v[5] += h.y, v[6] += h.z, v[7] += h.w;
+                }
+                uint4 h;
+                uint32_t* w = &h.x;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[e] = pack2<false>(alpha * v[2 * e], alpha * v[2 * e + 1]);
+                const uint32_t at = smem_addr(A + small_at(rank * own + r, c));
+                for (int s = 0; s < S.size; ++s) store_cluster16(cluster_addr(at, s), h);
+            }
+            asm volatile("fence.proxy.async;" ::: "memory");
+            fence_before();
+            cluster_sync();
+            fence_after();
+        } else {
+            fence_async();
+            fence_before();
+            __syncthreads();
+            fence_after();
+        }
+        // B = b A + c A A (A is symmetric)
+        if (warp == 0) {
+            if (elect_one()) {
+                fence_async();
+#pragma unroll
+                for (int k = 0; k < kSmallSide / 16; ++k) {
+                    const uint32_t at = a_at + ((k >> 2) * kSmallBlock + (k & 3) * 32 >> 4);
+                    mma_f16<1>(tmem, along | at, along | at, square, k > 0);
+                }
+                mma_commit<1>(bar);
+            }
+            __syncwarp();
+        }
+        finish();
+        {
+            uint32_t u[32];
+            tmem_load32(tmem + lanes + group * 32, u);
+            const float beta = S.b, gamma = S.c / kScaleA;
+#pragma unroll
+            for (int c = 0; c < 32; c += 8) {
+                const uint32_t at = small_at(row, group * 32 + c);
+                float o[8];
+                unpack8(*reinterpret_cast<const uint4*>(A + at), false, o);
+                uint4 h;
+                uint32_t* w = &h.x;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    w[e] = pack2<false>(gamma * __uint_as_float(u[c + 2 * e]) + beta * o[2 * e],
+                                        gamma * __uint_as_float(u[c + 2 * e + 1]) + beta * o[2 * e + 1]);
+                *reinterpret_cast<uint4*>(B + at) = h;
+            }
+        }
+        fence_async();
+        fence_before();
+        __syncthreads();
+        fence_after();
+        // x <- a x + B x
+        if (warp == 0) {
+            if (elect_one()) {
+                for (int n = 0; n < width; n += 256) {
+                    const uint32_t idesc = mma_desc(false, false, true, kSmallSide, min(256, width - n));
+#pragma unroll
+                    for (int k = 0; k < kSmallSide / 16; ++k)
+                        mma_f16<1>(tmem + to_x + n, along | (b_at + ((k >> 2) * kSmallBlock + (k & 3) * 32 >> 4)),
+                                   across | (x_at + (n / 64 * kSmallBlock + k * 2048 >> 4)), idesc, k > 0);
+                }
+                mma_commit<1>(bar);
+            }
+            __syncwarp();
+        }
+        finish();
+        const float unscale = (last ? S.scale / kScaleX : 1.f) * (first ? kappa : 1.f);
+        const float beta = S.a * unscale, gamma = unscale / kScaleA;
+        for (int c0 = group * 32; c0 < width; c0 += 128) {
+            uint32_t u[32], w[16];
+            tmem_load32(tmem + lanes + to_x + c0, u);
+#pragma unroll
+            for (int c = 0; c < 32; c += 8) {
+                unsigned char* p = x + small_at(row, c0 + c);
+                float o[8];
+                unpack8(*reinterpret_cast<const uint4*>(p), false, o);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] = gamma * __uint_as_float(u[c + e]) + beta * o[e];
+                const bool bf = last && S.out_bf;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    w[c / 2 + e] = bf ? pack2<true>(o[2 * e], o[2 * e + 1]) : pack2<false>(o[2 * e], o[2 * e + 1]);
+                if (!last)
+                    *reinterpret_cast<uint4*>(p) = make_uint4(w[c / 2], w[c / 2 + 1], w[c / 2 + 2], w[c / 2 + 3]);
+            }
+            if (last && row < S.side) {
+                const int n = cols - c0;         // columns of this thread's 32 that exist
+                uint16_t* o = S.out + (int64_t)entry * S.bs_out;
+                if (S.tall) {
+                    o += (int64_t)(col0 + c0) * S.ld_out + row;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e, o += S.ld_out)
+                        if (e < n) *o = (uint16_t)(w[e / 2] >> (e & 1) * 16);
+                } else {
+                    o += row * S.ld_out + col0 + c0;
+                    if (S.vec_out && n >= 32) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            reinterpret_cast<uint4*>(o)[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (e < n) o[e] = (uint16_t)(w[e / 2] >> (e & 1) * 16);
+                    }
+                }
+            }
+        }
+        fence_async();
+        fence_before();
+        __syncthreads();
+        fence_after();
+    }
+    if (failed && threadIdx.x == 0) atomicCAS(&g_status[0], 0, (int)CCL_ERR_TIMEOUT);
+    if (S.size > 1) cluster_sync();     // nobody leaves while another may still write to it
+    if (warp == 1) tmem_free<1>(tmem, 512);
+}
+
 // ======================================================================
 // Host side
 // ======================================================================
@@ -1157,6 +1468,8 @@ static ccl_status_t device(const Device** out)
                          "shared memory of the product kernel");
         TRY_CUDA(cudaFuncSetAttribute(chain_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBudget),
                  "shared memory of the chain kernel");
+        TRY_CUDA(cudaFuncSetAttribute(small_ortho_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBudget),
+                 "shared memory of the small orthogonalisation kernel");
         all[d].ready = true;
     }
     *out = &all[d];
@@ -1611,6 +1924,12 @@ static ccl_status_t orthogonalize(const ccl_ortho_t* a, char* base, int64_t* nee
     if (!a->out_stride) so = a->p * ldo;
     const int64_t r = std::min(a->p, a->q);
     const bool tall = a->p > a->q;
+    // threadblocks that a matrix with a short side of up to 128 takes: each
+    // holds up to 384 columns, or 256 beside the others' shares of A
+    const int64_t longer = std::max(a->p, a->q);
+    int size = 1;
+    while (size < 8 && longer > (size == 1 ? 384 : 256 * size)) size *= 2;
+    const bool small = r <= kSmallSide && longer <= (size == 1 ? 384 : 256 * size);
     Arena ws = {base};
     Matrix x[2], A, B;
     const int64_t ldx = round_up(a->q, 8), lda = round_up(r, 8);
@@ -1627,13 +1946,41 @@ static ccl_status_t orthogonalize(const ccl_ortho_t* a, char* base, int64_t* nee
     N.kappa2 = ws.take<float>(a->batch * 4);
     N.arrived = ws.take<uint32_t>(4);
     if (need) {
-        *need = ws.used;
+        *need = small ? 0 : ws.used;
         return CCL_OK;
     }
     if (a->batch == 0) return CCL_OK;
     if (!a->g || !a->out) return fail(CCL_ERR_INVALID_ARG, who + "null matrix");
     if ((uintptr_t)a->g % (a->dtype == CCL_F32 ? 4 : 2) || (uintptr_t)a->out % 2)
         return fail(CCL_ERR_INVALID_ARG, who + "a matrix is not aligned to its elements");
+    if (small) {
+        Small S = {};
+        S.g = a->g;
+        S.out = (uint16_t*)a->out;
+        S.ld_g = ldg;
+        S.bs_g = sg;
+        S.ld_out = ldo;
+        S.bs_out = so;
+        S.side = (int32_t)r;
+        S.length = (int32_t)longer;
+        S.tall = tall;
+        S.type = a->dtype;
+        S.out_bf = a->out_dtype == CCL_BF16;
+        S.steps = a->steps;
+        S.size = size;
+        S.width = (int32_t)round_up((longer + size - 1) / size, 64);
+        S.vec_out = vectors(a->out, ldo, so);
+        S.a = a->a;
+        S.b = a->b;
+        S.c = a->c;
+        S.eps = a->eps;
+        S.scale = a->scale;
+        const Device* dev = nullptr;
+        TRY(device(&dev));
+        const size_t smem = 1024 + (size_t)S.width / 64 * kSmallBlock + 4 * kSmallBlock +
+                            (size > 1 ? (size_t)kSmallSide * kSharePitch * 4 : 0);
+        return launch(small_ortho_kernel, dim3((unsigned)(a->batch * size)), kSmallThreads, smem, stream, S, size);
+    }
     N.g = a->g;
     N.x = (__half*)x[0].p;
     N.ld_g = ldg;

@@ -388,6 +388,24 @@ def test_orthogonalize(ccl, shape, dtype):
         assert rel <= 8e-3, rel
 
 
+@pytest.mark.parametrize("shape", [(1, 128, 384), (1, 385, 128), (2, 100, 900), (1, 2000, 77), (3, 128, 2048), (1, 60, 1025),
+                                   (40, 64, 257), (1, 2049, 128), (2, 127, 511), (1, 3, 2000)])
+def test_orthogonalize_with_a_short_side(ccl, shape):
+    """One threadblock or a cluster per matrix; same tolerance as above."""
+    g = rnd(gen(sum(shape)), *shape, dtype=torch.float32).mul_(3.0)
+    out = torch.full((shape[0], shape[1] + 1, shape[2] + 5), 7.0, dtype=torch.bfloat16, device="cuda")
+    view = out[:, :-1, 2:-3]
+    ccl.orthogonalize(g, out=view)
+    ccl.tensor_status()
+    mask = torch.ones_like(out, dtype=torch.bool)
+    mask[:, :-1, 2:-3] = False
+    assert bool((out[mask] == 7).all())
+    for i in range(shape[0]):
+        want = ns64(g[i].double(), 5, MUON)
+        rel = ((view[i].double() - want).norm() / want.norm()).item()
+        assert rel <= 8e-3, rel
+
+
 def test_orthogonalize_options(ccl):
     g = rnd(gen(3), 96, 160, dtype=torch.float32)
     cubic = (1.5, -0.5, 0.0)
