@@ -32,7 +32,7 @@ namespace tensor {
 // A threadblock owns 128 features x bn rows of the output at a time.  Warp 0
 // streams 128-wide slices of the reduction axis into a ring of shared-memory
 // stages with TMA, warp 1 issues tcgen05 matrix instructions into one of two
-// accumulators in tensor memory, warps 4..11 drain the other one through the
+// accumulators in tensor memory, warps 4..19 drain the other one through the
 // epilogue, so that an epilogue costs nothing as long as it is shorter than
 // the next tile's products.  Warp 3 clears what a ragged reduction must not
 // see.  Two ways to use a cluster:
@@ -49,9 +49,10 @@ constexpr int kTileM = 128;
 constexpr int kSliceK = 128;      // reduction elements per stage: two swizzled rows of 64, or 128 rows
 constexpr int kMaxStages = 6;
 constexpr int kMaxGroups = 1024;
-constexpr int kEpilogueWarps = 8;
+constexpr int kEpilogueWarps = 16;
 constexpr int kThreads = 128 + 32 * kEpilogueWarps;
-constexpr int kStagingBytes = kEpilogueWarps * 2048;   // a block of 32 x 32 outputs per epilogue warp
+constexpr int kBlockRows = 16;                  // an epilogue warp's block: 16 rows x 32 features
+constexpr int kStagingBytes = kEpilogueWarps * kBlockRows * 64;
 constexpr int kSmemBudget = 227 * 1024 - 6 * 1024;   // dynamic part; the rest is static
 
 enum { DENSE = 0, RAGGED_ROWS = 1, RAGGED_REDUCE = 2 };
@@ -284,27 +285,22 @@ __device__ __forceinline__ void side_range(int side, int64_t n, int f, int nfeat
     if (side < 0) lo = (int)max((int64_t)0, n - f + 1);
 }
 
-// 32 rows of C at one feature per lane: 64 neighbouring bytes a row and warp,
-// whatever the alignment (past L1: in a chain other SMs write C)
-__device__ __forceinline__ void fetch_c(const Scalars& P, uint16_t c[32], int g, int64_t row, int nrows, int f)
+// A block's rows of C at one feature per lane: 64 neighbouring bytes a row and
+// warp, whatever the alignment (past L1: in a chain other SMs write C).
+__device__ __forceinline__ void fetch_c(const Scalars& P, uint16_t c[kBlockRows], int g, int64_t row, int nrows, int f)
 {
     const uint16_t* p = P.c + g * P.bs_c + row * P.ld_c + f;
-    if (f < P.m && nrows >= 32) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i, p += P.ld_c) c[i] = __ldcg(p);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i, p += P.ld_c) c[i] = f < P.m && i < nrows ? __ldcg(p) : (uint16_t)0;
-    }
+    for (int i = 0; i < kBlockRows; ++i, p += P.ld_c) c[i] = f < P.m && i < nrows ? __ldcg(p) : (uint16_t)0;
 }
 
-// A block of 32 rows x 32 features (one feature per lane, two rows per word)
+// A block of 16 rows x 32 features (one feature per lane, two rows per word)
 // to global memory: through shared memory and a TMA store where the whole
 // block may be written (the parts of it outside the matrix are cut off by
 // TMA), else 64 neighbouring bytes of a row at a time.  below: the first row
 // this lane writes (symmetric outputs: feature <= row).  buf: this warp's
-// 2 KB of shared memory.
-__device__ __forceinline__ void store_block(const CUtensorMap* map, uint16_t* p, int64_t ld, const uint32_t w[16],
+// 1 KB of shared memory.
+__device__ __forceinline__ void store_block(const CUtensorMap* map, uint16_t* p, int64_t ld, const uint32_t w[kBlockRows / 2],
                                             unsigned char* buf, bool tma, int lane, int x, int y, int z, int nrows,
                                             int nfeat, int below)
 {
@@ -313,7 +309,7 @@ __device__ __forceinline__ void store_block(const CUtensorMap* map, uint16_t* p,
         __syncwarp();
         uint16_t* b = reinterpret_cast<uint16_t*>(buf) + lane;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < kBlockRows / 2; ++i) {
             b[i * 64] = (uint16_t)w[i];
             b[i * 64 + 32] = (uint16_t)(w[i] >> 16);
         }
@@ -322,39 +318,43 @@ __device__ __forceinline__ void store_block(const CUtensorMap* map, uint16_t* p,
         if (lane == 0) tma_store(map, smem_addr(buf), x, y, z);
     } else if (lane < nfeat) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i, p += ld)
+        for (int i = 0; i < kBlockRows; ++i, p += ld)
             if (i < nrows && i >= below) *p = (uint16_t)(w[i / 2] >> (i & 1) * 16);
     }
 }
 
-// Its mirror image in a symmetric output: a lane's 32 values are neighbours
+// Its mirror image in a symmetric output: a lane's 16 values are neighbours
 // in row `feature`, from the first one above the diagonal on (rows start at
 // multiples of 16 bytes).
-__device__ __forceinline__ void store_mirror(uint16_t* p, const uint32_t w[16], int from, int nrows)
+__device__ __forceinline__ void store_mirror(uint16_t* p, const uint32_t w[kBlockRows / 2], int from, int nrows)
 {
-    if (from <= 0 && nrows >= 32) {
+    if (from <= 0 && nrows >= kBlockRows) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < kBlockRows / 8; ++i)
             reinterpret_cast<uint4*>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
     } else {
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
+        for (int i = 0; i < kBlockRows; ++i)
             if (i >= from && i < nrows) p[i] = (uint16_t)(w[i / 2] >> (i & 1) * 16);
     }
 }
 
-template <bool BF>
-__device__ __forceinline__ void pack32(const float v[32], uint32_t w[16])
+__device__ __forceinline__ void pack_block(const float v[kBlockRows], uint32_t w[kBlockRows / 2], bool bf)
 {
+    if (bf) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) w[i] = pack2<BF>(v[2 * i], v[2 * i + 1]);
+        for (int i = 0; i < kBlockRows / 2; ++i) w[i] = pack2<true>(v[2 * i], v[2 * i + 1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kBlockRows / 2; ++i) w[i] = pack2<false>(v[2 * i], v[2 * i + 1]);
+    }
 }
 
 // FORM: storage of the operands, or ANY_FORM (looked up)
 enum { BOTH_K = 0, A_MN = 1, BOTH_MN = 2, ANY_FORM = 3 };
 
-// Wait (bounded) until all threadblocks have finished `phases` phases, and
-// let this thread's loads see what they wrote.
+// Wait (bounded) until all threadblocks have finished `phases` phases.  By
+// one thread of those that go on after it: polling is felt by the others.
 __device__ __noinline__ bool phases_done(const uint32_t* arrived, uint32_t phases, volatile int* failed)
 {
     const uint32_t want = phases * gridDim.x;
@@ -362,10 +362,7 @@ __device__ __noinline__ bool phases_done(const uint32_t* arrived, uint32_t phase
     for (int i = 0; i < kWaitSpins; ++i) {
         uint32_t v;
         asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(arrived) : "memory");
-        if (v >= want) {
-            asm volatile("fence.proxy.async;" ::: "memory");
-            return true;
-        }
+        if (v >= want) return true;
         if ((i & 255) == 255) {
             if (*failed) return false;
             const unsigned long long t = now_ns();
@@ -463,7 +460,11 @@ __device__ __forceinline__ void products(const Product* list, const Chain* chain
             TileAt q;
             if (cluster < total) q = tile_at<CG>(P, &sh, cluster);
             if (ph == 0) wait_for_previous();
-            if (CHAIN && ph && good) good = phases_done(chain->arrived, ph, failed);
+            if (CHAIN && ph && good) {
+                if (lane == 0) good = phases_done(chain->arrived, ph, failed);
+                good = __shfl_sync(~0u, good, 0);
+                asm volatile("fence.proxy.async;" ::: "memory");
+            }
             for (int t = cluster; t < total; t += clusters) {
                 if (t != cluster) q = tile_at<CG>(P, &sh, t);
                 const int m0 = q.m0 + (CG == 2 ? rank * kTileM : 0);
@@ -617,8 +618,9 @@ __device__ __forceinline__ void products(const Product* list, const Chain* chain
         }
         __syncwarp();
     } else if (warp >= 4) {
-        const int quad = warp & 3, half = (warp - 4) >> 2;
-        unsigned char* st = staging + (warp - 4) * 2048;
+        const int quad = warp & 3, slot = (warp - 4) >> 2;
+        constexpr int kStride = kEpilogueWarps / 4 * kBlockRows;     // rows that the warps of a quadrant take at once
+        unsigned char* st = staging + (warp - 4) * (kBlockRows * 64);
         uint32_t release[2];
         for (int i = 0; i < 2; ++i)
             release[i] = CG == 2 ? cluster_addr(smem_addr(&sh.acc_empty[i]), 0) : smem_addr(&sh.acc_empty[i]);
@@ -631,7 +633,10 @@ __device__ __forceinline__ void products(const Product* list, const Chain* chain
             TileAt q;
             if (cluster < total) q = tile_at<CG>(P, &sh, cluster);
             if (ph == 0) wait_for_previous();
-            if (CHAIN && ph) phases_done(chain->arrived, ph, failed);
+            if (CHAIN && ph) {
+                if (threadIdx.x == 128) phases_done(chain->arrived, ph, failed);
+                named_sync(3, 32 * kEpilogueWarps);
+            }
             for (int t = cluster; t < total; t += clusters) {
                 if (t != cluster) q = tile_at<CG>(P, &sh, t);
                 int first, last;
@@ -645,9 +650,9 @@ __device__ __forceinline__ void products(const Product* list, const Chain* chain
                 const float bias = P.bias && f < P.m ? load1(P.bias + q.g * P.bs_bias + f, P.in_bf) : 0.f;
                 const bool whole = P.ragged != RAGGED_ROWS;    // TMA may cut rows off at the end of the matrix only
                 const int zo = P.ragged == RAGGED_ROWS ? 0 : q.g;
-                uint16_t cv[32];
+                uint16_t cv[kBlockRows];
                 // C is read a block ahead of its use
-                if (P.c && size == CG) fetch_c(P, cv, q.g, row + half * 32, q.live - half * 32, f);
+                if (P.c && size == CG) fetch_c(P, cv, q.g, row + slot * kBlockRows, q.live - slot * kBlockRows, f);
                 if (some) {
                     if (!__all_sync(~0u, bar_wait(smem_addr(&sh.acc_full[acc]), (done >> 1) & 1, failed))) break;
                     fence_after();
@@ -656,71 +661,67 @@ __device__ __forceinline__ void products(const Product* list, const Chain* chain
                     // shares of the last tile have been read by their owners
                     if (!__all_sync(~0u, bar_wait<true>(smem_addr(&sh.taken), (round & 1) ^ 1, failed))) break;
                 }
-                for (int c = half * 32; c < q.live; c += 64) {
-                    uint32_t u[32];
+                const uint32_t from = tmem + ((uint32_t)(quad * 32) << 16) + acc * width;
+                for (int c = slot * kBlockRows; c < q.live; c += kStride) {
+                    uint32_t u[kBlockRows];
                     if (some) {
-                        tmem_load32(tmem + ((uint32_t)(quad * 32) << 16) + acc * width + c, u);
+                        tmem_load16(from + c, u);
                     } else {
-    #pragma unroll
-                        for (int i = 0; i < 32; ++i) u[i] = 0;
+#pragma unroll
+                        for (int i = 0; i < kBlockRows; ++i) u[i] = 0;
                     }
                     const int nrows = q.live - c;
                     if (size > CG) {
                         const int own = P.bn / size;
                         const uint32_t at = smem_addr(shares + (size_t)rank * own * kTileM + quad * 32 + lane);
                         // own is a power of two from 4 up: 4 rows at a time go to one owner
-    #pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
+#pragma unroll
+                        for (int i = 0; i < kBlockRows; i += 4) {
                             const int r = c + i;
                             const uint32_t to = cluster_addr(at + r % own * (kTileM * 4), r / own);
-    #pragma unroll
+#pragma unroll
                             for (int e = 0; e < 4; ++e)
                                 if (i + e < nrows) store_cluster(to + e * (kTileM * 4), __uint_as_float(u[i + e]));
                         }
                         continue;
                     }
-                    float v[32];
-    #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = fmaf(alpha, __uint_as_float(u[i]), bias);
-                    uint32_t w[16];
+                    float v[kBlockRows];
+                    uint32_t w[kBlockRows / 2];
+#pragma unroll
+                    for (int i = 0; i < kBlockRows; ++i) v[i] = fmaf(alpha, __uint_as_float(u[i]), bias);
                     if (P.pre) {
-                        if (P.in_bf)
-                            pack32<true>(v, w);
-                        else
-                            pack32<false>(v, w);
+                        pack_block(v, w, P.in_bf);
                         store_block(&maps.mp, P.pre + (row + c) * P.ld_pre + f, P.ld_pre, w, st,
-                                    P.tma_pre && (whole || nrows >= 32), lane, feat, (int)row + c, 0, nrows, nfeat, 0);
+                                    P.tma_pre && (whole || nrows >= kBlockRows), lane, feat, (int)row + c, 0, nrows, nfeat,
+                                    0);
                     }
                     if (P.act == ACT_RELU) {
-    #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = activate(v[i], ACT_RELU);
+#pragma unroll
+                        for (int i = 0; i < kBlockRows; ++i) v[i] = activate(v[i], ACT_RELU);
                     } else if (P.act == ACT_GELU) {
-    #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = activate(v[i], ACT_GELU);
+#pragma unroll
+                        for (int i = 0; i < kBlockRows; ++i) v[i] = activate(v[i], ACT_GELU);
                     } else if (P.act == ACT_SILU) {
-    #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = activate(v[i], ACT_SILU);
+#pragma unroll
+                        for (int i = 0; i < kBlockRows; ++i) v[i] = activate(v[i], ACT_SILU);
                     }
                     if (P.c) {
                         if (P.in_bf) {
-    #pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] += beta * __uint_as_float((uint32_t)cv[i] << 16);
+#pragma unroll
+                            for (int i = 0; i < kBlockRows; ++i) v[i] += beta * __uint_as_float((uint32_t)cv[i] << 16);
                         } else {
-    #pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] += beta * __half2float(__ushort_as_half(cv[i]));
+#pragma unroll
+                            for (int i = 0; i < kBlockRows; ++i) v[i] += beta * __half2float(__ushort_as_half(cv[i]));
                         }
-                        if (c + 64 < q.live) fetch_c(P, cv, q.g, row + c + 64, nrows - 64, f);
+                        if (c + kStride < q.live) fetch_c(P, cv, q.g, row + c + kStride, nrows - kStride, f);
                     }
                     const int over = feat + 31 - (q.n0 + c);      // symmetric: > 0 where the block reaches above the diagonal
-                    if (side && over >= 63) continue;             // nothing of it on this side
-                    if (P.out_bf)
-                        pack32<true>(v, w);
-                    else
-                        pack32<false>(v, w);
+                    if (side && over >= 31 + kBlockRows) continue;   // nothing of it on this side
+                    pack_block(v, w, P.out_bf);
                     const int below = side ? f - (q.n0 + c) : 0;   // first row this lane writes
                     store_block(&maps.mo, P.out + q.g * P.bs_out + (row + c) * P.ld_out + f, P.ld_out, w, st,
-                                P.tma_out && (whole || nrows >= 32) && !(side && over > 0), lane, feat, (int)row + c, zo,
-                                nrows, nfeat, below);
+                                P.tma_out && (whole || nrows >= kBlockRows) && !(side && over > 0), lane, feat,
+                                (int)row + c, zo, nrows, nfeat, below);
                     if (side && lane < nfeat)
                         store_mirror(P.out + q.g * P.bs_out + (int64_t)f * P.ld_out + q.n0 + c, w, below + 1, nrows);
                 }
@@ -1669,11 +1670,11 @@ static ccl_status_t complete(const Device* dev, Product* P, const Shape& sh, con
         const int64_t count = P->ragged == RAGGED_ROWS ? 1 : P->groups;
         P->tma_out = vectors(P->out, P->ld_out, P->bs_out);
         if (P->tma_out)
-            TRY(encode(dev, &P->mo, Matrix{P->out, P->n, P->m, P->ld_out, count, P->bs_out}, 32, 32,
+            TRY(encode(dev, &P->mo, Matrix{P->out, P->n, P->m, P->ld_out, count, P->bs_out}, 32, kBlockRows,
                        CU_TENSOR_MAP_SWIZZLE_NONE));
         P->tma_pre = P->pre && vectors(P->pre, P->ld_pre, 0);
         if (P->tma_pre)
-            TRY(encode(dev, &P->mp, Matrix{P->pre, P->n, P->m, P->ld_pre}, 32, 32, CU_TENSOR_MAP_SWIZZLE_NONE));
+            TRY(encode(dev, &P->mp, Matrix{P->pre, P->n, P->m, P->ld_pre}, 32, kBlockRows, CU_TENSOR_MAP_SWIZZLE_NONE));
     }
     return CCL_OK;
 }
