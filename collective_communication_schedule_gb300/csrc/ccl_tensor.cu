@@ -81,6 +81,42 @@ struct Product : Scalars {
     CUtensorMap ma, mb, mo, mp;    // operands; out and pre where TMA can store them
 };
 
+// Rows of a partial column sum of the activation's gradient (act_grad_kernel).
+constexpr int kGradRows = 64;
+
+struct GradPass {
+    const uint16_t *dy, *z;
+    uint16_t* dz;                  // may be null (sums only)
+    float* partial;                // may be null (no bias gradient)
+    uint16_t* db;
+    const int32_t* offsets;        // null: one expert with all rows
+    int64_t ld_dy, ld_z, ld_dz, bs_db;
+    int64_t ld_part;
+    int32_t rows, n, groups, act, bf, vec;
+};
+
+__device__ __forceinline__ int64_t chunk_base(const GradPass& G, int e, int lo) { return lo / kGradRows + e; }
+
+__device__ __forceinline__ void grad_range(const GradPass& G, int e, int& lo, int& len)
+{
+    lo = 0;
+    len = G.rows;
+    if (G.offsets) {
+        lo = min(max(G.offsets[e], 0), G.rows);
+        len = min(max(G.offsets[e + 1], lo), G.rows) - lo;
+    }
+}
+
+// The two products of a backward pass in one launch: they read the same dz and
+// do not depend on each other, so the second one's tiles fill the places that
+// the first one's last wave leaves, and warp 2 of every threadblock, idle
+// otherwise, adds up the bias gradient.
+struct Pair {
+    int32_t width, stages;         // the wider tile's rows; stages of that width
+    GradPass sums;                 // sums.db: null if there is no bias gradient
+    Product p[2];
+};
+
 // Products one after the other in one launch, each reading what the ones
 // before it wrote: the steps of the Newton-Schulz iteration.  `p` holds each
 // different product once; phase() tells which one comes when.
@@ -374,20 +410,68 @@ __device__ __noinline__ bool phases_done(const uint32_t* arrived, uint32_t phase
     return false;
 }
 
-// The products list[0 .. count) (CHAIN: those of a Chain, in its order, with
-// all threadblocks of the grid in step) on this threadblock's share of tiles.
-template <int CG, int FORM, bool CHAIN>
-__device__ __forceinline__ void products(const Product* list, const Chain* chain)
+// Sum a bias gradient's chunks, 32 columns of one expert at a time.
+__device__ __forceinline__ void add_chunks(const GradPass& G, int lane)
+{
+    const int columns = (G.n + 31) / 32;
+    for (int item = blockIdx.x; item < G.groups * columns; item += gridDim.x) {
+        const int e = item / columns, c = item % columns * 32 + lane;
+        int lo, len;
+        grad_range(G, e, lo, len);
+        if (c >= G.n) continue;
+        const int chunks = (len + kGradRows - 1) / kGradRows;
+        const float* p = G.partial + chunk_base(G, e, lo) * G.ld_part + c;
+        float s = 0.f;
+#pragma unroll 8
+        for (int i = 0; i < chunks; ++i) s += p[i * G.ld_part];
+        store1(G.db + e * G.bs_db + c, s, G.bf);
+    }
+}
+
+// MODE: one product; the two of a Pair; those of a Chain, in its order, with
+// all threadblocks of the grid in step
+enum { SINGLE = 0, PAIR = 1, CHAIN = 2 };
+
+template <int MODE>
+struct Sequence {
+    const Product* list;
+    __device__ int width() const { return list->bn; }
+    __device__ int stages() const { return list->stages; }
+    __device__ int split() const { return list->split; }
+    __device__ int phases() const { return 1; }
+    __device__ const Product& at(int) const { return *list; }
+};
+template <>
+struct Sequence<PAIR> {
+    const Pair* pair;
+    __device__ int width() const { return pair->width; }
+    __device__ int stages() const { return pair->stages; }
+    __device__ int split() const { return 1; }
+    __device__ int phases() const { return 2; }
+    __device__ const Product& at(int ph) const { return pair->p[ph]; }
+};
+template <>
+struct Sequence<CHAIN> {
+    const Chain* chain;
+    __device__ int width() const { return chain->width; }
+    __device__ int stages() const { return chain->stages; }
+    __device__ int split() const { return 1; }
+    __device__ int phases() const { return 3 * chain->steps; }
+    __device__ const Product& at(int ph) const { return chain->p[chain->phase(ph)]; }
+};
+
+// A threadblock's share of the tiles of a sequence of products.
+template <int CG, int FORM, int MODE>
+__device__ __forceinline__ void products(const Sequence<MODE> seq)
 {
     __shared__ __align__(8) Shared sh;
     extern __shared__ unsigned char raw[];
     unsigned char* dyn = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int size = CG == 2 ? 2 : CHAIN ? 1 : list->split;            // threadblocks of the cluster
+    const int size = CG == 2 ? 2 : seq.split();             // threadblocks of the cluster
     const int rank = size > 1 ? (int)cluster_rank() : 0;
     const int cluster = blockIdx.x / size, clusters = gridDim.x / size;
-    const int width = CHAIN ? chain->width : list->bn, stages = CHAIN ? chain->stages : list->stages;
-    const int phases = CHAIN ? 3 * chain->steps : 1;
+    const int width = seq.width(), stages = seq.stages(), phases = seq.phases();
     const uint32_t bytes_a = kTileM * kSliceK * 2;
     const uint32_t step = bytes_a + width / CG * kSliceK * 2;          // from one stage to the next
     unsigned char* staging = dyn + (size_t)stages * step;
@@ -411,12 +495,12 @@ __device__ __forceinline__ void products(const Product* list, const Chain* chain
     }
     if (threadIdx.x == 32) {
         sh.failed = 0;
-        tma_prefetch(&list->ma);
-        tma_prefetch(&list->mb);
+        tma_prefetch(&seq.at(0).ma);
+        tma_prefetch(&seq.at(0).mb);
     }
     let_next_in();
-    if (list->offsets) wait_for_previous();
-    if (!CHAIN) prepare_tiles<CG>(*list, &sh);
+    if (MODE != CHAIN && seq.at(0).offsets) wait_for_previous();
+    if (MODE != CHAIN) prepare_tiles<CG>(seq.at(0), &sh);
     if (size > 1)
         cluster_sync();
     else
@@ -433,6 +517,14 @@ __device__ __forceinline__ void products(const Product* list, const Chain* chain
         tmem = sh.tmem;
     }
 
+    // This threadblock's (cluster's) tiles of the next product: every
+    // `clusters`-th one.  In a pair they go on where the first product's
+    // stopped, in a chain every product starts anew.
+    int before = 0;
+    auto first_tile = [&]() { return MODE == PAIR ? (cluster + clusters - before % clusters) % clusters : cluster; };
+    const uint32_t* arrived = nullptr;
+    if constexpr (MODE == CHAIN) arrived = seq.chain->arrived;
+
     const uint32_t ring = smem_addr(dyn), full0 = smem_addr(sh.full), empty0 = smem_addr(sh.empty);
 
     // A wait that fails does not change the way through these loops: it only
@@ -443,12 +535,11 @@ __device__ __forceinline__ void products(const Product* list, const Chain* chain
         uint32_t flips = 0, used = 0;      // per stage: parity of its uses for cleared slices, whether any
         bool good = true;
         for (int ph = 0; ph < phases; ++ph) {
-            const Product& maps = CHAIN ? list[chain->phase(ph)] : *list;
+            const Product& maps = seq.at(ph);
             const Scalars P = maps;
-            if (CHAIN && ph + 1 < phases && lane == 0) {
-                const Product& next = list[chain->phase(ph + 1)];
-                tma_prefetch(&next.ma);
-                tma_prefetch(&next.mb);
+            if (MODE != SINGLE && ph + 1 < phases && lane == 0) {
+                tma_prefetch(&seq.at(ph + 1).ma);
+                tma_prefetch(&seq.at(ph + 1).mb);
             }
             const bool a_mn = FORM == ANY_FORM ? P.a_mn : FORM != BOTH_K, b_mn = FORM == ANY_FORM ? P.b_mn : FORM == BOTH_MN;
             const uint32_t bytes_b = P.bn / CG * kSliceK * 2;
@@ -458,15 +549,17 @@ __device__ __forceinline__ void products(const Product* list, const Chain* chain
             const int total = P.ragged == RAGGED_ROWS ? sh.total : P.total, bn = P.bn;
             // the first tile is found before the wait for what it reads
             TileAt q;
-            if (cluster < total) q = tile_at<CG>(P, &sh, cluster);
+            const int begin = first_tile();
+            if (begin < total) q = tile_at<CG>(P, &sh, begin);
             if (ph == 0) wait_for_previous();
-            if (CHAIN && ph && good) {
-                if (lane == 0) good = phases_done(chain->arrived, ph, failed);
+            if (MODE == CHAIN && ph && good) {
+                if (lane == 0) good = phases_done(arrived, ph, failed);
                 good = __shfl_sync(~0u, good, 0);
                 asm volatile("fence.proxy.async;" ::: "memory");
             }
-            for (int t = cluster; t < total; t += clusters) {
-                if (t != cluster) q = tile_at<CG>(P, &sh, t);
+            before += total;
+            for (int t = begin; t < total; t += clusters) {
+                if (t != begin) q = tile_at<CG>(P, &sh, t);
                 const int m0 = q.m0 + (CG == 2 ? rank * kTileM : 0);
                 const int n0 = q.n0 + (CG == 2 ? rank * (used_rows<CG>(P, q) / 2) : 0);
                 int first, last;
@@ -536,13 +629,14 @@ __device__ __forceinline__ void products(const Product* list, const Chain* chain
             uint32_t phase = 0, flips = 0;
             bool good = true;
             for (int ph = 0; ph < phases; ++ph) {
-                const Scalars P = CHAIN ? list[chain->phase(ph)] : *list;
+                const Scalars P = seq.at(ph);
                 const bool a_mn = FORM == ANY_FORM ? P.a_mn : FORM != BOTH_K, b_mn = FORM == ANY_FORM ? P.b_mn : FORM == BOTH_MN;
                 const uint32_t bytes_b = P.bn / CG * kSliceK * 2;
                 const uint32_t part_b = bytes_b / 2;      // one of a slice's two halves of B (reduction 0..63, 64..127)
                 const bool reduce_rows = b_mn && P.ragged == RAGGED_REDUCE;
-                const int total = P.ragged == RAGGED_ROWS ? sh.total : P.total;
-                for (int t = cluster; t < total; t += clusters) {
+                const int total = P.ragged == RAGGED_ROWS ? sh.total : P.total, begin = first_tile();
+                before += total;
+                for (int t = begin; t < total; t += clusters) {
                     const TileAt q = tile_at<CG>(P, &sh, t);
                     int first, last;
                     slices(q, CG == 2 ? 1 : size, rank, first, last);
@@ -585,35 +679,50 @@ __device__ __forceinline__ void products(const Product* list, const Chain* chain
             }
         }
         __syncwarp();
-    } else if (warp == 3 && !CHAIN && FORM == BOTH_MN && list->ragged == RAGGED_REDUCE) {
+    } else if (warp == 2 && MODE == PAIR) {
+        if constexpr (MODE == PAIR) {
+            if (seq.pair->sums.db) {
+                wait_for_previous();
+                add_chunks(seq.pair->sums, lane);
+            }
+            __syncwarp();
+        }
+    } else if (warp == 3 && MODE != CHAIN && (MODE == PAIR || FORM == BOTH_MN) &&
+               seq.at(phases - 1).ragged == RAGGED_REDUCE) {
         // 0 x Inf or NaN would not be 0: both operands are cleared
-        const Scalars P = *list;
         int it = 0;
         uint32_t flips = 0;
-        for (int t = cluster; t < P.total; t += clusters) {
-            const TileAt q = tile_at<CG>(P, &sh, t);
-            int first, last;
-            slices(q, CG == 2 ? 1 : size, rank, first, last);
-            if (first >= last) continue;
-            it += last - first;
-            if (!partial(q, last - 1)) continue;
-            const int s = (it - 1) % stages;
-            if (!__all_sync(~0u, bar_wait(smem_addr(&sh.land[s]), flips >> s & 1, failed))) break;
-            flips ^= 1u << s;
-            unsigned char* at = dyn + (size_t)s * step;
-            // only as far as the matrix instructions reach: 16 rows at a time
-            const int left = q.klen - (last - 1) * kSliceK, dead = -left & 15;
-            for (int i = lane; i < (int)(P.bn / CG + kTileM) / 64 * dead * 8; i += 32) {
-                const int blk = i / (dead * 8), o = i % (dead * 8);
-                *reinterpret_cast<uint4*>(at + blk * (kSliceK * 128) + left * 128 + o * 16) = make_uint4(0, 0, 0, 0);
-            }
-            fence_async();
-            __syncwarp();
-            if (lane == 0) {
-                if (CG == 2)
-                    bar_arrive_cluster(cluster_addr(smem_addr(&sh.fixed[s]), 0));
-                else
-                    bar_arrive(smem_addr(&sh.fixed[s]));
+        bool good = true;
+        for (int ph = 0; ph < phases; ++ph) {
+            const Scalars P = seq.at(ph);
+            const int total = P.ragged == RAGGED_ROWS ? sh.total : P.total, begin = first_tile();
+            before += total;
+            for (int t = begin; good && t < total; t += clusters) {
+                const TileAt q = tile_at<CG>(P, &sh, t);
+                int first, last;
+                slices(q, CG == 2 ? 1 : size, rank, first, last);
+                if (first >= last) continue;
+                it += last - first;
+                if (P.ragged != RAGGED_REDUCE || !partial(q, last - 1)) continue;
+                const int s = (it - 1) % stages;
+                good = __all_sync(~0u, bar_wait(smem_addr(&sh.land[s]), flips >> s & 1, failed));
+                if (!good) break;
+                flips ^= 1u << s;
+                unsigned char* at = dyn + (size_t)s * step;
+                // only as far as the matrix instructions reach: 16 rows at a time
+                const int left = q.klen - (last - 1) * kSliceK, dead = -left & 15;
+                for (int i = lane; i < (P.bn / CG + kTileM) / 64 * dead * 8; i += 32) {
+                    const int blk = i / (dead * 8), o = i % (dead * 8);
+                    *reinterpret_cast<uint4*>(at + blk * (kSliceK * 128) + left * 128 + o * 16) = make_uint4(0, 0, 0, 0);
+                }
+                fence_async();
+                __syncwarp();
+                if (lane == 0) {
+                    if (CG == 2)
+                        bar_arrive_cluster(cluster_addr(smem_addr(&sh.fixed[s]), 0));
+                    else
+                        bar_arrive(smem_addr(&sh.fixed[s]));
+                }
             }
         }
         __syncwarp();
@@ -626,19 +735,21 @@ __device__ __forceinline__ void products(const Product* list, const Chain* chain
             release[i] = CG == 2 ? cluster_addr(smem_addr(&sh.acc_empty[i]), 0) : smem_addr(&sh.acc_empty[i]);
         int done = 0, round = 0;
         for (int ph = 0; ph < phases; ++ph) {
-            const Product& maps = CHAIN ? list[chain->phase(ph)] : *list;
+            const Product& maps = seq.at(ph);
             const Scalars P = maps;
             const int side = P.symmetric ? 1 : 0;
             const int total = P.ragged == RAGGED_ROWS ? sh.total : P.total;
             TileAt q;
-            if (cluster < total) q = tile_at<CG>(P, &sh, cluster);
+            const int begin = first_tile();
+            before += total;
+            if (begin < total) q = tile_at<CG>(P, &sh, begin);
             if (ph == 0) wait_for_previous();
-            if (CHAIN && ph) {
-                if (threadIdx.x == 128) phases_done(chain->arrived, ph, failed);
+            if (MODE == CHAIN && ph) {
+                if (threadIdx.x == 128) phases_done(arrived, ph, failed);
                 named_sync(3, 32 * kEpilogueWarps);
             }
-            for (int t = cluster; t < total; t += clusters) {
-                if (t != cluster) q = tile_at<CG>(P, &sh, t);
+            for (int t = begin; t < total; t += clusters) {
+                if (t != begin) q = tile_at<CG>(P, &sh, t);
                 int first, last;
                 slices(q, CG == 2 ? 1 : size, rank, first, last);
                 const bool some = first < last;
@@ -798,14 +909,14 @@ __device__ __forceinline__ void products(const Product* list, const Chain* chain
                     ++round;
                 }
             }
-            if (CHAIN) {
+            if (MODE == CHAIN) {
                 // everything this threadblock wrote, by either route, is visible before it arrives
                 if (lane == 0) tma_stores_done();
                 __syncwarp();
                 asm volatile("fence.proxy.async;" ::: "memory");
                 named_sync(3, 32 * kEpilogueWarps);
                 if (threadIdx.x == 128)
-                    asm volatile("fence.acq_rel.gpu;\n\tred.release.gpu.global.add.u32 [%0], 1;" ::"l"(chain->arrived)
+                    asm volatile("fence.acq_rel.gpu;\n\tred.release.gpu.global.add.u32 [%0], 1;" ::"l"(arrived)
                                  : "memory");
             }
         }
@@ -836,11 +947,16 @@ __device__ __forceinline__ void products(const Product* list, const Chain* chain
 template <int CG, int FORM>
 __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ Product P)
 {
-    products<CG, FORM, false>(&P, nullptr);
+    products<CG, FORM, SINGLE>({&P});
+}
+template <int CG>
+__global__ void __launch_bounds__(kThreads, 1) pair_kernel(const __grid_constant__ Pair P)
+{
+    products<CG, ANY_FORM, PAIR>({&P});
 }
 __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constant__ Chain C)
 {
-    products<1, ANY_FORM, true>(C.p, &C);
+    products<1, ANY_FORM, CHAIN>({&C});
 }
 
 // ======================================================================
@@ -855,31 +971,6 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
 // bits and a fixed order, to partial[chunk][column]; bias_grad_kernel adds
 // an expert's chunks up in order.  Chunks of expert e start at
 // offsets[e] / kGradRows + e, which leaves every expert room for its rows.
-constexpr int kGradRows = 64;
-
-struct GradPass {
-    const uint16_t *dy, *z;
-    uint16_t* dz;                  // may be null (sums only)
-    float* partial;                // may be null (no bias gradient)
-    uint16_t* db;
-    const int32_t* offsets;        // null: one expert with all rows
-    int64_t ld_dy, ld_z, ld_dz, bs_db;
-    int64_t ld_part;
-    int32_t rows, n, groups, act, bf, vec;
-};
-
-__device__ __forceinline__ int64_t chunk_base(const GradPass& G, int e, int lo) { return lo / kGradRows + e; }
-
-__device__ __forceinline__ void grad_range(const GradPass& G, int e, int& lo, int& len)
-{
-    lo = 0;
-    len = G.rows;
-    if (G.offsets) {
-        lo = min(max(G.offsets[e], 0), G.rows);
-        len = min(max(G.offsets[e + 1], lo), G.rows) - lo;
-    }
-}
-
 __global__ void __launch_bounds__(256) act_grad_kernel(const GradPass G)
 {
     __shared__ float sums[8][256 + 8];
@@ -1467,6 +1558,9 @@ static ccl_status_t device(const Device** out)
             for (auto kernel : forms)
                 TRY_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBudget),
                          "shared memory of the product kernel");
+        for (auto kernel : {pair_kernel<1>, pair_kernel<2>})
+            TRY_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBudget),
+                     "shared memory of the pair kernel");
         TRY_CUDA(cudaFuncSetAttribute(chain_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBudget),
                  "shared memory of the chain kernel");
         TRY_CUDA(cudaFuncSetAttribute(small_ortho_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBudget),
@@ -1613,8 +1707,9 @@ struct Shape {
 // for 256, 128 and 64; and no SM gets more than about 68 bytes a clock from
 // L2.  An exchange of shares costs about 5000 clocks (1 x 4096 x 4096: 15.1,
 // 12.9, 11.7 and 19 us cut in 1, 2, 4 and 8), and clusters of 4 and 8 leave
-// SMs unused.  chain: only what the phases of a chain can take.
-static Shape choose(const Product& P, int sms, bool chain)
+// SMs unused.  The last three arguments narrow the
+// choice to what a sequence of products can take.
+static Shape choose(const Product& P, int sms, int least_cg = 1, int most_cg = 2, int most_split = 8)
 {
     const double rows = P.ragged == RAGGED_ROWS ? std::max(1.0, (double)P.n / P.groups) : (double)P.n;
     const double groups = P.ragged == RAGGED_ROWS ? std::min(P.n, P.groups) : P.groups;
@@ -1622,10 +1717,11 @@ static Shape choose(const Product& P, int sms, bool chain)
     const double slices = std::ceil(reduce / kSliceK);
     const double least = 2.0 * P.k * ((double)P.m * (P.ragged == RAGGED_REDUCE ? 1 : groups) + P.n) / 3400;
     Shape best = {0, 0, 0, 0};
-    for (int cg = 1; cg <= (chain ? 1 : 2); ++cg) {
+    for (int cg = least_cg; cg <= most_cg; ++cg) {
         for (int bn : {256, 192, 128, 64, 32}) {
-            if (bn / cg % (P.b_mn ? 64 : 16) || (bn > 64 && bn / 2 >= rows)) continue;
-            for (int split = 1; split <= (chain || cg == 2 || bn > 128 ? 1 : 8); split *= 2) {
+            const int unit = P.b_mn ? 64 * cg : 32;       // rows are loaded 64 at a time where they are consecutive
+            if (bn % unit || (bn > unit && bn / 2 >= rows)) continue;
+            for (int split = 1; split <= (cg == 2 || bn > 128 ? 1 : most_split); split *= 2) {
                 if (split > 1 && split * 2 > slices) continue;
                 const double tiles_m = std::ceil((double)P.m / (cg * kTileM)), tiles_n = std::ceil(rows / bn);
                 double tiles = groups * tiles_m * tiles_n;
@@ -1684,7 +1780,7 @@ static ccl_status_t run(Product P, const Matrix& a, const Matrix& b, cudaStream_
 {
     const Device* dev = nullptr;
     TRY(device(&dev));
-    const Shape sh = choose(P, dev->sms, false);
+    const Shape sh = choose(P, dev->sms);
     TRY(complete(dev, &P, sh, a, b));
     const int size = sh.cg == 2 ? 2 : sh.split;
     const int bytes = (kTileM + P.bn / sh.cg) * kSliceK * 2;
@@ -1698,6 +1794,25 @@ static ccl_status_t run(Product P, const Matrix& a, const Matrix& b, cudaStream_
     const int clusters = std::min(P.total, dev->sms / size);
     return launch(kKernels[sh.cg - 1][P.b_mn ? BOTH_MN : P.a_mn ? A_MN : BOTH_K], dim3((unsigned)(clusters * size)),
                   kThreads, smem, stream, P, size);
+}
+
+// Launch a pair of products that do not depend on each other.
+static ccl_status_t run_pair(const Device* dev, Pair* R, const Shape sh[2], const Matrix a[2], const Matrix b[2],
+                             cudaStream_t stream)
+{
+    const int cg = sh[0].cg;
+    int64_t most = 0;
+    for (int i = 0; i < 2; ++i) {
+        TRY(complete(dev, &R->p[i], sh[i], a[i], b[i]));
+        R->width = std::max(R->width, sh[i].bn);
+        most += R->p[i].total;
+    }
+    if (most > INT32_MAX) return fail(CCL_ERR_UNSUPPORTED, "too many tiles");
+    const int bytes = (kTileM + R->width / cg) * kSliceK * 2, fixed = 1024 + kStagingBytes;
+    R->stages = std::min(kMaxStages, (kSmemBudget - fixed) / bytes);
+    const int clusters = (int)std::min<int64_t>(most, dev->sms / cg);
+    return launch(cg == 2 ? pair_kernel<2> : pair_kernel<1>, dim3((unsigned)(clusters * cg)), kThreads,
+                  fixed + (size_t)R->stages * bytes, stream, *R, cg);
 }
 
 // --------------------------------------------------------- linear layers
@@ -1870,34 +1985,55 @@ static ccl_status_t linear_grad(const ccl_linear_grad_t* a, char* base, int64_t*
         G.bf = bf;
         G.vec = (aligned16(a->dy) && lddy % 8 == 0 ? 1 : 0) | (aligned16(a->z) && ldz % 8 == 0 ? 2 : 0);
         TRY(launch(act_grad_kernel, dim3((unsigned)chunks, (unsigned)((a->n + 255) / 256)), 256, 0, stream, G));
-        if (a->db)
-            TRY(launch(bias_grad_kernel, dim3((unsigned)((a->n + 31) / 32), (unsigned)count), 256, 0, stream, G));
     }
     Product P = {};
     P.groups = (int32_t)count;
     P.offsets = a->experts > 0 ? a->offsets : nullptr;
     P.alpha = 1.f;
     P.in_bf = bf;
+    Product px = P, pw = P;
     if (a->dx) {   // dx[t, k] = sum_n w[n, k] dz[t, n]
         TRY(loadable(&w, &ws, stream));
-        P.m = (int32_t)a->k;
-        P.n = (int32_t)a->rows;
-        P.k = (int32_t)a->n;
-        P.ragged = a->experts > 0 ? RAGGED_ROWS : DENSE;
-        P.a_mn = 1;
-        set_out(&P, a->dx, lddx, 0, bf);
-        TRY(run(P, w, dz, stream));
+        px.m = (int32_t)a->k;
+        px.n = (int32_t)a->rows;
+        px.k = (int32_t)a->n;
+        px.ragged = a->experts > 0 ? RAGGED_ROWS : DENSE;
+        px.a_mn = 1;
+        set_out(&px, a->dx, lddx, 0, bf);
     }
     if (a->dw) {   // dw[n, k] = sum_t x[t, k] dz[t, n]
         TRY(loadable(&x, &ws, stream));
-        P.m = (int32_t)a->k;
-        P.n = (int32_t)a->n;
-        P.k = (int32_t)a->rows;
-        P.ragged = a->experts > 0 ? RAGGED_REDUCE : DENSE;
-        P.a_mn = P.b_mn = 1;
-        set_out(&P, a->dw, lddw, sdw, bf);
-        TRY(run(P, x, dz, stream));
+        pw.m = (int32_t)a->k;
+        pw.n = (int32_t)a->n;
+        pw.k = (int32_t)a->rows;
+        pw.ragged = a->experts > 0 ? RAGGED_REDUCE : DENSE;
+        pw.a_mn = pw.b_mn = 1;
+        set_out(&pw, a->dw, lddw, sdw, bf);
     }
+    if (a->dx && a->dw) {
+        // one launch for both unless splitting or shapes of their own are worth more than the launch (9500 clocks)
+        const Device* dev = nullptr;
+        TRY(device(&dev));
+        Shape both[2][2];
+        double cost[2];
+        for (int cg = 1; cg <= 2; ++cg) {
+            both[cg - 1][0] = choose(px, dev->sms, cg, cg, 1);
+            both[cg - 1][1] = choose(pw, dev->sms, cg, cg, 1);
+            cost[cg - 1] = both[cg - 1][0].cost + both[cg - 1][1].cost;
+        }
+        const int cg = cost[1] <= cost[0] ? 2 : 1;
+        if (cost[cg - 1] < choose(px, dev->sms).cost + choose(pw, dev->sms).cost + 9500) {
+            Pair R = {};
+            R.p[0] = px;
+            R.p[1] = pw;
+            if (a->db) R.sums = G;
+            const Matrix left[2] = {w, x}, right[2] = {dz, dz};
+            return run_pair(dev, &R, both[cg - 1], left, right, stream);
+        }
+    }
+    if (a->db) TRY(launch(bias_grad_kernel, dim3((unsigned)((a->n + 31) / 32), (unsigned)count), 256, 0, stream, G));
+    if (a->dx) TRY(run(px, w, dz, stream));
+    if (a->dw) TRY(run(pw, x, dz, stream));
     return CCL_OK;
 }
 
@@ -2054,8 +2190,8 @@ static ccl_status_t orthogonalize(const ccl_ortho_t* a, char* base, int64_t* nee
     double apart = 0, chained = 0;
     for (int kind = 0; kind < 3; ++kind) {
         const Step s = product(kind, 0, false, false);
-        apart += choose(s.p, dev->sms, false).cost + 9500;
-        chained += choose(s.p, dev->sms, true).cost + 4500;
+        apart += choose(s.p, dev->sms).cost + 9500;
+        chained += choose(s.p, dev->sms, 1, 1, 1).cost + 4500;
     }
     if (chained < apart) {
         Chain C = {};
@@ -2068,7 +2204,7 @@ static ccl_status_t orthogonalize(const ccl_ortho_t* a, char* base, int64_t* nee
             const int from = last ? (a->steps - 1) & 1 : i == 2 || i == 6;
             const Step s = product(kind, from, kind == 0 ? i == 0 : kind == 2 && (i == 4 || (last && a->steps == 1)), last);
             C.p[i] = s.p;
-            const Shape sh = choose(s.p, dev->sms, true);
+            const Shape sh = choose(s.p, dev->sms, 1, 1, 1);
             TRY(complete(dev, &C.p[i], sh, *s.a, *s.b));
             C.width = std::max(C.width, sh.bn);
             most = std::max(most, C.p[i].total);

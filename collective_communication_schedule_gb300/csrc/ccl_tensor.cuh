@@ -359,7 +359,14 @@ __device__ __forceinline__ void store8(uint16_t* p, bool bf, bool vec, int lo, i
 // u = sqrt(2/pi) (z + 0.044715 z^3); silu is z sigmoid(z).  In 32 bits.
 enum { ACT_NONE = 0, ACT_RELU = 1, ACT_GELU = 2, ACT_SILU = 3 };
 
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+// 1 / (1 + 2^(-x log2 e)): two approximate instructions, each within 2^-22
+__device__ __forceinline__ float sigmoid(float x)
+{
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return r;
+}
 
 __device__ __forceinline__ float activate(float z, int act)
 {
