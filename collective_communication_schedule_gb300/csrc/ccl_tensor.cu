@@ -82,7 +82,7 @@ struct Product : Scalars {
 };
 
 // Rows of a partial column sum of the activation's gradient (act_grad_kernel).
-constexpr int kGradRows = 64;
+constexpr int kGradRows = 32;
 
 struct GradPass {
     const uint16_t *dy, *z;
@@ -966,11 +966,12 @@ __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constan
 // dz = dy * act'(z), and the column sums of dz that make the bias gradient.
 // A threadblock takes 256 columns of up to kGradRows rows of one expert
 // (dense: one expert with all rows); 32 threads cover the columns, 8 each,
-// and 8 groups of threads take the rows in turn, two at a time to keep more
-// loads in flight (bound by DRAM: 6 bytes an element).  The sums go, in 32
-// bits and a fixed order, to partial[chunk][column]; bias_grad_kernel adds
-// an expert's chunks up in order.  Chunks of expert e start at
-// offsets[e] / kGradRows + e, which leaves every expert room for its rows.
+// and 8 groups of threads take 4 rows each, all loads ahead of the
+// arithmetic (bound by DRAM: 6 bytes an element).  Rows that 16-byte loads
+// cannot address are read 32 neighbouring elements at a time instead.  The
+// sums go, in 32 bits and a fixed order, to partial[chunk][column]; an
+// expert's chunks are added up in order afterwards.  Chunks of expert e start
+// at offsets[e] / kGradRows + e, which leaves every expert room for its rows.
 __global__ void __launch_bounds__(256) act_grad_kernel(const GradPass G)
 {
     __shared__ float sums[8][256 + 8];
@@ -994,40 +995,68 @@ __global__ void __launch_bounds__(256) act_grad_kernel(const GradPass G)
     grad_range(G, e, lo, len);
     const int64_t first = (chunk - chunk_base(G, e, lo)) * kGradRows;
     if (first < 0 || first >= len) return;
+    constexpr int kRows = kGradRows / 8;
     const int nrows = (int)min((int64_t)kGradRows, len - first);
-    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-    const int col = blockIdx.y * 256 + tx * 8;
-    const int hi = min(8, G.n - col);
-    float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (hi > 0) {
-        for (int r = ty; r < nrows; r += 16) {
-            const int64_t row = lo + first + r;
-            const int n = r + 8 < nrows ? 2 : 1;
-            float v[2][8], z[2][8];
+    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, col = blockIdx.y * 256;
+    const int64_t row0 = lo + first + ty;
+    if (G.vec) {
+        const int c = col + tx * 8;
+        float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (c < G.n) {              // n is a multiple of 8
+            uint4 y[kRows], z[kRows];
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-                if (j < n) {
-                    load8(G.dy + (row + 8 * j) * G.ld_dy + col, G.bf, G.vec & 1, 0, hi, v[j]);
-                    if (G.act) load8(G.z + (row + 8 * j) * G.ld_z + col, G.bf, G.vec & 2, 0, hi, z[j]);
+            for (int j = 0; j < kRows; ++j)
+                if (ty + 8 * j < nrows) {
+                    y[j] = *reinterpret_cast<const uint4*>(G.dy + (row0 + 8 * j) * G.ld_dy + c);
+                    if (G.act) z[j] = *reinterpret_cast<const uint4*>(G.z + (row0 + 8 * j) * G.ld_z + c);
                 }
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-                if (j < n) {
+            for (int j = 0; j < kRows; ++j)
+                if (ty + 8 * j < nrows) {
+                    float v[8];
+                    unpack8(y[j], G.bf, v);
                     if (G.act) {
+                        float w[8];
+                        unpack8(z[j], G.bf, w);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) v[j][i] *= activate_grad(z[j][i], G.act);
+                        for (int i = 0; i < 8; ++i) v[i] *= activate_grad(w[i], G.act);
                     }
-                    if (G.dz) store8(G.dz + (row + 8 * j) * G.ld_dz + col, G.bf, true, 0, hi, v[j]);
+                    if (G.dz) store8(G.dz + (row0 + 8 * j) * G.ld_dz + c, G.bf, true, 0, 8, v);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) sum[i] += v[j][i];
+                    for (int i = 0; i < 8; ++i) sum[i] += v[i];
                 }
+        }
+        if (G.partial) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sums[ty][tx * 8 + i] = sum[i];
+        }
+    } else {
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) {
+            const int c = col + i * 32 + tx;
+            float sum = 0.f;
+            if (c < G.n) {
+                float y[kRows], z[kRows];
+#pragma unroll
+                for (int j = 0; j < kRows; ++j)
+                    if (ty + 8 * j < nrows) {
+                        y[j] = load1(G.dy + (row0 + 8 * j) * G.ld_dy + c, G.bf);
+                        if (G.act) z[j] = load1(G.z + (row0 + 8 * j) * G.ld_z + c, G.bf);
+                    }
+#pragma unroll
+                for (int j = 0; j < kRows; ++j)
+                    if (ty + 8 * j < nrows) {
+                        if (G.act) y[j] *= activate_grad(z[j], G.act);
+                        if (G.dz) store1(G.dz + (row0 + 8 * j) * G.ld_dz + c, y[j], G.bf);
+                        sum += y[j];
+                    }
+            }
+            if (G.partial) sums[ty][i * 32 + tx] = sum;
         }
     }
     if (!G.partial) return;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sums[ty][tx * 8 + i] = sum[i];
     __syncthreads();
-    const int c = blockIdx.y * 256 + threadIdx.x;
+    const int c = col + threadIdx.x;
     if (c < G.n) {
         float s = 0.f;
 #pragma unroll
@@ -1983,7 +2012,7 @@ static ccl_status_t linear_grad(const ccl_linear_grad_t* a, char* base, int64_t*
         G.groups = (int32_t)count;
         G.act = a->act;
         G.bf = bf;
-        G.vec = (aligned16(a->dy) && lddy % 8 == 0 ? 1 : 0) | (aligned16(a->z) && ldz % 8 == 0 ? 2 : 0);
+        G.vec = a->n % 8 == 0 && vectors(a->dy, lddy, 0) && (a->act == CCL_ACT_NONE || vectors(a->z, ldz, 0));
         TRY(launch(act_grad_kernel, dim3((unsigned)chunks, (unsigned)((a->n + 255) / 256)), 256, 0, stream, G));
     }
     Product P = {};
