@@ -333,12 +333,11 @@ __device__ __forceinline__ void fetch_c(const Scalars& P, uint16_t c[kBlockRows]
 // A block of 16 rows x 32 features (one feature per lane, two rows per word)
 // to global memory: through shared memory and a TMA store where the whole
 // block may be written (the parts of it outside the matrix are cut off by
-// TMA), else 64 neighbouring bytes of a row at a time.  below: the first row
-// this lane writes (symmetric outputs: feature <= row).  buf: this warp's
-// 1 KB of shared memory.
+// TMA), else 64 neighbouring bytes of a row at a time.  buf: this warp's 1 KB
+// of shared memory.
 __device__ __forceinline__ void store_block(const CUtensorMap* map, uint16_t* p, int64_t ld, const uint32_t w[kBlockRows / 2],
                                             unsigned char* buf, bool tma, int lane, int x, int y, int z, int nrows,
-                                            int nfeat, int below)
+                                            int nfeat)
 {
     if (tma && nfeat > 0) {
         if (lane == 0) tma_stores_read<0>();
@@ -355,23 +354,7 @@ __device__ __forceinline__ void store_block(const CUtensorMap* map, uint16_t* p,
     } else if (lane < nfeat) {
 #pragma unroll
         for (int i = 0; i < kBlockRows; ++i, p += ld)
-            if (i < nrows && i >= below) *p = (uint16_t)(w[i / 2] >> (i & 1) * 16);
-    }
-}
-
-// Its mirror image in a symmetric output: a lane's 16 values are neighbours
-// in row `feature`, from the first one above the diagonal on (rows start at
-// multiples of 16 bytes).
-__device__ __forceinline__ void store_mirror(uint16_t* p, const uint32_t w[kBlockRows / 2], int from, int nrows)
-{
-    if (from <= 0 && nrows >= kBlockRows) {
-#pragma unroll
-        for (int i = 0; i < kBlockRows / 8; ++i)
-            reinterpret_cast<uint4*>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < kBlockRows; ++i)
-            if (i >= from && i < nrows) p[i] = (uint16_t)(w[i / 2] >> (i & 1) * 16);
+            if (i < nrows) *p = (uint16_t)(w[i / 2] >> (i & 1) * 16);
     }
 }
 
@@ -803,8 +786,7 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
                     if (P.pre) {
                         pack_block(v, w, P.in_bf);
                         store_block(&maps.mp, P.pre + (row + c) * P.ld_pre + f, P.ld_pre, w, st,
-                                    P.tma_pre && (whole || nrows >= kBlockRows), lane, feat, (int)row + c, 0, nrows, nfeat,
-                                    0);
+                                    P.tma_pre && (whole || nrows >= kBlockRows), lane, feat, (int)row + c, 0, nrows, nfeat);
                     }
                     if (P.act == ACT_RELU) {
 #pragma unroll
@@ -826,15 +808,20 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
                         }
                         if (c + kStride < q.live) fetch_c(P, cv, q.g, row + c + kStride, nrows - kStride, f);
                     }
-                    const int over = feat + 31 - (q.n0 + c);      // symmetric: > 0 where the block reaches above the diagonal
-                    if (side && over >= 31 + kBlockRows) continue;   // nothing of it on this side
+                    // Symmetric outputs: blocks above the diagonal are left out, blocks that touch it are written as
+                    // they are (together they hold both sides of it: tiles start at multiples of 32), blocks below
+                    // it are written with their mirror images.
+                    const int over = feat + 31 - (q.n0 + c);      // > 0 where the block reaches above the diagonal
+                    if (side && over >= 31 + kBlockRows) continue;
                     pack_block(v, w, P.out_bf);
-                    const int below = side ? f - (q.n0 + c) : 0;   // first row this lane writes
                     store_block(&maps.mo, P.out + q.g * P.bs_out + (row + c) * P.ld_out + f, P.ld_out, w, st,
-                                P.tma_out && (whole || nrows >= kBlockRows) && !(side && over > 0), lane, feat,
-                                (int)row + c, zo, nrows, nfeat, below);
-                    if (side && lane < nfeat)
-                        store_mirror(P.out + q.g * P.bs_out + (int64_t)f * P.ld_out + q.n0 + c, w, below + 1, nrows);
+                                P.tma_out && (whole || nrows >= kBlockRows), lane, feat, (int)row + c, zo, nrows, nfeat);
+                    if (side && over <= 0 && lane < nfeat) {
+                        // a lane's 16 values are neighbours in row f; rows are padded to multiples of 8 (with zeros)
+                        uint4* m = reinterpret_cast<uint4*>(P.out + q.g * P.bs_out + (int64_t)f * P.ld_out + q.n0 + c);
+                        m[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                        if (nrows > 8) m[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                    }
                 }
                 if (some) {
                     fence_before();
@@ -1218,7 +1205,7 @@ __global__ void __launch_bounds__(256) scale_kernel(const NormPass N)
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = v[e] * f1 * f2;
-        store8((uint16_t*)N.x + blockIdx.y * N.bs_x + r * N.ld_x + c, false, true, 0, 8, v);   // rows are padded to 8
+        store8((uint16_t*)N.x + blockIdx.y * N.bs_x + r * N.ld_x + c, false, true, 0, 8, v);   // rows are padded
     }
 }
 
@@ -1736,37 +1723,45 @@ struct Shape {
 // for 256, 128 and 64; and no SM gets more than about 68 bytes a clock from
 // L2.  An exchange of shares costs about 5000 clocks (1 x 4096 x 4096: 15.1,
 // 12.9, 11.7 and 19 us cut in 1, 2, 4 and 8), and clusters of 4 and 8 leave
-// SMs unused.  The last three arguments narrow the
-// choice to what a sequence of products can take.
-static Shape choose(const Product& P, int sms, int least_cg = 1, int most_cg = 2, int most_split = 8)
+// SMs unused.
+struct Choices {
+    Shape best, single, pairs;     // of all; of single threadblocks without a split; of pairs
+};
+
+static Choices choose(const Product& P, int sms)
 {
-    const double rows = P.ragged == RAGGED_ROWS ? std::max(1.0, (double)P.n / P.groups) : (double)P.n;
-    const double groups = P.ragged == RAGGED_ROWS ? std::min(P.n, P.groups) : P.groups;
-    const double reduce = P.ragged == RAGGED_REDUCE ? std::max(1.0, (double)P.k / P.groups) : P.k;
-    const double slices = std::ceil(reduce / kSliceK);
-    const double least = 2.0 * P.k * ((double)P.m * (P.ragged == RAGGED_REDUCE ? 1 : groups) + P.n) / 3400;
-    Shape best = {0, 0, 0, 0};
-    for (int cg = least_cg; cg <= most_cg; ++cg) {
+    const bool ragged_rows = P.ragged == RAGGED_ROWS, ragged_reduce = P.ragged == RAGGED_REDUCE;
+    const int64_t rows = ragged_rows ? std::max(1, P.n / P.groups) : P.n;
+    const int64_t groups = ragged_rows ? std::min(P.n, P.groups) : P.groups;
+    const int64_t reduce = ragged_reduce ? std::max(1, P.k / P.groups) : P.k;
+    const int64_t slices = (reduce + kSliceK - 1) / kSliceK;
+    const double least = 2.0 * P.k * ((double)P.m * (ragged_reduce ? 1 : groups) + P.n) / 3400;
+    Choices c = {};
+    for (int cg = 1; cg <= 2; ++cg) {
+        const int64_t tiles_m = (P.m + (int64_t)cg * kTileM - 1) / (cg * kTileM);
         for (int bn : {256, 192, 128, 64, 32}) {
             const int unit = P.b_mn ? 64 * cg : 32;       // rows are loaded 64 at a time where they are consecutive
             if (bn % unit || (bn > unit && bn / 2 >= rows)) continue;
-            for (int split = 1; split <= (cg == 2 || bn > 128 ? 1 : most_split); split *= 2) {
-                if (split > 1 && split * 2 > slices) continue;
-                const double tiles_m = std::ceil((double)P.m / (cg * kTileM)), tiles_n = std::ceil(rows / bn);
-                double tiles = groups * tiles_m * tiles_n;
-                if (P.symmetric) tiles = groups * (tiles_m * tiles_n + std::max(tiles_m, tiles_n)) / 2;
-                const double slice = std::max(cg == 2 ? 150 + 1.85 * bn : 130 + 2.8 * bn, (kTileM + bn / cg) * 128.0 / 68);
-                const double main = std::ceil(slices / split) * 2 * slice;
-                const double exchange = split > 1 ? 5000 + 10 * bn : 0;
-                const double epilogue = 400 + 16 * std::min((double)bn, rows) / split + exchange;
+            const int64_t tiles_n = (rows + bn - 1) / bn;
+            const int64_t tiles = P.symmetric ? groups * (tiles_m * tiles_n + std::max(tiles_m, tiles_n)) / 2
+                                              : groups * tiles_m * tiles_n;
+            const double slice = std::max(cg == 2 ? 150 + 1.85 * bn : 130 + 2.8 * bn, (kTileM + bn / cg) * 128.0 / 68);
+            const double block = 400 + 16.0 * std::min<int64_t>(bn, rows);
+            for (int split = 1; split <= (cg == 2 || bn > 128 ? 1 : 8); split *= 2) {
+                if (split > 1 && (split * 2 > slices || tiles * split > 2 * sms)) break;
+                const double main = (double)((slices + split - 1) / split) * 2 * slice;
+                const double epilogue = split == 1 ? block : 400 + (block - 400) / split + 5000 + 10 * bn;
                 const int places = cg == 2 ? sms / 2 : split == 4 ? sms / 4 - 2 : split == 8 ? sms / 8 - 3 : sms / split;
-                const double cost = std::ceil(tiles / places) * std::max(main, epilogue) + std::min(main, epilogue);
-                const double total = std::max(cost, least) + 0.1 * cost;
-                if (best.cg == 0 || total < best.cost) best = {cg, bn, split, total};
+                const double cost = (double)((tiles + places - 1) / places) * std::max(main, epilogue) +
+                                    std::min(main, epilogue);
+                const Shape s = {cg, bn, split, std::max(cost, least) + 0.1 * cost};
+                if (c.best.cg == 0 || s.cost < c.best.cost) c.best = s;
+                Shape& own = cg == 1 ? c.single : c.pairs;
+                if (split == 1 && (own.cg == 0 || s.cost < own.cost)) own = s;
             }
         }
     }
-    return best;
+    return c;
 }
 
 // Complete a product for a shape: tiles and maps.
@@ -1805,11 +1800,8 @@ static ccl_status_t complete(const Device* dev, Product* P, const Shape& sh, con
 }
 
 // Complete a product and launch it.
-static ccl_status_t run(Product P, const Matrix& a, const Matrix& b, cudaStream_t stream)
+static ccl_status_t run(const Device* dev, Product P, const Shape& sh, const Matrix& a, const Matrix& b, cudaStream_t stream)
 {
-    const Device* dev = nullptr;
-    TRY(device(&dev));
-    const Shape sh = choose(P, dev->sms);
     TRY(complete(dev, &P, sh, a, b));
     const int size = sh.cg == 2 ? 2 : sh.split;
     const int bytes = (kTileM + P.bn / sh.cg) * kSliceK * 2;
@@ -1938,7 +1930,9 @@ static ccl_status_t linear(const ccl_linear_t* a, char* base, int64_t* need, cud
         P.bias = (const uint16_t*)a->bias;
         P.bs_bias = count > 1 ? sb : 0;
     }
-    return run(P, w, x, stream);
+    const Device* dev = nullptr;
+    TRY(device(&dev));
+    return run(dev, P, choose(P, dev->sms).best, w, x, stream);
 }
 
 static ccl_status_t linear_grad(const ccl_linear_grad_t* a, char* base, int64_t* need, cudaStream_t stream)
@@ -2039,30 +2033,25 @@ static ccl_status_t linear_grad(const ccl_linear_grad_t* a, char* base, int64_t*
         pw.a_mn = pw.b_mn = 1;
         set_out(&pw, a->dw, lddw, sdw, bf);
     }
+    const Device* dev = nullptr;
+    TRY(device(&dev));
+    const Choices cx = a->dx ? choose(px, dev->sms) : Choices(), cw = a->dw ? choose(pw, dev->sms) : Choices();
     if (a->dx && a->dw) {
         // one launch for both unless splitting or shapes of their own are worth more than the launch (9500 clocks)
-        const Device* dev = nullptr;
-        TRY(device(&dev));
-        Shape both[2][2];
-        double cost[2];
-        for (int cg = 1; cg <= 2; ++cg) {
-            both[cg - 1][0] = choose(px, dev->sms, cg, cg, 1);
-            both[cg - 1][1] = choose(pw, dev->sms, cg, cg, 1);
-            cost[cg - 1] = both[cg - 1][0].cost + both[cg - 1][1].cost;
-        }
-        const int cg = cost[1] <= cost[0] ? 2 : 1;
-        if (cost[cg - 1] < choose(px, dev->sms).cost + choose(pw, dev->sms).cost + 9500) {
+        const double one = cx.single.cost + cw.single.cost, two = cx.pairs.cost + cw.pairs.cost;
+        if (std::min(one, two) < cx.best.cost + cw.best.cost + 9500) {
             Pair R = {};
             R.p[0] = px;
             R.p[1] = pw;
             if (a->db) R.sums = G;
+            const Shape sh[2] = {two <= one ? cx.pairs : cx.single, two <= one ? cw.pairs : cw.single};
             const Matrix left[2] = {w, x}, right[2] = {dz, dz};
-            return run_pair(dev, &R, both[cg - 1], left, right, stream);
+            return run_pair(dev, &R, sh, left, right, stream);
         }
     }
     if (a->db) TRY(launch(bias_grad_kernel, dim3((unsigned)((a->n + 31) / 32), (unsigned)count), 256, 0, stream, G));
-    if (a->dx) TRY(run(px, w, dz, stream));
-    if (a->dw) TRY(run(pw, x, dz, stream));
+    if (a->dx) TRY(run(dev, px, cx.best, w, dz, stream));
+    if (a->dw) TRY(run(dev, pw, cw.best, x, dz, stream));
     return CCL_OK;
 }
 
@@ -2098,7 +2087,8 @@ static ccl_status_t orthogonalize(const ccl_ortho_t* a, char* base, int64_t* nee
     const bool small = r <= kSmallSide && longer <= (size == 1 ? 384 : 256 * size);
     Arena ws = {base};
     Matrix x[2], A, B;
-    const int64_t ldx = round_up(a->q, 8), lda = round_up(r, 8);
+    // rows start on cache lines: a 128-byte row of a tile would touch two of them otherwise
+    const int64_t ldx = round_up(a->q, 64), lda = round_up(r, 64);
     for (int i = 0; i < 2; ++i) {
         x[i] = {nullptr, a->p, a->q, ldx, a->batch, a->p * ldx};
         x[i].p = ws.take<void>(a->batch * a->p * ldx * 2);
@@ -2217,10 +2207,11 @@ static ccl_status_t orthogonalize(const ccl_ortho_t* a, char* base, int64_t* nee
     // about 4500 (waiting for all SMs); the chain runs tiles of single
     // threadblocks only.
     double apart = 0, chained = 0;
+    Choices shapes[3];
     for (int kind = 0; kind < 3; ++kind) {
-        const Step s = product(kind, 0, false, false);
-        apart += choose(s.p, dev->sms).cost + 9500;
-        chained += choose(s.p, dev->sms, 1, 1, 1).cost + 4500;
+        shapes[kind] = choose(product(kind, 0, false, false).p, dev->sms);
+        apart += shapes[kind].best.cost + 9500;
+        chained += shapes[kind].single.cost + 4500;
     }
     if (chained < apart) {
         Chain C = {};
@@ -2233,7 +2224,7 @@ static ccl_status_t orthogonalize(const ccl_ortho_t* a, char* base, int64_t* nee
             const int from = last ? (a->steps - 1) & 1 : i == 2 || i == 6;
             const Step s = product(kind, from, kind == 0 ? i == 0 : kind == 2 && (i == 4 || (last && a->steps == 1)), last);
             C.p[i] = s.p;
-            const Shape sh = choose(s.p, dev->sms, 1, 1, 1);
+            const Shape& sh = shapes[kind].single;
             TRY(complete(dev, &C.p[i], sh, *s.a, *s.b));
             C.width = std::max(C.width, sh.bn);
             most = std::max(most, C.p[i].total);
@@ -2245,7 +2236,7 @@ static ccl_status_t orthogonalize(const ccl_ortho_t* a, char* base, int64_t* nee
     }
     for (int i = 0; i < 3 * a->steps; ++i) {
         const Step s = product(i % 3, i / 3 & 1, i < 3, i / 3 + 1 == a->steps);
-        TRY(run(s.p, *s.a, *s.b, stream));
+        TRY(run(dev, s.p, shapes[i % 3].best, *s.a, *s.b, stream));
     }
     return CCL_OK;
 }
