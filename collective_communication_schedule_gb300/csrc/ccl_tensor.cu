@@ -53,7 +53,7 @@ constexpr int kEpilogueWarps = 16;
 constexpr int kThreads = 128 + 32 * kEpilogueWarps;
 constexpr int kBlockRows = 16;                  // an epilogue warp's block: 16 rows x 32 features
 constexpr int kStagingBytes = kEpilogueWarps * kBlockRows * 64;
-constexpr int kSmemBudget = 227 * 1024 - 6 * 1024;   // dynamic part; the rest is static
+constexpr int kSmemBudget = 227 * 1024 - 5 * 1024;   // dynamic part; the rest is static
 
 enum { DENSE = 0, RAGGED_ROWS = 1, RAGGED_REDUCE = 2 };
 
@@ -150,8 +150,9 @@ struct Shared {
     uint64_t got, taken;           // split: every share has arrived here, every share sent has been read
     uint32_t tmem;
     int failed;
-    int total;
-    int seg_end[kMaxGroups];
+    int total;                     // RAGGED_ROWS: tiles of all experts
+    int second;                    // pair: this cluster's first tile of the second product
+    int seg_end[kMaxGroups];       // RAGGED_ROWS: tiles of the experts up to each one
 };
 
 __device__ __forceinline__ void group_range(const Scalars& P, int g, int limit, int& lo, int& len)
@@ -160,8 +161,8 @@ __device__ __forceinline__ void group_range(const Scalars& P, int g, int limit, 
     len = min(max(P.offsets[g + 1], lo), limit) - lo;
 }
 
-// Tiles of the experts before and up to each one, for RAGGED_ROWS.
-template <int CG>
+// Before the products of a launch with offsets: a check of the offsets, and for
+// RAGGED_ROWS the tiles of the experts up to each one.
 __device__ __forceinline__ void prepare_tiles(const Scalars& P, Shared* sh)
 {
     if (!P.offsets) return;
@@ -394,7 +395,7 @@ __device__ __noinline__ bool phases_done(const uint32_t* arrived, uint32_t phase
 }
 
 // Sum a bias gradient's chunks, 32 columns of one expert at a time.
-__device__ __forceinline__ void add_chunks(const GradPass& G, int lane)
+__device__ __noinline__ void add_chunks(const GradPass& G, int lane)
 {
     const int columns = (G.n + 31) / 32;
     for (int item = blockIdx.x; item < G.groups * columns; item += gridDim.x) {
@@ -483,7 +484,11 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
     }
     let_next_in();
     if (MODE != CHAIN && seq.at(0).offsets) wait_for_previous();
-    if (MODE != CHAIN) prepare_tiles<CG>(seq.at(0), &sh);
+    if (MODE != CHAIN) prepare_tiles(seq.at(0), &sh);
+    if (MODE == PAIR && threadIdx.x == 0) {
+        const int total = seq.at(0).ragged == RAGGED_ROWS ? sh.total : seq.at(0).total;
+        sh.second = (cluster + clusters - total % clusters) % clusters;
+    }
     if (size > 1)
         cluster_sync();
     else
@@ -501,10 +506,17 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
     }
 
     // This threadblock's (cluster's) tiles of the next product: every
-    // `clusters`-th one.  In a pair they go on where the first product's
-    // stopped, in a chain every product starts anew.
-    int before = 0;
-    auto first_tile = [&]() { return MODE == PAIR ? (cluster + clusters - before % clusters) % clusters : cluster; };
+    // `clusters`-th one, so that tiles in flight at a time share operands
+    // (ranges of consecutive tiles, balanced by their cost, took 168 us
+    // instead of 117 for 8190 rows over 32 experts of 4096 x 2048).  In a pair
+    // the second product's go on where the first one's stopped, in a chain
+    // every product starts anew.
+    struct Run {
+        int begin, end;
+    };
+    auto next_run = [&](const Scalars& P, int ph) {
+        return Run{MODE == PAIR && ph ? sh.second : cluster, MODE != CHAIN && P.ragged == RAGGED_ROWS ? sh.total : P.total};
+    };
     const uint32_t* arrived = nullptr;
     if constexpr (MODE == CHAIN) arrived = seq.chain->arrived;
 
@@ -524,25 +536,25 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
                 tma_prefetch(&seq.at(ph + 1).ma);
                 tma_prefetch(&seq.at(ph + 1).mb);
             }
-            const bool a_mn = FORM == ANY_FORM ? P.a_mn : FORM != BOTH_K, b_mn = FORM == ANY_FORM ? P.b_mn : FORM == BOTH_MN;
+            const bool a_mn = FORM == ANY_FORM ? (MODE == PAIR || P.a_mn) : FORM != BOTH_K;
+            const bool b_mn = FORM == ANY_FORM ? (MODE == PAIR ? ph == 1 : P.b_mn) : FORM == BOTH_MN;
             const uint32_t bytes_b = P.bn / CG * kSliceK * 2;
             const uint32_t part_b = bytes_b / 2;      // one of a slice's two halves of B (reduction 0..63, 64..127)
             const uint32_t bytes = bytes_a + bytes_b;
             const bool reduce_rows = b_mn && P.ragged == RAGGED_REDUCE;
-            const int total = P.ragged == RAGGED_ROWS ? sh.total : P.total, bn = P.bn;
+            const int bn = P.bn;
             // the first tile is found before the wait for what it reads
             TileAt q;
-            const int begin = first_tile();
-            if (begin < total) q = tile_at<CG>(P, &sh, begin);
+            const Run run = next_run(P, ph);
+            if (run.begin < run.end) q = tile_at<CG>(P, &sh, run.begin);
             if (ph == 0) wait_for_previous();
             if (MODE == CHAIN && ph && good) {
                 if (lane == 0) good = phases_done(arrived, ph, failed);
                 good = __shfl_sync(~0u, good, 0);
                 asm volatile("fence.proxy.async;" ::: "memory");
             }
-            before += total;
-            for (int t = begin; t < total; t += clusters) {
-                if (t != begin) q = tile_at<CG>(P, &sh, t);
+            for (int t = run.begin; t < run.end; t += clusters) {
+                if (t != run.begin) q = tile_at<CG>(P, &sh, t);
                 const int m0 = q.m0 + (CG == 2 ? rank * kTileM : 0);
                 const int n0 = q.n0 + (CG == 2 ? rank * (used_rows<CG>(P, q) / 2) : 0);
                 int first, last;
@@ -613,13 +625,13 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
             bool good = true;
             for (int ph = 0; ph < phases; ++ph) {
                 const Scalars P = seq.at(ph);
-                const bool a_mn = FORM == ANY_FORM ? P.a_mn : FORM != BOTH_K, b_mn = FORM == ANY_FORM ? P.b_mn : FORM == BOTH_MN;
+                const bool a_mn = FORM == ANY_FORM ? (MODE == PAIR || P.a_mn) : FORM != BOTH_K;
+                const bool b_mn = FORM == ANY_FORM ? (MODE == PAIR ? ph == 1 : P.b_mn) : FORM == BOTH_MN;
                 const uint32_t bytes_b = P.bn / CG * kSliceK * 2;
                 const uint32_t part_b = bytes_b / 2;      // one of a slice's two halves of B (reduction 0..63, 64..127)
                 const bool reduce_rows = b_mn && P.ragged == RAGGED_REDUCE;
-                const int total = P.ragged == RAGGED_ROWS ? sh.total : P.total, begin = first_tile();
-                before += total;
-                for (int t = begin; t < total; t += clusters) {
+                const Run run = next_run(P, ph);
+                for (int t = run.begin; t < run.end; t += clusters) {
                     const TileAt q = tile_at<CG>(P, &sh, t);
                     int first, last;
                     slices(q, CG == 2 ? 1 : size, rank, first, last);
@@ -678,9 +690,8 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
         bool good = true;
         for (int ph = 0; ph < phases; ++ph) {
             const Scalars P = seq.at(ph);
-            const int total = P.ragged == RAGGED_ROWS ? sh.total : P.total, begin = first_tile();
-            before += total;
-            for (int t = begin; good && t < total; t += clusters) {
+            const Run run = next_run(P, ph);
+            for (int t = run.begin; good && t < run.end; t += clusters) {
                 const TileAt q = tile_at<CG>(P, &sh, t);
                 int first, last;
                 slices(q, CG == 2 ? 1 : size, rank, first, last);
@@ -712,6 +723,8 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
     } else if (warp >= 4) {
         const int quad = warp & 3, slot = (warp - 4) >> 2;
         constexpr int kStride = kEpilogueWarps / 4 * kBlockRows;     // rows that the warps of a quadrant take at once
+        // what the products of a mode can have
+        constexpr bool kLayer = MODE == SINGLE, kAdds = MODE != PAIR;
         unsigned char* st = staging + (warp - 4) * (kBlockRows * 64);
         uint32_t release[2];
         for (int i = 0; i < 2; ++i)
@@ -720,38 +733,36 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
         for (int ph = 0; ph < phases; ++ph) {
             const Product& maps = seq.at(ph);
             const Scalars P = maps;
-            const int side = P.symmetric ? 1 : 0;
-            const int total = P.ragged == RAGGED_ROWS ? sh.total : P.total;
+            const int side = kAdds && P.symmetric ? 1 : 0;
             TileAt q;
-            const int begin = first_tile();
-            before += total;
-            if (begin < total) q = tile_at<CG>(P, &sh, begin);
+            const Run run = next_run(P, ph);
+            if (run.begin < run.end) q = tile_at<CG>(P, &sh, run.begin);
             if (ph == 0) wait_for_previous();
             if (MODE == CHAIN && ph) {
                 if (threadIdx.x == 128) phases_done(arrived, ph, failed);
                 named_sync(3, 32 * kEpilogueWarps);
             }
-            for (int t = begin; t < total; t += clusters) {
-                if (t != begin) q = tile_at<CG>(P, &sh, t);
+            for (int t = run.begin; t < run.end; t += clusters) {
+                if (t != run.begin) q = tile_at<CG>(P, &sh, t);
                 int first, last;
                 slices(q, CG == 2 ? 1 : size, rank, first, last);
                 const bool some = first < last;
                 const int acc = done & 1;
                 const int feat = q.m0 + (CG == 2 ? rank * kTileM : 0) + quad * 32, nfeat = P.m - feat, f = feat + lane;
                 const int64_t row = (int64_t)q.row0 + q.n0;
-                const float alpha = P.alpha * (P.alpha_of ? P.alpha_of[q.g] : 1.f);
+                const float alpha = P.alpha * (kAdds && P.alpha_of ? P.alpha_of[q.g] : 1.f);
                 const float beta = P.beta * (P.beta_of ? P.beta_of[q.g] : 1.f);
-                const float bias = P.bias && f < P.m ? load1(P.bias + q.g * P.bs_bias + f, P.in_bf) : 0.f;
-                const bool whole = P.ragged != RAGGED_ROWS;    // TMA may cut rows off at the end of the matrix only
+                const float bias = kLayer && P.bias && f < P.m ? load1(P.bias + q.g * P.bs_bias + f, P.in_bf) : 0.f;
+                const bool whole = MODE == CHAIN || P.ragged != RAGGED_ROWS;    // TMA may cut rows off at the end of the matrix only
                 const int zo = P.ragged == RAGGED_ROWS ? 0 : q.g;
                 uint16_t cv[kBlockRows];
                 // C is read a block ahead of its use
-                if (P.c && size == CG) fetch_c(P, cv, q.g, row + slot * kBlockRows, q.live - slot * kBlockRows, f);
+                if (kAdds && P.c && size == CG) fetch_c(P, cv, q.g, row + slot * kBlockRows, q.live - slot * kBlockRows, f);
                 if (some) {
                     if (!__all_sync(~0u, bar_wait(smem_addr(&sh.acc_full[acc]), (done >> 1) & 1, failed))) break;
                     fence_after();
                 }
-                if (size > CG) {
+                if (kLayer && size > CG) {
                     // shares of the last tile have been read by their owners
                     if (!__all_sync(~0u, bar_wait<true>(smem_addr(&sh.taken), (round & 1) ^ 1, failed))) break;
                 }
@@ -765,7 +776,7 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
                         for (int i = 0; i < kBlockRows; ++i) u[i] = 0;
                     }
                     const int nrows = q.live - c;
-                    if (size > CG) {
+                    if (kLayer && size > CG) {
                         const int own = P.bn / size;
                         const uint32_t at = smem_addr(shares + (size_t)rank * own * kTileM + quad * 32 + lane);
                         // own is a power of two from 4 up: 4 rows at a time go to one owner
@@ -783,12 +794,13 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
                     uint32_t w[kBlockRows / 2];
 #pragma unroll
                     for (int i = 0; i < kBlockRows; ++i) v[i] = fmaf(alpha, __uint_as_float(u[i]), bias);
-                    if (P.pre) {
+                    if (kLayer && P.pre) {
                         pack_block(v, w, P.in_bf);
                         store_block(&maps.mp, P.pre + (row + c) * P.ld_pre + f, P.ld_pre, w, st,
                                     P.tma_pre && (whole || nrows >= kBlockRows), lane, feat, (int)row + c, 0, nrows, nfeat);
                     }
-                    if (P.act == ACT_RELU) {
+                    if (!kLayer) {
+                    } else if (P.act == ACT_RELU) {
 #pragma unroll
                         for (int i = 0; i < kBlockRows; ++i) v[i] = activate(v[i], ACT_RELU);
                     } else if (P.act == ACT_GELU) {
@@ -798,7 +810,7 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
 #pragma unroll
                         for (int i = 0; i < kBlockRows; ++i) v[i] = activate(v[i], ACT_SILU);
                     }
-                    if (P.c) {
+                    if (kAdds && P.c) {
                         if (P.in_bf) {
 #pragma unroll
                             for (int i = 0; i < kBlockRows; ++i) v[i] += beta * __uint_as_float((uint32_t)cv[i] << 16);
@@ -833,7 +845,7 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
                     }
                     ++done;
                 }
-                if (size > CG) {
+                if (kLayer && size > CG) {
                     __syncwarp();
                     if (lane < size) bar_arrive_cluster(cluster_addr(smem_addr(&sh.got), lane));
                     if (!__all_sync(~0u, bar_wait<true>(smem_addr(&sh.got), round & 1, failed))) break;
