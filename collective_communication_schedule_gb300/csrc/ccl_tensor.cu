@@ -117,22 +117,6 @@ struct Pair {
     Product p[2];
 };
 
-// Products one after the other in one launch, each reading what the ones
-// before it wrote: the steps of the Newton-Schulz iteration.  `p` holds each
-// different product once; phase() tells which one comes when.
-struct Chain {
-    int32_t steps, width, stages;  // width: the widest tile's rows; stages of that width
-    uint32_t* arrived;             // threadblocks that have finished a phase, in all phases so far
-    Product p[8];
-    __device__ int phase(int i) const
-    {
-        const int s = i / 3, kind = i % 3;
-        if (kind == 0) return s == 0 ? 0 : s & 1 ? 2 : 1;
-        if (kind == 1) return 3;
-        return s + 1 == steps ? 7 : s == 0 ? 4 : s & 1 ? 6 : 5;
-    }
-};
-
 // [0]: a ccl_status_t of a failed launch on this device, 0 if none
 __device__ int g_status[4];
 
@@ -274,31 +258,27 @@ __device__ __forceinline__ int used_rows(const Scalars& P, const TileAt& q)
     return P.ragged == RAGGED_ROWS ? min(P.bn, (q.live + 16 * CG - 1) / (16 * CG) * (16 * CG)) : P.bn;
 }
 
-// The part of the epilogue after alpha, for elements [lo, hi) of 8
-// consecutive features f.. of row n; c: their values of C, if any.
-__device__ __forceinline__ void finish8(const Scalars& P, float v[8], int g, int64_t n, int f, int lo, int hi,
-                                        float beta, const uint4* c)
+// The part of the epilogue after alpha, for the first `hi` of 8 consecutive
+// features f.. of row n, where 16-byte accesses are possible.
+__device__ __forceinline__ void finish8(const Scalars& P, float v[8], int g, int64_t n, int f, int hi, float beta)
 {
     float w[8];
     if (P.bias) {
-        load8(P.bias + g * P.bs_bias + f, P.in_bf, true, lo, hi, w);
+        load8(P.bias + g * P.bs_bias + f, P.in_bf, hi, w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] += w[i];
     }
-    if (P.pre) store8(P.pre + n * P.ld_pre + f, P.in_bf, true, lo, hi, v);
+    if (P.pre) store8(P.pre + n * P.ld_pre + f, P.in_bf, hi, v);
     if (P.act) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = activate(v[i], P.act);
     }
     if (P.c) {
-        if (c)
-            unpack8(*c, P.in_bf, w);
-        else
-            load8(P.c + g * P.bs_c + n * P.ld_c + f, P.in_bf, true, lo, hi, w);
+        load8(P.c + g * P.bs_c + n * P.ld_c + f, P.in_bf, hi, w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] += beta * w[i];
     }
-    store8(P.out + g * P.bs_out + n * P.ld_out + f, P.out_bf, true, lo, hi, v);
+    store8(P.out + g * P.bs_out + n * P.ld_out + f, P.out_bf, hi, v);
 }
 
 __device__ __forceinline__ void finish1(const Scalars& P, float v, int g, int64_t n, int f, float beta, float bias,
@@ -310,20 +290,8 @@ __device__ __forceinline__ void finish1(const Scalars& P, float v, int g, int64_
     store1(P.out + g * P.bs_out + n * P.ld_out + f, v + beta * c, P.out_bf);
 }
 
-// 8 features f.. of row n: which of them this side of a symmetric output
-// writes.  side: 0 = all; 1 = only feature <= row (the tile itself), -1 =
-// only feature > row (its mirror image): each element is written once and
-// the result is symmetric bit for bit.
-__device__ __forceinline__ void side_range(int side, int64_t n, int f, int nfeat, int& lo, int& hi)
-{
-    lo = 0;
-    hi = min(8, nfeat);
-    if (side > 0) hi = (int)min((int64_t)hi, n - f + 1);
-    if (side < 0) lo = (int)max((int64_t)0, n - f + 1);
-}
-
 // A block's rows of C at one feature per lane: 64 neighbouring bytes a row and
-// warp, whatever the alignment (past L1: in a chain other SMs write C).
+// warp, whatever the alignment.
 __device__ __forceinline__ void fetch_c(const Scalars& P, uint16_t c[kBlockRows], int g, int64_t row, int nrows, int f)
 {
     const uint16_t* p = P.c + g * P.bs_c + row * P.ld_c + f;
@@ -370,29 +338,8 @@ __device__ __forceinline__ void pack_block(const float v[kBlockRows], uint32_t w
     }
 }
 
-// FORM: storage of the operands, or ANY_FORM (looked up)
-enum { BOTH_K = 0, A_MN = 1, BOTH_MN = 2, ANY_FORM = 3 };
-
-// Wait (bounded) until all threadblocks have finished `phases` phases.  By
-// one thread of those that go on after it: polling is felt by the others.
-__device__ __noinline__ bool phases_done(const uint32_t* arrived, uint32_t phases, volatile int* failed)
-{
-    const uint32_t want = phases * gridDim.x;
-    unsigned long long t0 = 0;
-    for (int i = 0; i < kWaitSpins; ++i) {
-        uint32_t v;
-        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(arrived) : "memory");
-        if (v >= want) return true;
-        if ((i & 255) == 255) {
-            if (*failed) return false;
-            const unsigned long long t = now_ns();
-            if (!t0) t0 = t;
-            if (t - t0 > kWaitNs) break;
-        }
-    }
-    *failed = 1;
-    return false;
-}
+// FORM: storage of the operands (a pair: A_MN, then BOTH_MN)
+enum { BOTH_K = 0, A_MN = 1, BOTH_MN = 2 };
 
 // Sum a bias gradient's chunks, 32 columns of one expert at a time.
 __device__ __noinline__ void add_chunks(const GradPass& G, int lane)
@@ -412,9 +359,8 @@ __device__ __noinline__ void add_chunks(const GradPass& G, int lane)
     }
 }
 
-// MODE: one product; the two of a Pair; those of a Chain, in its order, with
-// all threadblocks of the grid in step
-enum { SINGLE = 0, PAIR = 1, CHAIN = 2 };
+// MODE: one product, or the two of a Pair
+enum { SINGLE = 0, PAIR = 1 };
 
 template <int MODE>
 struct Sequence {
@@ -434,16 +380,6 @@ struct Sequence<PAIR> {
     __device__ int phases() const { return 2; }
     __device__ const Product& at(int ph) const { return pair->p[ph]; }
 };
-template <>
-struct Sequence<CHAIN> {
-    const Chain* chain;
-    __device__ int width() const { return chain->width; }
-    __device__ int stages() const { return chain->stages; }
-    __device__ int split() const { return 1; }
-    __device__ int phases() const { return 3 * chain->steps; }
-    __device__ const Product& at(int ph) const { return chain->p[chain->phase(ph)]; }
-};
-
 // A threadblock's share of the tiles of a sequence of products.
 template <int CG, int FORM, int MODE>
 __device__ __forceinline__ void products(const Sequence<MODE> seq)
@@ -483,8 +419,8 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
         tma_prefetch(&seq.at(0).mb);
     }
     let_next_in();
-    if (MODE != CHAIN && seq.at(0).offsets) wait_for_previous();
-    if (MODE != CHAIN) prepare_tiles(seq.at(0), &sh);
+    if (seq.at(0).offsets) wait_for_previous();
+    prepare_tiles(seq.at(0), &sh);
     if (MODE == PAIR && threadIdx.x == 0) {
         const int total = seq.at(0).ragged == RAGGED_ROWS ? sh.total : seq.at(0).total;
         sh.second = (cluster + clusters - total % clusters) % clusters;
@@ -509,16 +445,13 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
     // `clusters`-th one, so that tiles in flight at a time share operands
     // (ranges of consecutive tiles, balanced by their cost, took 168 us
     // instead of 117 for 8190 rows over 32 experts of 4096 x 2048).  In a pair
-    // the second product's go on where the first one's stopped, in a chain
-    // every product starts anew.
+    // the second product's go on where the first one's stopped.
     struct Run {
         int begin, end;
     };
     auto next_run = [&](const Scalars& P, int ph) {
-        return Run{MODE == PAIR && ph ? sh.second : cluster, MODE != CHAIN && P.ragged == RAGGED_ROWS ? sh.total : P.total};
+        return Run{MODE == PAIR && ph ? sh.second : cluster, P.ragged == RAGGED_ROWS ? sh.total : P.total};
     };
-    const uint32_t* arrived = nullptr;
-    if constexpr (MODE == CHAIN) arrived = seq.chain->arrived;
 
     const uint32_t ring = smem_addr(dyn), full0 = smem_addr(sh.full), empty0 = smem_addr(sh.empty);
 
@@ -536,8 +469,8 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
                 tma_prefetch(&seq.at(ph + 1).ma);
                 tma_prefetch(&seq.at(ph + 1).mb);
             }
-            const bool a_mn = FORM == ANY_FORM ? (MODE == PAIR || P.a_mn) : FORM != BOTH_K;
-            const bool b_mn = FORM == ANY_FORM ? (MODE == PAIR ? ph == 1 : P.b_mn) : FORM == BOTH_MN;
+            const bool a_mn = MODE == PAIR || FORM != BOTH_K;
+            const bool b_mn = MODE == PAIR ? ph == 1 : FORM == BOTH_MN;
             const uint32_t bytes_b = P.bn / CG * kSliceK * 2;
             const uint32_t part_b = bytes_b / 2;      // one of a slice's two halves of B (reduction 0..63, 64..127)
             const uint32_t bytes = bytes_a + bytes_b;
@@ -548,11 +481,6 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
             const Run run = next_run(P, ph);
             if (run.begin < run.end) q = tile_at<CG>(P, &sh, run.begin);
             if (ph == 0) wait_for_previous();
-            if (MODE == CHAIN && ph && good) {
-                if (lane == 0) good = phases_done(arrived, ph, failed);
-                good = __shfl_sync(~0u, good, 0);
-                asm volatile("fence.proxy.async;" ::: "memory");
-            }
             for (int t = run.begin; t < run.end; t += clusters) {
                 if (t != run.begin) q = tile_at<CG>(P, &sh, t);
                 const int m0 = q.m0 + (CG == 2 ? rank * kTileM : 0);
@@ -625,8 +553,8 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
             bool good = true;
             for (int ph = 0; ph < phases; ++ph) {
                 const Scalars P = seq.at(ph);
-                const bool a_mn = FORM == ANY_FORM ? (MODE == PAIR || P.a_mn) : FORM != BOTH_K;
-                const bool b_mn = FORM == ANY_FORM ? (MODE == PAIR ? ph == 1 : P.b_mn) : FORM == BOTH_MN;
+                const bool a_mn = MODE == PAIR || FORM != BOTH_K;
+                const bool b_mn = MODE == PAIR ? ph == 1 : FORM == BOTH_MN;
                 const uint32_t bytes_b = P.bn / CG * kSliceK * 2;
                 const uint32_t part_b = bytes_b / 2;      // one of a slice's two halves of B (reduction 0..63, 64..127)
                 const bool reduce_rows = b_mn && P.ragged == RAGGED_REDUCE;
@@ -682,7 +610,7 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
             }
             __syncwarp();
         }
-    } else if (warp == 3 && MODE != CHAIN && (MODE == PAIR || FORM == BOTH_MN) &&
+    } else if (warp == 3 && (MODE == PAIR || FORM == BOTH_MN) &&
                seq.at(phases - 1).ragged == RAGGED_REDUCE) {
         // 0 x Inf or NaN would not be 0: both operands are cleared
         int it = 0;
@@ -738,10 +666,6 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
             const Run run = next_run(P, ph);
             if (run.begin < run.end) q = tile_at<CG>(P, &sh, run.begin);
             if (ph == 0) wait_for_previous();
-            if (MODE == CHAIN && ph) {
-                if (threadIdx.x == 128) phases_done(arrived, ph, failed);
-                named_sync(3, 32 * kEpilogueWarps);
-            }
             for (int t = run.begin; t < run.end; t += clusters) {
                 if (t != run.begin) q = tile_at<CG>(P, &sh, t);
                 int first, last;
@@ -753,7 +677,7 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
                 const float alpha = P.alpha * (kAdds && P.alpha_of ? P.alpha_of[q.g] : 1.f);
                 const float beta = P.beta * (P.beta_of ? P.beta_of[q.g] : 1.f);
                 const float bias = kLayer && P.bias && f < P.m ? load1(P.bias + q.g * P.bs_bias + f, P.in_bf) : 0.f;
-                const bool whole = MODE == CHAIN || P.ragged != RAGGED_ROWS;    // TMA may cut rows off at the end of the matrix only
+                const bool whole = P.ragged != RAGGED_ROWS;    // TMA may cut rows off at the end of the matrix only
                 const int zo = P.ragged == RAGGED_ROWS ? 0 : q.g;
                 uint16_t cv[kBlockRows];
                 // C is read a block ahead of its use
@@ -852,13 +776,10 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
                     // sum the shares of this threadblock's rows in rank order
                     const int own = P.bn / size, base = rank * own, mine = min(own, q.live - base);
                     const int id = (warp - 4) * 32 + lane;
-                    const int left = P.m - q.m0;
                     if (P.vec) {
                         for (int i = id; i < mine * (kTileM / 8); i += 32 * kEpilogueWarps) {
-                            const int r = i / (kTileM / 8), f = i % (kTileM / 8) * 8;
-                            int lo, hi;
-                            side_range(side, row + base + r, q.m0 + f, left - f, lo, hi);
-                            if (lo >= hi) continue;
+                            const int r = i / (kTileM / 8), f = i % (kTileM / 8) * 8, hi = min(8, P.m - q.m0 - f);
+                            if (hi <= 0) continue;
                             float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
                             for (int s = 0; s < size; ++s) {
                                 const float4* p =
@@ -867,15 +788,15 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
                                 v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
                                 v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
                             }
-    #pragma unroll
+#pragma unroll
                             for (int e = 0; e < 8; ++e) v[e] *= alpha;
-                            finish8(P, v, q.g, row + base + r, q.m0 + f, lo, hi, beta, nullptr);
+                            finish8(P, v, q.g, row + base + r, q.m0 + f, hi, beta);
                         }
                     } else {
                         for (int i = id; i < mine * kTileM; i += 32 * kEpilogueWarps) {
                             const int r = i / kTileM, f = q.m0 + i % kTileM;
                             const int64_t n = row + base + r;
-                            if (f >= P.m || (side && f > n)) continue;
+                            if (f >= P.m) continue;
                             float v = 0.f;
                             for (int s = 0; s < size; ++s) v += shares[((size_t)s * own + r) * kTileM + i % kTileM];
                             finish1(P, alpha * v, q.g, n, f, beta,
@@ -883,40 +804,10 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
                                     P.c ? load1(P.c + q.g * P.bs_c + n * P.ld_c + f, P.in_bf) : 0.f);
                         }
                     }
-                    if (side) {
-                        // the mirror image: 8 of this threadblock's rows at a time for one feature
-                        const int parts = (mine + 7) / 8;
-                        for (int i = id; i < parts * kTileM; i += 32 * kEpilogueWarps) {
-                            const int f = i % kTileM, r0 = i / kTileM * 8, n = q.n0 + base + r0;
-                            int lo, hi;
-                            side_range(-1, q.m0 + f, n, mine - r0, lo, hi);
-                            if (f >= left || lo >= hi) continue;
-                            float v[8];
-    #pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                v[e] = 0.f;
-                                if (e >= lo && e < hi)
-                                    for (int s = 0; s < size; ++s)
-                                        v[e] += shares[((size_t)s * own + r0 + e) * kTileM + f];
-                                v[e] *= alpha;
-                            }
-                            finish8(P, v, q.g, q.m0 + f, n, lo, hi, beta, nullptr);
-                        }
-                    }
                     __syncwarp();
                     if (lane < size) bar_arrive_cluster(cluster_addr(smem_addr(&sh.taken), lane));
                     ++round;
                 }
-            }
-            if (MODE == CHAIN) {
-                // everything this threadblock wrote, by either route, is visible before it arrives
-                if (lane == 0) tma_stores_done();
-                __syncwarp();
-                asm volatile("fence.proxy.async;" ::: "memory");
-                named_sync(3, 32 * kEpilogueWarps);
-                if (threadIdx.x == 128)
-                    asm volatile("fence.acq_rel.gpu;\n\tred.release.gpu.global.add.u32 [%0], 1;" ::"l"(arrived)
-                                 : "memory");
             }
         }
         fence_before();
@@ -951,11 +842,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 template <int CG>
 __global__ void __launch_bounds__(kThreads, 1) pair_kernel(const __grid_constant__ Pair P)
 {
-    products<CG, ANY_FORM, PAIR>({&P});
-}
-__global__ void __launch_bounds__(kThreads, 1) chain_kernel(const __grid_constant__ Chain C)
-{
-    products<1, ANY_FORM, CHAIN>({&C});
+    products<CG, A_MN, PAIR>({&P});
 }
 
 // ======================================================================
@@ -1020,7 +907,7 @@ __global__ void __launch_bounds__(256) act_grad_kernel(const GradPass G)
 #pragma unroll
                         for (int i = 0; i < 8; ++i) v[i] *= activate_grad(w[i], G.act);
                     }
-                    if (G.dz) store8(G.dz + (row0 + 8 * j) * G.ld_dz + c, G.bf, true, 0, 8, v);
+                    if (G.dz) store8(G.dz + (row0 + 8 * j) * G.ld_dz + c, G.bf, 8, v);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) sum[i] += v[i];
                 }
@@ -1101,7 +988,6 @@ struct NormPass {
     const void* g;
     __half* x;
     float *partial, *kappa, *kappa2;
-    uint32_t* arrived;             // the chain's counter, set to 0 here
     int64_t ld_g, bs_g, ld_x, bs_x;
     int64_t run;                   // elements of a run of consecutive ones: a row, or the whole matrix
     int32_t p, q, type, runs, blocks;
@@ -1128,7 +1014,12 @@ __device__ __forceinline__ void load_any8(const void* p, int64_t i, int type, fl
         }
     } else {
         const uint16_t* h = (const uint16_t*)p + i;
-        load8(h, type == CCL_BF16, ((uintptr_t)h & 15) == 0, 0, 8, v);
+        if (((uintptr_t)h & 15) == 0) {
+            unpack8(*reinterpret_cast<const uint4*>(h), type == CCL_BF16, v);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = load1(h + e, type == CCL_BF16);
+        }
     }
 }
 
@@ -1199,7 +1090,6 @@ __global__ void __launch_bounds__(256) scale_kernel(const NormPass N)
     float kappa, f1, f2;
     norm_scale(s, N.eps, kappa, f1, f2);
     if (blockIdx.x == 0 && threadIdx.x == 0) {
-        if (blockIdx.y == 0) *N.arrived = 0;
         N.kappa[blockIdx.y] = kappa;
         N.kappa2[blockIdx.y] = kappa * kappa;
     }
@@ -1217,7 +1107,7 @@ __global__ void __launch_bounds__(256) scale_kernel(const NormPass N)
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = v[e] * f1 * f2;
-        store8((uint16_t*)N.x + blockIdx.y * N.bs_x + r * N.ld_x + c, false, true, 0, 8, v);   // rows are padded
+        store8((uint16_t*)N.x + blockIdx.y * N.bs_x + r * N.ld_x + c, false, 8, v);   // rows are padded
     }
 }
 
@@ -1229,7 +1119,7 @@ __global__ void __launch_bounds__(256) scale_kernel(const NormPass N)
 // their parts of A = x x^T through distributed shared memory (each sums 128 /
 // size rows, in rank order, and hands them to all), the rest of the step
 // stays within a threadblock.  A tall matrix is transposed as it is loaded
-// and stored.  Bound by the latency of the chain of 3 x steps products.
+// and stored.  Bound by the latency of 3 x steps products in a row.
 //
 // Rows of 64 elements (128 bytes) in 1024-byte atoms of 8 rows, 16-byte pieces
 // exchanged by the row's index: element (i, j) of x is at piece (j / 8 % 8) ^
@@ -1589,8 +1479,6 @@ static ccl_status_t device(const Device** out)
         for (auto kernel : {pair_kernel<1>, pair_kernel<2>})
             TRY_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBudget),
                      "shared memory of the pair kernel");
-        TRY_CUDA(cudaFuncSetAttribute(chain_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBudget),
-                 "shared memory of the chain kernel");
         TRY_CUDA(cudaFuncSetAttribute(small_ortho_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBudget),
                  "shared memory of the small orthogonalisation kernel");
         all[d].ready = true;
@@ -1599,8 +1487,6 @@ static ccl_status_t device(const Device** out)
     return CCL_OK;
 }
 
-// cluster > 1: in clusters of that many threadblocks; 0: all threadblocks
-// resident at once, as ones that wait for each other have to be
 template <typename Arg>
 static ccl_status_t launch(void (*kernel)(const Arg), dim3 grid, int threads, size_t smem, cudaStream_t stream, const Arg& arg,
                            int cluster = 1)
@@ -1611,13 +1497,8 @@ static ccl_status_t launch(void (*kernel)(const Arg), dim3 grid, int threads, si
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute at[2];
-    if (cluster == 0) {
-        at[0].id = cudaLaunchAttributeCooperative;
-        at[0].val.cooperative = 1;
-    } else {
-        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        at[0].val.programmaticStreamSerializationAllowed = 1;
-    }
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
     at[1].id = cudaLaunchAttributeClusterDimension;
     at[1].val.clusterDim.x = (unsigned)cluster;
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
@@ -1732,10 +1613,11 @@ struct Shape {
 // constants are fits to measured times (bf16, 1.9 GHz, 4096 x 4096 x 4096
 // unless noted).  Per 64 reduction elements: pairs 620, 540, 378 and 278
 // clocks for 256, 192, 128 and 64 rows; single threadblocks 864, 476 and 300
-// for 256, 128 and 64; and no SM gets more than about 68 bytes a clock from
-// L2.  An exchange of shares costs about 5000 clocks (1 x 4096 x 4096: 15.1,
-// 12.9, 11.7 and 19 us cut in 1, 2, 4 and 8), and clusters of 4 and 8 leave
-// SMs unused.
+// for 256, 128 and 64; no SM gets more than about 68 bytes a clock from L2,
+// all together 8000.  An exchange of shares costs about 5000 clocks and 60 per
+// row (1 x 4096 x 4096: 15.1, 12.9, 11.7 and 19 us cut in 1, 2, 4 and 8; x x^T
+// of 1024 x 4096: 40 us more when cut in 4), and clusters of 4 and 8 leave SMs
+// unused.
 struct Choices {
     Shape best, single, pairs;     // of all; of single threadblocks without a split; of pairs
 };
@@ -1757,12 +1639,15 @@ static Choices choose(const Product& P, int sms)
             const int64_t tiles_n = (rows + bn - 1) / bn;
             const int64_t tiles = P.symmetric ? groups * (tiles_m * tiles_n + std::max(tiles_m, tiles_n)) / 2
                                               : groups * tiles_m * tiles_n;
-            const double slice = std::max(cg == 2 ? 150 + 1.85 * bn : 130 + 2.8 * bn, (kTileM + bn / cg) * 128.0 / 68);
+            const double bytes = (kTileM + bn / cg) * 128.0;
+            const double busy = (double)std::min<int64_t>(tiles * cg, sms);
             const double block = 400 + 16.0 * std::min<int64_t>(bn, rows);
-            for (int split = 1; split <= (cg == 2 || bn > 128 ? 1 : 8); split *= 2) {
+            for (int split = 1; split <= (cg == 2 || bn > 128 || P.symmetric ? 1 : 8); split *= 2) {
                 if (split > 1 && (split * 2 > slices || tiles * split > 2 * sms)) break;
+                const double slice = std::max({cg == 2 ? 150 + 1.85 * bn : 130 + 2.8 * bn, bytes / 68,
+                                               bytes * std::min<double>(sms, busy * split) / 8000});
                 const double main = (double)((slices + split - 1) / split) * 2 * slice;
-                const double epilogue = split == 1 ? block : 400 + (block - 400) / split + 5000 + 10 * bn;
+                const double epilogue = split == 1 ? block : 400 + (block - 400) / split + 5000 + 60.0 * std::min<int64_t>(bn, rows);
                 const int places = cg == 2 ? sms / 2 : split == 4 ? sms / 4 - 2 : split == 8 ? sms / 8 - 3 : sms / split;
                 const double cost = (double)((tiles + places - 1) / places) * std::max(main, epilogue) +
                                     std::min(main, epilogue);
@@ -2112,7 +1997,6 @@ static ccl_status_t orthogonalize(const ccl_ortho_t* a, char* base, int64_t* nee
     N.partial = ws.take<float>(a->batch * kNormBlocks * 4);
     N.kappa = ws.take<float>(a->batch * 4);
     N.kappa2 = ws.take<float>(a->batch * 4);
-    N.arrived = ws.take<uint32_t>(4);
     if (need) {
         *need = small ? 0 : ws.used;
         return CCL_OK;
@@ -2213,42 +2097,11 @@ static ccl_status_t orthogonalize(const ccl_ortho_t* a, char* base, int64_t* nee
     };
     const Device* dev = nullptr;
     TRY(device(&dev));
-    // One launch for all steps where the products are small: a launch of its
-    // own costs a product about 9500 clocks before and after its work (cold
-    // instructions, descriptors, the launch itself), a phase of the chain
-    // about 4500 (waiting for all SMs); the chain runs tiles of single
-    // threadblocks only.
-    double apart = 0, chained = 0;
-    Choices shapes[3];
-    for (int kind = 0; kind < 3; ++kind) {
-        shapes[kind] = choose(product(kind, 0, false, false).p, dev->sms);
-        apart += shapes[kind].best.cost + 9500;
-        chained += shapes[kind].single.cost + 4500;
-    }
-    if (chained < apart) {
-        Chain C = {};
-        C.steps = a->steps;
-        C.arrived = N.arrived;
-        int most = 0;
-        for (int i = 0; i < 8; ++i) {
-            // the order that Chain::phase() expects
-            const int kind = i < 3 ? 0 : i == 3 ? 1 : 2, last = i == 7;
-            const int from = last ? (a->steps - 1) & 1 : i == 2 || i == 6;
-            const Step s = product(kind, from, kind == 0 ? i == 0 : kind == 2 && (i == 4 || (last && a->steps == 1)), last);
-            C.p[i] = s.p;
-            const Shape& sh = shapes[kind].single;
-            TRY(complete(dev, &C.p[i], sh, *s.a, *s.b));
-            C.width = std::max(C.width, sh.bn);
-            most = std::max(most, C.p[i].total);
-        }
-        const int bytes = (kTileM + C.width) * kSliceK * 2, fixed = 1024 + kStagingBytes;
-        C.stages = std::min(kMaxStages, (kSmemBudget - fixed) / bytes);
-        return launch(chain_kernel, dim3((unsigned)std::min(most, dev->sms)), kThreads,
-                      fixed + (size_t)C.stages * bytes, stream, C, 0);
-    }
+    Shape shapes[3];
+    for (int kind = 0; kind < 3; ++kind) shapes[kind] = choose(product(kind, 0, false, false).p, dev->sms).best;
     for (int i = 0; i < 3 * a->steps; ++i) {
         const Step s = product(i % 3, i / 3 & 1, i < 3, i / 3 + 1 == a->steps);
-        TRY(run(dev, s.p, shapes[i % 3].best, *s.a, *s.b, stream));
+        TRY(run(dev, s.p, shapes[i % 3], *s.a, *s.b, stream));
     }
     return CCL_OK;
 }

@@ -325,20 +325,20 @@ __device__ __forceinline__ void unpack8(const uint4& u, bool bf, float v[8])
         v[2 * i + 1] = f.y;
     }
 }
-// elements [lo, hi) of 8 consecutive ones; the others read as 0 and are not
-// touched.  vec: the address is 16-byte aligned
-__device__ __forceinline__ void load8(const uint16_t* p, bool bf, bool vec, int lo, int hi, float v[8])
+// the first n of 8 consecutive elements at a multiple of 16 bytes; the others
+// read as 0 and are not touched
+__device__ __forceinline__ void load8(const uint16_t* p, bool bf, int n, float v[8])
 {
-    if (vec && lo == 0 && hi == 8) {
+    if (n >= 8) {
         unpack8(*reinterpret_cast<const uint4*>(p), bf, v);
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = i >= lo && i < hi ? load1(p + i, bf) : 0.f;
+        for (int i = 0; i < 8; ++i) v[i] = i < n ? load1(p + i, bf) : 0.f;
     }
 }
-__device__ __forceinline__ void store8(uint16_t* p, bool bf, bool vec, int lo, int hi, const float v[8])
+__device__ __forceinline__ void store8(uint16_t* p, bool bf, int n, const float v[8])
 {
-    if (vec && lo == 0 && hi == 8) {
+    if (n >= 8) {
         uint4 u;
         if (bf)
             u = make_uint4(pack2<true>(v[0], v[1]), pack2<true>(v[2], v[3]), pack2<true>(v[4], v[5]),
@@ -350,7 +350,7 @@ __device__ __forceinline__ void store8(uint16_t* p, bool bf, bool vec, int lo, i
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (i >= lo && i < hi) store1(p + i, v[i], bf);
+            if (i < n) store1(p + i, v[i], bf);
     }
 }
 
