@@ -21,7 +21,8 @@ SOURCES = ["ccl_runtime.cu", "ccl_static.cu", "ccl_tensor.cu", "ccl_compiler.cpp
            "ccl_planner.cpp", "ccl_tuner.cpp", "ccl_persist.cpp", "ccl_codegen.cpp"]
 # device headers the run-time compiler of generated kernels receives as text
 EMBEDDED = ["ccl_layout.h", "ccl_core.cuh"]
-HEADERS = ["ccl_internal.h", "ccl_plan.h", "ccl_layout.h", "ccl_core.cuh", "ccl_tensor.cuh"]
+HEADERS = ["ccl_internal.h", "ccl_plan.h", "ccl_layout.h", "ccl_core.cuh", "ccl_tensor.cuh", "ccl_tensor_ortho.cuh",
+           "ccl_tensor_passes.cuh", "ccl_tensor_product.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",

@@ -1,0 +1,460 @@
+// The orthogonalisation's own kernels: norm and scaling passes, and all of the
+// iteration in one launch for matrices with a short side.
+#pragma once
+
+#include <cstdint>
+
+#include "ccl_tensor.cuh"
+#include "ccl_tensor_passes.cuh"
+
+namespace ccl {
+namespace tensor {
+
+// The iteration keeps x, A and B in f16: 11 bits instead of bf16's 8, at the
+// same matrix rate, and their range is known (singular values of x stay
+// near 1), so fixed powers of two keep the entries clear of both ends.
+constexpr float kScaleX = 4096.f, kScaleA = 1024.f;
+constexpr int kNormBlocks = 256;
+
+struct NormPass {
+    const void* g;
+    __half* x;
+    float *partial, *kappa, *kappa2;
+    int64_t ld_g, bs_g, ld_x, bs_x;
+    int64_t run;                   // elements of a run of consecutive ones: a row, or the whole matrix
+    int32_t p, q, type, runs, blocks;
+    float eps;
+};
+
+__device__ __forceinline__ float load_any(const void* p, int64_t i, int type)
+{
+    if (type == CCL_F32) return ((const float*)p)[i];
+    return load1((const uint16_t*)p + i, type == CCL_BF16);
+}
+
+// 8 elements from i on, i any index
+__device__ __forceinline__ void load_any8(const void* p, int64_t i, int type, float v[8])
+{
+    if (type == CCL_F32) {
+        const float* f = (const float*)p + i;
+        if (((uintptr_t)f & 15) == 0) {
+            const float4 a = ((const float4*)f)[0], b = ((const float4*)f)[1];
+            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = f[e];
+        }
+    } else {
+        const uint16_t* h = (const uint16_t*)p + i;
+        if (((uintptr_t)h & 15) == 0) {
+            unpack8(*reinterpret_cast<const uint4*>(h), type == CCL_BF16, v);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = load1(h + e, type == CCL_BF16);
+        }
+    }
+}
+
+__device__ __forceinline__ float block_sum(float v, float* sm)
+{
+#pragma unroll
+    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(~0u, v, d);
+    if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
+    __syncthreads();
+    float s = 0.f;
+    for (int i = 0; i < (int)blockDim.x / 32; ++i) s += sm[i];
+    return s;
+}
+
+// Sums of squares (DRAM: 4 x 2048 x 4096 bf16 in 14 us): threadblocks take groups of 8 elements of all runs in
+// turn (one run where the matrix is packed), so the order is fixed.
+__global__ void __launch_bounds__(256) norm_kernel(const NormPass N)
+{
+    __shared__ float sm[8];
+    let_next_in();
+    wait_for_previous();
+    const int64_t base = blockIdx.y * N.bs_g, per = (N.run + 7) / 8, all = per * N.runs;
+    float s = 0.f;
+#pragma unroll 4
+    for (int64_t i = blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
+        const int64_t r = N.runs == 1 ? 0 : i / per, c = (i - r * per) * 8, at = base + r * N.ld_g + c;
+        float v[8];
+        if (c + 8 <= N.run) {
+            load_any8(N.g, at, N.type, v);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = c + e < N.run ? load_any(N.g, at + e, N.type) : 0.f;
+        }
+        float t = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) t = fmaf(v[e], v[e], t);
+        s += t;
+    }
+    s = block_sum(s, sm);
+    if (threadIdx.x == 0) N.partial[blockIdx.y * kNormBlocks + blockIdx.x] = s;
+}
+
+// x0 = g * 2^e in f16 (exact for bf16 gradients) with the power of two that
+// brings the norm to kScaleX / 2 .. kScaleX; the remaining factor kappa of
+// x0 = kScaleX * g / (norm + eps) is applied in 32 bits by the epilogues of
+// the first step.
+__device__ __forceinline__ void norm_scale(float sum, float eps, float& kappa, float& f1, float& f2)
+{
+    const float norm = sqrtf(sum);
+    int e = 0;
+    if (norm > 0.f && norm <= 3.4e38f) {
+        int x;
+        frexpf(norm, &x);            // norm in [2^(x-1), 2^x)
+        e = 12 - x;                  // kScaleX = 2^12
+    }
+    kappa = ldexpf(1.f, 12 - e) / (norm + eps);
+    f1 = ldexpf(1.f, e / 2);         // 2^e may leave the range of 32 bits: in two factors
+    f2 = ldexpf(1.f, e - e / 2);
+}
+
+__global__ void __launch_bounds__(256) scale_kernel(const NormPass N)
+{
+    __shared__ float sm[8];
+    let_next_in();
+    wait_for_previous();
+    float s = (int)threadIdx.x < N.blocks ? N.partial[blockIdx.y * kNormBlocks + threadIdx.x] : 0.f;
+    s = block_sum(s, sm);
+    float kappa, f1, f2;
+    norm_scale(s, N.eps, kappa, f1, f2);
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        N.kappa[blockIdx.y] = kappa;
+        N.kappa2[blockIdx.y] = kappa * kappa;
+    }
+    const int per = (N.q + 7) / 8;
+    const int64_t all = (int64_t)per * N.p;
+#pragma unroll 2
+    for (int64_t i = blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
+        const int64_t r = i / per, c = (i - r * per) * 8, at = blockIdx.y * N.bs_g + r * N.ld_g + c;
+        float v[8];
+        if (c + 8 <= N.q) {
+            load_any8(N.g, at, N.type, v);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = c + e < N.q ? load_any(N.g, at + e, N.type) : 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = v[e] * f1 * f2;
+        store8((uint16_t*)N.x + blockIdx.y * N.bs_x + r * N.ld_x + c, false, 8, v);   // rows are padded
+    }
+}
+
+// All of the iteration for matrices with a side of at most 128, in one launch
+// and without leaving the SM: x, A and B live in shared memory in the layout
+// the matrix instructions read, accumulators in tensor memory, and a step is
+// three products with a threadblock barrier after each.  A long side is cut
+// over the threadblocks of a cluster, `width` columns of x each: they add up
+// their parts of A = x x^T through distributed shared memory (each sums 128 /
+// size rows, in rank order, and hands them to all), the rest of the step
+// stays within a threadblock.  A tall matrix is transposed as it is loaded
+// and stored.  Bound by the latency of 3 x steps products in a row: 128 x 128 in
+// 19 us, of which a product with its barrier takes about 0.9 us; one launch per
+// product took 87 us.
+//
+// Rows of 64 elements (128 bytes) in 1024-byte atoms of 8 rows, 16-byte pieces
+// exchanged by the row's index: element (i, j) of x is at piece (j / 8 % 8) ^
+// (i % 8) of row i of block j / 64.  The same bytes are x with the reduction
+// along its columns (x x^T) and along its rows (B x).
+constexpr int kSmallSide = 128;
+constexpr int kSmallThreads = 512;
+constexpr int kSmallBlock = kSmallSide * 128;          // bytes of a block of 64 columns
+constexpr int kSharePitch = kSmallSide + 4;            // floats; rows 4 banks apart
+
+struct Small {
+    const void* g;
+    uint16_t* out;
+    int64_t ld_g, bs_g, ld_out, bs_out;
+    int32_t side, length;          // short and long side
+    int32_t tall, type, out_bf, steps;
+    int32_t size, width, vec_out;
+    float a, b, c, eps, scale;
+};
+
+__device__ __forceinline__ uint32_t small_at(int i, int j)
+{
+    return (uint32_t)(j >> 6) * kSmallBlock + i * 128 + (((j >> 3) & 7) ^ (i & 7)) * 16;
+}
+
+__device__ __forceinline__ void store_cluster16(uint32_t addr, uint4 v)
+{
+    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+
+__global__ void __launch_bounds__(kSmallThreads, 1) small_ortho_kernel(const __grid_constant__ Small S)
+{
+    __shared__ __align__(8) uint64_t done;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int failed;
+    __shared__ float sm[16], norms[8];
+    extern __shared__ unsigned char raw[];
+    unsigned char* dyn = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = warp & 3, group = warp >> 2;
+    const int rank = S.size > 1 ? (int)cluster_rank() : 0, entry = blockIdx.x / S.size;
+    const int width = S.width, col0 = rank * width, cols = max(0, min(width, S.length - col0));
+    unsigned char *x = dyn, *A = x + (size_t)width / 64 * kSmallBlock, *B = A + 2 * kSmallBlock;
+    float* shares = reinterpret_cast<float*>(B + 2 * kSmallBlock);   // size > 1: [source][own row][column of A]
+    const uint32_t bar = smem_addr(&done);
+    if (threadIdx.x == 0) {
+        bar_init(bar, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        failed = 0;
+    }
+    if (warp == 1) tmem_alloc<1>(smem_addr(&tmem_slot), 512);
+    let_next_in();
+    wait_for_previous();
+
+    // 8 columns j.. of row i of g (or of its transpose)
+    const int64_t base = (int64_t)entry * S.bs_g;
+    auto fetch = [&](int i, int j, float v[8]) {
+        if (i >= S.side || j >= cols) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = 0.f;
+        } else if (S.tall) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[e] = j + e < cols ? load_any(S.g, base + (int64_t)(col0 + j + e) * S.ld_g + i, S.type) : 0.f;
+        } else if (j + 8 <= cols) {
+            load_any8(S.g, base + i * S.ld_g + col0 + j, S.type, v);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[e] = j + e < cols ? load_any(S.g, base + i * S.ld_g + col0 + j + e, S.type) : 0.f;
+        }
+    };
+    // neighbouring threads take neighbouring elements in memory
+    const int pieces = width / 8, items = pieces * kSmallSide;
+    auto place = [&](int n, int& i, int& j) {
+        if (S.tall) {
+            i = n % kSmallSide;
+            j = n / kSmallSide * 8;
+        } else {
+            i = n / pieces;
+            j = n % pieces * 8;
+        }
+    };
+    float sum = 0.f;
+#pragma unroll 2
+    for (int n = threadIdx.x; n < items; n += kSmallThreads) {
+        int i, j;
+        place(n, i, j);
+        float v[8], t = 0.f;
+        fetch(i, j, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) t = fmaf(v[e], v[e], t);
+        sum += t;
+    }
+    sum = block_sum(sum, sm);
+    if (S.size > 1) {
+        cluster_sync();            // the others' shared memory is live from here on
+        if ((int)threadIdx.x < S.size) store_cluster(cluster_addr(smem_addr(&norms[rank]), threadIdx.x), sum);
+        cluster_sync();
+        sum = 0.f;
+        for (int i = 0; i < S.size; ++i) sum += norms[i];
+    }
+    float kappa, f1, f2;
+    norm_scale(sum, S.eps, kappa, f1, f2);
+#pragma unroll 2
+    for (int n = threadIdx.x; n < items; n += kSmallThreads) {
+        int i, j;
+        place(n, i, j);
+        float v[8];
+        fetch(i, j, v);
+        uint4 u;
+        uint32_t* w = &u.x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = pack2<false>(v[2 * e] * f1 * f2, v[2 * e + 1] * f1 * f2);
+        *reinterpret_cast<uint4*>(x + small_at(i, j)) = u;
+    }
+    fence_async();
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = tmem_slot, lanes = (uint32_t)(quad * 32) << 16;
+    const uint32_t x_at = (smem_addr(x) & 0x3ffff) >> 4, a_at = (smem_addr(A) & 0x3ffff) >> 4,
+                   b_at = (smem_addr(B) & 0x3ffff) >> 4;
+    const uint64_t along = operand_desc(0, 0, 1024), across = operand_desc(0, kSmallBlock, 1024);
+    const uint32_t square = mma_desc(false, false, false, kSmallSide, kSmallSide);
+    constexpr uint32_t to_x = kSmallSide;       // tensor memory: columns 0.. A or B, 128.. x
+    const int row = quad * 32 + lane;
+    uint32_t parity = 0;
+    // an accumulator's 32 columns from `col` of this thread's row, once all products issued so far are done
+    auto finish = [&]() {
+        if (!bar_wait(bar, parity, &failed)) failed = 1;
+        parity ^= 1;
+        fence_after();
+    };
+
+    for (int step = 0; step < S.steps; ++step) {
+        const bool first = step == 0, last = step + 1 == S.steps;
+        // A = x x^T
+        if (warp == 0) {
+            if (elect_one()) {
+                for (int k = 0; k < width / 16; ++k) {
+                    const uint32_t at = x_at + ((k >> 2) * kSmallBlock + (k & 3) * 32 >> 4);
+                    mma_f16<1>(tmem, along | at, along | at, square, k > 0);
+                }
+                mma_commit<1>(bar);
+            }
+            __syncwarp();
+        }
+        finish();
+        const float alpha = kScaleA / (kScaleX * kScaleX) * (first ? kappa * kappa : 1.f);
+        {
+            uint32_t u[32];
+            tmem_load32(tmem + lanes + group * 32, u);
+            if (S.size == 1) {
+#pragma unroll
+                for (int c = 0; c < 32; c += 8) {
+                    uint4 h;
+                    uint32_t* w = &h.x;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        w[e] = pack2<false>(alpha * __uint_as_float(u[c + 2 * e]), alpha * __uint_as_float(u[c + 2 * e + 1]));
+                    *reinterpret_cast<uint4*>(A + small_at(row, group * 32 + c)) = h;
+                }
+            } else {
+                const int own = kSmallSide / S.size, to = row / own;
+                const uint32_t at = cluster_addr(
+                    smem_addr(shares + ((size_t)rank * own + row % own) * kSharePitch + group * 32), to);
+#pragma unroll
+                for (int c = 0; c < 32; c += 4) store_cluster16(at + c * 4, make_uint4(u[c], u[c + 1], u[c + 2], u[c + 3]));
+            }
+        }
+        if (S.size > 1) {
+            cluster_sync();
+            const int own = kSmallSide / S.size;
+            for (int n = threadIdx.x; n < own * (kSmallSide / 8); n += kSmallThreads) {
+                const int r = n / (kSmallSide / 8), c = n % (kSmallSide / 8) * 8;
+                float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                for (int s = 0; s < S.size; ++s) {
+                    const float4* p = reinterpret_cast<const float4*>(shares + ((size_t)s * own + r) * kSharePitch + c);
+                    const float4 l = p[0], h = p[1];
+                    v[0] += l.x, v[1] += l.y, v[2] += l.z, v[3] += l.w;
+                    v[4] += h.x, v[5] += h.y, v[6] += h.z, v[7] += h.w;
+                }
+                uint4 h;
+                uint32_t* w = &h.x;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[e] = pack2<false>(alpha * v[2 * e], alpha * v[2 * e + 1]);
+                const uint32_t at = smem_addr(A + small_at(rank * own + r, c));
+                for (int s = 0; s < S.size; ++s) store_cluster16(cluster_addr(at, s), h);
+            }
+            asm volatile("fence.proxy.async;" ::: "memory");
+            fence_before();
+            cluster_sync();
+            fence_after();
+        } else {
+            fence_async();
+            fence_before();
+            __syncthreads();
+            fence_after();
+        }
+        // B = b A + c A A (A is symmetric)
+        if (warp == 0) {
+            if (elect_one()) {
+                fence_async();
+#pragma unroll
+                for (int k = 0; k < kSmallSide / 16; ++k) {
+                    const uint32_t at = a_at + ((k >> 2) * kSmallBlock + (k & 3) * 32 >> 4);
+                    mma_f16<1>(tmem, along | at, along | at, square, k > 0);
+                }
+                mma_commit<1>(bar);
+            }
+            __syncwarp();
+        }
+        finish();
+        {
+            uint32_t u[32];
+            tmem_load32(tmem + lanes + group * 32, u);
+            const float beta = S.b, gamma = S.c / kScaleA;
+#pragma unroll
+            for (int c = 0; c < 32; c += 8) {
+                const uint32_t at = small_at(row, group * 32 + c);
+                float o[8];
+                unpack8(*reinterpret_cast<const uint4*>(A + at), false, o);
+                uint4 h;
+                uint32_t* w = &h.x;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    w[e] = pack2<false>(gamma * __uint_as_float(u[c + 2 * e]) + beta * o[2 * e],
+                                        gamma * __uint_as_float(u[c + 2 * e + 1]) + beta * o[2 * e + 1]);
+                *reinterpret_cast<uint4*>(B + at) = h;
+            }
+        }
+        fence_async();
+        fence_before();
+        __syncthreads();
+        fence_after();
+        // x <- a x + B x
+        if (warp == 0) {
+            if (elect_one()) {
+                for (int n = 0; n < width; n += 256) {
+                    const uint32_t idesc = mma_desc(false, false, true, kSmallSide, min(256, width - n));
+#pragma unroll
+                    for (int k = 0; k < kSmallSide / 16; ++k)
+                        mma_f16<1>(tmem + to_x + n, along | (b_at + ((k >> 2) * kSmallBlock + (k & 3) * 32 >> 4)),
+                                   across | (x_at + (n / 64 * kSmallBlock + k * 2048 >> 4)), idesc, k > 0);
+                }
+                mma_commit<1>(bar);
+            }
+            __syncwarp();
+        }
+        finish();
+        const float unscale = (last ? S.scale / kScaleX : 1.f) * (first ? kappa : 1.f);
+        const float beta = S.a * unscale, gamma = unscale / kScaleA;
+        for (int c0 = group * 32; c0 < width; c0 += 128) {
+            uint32_t u[32], w[16];
+            tmem_load32(tmem + lanes + to_x + c0, u);
+#pragma unroll
+            for (int c = 0; c < 32; c += 8) {
+                unsigned char* p = x + small_at(row, c0 + c);
+                float o[8];
+                unpack8(*reinterpret_cast<const uint4*>(p), false, o);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] = gamma * __uint_as_float(u[c + e]) + beta * o[e];
+                const bool bf = last && S.out_bf;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    w[c / 2 + e] = bf ? pack2<true>(o[2 * e], o[2 * e + 1]) : pack2<false>(o[2 * e], o[2 * e + 1]);
+                if (!last)
+                    *reinterpret_cast<uint4*>(p) = make_uint4(w[c / 2], w[c / 2 + 1], w[c / 2 + 2], w[c / 2 + 3]);
+            }
+            if (last && row < S.side) {
+                const int n = cols - c0;         // columns of this thread's 32 that exist
+                uint16_t* o = S.out + (int64_t)entry * S.bs_out;
+                if (S.tall) {
+                    o += (int64_t)(col0 + c0) * S.ld_out + row;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e, o += S.ld_out)
+                        if (e < n) *o = (uint16_t)(w[e / 2] >> (e & 1) * 16);
+                } else {
+                    o += row * S.ld_out + col0 + c0;
+                    if (S.vec_out && n >= 32) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            reinterpret_cast<uint4*>(o)[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (e < n) o[e] = (uint16_t)(w[e / 2] >> (e & 1) * 16);
+                    }
+                }
+            }
+        }
+        fence_async();
+        fence_before();
+        __syncthreads();
+        fence_after();
+    }
+    if (failed && threadIdx.x == 0) atomicCAS(&g_status[0], 0, (int)CCL_ERR_TIMEOUT);
+    if (S.size > 1) cluster_sync();     // nobody leaves while another may still write to it
+    if (warp == 1) tmem_free<1>(tmem, 512);
+}
+
+}  // namespace tensor
+}  // namespace ccl

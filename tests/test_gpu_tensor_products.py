@@ -129,6 +129,25 @@ def test_linear_writes_only_its_output(ccl):
         assert bool((whole[mask] == 9).all())
 
 
+def test_rows_far_apart(ccl):
+    """Row strides that take offsets past 32 bits (a slice of a long cache)."""
+    rows, stride = 40000, 60000
+    g = gen(31)
+    cache = torch.empty(rows * stride, dtype=torch.bfloat16, device="cuda")      # 4.8 GB
+    wide = cache.view(rows, stride)
+    x, out, r = wide[:, 8:72], wide[:, 1000:1040], wide[:, 5000:5040]
+    x.normal_(0, 1, generator=g)
+    r.normal_(0, 1, generator=g)
+    w = rnd(g, 40, 64, dtype=torch.bfloat16)
+    want = x.double() @ w.double().T + r.double()
+    ccl.linear(x, w, residual=r, out=out)
+    close(out, want, product_slack(x.double().abs() @ w.double().abs().T, 64) + 2.0 ** -22 * want.abs(), torch.bfloat16)
+    dy, z = wide[:, 5000:5040], wide[:, 1000:1040]
+    got = ccl.linear_backward(dy, x, w, preact=z, act=ccl.ACT_SILU, bias=True)
+    check_grads(got, dy, x, w, z, 3, [(0, rows)], torch.bfloat16)
+    del cache
+
+
 def test_linear_adds_to_the_residual_in_place(ccl):
     g = gen(7)
     x, w, r = rnd(g, 33, 64, dtype=torch.bfloat16), rnd(g, 200, 64, dtype=torch.bfloat16), rnd(g, 33, 200,
