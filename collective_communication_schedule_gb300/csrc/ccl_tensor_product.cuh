@@ -319,6 +319,33 @@ __device__ __forceinline__ void pack_block(const float v[kBlockRows], uint32_t w
     }
 }
 
+// A warp's blocks of a tile that is only scaled, biased and rounded, all by TMA
+// stores: most tiles of products without an activation.  The general way
+// through the epilogue takes twice the instructions.
+template <bool BF>
+__device__ __forceinline__ void plain_blocks(const CUtensorMap* map, uint32_t from, int first, int live, int stride,
+                                             float alpha, float bias, unsigned char* buf, int lane, int x, int y, int z)
+{
+    const uint32_t at = smem_addr(buf) + lane * 2;
+#pragma unroll 1
+    for (int c = first; c < live; c += stride) {
+        uint32_t u[kBlockRows];
+        tmem_load16(from + c, u);
+        if (lane == 0) tma_stores_read<0>();
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < kBlockRows; i += 2) {
+            const uint32_t w = pack2<BF>(fmaf(alpha, __uint_as_float(u[i]), bias), fmaf(alpha, __uint_as_float(u[i + 1]), bias));
+            asm volatile("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\t"
+                         "st.shared.b16 [%0], l;\n\tst.shared.b16 [%0 + 64], h;\n\t}" ::"r"(at + i * 64), "r"(w)
+                         : "memory");
+        }
+        fence_async();
+        __syncwarp();
+        if (lane == 0) tma_store(map, smem_addr(buf), x, y + c, z);
+    }
+}
+
 // FORM: storage of the operands (a pair: A_MN, then BOTH_MN)
 enum { BOTH_K = 0, A_MN = 1, BOTH_MN = 2 };
 
@@ -654,7 +681,17 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
                     if (!__all_sync(~0u, bar_wait<true>(smem_addr(&sh.taken), (round & 1) ^ 1, failed))) break;
                 }
                 const uint32_t from = tmem + ((uint32_t)(quad * 32) << 16) + acc * width;
-                for (int c = slot * kBlockRows; c < q.live; c += kStride) {
+                const bool plain = some && whole && P.tma_out && nfeat > 0 && !side && !(kLayer && (P.pre || P.act || size > CG)) &&
+                                   !(kAdds && P.c);
+                if (plain) {
+                    if (P.out_bf)
+                        plain_blocks<true>(&maps.mo, from, slot * kBlockRows, q.live, kStride, alpha, bias, st, lane, feat,
+                                           (int)row, zo);
+                    else
+                        plain_blocks<false>(&maps.mo, from, slot * kBlockRows, q.live, kStride, alpha, bias, st, lane, feat,
+                                            (int)row, zo);
+                }
+                for (int c = plain ? q.live : slot * kBlockRows; c < q.live; c += kStride) {
                     uint32_t u[kBlockRows];
                     if (some) {
                         tmem_load16(from + c, u);
