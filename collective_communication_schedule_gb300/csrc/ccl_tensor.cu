@@ -271,6 +271,8 @@ static ccl_status_t complete(const Device* dev, Product* P, const Shape& sh, con
         P->tma_pre = P->pre && vectors(P->pre, P->ld_pre, 0);
         if (P->tma_pre)
             TRY(encode(dev, &P->mp, Matrix{P->pre, P->n, P->m, P->ld_pre}, 32, kBlockRows, CU_TENSOR_MAP_SWIZZLE_NONE));
+        const bool pieces = P->c && vectors(P->c, P->ld_c, P->bs_c) && (P->m % 8 == 0 || P->pad_c);
+        P->fast = P->tma_out && !P->pre && !P->symmetric && (!P->c || (pieces && P->act == CCL_ACT_NONE));
     }
     return CCL_OK;
 }
@@ -664,6 +666,7 @@ static ccl_status_t orthogonalize(const ccl_ortho_t* a, char* base, int64_t* nee
             P.alpha = unscale / kScaleA;
             P.alpha_of = P.beta_of = first ? N.kappa : nullptr;
             set_c(&P, x[from].p, ldx, a->p * ldx, a->a * unscale);
+            P.pad_c = 1;
             if (last)
                 set_out(&P, a->out, ldo, so, a->out_dtype == CCL_BF16);
             else

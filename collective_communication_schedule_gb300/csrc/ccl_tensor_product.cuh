@@ -78,6 +78,8 @@ struct Scalars {
                                    // consecutive reduction elements
     int32_t tma_out, tma_pre;
     int32_t vec;                   // rows of out, pre, c and bias allow 16-byte accesses
+    int32_t pad_c;                 // rows of c are padded to multiples of 8 elements
+    int32_t fast;                  // fast_blocks() can take whole tiles
     float alpha, beta;
     const int32_t* offsets;
     uint16_t *out, *pre;           // pre: the sum before the activation (may be null)
@@ -319,30 +321,74 @@ __device__ __forceinline__ void pack_block(const float v[kBlockRows], uint32_t w
     }
 }
 
-// A warp's blocks of a tile that is only scaled, biased and rounded, all by TMA
-// stores: most tiles of products without an activation.  The general way
-// through the epilogue takes twice the instructions.
-template <bool BF>
-__device__ __forceinline__ void plain_blocks(const CUtensorMap* map, uint32_t from, int first, int live, int stride,
-                                             float alpha, float bias, unsigned char* buf, int lane, int x, int y, int z)
+// A warp's whole blocks of a tile whose outputs TMA can store (and whose C, if
+// any, can be read in pieces of 16 bytes), with what varies between products
+// decided beforehand: half the instructions of the general way.  C is read a
+// block ahead, two pieces of 8 features a lane, and turned through the block's
+// shared memory to a feature a lane.
+template <int ACT, bool ADD>
+__device__ __forceinline__ void fast_blocks(const Scalars& P, const CUtensorMap* map, uint32_t from, int first, int live,
+                                            int stride, float alpha, float bias, float beta, unsigned char* buf, int lane,
+                                            int x, int nfeat, int64_t row, int g, int z)
 {
-    const uint32_t at = smem_addr(buf) + lane * 2;
+    const uint32_t at = smem_addr(buf) + lane * 2, piece = smem_addr(buf) + lane * 16;
+    const bool out_bf = P.out_bf, in_bf = P.in_bf;
+    const uint16_t* pc = nullptr;
+    int64_t ld = 0;
+    uint4 c0, c1;
+    const int cr = lane >> 2, ck = (lane & 3) * 8;
+    auto fetch = [&](int c) {
+        c0 = c1 = make_uint4(0, 0, 0, 0);
+        if (ck < nfeat) {               // a piece that the matrix cuts short lies in its row's padding
+            const uint16_t* p = pc + c * ld;
+            if (c + cr < live) c0 = __ldcg(reinterpret_cast<const uint4*>(p));
+            if (c + cr + 8 < live) c1 = __ldcg(reinterpret_cast<const uint4*>(p + 8 * ld));
+        }
+    };
+    if (ADD) {
+        ld = P.ld_c;
+        pc = P.c + g * P.bs_c + (row + cr) * ld + x + ck;
+        fetch(first);
+    }
 #pragma unroll 1
     for (int c = first; c < live; c += stride) {
-        uint32_t u[kBlockRows];
-        tmem_load16(from + c, u);
+        float v[kBlockRows];
+        {
+            uint32_t u[kBlockRows];
+            tmem_load16(from + c, u);
+#pragma unroll
+            for (int i = 0; i < kBlockRows; ++i) v[i] = fmaf(alpha, __uint_as_float(u[i]), bias);
+        }
+        if (ACT) {
+#pragma unroll
+            for (int i = 0; i < kBlockRows; ++i) v[i] = activate(v[i], ACT);
+        }
         if (lane == 0) tma_stores_read<0>();
         __syncwarp();
-#pragma unroll
-        for (int i = 0; i < kBlockRows; i += 2) {
-            const uint32_t w = pack2<BF>(fmaf(alpha, __uint_as_float(u[i]), bias), fmaf(alpha, __uint_as_float(u[i + 1]), bias));
-            asm volatile("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\t"
-                         "st.shared.b16 [%0], l;\n\tst.shared.b16 [%0 + 64], h;\n\t}" ::"r"(at + i * 64), "r"(w)
+        if (ADD) {
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n\tst.shared.v4.b32 [%0 + 512], {%5, %6, %7, %8};" ::"r"(piece),
+                         "r"(c0.x), "r"(c0.y), "r"(c0.z), "r"(c0.w), "r"(c1.x), "r"(c1.y), "r"(c1.z), "r"(c1.w)
                          : "memory");
+            __syncwarp();
+            if (c + stride < live) fetch(c + stride);
+#pragma unroll
+            for (int i = 0; i < kBlockRows; ++i) {
+                uint16_t h;
+                asm volatile("ld.shared.b16 %0, [%1];" : "=h"(h) : "r"(at + i * 64));
+                v[i] += beta * (in_bf ? __uint_as_float((uint32_t)h << 16) : __half2float(__ushort_as_half(h)));
+            }
+            __syncwarp();
         }
+        uint32_t w[kBlockRows / 2];
+        pack_block(v, w, out_bf);
+#pragma unroll
+        for (int i = 0; i < kBlockRows; i += 2)
+            asm volatile("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\t"
+                         "st.shared.b16 [%0], l;\n\tst.shared.b16 [%0 + 64], h;\n\t}" ::"r"(at + i * 64), "r"(w[i / 2])
+                         : "memory");
         fence_async();
         __syncwarp();
-        if (lane == 0) tma_store(map, smem_addr(buf), x, y + c, z);
+        if (lane == 0) tma_store(map, smem_addr(buf), x, (int)row + c, z);
     }
 }
 
@@ -681,15 +727,25 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
                     if (!__all_sync(~0u, bar_wait<true>(smem_addr(&sh.taken), (round & 1) ^ 1, failed))) break;
                 }
                 const uint32_t from = tmem + ((uint32_t)(quad * 32) << 16) + acc * width;
-                const bool plain = some && whole && P.tma_out && nfeat > 0 && !side && !(kLayer && (P.pre || P.act || size > CG)) &&
-                                   !(kAdds && P.c);
+                const bool plain = some && whole && P.fast && nfeat > 0;
                 if (plain) {
-                    if (P.out_bf)
-                        plain_blocks<true>(&maps.mo, from, slot * kBlockRows, q.live, kStride, alpha, bias, st, lane, feat,
-                                           (int)row, zo);
-                    else
-                        plain_blocks<false>(&maps.mo, from, slot * kBlockRows, q.live, kStride, alpha, bias, st, lane, feat,
-                                            (int)row, zo);
+                    const int c = slot * kBlockRows;
+#define FAST(act, add)                                                                                                  \
+    fast_blocks<act, add>(P, &maps.mo, from, c, q.live, kStride, alpha, bias, beta, st, lane, feat, nfeat, row, q.g, zo)
+                    if (!kLayer) {
+                        FAST(ACT_NONE, false);
+                    } else if (P.c) {
+                        if (c < q.live) FAST(ACT_NONE, true);
+                    } else if (P.act == ACT_NONE) {
+                        FAST(ACT_NONE, false);
+                    } else if (P.act == ACT_RELU) {
+                        FAST(ACT_RELU, false);
+                    } else if (P.act == ACT_GELU) {
+                        FAST(ACT_GELU, false);
+                    } else {
+                        FAST(ACT_SILU, false);
+                    }
+#undef FAST
                 }
                 for (int c = plain ? q.live : slot * kBlockRows; c < q.live; c += kStride) {
                     uint32_t u[kBlockRows];
