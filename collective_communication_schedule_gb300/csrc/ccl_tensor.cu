@@ -272,8 +272,9 @@ static ccl_status_t complete(const Device* dev, Product* P, const Shape& sh, con
         if (P->tma_pre)
             TRY(encode(dev, &P->mp, Matrix{P->pre, P->n, P->m, P->ld_pre}, 32, kBlockRows, CU_TENSOR_MAP_SWIZZLE_NONE));
         const bool pieces = P->c && vectors(P->c, P->ld_c, P->bs_c) && (P->m % 8 == 0 || P->pad_c);
-        P->fast = P->tma_out && !P->pre && !P->symmetric && (!P->c || (pieces && P->act == CCL_ACT_NONE));
+        P->fast = P->tma_out && !P->pre && (!P->c || (pieces && P->act == CCL_ACT_NONE));
     }
+    if (P->symmetric && !P->fast) return fail(CCL_ERR_INTERNAL, "a symmetric product whose rows TMA cannot store");
     return CCL_OK;
 }
 
@@ -656,6 +657,7 @@ static ccl_status_t orthogonalize(const ccl_ortho_t* a, char* base, int64_t* nee
             P.symmetric = 1;
             P.alpha = a->c / kScaleA;
             set_c(&P, A.p, lda, r * lda, a->b);
+            P.pad_c = 1;
             set_out(&P, const_cast<void*>(B.p), lda, r * lda, false);
             s.a = s.b = &A;
         } else {

@@ -325,8 +325,11 @@ __device__ __forceinline__ void pack_block(const float v[kBlockRows], uint32_t w
 // any, can be read in pieces of 16 bytes), with what varies between products
 // decided beforehand: half the instructions of the general way.  C is read a
 // block ahead, two pieces of 8 features a lane, and turned through the block's
-// shared memory to a feature a lane.
-template <int ACT, bool ADD>
+// shared memory to a feature a lane.  SYM: a symmetric output, of which blocks
+// above the diagonal are left out, blocks that touch it are written as they are
+// (together they hold both sides of it: tiles start at multiples of 32), and
+// blocks below it are written with their mirror images.
+template <int ACT, bool ADD, bool SYM = false>
 __device__ __forceinline__ void fast_blocks(const Scalars& P, const CUtensorMap* map, uint32_t from, int first, int live,
                                             int stride, float alpha, float bias, float beta, unsigned char* buf, int lane,
                                             int x, int nfeat, int64_t row, int g, int z)
@@ -352,6 +355,11 @@ __device__ __forceinline__ void fast_blocks(const Scalars& P, const CUtensorMap*
     }
 #pragma unroll 1
     for (int c = first; c < live; c += stride) {
+        const int over = x + 31 - ((int)row + c);        // > 0 where the block reaches above the diagonal
+        if (SYM && over >= 31 + kBlockRows) {
+            if (ADD && c + stride < live) fetch(c + stride);
+            continue;
+        }
         float v[kBlockRows];
         {
             uint32_t u[kBlockRows];
@@ -389,6 +397,12 @@ __device__ __forceinline__ void fast_blocks(const Scalars& P, const CUtensorMap*
         fence_async();
         __syncwarp();
         if (lane == 0) tma_store(map, smem_addr(buf), x, (int)row + c, z);
+        if (SYM && over <= 0 && lane < nfeat) {
+            // a lane's 16 values are neighbours in the row of its feature; rows are padded to multiples of 8 (with zeros)
+            uint4* m = reinterpret_cast<uint4*>(P.out + g * P.bs_out + (int64_t)(x + lane) * P.ld_out + row + c);
+            m[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            if (c + 8 < live) m[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        }
     }
 }
 
@@ -481,7 +495,8 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
     // This threadblock's (cluster's) tiles of the next product: every
     // `clusters`-th one, so that tiles in flight at a time share operands
     // (ranges of consecutive tiles, balanced by their cost, took 168 us
-    // instead of 117 for 8190 rows over 32 experts of 4096 x 2048).  In a pair
+    // instead of 117 for 8190 rows over 32 experts of 4096 x 2048; row tiles of
+    // equal length changed nothing there: the weights' 440 MB bound it).  In a pair
     // the second product's go on where the first one's stopped.
     struct Run {
         int begin, end;
@@ -713,7 +728,7 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
                 const float alpha = P.alpha * (kAdds && P.alpha_of ? P.alpha_of[q.g] : 1.f);
                 const float beta = P.beta * (P.beta_of ? P.beta_of[q.g] : 1.f);
                 const float bias = kLayer && P.bias && f < P.m ? load1(P.bias + q.g * P.bs_bias + f, P.in_bf) : 0.f;
-                const bool whole = P.ragged != RAGGED_ROWS;    // TMA may cut rows off at the end of the matrix only
+                const bool whole = P.ragged != RAGGED_ROWS;
                 const int zo = P.ragged == RAGGED_ROWS ? 0 : q.g;
                 uint16_t cv[kBlockRows];
                 // C is read a block ahead of its use
@@ -727,15 +742,20 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
                     if (!__all_sync(~0u, bar_wait<true>(smem_addr(&sh.taken), (round & 1) ^ 1, failed))) break;
                 }
                 const uint32_t from = tmem + ((uint32_t)(quad * 32) << 16) + acc * width;
-                const bool plain = some && whole && P.fast && nfeat > 0;
-                if (plain) {
+                // rows that the short way takes: an expert's last rows may end inside a block, and TMA cuts rows off at
+                // the end of the matrix only
+                const int short_to = !(some && P.fast && nfeat > 0) ? 0 : whole ? q.live : q.live & -kBlockRows;
+                if (short_to) {
                     const int c = slot * kBlockRows;
-#define FAST(act, add)                                                                                                  \
-    fast_blocks<act, add>(P, &maps.mo, from, c, q.live, kStride, alpha, bias, beta, st, lane, feat, nfeat, row, q.g, zo)
-                    if (!kLayer) {
+#define FAST(...)                                                                                                       \
+    fast_blocks<__VA_ARGS__>(P, &maps.mo, from, c, short_to, kStride, alpha, bias, beta, st, lane, feat, nfeat, row, q.g, zo)
+                    if (kAdds && side) {
+                        if (P.c && c < short_to) FAST(ACT_NONE, true, true);
+                        if (!P.c) FAST(ACT_NONE, false, true);
+                    } else if (!kLayer) {
                         FAST(ACT_NONE, false);
                     } else if (P.c) {
-                        if (c < q.live) FAST(ACT_NONE, true);
+                        if (c < short_to) FAST(ACT_NONE, true);
                     } else if (P.act == ACT_NONE) {
                         FAST(ACT_NONE, false);
                     } else if (P.act == ACT_RELU) {
@@ -747,7 +767,8 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
                     }
 #undef FAST
                 }
-                for (int c = plain ? q.live : slot * kBlockRows; c < q.live; c += kStride) {
+                for (int c = slot * kBlockRows; c < q.live; c += kStride) {
+                    if (c < short_to) continue;
                     uint32_t u[kBlockRows];
                     if (some) {
                         tmem_load16(from + c, u);
@@ -799,20 +820,9 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
                         }
                         if (c + kStride < q.live) fetch_c(P, cv, q.g, row + c + kStride, nrows - kStride, f);
                     }
-                    // Symmetric outputs: blocks above the diagonal are left out, blocks that touch it are written as
-                    // they are (together they hold both sides of it: tiles start at multiples of 32), blocks below
-                    // it are written with their mirror images.
-                    const int over = feat + 31 - (q.n0 + c);      // > 0 where the block reaches above the diagonal
-                    if (side && over >= 31 + kBlockRows) continue;
                     pack_block(v, w, P.out_bf);
                     store_block(&maps.mo, P.out + q.g * P.bs_out + (row + c) * P.ld_out + f, P.ld_out, w, st,
                                 P.tma_out && (whole || nrows >= kBlockRows), lane, feat, (int)row + c, zo, nrows, nfeat);
-                    if (side && over <= 0 && lane < nfeat) {
-                        // a lane's 16 values are neighbours in row f; rows are padded to multiples of 8 (with zeros)
-                        uint4* m = reinterpret_cast<uint4*>(P.out + q.g * P.bs_out + (int64_t)f * P.ld_out + q.n0 + c);
-                        m[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                        if (nrows > 8) m[1] = make_uint4(w[4], w[5], w[6], w[7]);
-                    }
                 }
                 if (some) {
                     fence_before();
