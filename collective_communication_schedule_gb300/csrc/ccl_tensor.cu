@@ -431,6 +431,7 @@ static ccl_status_t linear_grad(const ccl_linear_grad_t* a, char* base, int64_t*
     if (!a->dw_stride) sdw = a->n * lddw;
     TRY(stride("db expert", a->db_stride, a->n, &sdb));
     const int64_t count = a->experts > 0 ? a->experts : 1;
+    if (a->n > 256 * 65535) return fail(CCL_ERR_UNSUPPORTED, "ccl_linear_grad: n above " + std::to_string(256 * 65535));
     if (!need) {
         const bool some = a->rows > 0;
         TRY(pointer("dy", a->dy, some));

@@ -222,8 +222,10 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_ortho_kernel(const __g
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         failed = 0;
     }
-    if (warp == 1) tmem_alloc<1>(smem_addr(&tmem_slot), 512);
-    let_next_in();
+    if (warp == 1) {
+        tmem_alloc<1>(smem_addr(&tmem_slot), 512);
+        let_next_in();              // not before: the next kernel could take the tensor memory and wait for this one
+    }
     wait_for_previous();
 
     // 8 columns j.. of row i of g (or of its transpose)

@@ -469,7 +469,6 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
         tma_prefetch(&seq.at(0).ma);
         tma_prefetch(&seq.at(0).mb);
     }
-    let_next_in();
     if (seq.at(0).offsets) wait_for_previous();
     prepare_tiles(seq.at(0), &sh);
     if (MODE == PAIR && threadIdx.x == 0) {
@@ -481,10 +480,15 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
     else
         __syncthreads();
     volatile int* failed = &sh.failed;
-    // loads start while tensor memory is being allocated; everything up to
-    // here overlaps the end of the kernel before this one
+    // Loads start while tensor memory is being allocated; everything up to
+    // here overlaps the end of the kernel before this one.  The next kernel is
+    // let in only when this one holds its tensor memory: it could otherwise
+    // take it first and wait for this one to end.
     uint32_t tmem = 0;
-    if (warp == 2) tmem_alloc<CG>(smem_addr(&sh.tmem), tcols);
+    if (warp == 2) {
+        tmem_alloc<CG>(smem_addr(&sh.tmem), tcols);
+        let_next_in();
+    }
     if (warp != 0 && warp != 3) {
         fence_before();
         named_sync(1, 64 + 32 * kEpilogueWarps);

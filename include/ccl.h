@@ -812,9 +812,11 @@ typedef struct {
  *   x <- a x + (b A + c A A) x;   out = scale * x
  * (x^T x on the other side for p > q, which is the same matrix).  g is f32,
  * bf16 or f16; out (may be g where type and strides agree) is bf16 or f16.
- * Intermediate matrices are f16 with fixed power-of-two scales, which holds
- * for coefficients that keep the singular values of x below 8 and the
- * entries of b A + c A A below 63 in magnitude.
+ * The norm is summed in 32 bits (|g|_F below 1.8e19).  Intermediate matrices
+ * are f16 with fixed power-of-two scales (bf16 loses 8 times as much: 2 % of
+ * the update's norm where f16 is within 0.3 %), which holds for coefficients
+ * that keep the singular values of x below 8 and the entries of b A + c A A
+ * below 63 in magnitude.
  */
 typedef struct {
     int64_t batch, p, q;
