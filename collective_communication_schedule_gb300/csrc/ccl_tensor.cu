@@ -191,14 +191,16 @@ struct Shape {
 // and of its epilogue, and never less than DRAM takes for the operands.  The
 // constants are fits to measured times (bf16, 1.9 GHz, 4096 x 4096 x 4096
 // unless noted).  Per 64 reduction elements: pairs 620, 540, 378 and 278
-// clocks for 256, 192, 128 and 64 rows; single threadblocks 864, 476 and 300
-// for 256, 128 and 64; no SM gets more than about 68 bytes a clock from L2,
-// all together 8000.  An exchange of shares costs about 5000 clocks and 60 per
-// row (1 x 4096 x 4096: 15.1, 12.9, 11.7 and 19 us cut in 1, 2, 4 and 8; x x^T
-// of 1024 x 4096: 40 us more when cut in 4), and clusters of 4 and 8 leave SMs
-// unused.
+// clocks for 256, 192, 128 and 64 rows; single threadblocks 476 and 300 for
+// 128 and 64; no SM gets more than about 68 bytes a clock from L2, all
+// together 8000.  Widths between the powers of two fit the waves: 4096 x 4096
+// x 4096 takes 78 us in tiles of 224 rows (four whole waves), 81 of 256, 88 of
+// 192.  An exchange of shares costs about 5000 clocks and 60 per row (1 x 4096
+// x 4096: 15.1, 12.9, 11.7 and 19 us cut in 1, 2, 4 and 8; x x^T of 1024 x
+// 4096: 40 us more when cut in 4), and clusters of 4 and 8 leave SMs unused.
 struct Choices {
-    Shape best, single, pairs;     // of all; of single threadblocks without a split; of pairs
+    Shape best;                    // of all
+    Shape single, pairs;           // beside another product in one launch: of single threadblocks, of pairs
 };
 
 static Choices choose(const Product& P, int sms)
@@ -212,19 +214,20 @@ static Choices choose(const Product& P, int sms)
     Choices c = {};
     for (int cg = 1; cg <= 2; ++cg) {
         const int64_t tiles_m = (P.m + (int64_t)cg * kTileM - 1) / (cg * kTileM);
-        for (int bn : {256, 192, 128, 64, 32}) {
+        // single threadblocks lose to pairs on wide tiles: only what few rows want
+        for (int bn = cg == 2 ? 256 : 128; bn >= 32; bn = cg == 2 ? bn - 32 : bn / 2) {
             const int unit = P.b_mn ? 64 * cg : 32;       // rows are loaded 64 at a time where they are consecutive
-            if (bn % unit || (bn > unit && bn / 2 >= rows)) continue;
+            if (bn % unit || (bn > unit && bn - unit >= rows)) continue;
             const int64_t tiles_n = (rows + bn - 1) / bn;
             const int64_t tiles = P.symmetric ? groups * (tiles_m * tiles_n + std::max(tiles_m, tiles_n)) / 2
                                               : groups * tiles_m * tiles_n;
             const double bytes = (kTileM + bn / cg) * 128.0;
             const double busy = (double)std::min<int64_t>(tiles * cg, sms);
             const double block = 400 + 16.0 * std::min<int64_t>(bn, rows);
-            for (int split = 1; split <= (cg == 2 || bn > 128 || P.symmetric ? 1 : 8); split *= 2) {
+            for (int split = 1; split <= (cg == 2 || P.symmetric ? 1 : 8); split *= 2) {
                 if (split > 1 && (split * 2 > slices || tiles * split > 2 * sms)) break;
-                const double slice = std::max({cg == 2 ? 150 + 1.85 * bn : 130 + 2.8 * bn, bytes / 68,
-                                               bytes * std::min<double>(sms, busy * split) / 8000});
+                const double slice = std::max(std::max(cg == 2 ? 150 + 1.85 * bn : 130 + 2.8 * bn, bytes / 68),
+                                              bytes * std::min<double>(sms, busy * split) / 8000);
                 const double main = (double)((slices + split - 1) / split) * 2 * slice;
                 const double epilogue = split == 1 ? block : 400 + (block - 400) / split + 5000 + 60.0 * std::min<int64_t>(bn, rows);
                 const int places = cg == 2 ? sms / 2 : split == 4 ? sms / 4 - 2 : split == 8 ? sms / 8 - 3 : sms / split;
@@ -232,8 +235,11 @@ static Choices choose(const Product& P, int sms)
                                     std::min(main, epilogue);
                 const Shape s = {cg, bn, split, std::max(cost, least) + 0.1 * cost};
                 if (c.best.cg == 0 || s.cost < c.best.cost) c.best = s;
+                if (split > 1) continue;
+                // beside another product whole waves do not matter
+                const double beside = std::max(1.0, (double)tiles / places) * std::max(main, epilogue);
                 Shape& own = cg == 1 ? c.single : c.pairs;
-                if (split == 1 && (own.cg == 0 || s.cost < own.cost)) own = s;
+                if (own.cg == 0 || beside < own.cost) own = {cg, bn, 1, beside};
             }
         }
     }

@@ -47,12 +47,13 @@ namespace tensor {
 //     whole warps in the issuing loops keep addresses in uniform registers.
 //   few rows: DRAM and the start of a launch; 1 x 4096 x 4096 (33.6 MB) 11 us,
 //     37 x 8192 x 2048 11 us, 24 rows over 64 experts of 2048 x 1024 19 us.
-//   short reductions: the epilogue, about 8000 clocks for 256 x 256 outputs
-//     (4096 x 4096 outputs of 512 products each: 22 us); sixteen warps, since
-//     eight took 1.3 times as long.
-//   between: whole waves of tiles (4096 x 4096 x 4096: 83 us where four waves
-//     of 256 x 256 tiles hold 3.4), rows that start off a cache line (a
-//     128-byte row of a tile then costs two: 30 % more at k = 2056).
+//   short reductions: the epilogue, about 5000 clocks for 256 x 256 outputs
+//     that are only rounded (4096 x 4096 outputs of 64 products each: 15 us),
+//     twice that with an activation or a residual (22 and 24 us); sixteen warps,
+//     since eight took 1.3 times as long.
+//   between: whole waves of tiles (4096 x 4096 x 4096: 78 us, 1750 TFLOP/s),
+//     rows that start off a cache line (a 128-byte row of a tile then costs
+//     two: 1001 x 5000 takes 30 us at k = 2056, 21 at 2048).
 // ======================================================================
 constexpr int kTileM = 128;
 constexpr int kSliceK = 128;      // reduction elements per stage: two swizzled rows of 64, or 128 rows
