@@ -587,7 +587,9 @@ static ccl_status_t orthogonalize(const ccl_ortho_t* a, char* base, int64_t* nee
     N.kappa = ws.take<float>(a->batch * 4);
     N.kappa2 = ws.take<float>(a->batch * 4);
     if (need) {
-        *need = small ? 0 : ws.used;
+        // by the sizes alone: the small kernel leaves it unused, but which
+        // kernel runs is no part of what a caller has to know
+        *need = ws.used;
         return CCL_OK;
     }
     if (a->batch == 0) return CCL_OK;
