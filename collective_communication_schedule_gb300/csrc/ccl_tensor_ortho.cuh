@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(256) scale_kernel(const NormPass N)
 // size rows, in rank order, and hands them to all), the rest of the step
 // stays within a threadblock.  A tall matrix is transposed as it is loaded
 // and stored.  Bound by the latency of 3 x steps products in a row: 128 x 128 in
-// 19 us, 2.3 us a step; one launch per product took 87 us.
+// 19 us, 2.65 us a step; one launch per product took 87 us.
 //
 // Rows of 64 elements (128 bytes) in 1024-byte atoms of 8 rows, 16-byte pieces
 // exchanged by the row's index: element (i, j) of x is at piece (j / 8 % 8) ^

@@ -53,7 +53,7 @@ namespace tensor {
 //     since eight took 1.3 times as long.
 //   between: whole waves of tiles (4096 x 4096 x 4096: 78 us, 1750 TFLOP/s),
 //     rows that start off a cache line (a 128-byte row of a tile then costs
-//     two: 1001 x 5000 takes 30 us at k = 2056, 21 at 2048).
+//     two: 1001 x 5003 takes 30 us at k = 2056, 24 at 2048).
 // ======================================================================
 constexpr int kTileM = 128;
 constexpr int kSliceK = 128;      // reduction elements per stage: two swizzled rows of 64, or 128 rows
