@@ -569,7 +569,7 @@ static ccl_status_t orthogonalize(const ccl_ortho_t* a, char* base, int64_t* nee
     // holds up to 384 columns, or 256 beside the others' shares of A
     const int64_t longer = std::max(a->p, a->q);
     int size = 1;
-    while (size < 8 && longer > (size == 1 ? 384 : 256 * size)) size *= 2;
+    while (size < kSmallCluster && longer > (size == 1 ? 384 : 256 * size)) size *= 2;
     const bool small = r <= kSmallSide && longer <= (size == 1 ? 384 : 256 * size);
     Arena ws = {base};
     Matrix x[2], A, B;
@@ -613,6 +613,8 @@ static ccl_status_t orthogonalize(const ccl_ortho_t* a, char* base, int64_t* nee
         S.size = size;
         S.width = (int32_t)round_up((longer + size - 1) / size, 64);
         S.vec_out = vectors(a->out, ldo, so);
+        const int64_t each = a->dtype == CCL_F32 ? 4 : 8;      // elements of 16 bytes
+        S.vec_g = aligned16(a->g) && ldg % each == 0 && sg % each == 0;
         S.a = a->a;
         S.b = a->b;
         S.c = a->c;

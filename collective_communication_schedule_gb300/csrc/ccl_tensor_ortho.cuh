@@ -167,11 +167,12 @@ __global__ void __launch_bounds__(256) scale_kernel(const NormPass N)
 // the matrix instructions read, accumulators in tensor memory, and a step is
 // three products with a threadblock barrier after each.  A long side is cut
 // over the threadblocks of a cluster, `width` columns of x each: they add up
-// their parts of A = x x^T through distributed shared memory (each sums 128 /
-// size rows, in rank order, and hands them to all), the rest of the step
-// stays within a threadblock.  A tall matrix is transposed as it is loaded
+// their parts of A = x x^T through distributed shared memory (each reads 128 /
+// size rows of all, sums them in rank order, and hands them to all: 128 x 1024
+// in 45 us, 53 when the parts were pushed from the accumulators, where a
+// store of a warp went to 32 rows), the rest of the step stays within a threadblock.  A tall matrix is transposed as it is loaded
 // and stored.  Bound by the latency of 3 x steps products in a row: 128 x 128 in
-// 19 us, 2.65 us a step; one launch per product took 87 us.
+// 18 us, 2.5 us a step; one launch per product took 87 us.
 //
 // Rows of 64 elements (128 bytes) in 1024-byte atoms of 8 rows, 16-byte pieces
 // exchanged by the row's index: element (i, j) of x is at piece (j / 8 % 8) ^
@@ -179,6 +180,7 @@ __global__ void __launch_bounds__(256) scale_kernel(const NormPass N)
 // along its columns (x x^T) and along its rows (B x).
 constexpr int kSmallSide = 128;
 constexpr int kSmallThreads = 512;
+constexpr int kSmallCluster = 8;
 constexpr int kSmallBlock = kSmallSide * 128;          // bytes of a block of 64 columns
 constexpr int kSharePitch = kSmallSide + 4;            // floats; rows 4 banks apart
 
@@ -188,7 +190,7 @@ struct Small {
     int64_t ld_g, bs_g, ld_out, bs_out;
     int32_t side, length;          // short and long side
     int32_t tall, type, out_bf, steps;
-    int32_t size, width, vec_out;
+    int32_t size, width, vec_g, vec_out;
     float a, b, c, eps, scale;
 };
 
@@ -197,10 +199,83 @@ __device__ __forceinline__ uint32_t small_at(int i, int j)
     return (uint32_t)(j >> 6) * kSmallBlock + i * 128 + (((j >> 3) & 7) ^ (i & 7)) * 16;
 }
 
-__device__ __forceinline__ void store_cluster16(uint32_t addr, uint4 v)
+__device__ __forceinline__ void store_cluster8(uint32_t addr, uint2 v)
 {
-    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+    asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(v.x), "r"(v.y) : "memory");
+}
+
+__device__ __forceinline__ float4 load_cluster16(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
                  : "memory");
+    return v;
+}
+
+// use(i, j, v) for the pieces of 8 columns j.. of row i of a threadblock's part
+// of g (or of its transpose), zeros outside of it.  Neighbouring threads take
+// neighbouring elements in memory.  Four pieces are loaded before the first is
+// used: TYPE and the way of loading are settled outside of the loops, or each
+// piece would wait for the one before.
+template <int TYPE, class Use>
+__device__ __forceinline__ void small_pieces(const Small& S, int64_t base, int col0, int cols, Use use)
+{
+    const int pieces = S.width / 8, items = pieces * kSmallSide;
+    auto element = [&](int i, int j) {
+        const int64_t at = S.tall ? base + (int64_t)(col0 + j) * S.ld_g + i : base + i * S.ld_g + col0 + j;
+        return load_any(S.g, at, TYPE);
+    };
+    const bool vector = !S.tall && S.vec_g;
+    for (int n0 = threadIdx.x; n0 < items; n0 += 4 * kSmallThreads) {
+        float v[4][8];
+        int row[4], col[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int n = n0 + u * kSmallThreads;
+            row[u] = S.tall ? n % kSmallSide : n / pieces;
+            col[u] = S.tall ? n / kSmallSide * 8 : n % pieces * 8;
+        }
+        if (vector) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const bool in = row[u] < S.side;
+                if (in && col[u] + 8 <= cols) {
+                    load_any8(S.g, base + row[u] * S.ld_g + col0 + col[u], TYPE, v[u]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[u][e] = in && col[u] + e < cols ? element(row[u], col[u] + e) : 0.f;
+                }
+            }
+        } else {
+            // the last element stands in for those outside
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[u][e] = cols > 0 ? element(min(row[u], S.side - 1), min(col[u] + e, cols - 1)) : 0.f;
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (row[u] >= S.side || col[u] + e >= cols) v[u][e] = 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (n0 + u * kSmallThreads < items) use(row[u], col[u], v[u]);
+    }
+}
+
+template <class Use>
+__device__ __forceinline__ void small_pieces_of(const Small& S, int64_t base, int col0, int cols, Use use)
+{
+    if (S.type == CCL_F32)
+        small_pieces<CCL_F32>(S, base, col0, cols, use);
+    else if (S.type == CCL_BF16)
+        small_pieces<CCL_BF16>(S, base, col0, cols, use);
+    else
+        small_pieces<CCL_F16>(S, base, col0, cols, use);
 }
 
 __global__ void __launch_bounds__(kSmallThreads, 1) small_ortho_kernel(const __grid_constant__ Small S)
@@ -208,14 +283,14 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_ortho_kernel(const __g
     __shared__ __align__(8) uint64_t done;
     __shared__ uint32_t tmem_slot;
     __shared__ int failed;
-    __shared__ float sm[16], norms[8];
+    __shared__ float sm[16], norms[kSmallCluster];
     extern __shared__ unsigned char raw[];
     unsigned char* dyn = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = warp & 3, group = warp >> 2;
     const int rank = S.size > 1 ? (int)cluster_rank() : 0, entry = blockIdx.x / S.size;
     const int width = S.width, col0 = rank * width, cols = max(0, min(width, S.length - col0));
     unsigned char *x = dyn, *A = x + (size_t)width / 64 * kSmallBlock, *B = A + 2 * kSmallBlock;
-    float* shares = reinterpret_cast<float*>(B + 2 * kSmallBlock);   // size > 1: [source][own row][column of A]
+    float* share = reinterpret_cast<float*>(B + 2 * kSmallBlock);   // size > 1: this threadblock's part of A
     const uint32_t bar = smem_addr(&done);
     if (threadIdx.x == 0) {
         bar_init(bar, 1);
@@ -228,46 +303,14 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_ortho_kernel(const __g
     }
     wait_for_previous();
 
-    // 8 columns j.. of row i of g (or of its transpose)
     const int64_t base = (int64_t)entry * S.bs_g;
-    auto fetch = [&](int i, int j, float v[8]) {
-        if (i >= S.side || j >= cols) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = 0.f;
-        } else if (S.tall) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                v[e] = j + e < cols ? load_any(S.g, base + (int64_t)(col0 + j + e) * S.ld_g + i, S.type) : 0.f;
-        } else if (j + 8 <= cols) {
-            load_any8(S.g, base + i * S.ld_g + col0 + j, S.type, v);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                v[e] = j + e < cols ? load_any(S.g, base + i * S.ld_g + col0 + j + e, S.type) : 0.f;
-        }
-    };
-    // neighbouring threads take neighbouring elements in memory
-    const int pieces = width / 8, items = pieces * kSmallSide;
-    auto place = [&](int n, int& i, int& j) {
-        if (S.tall) {
-            i = n % kSmallSide;
-            j = n / kSmallSide * 8;
-        } else {
-            i = n / pieces;
-            j = n % pieces * 8;
-        }
-    };
     float sum = 0.f;
-#pragma unroll 2
-    for (int n = threadIdx.x; n < items; n += kSmallThreads) {
-        int i, j;
-        place(n, i, j);
-        float v[8], t = 0.f;
-        fetch(i, j, v);
+    small_pieces_of(S, base, col0, cols, [&](int, int, const float v[8]) {
+        float t = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) t = fmaf(v[e], v[e], t);
         sum += t;
-    }
+    });
     sum = block_sum(sum, sm);
     if (S.size > 1) {
         cluster_sync();            // the others' shared memory is live from here on
@@ -278,18 +321,13 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_ortho_kernel(const __g
     }
     float kappa, f1, f2;
     norm_scale(sum, S.eps, kappa, f1, f2);
-#pragma unroll 2
-    for (int n = threadIdx.x; n < items; n += kSmallThreads) {
-        int i, j;
-        place(n, i, j);
-        float v[8];
-        fetch(i, j, v);
+    small_pieces_of(S, base, col0, cols, [&](int i, int j, const float v[8]) {
         uint4 u;
         uint32_t* w = &u.x;
 #pragma unroll
         for (int e = 0; e < 4; ++e) w[e] = pack2<false>(v[2 * e] * f1 * f2, v[2 * e + 1] * f1 * f2);
         *reinterpret_cast<uint4*>(x + small_at(i, j)) = u;
-    }
+    });
     fence_async();
     fence_before();
     __syncthreads();
@@ -338,31 +376,29 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_ortho_kernel(const __g
                     *reinterpret_cast<uint4*>(A + small_at(row, group * 32 + c)) = h;
                 }
             } else {
-                const int own = kSmallSide / S.size, to = row / own;
-                const uint32_t at = cluster_addr(
-                    smem_addr(shares + ((size_t)rank * own + row % own) * kSharePitch + group * 32), to);
+                float* at = share + row * kSharePitch + group * 32;
 #pragma unroll
-                for (int c = 0; c < 32; c += 4) store_cluster16(at + c * 4, make_uint4(u[c], u[c + 1], u[c + 2], u[c + 3]));
+                for (int c = 0; c < 32; c += 4)
+                    *reinterpret_cast<uint4*>(at + c) = make_uint4(u[c], u[c + 1], u[c + 2], u[c + 3]);
             }
         }
         if (S.size > 1) {
             cluster_sync();
             const int own = kSmallSide / S.size;
-            for (int n = threadIdx.x; n < own * (kSmallSide / 8); n += kSmallThreads) {
-                const int r = n / (kSmallSide / 8), c = n % (kSmallSide / 8) * 8;
-                float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                for (int s = 0; s < S.size; ++s) {
-                    const float4* p = reinterpret_cast<const float4*>(shares + ((size_t)s * own + r) * kSharePitch + c);
-                    const float4 l = p[0], h = p[1];
-                    v[0] += l.x, v[1] += l.y, v[2] += l.z, v[3] += l.w;
-                    v[4] += h.x, v[5] += h.y, v[6] += h.z, v[7] += h.w;
-                }
-                uint4 h;
-                uint32_t* w = &h.x;
+            for (int n = threadIdx.x; n < own * (kSmallSide / 4); n += kSmallThreads) {
+                const int r = rank * own + n / (kSmallSide / 4), c = n % (kSmallSide / 4) * 4;
+                const uint32_t from = smem_addr(share + r * kSharePitch + c), at = smem_addr(A + small_at(r, c)) + (c & 4) * 2;
+                float4 p[kSmallCluster], v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) w[e] = pack2<false>(alpha * v[2 * e], alpha * v[2 * e + 1]);
-                const uint32_t at = smem_addr(A + small_at(rank * own + r, c));
-                for (int s = 0; s < S.size; ++s) store_cluster16(cluster_addr(at, s), h);
+                for (int i = 0; i < kSmallCluster; ++i)
+                    if (i < S.size) p[i] = load_cluster16(cluster_addr(from, i));
+#pragma unroll
+                for (int i = 0; i < kSmallCluster; ++i)
+                    if (i < S.size) v.x += p[i].x, v.y += p[i].y, v.z += p[i].z, v.w += p[i].w;
+                const uint2 h = {pack2<false>(alpha * v.x, alpha * v.y), pack2<false>(alpha * v.z, alpha * v.w)};
+#pragma unroll
+                for (int i = 0; i < kSmallCluster; ++i)
+                    if (i < S.size) store_cluster8(cluster_addr(at, i), h);
             }
             asm volatile("fence.proxy.async;" ::: "memory");
             fence_before();
@@ -441,35 +477,35 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_ortho_kernel(const __g
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     w[c / 2 + e] = bf ? pack2<true>(o[2 * e], o[2 * e + 1]) : pack2<false>(o[2 * e], o[2 * e + 1]);
-                if (!last)
+                if (!last || !S.tall)
                     *reinterpret_cast<uint4*>(p) = make_uint4(w[c / 2], w[c / 2 + 1], w[c / 2 + 2], w[c / 2 + 3]);
             }
-            if (last && row < S.side) {
+            if (last && S.tall && row < S.side) {
                 const int n = cols - c0;         // columns of this thread's 32 that exist
-                uint16_t* o = S.out + (int64_t)entry * S.bs_out;
-                if (S.tall) {
-                    o += (int64_t)(col0 + c0) * S.ld_out + row;
+                uint16_t* o = S.out + (int64_t)entry * S.bs_out + (int64_t)(col0 + c0) * S.ld_out + row;
 #pragma unroll
-                    for (int e = 0; e < 32; ++e, o += S.ld_out)
-                        if (e < n) *o = (uint16_t)(w[e / 2] >> (e & 1) * 16);
-                } else {
-                    o += row * S.ld_out + col0 + c0;
-                    if (S.vec_out && n >= 32) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            reinterpret_cast<uint4*>(o)[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (e < n) o[e] = (uint16_t)(w[e / 2] >> (e & 1) * 16);
-                    }
-                }
+                for (int e = 0; e < 32; ++e, o += S.ld_out)
+                    if (e < n) *o = (uint16_t)(w[e / 2] >> (e & 1) * 16);
             }
         }
         fence_async();
         fence_before();
         __syncthreads();
         fence_after();
+    }
+    if (!S.tall && cols > 0) {
+        // out of shared memory along the rows: from the accumulators, a store of
+        // a warp would touch 32 rows (with the batched loads: 128 x 385 in 52 us, 82 before)
+        uint16_t* o = S.out + (int64_t)entry * S.bs_out + col0;
+        const int whole = S.vec_out ? cols / 8 : 0, rest = cols - whole * 8;
+        for (int n = threadIdx.x; n < whole * S.side; n += kSmallThreads) {
+            const int i = n / whole, j = n % whole * 8;
+            *reinterpret_cast<uint4*>(o + i * S.ld_out + j) = *reinterpret_cast<const uint4*>(x + small_at(i, j));
+        }
+        for (int n = threadIdx.x; n < rest * S.side; n += kSmallThreads) {
+            const int i = n / rest, j = whole * 8 + n % rest;
+            o[i * S.ld_out + j] = reinterpret_cast<const uint16_t*>(x + small_at(i, j))[j & 7];
+        }
     }
     if (failed && threadIdx.x == 0) atomicCAS(&g_status[0], 0, (int)CCL_ERR_TIMEOUT);
     if (S.size > 1) cluster_sync();     // nobody leaves while another may still write to it
