@@ -50,8 +50,19 @@ static void (*const kKernels[2][3])(Product) = {
 struct Device {
     bool ready = false;
     int sms = 0;
+    int small_clusters[5] = {};    // of 2^i threadblocks of the small orthogonalisation kernel that run at once
     EncodeFn encode = nullptr;
 };
+
+// the small orthogonalisation kernel for `size` threadblocks a matrix, and its shared memory
+static void (*small_kernel(int size))(Small)
+{
+    return size == 1 ? small_ortho_kernel<1> : size <= 8 ? small_ortho_kernel<8> : small_ortho_kernel<16>;
+}
+static size_t small_smem(int size, int width)
+{
+    return 1024 + (size_t)width / 64 * kSmallBlock + 4 * kSmallBlock + (size > 1 ? (size_t)kSmallSide * kSharePitch * 4 : 0);
+}
 
 static ccl_status_t device(const Device** out)
 {
@@ -76,8 +87,26 @@ static ccl_status_t device(const Device** out)
         for (auto kernel : {pair_kernel<1>, pair_kernel<2>})
             TRY_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBudget),
                      "shared memory of the pair kernel");
-        TRY_CUDA(cudaFuncSetAttribute(small_ortho_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBudget),
-                 "shared memory of the small orthogonalisation kernel");
+        for (auto kernel : {small_ortho_kernel<1>, small_ortho_kernel<8>, small_ortho_kernel<16>})
+            TRY_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBudget),
+                     "shared memory of the small orthogonalisation kernel");
+        TRY_CUDA(cudaFuncSetAttribute(small_ortho_kernel<16>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1),
+                 "clusters of 16 of the small orthogonalisation kernel");
+        all[d].small_clusters[0] = all[d].sms;
+        for (int i = 1; 1 << i <= kSmallCluster; ++i) {
+            cudaLaunchConfig_t cfg = {};
+            cudaLaunchAttribute at;
+            at.id = cudaLaunchAttributeClusterDimension;
+            at.val.clusterDim.x = 1u << i;
+            at.val.clusterDim.y = at.val.clusterDim.z = 1;
+            cfg.gridDim = dim3(1u << i);
+            cfg.blockDim = dim3(kSmallThreads);
+            cfg.dynamicSmemBytes = small_smem(1 << i, 256);
+            cfg.attrs = &at;
+            cfg.numAttrs = 1;
+            TRY_CUDA(cudaOccupancyMaxActiveClusters(&all[d].small_clusters[i], small_kernel(1 << i), &cfg),
+                     "clusters of the small orthogonalisation kernel");
+        }
         all[d].ready = true;
     }
     *out = &all[d];
@@ -565,12 +594,6 @@ static ccl_status_t orthogonalize(const ccl_ortho_t* a, char* base, int64_t* nee
     if (!a->out_stride) so = a->p * ldo;
     const int64_t r = std::min(a->p, a->q);
     const bool tall = a->p > a->q;
-    // threadblocks that a matrix with a short side of up to 128 takes: each
-    // holds up to 384 columns, or 256 beside the others' shares of A
-    const int64_t longer = std::max(a->p, a->q);
-    int size = 1;
-    while (size < kSmallCluster && longer > (size == 1 ? 384 : 256 * size)) size *= 2;
-    const bool small = r <= kSmallSide && longer <= (size == 1 ? 384 : 256 * size);
     Arena ws = {base};
     Matrix x[2], A, B;
     // rows start on cache lines: a 128-byte row of a tile would touch two of them otherwise
@@ -596,6 +619,26 @@ static ccl_status_t orthogonalize(const ccl_ortho_t* a, char* base, int64_t* nee
     if (!a->g || !a->out) return fail(CCL_ERR_INVALID_ARG, who + "null matrix");
     if ((uintptr_t)a->g % (a->dtype == CCL_F32 ? 4 : 2) || (uintptr_t)a->out % 2)
         return fail(CCL_ERR_INVALID_ARG, who + "a matrix is not aligned to its elements");
+    const Device* dev = nullptr;
+    TRY(device(&dev));
+    // Threadblocks that a matrix with a short side of up to 128 takes: each
+    // holds up to 384 columns, or 256 beside its part of A.
+    const int64_t longer = std::max(a->p, a->q);
+    int log = 0;
+    while (1 << log < kSmallCluster && longer > (log == 0 ? 384 : 256 << log)) ++log;
+    const int size = 1 << log, at_once = dev->small_clusters[log];
+    bool small = r <= kSmallSide && longer <= (log == 0 ? 384 : 256 << log) && at_once > 0;
+    if (small && size > 1) {
+        // A matrix holds `size` SMs for all of its steps, so a large batch goes
+        // around several times, while one launch per product fills the machine.
+        // Fits in us to five steps, small against general: 128 x 4096 56 and 120,
+        // batch 64 576 and 441; 24 x 4096 batch 16 157 and 155, batch 64 519 and
+        // 284; 32 x 700 batch 64 99 and 115, batch 128 193 and 152; 128 x 2048
+        // batch 32 155 and 176, batch 128 496 and 429; 128 x 1024 batch 256 387
+        // and 452.  Single threadblocks always win (128 x 384 batch 512: 151, 438).
+        const float kilo = longer / 1024.f, rounds = (float)((a->batch + at_once - 1) / at_once);
+        small = rounds * (46.f + 4.f * kilo) < 75.f + 12.f * kilo + a->batch * kilo * (0.56f + 0.0067f * r);
+    }
     if (small) {
         Small S = {};
         S.g = a->g;
@@ -620,11 +663,8 @@ static ccl_status_t orthogonalize(const ccl_ortho_t* a, char* base, int64_t* nee
         S.c = a->c;
         S.eps = a->eps;
         S.scale = a->scale;
-        const Device* dev = nullptr;
-        TRY(device(&dev));
-        const size_t smem = 1024 + (size_t)S.width / 64 * kSmallBlock + 4 * kSmallBlock +
-                            (size > 1 ? (size_t)kSmallSide * kSharePitch * 4 : 0);
-        return launch(small_ortho_kernel, dim3((unsigned)(a->batch * size)), kSmallThreads, smem, stream, S, size);
+        return launch(small_kernel(size), dim3((unsigned)(a->batch * size)), kSmallThreads, small_smem(size, S.width), stream,
+                      S, size);
     }
     N.g = a->g;
     N.x = (__half*)x[0].p;
@@ -690,8 +730,6 @@ static ccl_status_t orthogonalize(const ccl_ortho_t* a, char* base, int64_t* nee
         }
         return s;
     };
-    const Device* dev = nullptr;
-    TRY(device(&dev));
     Shape shapes[3];
     for (int kind = 0; kind < 3; ++kind) shapes[kind] = choose(product(kind, 0, false, false).p, dev->sms).best;
     for (int i = 0; i < 3 * a->steps; ++i) {

@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(256) scale_kernel(const NormPass N)
 // along its columns (x x^T) and along its rows (B x).
 constexpr int kSmallSide = 128;
 constexpr int kSmallThreads = 512;
-constexpr int kSmallCluster = 8;
+constexpr int kSmallCluster = 16;
 constexpr int kSmallBlock = kSmallSide * 128;          // bytes of a block of 64 columns
 constexpr int kSharePitch = kSmallSide + 4;            // floats; rows 4 banks apart
 
@@ -278,6 +278,9 @@ __device__ __forceinline__ void small_pieces_of(const Small& S, int64_t base, in
         small_pieces<CCL_F16>(S, base, col0, cols, use);
 }
 
+// MOST: threadblocks of a matrix at most -- 1, 8 (2, 4 or 8 of them) or 16
+// (always 16); one kernel for all took 1 us longer for one and 3 us for 16.
+template <int MOST>
 __global__ void __launch_bounds__(kSmallThreads, 1) small_ortho_kernel(const __grid_constant__ Small S)
 {
     __shared__ __align__(8) uint64_t done;
@@ -286,8 +289,9 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_ortho_kernel(const __g
     __shared__ float sm[16], norms[kSmallCluster];
     extern __shared__ unsigned char raw[];
     unsigned char* dyn = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
+    const int size = MOST == 8 ? S.size : MOST;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = warp & 3, group = warp >> 2;
-    const int rank = S.size > 1 ? (int)cluster_rank() : 0, entry = blockIdx.x / S.size;
+    const int rank = MOST > 1 ? (int)cluster_rank() : 0, entry = blockIdx.x / size;
     const int width = S.width, col0 = rank * width, cols = max(0, min(width, S.length - col0));
     unsigned char *x = dyn, *A = x + (size_t)width / 64 * kSmallBlock, *B = A + 2 * kSmallBlock;
     float* share = reinterpret_cast<float*>(B + 2 * kSmallBlock);   // size > 1: this threadblock's part of A
@@ -312,12 +316,12 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_ortho_kernel(const __g
         sum += t;
     });
     sum = block_sum(sum, sm);
-    if (S.size > 1) {
+    if constexpr (MOST > 1) {
         cluster_sync();            // the others' shared memory is live from here on
-        if ((int)threadIdx.x < S.size) store_cluster(cluster_addr(smem_addr(&norms[rank]), threadIdx.x), sum);
+        if ((int)threadIdx.x < size) store_cluster(cluster_addr(smem_addr(&norms[rank]), threadIdx.x), sum);
         cluster_sync();
         sum = 0.f;
-        for (int i = 0; i < S.size; ++i) sum += norms[i];
+        for (int i = 0; i < size; ++i) sum += norms[i];
     }
     float kappa, f1, f2;
     norm_scale(sum, S.eps, kappa, f1, f2);
@@ -365,7 +369,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_ortho_kernel(const __g
         {
             uint32_t u[32];
             tmem_load32(tmem + lanes + group * 32, u);
-            if (S.size == 1) {
+            if constexpr (MOST == 1) {
 #pragma unroll
                 for (int c = 0; c < 32; c += 8) {
                     uint4 h;
@@ -382,23 +386,32 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_ortho_kernel(const __g
                     *reinterpret_cast<uint4*>(at + c) = make_uint4(u[c], u[c + 1], u[c + 2], u[c + 3]);
             }
         }
-        if (S.size > 1) {
+        if constexpr (MOST > 1) {
             cluster_sync();
-            const int own = kSmallSide / S.size;
+            const int own = kSmallSide / size;
             for (int n = threadIdx.x; n < own * (kSmallSide / 4); n += kSmallThreads) {
                 const int r = rank * own + n / (kSmallSide / 4), c = n % (kSmallSide / 4) * 4;
                 const uint32_t from = smem_addr(share + r * kSharePitch + c), at = smem_addr(A + small_at(r, c)) + (c & 4) * 2;
-                float4 p[kSmallCluster], v = {0.f, 0.f, 0.f, 0.f};
+                float4 v = {0.f, 0.f, 0.f, 0.f};
+                auto gather = [&](int first_rank) {
+                    float4 p[8];
 #pragma unroll
-                for (int i = 0; i < kSmallCluster; ++i)
-                    if (i < S.size) p[i] = load_cluster16(cluster_addr(from, i));
+                    for (int i = 0; i < 8; ++i)
+                        if (first_rank + i < size) p[i] = load_cluster16(cluster_addr(from, first_rank + i));
 #pragma unroll
-                for (int i = 0; i < kSmallCluster; ++i)
-                    if (i < S.size) v.x += p[i].x, v.y += p[i].y, v.z += p[i].z, v.w += p[i].w;
+                    for (int i = 0; i < 8; ++i)
+                        if (first_rank + i < size) v.x += p[i].x, v.y += p[i].y, v.z += p[i].z, v.w += p[i].w;
+                };
+                gather(0);
+                if constexpr (MOST > 8) gather(8);
                 const uint2 h = {pack2<false>(alpha * v.x, alpha * v.y), pack2<false>(alpha * v.z, alpha * v.w)};
+                auto hand_out = [&](int first_rank) {
 #pragma unroll
-                for (int i = 0; i < kSmallCluster; ++i)
-                    if (i < S.size) store_cluster8(cluster_addr(at, i), h);
+                    for (int i = 0; i < 8; ++i)
+                        if (first_rank + i < size) store_cluster8(cluster_addr(at, first_rank + i), h);
+                };
+                hand_out(0);
+                if constexpr (MOST > 8) hand_out(8);
             }
             asm volatile("fence.proxy.async;" ::: "memory");
             fence_before();
@@ -508,7 +521,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_ortho_kernel(const __g
         }
     }
     if (failed && threadIdx.x == 0) atomicCAS(&g_status[0], 0, (int)CCL_ERR_TIMEOUT);
-    if (S.size > 1) cluster_sync();     // nobody leaves while another may still write to it
+    if constexpr (MOST > 1) cluster_sync();     // nobody leaves while another may still write to it
     if (warp == 1) tmem_free<1>(tmem, 512);
 }
 

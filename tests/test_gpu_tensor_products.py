@@ -425,6 +425,41 @@ def test_orthogonalize_with_a_short_side(ccl, shape):
         assert rel <= 8e-3, rel
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32], ids=["bf16", "f16", "f32"])
+@pytest.mark.parametrize("shape", [(1, 128, 2049), (1, 4096, 128), (2, 77, 3333), (1, 3001, 5), (1, 128, 4097), (9, 16, 4095),
+                                   (33, 40, 2500), (150, 24, 700)])
+def test_orthogonalize_with_a_long_side_and_in_batches(ccl, shape, dtype):
+    """The largest clusters, and batches that go around them or leave them to
+    the general products; same tolerance as above."""
+    g = rnd(gen(sum(shape)), *shape, dtype=torch.float32).mul_(0.1).to(dtype)
+    out = ccl.orthogonalize(g)
+    ccl.tensor_status()
+    assert torch.equal(out, ccl.orthogonalize(g))
+    for i in {0, shape[0] // 2, shape[0] - 1}:
+        want = ns64(g[i].double(), 5, MUON)
+        rel = ((out[i].double() - want).norm() / want.norm()).item()
+        assert rel <= 8e-3, rel
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32], ids=["bf16", "f16", "f32"])
+@pytest.mark.parametrize("p,q", [(128, 385), (65, 130), (127, 1001), (385, 7), (3, 2047), (90, 64)])
+def test_orthogonalize_loads_the_same_from_any_alignment(ccl, p, q, dtype):
+    """Rows on 16-byte boundaries and off them, and in place, with nothing but
+    NaN around the matrix: the same bits."""
+    g = rnd(gen(p + q), p, q, dtype=torch.float32).to(dtype)
+    want = ccl.orthogonalize(g, out=torch.empty(p, q, dtype=torch.bfloat16, device="cuda"))
+    for lead, pitch in ((8, -(-q // 8) * 8 + 16), (1, q + 1), (3, q + 7)):
+        held = torch.full((p + 2, pitch + lead), float("nan"), dtype=dtype, device="cuda")
+        view = held[1:-1, lead:lead + q]
+        view.copy_(g)
+        assert torch.equal(ccl.orthogonalize(view), want)
+        if dtype == torch.bfloat16:
+            ccl.orthogonalize(view, out=view)
+            assert torch.equal(view, want)
+            held[1:-1, lead:lead + q] = float("nan")
+            assert bool(held.isnan().all())
+
+
 def test_orthogonalize_options(ccl):
     g = rnd(gen(3), 96, 160, dtype=torch.float32)
     cubic = (1.5, -0.5, 0.0)
