@@ -735,9 +735,13 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
                 const float bias = kLayer && P.bias && f < P.m ? load1(P.bias + q.g * P.bs_bias + f, P.in_bf) : 0.f;
                 const bool whole = P.ragged != RAGGED_ROWS;
                 const int zo = P.ragged == RAGGED_ROWS ? 0 : q.g;
+                // rows that the short way takes: an expert's last rows may end inside a block, and TMA cuts rows off at
+                // the end of the matrix only
+                const int short_to = !(some && P.fast && nfeat > 0) ? 0 : whole ? q.live : q.live & -kBlockRows;
+                int c = slot * kBlockRows;          // this warp's next block
                 uint16_t cv[kBlockRows];
-                // C is read a block ahead of its use
-                if (kAdds && P.c && size == CG) fetch_c(P, cv, q.g, row + slot * kBlockRows, q.live - slot * kBlockRows, f);
+                // the general way reads C a block ahead of its use, the short way reads it by itself
+                if (kAdds && P.c && size == CG && !short_to) fetch_c(P, cv, q.g, row + c, q.live - c, f);
                 if (some) {
                     if (!__all_sync(~0u, bar_wait(smem_addr(&sh.acc_full[acc]), (done >> 1) & 1, failed))) break;
                     fence_after();
@@ -747,11 +751,7 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
                     if (!__all_sync(~0u, bar_wait<true>(smem_addr(&sh.taken), (round & 1) ^ 1, failed))) break;
                 }
                 const uint32_t from = tmem + ((uint32_t)(quad * 32) << 16) + acc * width;
-                // rows that the short way takes: an expert's last rows may end inside a block, and TMA cuts rows off at
-                // the end of the matrix only
-                const int short_to = !(some && P.fast && nfeat > 0) ? 0 : whole ? q.live : q.live & -kBlockRows;
                 if (short_to) {
-                    const int c = slot * kBlockRows;
 #define FAST(...)                                                                                                       \
     fast_blocks<__VA_ARGS__>(P, &maps.mo, from, c, short_to, kStride, alpha, bias, beta, st, lane, feat, nfeat, row, q.g, zo)
                     if (kAdds && side) {
@@ -771,9 +771,10 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
                         FAST(ACT_SILU, false);
                     }
 #undef FAST
+                    while (c < short_to) c += kStride;
+                    if (kAdds && P.c && c < q.live) fetch_c(P, cv, q.g, row + c, q.live - c, f);
                 }
-                for (int c = slot * kBlockRows; c < q.live; c += kStride) {
-                    if (c < short_to) continue;
+                for (; c < q.live; c += kStride) {
                     uint32_t u[kBlockRows];
                     if (some) {
                         tmem_load16(from + c, u);

@@ -513,3 +513,45 @@ def test_results_repeat_bit_for_bit_on_other_streams_and_in_graphs(ccl):
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(want, held))
+
+
+# ---------------------------------------------- experts through the C entry
+def c_call(ccl, name, args):
+    """A call of the C interface with the workspace it asks for, on the current stream."""
+    import ctypes
+    size = ctypes.c_int64()
+    fail = getattr(ccl.lib, name + "_workspace")(ctypes.byref(args), ctypes.byref(size))
+    assert fail == 0, ccl.lib.ccl_last_error_detail().decode()
+    ws = torch.empty(max(size.value, 1), dtype=torch.uint8, device="cuda")
+    fail = getattr(ccl.lib, name)(ctypes.byref(args), ws.data_ptr(), size.value, torch.cuda.current_stream().cuda_stream)
+    assert fail == 0, ccl.lib.ccl_last_error_detail().decode()
+
+
+@pytest.mark.parametrize("in_place", [False, True], ids=["apart", "in place"])
+@pytest.mark.parametrize("dtype", DT, ids=["bf16", "f16"])
+@pytest.mark.parametrize("counts", [[100], [70, 0, 65, 300, 255, 129, 97], [250, 17, 1], [68] * 12, [5, 16, 0, 33]],
+                         ids=lambda c: f"{len(c)}x{sum(c)}")
+@pytest.mark.parametrize("n,k,act", [(136, 64, 0), (1024, 264, 0), (131, 72, 0), (136, 64, 2)])
+def test_experts_with_a_residual(ccl, n, k, act, counts, dtype, in_place):
+    """Every row gets its own row of the residual, also the last rows of an
+    expert whose tile does not end with a block of 16."""
+    first, tail = 3, 4          # rows before and after the experts' own
+    offs = offsets_of(counts, first)
+    rows, e = offs[-1] + tail, len(counts)
+    g = gen(rows + n)
+    x, w = rnd(g, rows, k, dtype=dtype), rnd(g, e, n, k, dtype=dtype, scale=k ** -0.5)
+    r = rnd(g, rows, n, dtype=dtype, scale=4.0)
+    o = torch.tensor(offs, dtype=torch.int32, device="cuda")
+    out = r.clone() if in_place else torch.full((rows, n), 5.0, dtype=dtype, device="cuda")
+    before = out.clone()
+    c_call(ccl, "ccl_linear", ccl.Linear(
+        rows=rows, n=n, k=k, dtype=ccl.BF16 if dtype == torch.bfloat16 else ccl.F16, act=act, experts=e, x=x.data_ptr(),
+        w=w.data_ptr(), residual=(out if in_place else r).data_ptr(), offsets=o.data_ptr(), y=out.data_ptr()))
+    ccl.tensor_status()
+    assert torch.equal(out[:first], before[:first]) and torch.equal(out[offs[-1]:], before[offs[-1]:])
+    for i in range(e):
+        s = slice(offs[i], offs[i + 1])
+        z = x[s].double() @ w[i].double().T
+        want = act64(z, act) + r[s].double()
+        slack = 1.13 * product_slack(x[s].double().abs() @ w[i].double().abs().T, k) + 2.0 ** -16 * z.abs()
+        close(out[s], want, slack + 2.0 ** -22 * (z.abs() + want.abs()), dtype)
