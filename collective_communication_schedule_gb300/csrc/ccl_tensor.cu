@@ -5,6 +5,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <string>
 
@@ -390,6 +391,12 @@ static ccl_status_t pointer(const char* what, const void* p, bool needed)
     return CCL_OK;
 }
 
+// Whether an output that is asked for starts where one of these does.
+static bool same(const void* out, std::initializer_list<const void*> others)
+{
+    return out && std::find(others.begin(), others.end(), out) != others.end();
+}
+
 static ccl_status_t linear(const ccl_linear_t* a, char* base, int64_t* need, cudaStream_t stream)
 {
     if (!a) return fail(CCL_ERR_INVALID_ARG, "ccl_linear: null arguments");
@@ -476,8 +483,12 @@ static ccl_status_t linear_grad(const ccl_linear_grad_t* a, char* base, int64_t*
         TRY(pointer("dx", a->dx, false));
         TRY(pointer("dw", a->dw, false));
         TRY(pointer("db", a->db, false));
-        if ((a->dx && (a->dx == a->dy || a->dx == a->w)) || (a->dw && (a->dw == a->dy || a->dw == a->x)))
+        // the two products and the bias gradient run at one time: none may write what another one reads
+        const void *x_read = a->dw ? a->x : nullptr, *w_read = a->dx ? a->w : nullptr;
+        if (same(a->dx, {a->dy, a->w, x_read}) || same(a->dw, {a->dy, a->x, w_read}) || same(a->db, {a->dy, x_read, w_read}))
             return fail(CCL_ERR_INVALID_ARG, "ccl_linear_grad: an output is also an operand");
+        if (same(a->dx, {a->dw, a->db}) || same(a->dw, {a->db}))
+            return fail(CCL_ERR_INVALID_ARG, "ccl_linear_grad: an output is also another output");
         if (!some) {
             if (a->dw)
                 for (int64_t e = 0; e < count; ++e)

@@ -792,7 +792,9 @@ typedef struct {
  * The gradient of the residual is dy itself.  z is needed when act is not
  * CCL_ACT_NONE.  dx, dw, db may be null (not computed; then w, x are not
  * read).  dz is rounded to the element type between the two products, as z
- * and y are between layers; db sums it unrounded.
+ * and y are between layers; db sums it unrounded.  The outputs are computed
+ * side by side: none may overlap another one or dy, nor x where dw is asked
+ * for, nor w where dx is (matrices that start at one address are refused).
  */
 typedef struct {
     int64_t rows, n, k;

@@ -132,3 +132,18 @@ def test_python_refusals():
                  lambda: ccl.linear_backward(x, x, w, act=ccl.ACT_GELU), lambda: ccl.orthogonalize(x[0])):
         with pytest.raises(ValueError):
             call()
+
+
+@pytest.mark.parametrize("a", [
+    grad(dx=2 * A),                              # over x, which dw reads
+    grad(dw=3 * A),                              # over w, which dx reads
+    grad(dx=6 * A, dw=6 * A),
+    grad(db=A), grad(db=2 * A), grad(db=3 * A), grad(db=4 * A), grad(db=5 * A),
+    grad(act=ccl.ACT_GELU, z=6 * A, dx=2 * A),
+    grad(experts=2, offsets=7 * A, dw=3 * A),
+    grad(x=2 * A + 2, dx=2 * A + 2),             # copied to the workspace first, but refused all the same
+], ids=range(11))
+def test_gradients_over_operands_are_refused(a):
+    """The two products run at one time: neither may write what the other reads."""
+    assert code("ccl_linear_grad", a) == INVALID
+    assert "also" in ccl.lib.ccl_last_error_detail().decode()
