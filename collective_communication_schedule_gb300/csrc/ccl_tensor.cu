@@ -421,8 +421,11 @@ static ccl_status_t linear(const ccl_linear_t* a, char* base, int64_t* need, cud
         TRY(pointer("z", a->z, false));
         TRY(pointer("bias", a->bias, false));
         TRY(pointer("residual", a->residual, false));
-        if (some && (a->y == a->x || a->y == a->w || (a->z && a->z == a->y)))
-            return fail(CCL_ERR_INVALID_ARG, "ccl_linear: an output is also an operand");
+        if (some && (same(a->y, {a->x, a->w, a->bias, a->z}) || same(a->z, {a->x, a->w, a->bias, a->residual})))
+            return fail(CCL_ERR_INVALID_ARG, "ccl_linear: an output is also an operand or another output");
+        // in place, a row of y may be written while the rows after it are read
+        if (a->rows > 1 && same(a->y, {a->residual}) && ldr != ldy)
+            return fail(CCL_ERR_INVALID_ARG, "ccl_linear: y over a residual of another row stride");
         if (!some) return CCL_OK;
     }
     if (need) {

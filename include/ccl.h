@@ -770,7 +770,8 @@ ccl_status_t ccl_schedule_read_json(const char* path, ccl_schedule_t* out);
  *     vectors bias_stride apart.
  * bias, residual (rows x n) and z (output, rows x n, the values before the
  * activation, for the backward pass) may be null.  y may be residual (same
- * stride), no other operand.
+ * stride); otherwise neither y nor z may overlap the other or an operand
+ * (matrices that start at one address are refused).
  */
 typedef struct {
     int64_t rows, n, k;

@@ -147,3 +147,16 @@ def test_gradients_over_operands_are_refused(a):
     """The two products run at one time: neither may write what the other reads."""
     assert code("ccl_linear_grad", a) == INVALID
     assert "also" in ccl.lib.ccl_last_error_detail().decode()
+
+
+@pytest.mark.parametrize("a", [
+    linear(z=A), linear(z=2 * A), linear(z=3 * A),
+    linear(residual=4 * A, z=4 * A),                          # z is stored before the residual is read
+    linear(bias=4 * A, z=4 * A), linear(bias=3 * A),
+    linear(residual=3 * A, ldr=24),                           # y over a residual with other strides
+    linear(residual=3 * A, ldy=24),
+    linear(experts=2, offsets=5 * A, residual=4 * A, z=4 * A),
+], ids=range(9))
+def test_products_over_operands_are_refused(a):
+    assert code("ccl_linear", a) == INVALID
+    assert "operand" in ccl.lib.ccl_last_error_detail().decode() or "stride" in ccl.lib.ccl_last_error_detail().decode()
