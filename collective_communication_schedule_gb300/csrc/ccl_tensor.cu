@@ -633,6 +633,10 @@ static ccl_status_t orthogonalize(const ccl_ortho_t* a, char* base, int64_t* nee
     if (!a->g || !a->out) return fail(CCL_ERR_INVALID_ARG, who + "null matrix");
     if ((uintptr_t)a->g % (a->dtype == CCL_F32 ? 4 : 2) || (uintptr_t)a->out % 2)
         return fail(CCL_ERR_INVALID_ARG, who + "a matrix is not aligned to its elements");
+    // a matrix of a batch is written while others may not have been read: in
+    // place each must stay within its own bytes
+    if (a->out == a->g && a->batch > 1 && (a->dtype == CCL_F32 || sg != so))
+        return fail(CCL_ERR_INVALID_ARG, who + "in place with another element size or matrix stride");
     const Device* dev = nullptr;
     TRY(device(&dev));
     // Threadblocks that a matrix with a short side of up to 128 takes: each

@@ -814,7 +814,8 @@ typedef struct {
  *   x = g / (|g|_F + eps);  `steps` times:  A = x x^T,
  *   x <- a x + (b A + c A A) x;   out = scale * x
  * (x^T x on the other side for p > q, which is the same matrix).  g is f32,
- * bf16 or f16; out (may be g where type and strides agree) is bf16 or f16.
+ * bf16 or f16; out is bf16 or f16, and may be g: in a batch only where the
+ * elements have the same size and the matrices the same stride.
  * The norm is summed in 32 bits (|g|_F below 1.8e19).  Intermediate matrices
  * are f16 with fixed power-of-two scales (bf16 loses 8 times as much: 1.1 % of
  * the update's norm on Gaussian matrices where f16 loses 0.13 %, 1.8 and 0.22 %

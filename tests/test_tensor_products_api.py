@@ -160,3 +160,13 @@ def test_gradients_over_operands_are_refused(a):
 def test_products_over_operands_are_refused(a):
     assert code("ccl_linear", a) == INVALID
     assert "operand" in ccl.lib.ccl_last_error_detail().decode() or "stride" in ccl.lib.ccl_last_error_detail().decode()
+
+
+@pytest.mark.parametrize("a", [ortho(batch=2, out=A),                                    # f32 over bf16: matrices apart
+                               ortho(batch=2, dtype=ccl.BF16, out=A, out_stride=1024),
+                               ortho(batch=3, dtype=ccl.F16, out=A, ldg=40),
+                               ortho(batch=2, p=64, q=5000, dtype=ccl.F32, out=A)], ids=range(4))
+def test_updates_over_gradients_of_other_strides_are_refused(a):
+    """A matrix may be written while another one of the batch is read."""
+    assert code("ccl_orthogonalize", a) == INVALID
+    assert "in place" in ccl.lib.ccl_last_error_detail().decode()
