@@ -377,6 +377,9 @@ __device__ __forceinline__ float activate(float z, int act)
 __device__ __forceinline__ float activate_grad(float z, int act)
 {
     if (act == ACT_RELU) return z > 0.f ? 1.f : 0.f;
+    // both slopes are 0 or 1 in 32 bits beyond 100; limiting z there (NaN passes) keeps
+    // 0 x Inf out of the terms below: z z overflows from 1.8e19 on, a kept z may be Inf
+    z = z > 100.f ? 100.f : z < -100.f ? -100.f : z;
     if (act == ACT_SILU) {
         const float s = sigmoid(z);
         return s * (1.f + z * (1.f - s));

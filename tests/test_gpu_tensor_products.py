@@ -555,3 +555,22 @@ def test_experts_with_a_residual(ccl, n, k, act, counts, dtype, in_place):
         want = act64(z, act) + r[s].double()
         slack = 1.13 * product_slack(x[s].double().abs() @ w[i].double().abs().T, k) + 2.0 ** -16 * z.abs()
         close(out[s], want, slack + 2.0 ** -22 * (z.abs() + want.abs()), dtype)
+
+
+@pytest.mark.parametrize("dtype", DT, ids=["bf16", "f16"])
+@pytest.mark.parametrize("act", [2, 3])
+def test_activation_gradients_at_the_ends_of_the_range(ccl, act, dtype):
+    """The slope is 0 far below zero and 1 far above, up to the largest finite
+    value and at the infinities that a kept z can overflow to; NaN stays."""
+    big = [100.0, 1000.0, 6e4] + ([1e10, 1.8e19, 2e19, 1e30, 3e38] if dtype == torch.bfloat16 else []) + [float("inf")]
+    z = torch.tensor([[-v for v in big] + big + [float("nan")]], dtype=dtype, device="cuda")
+    want = torch.tensor([[0.0] * len(big) + [1.0] * len(big)], dtype=dtype, device="cuda")
+    n = z.shape[1]
+    one, x = torch.ones_like(z), torch.ones(1, 8, dtype=dtype, device="cuda")
+    dx, dw, db = ccl.linear_backward(one, x, torch.ones(n, 8, dtype=dtype, device="cuda"), preact=z, act=act, bias=True)
+    assert torch.equal(db[None, :-1], want) and bool(db[-1].isnan())
+    assert torch.equal(dw[:-1], want.T.expand(-1, 8)) and bool(dw[-1].isnan().all())
+    for i in range(n - 1):          # an element's own product
+        dx, _, _ = ccl.linear_backward(one[:, :1], x, torch.ones(1, 8, dtype=dtype, device="cuda"), preact=z[:, i:i + 1],
+                                       act=act, need_dw=False)
+        assert bool((dx == want[0, i]).all()), z[0, i]
