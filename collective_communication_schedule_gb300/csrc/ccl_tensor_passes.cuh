@@ -168,7 +168,8 @@ __global__ void __launch_bounds__(256) bias_grad_kernel(const GradPass G)
     }
 }
 
-// Sum a bias gradient's chunks, 32 columns of one expert at a time.
+// The same sums in the same order beside the products of a pair, 32 columns of
+// one expert at a time.
 __device__ __noinline__ void add_chunks(const GradPass& G, int lane)
 {
     const int columns = (G.n + 31) / 32;
@@ -179,10 +180,17 @@ __device__ __noinline__ void add_chunks(const GradPass& G, int lane)
         if (c >= G.n) continue;
         const int chunks = (len + kGradRows - 1) / kGradRows;
         const float* p = G.partial + chunk_base(G, e, lo) * G.ld_part + c;
-        float s = 0.f;
-#pragma unroll 8
-        for (int i = 0; i < chunks; ++i) s += p[i * G.ld_part];
-        store1(G.db + e * G.bs_db + c, s, G.bf);
+        float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        int i = 0;
+        for (; i + 8 <= chunks; i += 8)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s[j] += p[(i + j) * G.ld_part];
+#pragma unroll
+        for (int j = 0; j < 7; ++j)
+            if (i + j < chunks) s[j] += p[(i + j) * G.ld_part];
+#pragma unroll
+        for (int j = 1; j < 8; ++j) s[0] += s[j];
+        store1(G.db + e * G.bs_db + c, s[0], G.bf);
     }
 }
 

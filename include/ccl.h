@@ -747,7 +747,8 @@ ccl_status_t ccl_schedule_read_json(const char* path, ccl_schedule_t* out);
  * Any stride and alignment is accepted; operands whose base or row stride is
  * no multiple of 16 bytes are first copied into the workspace.  Sums are
  * held in 32 bits and rounded once per output; the order of every sum is
- * fixed by the sizes, so equal calls give equal bits.
+ * fixed by the sizes (for dx and dw also by whether both are asked for), so
+ * equal calls give equal bits.
  * ====================================================================== */
 
 /* Activations.  GELU is the tanh form, 0.5 z (1 + tanh(sqrt(2/pi) (z +

@@ -574,3 +574,30 @@ def test_activation_gradients_at_the_ends_of_the_range(ccl, act, dtype):
         dx, _, _ = ccl.linear_backward(one[:, :1], x, torch.ones(1, 8, dtype=dtype, device="cuda"), preact=z[:, i:i + 1],
                                        act=act, need_dw=False)
         assert bool((dx == want[0, i]).all()), z[0, i]
+
+
+@pytest.mark.parametrize("counts", [None, [600, 0, 2400, 514, 66]], ids=["dense", "experts"])
+@pytest.mark.parametrize("n,k", [(200, 136), (131, 72), (520, 264)])
+def test_bias_gradient_does_not_depend_on_what_else_is_asked(ccl, n, k, counts):
+    """Many chunks of rows, whose sums cancel but for the roundings of the
+    additions: what is left shows the order, which the sizes alone give."""
+    rows, dt = 3580, torch.bfloat16
+    g = gen(rows + n)
+    dy, x = rnd(g, rows, n, dtype=dt), rnd(g, rows, k, dtype=dt)
+    offs = offsets_of(counts or [rows])
+    for i, j in zip(offs[:-1], offs[1:]):
+        dy[(i + j) // 2:j] = -dy[i:(i + j) // 2]
+    if counts:
+        w = rnd(g, len(counts), n, k, dtype=dt)
+        o = torch.tensor(offs, dtype=torch.int32, device="cuda")
+
+        def call(**kw):
+            return ccl.grouped_linear_backward(dy, x, w, o, bias=True, **kw)[2]
+    else:
+        w = rnd(g, n, k, dtype=dt)
+
+        def call(**kw):
+            return ccl.linear_backward(dy, x, w, bias=True, **kw)[2]
+    want = call()
+    for dx, dw in ((0, 0), (1, 0), (0, 1)):
+        assert torch.equal(call(need_dx=bool(dx), need_dw=bool(dw)), want), (dx, dw)
