@@ -501,12 +501,14 @@ static ccl_status_t linear_grad(const ccl_linear_grad_t* a, char* base, int64_t*
             return CCL_OK;
         }
     }
-    // dz: dy itself where there is no activation and TMA can read it
-    const bool own_dz = a->act != CCL_ACT_NONE || !aligned16(a->dy) || lddy % 8 != 0;
+    if (!a->dx && !a->dw && !a->db) {
+        if (need) *need = 0;
+        return CCL_OK;
+    }
+    // dz, for the products: dy itself where there is no activation and TMA can read it
+    const bool own_dz = (a->dx || a->dw) && (a->act != CCL_ACT_NONE || !aligned16(a->dy) || lddy % 8 != 0);
     Arena ws = {base};
     Matrix dz = {a->dy, a->rows, a->n, lddy}, x = {a->x, a->rows, a->k, ldx}, w = {a->w, a->n, a->k, ldw, count, sw};
-    if (!a->dx) w.p = nullptr, w.ld = 8;
-    if (!a->dw) x.p = nullptr, x.ld = 8;
     GradPass G = {};
     const int64_t chunks = a->rows / kGradRows + count;
     G.ld_part = round_up(a->n, 64);
@@ -518,7 +520,7 @@ static ccl_status_t linear_grad(const ccl_linear_grad_t* a, char* base, int64_t*
     }
     if (a->db) G.partial = ws.take<float>(chunks * G.ld_part * 4);
     if (need) {
-        *need = ws.used + w.packed_bytes() + x.packed_bytes();
+        *need = ws.used + (a->dx ? w.packed_bytes() : 0) + (a->dw ? x.packed_bytes() : 0);
         return CCL_OK;
     }
     const bool bf = a->dtype == CCL_BF16;

@@ -170,3 +170,26 @@ def test_updates_over_gradients_of_other_strides_are_refused(a):
     """A matrix may be written while another one of the batch is read."""
     assert code("ccl_orthogonalize", a) == INVALID
     assert "in place" in ccl.lib.ccl_last_error_detail().decode()
+
+
+def test_gradients_ask_for_no_more_than_they_use():
+    def need(a):
+        n = ctypes.c_int64(-1)
+        assert ccl.lib.ccl_linear_grad_workspace(ctypes.byref(a), ctypes.byref(n)) == 0
+        return n.value
+
+    rows, n, k = 3200, 136, 33                       # k = 33: x and w are copied to padded rows for a product
+    size = dict(rows=rows, n=n, k=k)
+    sums = (rows // 32 + 1) * 192 * 4 + 256          # one row of 32-bit sums for every 32 rows
+    for act, z in ((ccl.ACT_NONE, None), (ccl.ACT_GELU, 6 * A)):
+        alone = dict(size, act=act, z=z, dx=None, dw=None)
+        assert need(grad(**alone)) == 0
+        assert code("ccl_linear_grad", grad(**alone), ws=None, size=0) == 0          # nothing to do
+        assert 0 < need(grad(db=7 * A, **alone)) <= sums
+        assert 0 < need(grad(db=7 * A, experts=3, offsets=8 * A, **alone)) <= sums + 2 * 192 * 4
+        assert 0 < need(grad(db=7 * A, dy=A + 2, **alone)) <= sums
+    # the operand of a product that is not asked for is not copied
+    apart = need(grad(dw=None, **size)), need(grad(dx=None, **size))
+    assert apart[0] == -(-n * 40 * 2 // 256) * 256 and apart[1] == rows * 40 * 2
+    assert need(grad(experts=2, offsets=8 * A, dx=None, n=7, k=40, lddw=40)) == need(grad(dx=None, n=7, k=40))
+    assert need(grad(experts=2, offsets=8 * A, dx=None, n=7, k=40, ldw=44, w_stride=308)) == need(grad(dx=None, n=7, k=40))
