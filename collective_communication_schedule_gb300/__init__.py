@@ -580,6 +580,11 @@ def _on_stream(stream):
     return torch.cuda.stream(stream)
 
 
+def _no_graph():
+    raise ValueError("the tensor products record no autograd graph, and an operand requires gradients: "
+                     "call under torch.no_grad(), and take the gradients from linear_backward")
+
+
 def _run(call, workspace, args, device, handle, need=None):
     """Run a tensor product with the workspace it asks for (``need``: its size
     where the caller knows it)."""
@@ -618,6 +623,9 @@ def _forward(x, w, offsets, bias, residual, act, preact, out, stream):
     torch = _torch or _lazy_torch()
     rows, k, n, experts, vector = _operands(x, w, offsets is not None)
     device, dtype = x.device, x.dtype
+    if (x.requires_grad or w.requires_grad or (bias is not None and bias.requires_grad) or
+            (residual is not None and residual.requires_grad)) and torch.is_grad_enabled():
+        _no_graph()
     handle = _handle(device)
     a = Linear(rows, n, k, _type_code(dtype), act, experts)
     a.x = px = x.data_ptr()
@@ -690,7 +698,9 @@ def _backward(dy, x, w, offsets, preact, act, bias, need_dx, need_dw, stream):
 def linear(x, w, bias=None, residual=None, act=ACT_NONE, preact=False, out=None, stream=None):
     """act(x w^T + bias) + residual (``ccl_linear``) for x (rows, k) and w
     (n, k), bf16 or f16.  With ``preact`` also the values before the
-    activation, which ``linear_backward`` needs: (y, z)."""
+    activation, which ``linear_backward`` needs: (y, z).  No autograd graph is
+    recorded: operands that require gradients are refused outside of
+    ``torch.no_grad()``."""
     return _forward(x, w, None, bias, residual, act, preact, out, stream)
 
 
@@ -724,6 +734,8 @@ def orthogonalize(g, steps=5, coeffs=(3.4445, -4.7750, 2.0315), eps=1e-7, scale=
     shape, device = g.shape, g.device
     if len(shape) not in (2, 3):
         raise ValueError("g must be a matrix or a stack of matrices")
+    if g.requires_grad and torch.is_grad_enabled():
+        _no_graph()
     handle = _handle(device)
     if out is None:
         out = torch.empty(shape, dtype=torch.bfloat16, device=device)

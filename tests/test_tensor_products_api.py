@@ -193,3 +193,21 @@ def test_gradients_ask_for_no_more_than_they_use():
     assert apart[0] == -(-n * 40 * 2 // 256) * 256 and apart[1] == rows * 40 * 2
     assert need(grad(experts=2, offsets=8 * A, dx=None, n=7, k=40, lddw=40)) == need(grad(dx=None, n=7, k=40))
     assert need(grad(experts=2, offsets=8 * A, dx=None, n=7, k=40, ldw=44, w_stride=308)) == need(grad(dx=None, n=7, k=40))
+
+
+def test_operands_that_want_gradients_are_refused():
+    """The products record no autograd graph: the gradient would be lost without a word."""
+    torch = pytest.importorskip("torch")
+    plain = dict(dtype=torch.bfloat16)
+    x, w, b, r = torch.zeros(4, 8, **plain), torch.zeros(6, 8, **plain), torch.zeros(6, **plain), torch.zeros(4, 6, **plain)
+    offs = torch.zeros(3, dtype=torch.int32)
+    calls = [lambda t: ccl.linear(t(x), w), lambda t: ccl.linear(x, t(w)), lambda t: ccl.linear(x, w, bias=t(b)),
+             lambda t: ccl.linear(x, w, residual=t(r)), lambda t: ccl.grouped_linear(x, t(w).expand(2, 6, 8), offs),
+             lambda t: ccl.orthogonalize(t(w))]
+    for call in calls:
+        with pytest.raises(ValueError, match="autograd"):
+            call(lambda t: t.clone().requires_grad_(True))
+        with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
+            call(lambda t: t.clone().requires_grad_(True))
+        with pytest.raises(ValueError, match="CUDA"):
+            call(lambda t: t)
