@@ -601,3 +601,53 @@ def test_bias_gradient_does_not_depend_on_what_else_is_asked(ccl, n, k, counts):
     want = call()
     for dx, dw in ((0, 0), (1, 0), (0, 1)):
         assert torch.equal(call(need_dx=bool(dx), need_dw=bool(dw)), want), (dx, dw)
+
+
+@pytest.mark.parametrize("offs,sound", [([0, 20, 10, 60], [(0, 0, 10), (2, 20, 60)]),
+                                        ([0, 10, 20, 61], [(0, 0, 10), (1, 10, 20), (2, 20, 60)]),
+                                        ([-5, 10, 20, 60], [(0, 0, 10), (1, 10, 20), (2, 20, 60)]),
+                                        ([70, 80, 90, 100], []),
+                                        ([0, 2 ** 31 - 1, -2 ** 31, 2 ** 31 - 1], [])])
+@pytest.mark.parametrize("n", [40, 37])
+def test_bad_offsets_write_nothing_around_the_outputs(ccl, offs, sound, n):
+    """Outputs lie inside larger tensors whose rest stays as it is; rows of
+    ranges that overlap no other (expert, first, end) are right."""
+    rows, k, e, dt = 60, 64, 3, torch.bfloat16
+    g = gen(13)
+    x, dy, z = rnd(g, rows, k, dtype=dt), rnd(g, rows, n, dtype=dt), rnd(g, rows, n, dtype=dt)
+    w = rnd(g, e, n, k, dtype=dt, scale=k ** -0.5)
+    o = torch.tensor(offs, dtype=torch.int32, device="cuda")
+
+    def inside(*shape):
+        """A packed view with a matrix's worth of other memory on both sides."""
+        size = 1
+        for v in shape:
+            size *= v
+        held = torch.full((3 * size + 16,), 7.0, dtype=dt, device="cuda")
+        lead = size + -size % 8
+        return held, lead, size, held[lead:lead + size].view(shape)
+
+    held = {name: inside(*s) for name, s in (("y", (rows, n)), ("z", (rows, n)), ("dx", (rows, k)), ("dw", (e, n, k)),
+                                             ("db", (e, n)))}
+    at = {name: h[3].data_ptr() for name, h in held.items()}
+    ccl.tensor_status()
+    common = dict(rows=rows, n=n, k=k, dtype=ccl.BF16, experts=e, x=x.data_ptr(), w=w.data_ptr(), offsets=o.data_ptr())
+    c_call(ccl, "ccl_linear", ccl.Linear(act=ccl.ACT_SILU, y=at["y"], z=at["z"], **common))
+    with pytest.raises(ccl.CclError):
+        ccl.tensor_status()
+    c_call(ccl, "ccl_linear_grad", ccl.LinearGrad(act=ccl.ACT_SILU, dy=dy.data_ptr(), z=z.data_ptr(), dx=at["dx"],
+                                                  dw=at["dw"], db=at["db"], **common))
+    with pytest.raises(ccl.CclError):
+        ccl.tensor_status()
+    for name, (whole, lead, size, _) in held.items():
+        assert bool((whole[:lead] == 7).all()) and bool((whole[lead + size:] == 7).all()), name
+    dz = dy.double() * act_grad64(z.double(), 3)
+    for i, a, b in sound:
+        s = slice(a, b)
+        v = x[s].double() @ w[i].double().T
+        slack = product_slack(x[s].double().abs() @ w[i].double().abs().T, k)
+        close(held["z"][3][s], v, slack + 2.0 ** -22 * v.abs(), dt)
+        close(held["y"][3][s], act64(v, 3), 1.13 * slack + 2.0 ** -15 * v.abs(), dt)
+        own = 2.0 ** -14 * (1 + z[s].double().abs()) * dy[s].double().abs()
+        slack = (dz[s].abs() + own) @ w[i].double().abs() * (2.0 ** -8 + n * 2.0 ** -23) + own @ w[i].double().abs()
+        close(held["dx"][3][s], dz[s] @ w[i].double(), slack, dt)
