@@ -651,3 +651,34 @@ def test_bad_offsets_write_nothing_around_the_outputs(ccl, offs, sound, n):
         own = 2.0 ** -14 * (1 + z[s].double().abs()) * dy[s].double().abs()
         slack = (dz[s].abs() + own) @ w[i].double().abs() * (2.0 ** -8 + n * 2.0 ** -23) + own @ w[i].double().abs()
         close(held["dx"][3][s], dz[s] @ w[i].double(), slack, dt)
+
+
+@pytest.mark.parametrize("lead", [8, 3], ids=["on 16 bytes", "off 16 bytes"])
+def test_stacks_of_experts_apart(ccl, lead):
+    """Weights, biases and their gradients as slices of larger stacks (row and
+    matrix strides that are not packed): the bits of packed ones, and nothing
+    written beside the gradients."""
+    e, n, k, dt = 4, 136, 72, torch.bfloat16
+    offs = offsets_of([70, 0, 33, 150])
+    rows = offs[-1]
+    g = gen(lead)
+    x, dy = rnd(g, rows, k, dtype=dt), rnd(g, rows, n, dtype=dt)
+    w = rnd(g, e, n + 5, k + 24, dtype=dt)[:, 2:2 + n, lead:lead + k]
+    b = rnd(g, e, n + 16, dtype=dt)[:, lead:lead + n]
+    o = torch.tensor(offs, dtype=torch.int32, device="cuda")
+    assert torch.equal(ccl.grouped_linear(x, w, o, bias=b, act=ccl.ACT_SILU),
+                       ccl.grouped_linear(x, w.contiguous(), o, bias=b.contiguous(), act=ccl.ACT_SILU))
+    dx, dw, db = ccl.grouped_linear_backward(dy, x, w, o, bias=True)
+    want = ccl.grouped_linear_backward(dy, x, w.contiguous(), o, bias=True)
+    assert all(torch.equal(p, q) for p, q in zip((dx, dw, db), want))
+    whole = torch.full((e, n + 5, k + 24), 7.0, dtype=dt, device="cuda")
+    sums = torch.full((e, n + 16), 7.0, dtype=dt, device="cuda")
+    dw, db = whole[:, 2:2 + n, lead:lead + k], sums[:, lead:lead + n]
+    c_call(ccl, "ccl_linear_grad", ccl.LinearGrad(
+        rows=rows, n=n, k=k, dtype=ccl.BF16, experts=e, dy=dy.data_ptr(), x=x.data_ptr(), offsets=o.data_ptr(),
+        dw=dw.data_ptr(), db=db.data_ptr(), lddw=dw.stride(1), dw_stride=dw.stride(0), db_stride=db.stride(0)))
+    only = ccl.grouped_linear_backward(dy, x, w, o, bias=True, need_dx=False)
+    assert torch.equal(dw, only[1]) and torch.equal(db, only[2])
+    dw.fill_(7.0)
+    db.fill_(7.0)
+    assert bool((whole == 7).all()) and bool((sums == 7).all())
