@@ -322,10 +322,6 @@ static ccl_status_t run(const Device* dev, Product P, const Shape& sh, const Mat
     const int bytes = (kTileM + P.bn / sh.cg) * kSliceK * 2;
     const int fixed = 1024 + kStagingBytes + (sh.split > 1 ? P.bn * kTileM * 4 : 0);
     P.stages = std::min(kMaxStages, (kSmemBudget - fixed) / bytes);
-    // one tile each: no more stages than it has slices, so that the next
-    // kernel's threadblocks find room beside this one's
-    if (P.total <= dev->sms / size)
-        P.stages = (int)std::min<int64_t>(P.stages, ((P.k + kSliceK - 1) / kSliceK + P.split - 1) / P.split);
     const size_t smem = fixed + (size_t)P.stages * bytes;
     const int clusters = std::min(P.total, dev->sms / size);
     return launch(kKernels[sh.cg - 1][P.b_mn ? BOTH_MN : P.a_mn ? A_MN : BOTH_K], dim3((unsigned)(clusters * size)),

@@ -482,9 +482,10 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
         __syncthreads();
     volatile int* failed = &sh.failed;
     // Loads start while tensor memory is being allocated; everything up to
-    // here overlaps the end of the kernel before this one.  The next kernel is
-    // let in only when this one holds its tensor memory: it could otherwise
-    // take it first and wait for this one to end.
+    // here overlaps the end of the kernel before this one, on SMs that it has
+    // left (two of these kernels need more registers than an SM has).  The next
+    // kernel is let in only when this one holds its tensor memory: on a shared
+    // SM it could otherwise take it first and wait for this one to end.
     uint32_t tmem = 0;
     if (warp == 2) {
         tmem_alloc<CG>(smem_addr(&sh.tmem), tcols);
@@ -707,8 +708,8 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
     } else if (warp >= 4) {
         const int quad = warp & 3, slot = (warp - 4) >> 2;
         constexpr int kStride = kEpilogueWarps / 4 * kBlockRows;     // rows that the warps of a quadrant take at once
-        // what the products of a mode can have
-        constexpr bool kLayer = MODE == SINGLE, kAdds = MODE != PAIR;
+        // the products of a pair are only rounded: no bias, activation, C, split or mirror image
+        constexpr bool kAll = MODE == SINGLE;
         unsigned char* st = staging + (warp - 4) * (kBlockRows * 64);
         uint32_t release[2];
         for (int i = 0; i < 2; ++i)
@@ -717,7 +718,7 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
         for (int ph = 0; ph < phases; ++ph) {
             const Product& maps = seq.at(ph);
             const Scalars P = maps;
-            const int side = kAdds && P.symmetric ? 1 : 0;
+            const int side = kAll && P.symmetric ? 1 : 0;
             TileAt q;
             const Run run = next_run(P, ph);
             if (run.begin < run.end) q = tile_at<CG>(P, &sh, run.begin);
@@ -730,9 +731,9 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
                 const int acc = done & 1;
                 const int feat = q.m0 + (CG == 2 ? rank * kTileM : 0) + quad * 32, nfeat = P.m - feat, f = feat + lane;
                 const int64_t row = (int64_t)q.row0 + q.n0;
-                const float alpha = P.alpha * (kAdds && P.alpha_of ? P.alpha_of[q.g] : 1.f);
+                const float alpha = P.alpha * (kAll && P.alpha_of ? P.alpha_of[q.g] : 1.f);
                 const float beta = P.beta * (P.beta_of ? P.beta_of[q.g] : 1.f);
-                const float bias = kLayer && P.bias && f < P.m ? load1(P.bias + q.g * P.bs_bias + f, P.in_bf) : 0.f;
+                const float bias = kAll && P.bias && f < P.m ? load1(P.bias + q.g * P.bs_bias + f, P.in_bf) : 0.f;
                 const bool whole = P.ragged != RAGGED_ROWS;
                 const int zo = P.ragged == RAGGED_ROWS ? 0 : q.g;
                 // rows that the short way takes: an expert's last rows may end inside a block, and TMA cuts rows off at
@@ -741,12 +742,12 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
                 int c = slot * kBlockRows;          // this warp's next block
                 uint16_t cv[kBlockRows];
                 // the general way reads C a block ahead of its use, the short way reads it by itself
-                if (kAdds && P.c && size == CG && !short_to) fetch_c(P, cv, q.g, row + c, q.live - c, f);
+                if (kAll && P.c && size == CG && !short_to) fetch_c(P, cv, q.g, row + c, q.live - c, f);
                 if (some) {
                     if (!__all_sync(~0u, bar_wait(smem_addr(&sh.acc_full[acc]), (done >> 1) & 1, failed))) break;
                     fence_after();
                 }
-                if (kLayer && size > CG) {
+                if (kAll && size > CG) {
                     // shares of the last tile have been read by their owners
                     if (!__all_sync(~0u, bar_wait<true>(smem_addr(&sh.taken), (round & 1) ^ 1, failed))) break;
                 }
@@ -754,10 +755,10 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
                 if (short_to) {
 #define FAST(...)                                                                                                       \
     fast_blocks<__VA_ARGS__>(P, &maps.mo, from, c, short_to, kStride, alpha, bias, beta, st, lane, feat, nfeat, row, q.g, zo)
-                    if (kAdds && side) {
+                    if (kAll && side) {
                         if (P.c && c < short_to) FAST(ACT_NONE, true, true);
                         if (!P.c) FAST(ACT_NONE, false, true);
-                    } else if (!kLayer) {
+                    } else if (!kAll) {
                         FAST(ACT_NONE, false);
                     } else if (P.c) {
                         if (c < short_to) FAST(ACT_NONE, true);
@@ -772,7 +773,7 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
                     }
 #undef FAST
                     while (c < short_to) c += kStride;
-                    if (kAdds && P.c && c < q.live) fetch_c(P, cv, q.g, row + c, q.live - c, f);
+                    if (kAll && P.c && c < q.live) fetch_c(P, cv, q.g, row + c, q.live - c, f);
                 }
                 for (; c < q.live; c += kStride) {
                     uint32_t u[kBlockRows];
@@ -783,7 +784,7 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
                         for (int i = 0; i < kBlockRows; ++i) u[i] = 0;
                     }
                     const int nrows = q.live - c;
-                    if (kLayer && size > CG) {
+                    if (kAll && size > CG) {
                         const int own = P.bn / size;
                         const uint32_t at = smem_addr(shares + (size_t)rank * own * kTileM + quad * 32 + lane);
                         // own is a power of two from 4 up: 4 rows at a time go to one owner
@@ -801,22 +802,22 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
                     uint32_t w[kBlockRows / 2];
 #pragma unroll
                     for (int i = 0; i < kBlockRows; ++i) v[i] = fmaf(alpha, __uint_as_float(u[i]), bias);
-                    if (kLayer && P.pre) {
+                    if (kAll && P.pre) {
                         pack_block(v, w, P.in_bf);
                         store_block(&maps.mp, P.pre + (row + c) * P.ld_pre + f, P.ld_pre, w, st,
                                     P.tma_pre && (whole || nrows >= kBlockRows), lane, feat, (int)row + c, 0, nrows, nfeat);
                     }
-                    if (kLayer && P.act == ACT_RELU) {
+                    if (kAll && P.act == ACT_RELU) {
 #pragma unroll
                         for (int i = 0; i < kBlockRows; ++i) v[i] = activate(v[i], ACT_RELU);
-                    } else if (kLayer && P.act == ACT_GELU) {
+                    } else if (kAll && P.act == ACT_GELU) {
 #pragma unroll
                         for (int i = 0; i < kBlockRows; ++i) v[i] = activate(v[i], ACT_GELU);
-                    } else if (kLayer && P.act == ACT_SILU) {
+                    } else if (kAll && P.act == ACT_SILU) {
 #pragma unroll
                         for (int i = 0; i < kBlockRows; ++i) v[i] = activate(v[i], ACT_SILU);
                     }
-                    if (kAdds && P.c) {
+                    if (kAll && P.c) {
                         if (P.in_bf) {
 #pragma unroll
                             for (int i = 0; i < kBlockRows; ++i) v[i] += beta * __uint_as_float((uint32_t)cv[i] << 16);
@@ -840,7 +841,7 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
                     }
                     ++done;
                 }
-                if (kLayer && size > CG) {
+                if (kAll && size > CG) {
                     __syncwarp();
                     if (lane < size) bar_arrive_cluster(cluster_addr(smem_addr(&sh.got), lane));
                     if (!__all_sync(~0u, bar_wait<true>(smem_addr(&sh.got), round & 1, failed))) break;
