@@ -713,20 +713,25 @@ def linear_backward(dy, x, w, preact=None, act=ACT_NONE, bias=False, need_dx=Tru
 def grouped_linear(x, w, offsets, bias=None, act=ACT_NONE, preact=False, out=None, stream=None):
     """``linear`` with a weight (and bias) per expert: w (experts, n, k), rows
     of x sorted by expert, rows offsets[e] .. offsets[e + 1] - 1 (int32, on the
-    device) for expert e.  Rows that no expert owns are not written."""
+    device) for expert e.  Rows that no expert owns are not written: without
+    ``out`` they, and those of the pre-activation, are uninitialised memory."""
     return _forward(x, w, offsets, bias, None, act, preact, out, stream)
 
 
 def grouped_linear_backward(dy, x, w, offsets, preact=None, act=ACT_NONE, bias=False, need_dx=True, need_dw=True,
                             stream=None):
-    """(dx, dw, db) of ``grouped_linear``; experts without rows get zeros."""
+    """(dx, dw, db) of ``grouped_linear``; experts without rows get zeros, rows
+    of dx that no expert owns are uninitialised memory."""
     return _backward(dy, x, w, offsets, preact, act, bias, need_dx, need_dw, stream)
 
 
 def orthogonalize(g, steps=5, coeffs=(3.4445, -4.7750, 2.0315), eps=1e-7, scale=1.0, out=None, stream=None):
     """Newton-Schulz orthogonalisation of a gradient matrix (p, q) or a stack
     (batch, p, q) of them, f32, bf16 or f16 (``ccl_orthogonalize``).  The
-    update is bf16 unless ``out`` is a given f16 matrix."""
+    update is bf16 unless ``out`` is a given f16 matrix.  ``coeffs`` must keep
+    the singular values of x below 8 and the entries of b A + c A A below 63
+    (the usual ones do): between products both are f16, and overflow gives Inf
+    or NaN without a report."""
     if stream is not None:
         with _on_stream(stream):
             return orthogonalize(g, steps, coeffs, eps, scale, out, None)
@@ -752,7 +757,9 @@ def orthogonalize(g, steps=5, coeffs=(3.4445, -4.7750, 2.0315), eps=1e-7, scale=
 
 def tensor_status():
     """Raise what went wrong inside the tensor products launched since the
-    last call (``ccl_tensor_status``; synchronizes the device)."""
+    last call (``ccl_tensor_status``; synchronizes the device).  No other call
+    looks: until this one has returned, outputs may be incomplete.  The status
+    is the device's, not the caller's: it is cleared for all who launch on it."""
     _check(lib.ccl_tensor_status())
 
 

@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(256) scale_kernel(const NormPass N)
 // in 45 us, 53 when the parts were pushed from the accumulators, where a
 // store of a warp went to 32 rows), the rest of the step stays within a threadblock.  A tall matrix is transposed as it is loaded
 // and stored.  Bound by the latency of 3 x steps products in a row: 128 x 128 in
-// 18 us, 2.5 us a step; one launch per product took 87 us.
+// 19 us, 2.5 us a step; one launch per product took 87 us.
 //
 // Rows of 64 elements (128 bytes) in 1024-byte atoms of 8 rows, 16-byte pieces
 // exchanged by the row's index: element (i, j) of x is at piece (j / 8 % 8) ^

@@ -45,8 +45,9 @@ namespace tensor {
 //     4096 with gelu and both outputs 301 us, 1830 TFLOP/s.  Slices of 128
 //     instead of 64 halved the cost of handing slices over (338 -> 304 us),
 //     whole warps in the issuing loops keep addresses in uniform registers.
-//   few rows: DRAM and the start of a launch; 1 x 4096 x 4096 (33.6 MB) 11 us,
-//     37 x 8192 x 2048 11 us, 24 rows over 64 experts of 2048 x 1024 19 us.
+//   few rows: DRAM and the start of a launch; 1 x 4096 x 4096 (33.6 MB) 12 us,
+//     37 x 8192 x 2048 11 us, 24 rows over 64 experts of 2048 x 1024 (74 MB for the
+//     18 experts that have rows) 19 us.
 //   short reductions: the epilogue, about 5000 clocks for 256 x 256 outputs
 //     that are only rounded (4096 x 4096 outputs of 64 products each: 15 us),
 //     twice that with an activation or a residual (22 and 24 us); sixteen warps,

@@ -764,8 +764,9 @@ ccl_status_t ccl_schedule_read_json(const char* path, ccl_schedule_t* out);
  *   experts > 0 (at most 1024): row t of x meets the weight of its expert.
  *     Rows are sorted by expert; expert e owns rows offsets[e] ..
  *     offsets[e + 1] - 1 (device array of experts + 1 int32, may repeat:
- *     experts without rows).  Rows outside [offsets[0], offsets[experts])
- *     are not written.  Offsets are read on the device, clamped to the rows;
+ *     experts without rows).  Rows of y and z outside [offsets[0],
+ *     offsets[experts]) are not written.  Offsets are read on the device, clamped
+ *     to the rows;
  *     ones that decrease or leave the rows are reported by
  *     ccl_tensor_status.  w is experts matrices w_stride apart, bias experts
  *     vectors bias_stride apart.
@@ -791,7 +792,8 @@ typedef struct {
  * Gradients of ccl_linear from dy (rows x n):
  *   dz = dy * act'(z),  dx = dz w,  dw = dz^T x,  db = sum over rows of dz
  * (by expert where experts > 0; an expert without rows gets dw = db = 0).
- * The gradient of the residual is dy itself.  z is needed when act is not
+ * Rows of dx that no expert owns are not written.  The gradient of the residual
+ * is dy itself.  z is needed when act is not
  * CCL_ACT_NONE.  dx, dw, db may be null (not computed; then w, x are not
  * read).  dz is rounded to the element type between the two products, as z
  * and y are between layers; db sums it unrounded.  The outputs are computed
@@ -817,12 +819,16 @@ typedef struct {
  * (x^T x on the other side for p > q, which is the same matrix).  g is f32,
  * bf16 or f16; out is bf16 or f16, and may be g: in a batch only where the
  * elements have the same size and the matrices the same stride.
- * The norm is summed in 32 bits (|g|_F below 1.8e19).  Intermediate matrices
+ * The norm is summed in 32 bits: right for |g|_F from 1e-19 to 1.8e19; a smaller
+ * norm loses bits and counts as 0 from 1e-23 down, which shows only where eps is
+ * smaller still.  A gradient far below eps gives an update of the size of
+ * |g|_F / eps, whose entries lose bits below about 1e-8.  Intermediate matrices
  * are f16 with fixed power-of-two scales (bf16 loses 8 times as much: 1.1 % of
  * the update's norm on Gaussian matrices where f16 loses 0.13 %, 1.8 and 0.22 %
  * with a few strong directions), which holds for coefficients
  * that keep the singular values of x below 8 and the entries of b A + c A A
- * below 63 in magnitude.
+ * below 63 in magnitude.  Beyond that the update is Inf or NaN, and nothing is
+ * reported.
  */
 typedef struct {
     int64_t batch, p, q;
@@ -847,7 +853,8 @@ ccl_status_t ccl_orthogonalize(const ccl_ortho_t* a, void* ws, int64_t ws_bytes,
 /* Synchronize the device and report (once) what went wrong inside the tensor
  * products launched on it since the last call: CCL_ERR_TIMEOUT (a wait on the
  * device ran out; the outputs are incomplete) or CCL_ERR_INVALID_ARG (expert
- * offsets that decrease or leave the rows). */
+ * offsets that decrease or leave the rows).  One word per device holds the first
+ * failure for all callers: whoever asks takes it.  No other call looks at it. */
 ccl_status_t ccl_tensor_status(void);
 
 const char* ccl_error_string(ccl_status_t s);
