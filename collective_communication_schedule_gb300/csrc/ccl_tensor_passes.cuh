@@ -13,6 +13,13 @@ namespace tensor {
 // [0]: a ccl_status_t of a failed launch on this device, 0 if none
 __device__ int g_status[4];
 
+// An expert's offsets that decrease or leave the rows are reported, once.
+__device__ __forceinline__ void check_offsets(const int32_t* offsets, int e, int rows)
+{
+    if (offsets[e] < 0 || offsets[e + 1] < offsets[e] || offsets[e + 1] > rows)
+        atomicCAS(&g_status[0], 0, (int)CCL_ERR_INVALID_ARG);
+}
+
 // Rows of a partial column sum of the activation's gradient (act_grad_kernel).
 constexpr int kGradRows = 32;
 
@@ -152,6 +159,8 @@ __global__ void __launch_bounds__(256) bias_grad_kernel(const GradPass G)
     const int e = blockIdx.y, tx = threadIdx.x & 31, ty = threadIdx.x >> 5, c = blockIdx.x * 32 + tx;
     int lo, len;
     grad_range(G, e, lo, len);
+    // (no product may follow that checks them)
+    if (G.offsets && blockIdx.x == 0 && threadIdx.x == 0) check_offsets(G.offsets, e, G.rows);
     const int chunks = (len + kGradRows - 1) / kGradRows;
     float s = 0.f;
     if (c < G.n) {

@@ -137,9 +137,7 @@ __device__ __forceinline__ void prepare_tiles(const Scalars& P, Shared* sh)
     const int lane = threadIdx.x & 31;
     if (blockIdx.x == 0) {
         const int limit = P.ragged == RAGGED_ROWS ? P.n : P.k;
-        for (int s = threadIdx.x; s < P.groups; s += kThreads)
-            if (P.offsets[s] < 0 || P.offsets[s + 1] < P.offsets[s] || P.offsets[s + 1] > limit)
-                atomicCAS(&g_status[0], 0, (int)CCL_ERR_INVALID_ARG);
+        for (int s = threadIdx.x; s < P.groups; s += kThreads) check_offsets(P.offsets, s, limit);
     }
     if (P.ragged == RAGGED_ROWS && threadIdx.x < 32) {
         long long base = 0;

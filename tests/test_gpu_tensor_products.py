@@ -682,3 +682,19 @@ def test_stacks_of_experts_apart(ccl, lead):
     dw.fill_(7.0)
     db.fill_(7.0)
     assert bool((whole == 7).all()) and bool((sums == 7).all())
+
+
+def test_bad_offsets_are_reported_whatever_is_asked(ccl):
+    g = gen(14)
+    dt = torch.bfloat16
+    dy, x, w = rnd(g, 60, 40, dtype=dt), rnd(g, 60, 64, dtype=dt), rnd(g, 3, 40, 64, dtype=dt)
+    for offs, sound in (([0, 20, 10, 60], False), ([0, 10, 20, 61], False), ([-5, 10, 20, 60], False), ([3, 3, 20, 59], True)):
+        o = torch.tensor(offs, dtype=torch.int32, device="cuda")
+        for dx, dw, bias in ((0, 0, 1), (1, 0, 0), (0, 1, 0), (1, 0, 1), (0, 1, 1), (1, 1, 0)):
+            ccl.tensor_status()
+            ccl.grouped_linear_backward(dy, x, w, o, bias=bool(bias), need_dx=bool(dx), need_dw=bool(dw))
+            if sound:
+                ccl.tensor_status()
+            else:
+                with pytest.raises(ccl.CclError, match="offsets"):
+                    ccl.tensor_status()
