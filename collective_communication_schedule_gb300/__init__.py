@@ -32,6 +32,7 @@ LINK_FIFO, LINK_DIRECT = 0, 1
 PROTO_SIMPLE, PROTO_LL = 0, 1
 ENGINE_PIPELINED, ENGINE_SEQUENTIAL = 0, 1
 ACT_NONE, ACT_RELU, ACT_GELU, ACT_SILU = range(4)
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 KIND_NAMES = ["copy", "reduce", "send", "recv", "rrc", "rcs", "fwd", "rrs", "rrcs", "copy_send", "copy2", "rrc2",
               "rrs3", "rrc3", "rrcs3", "rsend", "rcsend", "rrc3d", "reduce2", "copy3"]
 DTYPE_NAMES = {F32: "f32", BF16: "bf16", F16: "f16", I32: "i32"}
@@ -141,6 +142,50 @@ class Ortho(ctypes.Structure):
                 ("g_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64)]
 
 
+def _struct(fields):
+    """Fields of a structure: names by type (q int64, i int32, f float, p pointer)."""
+    types = {"q": ctypes.c_int64, "i": ctypes.c_int32, "f": ctypes.c_float, "p": ctypes.c_void_p}
+    return [(n, types[t]) for t, names in fields for n in names.split()]
+
+
+class Route(ctypes.Structure):
+    _fields_ = _struct([("q", "rows experts"), ("i", "k dtype score groups top_groups group_best renormalize"),
+                        ("f", "scale"), ("p", "logits bias weights chosen offsets place"), ("q", "ld")])
+
+
+class RouteGrad(ctypes.Structure):
+    _fields_ = _struct([("q", "rows experts"), ("i", "k dtype score renormalize"), ("f", "scale"), ("i", "reserved"),
+                        ("p", "logits chosen dweights dlogits"), ("q", "ld ldd")])
+
+
+class ExpertOrder(ctypes.Structure):
+    _fields_ = _struct([("q", "slots"), ("i", "experts reserved"), ("p", "chosen offsets place")])
+
+
+class Dispatch(ctypes.Structure):
+    _fields_ = _struct([("q", "rows count h"), ("i", "k dtype"), ("p", "x place out"), ("q", "ldx ldo")])
+
+
+class Combine(ctypes.Structure):
+    _fields_ = _struct([("q", "rows count h"), ("i", "k dtype"), ("p", "r place weights residual y"),
+                        ("q", "ldr lds ldy")])
+
+
+class CombineGrad(ctypes.Structure):
+    _fields_ = _struct([("q", "rows count h"), ("i", "k dtype"), ("p", "dy r place weights dr dweights"),
+                        ("q", "lddy ldr lddr")])
+
+
+class LayerNorm(ctypes.Structure):
+    _fields_ = _struct([("q", "rows n"), ("i", "dtype wdtype"), ("f", "eps"), ("i", "reserved"),
+                        ("p", "x w b y mean rstd"), ("q", "ldx ldy")])
+
+
+class LayerNormGrad(ctypes.Structure):
+    _fields_ = _struct([("q", "rows n"), ("i", "dtype wdtype"), ("p", "dy x w mean rstd dx dw db"),
+                        ("q", "lddy ldx lddx")])
+
+
 PROBE_FN = ctypes.CFUNCTYPE(ctypes.c_double, ctypes.c_void_p, ctypes.POINTER(PlanOpts))
 
 
@@ -189,6 +234,17 @@ def _load():
         "ccl_linear": [ctypes.POINTER(Linear), P, I64_, P],
         "ccl_linear_grad_workspace": [ctypes.POINTER(LinearGrad), ctypes.POINTER(I64_)],
         "ccl_linear_grad": [ctypes.POINTER(LinearGrad), P, I64_, P],
+        "ccl_route_workspace": [ctypes.POINTER(Route), ctypes.POINTER(I64_)],
+        "ccl_route": [ctypes.POINTER(Route), P, I64_, P],
+        "ccl_route_grad": [ctypes.POINTER(RouteGrad), P],
+        "ccl_expert_order_workspace": [ctypes.POINTER(ExpertOrder), ctypes.POINTER(I64_)],
+        "ccl_expert_order": [ctypes.POINTER(ExpertOrder), P, I64_, P],
+        "ccl_dispatch": [ctypes.POINTER(Dispatch), P],
+        "ccl_combine": [ctypes.POINTER(Combine), P],
+        "ccl_combine_grad": [ctypes.POINTER(CombineGrad), P],
+        "ccl_layer_norm": [ctypes.POINTER(LayerNorm), P],
+        "ccl_layer_norm_grad_workspace": [ctypes.POINTER(LayerNormGrad), ctypes.POINTER(I64_)],
+        "ccl_layer_norm_grad": [ctypes.POINTER(LayerNormGrad), P, I64_, P],
         "ccl_orthogonalize_workspace": [ctypes.POINTER(Ortho), ctypes.POINTER(I64_)],
         "ccl_orthogonalize": [ctypes.POINTER(Ortho), P, I64_, P],
         "ccl_tensor_status": [],
@@ -753,6 +809,259 @@ def orthogonalize(g, steps=5, coeffs=(3.4445, -4.7750, 2.0315), eps=1e-7, scale=
         a.g_stride, a.out_stride = _stacked("g", g), _stacked("out", out)
     _run(lib.ccl_orthogonalize, lib.ccl_orthogonalize_workspace, a, device, handle)
     return out
+
+
+# ------------------------- around the expert products: router, rows, norm
+def _graphless(*operands):
+    """Refuse operands whose gradients would be lost without a word."""
+    if _torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in operands):
+        raise ValueError("the layer operators record no autograd graph, and an operand requires gradients: call under "
+                         "torch.no_grad(), and take the gradients from the _backward functions")
+
+
+def _packed(name, t, shape, dtype, device):
+    """Address of a packed tensor that must be this."""
+    if t.shape != shape or t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name} is {tuple(t.shape)} {t.dtype} on {t.device}, not {tuple(shape)} {dtype} on {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows(name, t):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix")
+    return t.shape
+
+
+def route(logits, k, score=SCORE_SOFTMAX, bias=None, groups=1, top_groups=1, group_best=1, renormalize=True, scale=1.0,
+          order=False, stream=None):
+    """The k best experts of every row of ``logits`` (rows, experts) and their
+    weights (``ccl_route``): (weights f32, chosen int32), both (rows, k), best
+    first; -1 with weight 0 where a row has no expert left (logits of -inf are
+    closed).  ``bias`` (experts, f32) enters the choice but not the weights;
+    with ``groups`` only the experts of the ``top_groups`` best groups are
+    open, a group's value being its best expert's or the sum of its
+    ``group_best`` = 2 best.  With ``order`` also what ``expert_order`` gives:
+    (weights, chosen, offsets, place)."""
+    if stream is not None:
+        with _on_stream(stream):
+            return route(logits, k, score, bias, groups, top_groups, group_best, renormalize, scale, order, None)
+    torch = _torch or _lazy_torch()
+    rows, experts = _rows("logits", logits)
+    device = logits.device
+    _graphless(logits, bias)
+    handle = _handle(device)
+    a = Route(rows, experts, k, _type_code(logits.dtype), score, groups, top_groups, group_best, bool(renormalize), scale)
+    a.logits, a.ld = _matrix("logits", logits, logits.shape, logits.dtype, device)
+    if bias is not None:
+        a.bias = _packed("bias", bias, (experts,), torch.float32, device)
+    slots = rows * max(0, k)
+    # one allocation for all outputs
+    out = torch.empty((4 if order else 2) * slots + (experts + 1 if order else 0), dtype=torch.int32, device=device)
+    chosen, weights = out[:slots].view(rows, k), out[slots:2 * slots].view(torch.float32).view(rows, k)
+    a.chosen, a.weights = chosen.data_ptr(), weights.data_ptr()
+    if order:
+        place, offsets = out[2 * slots:3 * slots].view(rows, k), out[3 * slots:3 * slots + experts + 1]
+        a.place, a.offsets = place.data_ptr(), offsets.data_ptr()
+        _run(lib.ccl_route, lib.ccl_route_workspace, a, device, handle)
+        return weights, chosen, offsets, place
+    _run(lib.ccl_route, lib.ccl_route_workspace, a, device, handle, 0)
+    return weights, chosen
+
+
+def route_backward(dweights, logits, chosen, score=SCORE_SOFTMAX, renormalize=True, scale=1.0, stream=None):
+    """The gradient of the logits (their type) from that of ``route``'s weights
+    (``ccl_route_grad``), the choices held fixed."""
+    if stream is not None:
+        with _on_stream(stream):
+            return route_backward(dweights, logits, chosen, score, renormalize, scale, None)
+    torch = _torch or _lazy_torch()
+    rows, experts = _rows("logits", logits)
+    _, k = _rows("chosen", chosen)
+    device = logits.device
+    handle = _handle(device)
+    a = RouteGrad(rows, experts, k, _type_code(logits.dtype), score, bool(renormalize), scale)
+    a.logits, a.ld = _matrix("logits", logits, logits.shape, logits.dtype, device)
+    a.chosen = _packed("chosen", chosen, (rows, k), torch.int32, device)
+    a.dweights = _packed("dweights", dweights, (rows, k), torch.float32, device)
+    dlogits = torch.empty((rows, experts), dtype=logits.dtype, device=device)
+    a.dlogits = dlogits.data_ptr()
+    _check(lib.ccl_route_grad(ctypes.byref(a), handle))
+    return dlogits
+
+
+def expert_order(chosen, experts, stream=None):
+    """(offsets, place) that sort the slots of ``chosen`` (int32, any shape) by
+    expert (``ccl_expert_order``): slot s goes to position place[s] (shape of
+    ``chosen``; -1 where chosen is negative), expert e owns positions
+    offsets[e] .. offsets[e + 1] - 1."""
+    if stream is not None:
+        with _on_stream(stream):
+            return expert_order(chosen, experts, None)
+    torch = _torch or _lazy_torch()
+    device = chosen.device
+    handle = _handle(device)
+    a = ExpertOrder(chosen.numel(), experts)
+    a.chosen = _packed("chosen", chosen, chosen.shape, torch.int32, device)
+    place = torch.empty_like(chosen)
+    offsets = torch.empty(max(0, experts) + 1, dtype=torch.int32, device=device)
+    a.place, a.offsets = place.data_ptr(), offsets.data_ptr()
+    _run(lib.ccl_expert_order, lib.ccl_expert_order_workspace, a, device, handle)
+    return offsets, place
+
+
+def _places(place, rows, device):
+    if place.dim() != 2 or place.shape[0] != rows:
+        raise ValueError(f"place is {tuple(place.shape)}, not ({rows}, choices)")
+    return _packed("place", place, place.shape, _torch.int32, device), place.shape[1]
+
+
+def dispatch(x, place, out=None, stream=None):
+    """Rows of x (rows, h) to the places of their choices (``ccl_dispatch``):
+    out[place[t, j]] = x[t].  ``out`` has rows * k rows unless given; rows that
+    no place names are not written (uninitialised memory without ``out``)."""
+    if stream is not None:
+        with _on_stream(stream):
+            return dispatch(x, place, out, None)
+    torch = _torch or _lazy_torch()
+    rows, h = _rows("x", x)
+    device, dtype = x.device, x.dtype
+    _graphless(x)
+    handle = _handle(device)
+    where, k = _places(place, rows, device)
+    if out is None:
+        out = torch.empty((rows * k, h), dtype=dtype, device=device)
+    a = Dispatch(rows, _rows("out", out)[0], h, k, _type_code(dtype), x.data_ptr(), where)
+    a.x, a.ldx = _matrix("x", x, x.shape, dtype, device)
+    a.out, a.ldo = _matrix("out", out, (out.shape[0], h), dtype, device)
+    _check(lib.ccl_dispatch(ctypes.byref(a), handle))
+    return out
+
+
+def combine(r, place, weights=None, residual=None, out=None, stream=None):
+    """y[t] = sum over j of weights[t, j] r[place[t, j]] + residual[t]
+    (``ccl_combine``) for r (places, h), place (rows, k) and weights (rows, k) in
+    f32 (1 without)."""
+    if stream is not None:
+        with _on_stream(stream):
+            return combine(r, place, weights, residual, out, None)
+    torch = _torch or _lazy_torch()
+    count, h = _rows("r", r)
+    device, dtype = r.device, r.dtype
+    _graphless(r, weights, residual)
+    handle = _handle(device)
+    rows = place.shape[0]
+    where, k = _places(place, rows, device)
+    a = Combine(rows, count, h, k, _type_code(dtype))
+    a.place = where
+    a.r, a.ldr = _matrix("r", r, r.shape, dtype, device)
+    if weights is not None:
+        a.weights = _packed("weights", weights, (rows, k), torch.float32, device)
+    if residual is not None:
+        a.residual, a.lds = _matrix("residual", residual, (rows, h), dtype, device)
+    if out is None:
+        out = torch.empty((rows, h), dtype=dtype, device=device)
+    a.y, a.ldy = _matrix("out", out, (rows, h), dtype, device)
+    _check(lib.ccl_combine(ctypes.byref(a), handle))
+    return out
+
+
+def dispatch_backward(dout, place, stream=None):
+    """The gradient of ``dispatch``'s x: the sum over a row's choices."""
+    return combine(dout, place, stream=stream)
+
+
+def combine_backward(dy, r, place, weights=None, out=None, need_dr=True, need_dweights=True, stream=None):
+    """(dr, dweights) of ``combine`` (``ccl_combine_grad``); an output that is
+    not asked for is None.  Rows of dr that no place names are not written
+    (uninitialised memory without ``out``).  The residual's gradient is dy."""
+    if stream is not None:
+        with _on_stream(stream):
+            return combine_backward(dy, r, place, weights, out, need_dr, need_dweights, None)
+    torch = _torch or _lazy_torch()
+    rows, h = _rows("dy", dy)
+    count = _rows("r", r)[0]
+    device, dtype = dy.device, dy.dtype
+    handle = _handle(device)
+    where, k = _places(place, rows, device)
+    a = CombineGrad(rows, count, h, k, _type_code(dtype))
+    a.place = where
+    a.dy, a.lddy = _matrix("dy", dy, dy.shape, dtype, device)
+    a.r, a.ldr = _matrix("r", r, (count, h), dtype, device)
+    if weights is not None:
+        a.weights = _packed("weights", weights, (rows, k), torch.float32, device)
+    dr = dweights = None
+    if need_dr:
+        dr = torch.empty((count, h), dtype=dtype, device=device) if out is None else out
+        a.dr, a.lddr = _matrix("out", dr, (count, h), dtype, device)
+    if need_dweights:
+        dweights = torch.empty((rows, k), dtype=torch.float32, device=device)
+        a.dweights = dweights.data_ptr()
+    _check(lib.ccl_combine_grad(ctypes.byref(a), handle))
+    return dr, dweights
+
+
+def layer_norm(x, w=None, b=None, eps=1e-5, stats=False, out=None, stream=None):
+    """(x - mean) rstd w + b over the rows of x (rows, n), f32, bf16 or f16
+    (``ccl_layer_norm``); w and b (n) have the type of x or are f32.  With
+    ``stats`` also what ``layer_norm_backward`` needs: (y, mean, rstd)."""
+    if stream is not None:
+        with _on_stream(stream):
+            return layer_norm(x, w, b, eps, stats, out, None)
+    torch = _torch or _lazy_torch()
+    rows, n = _rows("x", x)
+    device, dtype = x.device, x.dtype
+    _graphless(x, w, b)
+    handle = _handle(device)
+    wtype = w.dtype if w is not None else b.dtype if b is not None else dtype
+    a = LayerNorm(rows, n, _type_code(dtype), _type_code(wtype), eps)
+    a.x, a.ldx = _matrix("x", x, x.shape, dtype, device)
+    if w is not None:
+        a.w = _packed("w", w, (n,), wtype, device)
+    if b is not None:
+        a.b = _packed("b", b, (n,), wtype, device)
+    y = torch.empty((rows, n), dtype=dtype, device=device) if out is None else out
+    a.y, a.ldy = _matrix("out", y, (rows, n), dtype, device)
+    if not stats:
+        _check(lib.ccl_layer_norm(ctypes.byref(a), handle))
+        return y
+    mean, rstd = torch.empty((2, rows), dtype=torch.float32, device=device).unbind(0)
+    a.mean, a.rstd = mean.data_ptr(), rstd.data_ptr()
+    _check(lib.ccl_layer_norm(ctypes.byref(a), handle))
+    return y, mean, rstd
+
+
+def layer_norm_backward(dy, x, w, mean, rstd, bias=False, need_dx=True, need_dw=True, stream=None):
+    """(dx, dw, db) of ``layer_norm`` (``ccl_layer_norm_grad``); an output that
+    is not asked for is None.  dw and db have the type of w (of x without)."""
+    if stream is not None:
+        with _on_stream(stream):
+            return layer_norm_backward(dy, x, w, mean, rstd, bias, need_dx, need_dw, None)
+    torch = _torch or _lazy_torch()
+    rows, n = _rows("x", x)
+    device, dtype = x.device, x.dtype
+    handle = _handle(device)
+    wtype = w.dtype if w is not None else dtype
+    a = LayerNormGrad(rows, n, _type_code(dtype), _type_code(wtype))
+    a.dy, a.lddy = _matrix("dy", dy, (rows, n), dtype, device)
+    a.x, a.ldx = _matrix("x", x, x.shape, dtype, device)
+    if w is not None:
+        a.w = _packed("w", w, (n,), wtype, device)
+    a.mean = _packed("mean", mean, (rows,), torch.float32, device)
+    a.rstd = _packed("rstd", rstd, (rows,), torch.float32, device)
+    dx = dw = db = None
+    if need_dx:
+        dx = torch.empty((rows, n), dtype=dtype, device=device)
+        a.dx = dx.data_ptr()
+    if need_dw:
+        dw = torch.empty(n, dtype=wtype, device=device)
+        a.dw = dw.data_ptr()
+    if bias:
+        db = torch.empty(n, dtype=wtype, device=device)
+        a.db = db.data_ptr()
+    _run(lib.ccl_layer_norm_grad, lib.ccl_layer_norm_grad_workspace, a, device, handle)
+    return dx, dw, db
 
 
 def tensor_status():

@@ -10,8 +10,9 @@
 namespace ccl {
 namespace tensor {
 
-// [0]: a ccl_status_t of a failed launch on this device, 0 if none
-__device__ int g_status[4];
+// [0]: a ccl_status_t of a failed launch on this device, 0 if none.  Every translation
+// unit has its own; ccl_tensor_status asks all of them.
+static __device__ int g_status[4];
 
 // An expert's offsets that decrease or leave the rows are reported, once.
 __device__ __forceinline__ void check_offsets(const int32_t* offsets, int e, int rows)
@@ -56,7 +57,7 @@ __device__ __forceinline__ void grad_range(const GradPass& G, int e, int& lo, in
 // sums go, in 32 bits and a fixed order, to partial[chunk][column]; an
 // expert's chunks are added up in order afterwards.  Chunks of expert e start
 // at offsets[e] / kGradRows + e, which leaves every expert room for its rows.
-__global__ void __launch_bounds__(256) act_grad_kernel(const GradPass G)
+static __global__ void __launch_bounds__(256) act_grad_kernel(const GradPass G)
 {
     __shared__ float sums[8][256 + 8];
     let_next_in();
@@ -151,7 +152,7 @@ __global__ void __launch_bounds__(256) act_grad_kernel(const GradPass G)
 
 // 32 columns per threadblock; 8 groups of threads take an expert's chunks in
 // turn, and their sums are added in order.
-__global__ void __launch_bounds__(256) bias_grad_kernel(const GradPass G)
+static __global__ void __launch_bounds__(256) bias_grad_kernel(const GradPass G)
 {
     __shared__ float sums[8][32];
     let_next_in();
@@ -211,7 +212,7 @@ struct PackArgs {
 // Copy a matrix whose base or row stride TMA cannot address (not a multiple
 // of 16 bytes) into rows padded to 8 elements, 2 bytes a thread: a weight of 4096 x
 // 4095 in 34 us (1.0 TB/s), three times what its product with one row takes.
-__global__ void __launch_bounds__(256) pack_rows_kernel(const PackArgs a)
+static __global__ void __launch_bounds__(256) pack_rows_kernel(const PackArgs a)
 {
     let_next_in();
     wait_for_previous();

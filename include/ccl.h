@@ -850,11 +850,176 @@ ccl_status_t ccl_linear_grad(const ccl_linear_grad_t* a, void* ws, int64_t ws_by
 ccl_status_t ccl_orthogonalize_workspace(const ccl_ortho_t* a, int64_t* bytes);
 ccl_status_t ccl_orthogonalize(const ccl_ortho_t* a, void* ws, int64_t ws_bytes, void* stream);
 
+/* ======================================================================
+ * Around the expert products: router, rows to their experts and back, norm
+ *
+ * The conventions of the tensor products hold: asynchronous on `stream`, no
+ * allocation, nothing kept between calls, capturable after one call on the
+ * device outside capture, strides in elements with 0 = packed, any stride and
+ * alignment, sums in 32 bits in an order that the sizes fix and, for the norm and
+ * the gradients of weights, whether all rows start on 16 bytes.  Vectors and
+ * arrays of choices are packed.  Types: CCL_F32, CCL_BF16, CCL_F16.
+ * ====================================================================== */
+
+#define CCL_SCORE_SOFTMAX 0
+#define CCL_SCORE_SIGMOID 1
+
+/*
+ * The k best experts (at most 32, of at most 1024) of every row and their weights:
+ *   s = softmax(logits) over the experts, or sigmoid(logits)
+ *   c = s + bias                      (bias: balance; it does not enter the weights)
+ *   with groups > 1 (at most 32 of equal size): experts of one group are
+ *     neighbours, a group's value is its largest c (group_best = 1) or the sum
+ *     of its two largest (2), and only the top_groups best groups stay open
+ *   chosen = the k largest c of open experts, descending
+ *   weights = scale * s[chosen], or with renormalize scale * s / sum over the chosen of s
+ * Ties go to the lower expert (and group).  The order is that of the exact c:
+ * values that lie nearer to each other than 32 bits can tell are computed in 64.
+ * An expert whose logit (or bias) is -Inf is closed; where fewer than k are
+ * open, the choices that are left are -1 with weight 0 (a row of -Inf: all of
+ * them).  A NaN ranks behind every number; with softmax it makes the row's
+ * weights NaN.
+ * offsets and place (both or neither) are those of ccl_expert_order.
+ */
+typedef struct {
+    int64_t rows, experts;
+    int32_t k, dtype, score;
+    int32_t groups, top_groups, group_best;    /* groups 0 or 1: none */
+    int32_t renormalize;
+    float scale;
+    const void* logits;          /* rows x experts */
+    const float* bias;           /* experts, may be null */
+    float* weights;              /* rows x k */
+    int32_t *chosen;             /* rows x k */
+    int32_t *offsets, *place;    /* experts + 1, rows x k; may be null */
+    int64_t ld;
+} ccl_route_t;
+
+/* Gradient of the logits from that of the weights, the choices held fixed.
+ * Choices of -1 have none; an expert chosen twice gets the sum. */
+typedef struct {
+    int64_t rows, experts;
+    int32_t k, dtype, score, renormalize;
+    float scale;
+    int32_t reserved;
+    const void* logits;
+    const int32_t* chosen;
+    const float* dweights;
+    void* dlogits;               /* rows x experts, the type of logits */
+    int64_t ld, ldd;
+} ccl_route_grad_t;
+
+/*
+ * The order that the expert products want: slots (choice j of row t is slot
+ * t * k + j) sorted by expert, those of one expert in order.  place[s] is the
+ * position of slot s, -1 where chosen[s] is negative (no expert, or one that
+ * lives elsewhere); expert e owns positions offsets[e] .. offsets[e + 1] - 1.
+ * A chosen expert beyond `experts` counts as -1 and is reported by
+ * ccl_tensor_status.
+ */
+typedef struct {
+    int64_t slots;
+    int32_t experts;
+    int32_t reserved;
+    const int32_t* chosen;
+    int32_t *offsets, *place;
+} ccl_expert_order_t;
+
+/*
+ * out[place[t, j]] = x[t] for every choice j of every row t.  Places are
+ * distinct, as ccl_expert_order makes them.  Rows of out that no place names
+ * are not written, negative places are passed over, and places from `count` on
+ * are passed over and reported by ccl_tensor_status.  The gradient is
+ * ccl_combine without weights.
+ */
+typedef struct {
+    int64_t rows, count, h;      /* rows of x, rows of out, elements of a row */
+    int32_t k, dtype;
+    const void* x;
+    const int32_t* place;        /* rows x k */
+    void* out;
+    int64_t ldx, ldo;
+} ccl_dispatch_t;
+
+/*
+ * y[t] = sum over j of weights[t, j] r[place[t, j]] + residual[t], j ascending.
+ * weights (null: 1) and residual may be null; y may be residual (same stride).
+ * Negative places add nothing; places from `count` on add nothing and are
+ * reported.
+ */
+typedef struct {
+    int64_t rows, count, h;
+    int32_t k, dtype;
+    const void* r;               /* count x h */
+    const int32_t* place;
+    const float* weights;
+    const void* residual;
+    void* y;
+    int64_t ldr, lds, ldy;
+} ccl_combine_t;
+
+/* dr[place[t, j]] = weights[t, j] dy[t],  dweights[t, j] = <dy[t], r[place[t, j]]>
+ * (0 for choices without a place).  Either output may be null; r is read for
+ * dweights only.  Places as for ccl_dispatch.  The residual's gradient is dy. */
+typedef struct {
+    int64_t rows, count, h;
+    int32_t k, dtype;
+    const void *dy, *r;
+    const int32_t* place;
+    const float* weights;
+    void* dr;
+    float* dweights;
+    int64_t lddy, ldr, lddr;
+} ccl_combine_grad_t;
+
+/*
+ * y = (x - mean) rstd w + b by row, rstd = 1 / sqrt(var + eps), the variance
+ * summed over differences from the mean.  w and b (null: 1 and 0) have the type
+ * of x or are f32 (wdtype); mean and rstd (rows, f32, kept for the backward
+ * pass) may be null.  y may be x (same stride).
+ */
+typedef struct {
+    int64_t rows, n;
+    int32_t dtype, wdtype;
+    float eps;
+    int32_t reserved;
+    const void *x, *w, *b;
+    void* y;
+    float *mean, *rstd;
+    int64_t ldx, ldy;
+} ccl_layer_norm_t;
+
+/* xh = (x - mean) rstd, g = dy w:  dx = rstd (g - mean(g) - xh mean(g xh)),
+ * dw = sum over rows of dy xh, db = sum over rows of dy (type wdtype).  Each
+ * output may be null; none may be an operand. */
+typedef struct {
+    int64_t rows, n;
+    int32_t dtype, wdtype;
+    const void *dy, *x, *w;
+    const float *mean, *rstd;
+    void *dx, *dw, *db;
+    int64_t lddy, ldx, lddx;
+} ccl_layer_norm_grad_t;
+
+ccl_status_t ccl_route_workspace(const ccl_route_t* a, int64_t* bytes);
+ccl_status_t ccl_route(const ccl_route_t* a, void* ws, int64_t ws_bytes, void* stream);
+ccl_status_t ccl_route_grad(const ccl_route_grad_t* a, void* stream);
+ccl_status_t ccl_expert_order_workspace(const ccl_expert_order_t* a, int64_t* bytes);
+ccl_status_t ccl_expert_order(const ccl_expert_order_t* a, void* ws, int64_t ws_bytes, void* stream);
+ccl_status_t ccl_dispatch(const ccl_dispatch_t* a, void* stream);
+ccl_status_t ccl_combine(const ccl_combine_t* a, void* stream);
+ccl_status_t ccl_combine_grad(const ccl_combine_grad_t* a, void* stream);
+ccl_status_t ccl_layer_norm(const ccl_layer_norm_t* a, void* stream);
+ccl_status_t ccl_layer_norm_grad_workspace(const ccl_layer_norm_grad_t* a, int64_t* bytes);
+ccl_status_t ccl_layer_norm_grad(const ccl_layer_norm_grad_t* a, void* ws, int64_t ws_bytes, void* stream);
+
 /* Synchronize the device and report (once) what went wrong inside the tensor
- * products launched on it since the last call: CCL_ERR_TIMEOUT (a wait on the
- * device ran out; the outputs are incomplete) or CCL_ERR_INVALID_ARG (expert
- * offsets that decrease or leave the rows).  One word per device holds the first
- * failure for all callers: whoever asks takes it.  No other call looks at it. */
+ * products and the calls around them launched on it since the last call:
+ * CCL_ERR_TIMEOUT (a wait on the device ran out; the outputs are incomplete) or
+ * CCL_ERR_INVALID_ARG (expert offsets that decrease or leave the rows, places or
+ * chosen experts out of range).  One word per device for the products and one for
+ * the router and the row moves hold the first failure for all callers: whoever
+ * asks takes them (the first of them that is set).  No other call looks at them. */
 ccl_status_t ccl_tensor_status(void);
 
 const char* ccl_error_string(ccl_status_t s);
