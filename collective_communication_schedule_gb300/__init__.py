@@ -186,6 +186,16 @@ class LayerNormGrad(ctypes.Structure):
                         ("q", "lddy ldx lddx")])
 
 
+class CrossEntropy(ctypes.Structure):
+    _fields_ = _struct([("q", "rows vocab k"), ("i", "dtype target_bits"), ("q", "ignore_index"),
+                        ("p", "x w target loss lse"), ("q", "ldx ldw")])
+
+
+class CrossEntropyGrad(ctypes.Structure):
+    _fields_ = _struct([("q", "rows vocab k"), ("i", "dtype target_bits"), ("q", "ignore_index"),
+                        ("p", "x w target dloss dlse lse dx dw"), ("q", "ldx ldw lddx lddw")])
+
+
 PROBE_FN = ctypes.CFUNCTYPE(ctypes.c_double, ctypes.c_void_p, ctypes.POINTER(PlanOpts))
 
 
@@ -245,6 +255,10 @@ def _load():
         "ccl_layer_norm": [ctypes.POINTER(LayerNorm), P],
         "ccl_layer_norm_grad_workspace": [ctypes.POINTER(LayerNormGrad), ctypes.POINTER(I64_)],
         "ccl_layer_norm_grad": [ctypes.POINTER(LayerNormGrad), P, I64_, P],
+        "ccl_cross_entropy_workspace": [ctypes.POINTER(CrossEntropy), ctypes.POINTER(I64_)],
+        "ccl_cross_entropy": [ctypes.POINTER(CrossEntropy), P, I64_, P],
+        "ccl_cross_entropy_grad_workspace": [ctypes.POINTER(CrossEntropyGrad), ctypes.POINTER(I64_)],
+        "ccl_cross_entropy_grad": [ctypes.POINTER(CrossEntropyGrad), P, I64_, P],
         "ccl_orthogonalize_workspace": [ctypes.POINTER(Ortho), ctypes.POINTER(I64_)],
         "ccl_orthogonalize": [ctypes.POINTER(Ortho), P, I64_, P],
         "ccl_tensor_status": [],
@@ -1062,6 +1076,72 @@ def layer_norm_backward(dy, x, w, mean, rstd, bias=False, need_dx=True, need_dw=
         a.db = db.data_ptr()
     _run(lib.ccl_layer_norm_grad, lib.ccl_layer_norm_grad_workspace, a, device, handle)
     return dx, dw, db
+
+
+def _target(target, rows, device):
+    bits = {_torch.int64: 64, _torch.int32: 32}.get(target.dtype)
+    if bits is None:
+        raise ValueError(f"targets are int64 or int32, not {target.dtype}")
+    return _packed("target", target, (rows,), target.dtype, device), bits
+
+
+def linear_cross_entropy(x, w, target, ignore_index=-100, stream=None):
+    """Softmax cross entropy of x w^T against ``target`` (rows, int64 or int32)
+    without the logits in memory (``ccl_cross_entropy``), for x (rows, k) and w
+    (vocab, k), bf16 or f16: (loss, lse), both (rows) in f32; 0 for rows whose
+    target is ``ignore_index``.  lse, the log of the sum of exponentials, is what
+    ``linear_cross_entropy_backward`` needs."""
+    if stream is not None:
+        with _on_stream(stream):
+            return linear_cross_entropy(x, w, target, ignore_index, None)
+    torch = _torch or _lazy_torch()
+    rows, k = _rows("x", x)
+    vocab = _rows("w", w)[0]
+    device, dtype = x.device, x.dtype
+    _graphless(x, w)
+    handle = _handle(device)
+    where, bits = _target(target, rows, device)
+    a = CrossEntropy(rows, vocab, k, _type_code(dtype), bits, ignore_index)
+    a.target = where
+    a.x, a.ldx = _matrix("x", x, x.shape, dtype, device)
+    a.w, a.ldw = _matrix("w", w, (vocab, k), dtype, device)
+    loss, lse = torch.empty((2, rows), dtype=torch.float32, device=device).unbind(0)
+    a.loss, a.lse = loss.data_ptr(), lse.data_ptr()
+    _run(lib.ccl_cross_entropy, lib.ccl_cross_entropy_workspace, a, device, handle)
+    return loss, lse
+
+
+def linear_cross_entropy_backward(dloss, x, w, target, lse, dlse=None, ignore_index=-100, need_dx=True, need_dw=True,
+                                  stream=None):
+    """(dx, dw) of ``linear_cross_entropy`` (``ccl_cross_entropy_grad``) from
+    the gradients of its losses and, where they are used, of its log-sums (rows,
+    f32); an output that is not asked for is None.  Ignored rows have none."""
+    if stream is not None:
+        with _on_stream(stream):
+            return linear_cross_entropy_backward(dloss, x, w, target, lse, dlse, ignore_index, need_dx, need_dw, None)
+    torch = _torch or _lazy_torch()
+    rows, k = _rows("x", x)
+    vocab = _rows("w", w)[0]
+    device, dtype = x.device, x.dtype
+    handle = _handle(device)
+    where, bits = _target(target, rows, device)
+    a = CrossEntropyGrad(rows, vocab, k, _type_code(dtype), bits, ignore_index)
+    a.target = where
+    a.x, a.ldx = _matrix("x", x, x.shape, dtype, device)
+    a.w, a.ldw = _matrix("w", w, (vocab, k), dtype, device)
+    a.dloss = _packed("dloss", dloss, (rows,), torch.float32, device)
+    a.lse = _packed("lse", lse, (rows,), torch.float32, device)
+    if dlse is not None:
+        a.dlse = _packed("dlse", dlse, (rows,), torch.float32, device)
+    dx = dw = None
+    if need_dx:
+        dx = torch.empty((rows, k), dtype=dtype, device=device)
+        a.dx = dx.data_ptr()
+    if need_dw:
+        dw = torch.empty((vocab, k), dtype=dtype, device=device)
+        a.dw = dw.data_ptr()
+    _run(lib.ccl_cross_entropy_grad, lib.ccl_cross_entropy_grad_workspace, a, device, handle)
+    return dx, dw
 
 
 def tensor_status():

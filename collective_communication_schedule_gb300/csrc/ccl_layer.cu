@@ -388,7 +388,7 @@ ccl_status_t take_layer_status()
 {
     int st[4] = {0, 0, 0, 0};
     TRY_CUDA(cudaMemcpyFromSymbol(st, g_layer_status, sizeof(st)), "status word");
-    if (st[0] == 0) return CCL_OK;
+    if (st[0] == 0) return take_loss_status();
     const int zero[4] = {0, 0, 0, 0};
     TRY_CUDA(cudaMemcpyToSymbol(g_layer_status, zero, sizeof(zero)), "status word");
     return fail((ccl_status_t)st[0], st[1] == REPORT_PLACE ? "a place beyond the rows" : "a chosen expert beyond the experts");

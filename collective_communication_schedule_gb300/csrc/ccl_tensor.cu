@@ -75,9 +75,10 @@ static ccl_status_t device(const Device** out)
 }
 
 // Complete a product and launch it.
-static ccl_status_t run(const Device* dev, Product P, const Shape& sh, const Matrix& a, const Matrix& b, cudaStream_t stream)
+static ccl_status_t run(const Device* dev, Product P, const Shape& sh, const Matrix& a, const Matrix& b, cudaStream_t stream,
+                        const Matrix* alt = nullptr)
 {
-    TRY(complete(dev, &P, sh, a, b));
+    TRY(complete(dev, &P, sh, a, b, alt));
     const int size = sh.cg == 2 ? 2 : sh.split;
     const int bytes = (kTileM + P.bn / sh.cg) * kSliceK * 2;
     const int fixed = 1024 + kStagingBytes + (sh.split > 1 ? P.bn * kTileM * 4 : 0);
@@ -86,6 +87,14 @@ static ccl_status_t run(const Device* dev, Product P, const Shape& sh, const Mat
     const int clusters = std::min(P.total, dev->sms / size);
     return launch(kKernels[sh.cg - 1][P.b_mn ? BOTH_MN : P.a_mn ? A_MN : BOTH_K], dim3((unsigned)(clusters * size)),
                   kThreads, smem, stream, P, size);
+}
+
+ccl_status_t run_product(const Product& P, const Shape& sh, const Matrix& a, const Matrix& b, const Matrix* alt,
+                         cudaStream_t stream)
+{
+    const Device* dev = nullptr;
+    TRY(device(&dev));
+    return run(dev, P, sh, a, b, stream, alt);
 }
 
 // Launch a pair of products that do not depend on each other.

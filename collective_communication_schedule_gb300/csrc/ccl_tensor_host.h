@@ -26,8 +26,9 @@ namespace tensor {
         if (s_ != CCL_OK) return s_;              \
     } while (0)
 
-// what the router and the row moves have reported on this device (and take it back)
+// what the router and the row moves, then the cross entropy, have reported on this device (and take it back)
 ccl_status_t take_layer_status();
+ccl_status_t take_loss_status();
 
 inline int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 inline bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }

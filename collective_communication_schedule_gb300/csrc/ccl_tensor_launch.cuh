@@ -119,7 +119,7 @@ struct Choices {
     Shape single, pairs;           // beside another product in one launch: of single threadblocks, of pairs
 };
 
-inline Choices choose(const Product& P, int sms)
+inline Choices choose(const Product& P, int sms, int max_split = 8)
 {
     const bool ragged_rows = P.ragged == RAGGED_ROWS, ragged_reduce = P.ragged == RAGGED_REDUCE;
     const int64_t rows = ragged_rows ? std::max(1, P.n / P.groups) : P.n;
@@ -140,7 +140,7 @@ inline Choices choose(const Product& P, int sms)
             const double bytes = (kTileM + bn / cg) * 128.0;
             const double busy = (double)std::min<int64_t>(tiles * cg, sms);
             const double block = 400 + 16.0 * std::min<int64_t>(bn, rows);
-            for (int split = 1; split <= (cg == 2 || P.symmetric ? 1 : 8); split *= 2) {
+            for (int split = 1; split <= (cg == 2 || P.symmetric ? 1 : max_split); split *= 2) {
                 if (split > 1 && (split * 2 > slices || tiles * split > 2 * sms)) break;
                 const double slice = std::max(std::max(cg == 2 ? 150 + 1.85 * bn : 130 + 2.8 * bn, bytes / 68),
                                               bytes * std::min<double>(sms, busy * split) / 8000);
@@ -162,8 +162,9 @@ inline Choices choose(const Product& P, int sms)
     return c;
 }
 
-// Complete a product for a shape: tiles and maps.
-[[maybe_unused]] static ccl_status_t complete(const Device* dev, Product* P, const Shape& sh, const Matrix& a, const Matrix& b)
+// Complete a product for a shape: tiles and maps.  alt: A as P->alt's flag has it read.
+[[maybe_unused]] static ccl_status_t complete(const Device* dev, Product* P, const Shape& sh, const Matrix& a, const Matrix& b,
+                                              const Matrix* alt = nullptr)
 {
     set_vec(P);
     P->bn = sh.bn;
@@ -184,9 +185,10 @@ inline Choices choose(const Product& P, int sms)
     P->total = (int32_t)most;
     TRY(encode(dev, &P->ma, a, 64, P->a_mn ? kSliceK : kTileM));
     TRY(encode(dev, &P->mb, b, 64, P->b_mn ? kSliceK : P->bn / sh.cg));
+    if (alt) TRY(encode(dev, &P->mp, *alt, 64, P->a_mn ? kSliceK : kTileM));
     if (sh.split == 1) {
         const int64_t count = P->ragged == RAGGED_ROWS ? 1 : P->groups;
-        P->tma_out = vectors(P->out, P->ld_out, P->bs_out);
+        P->tma_out = P->out && vectors(P->out, P->ld_out, P->bs_out);
         if (P->tma_out)
             TRY(encode(dev, &P->mo, Matrix{P->out, P->n, P->m, P->ld_out, count, P->bs_out}, 32, kBlockRows,
                        CU_TENSOR_MAP_SWIZZLE_NONE));
@@ -194,11 +196,15 @@ inline Choices choose(const Product& P, int sms)
         if (P->tma_pre)
             TRY(encode(dev, &P->mp, Matrix{P->pre, P->n, P->m, P->ld_pre}, 32, kBlockRows, CU_TENSOR_MAP_SWIZZLE_NONE));
         const bool pieces = P->c && vectors(P->c, P->ld_c, P->bs_c) && (P->m % 8 == 0 || P->pad_c);
-        P->fast = P->tma_out && !P->pre && (!P->c || (pieces && P->act == CCL_ACT_NONE));
+        P->fast = P->tma_out && !P->pre && !P->sum && (!P->c || (pieces && P->act == CCL_ACT_NONE));
     }
     if (P->symmetric && !P->fast) return fail(CCL_ERR_INTERNAL, "a symmetric product whose rows TMA cannot store");
     return CCL_OK;
 }
+
+// A single product on the current device (ccl_tensor.cu).
+ccl_status_t run_product(const Product& P, const Shape& sh, const Matrix& a, const Matrix& b, const Matrix* alt,
+                         cudaStream_t stream);
 
 }  // namespace tensor
 }  // namespace ccl

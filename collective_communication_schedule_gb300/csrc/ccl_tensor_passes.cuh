@@ -180,7 +180,7 @@ static __global__ void __launch_bounds__(256) bias_grad_kernel(const GradPass G)
 
 // The same sums in the same order beside the products of a pair, 32 columns of
 // one expert at a time.
-__device__ __noinline__ void add_chunks(const GradPass& G, int lane)
+[[maybe_unused]] static __device__ __noinline__ void add_chunks(const GradPass& G, int lane)
 {
     const int columns = (G.n + 31) / 32;
     for (int item = blockIdx.x; item < G.groups * columns; item += gridDim.x) {

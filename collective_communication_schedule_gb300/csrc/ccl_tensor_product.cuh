@@ -88,6 +88,10 @@ struct Scalars {
     const uint16_t *c, *bias;
     const float *alpha_of, *beta_of;   // device factors per batch entry (may be null)
     int64_t ld_out, bs_out, ld_pre, ld_c, bs_c, bs_bias;
+    float* sum;                    // SUM_PAIR: an output that grows over several launches, in 32 bits (may be null)
+    int64_t ld_sum;
+    int32_t sum_first, sum_last;   // nothing in it yet; the rounded result goes to out
+    const int32_t* alt;            // device word: not 0 if A is to be read through mp (may be null)
 };
 
 struct Product : Scalars {
@@ -102,6 +106,19 @@ struct Pair {
     int32_t width, stages;         // the wider tile's rows; stages of that width
     GradPass sums;                 // sums.db: null if there is no bias gradient
     Product p[2];
+};
+
+// A product x w^T whose lanes are rows of x, for what is done with a row of
+// its values where they are made, in 32 bits (the values themselves are stored
+// nowhere): STATS its sum of exponentials, SLOPE the derivative of a loss.
+struct Rowwise {
+    Product p;                     // A: rows of x, B: rows of w
+    const void* target;            // STATS: rows' targets, whose values go to `picked`
+    int32_t wide;                  // targets of 64 bits
+    float* picked;
+    float2* part;                  // STATS: a row's largest value and sum of exp(value - largest), by row tile of B
+    const float4* coef;            // SLOPE: log-sum, a, b, target
+    int32_t first;                 // SLOPE: the number of the first row of B
 };
 
 struct TileAt {
@@ -282,6 +299,14 @@ __device__ __forceinline__ void fetch_c(const Scalars& P, uint16_t c[kBlockRows]
     for (int i = 0; i < kBlockRows; ++i, p += P.ld_c) c[i] = f < P.m && i < nrows ? __ldcg(p) : (uint16_t)0;
 }
 
+// The same of an output's sum so far, 128 neighbouring bytes a row and warp.
+__device__ __forceinline__ void fetch_sum(const Scalars& P, float* v, int64_t row, int nrows, int f)
+{
+    const float* p = P.sum + row * P.ld_sum + f;
+#pragma unroll
+    for (int i = 0; i < kBlockRows; ++i, p += P.ld_sum) v[i] = f < P.m && i < nrows ? __ldcg(p) : 0.f;
+}
+
 // A block of 16 rows x 32 features (one feature per lane, two rows per word)
 // to global memory: through shared memory and a TMA store where the whole
 // block may be written (the parts of it outside the matrix are cut off by
@@ -409,8 +434,11 @@ __device__ __forceinline__ void fast_blocks(const Scalars& P, const CUtensorMap*
 // FORM: storage of the operands (a pair: A_MN, then BOTH_MN)
 enum { BOTH_K = 0, A_MN = 1, BOTH_MN = 2 };
 
-// MODE: one product, or the two of a Pair
-enum { SINGLE = 0, PAIR = 1 };
+// MODE: one product, the two of a Pair, those with an output that grows over
+// several launches, or a Rowwise one
+enum { SINGLE = 0, PAIR = 1, SUM_PAIR = 2, STATS = 3, SLOPE = 4 };
+__host__ __device__ constexpr bool is_pair(int mode) { return mode == PAIR || mode == SUM_PAIR; }
+__host__ __device__ constexpr bool is_rowwise(int mode) { return mode == STATS || mode == SLOPE; }
 
 template <int MODE>
 struct Sequence {
@@ -421,8 +449,7 @@ struct Sequence {
     __device__ int phases() const { return 1; }
     __device__ const Product& at(int) const { return *list; }
 };
-template <>
-struct Sequence<PAIR> {
+struct PairSequence {
     const Pair* pair;
     __device__ int width() const { return pair->width; }
     __device__ int stages() const { return pair->stages; }
@@ -430,6 +457,106 @@ struct Sequence<PAIR> {
     __device__ int phases() const { return 2; }
     __device__ const Product& at(int ph) const { return pair->p[ph]; }
 };
+template <>
+struct Sequence<PAIR> : PairSequence {};
+template <>
+struct Sequence<SUM_PAIR> : PairSequence {};
+struct RowwiseSequence {
+    const Rowwise* rows;
+    __device__ int width() const { return rows->p.bn; }
+    __device__ int stages() const { return rows->p.stages; }
+    __device__ int split() const { return 1; }
+    __device__ int phases() const { return 1; }
+    __device__ const Product& at(int) const { return rows->p; }
+};
+template <>
+struct Sequence<STATS> : RowwiseSequence {};
+template <>
+struct Sequence<SLOPE> : RowwiseSequence {};
+
+__device__ __forceinline__ float exp2_fast(float x)      // within 2^-22
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+// The largest value and the sum of exp(value - largest) of two parts.
+__device__ __forceinline__ float2 join(float2 a, float2 b)
+{
+    const float m = fmaxf(a.x, b.x), z = m == -INFINITY ? 0.f : m;      // (nothing but -Inf: 0 of them)
+    return make_float2(m, a.y * exp2_fast((a.x - z) * kLog2e) + b.y * exp2_fast((b.x - z) * kLog2e));
+}
+
+// A warp's 32 rows of a tile, 16 columns at a time and every fourth 16 of them:
+// largest value and sum of exponentials so far, and the target's value.  at:
+// the target's column in the tile.
+__device__ __forceinline__ float2 stats_blocks(uint32_t from, int first, int live, int stride, int at, float* picked)
+{
+    float2 s = make_float2(-INFINITY, 0.f);
+#pragma unroll 1
+    for (int c = first; c < live; c += stride) {
+        uint32_t u[kBlockRows];
+        float v[kBlockRows];
+        tmem_load16(from + c, u);
+#pragma unroll
+        for (int i = 0; i < kBlockRows; ++i) v[i] = c + i < live ? __uint_as_float(u[i]) : -INFINITY;
+        float m = s.x;
+#pragma unroll
+        for (int i = 0; i < kBlockRows; ++i) m = fmaxf(m, v[i]);
+        // (the difference first: it is exact near the largest value, where m log2 e would round)
+        const float z = m == -INFINITY ? 0.f : m;
+        if ((unsigned)(at - c) < (unsigned)kBlockRows) {
+            float p = 0.f;
+#pragma unroll
+            for (int i = 0; i < kBlockRows; ++i) p = at - c == i ? v[i] : p;
+            *picked = p;
+        }
+        // added up as a tree: small terms beside a large one lose few digits
+#pragma unroll
+        for (int i = 0; i < kBlockRows; ++i) v[i] = exp2_fast((v[i] - z) * kLog2e);
+#pragma unroll
+        for (int d = kBlockRows / 2; d; d /= 2)
+#pragma unroll
+            for (int i = 0; i < d; ++i) v[i] += v[i + d];
+        s.y = fmaf(s.y, exp2_fast((s.x - z) * kLog2e), v[0]);
+        s.x = m;
+        __syncwarp();
+    }
+    return s;
+}
+
+// The same walk for dl = a exp(value - log-sum) - b [column = target], rounded
+// to 16 bits: 32 neighbouring bytes of a row a lane.  A row that counts for
+// nothing (a = b = 0) gives 0 whatever its values are.
+template <bool BF>
+__device__ __forceinline__ void slope_blocks(uint32_t from, int first, int live, int stride, float4 k, int at, uint16_t* out)
+{
+    const bool dead = k.y == 0.f && k.z == 0.f;
+#pragma unroll 1
+    for (int c = first; c < live; c += stride) {
+        uint32_t u[kBlockRows];
+        float v[kBlockRows];
+        tmem_load16(from + c, u);
+#pragma unroll
+        for (int i = 0; i < kBlockRows; ++i) v[i] = k.y * exp2_fast((__uint_as_float(u[i]) - k.x) * kLog2e);
+        if ((unsigned)(at - c) < (unsigned)kBlockRows) {
+#pragma unroll
+            for (int i = 0; i < kBlockRows; ++i) v[i] -= at - c == i ? k.z : 0.f;
+        }
+        if (dead) {
+#pragma unroll
+            for (int i = 0; i < kBlockRows; ++i) v[i] = 0.f;
+        }
+        if (out) {
+            uint4* p = reinterpret_cast<uint4*>(out + c);
+            p[0] = make_uint4(pack2<BF>(v[0], v[1]), pack2<BF>(v[2], v[3]), pack2<BF>(v[4], v[5]), pack2<BF>(v[6], v[7]));
+            p[1] = make_uint4(pack2<BF>(v[8], v[9]), pack2<BF>(v[10], v[11]), pack2<BF>(v[12], v[13]), pack2<BF>(v[14], v[15]));
+        }
+        __syncwarp();
+    }
+}
 
 // A threadblock's share of the tiles of a sequence of products.
 template <int CG, int FORM, int MODE>
@@ -471,7 +598,7 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
     }
     if (seq.at(0).offsets) wait_for_previous();
     prepare_tiles(seq.at(0), &sh);
-    if (MODE == PAIR && threadIdx.x == 0) {
+    if (is_pair(MODE) && threadIdx.x == 0) {
         const int total = seq.at(0).ragged == RAGGED_ROWS ? sh.total : seq.at(0).total;
         sh.second = (cluster + clusters - total % clusters) % clusters;
     }
@@ -507,7 +634,7 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
         int begin, end;
     };
     auto next_run = [&](const Scalars& P, int ph) {
-        return Run{MODE == PAIR && ph ? sh.second : cluster, P.ragged == RAGGED_ROWS ? sh.total : P.total};
+        return Run{is_pair(MODE) && ph ? sh.second : cluster, P.ragged == RAGGED_ROWS ? sh.total : P.total};
     };
 
     const uint32_t ring = smem_addr(dyn), full0 = smem_addr(sh.full), empty0 = smem_addr(sh.empty);
@@ -526,8 +653,8 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
                 tma_prefetch(&seq.at(ph + 1).ma);
                 tma_prefetch(&seq.at(ph + 1).mb);
             }
-            const bool a_mn = MODE == PAIR || FORM != BOTH_K;
-            const bool b_mn = MODE == PAIR ? ph == 1 : FORM == BOTH_MN;
+            const bool a_mn = is_pair(MODE) || FORM != BOTH_K;
+            const bool b_mn = is_pair(MODE) ? ph == 1 : FORM == BOTH_MN;
             const uint32_t bytes_b = P.bn / CG * kSliceK * 2;
             const uint32_t part_b = bytes_b / 2;      // one of a slice's two halves of B (reduction 0..63, 64..127)
             const uint32_t bytes = bytes_a + bytes_b;
@@ -538,6 +665,8 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
             const Run run = next_run(P, ph);
             if (run.begin < run.end) q = tile_at<CG>(P, &sh, run.begin);
             if (ph == 0) wait_for_previous();
+            const CUtensorMap* map_a = &maps.ma;
+            if ((MODE == SUM_PAIR || (MODE == SINGLE && FORM == BOTH_MN)) && P.alt && *P.alt) map_a = &maps.mp;
             for (int t = run.begin; t < run.end; t += clusters) {
                 if (t != run.begin) q = tile_at<CG>(P, &sh, t);
                 const int m0 = q.m0 + (CG == 2 ? rank * kTileM : 0);
@@ -569,11 +698,11 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
                                 tma_load_pair(dst, map, bar, x, y, z);
                         };
                         if (a_mn) {
-                            load(a, &maps.ma, m0, q.k0 + k, q.za);
-                            load(a + kSliceK * 128, &maps.ma, m0 + 64, q.k0 + k, q.za);
+                            load(a, map_a, m0, q.k0 + k, q.za);
+                            load(a + kSliceK * 128, map_a, m0 + 64, q.k0 + k, q.za);
                         } else {
-                            load(a, &maps.ma, k, m0, q.za);
-                            load(a + kTileM * 128, &maps.ma, k + 64, m0, q.za);
+                            load(a, map_a, k, m0, q.za);
+                            load(a + kTileM * 128, map_a, k + 64, m0, q.za);
                         }
                         if (b_mn) {
                             for (int i = 0; i < bn / CG; i += 64)
@@ -610,8 +739,8 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
             bool good = true;
             for (int ph = 0; ph < phases; ++ph) {
                 const Scalars P = seq.at(ph);
-                const bool a_mn = MODE == PAIR || FORM != BOTH_K;
-                const bool b_mn = MODE == PAIR ? ph == 1 : FORM == BOTH_MN;
+                const bool a_mn = is_pair(MODE) || FORM != BOTH_K;
+                const bool b_mn = is_pair(MODE) ? ph == 1 : FORM == BOTH_MN;
                 const uint32_t bytes_b = P.bn / CG * kSliceK * 2;
                 const uint32_t part_b = bytes_b / 2;      // one of a slice's two halves of B (reduction 0..63, 64..127)
                 const bool reduce_rows = b_mn && P.ragged == RAGGED_REDUCE;
@@ -667,7 +796,7 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
             }
         }
         __syncwarp();
-    } else if (warp == 3 && (MODE == PAIR || FORM == BOTH_MN) && seq.at(phases - 1).ragged == RAGGED_REDUCE) {
+    } else if (warp == 3 && (is_pair(MODE) || FORM == BOTH_MN) && seq.at(phases - 1).ragged == RAGGED_REDUCE) {
         // 0 x Inf or NaN would not be 0: both operands are cleared
         int it = 0;
         uint32_t flips = 0;
@@ -730,7 +859,56 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
                 const int acc = done & 1;
                 const int feat = q.m0 + (CG == 2 ? rank * kTileM : 0) + quad * 32, nfeat = P.m - feat, f = feat + lane;
                 const int64_t row = (int64_t)q.row0 + q.n0;
-                const float alpha = P.alpha * (kAll && P.alpha_of ? P.alpha_of[q.g] : 1.f);
+                if constexpr (is_rowwise(MODE)) {
+                    // lanes are rows of x, columns the rows of w
+                    const Rowwise& R = *seq.rows;
+                    const bool own = f < P.m;
+                    int at = -1;               // the target's column in this tile (elsewhere: none)
+                    float4 coef = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (own && MODE == STATS) {
+                        const int64_t target = R.wide ? ((const int64_t*)R.target)[f] : ((const int32_t*)R.target)[f];
+                        if (target >= q.n0 && target < q.n0 + q.live) at = (int)(target - q.n0);
+                    }
+                    if (own && MODE == SLOPE) {
+                        coef = R.coef[f];
+                        at = __float_as_int(coef.w) - R.first - q.n0;
+                    }
+                    if (!__all_sync(~0u, bar_wait(smem_addr(&sh.acc_full[acc]), (done >> 1) & 1, failed))) break;
+                    fence_after();
+                    const uint32_t from = tmem + ((uint32_t)(quad * 32) << 16) + acc * width;
+                    float2 part;
+                    if (MODE == STATS) {
+                        part = stats_blocks(from, slot * kBlockRows, q.live, kStride, at, R.picked + f);
+                    } else {
+                        uint16_t* out = own ? P.out + f * P.ld_out + q.n0 : nullptr;
+                        if (P.out_bf)
+                            slope_blocks<true>(from, slot * kBlockRows, q.live, kStride, coef, at, out);
+                        else
+                            slope_blocks<false>(from, slot * kBlockRows, q.live, kStride, coef, at, out);
+                    }
+                    fence_before();
+                    if (lane == 0) {
+                        if (CG == 2)
+                            bar_arrive_cluster(release[acc]);
+                        else
+                            bar_arrive(release[acc]);
+                    }
+                    if (MODE == STATS) {
+                        // the four warps of these rows put their parts together (in turn in two places: the next
+                        // tile's parts do not meet this one's)
+                        float2* parts = reinterpret_cast<float2*>(staging) + acc * (4 * kTileM) + quad * 32 + lane;
+                        parts[slot * kTileM] = part;
+                        named_sync(3 + quad, 128);
+                        if (slot == 0) {
+#pragma unroll
+                            for (int i = 1; i < 4; ++i) part = join(part, parts[i * kTileM]);
+                            if (own) R.part[(int64_t)(q.n0 / P.bn) * P.m + f] = part;
+                        }
+                    }
+                    ++done;
+                    continue;
+                }
+                const float alpha = P.alpha * ((kAll || MODE == SUM_PAIR) && P.alpha_of ? P.alpha_of[q.g] : 1.f);
                 const float beta = P.beta * (P.beta_of ? P.beta_of[q.g] : 1.f);
                 const float bias = kAll && P.bias && f < P.m ? load1(P.bias + q.g * P.bs_bias + f, P.in_bf) : 0.f;
                 const bool whole = P.ragged != RAGGED_ROWS;
@@ -742,6 +920,10 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
                 uint16_t cv[kBlockRows];
                 // the general way reads C a block ahead of its use, the short way reads it by itself
                 if (kAll && P.c && size == CG && !short_to) fetch_c(P, cv, q.g, row + c, q.live - c, f);
+                // so far, of an output that grows over several launches: read a block ahead too
+                const bool grown = MODE == SUM_PAIR && P.sum && !P.sum_first;
+                float so_far[MODE == SUM_PAIR ? kBlockRows : 1];
+                if (grown) fetch_sum(P, so_far, row + c, q.live - c, f);
                 if (some) {
                     if (!__all_sync(~0u, bar_wait(smem_addr(&sh.acc_full[acc]), (done >> 1) & 1, failed))) break;
                     fence_after();
@@ -801,6 +983,20 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
                     uint32_t w[kBlockRows / 2];
 #pragma unroll
                     for (int i = 0; i < kBlockRows; ++i) v[i] = fmaf(alpha, __uint_as_float(u[i]), bias);
+                    if (MODE == SUM_PAIR && P.sum) {
+                        if (grown) {
+#pragma unroll
+                            for (int i = 0; i < kBlockRows; ++i) v[i] += so_far[MODE == SUM_PAIR ? i : 0];
+                            if (c + kStride < q.live) fetch_sum(P, so_far, row + c + kStride, nrows - kStride, f);
+                        }
+                        if (!P.sum_last) {
+                            float* p = P.sum + (row + c) * P.ld_sum + f;
+#pragma unroll
+                            for (int i = 0; i < kBlockRows; ++i, p += P.ld_sum)
+                                if (f < P.m && i < nrows) *p = v[i];
+                            continue;
+                        }
+                    }
                     if (kAll && P.pre) {
                         pack_block(v, w, P.in_bf);
                         store_block(&maps.mp, P.pre + (row + c) * P.ld_pre + f, P.ld_pre, w, st,
@@ -913,7 +1109,17 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 template <int CG>
 __global__ void __launch_bounds__(kThreads, 1) pair_kernel(const __grid_constant__ Pair P)
 {
-    products<CG, A_MN, PAIR>({&P});
+    products<CG, A_MN, PAIR>({{&P}});
+}
+template <int CG>
+__global__ void __launch_bounds__(kThreads, 1) sum_pair_kernel(const __grid_constant__ Pair P)
+{
+    products<CG, A_MN, SUM_PAIR>({{&P}});
+}
+template <int CG, int MODE>
+__global__ void __launch_bounds__(kThreads, 1) rowwise_kernel(const __grid_constant__ Rowwise R)
+{
+    products<CG, BOTH_K, MODE>({{&R}});
 }
 
 }  // namespace tensor

@@ -1001,6 +1001,54 @@ typedef struct {
     int64_t lddy, ldx, lddx;
 } ccl_layer_norm_grad_t;
 
+/*
+ * Softmax cross entropy of the values x w^T (rows x vocab) against a target
+ * class per row, without the values in memory:
+ *   lse = log sum over v of exp(x w_v),  loss = lse - x w_target.
+ * Rows whose target is ignore_index count for nothing: loss and lse 0.  A target
+ * that is neither that nor within the vocabulary counts as ignored and is
+ * reported by ccl_tensor_status.  Values and sums are 32 bits.  x and w are bf16 or
+ * f16; lse (may be null) is kept for the backward pass.  The order of the sums is
+ * fixed by the sizes.
+ */
+typedef struct {
+    int64_t rows, vocab, k;
+    int32_t dtype;
+    int32_t target_bits;         /* 32 or 64: the type of target */
+    int64_t ignore_index;
+    const void *x, *w, *target;
+    float *loss, *lse;
+    int64_t ldx, ldw;
+} ccl_cross_entropy_t;
+
+/*
+ * Gradients of ccl_cross_entropy from those of loss and lse (dlse may be null: 0):
+ *   dl = (dloss + dlse) softmax(x w^T) - dloss onehot(target),
+ *   dx = dl w,  dw = dl^T x,
+ * with the softmax computed again from lse.  Ignored rows have dl = 0 whatever x
+ * and lse hold.  dl is rounded to the element type between the products, as
+ * ccl_linear_grad rounds dz (f16: scaled by a power of two so that the largest
+ * |dloss|, |dloss + dlse| of a row is just below 2^14; it keeps what is down to
+ * 2^-38 of that).  The vocabulary is taken in pieces whose dl fits 256 MB of the
+ * workspace (1024 classes at least); dx is summed over pieces in 32 bits.  dx
+ * or dw may be null; neither may overlap the other or an operand.
+ */
+typedef struct {
+    int64_t rows, vocab, k;
+    int32_t dtype;
+    int32_t target_bits;
+    int64_t ignore_index;
+    const void *x, *w, *target;
+    const float *dloss, *dlse, *lse;
+    void *dx, *dw;
+    int64_t ldx, ldw, lddx, lddw;
+} ccl_cross_entropy_grad_t;
+
+ccl_status_t ccl_cross_entropy_workspace(const ccl_cross_entropy_t* a, int64_t* bytes);
+ccl_status_t ccl_cross_entropy(const ccl_cross_entropy_t* a, void* ws, int64_t ws_bytes, void* stream);
+ccl_status_t ccl_cross_entropy_grad_workspace(const ccl_cross_entropy_grad_t* a, int64_t* bytes);
+ccl_status_t ccl_cross_entropy_grad(const ccl_cross_entropy_grad_t* a, void* ws, int64_t ws_bytes, void* stream);
+
 ccl_status_t ccl_route_workspace(const ccl_route_t* a, int64_t* bytes);
 ccl_status_t ccl_route(const ccl_route_t* a, void* ws, int64_t ws_bytes, void* stream);
 ccl_status_t ccl_route_grad(const ccl_route_grad_t* a, void* stream);
@@ -1016,10 +1064,11 @@ ccl_status_t ccl_layer_norm_grad(const ccl_layer_norm_grad_t* a, void* ws, int64
 /* Synchronize the device and report (once) what went wrong inside the tensor
  * products and the calls around them launched on it since the last call:
  * CCL_ERR_TIMEOUT (a wait on the device ran out; the outputs are incomplete) or
- * CCL_ERR_INVALID_ARG (expert offsets that decrease or leave the rows, places or
- * chosen experts out of range).  One word per device for the products and one for
- * the router and the row moves hold the first failure for all callers: whoever
- * asks takes them (the first of them that is set).  No other call looks at them. */
+ * CCL_ERR_INVALID_ARG (expert offsets that decrease or leave the rows, places,
+ * chosen experts or targets out of range).  One word per device each for the
+ * products, the router with the row moves, and the cross entropy holds the first
+ * failure for all callers: whoever asks takes the first of them that is set.  No
+ * other call looks at them. */
 ccl_status_t ccl_tensor_status(void);
 
 const char* ccl_error_string(ccl_status_t s);

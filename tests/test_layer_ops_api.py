@@ -1,5 +1,5 @@
-"""Refusals, workspace sizes and struct layouts of the router, the row moves and
-the norm (no GPU needed: arguments are checked before any device is touched)."""
+"""Refusals, workspace sizes and struct layouts of the router, the row moves, the
+norm and the cross entropy (no GPU needed: arguments are checked before any device is touched)."""
 import ctypes
 import os
 import shutil
@@ -34,7 +34,11 @@ combine_grad = maker(ccl.CombineGrad, rows=4, count=8, h=32, k=2, dtype=ccl.F16,
 norm = maker(ccl.LayerNorm, rows=4, n=32, dtype=ccl.BF16, wdtype=ccl.F32, eps=1e-5, x=A, w=2 * A, b=3 * A, y=4 * A)
 norm_grad = maker(ccl.LayerNormGrad, rows=4, n=32, dtype=ccl.BF16, wdtype=ccl.BF16, dy=A, x=2 * A, w=3 * A, mean=4 * A,
                   rstd=5 * A, dx=6 * A, dw=7 * A, db=8 * A)
-WITH_WORKSPACE = {"ccl_route", "ccl_expert_order", "ccl_layer_norm_grad"}
+ce = maker(ccl.CrossEntropy, rows=40, vocab=100, k=32, dtype=ccl.BF16, target_bits=64, ignore_index=-100, x=A, w=2 * A,
+           target=3 * A, loss=4 * A, lse=5 * A)
+ce_grad = maker(ccl.CrossEntropyGrad, rows=40, vocab=100, k=32, dtype=ccl.F16, target_bits=32, ignore_index=-100, x=A, w=2 * A,
+                target=3 * A, dloss=4 * A, lse=5 * A, dx=6 * A, dw=7 * A)
+WITH_WORKSPACE = {"ccl_route", "ccl_expert_order", "ccl_layer_norm_grad", "ccl_cross_entropy", "ccl_cross_entropy_grad"}
 
 
 def code(name, a, ws=64 * A, size=1 << 40):
@@ -108,6 +112,27 @@ REFUSED = [
     ("ccl_layer_norm_grad", norm_grad(dx=2 * A), INVALID, "also"),
     ("ccl_layer_norm_grad", norm_grad(dw=8 * A), INVALID, "also"),
     ("ccl_layer_norm_grad", norm_grad(dw=3 * A), INVALID, "also"),
+    ("ccl_cross_entropy", ce(dtype=ccl.F32), UNSUPPORTED, "bf16 and f16"),
+    ("ccl_cross_entropy", ce(rows=-1), INVALID, "sizes"),
+    ("ccl_cross_entropy", ce(vocab=0), INVALID, "sizes"),
+    ("ccl_cross_entropy", ce(vocab=(1 << 30) + 1), INVALID, "sizes"),
+    ("ccl_cross_entropy", ce(k=0), INVALID, "sizes"),
+    ("ccl_cross_entropy", ce(target_bits=16), INVALID, "32 nor 64"),
+    ("ccl_cross_entropy", ce(ldw=31), INVALID, "w stride"),
+    ("ccl_cross_entropy", ce(x=None), INVALID, "x is null"),
+    ("ccl_cross_entropy", ce(target=None), INVALID, "target is null"),
+    ("ccl_cross_entropy", ce(target=3 * A + 4), INVALID, "not aligned"),
+    ("ccl_cross_entropy", ce(loss=None), INVALID, "loss is null"),
+    ("ccl_cross_entropy", ce(loss=5 * A), INVALID, "also"),
+    ("ccl_cross_entropy", ce(lse=3 * A), INVALID, "also"),
+    ("ccl_cross_entropy_grad", ce_grad(dtype=ccl.F32), UNSUPPORTED, "bf16 and f16"),
+    ("ccl_cross_entropy_grad", ce_grad(lse=None), INVALID, "lse is null"),
+    ("ccl_cross_entropy_grad", ce_grad(dloss=None), INVALID, "dloss is null"),
+    ("ccl_cross_entropy_grad", ce_grad(dlse=A + 2), INVALID, "not aligned"),
+    ("ccl_cross_entropy_grad", ce_grad(dx=A), INVALID, "also"),
+    ("ccl_cross_entropy_grad", ce_grad(dw=2 * A), INVALID, "also"),
+    ("ccl_cross_entropy_grad", ce_grad(dw=6 * A), INVALID, "also"),
+    ("ccl_cross_entropy_grad", ce_grad(lddw=16), INVALID, "dw stride"),
 ]
 
 
@@ -129,6 +154,15 @@ def test_workspaces_are_asked_for_and_checked():
     assert need("ccl_expert_order", order()) > 0 and need("ccl_expert_order", order(slots=100)) == 0
     assert need("ccl_layer_norm_grad", norm_grad()) >= 2 * 32 * 4
     assert need("ccl_layer_norm_grad", norm_grad(dw=None, db=None)) == 0
+    assert need("ccl_cross_entropy", ce()) >= 40 * 8
+    assert need("ccl_cross_entropy", ce(rows=0)) == 0 and need("ccl_cross_entropy_grad", ce_grad(rows=0)) == 0
+    assert need("ccl_cross_entropy_grad", ce_grad(dx=None, dw=None)) == 0
+    assert need("ccl_cross_entropy", ce(k=33)) >= need("ccl_cross_entropy", ce(k=40)) + 140 * 40 * 2
+    # the derivatives of a piece of the vocabulary, and dx's sum: never those of all of it
+    size = dict(rows=8192, vocab=1 << 20, k=1024)
+    assert need("ccl_cross_entropy_grad", ce_grad(**size)) < (256 << 20) + 8192 * (1024 * 6 + 64) + (1 << 20)
+    assert code("ccl_cross_entropy_grad", ce_grad(), ws=None, size=0) == INVALID
+    assert "workspace" in ccl.lib.ccl_last_error_detail().decode()
     assert code("ccl_expert_order", order(), ws=None, size=0) == INVALID
     assert "workspace" in ccl.lib.ccl_last_error_detail().decode()
     assert code("ccl_layer_norm_grad", norm_grad(), ws=64 * A + 16) == INVALID
@@ -144,9 +178,11 @@ def test_empty_calls_need_no_device():
     assert code("ccl_combine", combine(rows=0)) == 0
     assert code("ccl_combine_grad", combine_grad(dr=None, dweights=None)) == 0
     assert code("ccl_layer_norm", norm(rows=0)) == 0
+    assert code("ccl_cross_entropy", ce(rows=0)) == 0
+    assert code("ccl_cross_entropy_grad", ce_grad(dx=None, dw=None)) == 0
     assert code("ccl_layer_norm_grad", norm_grad(dx=None, dw=None, db=None)) == 0
     for name in ("ccl_route", "ccl_route_grad", "ccl_expert_order", "ccl_dispatch", "ccl_combine", "ccl_combine_grad",
-                 "ccl_layer_norm", "ccl_layer_norm_grad"):
+                 "ccl_layer_norm", "ccl_layer_norm_grad", "ccl_cross_entropy", "ccl_cross_entropy_grad"):
         fn = getattr(ccl.lib, name)
         assert (fn(None, None, 0, None) if name in WITH_WORKSPACE else fn(None, None)) == INVALID
 
@@ -157,7 +193,8 @@ def test_structs_match_the_header_layout(tmp_path):
         pytest.skip("no C compiler")
     pairs = [(ccl.Route, "ccl_route_t"), (ccl.RouteGrad, "ccl_route_grad_t"), (ccl.ExpertOrder, "ccl_expert_order_t"),
              (ccl.Dispatch, "ccl_dispatch_t"), (ccl.Combine, "ccl_combine_t"), (ccl.CombineGrad, "ccl_combine_grad_t"),
-             (ccl.LayerNorm, "ccl_layer_norm_t"), (ccl.LayerNormGrad, "ccl_layer_norm_grad_t")]
+             (ccl.LayerNorm, "ccl_layer_norm_t"), (ccl.LayerNormGrad, "ccl_layer_norm_grad_t"),
+             (ccl.CrossEntropy, "ccl_cross_entropy_t"), (ccl.CrossEntropyGrad, "ccl_cross_entropy_grad_t")]
     lines, want = ["#include <stddef.h>", "#include <stdio.h>", '#include "ccl.h"', "int main(void) {"], []
     for cls, name in pairs:
         lines.append(f'    printf("%zu\\n", sizeof({name}));')
@@ -178,7 +215,8 @@ def test_python_refusals():
     calls = [lambda: ccl.route(x, 2), lambda: ccl.route(x[0], 2), lambda: ccl.route_backward(w, x, i),
              lambda: ccl.expert_order(i, 4), lambda: ccl.dispatch(x, i), lambda: ccl.combine(x, i, w),
              lambda: ccl.combine_backward(x, x, i, w), lambda: ccl.dispatch_backward(x, i), lambda: ccl.layer_norm(x),
-             lambda: ccl.layer_norm(x[0]), lambda: ccl.layer_norm_backward(x, x, None, v, v)]
+             lambda: ccl.linear_cross_entropy(x, x, v.long()), lambda: ccl.linear_cross_entropy(x, x, v),
+             lambda: ccl.linear_cross_entropy_backward(v, x, x, v.long(), v), lambda: ccl.layer_norm(x[0]), lambda: ccl.layer_norm_backward(x, x, None, v, v)]
     for call in calls:
         with pytest.raises(ValueError):
             call()
@@ -191,7 +229,8 @@ def test_operands_that_want_gradients_are_refused():
     n = torch.zeros(8)
     calls = [lambda t: ccl.route(t(x), 2), lambda t: ccl.route(x, 2, bias=t(n)), lambda t: ccl.dispatch(t(x), i),
              lambda t: ccl.combine(t(x), i, w), lambda t: ccl.combine(x, i, t(w)), lambda t: ccl.combine(x, i, w, residual=t(x)),
-             lambda t: ccl.layer_norm(t(x)), lambda t: ccl.layer_norm(x, t(n)), lambda t: ccl.layer_norm(x, n, t(n))]
+             lambda t: ccl.linear_cross_entropy(t(x), x, i[:, 0].contiguous()),
+             lambda t: ccl.linear_cross_entropy(x, t(x), i[:, 0].contiguous()), lambda t: ccl.layer_norm(t(x)), lambda t: ccl.layer_norm(x, t(n)), lambda t: ccl.layer_norm(x, n, t(n))]
     for call in calls:
         with pytest.raises(ValueError, match="autograd"):
             call(lambda t: t.clone().requires_grad_(True))
