@@ -828,7 +828,12 @@ def orthogonalize(g, steps=5, coeffs=(3.4445, -4.7750, 2.0315), eps=1e-7, scale=
 # ------------------------- around the expert products: router, rows, norm
 def _graphless(*operands):
     """Refuse operands whose gradients would be lost without a word."""
-    if _torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in operands):
+    for t in operands:
+        if t is not None and t.requires_grad:
+            break
+    else:
+        return
+    if _torch.is_grad_enabled():
         raise ValueError("the layer operators record no autograd graph, and an operand requires gradients: call under "
                          "torch.no_grad(), and take the gradients from the _backward functions")
 
@@ -870,18 +875,18 @@ def route(logits, k, score=SCORE_SOFTMAX, bias=None, groups=1, top_groups=1, gro
     a.logits, a.ld = _matrix("logits", logits, logits.shape, logits.dtype, device)
     if bias is not None:
         a.bias = _packed("bias", bias, (experts,), torch.float32, device)
-    slots = rows * max(0, k)
-    # one allocation for all outputs
-    out = torch.empty((4 if order else 2) * slots + (experts + 1 if order else 0), dtype=torch.int32, device=device)
-    chosen, weights = out[:slots].view(rows, k), out[slots:2 * slots].view(torch.float32).view(rows, k)
+    shape = (rows, max(0, k))
+    chosen = torch.empty(shape, dtype=torch.int32, device=device)
+    weights = torch.empty(shape, dtype=torch.float32, device=device)
     a.chosen, a.weights = chosen.data_ptr(), weights.data_ptr()
-    if order:
-        place, offsets = out[2 * slots:3 * slots].view(rows, k), out[3 * slots:3 * slots + experts + 1]
-        a.place, a.offsets = place.data_ptr(), offsets.data_ptr()
-        _run(lib.ccl_route, lib.ccl_route_workspace, a, device, handle)
-        return weights, chosen, offsets, place
-    _run(lib.ccl_route, lib.ccl_route_workspace, a, device, handle, 0)
-    return weights, chosen
+    if not order:
+        _run(lib.ccl_route, lib.ccl_route_workspace, a, device, handle, 0)
+        return weights, chosen
+    place = torch.empty(shape, dtype=torch.int32, device=device)
+    offsets = torch.empty(experts + 1, dtype=torch.int32, device=device)
+    a.place, a.offsets = place.data_ptr(), offsets.data_ptr()
+    _run(lib.ccl_route, lib.ccl_route_workspace, a, device, handle)
+    return weights, chosen, offsets, place
 
 
 def route_backward(dweights, logits, chosen, score=SCORE_SOFTMAX, renormalize=True, scale=1.0, stream=None):
@@ -1040,7 +1045,8 @@ def layer_norm(x, w=None, b=None, eps=1e-5, stats=False, out=None, stream=None):
     if not stats:
         _check(lib.ccl_layer_norm(ctypes.byref(a), handle))
         return y
-    mean, rstd = torch.empty((2, rows), dtype=torch.float32, device=device).unbind(0)
+    mean = torch.empty(rows, dtype=torch.float32, device=device)
+    rstd = torch.empty(rows, dtype=torch.float32, device=device)
     a.mean, a.rstd = mean.data_ptr(), rstd.data_ptr()
     _check(lib.ccl_layer_norm(ctypes.byref(a), handle))
     return y, mean, rstd
@@ -1105,7 +1111,8 @@ def linear_cross_entropy(x, w, target, ignore_index=-100, stream=None):
     a.target = where
     a.x, a.ldx = _matrix("x", x, x.shape, dtype, device)
     a.w, a.ldw = _matrix("w", w, (vocab, k), dtype, device)
-    loss, lse = torch.empty((2, rows), dtype=torch.float32, device=device).unbind(0)
+    loss = torch.empty(rows, dtype=torch.float32, device=device)
+    lse = torch.empty(rows, dtype=torch.float32, device=device)
     a.loss, a.lse = loss.data_ptr(), lse.data_ptr()
     _run(lib.ccl_cross_entropy, lib.ccl_cross_entropy_workspace, a, device, handle)
     return loss, lse

@@ -31,21 +31,25 @@ static ccl_status_t array(const std::string& who, const char* what, const void* 
 }
 
 // ---------------------------------------------------------------- router
-constexpr int kRouteThreads = 512;
+constexpr int kOrderThreads = 512;
 constexpr int kRouteSmem = 16 * kMostRouted * 8 + kMostRouted * 4;     // 16 warps' values and a block's counts
 
-static void (*route_kernel_for(int experts, int order))(const Route)
+// The kernels for every number of experts a lane, from the smallest up: widths
+// that usual numbers of experts fill, so that groups of them are whole lanes.
+struct RouteKernel {
+    int vpl;
+    void (*route)(const Route);
+    void (*grad)(const Route);
+};
+#define ROUTE(vpl) {vpl, route_kernel<vpl>, route_grad_kernel<vpl>}
+static const RouteKernel kRoute[] = {ROUTE(1), ROUTE(2), ROUTE(3), ROUTE(4),  ROUTE(5),
+                                     ROUTE(6), ROUTE(8), ROUTE(12), ROUTE(16), ROUTE(32)};
+#undef ROUTE
+static const RouteKernel& route_kernel_for(int64_t experts)
 {
-    int i = 0;
-    while (32 << i < experts) ++i;
-    static void (*const all[6][3])(const Route) = {
-        {route_kernel<1, 0>, route_kernel<1, 1>, route_kernel<1, 2>},
-        {route_kernel<2, 0>, route_kernel<2, 1>, route_kernel<2, 2>},
-        {route_kernel<4, 0>, route_kernel<4, 1>, route_kernel<4, 2>},
-        {route_kernel<8, 0>, route_kernel<8, 1>, route_kernel<8, 2>},
-        {route_kernel<16, 0>, route_kernel<16, 1>, route_kernel<16, 2>},
-        {route_kernel<32, 0>, route_kernel<32, 1>, route_kernel<32, 2>}};
-    return all[i][order];
+    const RouteKernel* k = kRoute;
+    while (32 * k->vpl < experts) ++k;
+    return *k;
 }
 
 // once per device: how many SMs it has; kernels that take more than 48 KB of shared memory are told so
@@ -58,10 +62,9 @@ static ccl_status_t layer_device(int* sms)
     if (d < 0 || d >= 64) return fail(CCL_ERR_UNSUPPORTED, "device index above 63");
     std::lock_guard<std::mutex> lock(mu);
     if (!known[d]) {
-        for (int e = 32; e <= kMostRouted; e *= 2)
-            for (int order = 0; order < 3; ++order)
-                TRY_CUDA(cudaFuncSetAttribute(route_kernel_for(e, order), cudaFuncAttributeMaxDynamicSharedMemorySize, kRouteSmem),
-                         "shared memory of the router");
+        for (const RouteKernel& k : kRoute)
+            TRY_CUDA(cudaFuncSetAttribute(k.route, cudaFuncAttributeMaxDynamicSharedMemorySize, kRouteSmem),
+                     "shared memory of the router");
         for (auto kernel : {place_kernel<true>, place_kernel<false>})
             TRY_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRouteSmem),
                      "shared memory of the row order");
@@ -80,7 +83,8 @@ static int order_blocks(int64_t items, int least)
 {
     return (int)std::min<int64_t>(kOrderBlocks, (items + least - 1) / least);
 }
-static size_t order_smem(int experts) { return (size_t)(kRouteThreads / 32 + 2) * experts * 4; }
+static size_t order_smem(int experts, int threads) { return (size_t)(threads / 32 + 2) * experts * 4; }
+static int64_t hist_bytes(int blocks, int64_t experts) { return blocks * round_up(experts, 4) * 4; }
 
 static ccl_status_t check_router(const std::string& who, int64_t rows, int64_t experts, int k, int dtype, int score)
 {
@@ -95,7 +99,7 @@ static ccl_status_t check_router(const std::string& who, int64_t rows, int64_t e
     return CCL_OK;
 }
 
-// rows of a threadblock's two warps: fewer rows go to one threadblock, which orders them as well
+// As many rows go to one threadblock, which orders them as well.
 constexpr int kRowsOfOne = 32;
 
 static ccl_status_t route(const ccl_route_t* a, char* base, int64_t* need, cudaStream_t stream)
@@ -119,8 +123,8 @@ static ccl_status_t route(const ccl_route_t* a, char* base, int64_t* need, cudaS
     Arena ws = {base};
     Route R = {};
     const bool one = a->rows <= kRowsOfOne;
-    R.blocks = one ? 1 : order_blocks(a->rows, kRouteThreads / 32);
-    if (order && !one) R.hist = ws.take<int32_t>((int64_t)R.blocks * a->experts * 4);
+    R.blocks = one ? 1 : order_blocks(a->rows, 16);
+    if (order && !one) R.hist = ws.take<int32_t>(hist_bytes(R.blocks, a->experts));
     if (need) {
         *need = ws.used;
         return CCL_OK;
@@ -156,24 +160,36 @@ static ccl_status_t route(const ccl_route_t* a, char* base, int64_t* need, cudaS
     R.top_groups = a->top_groups;
     R.group_best = groups > 1 ? a->group_best : 1;
     R.renormalize = a->renormalize != 0;
+    R.scored = a->bias || R.group_best == 2;
     R.scale = a->scale;
     int sms;
     TRY(layer_device(&sms));
-    const size_t values = groups > 1 ? (size_t)kRouteThreads / 32 * a->experts * 8 : 0;
+    const int64_t each = 16 / element_bytes(a->dtype);
+    R.vec = aligned16(a->logits) && ld % each == 0 && a->experts % each == 0;
+    const RouteKernel& k = route_kernel_for(a->experts);
+    const int most = route_threads(k.vpl);
+    // values in 64 bits (and groups that are not whole lanes) need shared memory: for a warp each
+    const bool held = a->bias || groups > 1;
+    auto values = [&](int threads) { return held ? (size_t)threads / 32 * a->experts * 8 : 0; };
     if (!order) {
-        const int64_t blocks = std::min<int64_t>((a->rows + kRouteThreads / 32 - 1) / (kRouteThreads / 32), 1 << 20);
-        R.per_block = (a->rows + blocks - 1) / blocks;
-        return launch(route_kernel_for(R.experts, 0), dim3((unsigned)blocks), kRouteThreads, values, stream, R);
+        const int threads = 256;
+        const int64_t blocks = (a->rows + 7) / 8;
+        R.per_block = 8;
+        return launch(k.route, dim3((unsigned)blocks), threads, values(threads), stream, R);
     }
     if (one) {
+        const int threads = (int)std::min<int64_t>(most, round_up(std::max<int64_t>(a->rows, 4), 4) * 32);
+        R.order = 1;
         R.per_block = a->rows;
-        return launch(route_kernel_for(R.experts, 1), dim3(1), kRouteThreads, std::max(values, order_smem(R.experts)), stream, R);
+        return launch(k.route, dim3(1), threads, std::max(values(threads), order_smem(R.experts, threads)), stream, R);
     }
+    R.order = 2;
     R.per_block = (a->rows + R.blocks - 1) / R.blocks;
     R.blocks = (int32_t)((a->rows + R.per_block - 1) / R.per_block);
-    TRY(launch(route_kernel_for(R.experts, 2), dim3(R.blocks), kRouteThreads, round_up(a->experts * 4, 8) + values, stream, R));
+    const int threads = (int)std::min<int64_t>(most, round_up(R.per_block, 4) * 32);
+    TRY(launch(k.route, dim3(R.blocks), threads, round_up(a->experts * 4, 8) + values(threads), stream, R));
     R.per_block *= a->k;
-    return launch(place_kernel<false>, dim3(R.blocks), kRouteThreads, order_smem(R.experts), stream, R);
+    return launch(place_kernel<false>, dim3(R.blocks), kOrderThreads, order_smem(R.experts, kOrderThreads), stream, R);
 }
 
 static ccl_status_t expert_order(const ccl_expert_order_t* a, char* base, int64_t* need, cudaStream_t stream)
@@ -185,8 +201,8 @@ static ccl_status_t expert_order(const ccl_expert_order_t* a, char* base, int64_
     if (a->slots < 0 || a->slots > INT32_MAX) return fail(CCL_ERR_INVALID_ARG, who + "slots out of range");
     Arena ws = {base};
     Route R = {};
-    R.blocks = order_blocks(a->slots, 4 * kRouteThreads);
-    if (R.blocks > 1) R.hist = ws.take<int32_t>((int64_t)R.blocks * a->experts * 4);
+    R.blocks = order_blocks(a->slots, 4 * kOrderThreads);
+    if (R.blocks > 1) R.hist = ws.take<int32_t>(hist_bytes(R.blocks, a->experts));
     if (need) {
         *need = ws.used;
         return CCL_OK;
@@ -209,10 +225,10 @@ static ccl_status_t expert_order(const ccl_expert_order_t* a, char* base, int64_
     int sms;
     TRY(layer_device(&sms));
     R.per_block = (a->slots + R.blocks - 1) / R.blocks;
-    if (R.blocks == 1) return launch(place_kernel<true>, dim3(1), kRouteThreads, order_smem(R.experts), stream, R);
+    if (R.blocks == 1) return launch(place_kernel<true>, dim3(1), kOrderThreads, order_smem(R.experts, kOrderThreads), stream, R);
     R.blocks = (int32_t)((a->slots + R.per_block - 1) / R.per_block);
-    TRY(launch(count_kernel, dim3(R.blocks), kRouteThreads, a->experts * 4, stream, R));
-    return launch(place_kernel<false>, dim3(R.blocks), kRouteThreads, order_smem(R.experts), stream, R);
+    TRY(launch(count_kernel, dim3(R.blocks), kOrderThreads, a->experts * 4, stream, R));
+    return launch(place_kernel<false>, dim3(R.blocks), kOrderThreads, order_smem(R.experts, kOrderThreads), stream, R);
 }
 
 static ccl_status_t route_grad(const ccl_route_grad_t* a, cudaStream_t stream)
@@ -247,11 +263,10 @@ static ccl_status_t route_grad(const ccl_route_grad_t* a, cudaStream_t stream)
     R.scale = a->scale;
     int sms;
     TRY(layer_device(&sms));
-    int i = 0;
-    while (32 << i < R.experts) ++i;
-    static void (*const all[6])(const Route) = {route_grad_kernel<1>, route_grad_kernel<2>,  route_grad_kernel<4>,
-                                                route_grad_kernel<8>, route_grad_kernel<16>, route_grad_kernel<32>};
-    return launch(all[i], dim3((unsigned)((a->rows + 7) / 8)), 256, 0, stream, R);
+    const int64_t each = 16 / es;
+    R.vec = aligned16(a->logits) && ld % each == 0 && a->experts % each == 0;
+    R.vec_d = aligned16(a->dlogits) && ldd % each == 0 && a->experts % each == 0;
+    return launch(route_kernel_for(a->experts).grad, dim3((unsigned)((a->rows + 7) / 8)), 256, 0, stream, R);
 }
 
 // ------------------------------------------------------------- row moves

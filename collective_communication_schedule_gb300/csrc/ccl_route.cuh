@@ -23,6 +23,10 @@ struct Route {
     int64_t rows, ld, ld_d;
     int64_t slots, per_block;      // rows x k; rows of a block (route), slots of a block (order)
     int32_t experts, k, type, score, groups, top_groups, group_best, renormalize, blocks;
+    int32_t scored;                // values other than the logits decide something
+    int32_t order;                 // 0: choices and weights only, 1: one threadblock, which orders the rows as well, 2: counts for
+                                   // place_kernel are left in hist
+    int32_t vec, vec_d;            // rows of logits can be read, of dlogits written 16 bytes at a time
     float scale;
 };
 
@@ -39,227 +43,456 @@ __device__ __forceinline__ void store_as(void* p, int64_t i, int type, float v)
 }
 
 __device__ __forceinline__ float sigmoid32(float l) { return 1.f / (1.f + expf(-l)); }
+__device__ __forceinline__ float exp2_near(float x)      // within 2^-22
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
 
 // Keys: unsigned numbers in the order of the values.  0 is a closed expert
 // (logit or bias -inf), which nothing but another closed one ties with; NaN comes
 // behind every number.
 __device__ __forceinline__ uint32_t key_of(float v)
 {
-    const uint32_t b = __float_as_uint(v != v ? -3.402823466e38f : v == 0.f ? 0.f : v);
-    return b & 0x80000000u ? ~b : b | 0x80000000u;
+    const uint32_t b = __float_as_uint(fmaxf(v, -3.402823466e38f) + 0.f);     // (+ 0: one zero)
+    return v == -INFINITY ? 0u : b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
-__device__ __forceinline__ unsigned long long key_of(double v)
+__device__ __forceinline__ float value_of(uint32_t key)
 {
-    const unsigned long long b = (unsigned long long)__double_as_longlong(v != v ? -1.7976931348623157e308 : v == 0. ? 0. : v);
-    return b >> 63 ? ~b : b | 1ull << 63;
-}
-__device__ __forceinline__ uint32_t warp_most(uint32_t v) { return __reduce_max_sync(~0u, v); }
-__device__ __forceinline__ unsigned long long warp_most(unsigned long long v)
-{
-    const uint32_t hi = __reduce_max_sync(~0u, (uint32_t)(v >> 32));
-    const uint32_t lo = __reduce_max_sync(~0u, (uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
-    return (unsigned long long)hi << 32 | lo;
+    return __uint_as_float(key >> 31 ? key ^ 0x80000000u : ~key);
 }
 
-// Close the experts of all but the best groups.  val: the row's values in
-// shared memory.  Returns whether the border between the groups is nearer
-// than `near` (never without scores: values are exact then).
-template <int VPL, typename F, typename K>
-__device__ __forceinline__ bool keep_groups(const Route& R, const F (&v)[VPL], K (&key)[VPL], F* val, int lane, F near)
+// From the groups' values, lane g's group g (a: -inf if all of it is closed),
+// which are kept, as a mask; sets `close` where an open group lies nearer behind the
+// border than `near` and 2^-21 of what the two were added up from (size).
+template <typename F>
+__device__ __forceinline__ uint32_t best_groups(const Route& R, F a, F size, int lane, F near, bool& close)
 {
-    const int size = R.experts / R.groups;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        const int e = i * 32 + lane;
-        if (e < R.experts) val[e] = key[i] ? v[i] : (F)-INFINITY;
-    }
-    __syncwarp();
-    // a lane a group: its largest value, or the sum of the two largest
-    F a = (F)-INFINITY, b = (F)-INFINITY;
-    if (lane < R.groups) {
-        for (int i = 0; i < size; ++i) {
-            F u = val[lane * size + i];
-            if (u != u) u = (F)-3.402823466e38f;
-            if (u > a)
-                b = a, a = u;
-            else if (u > b)
-                b = u;
-        }
-    }
-    __syncwarp();
-    const bool open = a != (F)-INFINITY;
-    if (R.group_best == 2 && b != (F)-INFINITY) a += b;
     int rank = 0;
     for (int g = 0; g < R.groups; ++g) {
         const F u = __shfl_sync(~0u, a, g);
         rank += u > a || (u == a && g < lane);
     }
-    const bool kept = lane < R.groups && rank < R.top_groups;
-    const uint32_t mask = __ballot_sync(~0u, kept);
-    // the worst kept and the best dropped group, where both are open
-    const uint32_t worst = __ballot_sync(~0u, lane < R.groups && rank == R.top_groups - 1);
-    const uint32_t next = __ballot_sync(~0u, lane < R.groups && rank == R.top_groups);
-    bool close = false;
+    const bool mine = lane < R.groups;
+    const uint32_t worst = __ballot_sync(~0u, mine && rank == R.top_groups - 1);
+    const uint32_t next = __ballot_sync(~0u, mine && rank == R.top_groups);
     if (next) {
-        const F u = __shfl_sync(~0u, a, __ffs(worst) - 1), w = __shfl_sync(~0u, a, __ffs(next) - 1);
-        const bool both = __shfl_sync(~0u, (int)open, __ffs(next) - 1);
-        close = both && !(u - w >= near);
+        const int p = __ffs(worst) - 1, q = __ffs(next) - 1;
+        const F u = __shfl_sync(~0u, a, p), w = __shfl_sync(~0u, a, q);
+        const F most = max(__shfl_sync(~0u, size, p), __shfl_sync(~0u, size, q));
+        close = w != (F)-INFINITY && !(u - w >= near + (F)0x1p-21 * most);
     }
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        const int e = i * 32 + lane;
-        if (e < R.experts && !(mask >> e / size & 1)) key[i] = 0;
-    }
-    return close;
+    return __ballot_sync(~0u, mine && rank < R.top_groups);
 }
 
-// The `count` largest keys of a row, ties to the lower expert; lane j gets the
-// j-th one's expert (-1: none left) and key.
-template <int VPL, typename K>
-__device__ __forceinline__ void pick(K (&key)[VPL], int count, int lane, int& expert, K& found)
+// Close the experts of all but the best groups: their values (-inf: closed)
+// become -inf.  A lane holds VPL neighbours; where groups are whole lanes, their
+// two largest values are found in registers first, else by a lane a group in
+// shared memory (val).
+template <int VPL>
+__device__ __forceinline__ uint32_t keep_groups(const Route& R, const float (&v)[VPL], float* val, int lane, float near,
+                                                bool& close)
 {
-    expert = -1;
-    found = 0;
-    K best = 0;
-    int at = 0;
+    const int size = R.experts / R.groups, lanes = size / VPL;
+    float a = -INFINITY, b = -INFINITY;
+    if (lanes * VPL == size) {
+        float x = -INFINITY, y = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i)
-        if (key[i] > best) best = key[i], at = i;
-    for (int j = 0; j < count; ++j) {
-        const K most = warp_most(best);
-        if (most == 0) break;
-        const uint32_t e = __reduce_min_sync(~0u, best == most ? (uint32_t)(at * 32 + lane) : ~0u);
-        if (lane == j) expert = (int)e, found = most;
-        if ((e & 31) == lane) {
-            best = 0;
+        for (int i = 0; i < VPL; ++i) {
+            y = fmaxf(y, fminf(x, v[i]));
+            x = fmaxf(x, v[i]);
+        }
+        for (int i = 0; i < lanes; ++i) {
+            const float u = __shfl_sync(~0u, x, lane * lanes + i), w = __shfl_sync(~0u, y, lane * lanes + i);
+            b = fmaxf(fmaxf(b, w), fminf(a, u));
+            a = fmaxf(a, u);
+        }
+    } else {
 #pragma unroll
-            for (int i = 0; i < VPL; ++i) {
-                if (i == (int)(e >> 5)) key[i] = 0;
-                if (key[i] > best) best = key[i], at = i;
+        for (int i = 0; i < VPL; ++i)
+            if (lane * VPL + i < R.experts) val[lane * VPL + i] = v[i];
+        __syncwarp();
+        if (lane < R.groups)
+            for (int i = 0; i < size; ++i) {
+                const float u = val[lane * size + i];
+                b = fmaxf(b, fminf(a, u));
+                a = fmaxf(a, u);
             }
+        __syncwarp();
+    }
+    float from = fabsf(a);
+    if (R.group_best == 2 && b != -INFINITY) from += fabsf(b), a += b;
+    if (lane >= R.groups) a = -INFINITY;
+    return best_groups(R, a, R.scored ? from : 0.f, lane, near, close);
+}
+
+// The largest keys of a row one after another, ties to the lower expert.  A
+// lane knows its two largest and looks for another one only when it has to give
+// a third, which happens about once a row.
+template <int VPL>
+struct Picker {
+    uint32_t best = 0, second = 0;
+    int at = 0, at2 = 0;
+    bool two = true;               // second is the one behind best
+    __device__ __forceinline__ explicit Picker(const uint32_t (&key)[VPL])
+    {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            const bool first = key[i] > best, next = key[i] > second;
+            at2 = first ? at : next ? i : at2;
+            second = first ? best : next ? key[i] : second;
+            at = first ? i : at;
+            best = first ? key[i] : best;
         }
     }
+    // the largest key that is left (0: none)
+    __device__ __forceinline__ uint32_t most() const { return __reduce_max_sync(~0u, best); }
+    // takes it away, and says whose it is
+    __device__ __forceinline__ int take(const uint32_t (&key)[VPL], uint32_t largest, int lane)
+    {
+        const int owner = __ffs(__ballot_sync(~0u, best == largest)) - 1;
+        const int expert = owner * VPL + __shfl_sync(~0u, at, owner);
+        if (lane == owner) {
+            if (two) {
+                best = second, at = at2, two = false;
+            } else {
+                uint32_t b = 0;
+                int a = 0;
+#pragma unroll
+                for (int i = 0; i < VPL; ++i)
+                    if ((key[i] < best || (key[i] == best && i > at)) && key[i] > b) b = key[i], a = i;
+                best = b, at = a;
+            }
+        }
+        return expert;
+    }
+};
+
+// An expert's score in 64 bits, sum and most being the softmax's.
+__device__ __forceinline__ double score64(const Route& R, double l, double most, double sum)
+{
+    return R.score == CCL_SCORE_SIGMOID ? 1 / (1 + exp(-l)) : exp(l - most) / sum;
+}
+__device__ __noinline__ double2 softmax64(const Route& R, int64_t row, int lane)
+{
+    double most = -INFINITY, sum = 0;
+    if (R.score != CCL_SCORE_SIGMOID) {
+        for (int e = lane; e < R.experts; e += 32) most = fmax(most, (double)load_as(R.logits, row * R.ld + e, R.type));
+#pragma unroll
+        for (int d = 16; d; d >>= 1) most = fmax(most, __shfl_xor_sync(~0u, most, d));
+#pragma unroll 2
+        for (int e = lane; e < R.experts; e += 32) {
+            const double l = load_as(R.logits, row * R.ld + e, R.type);
+            sum += l == -INFINITY ? 0 : exp(l - most);
+        }
+#pragma unroll
+        for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
+    }
+    return make_double2(most, sum);
 }
 
-// A row's choices in 64 bits, for rows whose values lie too near to each other.
-template <int VPL>
+// The order of `n` candidates, lane j's the j-th, decided in 64 bits: lane j
+// gets the j-th of that order.
+__device__ __noinline__ int order64(const Route& R, int64_t row, int expert, int n, int lane)
+{
+    const double2 s = softmax64(R, row, lane);
+    double c = -INFINITY;
+    if (lane < n) {
+        c = score64(R, load_as(R.logits, row * R.ld + expert, R.type), s.x, s.y) + (double)R.bias[expert];
+        if (c != c) c = -1.7976931348623157e308;
+    }
+    int rank = 0;
+    for (int i = 0; i < n; ++i) {
+        const double u = __shfl_sync(~0u, c, i);
+        const int e = __shfl_sync(~0u, expert, i);
+        rank += u > c || (u == c && e < expert);
+    }
+    int mine = -1;
+    for (int i = 0; i < n; ++i) {
+        const int r = __shfl_sync(~0u, rank, i), e = __shfl_sync(~0u, expert, i);
+        if (r == lane) mine = e;
+    }
+    return mine;
+}
+
+// Which groups are kept, decided in 64 bits: lane g takes the largest values of
+// group g and computes them again.  Says whether it could: not where the second
+// and the third value of a group may be in the wrong order.
+__device__ __noinline__ bool groups64(const Route& R, int64_t row, int lane, float most, float inv, float near, uint32_t& kept)
+{
+    const int size = R.experts / R.groups;
+    const bool softmax = R.score != CCL_SCORE_SIGMOID;
+    float a = -INFINITY, b = -INFINITY, third = -INFINITY;
+    int at_a = -1, at_b = -1;
+    if (lane < R.groups) {
+#pragma unroll 4
+        for (int i = 0; i < size; ++i) {
+            const int e = lane * size + i;
+            const float l = load_as(R.logits, row * R.ld + e, R.type);
+            float c = l;                       // (without a bias the logits are in the scores' order)
+            if (R.bias && l != -INFINITY) c = (softmax ? exp2_near((l - most) * 1.4426950408889634f) * inv : sigmoid(l)) + __ldg(R.bias + e);
+            if (c != c) c = -3.402823466e38f;
+            third = fmaxf(third, fminf(b, c));
+            if (c > a)
+                b = a, at_b = at_a, a = c, at_a = e;
+            else if (c > b)
+                b = c, at_b = e;
+        }
+    }
+    const float bound = fmaf(fmaxf(fabsf(b), fabsf(third)), 0x1p-22f, near);
+    const bool unsure = R.bias && R.group_best == 2 && third != -INFINITY && !(b - third >= bound);
+    if (__any_sync(~0u, unsure)) return false;
+    const double2 s = softmax64(R, row, lane);
+    double v = -INFINITY;
+    auto value = [&](int e) {
+        const double c = score64(R, load_as(R.logits, row * R.ld + e, R.type), s.x, s.y) + (R.bias ? (double)R.bias[e] : 0.);
+        return c != c ? -1.7976931348623157e308 : c;
+    };
+    if (at_a >= 0) {
+        v = value(at_a);
+        if (R.group_best == 2 && at_b >= 0) v += value(at_b);
+    }
+    bool close = false;
+    kept = best_groups(R, v, 0., lane, 0., close);
+    return true;
+}
+
+// A row's choices all in 64 bits, for values of a group or more candidates than
+// lanes too near to each other (rare: values in shared memory, so that the
+// common way keeps its registers).
 __device__ __noinline__ int choose64(const Route& R, int64_t row, double* val, int lane)
 {
-    double v[VPL];
-    unsigned long long key[VPL];
-    double most = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        const int e = i * 32 + lane;
-        v[i] = e < R.experts ? (double)load_as(R.logits, row * R.ld + e, R.type) : -INFINITY;
-        key[i] = v[i] == -INFINITY ? 0 : 1;
-        most = fmax(most, v[i]);
+    const int E = R.experts;
+    const double2 s = softmax64(R, row, lane);
+    __syncwarp();
+    for (int e = lane; e < E; e += 32) {
+        const double l = load_as(R.logits, row * R.ld + e, R.type);
+        double c = -INFINITY;
+        if (l != -INFINITY) {
+            c = score64(R, l, s.x, s.y) + (R.bias ? (double)R.bias[e] : 0.);
+            if (c != c) c = -1.7976931348623157e308;
+        }
+        val[e] = c;
     }
-#pragma unroll
-    for (int d = 16; d; d >>= 1) most = fmax(most, __shfl_xor_sync(~0u, most, d));
-    double sum = 0;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        v[i] = R.score == CCL_SCORE_SIGMOID ? 1 / (1 + exp(-v[i])) : exp(v[i] - most);
-        sum += key[i] ? v[i] : 0;
+    __syncwarp();
+    if (R.groups > 1) {
+        const int size = E / R.groups;
+        double a = -INFINITY, b = -INFINITY;
+        if (lane < R.groups)
+            for (int i = 0; i < size; ++i) {
+                const double u = val[lane * size + i];
+                b = fmax(b, fmin(a, u));
+                a = fmax(a, u);
+            }
+        if (R.group_best == 2 && b != -INFINITY) a += b;
+        bool close = false;
+        const uint32_t kept = best_groups(R, a, 0., lane, 0., close);
+        __syncwarp();
+        for (int e = lane; e < E; e += 32) {
+            if (!(kept >> e / size & 1)) {
+                val[e] = -INFINITY;
+            } else if (!R.bias) {          // scores order the experts as the logits do
+                const double l = load_as(R.logits, row * R.ld + e, R.type);
+                val[e] = l != l ? -1.7976931348623157e308 : l;
+            }
+        }
+        __syncwarp();
     }
+    int expert = -1;
+    for (int j = 0; j < R.k; ++j) {
+        double c = -INFINITY;
+        int at = INT32_MAX;
+        for (int e = lane; e < E; e += 32)
+            if (val[e] > c) c = val[e], at = e;
 #pragma unroll
-    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        if (!key[i]) continue;
-        if (R.score != CCL_SCORE_SIGMOID) v[i] /= sum;
-        if (R.bias) v[i] += (double)R.bias[i * 32 + lane];
-        key[i] = v[i] == -INFINITY ? 0 : key_of(v[i]);
+        for (int d = 16; d; d >>= 1) {
+            const double u = __shfl_xor_sync(~0u, c, d);
+            const int e = __shfl_xor_sync(~0u, at, d);
+            if (u > c || (u == c && e < at)) c = u, at = e;
+        }
+        if (c == -INFINITY) break;
+        if (lane == j) expert = at;
+        if (lane == (at & 31)) val[at] = -INFINITY;
+        __syncwarp();
     }
-    if (R.groups > 1) keep_groups<VPL>(R, v, key, val, lane, 0.);
-    int expert;
-    unsigned long long found;
-    pick<VPL>(key, R.k, lane, expert, found);
+    __syncwarp();
     return expert;
 }
 
-// The choices of a row (lane j: the j-th) and their weights.
+// A lane's VPL neighbours of a row of n; -inf beyond it.
+template <int VPL, typename E>
+__device__ __forceinline__ void load_row(const typename E::Raw* p, int at, int n, bool vec, float (&l)[VPL])
+{
+    constexpr int W = E::kVec;
+    if (VPL % W == 0 && vec) {         // (rows on 16 bytes, n a multiple of a vector)
+#pragma unroll
+        for (int i = 0; i < VPL; i += W) {
+            if (at + i < n) {
+                E::unpack(*reinterpret_cast<const uint4*>(p + at + i), l + i);
+            } else {
+#pragma unroll
+                for (int q = 0; q < (W < VPL ? W : VPL); ++q) l[i + q] = -INFINITY;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) l[i] = at + i < n ? E::load(p + at + i) : -INFINITY;
+    }
+}
+template <int VPL>
+__device__ __forceinline__ void load_row(const Route& R, int64_t row, int lane, float (&l)[VPL])
+{
+    const int at = lane * VPL;
+    const int64_t o = row * R.ld;
+    if (R.type == CCL_F32)
+        load_row<VPL, Type<CCL_F32>>((const float*)R.logits + o, at, R.experts, R.vec, l);
+    else if (R.type == CCL_BF16)
+        load_row<VPL, Type<CCL_BF16>>((const uint16_t*)R.logits + o, at, R.experts, R.vec, l);
+    else
+        load_row<VPL, Type<CCL_F16>>((const uint16_t*)R.logits + o, at, R.experts, R.vec, l);
+}
+
+template <int VPL, typename E>
+__device__ __forceinline__ void store_row(typename E::Raw* p, int at, int n, bool vec, const float (&v)[VPL])
+{
+    constexpr int W = E::kVec;
+    if (VPL % W == 0 && vec) {
+#pragma unroll
+        for (int i = 0; i < VPL; i += W)
+            if (at + i < n) *reinterpret_cast<uint4*>(p + at + i) = E::pack(v + i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            if (at + i < n) E::store(p + at + i, v[i]);
+    }
+}
+
+// The choices of a row (lane j: the j-th) and their weights.  A lane holds VPL
+// neighbouring experts.
 //
-// Which experts come first is decided as in 64 bits.  Without a bias and sums
-// of two, scores order the experts as the logits do, and the logits are
-// compared.  Else values are computed in 32 bits with an error bound `near`; a
-// row with two neighbours in the order (or two groups at the border) nearer
-// than that is done again in 64 bits, about one in a thousand.
-//   sigmoid: exp within 2 units, a sum, a division: 2^-21.4 of a score; two of
-//     them, 2^-20 with the rounding of the comparison;
+// Which experts come first is decided as in 64 bits.  Without a bias, scores
+// order the experts as the logits do, and the logits are compared.  Else (and
+// for groups by the sum of two) values are computed in 32 bits with an error
+// bound: two values nearer than `near` may be in the wrong order.  Where that is so
+// for neighbours in the order, all that lie within `near` of the k-th are ordered
+// again in 64 bits, about one row in a hundred; where it is so for the groups at
+// the border, or for more than 32 candidates, the whole row is.
+//   sigmoid: 2^(-l log2 e) within 2^-22 and its argument within 2^-24 of itself,
+//     which |l| s (1 - s) < 0.23 turns into 2^-25 of s; a sum and a reciprocal
+//     within 2^-22: less than 2^-21.4 in all, twice that for two of them;
 //   softmax: the sum is off by up to 37 roundings and scales all scores alike,
-//     exp within 2 units, and l - max rounds to 2^-24 |l - max| of a score, at
-//     most 2^-24 / e: 2^-18 of the largest score;
-//   adding the bias rounds to 2^-24 of the value, twice.
+//     the exponential is within 2^-22, and l - max and its product with log2 e
+//     round to 2^-24 |l - max| of a score, at most 2^-24: 2^-18 of the largest
+//     score, which is 1 / sum;
+//   adding the bias, or two values, rounds to 2^-24 of the larger, twice.
 template <int VPL>
 __device__ __forceinline__ void route_row(const Route& R, int64_t row, double* val, int lane, int& expert, float& weight)
 {
-    float l[VPL], v[VPL];
-    uint32_t key[VPL];
-    bool poison = false;
-    float most = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        const int e = i * 32 + lane;
-        l[i] = e < R.experts ? load_as(R.logits, row * R.ld + e, R.type) : -INFINITY;
-    }
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        most = fmaxf(most, l[i]);
-        poison |= l[i] != l[i];
-        v[i] = l[i];
-    }
-    most = warp_max(most);
+    float l[VPL];
+    load_row<VPL>(R, row, lane, l);
     const bool softmax = R.score != CCL_SCORE_SIGMOID;
-    const bool scored = R.bias || (R.groups > 1 && R.group_best == 2);
-    poison = __any_sync(~0u, poison);
-    float sum = 1.f, near = 0.f;
-    if (softmax && (scored || !R.renormalize)) {
-        sum = 0.f;
+    bool poison = false;
+    float most = 0.f, sum = 1.f;
+    if (softmax) {
+        most = l[0];
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
-            const float p = l[i] == -INFINITY ? 0.f : expf(l[i] - most);
-            if (scored) v[i] = p;
-            sum += p;
+            most = fmaxf(most, l[i]);
+            poison |= l[i] != l[i];
         }
-        sum = warp_sum(sum);
-    }
-    if (scored) {
-        float top = 0.f, far = 0.f;
+        most = warp_max(most);
+        poison = __any_sync(~0u, poison);
+        if (R.scored || !R.renormalize) {
+            sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-            const int e = i * 32 + lane;
-            v[i] = softmax ? v[i] / sum : sigmoid32(l[i]);
-            if (l[i] != -INFINITY) top = fmaxf(top, v[i]);
-            if (R.bias && e < R.experts) v[i] += R.bias[e];
-            if (l[i] != -INFINITY && fabsf(v[i]) < INFINITY) far = fmaxf(far, fabsf(v[i]));
+            for (int i = 0; i < VPL; ++i) sum += l[i] == -INFINITY ? 0.f : exp2_near((l[i] - most) * 1.4426950408889634f);
+            sum = warp_sum(sum);
         }
-        near = warp_max(top) * (softmax ? 0x1p-18f : 0x1p-20f) + warp_max(far) * 0x1p-22f;
     }
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) key[i] = l[i] == -INFINITY || v[i] == -INFINITY ? 0u : key_of(v[i]);
+    uint32_t key[VPL];
+    float near = 0.f;
     bool again = false;
-    if (R.groups > 1) again = keep_groups<VPL>(R, v, key, (float*)val, lane, scored ? 2.f * near : 0.f) && scored;
-    uint32_t found;
-    pick<VPL>(key, min(R.k + (scored ? 1 : 0), 32), lane, expert, found);
-    float own = expert < 0 ? 0.f : load_as(R.logits, row * R.ld + expert, R.type);
-    if (scored) {
-        // neighbours in the order: near, and not for the same logit and bias
-        const uint32_t below = __shfl_down_sync(~0u, found, 1);
-        const float b = expert < 0 || !R.bias ? 0.f : R.bias[expert];
-        const float own_below = __shfl_down_sync(~0u, own, 1), b_below = __shfl_down_sync(~0u, b, 1);
-        const float value = __uint_as_float(found >> 31 ? found ^ 0x80000000u : ~found);
-        const float next = __uint_as_float(below >> 31 ? below ^ 0x80000000u : ~below);
-        again |= lane < R.k && lane < 31 && found && below && !(value - next >= near) && (own != own_below || b != b_below);
-        // (with 32 choices the one behind the last is not looked at above)
-        again |= R.k == 32 && R.experts > 32;
-        if (__any_sync(~0u, again)) {
-            __syncwarp();
-            expert = choose64<VPL>(R, row, val, lane);
-            own = expert < 0 ? 0.f : load_as(R.logits, row * R.ld + expert, R.type);
+    {
+        float v[VPL];
+        if (R.scored) {
+            const float inv = 1.f / sum;
+            near = softmax ? inv * 0x1p-18f : 0x1p-20f;
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) {
+                float c = softmax ? exp2_near((l[i] - most) * 1.4426950408889634f) * inv : sigmoid(l[i]);
+                if (R.bias && lane * VPL + i < R.experts) c += __ldg(R.bias + lane * VPL + i);
+                v[i] = l[i] == -INFINITY || c == -INFINITY ? -INFINITY : fmaxf(c, -3.402823466e38f);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) v[i] = l[i] == -INFINITY ? -INFINITY : fmaxf(l[i], -3.402823466e38f);
+        }
+        uint32_t kept = ~0u;
+        if (R.groups > 1) {
+            kept = keep_groups<VPL>(R, v, (float*)val, lane, R.scored ? 2.f * near : 0.f, again);
+            if (again) again = !groups64(R, row, lane, most, 1.f / sum, near, kept);
+        }
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) key[i] = v[i] == -INFINITY ? 0u : key_of(R.bias ? v[i] : l[i]);
+        if (R.groups > 1) {
+            const int size = R.experts / R.groups;
+            if (size % VPL == 0) {
+                if (!(kept >> min(lane / (size / VPL), 31) & 1)) {
+#pragma unroll
+                    for (int i = 0; i < VPL; ++i) key[i] = 0;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < VPL; ++i)
+                    if (!(kept >> min((lane * VPL + i) / size, 31) & 1)) key[i] = 0;
+            }
         }
     }
+    expert = -1;
+    if (!again) {
+        Picker<VPL> left(key);
+        uint32_t found = 0;
+        for (int j = 0; j < R.k; ++j) {
+            const uint32_t largest = left.most();
+            if (largest == 0) break;
+            const int e = left.take(key, largest, lane);
+            if (lane == j) expert = e, found = largest;
+        }
+        if (R.bias) {
+            // neighbours in the order that are nearer than the bound, and not for the same logit and bias
+            int n = __popc(__ballot_sync(~0u, found != 0));
+            uint32_t next = left.most();
+            auto unsure = [&](bool same) {
+                uint32_t below = __shfl_down_sync(~0u, found, 1);
+                if (lane == n - 1) below = next;
+                const float own = expert < 0 ? 0.f : load_as(R.logits, row * R.ld + expert, R.type);
+                const float b = expert < 0 ? 0.f : __ldg(R.bias + expert);
+                const float own_below = __shfl_down_sync(~0u, own, 1), b_below = __shfl_down_sync(~0u, b, 1);
+                const float x = value_of(found), y = value_of(below);
+                const bool close = lane < (same ? n - 1 : n) && lane < 31 && below &&
+                                   !(x - y >= fmaf(fmaxf(fabsf(x), fabsf(y)), 0x1p-22f, near));
+                return __any_sync(~0u, close && (lane == n - 1 || own != own_below || b != b_below));
+            };
+            if (n > 0 && (unsure(false) || n == 32)) {
+                // candidates: all down to the k-th value less the bound
+                const float kth = value_of(__shfl_sync(~0u, found, n - 1)), to = kth - fmaf(fabsf(kth), 0x1p-22f, near);
+                while (n >= R.k && next != 0 && !(value_of(next) < to)) {
+                    if (n == 32) {
+                        again = true;
+                        break;
+                    }
+                    const int e = left.take(key, next, lane);
+                    if (lane == n) expert = e, found = next;
+                    ++n;
+                    next = left.most();
+                }
+                if (!again && unsure(true)) expert = order64(R, row, expert, n, lane);
+            }
+        }
+    }
+    if (again) expert = choose64(R, row, val, lane);
+    const float own = expert < 0 ? 0.f : load_as(R.logits, row * R.ld + expert, R.type);
     if (lane >= R.k) expert = -1;
     // weights of the choices
     const bool on = expert >= 0;
@@ -306,70 +539,74 @@ __device__ __forceinline__ void count_slots(const Route& R, int64_t from, int64_
 }
 
 template <bool SINGLE>
-__device__ __forceinline__ void place_slots(const Route& R, int block, int32_t* at)
+__device__ __forceinline__ void place_slots(const Route& R, int block, int64_t per_block, int32_t* at)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, E = R.experts;
     int32_t *total = at + warps * E, *before = total + E;
-    const int64_t first = block * R.per_block, last = min(first + R.per_block, R.slots);
+    const int64_t first = block * per_block, last = min(first + per_block, R.slots);
     const int64_t each = ((last - first + warps - 1) / warps + 31) / 32 * 32;
     const int64_t from = min(first + warp * each, last), to = min(from + each, last);
-    for (int i = threadIdx.x; i < warps * E; i += blockDim.x) at[i] = 0;
+    for (int i = threadIdx.x; i < (warps + 2) * E; i += blockDim.x) at[i] = 0;
     __syncthreads();
     count_slots(R, from, to, at + warp * E, lane);
-    __syncthreads();
     // of every expert: slots of all blocks, of the blocks before this one
     if (SINGLE) {
+        __syncthreads();
         for (int e = threadIdx.x; e < E; e += blockDim.x) {
             int all = 0;
+#pragma unroll 8
             for (int w = 0; w < warps; ++w) all += at[w * E + e];
             total[e] = all;
-            before[e] = 0;
         }
     } else {
-        // several threads an expert, each some of the blocks
-        int width = 32;
-        while (width < E && width < (int)blockDim.x) width *= 2;
-        const int part = threadIdx.x / width, parts = blockDim.x / width;
-        for (int e = threadIdx.x; e < E; e += blockDim.x) total[e] = before[e] = 0;
-        __syncthreads();
-        for (int e = threadIdx.x % width; e < E; e += width) {
-            int all = 0, less = 0;
+        // four experts a thread (hist has rows of a multiple of four), several threads for them, each some of the blocks
+        const int quads = (E + 3) / 4, parts = max(1, (int)blockDim.x / quads);
+        for (int i = threadIdx.x; i < quads * parts; i += blockDim.x) {
+            const int q = i % quads;
+            int4 all = make_int4(0, 0, 0, 0), less = all;
 #pragma unroll 8
-            for (int b = part; b < R.blocks; b += parts) {
-                const int n = R.hist[(int64_t)b * E + e];
-                all += n;
-                less += b < block ? n : 0;
+            for (int b = i / quads; b < R.blocks; b += parts) {
+                const int4 n = __ldcg(reinterpret_cast<const int4*>(R.hist + ((int64_t)b * quads + q) * 4));
+                all.x += n.x, all.y += n.y, all.z += n.z, all.w += n.w;
+                if (b < block) less.x += n.x, less.y += n.y, less.z += n.z, less.w += n.w;
             }
-            atomicAdd(&total[e], all);         // (whole numbers: any order gives the same sum)
-            atomicAdd(&before[e], less);
-        }
-    }
-    __syncthreads();
-    if (warp == 0) {
-        int base = 0;
-        for (int e0 = 0; e0 < E; e0 += 32) {
-            const int e = e0 + lane, n = e < E ? total[e] : 0;
-            int v = n;
+            const int a[4] = {all.x, all.y, all.z, all.w}, l[4] = {less.x, less.y, less.z, less.w};
 #pragma unroll
-            for (int d = 1; d < 32; d *= 2) {
-                const int u = __shfl_up_sync(~0u, v, d);
-                if (lane >= d) v += u;
-            }
-            if (e < E) {
-                before[e] += base + v - n;
-                if (block == 0) R.offsets[e] = base + v - n;
-            }
-            base += __shfl_sync(~0u, v, 31);
+            for (int j = 0; j < 4; ++j)
+                if (q * 4 + j < E) {
+                    atomicAdd(&total[q * 4 + j], a[j]);         // (whole numbers: any order gives the same sum)
+                    atomicAdd(&before[q * 4 + j], l[j]);
+                }
         }
-        if (block == 0 && lane == 0) R.offsets[E] = base;
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < E; e += blockDim.x) {
-        int p = before[e];
-        for (int w = 0; w < warps; ++w) {
-            const int n = at[w * E + e];
-            at[w * E + e] = p;
-            p += n;
+    // a warp 32 experts: slots of the experts before them, then of each before it
+    __shared__ int32_t sums[kMostRouted / 32];
+    for (int e0 = warp * 32; e0 < E; e0 += warps * 32) {
+        const int n = e0 + lane < E ? total[e0 + lane] : 0, all = __reduce_add_sync(~0u, n);
+        if (lane == 0) sums[e0 / 32] = all;
+    }
+    __syncthreads();
+    for (int e0 = warp * 32; e0 < E; e0 += warps * 32) {
+        const int base = __reduce_add_sync(~0u, lane < e0 / 32 ? sums[lane] : 0), e = e0 + lane, n = e < E ? total[e] : 0;
+        int v = n;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int u = __shfl_up_sync(~0u, v, d);
+            if (lane >= d) v += u;
+        }
+        if (e < E) {
+            int p = base + v - n;
+            if (block == 0) R.offsets[e] = p;
+            if (block == 0 && e == E - 1) R.offsets[E] = p + n;
+            // where the slots of each of this block's warps begin
+            p += before[e];
+#pragma unroll 8
+            for (int w = 0; w < warps; ++w) {
+                const int m = at[w * E + e];
+                at[w * E + e] = p;
+                p += m;
+            }
         }
     }
     __syncthreads();
@@ -385,20 +622,29 @@ __device__ __forceinline__ void place_slots(const Route& R, int block, int32_t* 
     }
 }
 
-// A warp a row, a threadblock `per_block` consecutive rows.  ORDER: 0 choices
-// and weights only; 1 one threadblock, which orders the rows as well; 2 every
-// threadblock leaves its counts for place_kernel.
-template <int VPL, int ORDER>
-__global__ void __launch_bounds__(512) route_kernel(const Route R)
+// A block's counts go to its row of hist, padded with zeros to a multiple of four.
+__device__ __forceinline__ void leave_counts(const Route& R, const int32_t* counts)
+{
+    const int width = (R.experts + 3) / 4 * 4;
+    for (int e = threadIdx.x; e < width; e += blockDim.x)
+        R.hist[(int64_t)blockIdx.x * width + e] = e < R.experts ? counts[e] : 0;
+}
+
+// Threads that a block of the router may have: more than 64 registers a thread
+// are needed from 16 experts a lane on.
+constexpr int route_threads(int vpl) { return vpl < 16 ? 1024 : 512; }
+
+// A warp a row, a threadblock `per_block` consecutive rows.
+template <int VPL>
+__global__ void __launch_bounds__(route_threads(VPL)) route_kernel(const Route R)
 {
     extern __shared__ __align__(16) unsigned char smem[];
     let_next_in();
     wait_for_previous();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     int32_t* hist = reinterpret_cast<int32_t*>(smem);
-    double* val = reinterpret_cast<double*>(smem + (ORDER == 2 ? (R.experts * 4 + 7) & ~7 : 0)) +
-                  (R.groups > 1 ? warp * R.experts : 0);
-    if (ORDER == 2) {
+    double* val = reinterpret_cast<double*>(smem + (R.order == 2 ? (R.experts * 4 + 7) & ~7 : 0)) + warp * R.experts;
+    if (R.order == 2) {
         for (int e = threadIdx.x; e < R.experts; e += blockDim.x) hist[e] = 0;
         __syncthreads();
     }
@@ -411,17 +657,14 @@ __global__ void __launch_bounds__(512) route_kernel(const Route R)
             R.chosen[row * R.k + lane] = expert;
             R.weights[row * R.k + lane] = weight;
         }
-        if (ORDER == 2 && expert >= 0) atomicAdd(&hist[expert], 1);
+        if (R.order == 2 && expert >= 0) atomicAdd(&hist[expert], 1);
     }
-    if (ORDER == 0) return;
+    if (R.order == 0) return;
     __syncthreads();
-    if (ORDER == 1) {
-        Route S = R;
-        S.per_block = R.slots;
-        place_slots<true>(S, 0, hist);
-    } else {
-        for (int e = threadIdx.x; e < R.experts; e += blockDim.x) R.hist[(int64_t)blockIdx.x * R.experts + e] = hist[e];
-    }
+    if (R.order == 1)
+        place_slots<true>(R, 0, R.slots, hist);
+    else
+        leave_counts(R, hist);
 }
 
 __global__ void __launch_bounds__(512) count_kernel(const Route R)
@@ -438,7 +681,7 @@ __global__ void __launch_bounds__(512) count_kernel(const Route R)
         if (e >= 0) atomicAdd(&hist[e], 1);
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < R.experts; e += blockDim.x) R.hist[(int64_t)blockIdx.x * R.experts + e] = hist[e];
+    leave_counts(R, hist);
 }
 
 template <bool SINGLE>
@@ -447,7 +690,7 @@ __global__ void __launch_bounds__(512) place_kernel(const Route R)
     extern __shared__ __align__(16) unsigned char smem[];
     let_next_in();
     wait_for_previous();
-    place_slots<SINGLE>(R, blockIdx.x, reinterpret_cast<int32_t*>(smem));
+    place_slots<SINGLE>(R, blockIdx.x, R.per_block, reinterpret_cast<int32_t*>(smem));
 }
 
 // The gradient of a row's logits from those of its weights, for the choices as they are:
@@ -477,11 +720,7 @@ __global__ void __launch_bounds__(256) route_grad_kernel(const Route R)
     const bool on = expert >= 0;
     float l[VPL], most = 0.f, sum = 1.f;
     if (dense) {
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-            const int e = i * 32 + lane;
-            l[i] = e < R.experts ? load_as(R.logits, row * R.ld + e, R.type) : -INFINITY;
-        }
+        load_row<VPL>(R, row, lane, l);
         most = l[0];
 #pragma unroll
         for (int i = 1; i < VPL; ++i) most = fmaxf(most, l[i]);
@@ -493,8 +732,9 @@ __global__ void __launch_bounds__(256) route_grad_kernel(const Route R)
             sum += l[i];
         }
         sum = warp_sum(sum);
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) l[i] = sum == 0.f ? 0.f : l[i] / sum;
+        for (int i = 0; i < VPL; ++i) l[i] *= inv;
     }
     float part = 0.f;              // of a choice: its own term of the gradient
     float all = 0.f;
@@ -514,17 +754,22 @@ __global__ void __launch_bounds__(256) route_grad_kernel(const Route R)
 #pragma unroll
     for (int i = 0; i < VPL; ++i) d[i] = 0.f;
     for (int j = 0; j < R.k; ++j) {
-        const int e = __shfl_sync(~0u, expert, j);
+        const int e = __shfl_sync(~0u, expert, j) - lane * VPL;
         const float v = __shfl_sync(~0u, part, j);
 #pragma unroll
         for (int i = 0; i < VPL; ++i)
-            if (e == i * 32 + lane) d[i] += v;
+            if (e == i) d[i] += v;
     }
+    if (dense) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        const int e = i * 32 + lane;
-        if (e < R.experts) store_as(R.dlogits, row * R.ld_d + e, R.type, dense ? l[i] * (d[i] - all) : d[i]);
+        for (int i = 0; i < VPL; ++i) d[i] = l[i] * (d[i] - all);
     }
+    if (R.type == CCL_F32)
+        store_row<VPL, Type<CCL_F32>>((float*)R.dlogits + row * R.ld_d, lane * VPL, R.experts, R.vec_d, d);
+    else if (R.type == CCL_BF16)
+        store_row<VPL, Type<CCL_BF16>>((uint16_t*)R.dlogits + row * R.ld_d, lane * VPL, R.experts, R.vec_d, d);
+    else
+        store_row<VPL, Type<CCL_F16>>((uint16_t*)R.dlogits + row * R.ld_d, lane * VPL, R.experts, R.vec_d, d);
 }
 
 }  // namespace tensor
