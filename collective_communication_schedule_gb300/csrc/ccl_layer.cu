@@ -31,8 +31,8 @@ static ccl_status_t array(const std::string& who, const char* what, const void* 
 }
 
 // ---------------------------------------------------------------- router
-constexpr int kOrderThreads = 512;
-constexpr int kRouteSmem = 16 * kMostRouted * 8 + kMostRouted * 4;     // 16 warps' values and a block's counts
+constexpr int kOrderThreads = 1024;
+constexpr int kRouteSmem = 34 * kMostRouted * 4;       // counts of 32 warps and two of the block (more than 16 warps' values)
 
 // The kernels for every number of experts a lane, from the smallest up: widths
 // that usual numbers of experts fill, so that groups of them are whole lanes.
@@ -100,7 +100,7 @@ static ccl_status_t check_router(const std::string& who, int64_t rows, int64_t e
 }
 
 // As many rows go to one threadblock, which orders them as well.
-constexpr int kRowsOfOne = 32;
+constexpr int kRowsOfOne = 16;
 
 static ccl_status_t route(const ccl_route_t* a, char* base, int64_t* need, cudaStream_t stream)
 {
@@ -167,6 +167,11 @@ static ccl_status_t route(const ccl_route_t* a, char* base, int64_t* need, cudaS
     const int64_t each = 16 / element_bytes(a->dtype);
     R.vec = aligned16(a->logits) && ld % each == 0 && a->experts % each == 0;
     const RouteKernel& k = route_kernel_for(a->experts);
+    R.vec_b = aligned16(a->bias) && a->experts % 4 == 0;
+    if (groups > 1) {
+        R.group_size = R.experts / groups;
+        R.group_lanes = R.group_size % k.vpl ? 0 : R.group_size / k.vpl;
+    }
     const int most = route_threads(k.vpl);
     // values in 64 bits (and groups that are not whole lanes) need shared memory: for a warp each
     const bool held = a->bias || groups > 1;
@@ -227,7 +232,7 @@ static ccl_status_t expert_order(const ccl_expert_order_t* a, char* base, int64_
     R.per_block = (a->slots + R.blocks - 1) / R.blocks;
     if (R.blocks == 1) return launch(place_kernel<true>, dim3(1), kOrderThreads, order_smem(R.experts, kOrderThreads), stream, R);
     R.blocks = (int32_t)((a->slots + R.per_block - 1) / R.per_block);
-    TRY(launch(count_kernel, dim3(R.blocks), kOrderThreads, a->experts * 4, stream, R));
+    TRY(launch(count_kernel, dim3(R.blocks), 512, a->experts * 4, stream, R));
     return launch(place_kernel<false>, dim3(R.blocks), kOrderThreads, order_smem(R.experts, kOrderThreads), stream, R);
 }
 

@@ -51,11 +51,11 @@ __device__ __forceinline__ float warp_sum(float v)
     for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(~0u, v, d);
     return v;
 }
-__device__ __forceinline__ float warp_max(float v)
+__device__ __forceinline__ float warp_max(float v)       // NaN counts for nothing
 {
-#pragma unroll
-    for (int d = 16; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, d));
-    return v;
+    float r;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
 }
 
 }  // namespace tensor

@@ -24,6 +24,8 @@ struct Route {
     int64_t slots, per_block;      // rows x k; rows of a block (route), slots of a block (order)
     int32_t experts, k, type, score, groups, top_groups, group_best, renormalize, blocks;
     int32_t scored;                // values other than the logits decide something
+    int32_t group_size, group_lanes;   // experts of a group; lanes of one where they are whole lanes, else 0
+    int32_t vec_b;                 // bias can be read 16 bytes at a time
     int32_t order;                 // 0: choices and weights only, 1: one threadblock, which orders the rows as well, 2: counts for
                                    // place_kernel are left in hist
     int32_t vec, vec_d;            // rows of logits can be read, of dlogits written 16 bytes at a time
@@ -70,6 +72,7 @@ template <typename F>
 __device__ __forceinline__ uint32_t best_groups(const Route& R, F a, F size, int lane, F near, bool& close)
 {
     int rank = 0;
+#pragma unroll 8
     for (int g = 0; g < R.groups; ++g) {
         const F u = __shfl_sync(~0u, a, g);
         rank += u > a || (u == a && g < lane);
@@ -94,15 +97,16 @@ template <int VPL>
 __device__ __forceinline__ uint32_t keep_groups(const Route& R, const float (&v)[VPL], float* val, int lane, float near,
                                                 bool& close)
 {
-    const int size = R.experts / R.groups, lanes = size / VPL;
+    const int size = R.group_size, lanes = R.group_lanes;
     float a = -INFINITY, b = -INFINITY;
-    if (lanes * VPL == size) {
+    if (lanes) {
         float x = -INFINITY, y = -INFINITY;
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
             y = fmaxf(y, fminf(x, v[i]));
             x = fmaxf(x, v[i]);
         }
+#pragma unroll 4
         for (int i = 0; i < lanes; ++i) {
             const float u = __shfl_sync(~0u, x, lane * lanes + i), w = __shfl_sync(~0u, y, lane * lanes + i);
             b = fmaxf(fmaxf(b, w), fminf(a, u));
@@ -221,7 +225,7 @@ __device__ __noinline__ int order64(const Route& R, int64_t row, int expert, int
 // and the third value of a group may be in the wrong order.
 __device__ __noinline__ bool groups64(const Route& R, int64_t row, int lane, float most, float inv, float near, uint32_t& kept)
 {
-    const int size = R.experts / R.groups;
+    const int size = R.group_size;
     const bool softmax = R.score != CCL_SCORE_SIGMOID;
     float a = -INFINITY, b = -INFINITY, third = -INFINITY;
     int at_a = -1, at_b = -1;
@@ -277,7 +281,7 @@ __device__ __noinline__ int choose64(const Route& R, int64_t row, double* val, i
     }
     __syncwarp();
     if (R.groups > 1) {
-        const int size = E / R.groups;
+        const int size = R.group_size;
         double a = -INFINITY, b = -INFINITY;
         if (lane < R.groups)
             for (int i = 0; i < size; ++i) {
@@ -387,7 +391,8 @@ __device__ __forceinline__ void store_row(typename E::Raw* p, int at, int n, boo
 //     score, which is 1 / sum;
 //   adding the bias, or two values, rounds to 2^-24 of the larger, twice.
 template <int VPL>
-__device__ __forceinline__ void route_row(const Route& R, int64_t row, double* val, int lane, int& expert, float& weight)
+__device__ __forceinline__ void route_row(const Route& R, int64_t row, double* val, int lane, int group, int& expert,
+                                          float& weight)
 {
     float l[VPL];
     load_row<VPL>(R, row, lane, l);
@@ -418,10 +423,13 @@ __device__ __forceinline__ void route_row(const Route& R, int64_t row, double* v
         if (R.scored) {
             const float inv = 1.f / sum;
             near = softmax ? inv * 0x1p-18f : 0x1p-20f;
+            float bias[VPL];
+            if (R.bias)
+                load_row<VPL, Type<CCL_F32>>(R.bias, lane * VPL, R.experts, R.vec_b, bias);
 #pragma unroll
             for (int i = 0; i < VPL; ++i) {
                 float c = softmax ? exp2_near((l[i] - most) * 1.4426950408889634f) * inv : sigmoid(l[i]);
-                if (R.bias && lane * VPL + i < R.experts) c += __ldg(R.bias + lane * VPL + i);
+                if (R.bias) c += bias[i];
                 v[i] = l[i] == -INFINITY || c == -INFINITY ? -INFINITY : fmaxf(c, -3.402823466e38f);
             }
         } else {
@@ -435,24 +443,21 @@ __device__ __forceinline__ void route_row(const Route& R, int64_t row, double* v
         }
 #pragma unroll
         for (int i = 0; i < VPL; ++i) key[i] = v[i] == -INFINITY ? 0u : key_of(R.bias ? v[i] : l[i]);
-        if (R.groups > 1) {
-            const int size = R.experts / R.groups;
-            if (size % VPL == 0) {
-                if (!(kept >> min(lane / (size / VPL), 31) & 1)) {
+        if (R.group_lanes) {
+            if (!(kept >> group & 1)) {
 #pragma unroll
-                    for (int i = 0; i < VPL; ++i) key[i] = 0;
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < VPL; ++i)
-                    if (!(kept >> min((lane * VPL + i) / size, 31) & 1)) key[i] = 0;
+                for (int i = 0; i < VPL; ++i) key[i] = 0;
             }
+        } else if (R.groups > 1) {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                if (!(kept >> min((lane * VPL + i) / R.group_size, 31) & 1)) key[i] = 0;
         }
     }
     expert = -1;
+    uint32_t found = 0;
     if (!again) {
         Picker<VPL> left(key);
-        uint32_t found = 0;
         for (int j = 0; j < R.k; ++j) {
             const uint32_t largest = left.most();
             if (largest == 0) break;
@@ -492,7 +497,8 @@ __device__ __forceinline__ void route_row(const Route& R, int64_t row, double* v
         }
     }
     if (again) expert = choose64(R, row, val, lane);
-    const float own = expert < 0 ? 0.f : load_as(R.logits, row * R.ld + expert, R.type);
+    float own = value_of(found);       // of a number's key, without a bias, the logit itself
+    if (R.bias || again || !(own > -3.402823466e38f)) own = expert < 0 ? 0.f : load_as(R.logits, row * R.ld + expert, R.type);
     if (lane >= R.k) expert = -1;
     // weights of the choices
     const bool on = expert >= 0;
@@ -527,15 +533,12 @@ __device__ __forceinline__ int expert_at(const Route& R, int64_t s)
     }
     return e;
 }
-// warps' counts of the experts of their slots
-__device__ __forceinline__ void count_slots(const Route& R, int64_t from, int64_t to, int32_t* mine, int lane)
+// A warp's count of the experts of 32 slots (a lane each, -1: none)
+__device__ __forceinline__ void count_32(int e, int32_t* mine, int lane)
 {
-    for (int64_t s = from + lane; s - lane < to; s += 32) {
-        const int e = s < to ? expert_at(R, s) : -1;
-        const uint32_t peers = __match_any_sync(~0u, e);
-        if (e >= 0 && lane == __ffs(peers) - 1) mine[e] += __popc(peers);
-        __syncwarp();
-    }
+    const uint32_t peers = __match_any_sync(~0u, e);
+    if (e >= 0 && lane == __ffs(peers) - 1) mine[e] += __popc(peers);
+    __syncwarp();
 }
 
 template <bool SINGLE>
@@ -546,9 +549,12 @@ __device__ __forceinline__ void place_slots(const Route& R, int block, int64_t p
     const int64_t first = block * per_block, last = min(first + per_block, R.slots);
     const int64_t each = ((last - first + warps - 1) / warps + 31) / 32 * 32;
     const int64_t from = min(first + warp * each, last), to = min(from + each, last);
+    // (the first 32 slots of a warp, mostly all of them, are read once and early)
+    const int own = from + lane < to ? expert_at(R, from + lane) : -1;
     for (int i = threadIdx.x; i < (warps + 2) * E; i += blockDim.x) at[i] = 0;
     __syncthreads();
-    count_slots(R, from, to, at + warp * E, lane);
+    count_32(own, at + warp * E, lane);
+    for (int64_t s = from + 32 + lane; s - lane < to; s += 32) count_32(s < to ? expert_at(R, s) : -1, at + warp * E, lane);
     // of every expert: slots of all blocks, of the blocks before this one
     if (SINGLE) {
         __syncthreads();
@@ -601,18 +607,22 @@ __device__ __forceinline__ void place_slots(const Route& R, int block, int64_t p
             if (block == 0 && e == E - 1) R.offsets[E] = p + n;
             // where the slots of each of this block's warps begin
             p += before[e];
-#pragma unroll 8
-            for (int w = 0; w < warps; ++w) {
-                const int m = at[w * E + e];
-                at[w * E + e] = p;
-                p += m;
+            for (int w0 = 0; w0 < warps; w0 += 8) {
+                int m[8];
+#pragma unroll
+                for (int w = 0; w < 8; ++w) m[w] = w0 + w < warps ? at[(w0 + w) * E + e] : 0;
+#pragma unroll
+                for (int w = 0; w < 8; ++w) {
+                    if (w0 + w < warps) at[(w0 + w) * E + e] = p;
+                    p += m[w];
+                }
             }
         }
     }
     __syncthreads();
     int32_t* next = at + warp * E;
     for (int64_t s = from + lane; s - lane < to; s += 32) {
-        const int e = s < to ? expert_at(R, s) : -1;
+        const int e = s - lane == from ? own : s < to ? expert_at(R, s) : -1;
         const uint32_t peers = __match_any_sync(~0u, e);
         const int p = e >= 0 ? next[e] + __popc(peers & ((1u << lane) - 1)) : -1;
         __syncwarp();
@@ -648,11 +658,12 @@ __global__ void __launch_bounds__(route_threads(VPL)) route_kernel(const Route R
         for (int e = threadIdx.x; e < R.experts; e += blockDim.x) hist[e] = 0;
         __syncthreads();
     }
+    const int group = R.group_lanes ? min(lane / R.group_lanes, 31) : 0;       // of this lane's experts
     const int64_t first = blockIdx.x * R.per_block, last = min(first + R.per_block, R.rows);
     for (int64_t row = first + warp; row < last; row += warps) {
         int expert;
         float weight;
-        route_row<VPL>(R, row, val, lane, expert, weight);
+        route_row<VPL>(R, row, val, lane, group, expert, weight);
         if (lane < R.k) {
             R.chosen[row * R.k + lane] = expert;
             R.weights[row * R.k + lane] = weight;
@@ -685,7 +696,7 @@ __global__ void __launch_bounds__(512) count_kernel(const Route R)
 }
 
 template <bool SINGLE>
-__global__ void __launch_bounds__(512) place_kernel(const Route R)
+__global__ void __launch_bounds__(1024) place_kernel(const Route R)
 {
     extern __shared__ __align__(16) unsigned char smem[];
     let_next_in();

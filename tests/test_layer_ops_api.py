@@ -150,7 +150,7 @@ def test_workspaces_are_asked_for_and_checked():
 
     assert need("ccl_route", route()) == 0
     assert need("ccl_route", route(offsets=4 * A, place=5 * A)) >= 3 * 16 * 4      # counts of three blocks of 16 rows
-    assert need("ccl_route", route(offsets=4 * A, place=5 * A, rows=32)) == 0
+    assert need("ccl_route", route(offsets=4 * A, place=5 * A, rows=16)) == 0
     assert need("ccl_expert_order", order()) > 0 and need("ccl_expert_order", order(slots=100)) == 0
     assert need("ccl_layer_norm_grad", norm_grad()) >= 2 * 32 * 4
     assert need("ccl_layer_norm_grad", norm_grad(dw=None, db=None)) == 0
