@@ -17,13 +17,14 @@ LIB = os.path.join(HERE, "libccl.so")
 ROOT = os.path.dirname(HERE)
 INCLUDE = os.path.join(ROOT, "include")
 
-SOURCES = ["ccl_runtime.cu", "ccl_static.cu", "ccl_tensor.cu", "ccl_layer.cu", "ccl_norm.cu", "ccl_loss.cu", "ccl_compiler.cpp", "ccl_builtin.cpp",
+SOURCES = ["ccl_runtime.cu", "ccl_static.cu", "ccl_tensor.cu", "ccl_layer.cu", "ccl_norm.cu", "ccl_norm_f32.cu", "ccl_norm_bf16.cu",
+           "ccl_norm_f16.cu", "ccl_loss.cu", "ccl_compiler.cpp", "ccl_builtin.cpp",
            "ccl_planner.cpp", "ccl_tuner.cpp", "ccl_persist.cpp", "ccl_codegen.cpp"]
 # device headers the run-time compiler of generated kernels receives as text
 EMBEDDED = ["ccl_layout.h", "ccl_core.cuh"]
 HEADERS = ["ccl_internal.h", "ccl_plan.h", "ccl_layout.h", "ccl_core.cuh", "ccl_tensor.cuh", "ccl_tensor_ortho.cuh",
            "ccl_tensor_passes.cuh", "ccl_tensor_product.cuh", "ccl_tensor_host.h", "ccl_tensor_launch.cuh",
-           "ccl_layer_common.cuh", "ccl_route.cuh", "ccl_rows.cuh", "ccl_norm.cuh", "ccl_loss.cuh"]
+           "ccl_layer_common.cuh", "ccl_route.cuh", "ccl_rows.cuh", "ccl_norm.cuh", "ccl_norm_kernels.cuh", "ccl_loss.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",

@@ -1,65 +1,55 @@
 // Layer norm and its gradients.  C ABI in include/ccl.h.
 #include <algorithm>
+#include <mutex>
 #include <string>
+#include <vector>
 
 #include <cuda_runtime.h>
 
-#include "ccl_norm.cuh"
+#include "ccl_norm_kernels.cuh"
 #include "ccl_tensor_host.h"
 
 namespace ccl {
 namespace tensor {
 
-// The kernels of one pair of types: rows in registers by vectors and by
-// elements, from the narrowest up, then rows of any length.
-struct NormKernels {
-    struct Rows {
-        int64_t width;             // elements of the longest row
-        int threads, rows;         // of a threadblock
-        void (*kernel)(const Norm);
-    };
-    Rows forward[2][4], backward[2][5];
-    void (*forward_long)(const Norm);
-    void (*backward_long)(const Norm);
-    void (*sums_long)(const Norm);
-    void (*sums)(const Norm);
-};
-
-template <int T, int TW>
-static const NormKernels& norm_kernels()
-{
-    constexpr int W = Type<T>::kVec, M = 8 / W;       // f32: half the elements a piece, twice the pieces
-    static const NormKernels k = {
-        {{{32 * 4 * 8, 128, 4, norm_kernel_rows<T, TW, 32, 4 * M, true>},
-          {128 * 4 * 8, 128, 1, norm_kernel_rows<T, TW, 128, 4 * M, true>},
-          {512 * 4 * 8, 512, 1, norm_kernel_rows<T, TW, 512, 4 * M, true>},
-          {1024 * 2 * 8, 1024, 1, norm_kernel_rows<T, TW, 1024, 2 * M, true>}},
-         {{32 * 16, 128, 4, norm_kernel_rows<T, TW, 32, 16, false>},
-          {128 * 16, 128, 1, norm_kernel_rows<T, TW, 128, 16, false>},
-          {512 * 16, 512, 1, norm_kernel_rows<T, TW, 512, 16, false>},
-          {1024 * 16, 1024, 1, norm_kernel_rows<T, TW, 1024, 16, false>}}},
-        {{{32 * 8, 256, 8, norm_grad_kernel_rows<T, TW, 32, M, true>},
-          {128 * 8, 256, 2, norm_grad_kernel_rows<T, TW, 128, M, true>},
-          {512 * 8, 512, 1, norm_grad_kernel_rows<T, TW, 512, M, true>},
-          {1024 * 8, 1024, 1, norm_grad_kernel_rows<T, TW, 1024, M, true>},
-          {512 * 4 * 8, 512, 1, norm_grad_kernel_rows<T, TW, 512, 4 * M, true>}},
-         {{32 * 8, 256, 8, norm_grad_kernel_rows<T, TW, 32, 8, false>},
-          {128 * 8, 256, 2, norm_grad_kernel_rows<T, TW, 128, 8, false>},
-          {512 * 8, 512, 1, norm_grad_kernel_rows<T, TW, 512, 8, false>},
-          {1024 * 8, 1024, 1, norm_grad_kernel_rows<T, TW, 1024, 8, false>},
-          {512 * 32, 512, 1, norm_grad_kernel_rows<T, TW, 512, 32, false>}}},
-        norm_kernel_long<T, TW>,
-        norm_grad_kernel_long<T, TW>,
-        norm_sums_kernel_long<T>,
-        norm_sums_kernel<TW>};
-    return k;
-}
+#define NORM_KERNELS(t, tw) const NormKernels& norm_kernels_##t##_##tw()
+NORM_KERNELS(f32, f32);
+NORM_KERNELS(bf16, bf16);
+NORM_KERNELS(bf16, f32);
+NORM_KERNELS(f16, f16);
+NORM_KERNELS(f16, f32);
+#undef NORM_KERNELS
 
 static const NormKernels& norm_kernels(int t, int tw)
 {
-    if (t == CCL_F32) return norm_kernels<CCL_F32, CCL_F32>();
-    if (t == CCL_BF16) return tw == CCL_F32 ? norm_kernels<CCL_BF16, CCL_F32>() : norm_kernels<CCL_BF16, CCL_BF16>();
-    return tw == CCL_F32 ? norm_kernels<CCL_F16, CCL_F32>() : norm_kernels<CCL_F16, CCL_F16>();
+    if (t == CCL_F32) return norm_kernels_f32_f32();
+    if (t == CCL_BF16) return tw == CCL_F32 ? norm_kernels_bf16_f32() : norm_kernels_bf16_bf16();
+    return tw == CCL_F32 ? norm_kernels_f16_f32() : norm_kernels_f16_f16();
+}
+
+// Shared memory of a backward pass: what its threads have on their way, or what
+// the sums of its groups go through.
+static size_t grad_smem(const NormKernels::Backward& r)
+{
+    return std::max<size_t>(r.each > 1 ? (size_t)rows_ahead(r.pieces) * 2 * r.pieces * kGradThreads * 16 : 0, (size_t)kGradThreads * r.each * 4);
+}
+
+// Once per device: the kernels of a pair of types may use that much.
+static ccl_status_t norm_device(const NormKernels& k)
+{
+    static std::mutex mu;
+    static std::vector<const NormKernels*> known[64];
+    int d = 0;
+    TRY_CUDA(cudaGetDevice(&d), "cudaGetDevice");
+    if (d < 0 || d >= 64) return fail(CCL_ERR_UNSUPPORTED, "device index above 63");
+    std::lock_guard<std::mutex> lock(mu);
+    if (std::find(known[d].begin(), known[d].end(), &k) != known[d].end()) return CCL_OK;
+    for (const auto& form : k.backward)
+        for (const auto& r : form)
+            TRY_CUDA(cudaFuncSetAttribute(r.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)grad_smem(r)),
+                     "shared memory of a norm's gradient");
+    known[d].push_back(&k);
+    return CCL_OK;
 }
 
 static ccl_status_t check_norm(const std::string& who, int64_t rows, int64_t n, int dtype, int wdtype)
@@ -119,11 +109,9 @@ static ccl_status_t layer_norm(const ccl_layer_norm_t* a, cudaStream_t stream)
     return launch(k.forward_long, dim3((unsigned)a->rows), 1024, 0, stream, N);
 }
 
-// Blocks that keep sums of dw and db: by the sizes alone, so that the order of
-// the sums is.
 static int norm_blocks(int64_t rows, int64_t at_once)
 {
-    return (int)std::min<int64_t>(304, std::max<int64_t>(1, (rows + at_once - 1) / at_once));
+    return (int)std::min<int64_t>(kNormBlocks, std::max<int64_t>(1, (rows + at_once - 1) / at_once));
 }
 
 static ccl_status_t layer_norm_grad(const ccl_layer_norm_grad_t* a, char* base, int64_t* need, cudaStream_t stream)
@@ -178,18 +166,19 @@ static ccl_status_t layer_norm_grad(const ccl_layer_norm_grad_t* a, char* base, 
     const int64_t each = a->dtype == CCL_F32 ? 4 : 8;
     const bool vec = a->n % each == 0 && aligned16(a->x) && aligned16(a->dy) && aligned16(a->dx) && aligned16(a->w) &&
                      N.ld_x % each == 0 && N.ld_dy % each == 0 && N.ld_dx % each == 0;
-    const NormKernels::Rows* fit = nullptr;
+    TRY(norm_device(k));
+    const NormKernels::Backward* fit = nullptr;
     for (const auto& r : k.backward[!vec])
         if (!fit && a->n <= r.width) fit = &r;
     if (fit) {
-        N.blocks = norm_blocks(a->rows, fit->rows);
-        TRY(launch(fit->kernel, dim3(N.blocks), fit->threads, 0, stream, N));
+        N.blocks = norm_blocks(a->rows, kGradThreads / fit->across);
+        TRY(launch(fit->kernel, dim3(N.blocks), kGradThreads, grad_smem(*fit), stream, N));
     } else {
         if (a->dx) TRY(launch(k.backward_long, dim3((unsigned)a->rows), 1024, 0, stream, N));
         N.blocks = norm_blocks(a->rows, 32);
         if (sums) TRY(launch(k.sums_long, dim3((unsigned)((a->n + 255) / 256), N.blocks), 256, 0, stream, N));
     }
-    if (sums) TRY(launch(k.sums, dim3((unsigned)((a->n + 31) / 32), 2), 512, 0, stream, N));
+    if (sums) TRY(launch(k.sums, dim3((unsigned)((a->n + 31) / 32), 2), 1024, 0, stream, N));
     return CCL_OK;
 }
 

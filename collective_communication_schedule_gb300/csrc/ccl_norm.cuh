@@ -6,6 +6,13 @@
 namespace ccl {
 namespace tensor {
 
+// Blocks of a backward pass that keep sums of dw and db: by the sizes alone, so
+// that the order of the sums is.
+constexpr int kNormBlocks = 152;
+constexpr int kGradThreads = 1024;
+// rows that the backward pass has on their way, for so many pieces of 16 bytes a thread: what shared memory holds
+__host__ __device__ constexpr int rows_ahead(int pieces) { return pieces == 1 ? 4 : pieces == 2 ? 3 : 1; }
+
 struct Norm {
     const void *x, *dy, *w, *b;
     void *y, *dx, *dw, *db;
@@ -17,45 +24,37 @@ struct Norm {
     float eps;
 };
 
-// Sum over the TPR threads of a row (all of them get it): a warp, or warps of
-// a threadblock through shared memory.  buf: 32 floats a row.
+// Sum over the TPR threads of a row (all of them get it): a warp, or a
+// threadblock through shared memory.  buf: 32 words, not read by a slower warp any
+// more (calls take turns with two, each behind the other's barrier).
 template <int TPR>
 __device__ __forceinline__ float row_sum(float v, float* buf, int tid)
 {
     v = warp_sum(v);
     if (TPR == 32) return v;
-    __syncthreads();
     if ((tid & 31) == 0) buf[tid >> 5] = v;
     __syncthreads();
     float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < TPR / 32; ++i) s += buf[i];
-    return s;
-}
-template <int TPR>
-__device__ __forceinline__ float2 row_sum2(float2 v, float2* buf, int tid)
-{
-    v.x = warp_sum(v.x);
-    v.y = warp_sum(v.y);
-    if (TPR == 32) return v;
-    __syncthreads();
-    if ((tid & 31) == 0) buf[tid >> 5] = v;
-    __syncthreads();
-    float2 s = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int i = 0; i < TPR / 32; ++i) s.x += buf[i].x, s.y += buf[i].y;
+    for (int i = 0; i < TPR / 32; i += 4) {
+        const float4 p = *reinterpret_cast<const float4*>(buf + i);
+        s += (p.x + p.y) + (p.z + p.w);
+    }
     return s;
 }
 
-// W consecutive elements at p (VEC: 16 bytes), in 32 bits
+// W consecutive elements at p, in 32 bits: at a time where they fill 8 or 16 bytes (VEC), else one by one.
 template <typename E, bool VEC, int W>
 __device__ __forceinline__ void read(const typename E::Raw* p, float* v)
 {
-    if (VEC && W == E::kVec) {
+    if (VEC && W == 8 && E::kVec == 8) {
         E::unpack(*reinterpret_cast<const uint4*>(p), v);
-    } else if (VEC && W == 8 && E::kVec == 4) {
-        E::unpack(*reinterpret_cast<const uint4*>(p), v);
-        E::unpack(*reinterpret_cast<const uint4*>(p + 4), v + 4);
+    } else if (VEC && W == 4 && E::kVec == 8) {
+        const uint2 u = *reinterpret_cast<const uint2*>(p);
+        E::unpack4(u, v);
+    } else if (VEC && E::kVec == 4) {
+#pragma unroll
+        for (int i = 0; i < W; i += 4) E::unpack(*reinterpret_cast<const uint4*>(p + i), v + i);
     } else {
 #pragma unroll
         for (int i = 0; i < W; ++i) v[i] = E::load(p + i);
@@ -64,11 +63,13 @@ __device__ __forceinline__ void read(const typename E::Raw* p, float* v)
 template <typename E, bool VEC, int W>
 __device__ __forceinline__ void write(typename E::Raw* p, const float* v)
 {
-    if (VEC && W == E::kVec) {
+    if (VEC && W == 8 && E::kVec == 8) {
         *reinterpret_cast<uint4*>(p) = E::pack(v);
-    } else if (VEC && W == 8 && E::kVec == 4) {
-        *reinterpret_cast<uint4*>(p) = E::pack(v);
-        *reinterpret_cast<uint4*>(p + 4) = E::pack(v + 4);
+    } else if (VEC && W == 4 && E::kVec == 8) {
+        *reinterpret_cast<uint2*>(p) = E::pack4(v);
+    } else if (VEC && E::kVec == 4) {
+#pragma unroll
+        for (int i = 0; i < W; i += 4) *reinterpret_cast<uint4*>(p + i) = E::pack(v + i);
     } else {
 #pragma unroll
         for (int i = 0; i < W; ++i) E::store(p + i, v[i]);
@@ -83,69 +84,104 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_kernel_rows(const 
 {
     typedef Type<T> E;
     typedef Type<TW> EW;
+    typedef typename E::Raw Raw;
     constexpr int W = VEC ? E::kVec : 1;
     constexpr int kRows = TPR < 128 ? 128 / TPR : 1;
-    __shared__ float buf[2][32];
+    __shared__ __align__(16) float buf[2][32];
     let_next_in();
     wait_for_previous();
-    const int tid = threadIdx.x % TPR;
+    const int tid = threadIdx.x % TPR, n = (int)N.n;
     const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
     if (kRows > 1 && row >= N.rows) return;
-    const typename E::Raw* x = (const typename E::Raw*)N.x + row * N.ld_x;
-    float v[V][W];
-    float s = 0.f;
+    const Raw* x = (const Raw*)N.x + row * N.ld_x;
+    Raw* y = (Raw*)N.y + row * N.ld_y;
+    const typename EW::Raw *w = (const typename EW::Raw*)N.w, *b = (const typename EW::Raw*)N.b;
+    const float inv = 1.f / (float)n;
+    if constexpr (VEC) {
+        float v[V][W], t = 0.f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int64_t c = (int64_t)(i * TPR + tid) * W;
-        if (c < N.n) {
-            read<E, VEC, W>(x + c, v[i]);
-        } else {
+        for (int i = 0; i < V; ++i) {
+            if ((i * TPR + tid) * W < n) {
+                read<E, VEC, W>(x + (i * TPR + tid) * W, v[i]);
+            } else {
 #pragma unroll
-            for (int e = 0; e < W; ++e) v[i][e] = 0.f;
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-#pragma unroll
-        for (int e = 0; e < W; ++e) s += v[i][e];
-    const float inv = 1.f / (float)N.n;
-    const float mean = row_sum<TPR>(s, buf[0], tid) * inv;
-    s = 0.f;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-        if ((int64_t)(i * TPR + tid) * W < N.n) {
-#pragma unroll
-            for (int e = 0; e < W; ++e) {
-                const float d = v[i][e] - mean;
-                s = fmaf(d, d, s);
+                for (int e = 0; e < W; ++e) v[i][e] = 0.f;
             }
         }
-    const float rstd = 1.f / sqrtf(row_sum<TPR>(s, buf[1], tid) * inv + N.eps);
-    if (tid == 0) {
-        if (N.mean) N.mean[row] = mean;
-        if (N.rstd) N.rstd[row] = rstd;
-    }
-    typename E::Raw* y = (typename E::Raw*)N.y + row * N.ld_y;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int64_t c = (int64_t)(i * TPR + tid) * W;
-        if (c < N.n) {
-            float o[W];
+        for (int i = 0; i < V; ++i)
 #pragma unroll
-            for (int e = 0; e < W; ++e) o[e] = (v[i][e] - mean) * rstd;
-            if (N.w) {
-                float w[W];
-                read<EW, VEC, W>((const typename EW::Raw*)N.w + c, w);
+            for (int e = 0; e < W; ++e) t += v[i][e];
+        const float mean = row_sum<TPR>(t, buf[0], tid) * inv;
+        t = 0.f;
 #pragma unroll
-                for (int e = 0; e < W; ++e) o[e] *= w[e];
+        for (int i = 0; i < V; ++i)
+            if ((i * TPR + tid) * W < n) {
+#pragma unroll
+                for (int e = 0; e < W; ++e) {
+                    v[i][e] -= mean;
+                    t = fmaf(v[i][e], v[i][e], t);
+                }
             }
-            if (N.b) {
-                float b[W];
-                read<EW, VEC, W>((const typename EW::Raw*)N.b + c, b);
+        const float rstd = 1.f / sqrtf(row_sum<TPR>(t, buf[1], tid) * inv + N.eps);
+        if (tid == 0) {
+            if (N.mean) N.mean[row] = mean;
+            if (N.rstd) N.rstd[row] = rstd;
+        }
 #pragma unroll
-                for (int e = 0; e < W; ++e) o[e] += b[e];
+        for (int i = 0; i < V; ++i) {
+            const int c = (i * TPR + tid) * W;
+            if (c < n) {
+                float k[W];
+#pragma unroll
+                for (int e = 0; e < W; ++e) v[i][e] *= rstd;
+                if (w) {
+                    read<EW, VEC, W>(w + c, k);
+#pragma unroll
+                    for (int e = 0; e < W; ++e) v[i][e] *= k[e];
+                }
+                if (b) {
+                    read<EW, VEC, W>(b + c, k);
+#pragma unroll
+                    for (int e = 0; e < W; ++e) v[i][e] += k[e];
+                }
+                write<E, VEC, W>(y + c, v[i]);
             }
-            write<E, VEC, W>(y + c, o);
+        }
+    } else {
+        const int used = (n + TPR - 1) / TPR;              // elements that anybody has
+        Raw raw[V];
+        float v[V], t = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (i < used && i * TPR + tid < n) raw[i] = x[i * TPR + tid];
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (i < used && i * TPR + tid < n) {
+                v[i] = E::load(raw + i);
+                t += v[i];
+            }
+        const float mean = row_sum<TPR>(t, buf[0], tid) * inv;
+        t = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (i < used && i * TPR + tid < n) {
+                v[i] -= mean;
+                t = fmaf(v[i], v[i], t);
+            }
+        const float rstd = 1.f / sqrtf(row_sum<TPR>(t, buf[1], tid) * inv + N.eps);
+        if (tid == 0) {
+            if (N.mean) N.mean[row] = mean;
+            if (N.rstd) N.rstd[row] = rstd;
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = i * TPR + tid;
+            if (i >= used || c >= n) continue;
+            float o = v[i] * rstd;
+            if (w) o *= EW::load(w + c);
+            if (b) o += EW::load(b + c);
+            E::store(y + c, o);
         }
     }
 }
@@ -156,7 +192,7 @@ __global__ void __launch_bounds__(1024) norm_kernel_long(const Norm N)
 {
     typedef Type<T> E;
     typedef Type<TW> EW;
-    __shared__ float buf[2][32];
+    __shared__ __align__(16) float buf[2][32];
     let_next_in();
     wait_for_previous();
     const int tid = threadIdx.x;
@@ -188,98 +224,205 @@ __global__ void __launch_bounds__(1024) norm_kernel_long(const Norm N)
     }
 }
 
+__device__ __forceinline__ void copy16(uint32_t to, const void* from)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copies_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
+// Sums of two numbers over the ACROSS threads of a group (all of them get
+// both).  part: 32 pairs, not read by a slower warp any more.
+template <int ACROSS>
+__device__ __forceinline__ float2 group_sums(float2 s, float* part, int group, int warp, int lane)
+{
+    // the halves of a warp take one sum each
+    const bool up = lane & 16;
+    float v = (up ? s.y : s.x) + __shfl_xor_sync(~0u, up ? s.x : s.y, 16);
+#pragma unroll
+    for (int d = 8; d; d /= 2) v += __shfl_xor_sync(~0u, v, d);
+    if (ACROSS > 32) {
+        // sums of x in part[0..31], of y in part[32..63], by warp
+        if ((lane & 15) == 0) part[(up ? 32 : 0) + warp] = v;
+        named_sync(1 + group, ACROSS);
+        constexpr int width = ACROSS / 32;
+        const int l = lane & 15;
+        const float* p = part + (up ? 32 : 0) + group * width;
+        v = p[l & (width - 1)];
+        if (width == 32) v += p[l + 16];
+#pragma unroll
+        for (int d = width < 16 ? width / 2 : 8; d; d /= 2) v += __shfl_xor_sync(~0u, v, d);
+    }
+    return make_float2(__shfl_sync(~0u, v, 0), __shfl_sync(~0u, v, 16));
+}
+
 // dx = rstd (g - mean(g) - xh mean(g xh)) with g = dy w, and, over this
-// block's rows, the sums of dy xh and dy that make dw and db.  Blocks take rows
-// in turn, TPR threads a row; sums stay in registers until the last row.
-template <int T, int TW, int TPR, int V, bool VEC>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_grad_kernel_rows(const Norm N)
+// block's rows, the sums of dy xh and dy that make dw and db.  ACROSS threads (a
+// warp, or a power of two from 128 up) lie across a row and own its columns, V
+// pieces each, whose sums they keep in registers; the block's groups of them take
+// rows in turn.  VEC: pieces of 16 bytes, which every thread copies for itself into
+// its own places in shared memory some rows before it needs them; else of
+// one element, read a row ahead.
+template <int T, int TW, int ACROSS, int V, bool VEC>
+__global__ void __launch_bounds__(kGradThreads) norm_grad_kernel_rows(const Norm N)
 {
     typedef Type<T> E;
     typedef Type<TW> EW;
-    constexpr int W = VEC ? E::kVec : 1;
-    constexpr int kThreadsHere = TPR < 256 ? 256 : TPR, kRows = kThreadsHere / TPR;
-    __shared__ float2 buf[kRows][32];
-    __shared__ float sums[kRows > 1 ? kRows : 1][kRows > 1 ? TPR * W : 1];
+    typedef typename E::Raw Raw;
+    constexpr int W = VEC ? E::kVec : 1, kAhead = rows_ahead(V);
+    __shared__ float part[2][64];
+    extern __shared__ __align__(16) unsigned char dyn[];
     let_next_in();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = (int)N.n;
+    constexpr int across = ACROSS, groups = kGradThreads / ACROSS;
+    const int group = threadIdx.x / across, tid = threadIdx.x & (across - 1);
+    const float inv = 1.f / (float)n;
+    const int step = gridDim.x * groups, row = blockIdx.x * groups + group;
+    int left = row < (int)N.rows ? ((int)N.rows - row - 1) / step + 1 : 0;       // rows of this group
+    // places of this thread: [row ahead][x, dy][piece], 16 bytes each, neighbours for neighbouring threads
+    unsigned char* place = dyn + threadIdx.x * 16;
+    const uint32_t place0 = smem_addr(place);
+    constexpr int kPlace = kGradThreads * 16;
+    bool mine[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) mine[i] = (i * across + tid) * W < n;
+    const Raw *px = (const Raw*)N.x + row * N.ld_x + tid * W, *pd = (const Raw*)N.dy + row * N.ld_dy + tid * W;
+    const int64_t next_x = step * N.ld_x, next_d = step * N.ld_dy;
     wait_for_previous();
-    const int tid = threadIdx.x % TPR, slot = threadIdx.x / TPR;
-    const float inv = 1.f / (float)N.n;
+    auto fetch = [&](int slot, bool any) {
+        if (any) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (mine[i]) {
+                    copy16(place0 + ((slot * 2 + 0) * V + i) * kPlace, px + i * across * W);
+                    copy16(place0 + ((slot * 2 + 1) * V + i) * kPlace, pd + i * across * W);
+                }
+        }
+        copies_end();
+        px += next_x;
+        pd += next_d;
+    };
+    Raw nx[VEC ? 1 : V], nd[VEC ? 1 : V];
+    auto fetch1 = [&](bool any) {
+        if (any) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (mine[i]) {
+                    nx[VEC ? 0 : i] = px[i * across];
+                    nd[VEC ? 0 : i] = pd[i * across];
+                }
+        }
+        px += next_x;
+        pd += next_d;
+    };
+    if constexpr (VEC) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) fetch(i, i < left);
+    } else {
+        fetch1(left > 0);
+    }
     float w[V][W], dw[V][W], db[V][W];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int64_t c = (int64_t)(i * TPR + tid) * W;
 #pragma unroll
         for (int e = 0; e < W; ++e) w[i][e] = 1.f, dw[i][e] = db[i][e] = 0.f;
-        if (N.w && c < N.n) read<EW, VEC, W>((const typename EW::Raw*)N.w + c, w[i]);
+        if (N.w && mine[i]) read<EW, VEC, W>((const typename EW::Raw*)N.w + (i * across + tid) * W, w[i]);
     }
-    for (int64_t first = (int64_t)blockIdx.x * kRows; first < N.rows; first += (int64_t)gridDim.x * kRows) {
-        const int64_t row = first + slot;
-        const bool live = row < N.rows;
-        float x[V][W], g[V][W];
-        float2 s = make_float2(0.f, 0.f);
-        const float mean = live ? N.mean[row] : 0.f, rstd = live ? N.rstd[row] : 0.f;
+    const float *pm = N.mean + row, *pr = N.rstd + row;
+    float next_mean = left > 0 ? *pm : 0.f, next_rstd = left > 0 ? *pr : 0.f;
+    Raw* dx = N.dx ? (Raw*)N.dx + row * N.ld_dx + tid * W : nullptr;
+    const int64_t next_o = step * N.ld_dx;
+    int slot = 0, turn = 0;
+    for (; left > 0; --left, turn ^= 1) {
+        const float mean = next_mean, rstd = next_rstd;
+        if (left > 1) next_mean = *(pm += step), next_rstd = *(pr += step);
+        // (16-byte pieces are read again from shared memory for dx, single elements kept)
+        float xh[V][W], g[V][W];
+        const unsigned char* at = place + slot * 2 * V * kPlace;
+        if constexpr (VEC) {
+            copies_wait<kAhead - 1>();
+        } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int64_t c = (int64_t)(i * TPR + tid) * W;
-            if (live && c < N.n) {
-                read<E, VEC, W>((const typename E::Raw*)N.x + row * N.ld_x + c, x[i]);
-                read<E, VEC, W>((const typename E::Raw*)N.dy + row * N.ld_dy + c, g[i]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < W; ++e) x[i][e] = mean, g[i][e] = 0.f;
-            }
+            for (int i = 0; i < V; ++i)
+                if (mine[i]) xh[i][0] = E::load(nx + i), g[i][0] = E::load(nd + i);
+            fetch1(left > 1);
         }
+        float2 s = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < V; ++i)
+            if (mine[i]) {
+                if constexpr (VEC) {
+                    read<E, VEC, W>((const Raw*)(at + i * kPlace), xh[i]);
+                    read<E, VEC, W>((const Raw*)(at + (V + i) * kPlace), g[i]);
+                }
 #pragma unroll
-            for (int e = 0; e < W; ++e) {
-                x[i][e] = (x[i][e] - mean) * rstd;
-                dw[i][e] = fmaf(g[i][e], x[i][e], dw[i][e]);
-                db[i][e] += g[i][e];
-                g[i][e] *= w[i][e];
-                s.x += g[i][e];
-                s.y = fmaf(g[i][e], x[i][e], s.y);
-            }
-        if (N.dx) {
-            s = row_sum2<TPR>(s, buf[slot], tid);
-            const float a = s.x * inv, b = s.y * inv;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int64_t c = (int64_t)(i * TPR + tid) * W;
-                if (live && c < N.n) {
-                    float o[W];
-#pragma unroll
-                    for (int e = 0; e < W; ++e) o[e] = rstd * (g[i][e] - a - x[i][e] * b);
-                    write<E, VEC, W>((typename E::Raw*)N.dx + row * N.ld_dx + c, o);
+                for (int e = 0; e < W; ++e) {
+                    xh[i][e] = (xh[i][e] - mean) * rstd;
+                    dw[i][e] = fmaf(g[i][e], xh[i][e], dw[i][e]);
+                    db[i][e] += g[i][e];
+                    g[i][e] *= w[i][e];
+                    s.x += g[i][e];
+                    s.y = fmaf(g[i][e], xh[i][e], s.y);
                 }
             }
+        if (dx) {
+            s = group_sums<ACROSS>(s, part[turn], group, warp, lane);
+            // rstd (g - a - xh b) = g rstd - a rstd - xh (b rstd)
+            const float ka = -s.x * inv * rstd, kb = -s.y * inv * rstd;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (mine[i]) {
+                    if constexpr (VEC) {
+                        asm volatile("" ::: "memory");
+                        read<E, VEC, W>((const Raw*)(at + i * kPlace), xh[i]);
+                        read<E, VEC, W>((const Raw*)(at + (V + i) * kPlace), g[i]);
+#pragma unroll
+                        for (int e = 0; e < W; ++e) xh[i][e] = (xh[i][e] - mean) * rstd, g[i][e] *= w[i][e];
+                    }
+#pragma unroll
+                    for (int e = 0; e < W; ++e) g[i][e] = fmaf(xh[i][e], kb, fmaf(g[i][e], rstd, ka));
+                    write<E, VEC, W>(dx + i * across * W, g[i]);
+                }
+            dx += next_o;
+        }
+        if constexpr (VEC) {
+            fetch(slot, left > kAhead);
+            slot = slot + 1 == kAhead ? 0 : slot + 1;
         }
     }
     if (!N.partial) return;
-    float* out = N.partial + (int64_t)blockIdx.x * 2 * N.n;
+    if (VEC) copies_wait<0>();
+    // the groups' sums, in turn through the places' memory
+    float* sums = reinterpret_cast<float*>(dyn);
+    float* out = N.partial + (int64_t)blockIdx.x * 2 * n;
 #pragma unroll
     for (int which = 0; which < 2; ++which)
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int64_t c = (int64_t)(i * TPR + tid) * W;
+            const int c = (i * across + tid) * W;
             float v[W];
 #pragma unroll
             for (int e = 0; e < W; ++e) v[e] = which ? db[i][e] : dw[i][e];
-            if (kRows > 1) {
+            if (groups > 1) {
                 __syncthreads();
 #pragma unroll
-                for (int e = 0; e < W; ++e) sums[slot][tid * W + e] = v[e];
+                for (int e = 0; e < W; ++e) sums[(group * W + e) * across + tid] = v[e];
                 __syncthreads();
+                if (group > 0) continue;
 #pragma unroll
                 for (int e = 0; e < W; ++e) {
                     v[e] = 0.f;
-#pragma unroll
-                    for (int r = 0; r < kRows; ++r) v[e] += sums[r][tid * W + e];
+#pragma unroll 4
+                    for (int r = 0; r < groups; ++r) v[e] += sums[(r * W + e) * across + tid];
                 }
             }
-            if (slot == 0 && c < N.n) {
+            if (c < n) {
 #pragma unroll
-                for (int e = 0; e < W; ++e) out[which * N.n + c + e] = v[e];
+                for (int e = 0; e < W; ++e) out[which * n + c + e] = v[e];
             }
         }
 }
@@ -290,7 +433,7 @@ __global__ void __launch_bounds__(1024) norm_grad_kernel_long(const Norm N)
 {
     typedef Type<T> E;
     typedef Type<TW> EW;
-    __shared__ float2 buf[32];
+    __shared__ __align__(16) float buf[2][32];
     let_next_in();
     wait_for_previous();
     const int tid = threadIdx.x;
@@ -305,7 +448,8 @@ __global__ void __launch_bounds__(1024) norm_grad_kernel_long(const Norm N)
         s.x += g;
         s.y = fmaf(g, (E::load(x + c) - mean) * rstd, s.y);
     }
-    s = row_sum2<1024>(s, buf, tid);
+    s.x = row_sum<1024>(s.x, buf[0], tid);
+    s.y = row_sum<1024>(s.y, buf[1], tid);
     const float a = s.x * inv, b = s.y * inv;
     typename E::Raw* dx = (typename E::Raw*)N.dx + row * N.ld_dx;
 #pragma unroll 4
@@ -336,13 +480,13 @@ __global__ void __launch_bounds__(256) norm_sums_kernel_long(const Norm N)
     out[N.n + c] = db;
 }
 
-// The blocks' sums added up in order: 32 columns a threadblock, 16 groups of
+// The blocks' sums added up in order: 32 columns a threadblock, 32 groups of
 // threads take the blocks in turn.  blockIdx.y: dw, db.
 template <int TW>
-__global__ void __launch_bounds__(512) norm_sums_kernel(const Norm N)
+__global__ void __launch_bounds__(1024) norm_sums_kernel(const Norm N)
 {
     typedef Type<TW> EW;
-    __shared__ float sums[16][32];
+    __shared__ float sums[32][32];
     let_next_in();
     wait_for_previous();
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
@@ -352,14 +496,18 @@ __global__ void __launch_bounds__(512) norm_sums_kernel(const Norm N)
     float s = 0.f;
     if (c < N.n) {
         const float* p = N.partial + blockIdx.y * N.n + c;
-#pragma unroll 8
-        for (int i = ty; i < N.blocks; i += 16) s += p[(int64_t)i * 2 * N.n];
+        // (at most kNormBlocks / 32 loads a thread, all on their way at a time)
+        float v[(kNormBlocks + 31) / 32];
+#pragma unroll
+        for (int i = 0; i < (kNormBlocks + 31) / 32; ++i) v[i] = i * 32 + ty < N.blocks ? __ldcg(p + (int64_t)(i * 32 + ty) * 2 * N.n) : 0.f;
+#pragma unroll
+        for (int i = 0; i < (kNormBlocks + 31) / 32; ++i) s += v[i];
     }
     sums[ty][tx] = s;
     __syncthreads();
     if (ty == 0 && c < N.n) {
 #pragma unroll
-        for (int i = 1; i < 16; ++i) s += sums[i][tx];
+        for (int i = 1; i < 32; ++i) s += sums[i][tx];
         EW::store(out + c, s);
     }
 }

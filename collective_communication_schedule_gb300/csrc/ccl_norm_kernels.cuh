@@ -1,0 +1,57 @@
+// The norm's kernels of one pair of types, one translation unit a type.
+#pragma once
+
+#include "ccl_norm.cuh"
+
+namespace ccl {
+namespace tensor {
+
+// Kernels for rows on 16 bytes and for any others, from the narrowest up, then
+// for rows of any length.
+struct NormKernels {
+    struct Forward {
+        int64_t width;             // elements of the longest row
+        int threads, rows;         // of a threadblock
+        void (*kernel)(const Norm);
+    };
+    struct Backward {
+        int64_t width;
+        int across;                // threads of a row
+        int pieces, each;          // of a thread, elements of one
+        void (*kernel)(const Norm);
+    };
+    Forward forward[2][7];
+    Backward backward[2][6];
+    void (*forward_long)(const Norm);
+    void (*backward_long)(const Norm);
+    void (*sums_long)(const Norm);
+    void (*sums)(const Norm);
+};
+
+template <int T, int TW>
+const NormKernels& norm_kernels_of()
+{
+    // (f32: half the elements a piece, twice the pieces)
+    constexpr int W = Type<T>::kVec, M = 8 / W;
+#define FORWARD(tpr, v, vec) {(tpr) * (v) * ((vec) ? W : 1), (tpr) < 128 ? 128 : (tpr), (tpr) < 128 ? 128 / (tpr) : 1, norm_kernel_rows<T, TW, tpr, v, vec>}
+#define BACKWARD(tpr, v, vec) {(tpr) * (v) * ((vec) ? W : 1), tpr, v, (vec) ? W : 1, norm_grad_kernel_rows<T, TW, tpr, v, vec>}
+    static const NormKernels k = {
+        {{FORWARD(32, M, true), FORWARD(32, 4 * M, true), FORWARD(128, 2 * M, true), FORWARD(128, 4 * M, true),
+          FORWARD(512, 2 * M, true), FORWARD(512, 4 * M, true), FORWARD(1024, 2 * M, true)},
+         {FORWARD(32, 4, false), FORWARD(32, 16, false), FORWARD(128, 16, false), FORWARD(256, 10, false), FORWARD(256, 16, false),
+          FORWARD(512, 16, false), FORWARD(1024, 16, false)}},
+        {{BACKWARD(32, 1, true), BACKWARD(128, 1, true), BACKWARD(256, 1, true), BACKWARD(512, 1, true), BACKWARD(1024, 1, true),
+          BACKWARD(1024, 2, true)},
+         {BACKWARD(32, 5, false), BACKWARD(128, 5, false), BACKWARD(256, 5, false), BACKWARD(512, 5, false), BACKWARD(1024, 5, false),
+          BACKWARD(1024, 8, false)}},
+        norm_kernel_long<T, TW>,
+        norm_grad_kernel_long<T, TW>,
+        norm_sums_kernel_long<T>,
+        norm_sums_kernel<TW>};
+#undef FORWARD
+#undef BACKWARD
+    return k;
+}
+
+}  // namespace tensor
+}  // namespace ccl
