@@ -22,12 +22,13 @@ static ccl_status_t loss_device(const Device** out)
     std::lock_guard<std::mutex> lock(mu);
     if (!all[d].ready) {
         TRY(look_up(&all[d], d));
-        for (auto kernel : {rowwise_kernel<1, STATS>, rowwise_kernel<2, STATS>, rowwise_kernel<1, SLOPE>, rowwise_kernel<2, SLOPE>})
+        for (auto kernel : {rowwise_kernel<1, STATS>, rowwise_kernel<2, STATS>, rowwise_kernel<1, SLOPE>, rowwise_kernel<2, SLOPE>,
+                            rowwise_kernel<1, STATS_TURNED>, rowwise_kernel<2, STATS_TURNED>, rowwise_kernel<1, SLOPE_TURNED>,
+                            rowwise_kernel<2, SLOPE_TURNED>})
             TRY_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBudget),
                      "shared memory of the rowwise kernel");
-        for (auto kernel : {sum_pair_kernel<1>, sum_pair_kernel<2>})
-            TRY_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBudget),
-                     "shared memory of the pair kernel");
+        TRY_CUDA(cudaFuncSetAttribute(sum_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBudget),
+                 "shared memory of the pair kernel");
         all[d].ready = true;
     }
     *out = &all[d];
@@ -38,30 +39,46 @@ static ccl_status_t loss_device(const Device** out)
 // sums depend on the sizes alone.
 constexpr int kShapeSms = 152;
 
-static Product values_of(int64_t rows, int64_t vocab, int64_t k, bool bf)
+// Up to this many rows, rows of w lie along the lanes: 128 rows of x or less would
+// leave lanes idle and cost the matrix instructions the same.
+constexpr int kTurnedRows = 128;
+
+// The product x w^T, in either orientation, and its shape.
+static Product values_of(int64_t rows, int64_t vocab, int64_t k, bool bf, Shape* sh)
 {
     Product P = {};
-    P.m = (int32_t)rows;
-    P.n = (int32_t)vocab;
+    const bool turned = rows <= kTurnedRows;
+    P.m = (int32_t)(turned ? vocab : rows);
+    P.n = (int32_t)(turned ? rows : vocab);
     P.k = (int32_t)k;
     P.groups = 1;
     P.alpha = 1.f;
     P.in_bf = P.out_bf = bf;
+    *sh = choose(P, kShapeSms, 1).best;
     return P;
 }
+// parts of a row's statistics
+static int64_t parts_of(int64_t rows, int64_t vocab, const Shape& sh)
+{
+    return rows <= kTurnedRows ? (vocab + 31) / 32 : (vocab + sh.bn - 1) / sh.bn;
+}
 
+// mode: STATS or SLOPE
 static ccl_status_t run_rowwise(const Device* dev, int mode, Rowwise* R, const Shape& sh, const Matrix& x, const Matrix& w,
                                 uint16_t* out, int64_t ld_out, cudaStream_t stream)
 {
-    TRY(complete(dev, &R->p, sh, x, w));
+    const bool turned = x.rows <= kTurnedRows;
+    if (turned) set_out(&R->p, out, ld_out, 0, R->p.out_bf);
+    TRY(complete(dev, &R->p, sh, turned ? w : x, turned ? x : w));
     R->p.out = out;
     R->p.ld_out = ld_out;
     const int bytes = (kTileM + sh.bn / sh.cg) * kSliceK * 2, fixed = 1024 + kStagingBytes;
     R->p.stages = std::min(kMaxStages, (kSmemBudget - fixed) / bytes);
     const int clusters = std::min(R->p.total, dev->sms / sh.cg);
-    void (*const kernels[2][2])(Rowwise) = {{rowwise_kernel<1, STATS>, rowwise_kernel<2, STATS>},
-                                            {rowwise_kernel<1, SLOPE>, rowwise_kernel<2, SLOPE>}};
-    return launch(kernels[mode == SLOPE][sh.cg - 1], dim3((unsigned)(clusters * sh.cg)), kThreads,
+    void (*const kernels[2][2][2])(Rowwise) = {
+        {{rowwise_kernel<1, STATS>, rowwise_kernel<2, STATS>}, {rowwise_kernel<1, STATS_TURNED>, rowwise_kernel<2, STATS_TURNED>}},
+        {{rowwise_kernel<1, SLOPE>, rowwise_kernel<2, SLOPE>}, {rowwise_kernel<1, SLOPE_TURNED>, rowwise_kernel<2, SLOPE_TURNED>}}};
+    return launch(kernels[mode == SLOPE][turned][sh.cg - 1], dim3((unsigned)(clusters * sh.cg)), kThreads,
                   fixed + (size_t)R->p.stages * bytes, stream, *R, sh.cg);
 }
 
@@ -95,12 +112,11 @@ static ccl_status_t cross_entropy(const ccl_cross_entropy_t* a, char* base, int6
     Arena ws = {base};
     Matrix x = {a->x, a->rows, a->k, ldx}, w = {a->w, a->vocab, a->k, ldw};
     Rowwise R = {};
-    R.p = values_of(a->rows, a->vocab, a->k, a->dtype == CCL_BF16);
     LossRows L = {};
     Shape sh = {};
     if (a->rows > 0) {
-        sh = choose(R.p, kShapeSms, 1).best;
-        L.tiles = (a->vocab + sh.bn - 1) / sh.bn;
+        R.p = values_of(a->rows, a->vocab, a->k, a->dtype == CCL_BF16, &sh);
+        L.tiles = parts_of(a->rows, a->vocab, sh);
         R.part = ws.take<float2>(L.tiles * a->rows * sizeof(float2));
         R.picked = ws.take<float>(a->rows * 4);
     }
@@ -130,7 +146,7 @@ static ccl_status_t cross_entropy(const ccl_cross_entropy_t* a, char* base, int6
     L.picked = R.picked;
     L.loss = a->loss;
     L.lse = a->lse;
-    return launch(loss_kernel, dim3((unsigned)((a->rows + 31) / 32)), 512, 0, stream, L);
+    return launch(loss_kernel, dim3((unsigned)((a->rows + 7) / 8)), 512, 0, stream, L);
 }
 
 // Rows of w whose derivatives are held at a time: what keeps them within 256 MB.
@@ -140,6 +156,36 @@ static int64_t piece_of(int64_t rows, int64_t vocab)
     const int64_t most = std::max<int64_t>(1024, kPieceBytes / 2 / std::max<int64_t>(1, rows) / 256 * 256);
     const int64_t pieces = (vocab + most - 1) / most;
     return pieces == 1 ? vocab : round_up((vocab + pieces - 1) / pieces, 256);
+}
+
+// dx of a piece: the product's shape, and the segments of the piece's classes
+// that are reduced side by side where its tiles alone would leave SMs idle.
+struct DxShape {
+    Shape shape;
+    int32_t segment, parts;
+};
+static DxShape dx_shape(int64_t rows, int64_t k, int64_t width)
+{
+    Product P = {};
+    P.m = (int32_t)k;
+    P.n = (int32_t)rows;
+    P.a_mn = 1;
+    DxShape best = {};
+    double least = 0;
+    for (int parts : {1, 2, 3, 4, 6, 8, 12, 16}) {
+        const int64_t segment = round_up((width + parts - 1) / parts, kSliceK);
+        if (parts > 1 && (segment < 8 * kSliceK || (parts - 1) * segment >= width)) break;
+        P.groups = parts;
+        P.k = (int32_t)std::min(segment, width);
+        const Choices c = choose(P, kShapeSms, 1);
+        const Shape& sh = c.pairs;
+        // whole waves of tiles, and the parts' way through memory and back at 3400 bytes a clock
+        const int64_t tiles = (k + 2 * kTileM - 1) / (2 * kTileM) * ((rows + sh.bn - 1) / sh.bn) * parts;
+        const double one = sh.cost / std::max(1.0, (double)tiles / (kShapeSms / 2));
+        const double cost = (double)((tiles + kShapeSms / 2 - 1) / (kShapeSms / 2)) * one + (parts > 1 ? 8.0 * parts * rows * k / 3400 + 4000 : 0);
+        if (best.parts == 0 || cost < least) best = {sh, parts > 1 ? (int32_t)segment : 0, parts}, least = cost;
+    }
+    return best;
 }
 
 static ccl_status_t cross_entropy_grad(const ccl_cross_entropy_grad_t* a, char* base, int64_t* need, cudaStream_t stream)
@@ -157,14 +203,19 @@ static ccl_status_t cross_entropy_grad(const ccl_cross_entropy_grad_t* a, char* 
     const int64_t piece = piece_of(a->rows, a->vocab), ld_dl = round_up(piece, 64), ld_sum = round_up(a->k, 32);
     const bool several = piece < a->vocab, bf = a->dtype == CCL_BF16, some = a->rows > 0 && (a->dx || a->dw);
     LossRows L = {};
+    DxShape dxs = {};
     uint16_t* dl = nullptr;
     float* sum = nullptr;
     Matrix clean = {nullptr, a->rows, a->k, round_up(a->k, 8)};
     if (some) {
         L.coef = ws.take<float4>(a->rows * sizeof(float4));
         L.scale = ws.take<float>(16);
+        L.block = ws.take<float2>((a->rows + 7) / 8 * sizeof(float2));
         dl = ws.take<uint16_t>(a->rows * ld_dl * 2);
-        if (several && a->dx) sum = ws.take<float>(a->rows * ld_sum * 4);
+        if (a->dx) {
+            dxs = dx_shape(a->rows, a->k, piece);
+            if (several || dxs.parts > 1) sum = ws.take<float>(dxs.parts * a->rows * ld_sum * 4);
+        }
         if (a->dw) clean.p = ws.take<uint16_t>(a->rows * clean.ld * 2);
     }
     if (need) {
@@ -210,19 +261,20 @@ static ccl_status_t cross_entropy_grad(const ccl_cross_entropy_grad_t* a, char* 
         L.clean = (uint16_t*)clean.p;
         L.ld_clean = clean.ld;
     }
-    TRY(launch(loss_scale_kernel, dim3(1), 1024, 0, stream, L));
     TRY(launch(loss_rows_kernel, dim3((unsigned)((a->rows + 7) / 8)), 256, 0, stream, L));
-    if (a->dw) TRY(launch(loss_clean_kernel, dim3((unsigned)std::min<int64_t>(a->rows, 608)), 256, 0, stream, L));
+    TRY(launch(loss_ready_kernel, dim3((unsigned)(a->dw ? std::min<int64_t>(a->rows, 152) : 1)), 256, 0, stream, L));
     for (int64_t first = 0; first < a->vocab; first += piece) {
         const int64_t width = std::min(piece, a->vocab - first);
         Matrix wp = w, dlp = {dl, a->rows, width, ld_dl};
         wp.p = (const uint16_t*)w.p + first * w.ld;
         wp.rows = width;
         Rowwise R = {};
-        R.p = values_of(a->rows, width, a->k, bf);
+        Shape shape;
+        R.p = values_of(a->rows, width, a->k, bf, &shape);
         R.coef = L.coef;
+        R.scale = L.scale;
         R.first = (int32_t)first;
-        TRY(run_rowwise(dev, SLOPE, &R, choose(R.p, kShapeSms, 1).best, x, wp, dl, ld_dl, stream));
+        TRY(run_rowwise(dev, SLOPE, &R, shape, x, wp, dl, ld_dl, stream));
         Product P = {};
         P.groups = 1;
         P.alpha = 1.f;
@@ -237,8 +289,12 @@ static ccl_status_t cross_entropy_grad(const ccl_cross_entropy_grad_t* a, char* 
             set_out(&px, a->dx, lddx, 0, bf);
             px.sum = sum;
             px.ld_sum = ld_sum;
+            px.bs_sum = a->rows * ld_sum;
             px.sum_first = first == 0;
-            px.sum_last = first + piece >= a->vocab;
+            if (dxs.parts > 1) {
+                px.groups = dxs.parts;
+                px.segment = dxs.segment;
+            }
         }
         if (a->dw) {   // dw[v, k] = sum_t x[t, k] dl[t, v]
             pw.m = (int32_t)a->k;
@@ -248,35 +304,37 @@ static ccl_status_t cross_entropy_grad(const ccl_cross_entropy_grad_t* a, char* 
             pw.alt = L.dirty;
             set_out(&pw, (uint16_t*)a->dw + first * lddw, lddw, 0, bf);
         }
-        const Choices cx = a->dx ? choose(px, kShapeSms) : Choices(), cw = a->dw ? choose(pw, kShapeSms) : Choices();
-        // one launch for both unless splitting or shapes of their own are worth more than the launch (9500 clocks)
-        const double one = cx.single.cost + cw.single.cost, two = cx.pairs.cost + cw.pairs.cost;
-        if (sum || (a->dx && a->dw && std::min(one, two) < cx.best.cost + cw.best.cost + 9500)) {
-            Pair S = {};
-            const Shape sx = two <= one ? cx.pairs : cx.single, sw = two <= one ? cw.pairs : cw.single;
-            S.p[0] = px;
-            TRY(complete(dev, &S.p[0], sx, wp, dlp));
-            int64_t most = S.p[0].total;
-            S.width = sx.bn;
-            if (a->dw) {
-                S.p[1] = pw;
-                TRY(complete(dev, &S.p[1], sw, x, dlp, &clean));
-                S.width = std::max(S.width, sw.bn);
-                most += S.p[1].total;
-            } else {
-                S.p[1] = S.p[0];
-                S.p[1].total = 0;
-            }
-            if (most > INT32_MAX) return fail(CCL_ERR_UNSUPPORTED, who + "too many tiles");
-            const int cg = sx.cg, bytes = (kTileM + S.width / cg) * kSliceK * 2, fixed = 1024 + kStagingBytes;
-            S.stages = std::min(kMaxStages, (kSmemBudget - fixed) / bytes);
-            const int clusters = (int)std::min<int64_t>(most, dev->sms / cg);
-            TRY(launch(cg == 2 ? sum_pair_kernel<2> : sum_pair_kernel<1>, dim3((unsigned)(clusters * cg)), kThreads,
-                       fixed + (size_t)S.stages * bytes, stream, S, cg));
+        if (!a->dx) {
+            TRY(run_product(pw, choose(pw, kShapeSms).best, x, dlp, &clean, stream));
             continue;
         }
-        if (a->dx) TRY(run_product(px, cx.best, wp, dlp, nullptr, stream));
-        if (a->dw) TRY(run_product(pw, cw.best, x, dlp, &clean, stream));
+        // both in one launch: the tiles of dw fill the places that those of dx leave
+        Pair S = {};
+        S.p[0] = px;
+        TRY(complete(dev, &S.p[0], dxs.shape, wp, dlp));
+        int64_t most = S.p[0].total;
+        S.width = dxs.shape.bn;
+        if (a->dw) {
+            const Shape sw = choose(pw, kShapeSms).pairs;
+            S.p[1] = pw;
+            TRY(complete(dev, &S.p[1], sw, x, dlp, &clean));
+            S.width = std::max(S.width, sw.bn);
+            most += S.p[1].total;
+        } else {
+            S.p[1] = S.p[0];
+            S.p[1].total = 0;
+        }
+        if (most > INT32_MAX) return fail(CCL_ERR_UNSUPPORTED, who + "too many tiles");
+        const int bytes = (kTileM + S.width / 2) * kSliceK * 2, fixed = 1024 + kStagingBytes;
+        S.stages = std::min(kMaxStages, (kSmemBudget - fixed) / bytes);
+        const int clusters = (int)std::min<int64_t>(most, dev->sms / 2);
+        TRY(launch(sum_pair_kernel, dim3((unsigned)(clusters * 2)), kThreads, fixed + (size_t)S.stages * bytes, stream, S, 2));
+    }
+    if (sum) {
+        LossSum Q = {sum, (uint16_t*)a->dx, a->rows, a->k, ld_sum, a->rows * ld_sum, lddx, dxs.parts, bf};
+        const int64_t blocks = (a->rows * ((a->k + 3) / 4) + 255) / 256;
+        if (blocks > INT32_MAX) return fail(CCL_ERR_UNSUPPORTED, who + "dx is too large");
+        TRY(launch(loss_sum_kernel, dim3((unsigned)blocks), 256, 0, stream, Q));
     }
     return CCL_OK;
 }

@@ -21,7 +21,8 @@ struct LossRows {
     const float *dloss, *dlse, *lse_in;
     float4* coef;
     float* scale;                  // [0]: of the derivatives (a power of two), [1]: its inverse
-    int32_t* dirty;                // not 0: a row that counts for nothing holds Inf or NaN
+    float2* block;                 // by 8 rows: the largest factor; not 0 if a row that counts for nothing holds Inf or NaN
+    int32_t* dirty;                // not 0 if one of all rows does
     const uint16_t* x;             // null: nobody asks
     uint16_t* clean;
     int64_t ld_x, ld_clean, k;
@@ -42,31 +43,33 @@ __device__ __forceinline__ int64_t target_of(const LossRows& L, int64_t row)
 
 // The parts of a row's tiles put together, in an order that the sizes fix:
 // lse = m + log(sum), loss = log(sum) + (m - the target's value), which keeps
-// the digits of a small loss.  32 rows a threadblock; 16 groups of threads take
+// the digits of a small loss.  8 rows a threadblock; 64 groups of threads take
 // the tiles in turn.
 static __global__ void __launch_bounds__(512) loss_kernel(const LossRows L)
 {
-    __shared__ float2 parts[16][32];
+    __shared__ float2 parts[64][8];
     let_next_in();
     wait_for_previous();
-    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-    const int64_t row = (int64_t)blockIdx.x * 32 + tx;
+    const int tx = threadIdx.x & 7, ty = threadIdx.x >> 3;
+    const int64_t row = (int64_t)blockIdx.x * 8 + tx;
     float2 s = make_float2(-INFINITY, 0.f);
     if (row < L.rows) {
-        for (int64_t t = ty; t < L.tiles; t += 64) {
-            float2 p[4];
+        for (int64_t t = ty; t < L.tiles; t += 512) {
+            float2 p[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                p[i] = t + i * 16 < L.tiles ? L.part[(t + i * 16) * L.rows + row] : make_float2(-INFINITY, 0.f);
+            for (int i = 0; i < 8; ++i)
+                p[i] = t + i * 64 < L.tiles ? __ldcg(L.part + (t + i * 64) * L.rows + row) : make_float2(-INFINITY, 0.f);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s = join(s, p[i]);
+            for (int i = 0; i < 8; ++i) s = join(s, p[i]);
         }
     }
     parts[ty][tx] = s;
-    __syncthreads();
-    if (ty == 0 && row < L.rows) {
 #pragma unroll
-        for (int i = 1; i < 16; ++i) s = join(s, parts[i][tx]);
+    for (int n = 32; n; n /= 2) {
+        __syncthreads();
+        if (ty < n) parts[ty][tx] = s = join(s, parts[ty + n][tx]);
+    }
+    if (ty == 0 && row < L.rows) {
         float loss = 0.f, lse = 0.f;
         if (target_of(L, row) >= 0) {
             const float l = logf(s.y);
@@ -78,75 +81,116 @@ static __global__ void __launch_bounds__(512) loss_kernel(const LossRows L)
     }
 }
 
-// Before a backward pass, one threadblock: no row is known to be dirty, and for
-// f16 the scale that brings the largest factor of a row to below 2^14 (sums of
-// two below 2^15; f16 then holds what is 2^-38 of it to half a unit).
-static __global__ void __launch_bounds__(1024) loss_scale_kernel(const LossRows L)
-{
-    __shared__ float most[32];
-    let_next_in();
-    wait_for_previous();
-    float m = 0.f;
-    if (L.f16)
-        for (int64_t row = threadIdx.x; row < L.rows; row += 1024) {
-            if (target_of(L, row) < 0) continue;
-            const float b = L.dloss[row], a = L.dlse ? b + L.dlse[row] : b;
-            if (fabsf(a) < INFINITY) m = fmaxf(m, fabsf(a));
-            if (fabsf(b) < INFINITY) m = fmaxf(m, fabsf(b));
-        }
-#pragma unroll
-    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
-    if ((threadIdx.x & 31) == 0) most[threadIdx.x >> 5] = m;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int i = 1; i < 32; ++i) m = fmaxf(m, most[i]);
-        int e = 0;
-        if (m > 0.f) frexpf(m, &e);            // m < 2^e
-        const int shift = L.f16 && m > 0.f ? max(-100, min(100, 14 - e)) : 0;
-        L.scale[0] = ldexpf(1.f, shift);
-        L.scale[1] = ldexpf(1.f, -shift);
-        *L.dirty = 0;
-    }
-}
-
-// A row's coefficients for the products' epilogue, a warp a row, and whether a
-// row that counts for nothing holds Inf or NaN (0 times which would reach dw).
+// A row's coefficients for the products' epilogue, a warp a row, whether a row
+// that counts for nothing holds Inf or NaN (0 times which would reach dw), and the
+// largest factor of 8 rows.
 static __global__ void __launch_bounds__(256) loss_rows_kernel(const LossRows L)
 {
+    __shared__ float2 found[8];
     let_next_in();
     wait_for_previous();
-    const int lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (row >= L.rows) return;
-    const int64_t t = target_of(L, row);
-    const float b = t < 0 ? 0.f : L.dloss[row], a = t >= 0 && L.dlse ? b + L.dlse[row] : b;
-    if (lane == 0) {
-        const float s = L.scale[0];
-        L.coef[row] = make_float4(t < 0 ? 0.f : L.lse_in[row], a * s, b * s,
-                                  __int_as_float(t < 0 ? -1 : (int)t));
-    }
-    if (L.x && a == 0.f && b == 0.f) {
-        bool bad = false;
-        for (int64_t c = lane; c < L.k; c += 32) {
-            const float v = load1(L.x + row * L.ld_x + c, !L.f16);
-            bad |= !(fabsf(v) < INFINITY);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t row = (int64_t)blockIdx.x * 8 + warp;
+    float most = 0.f;
+    bool bad = false;
+    if (row < L.rows) {
+        const int64_t t = target_of(L, row);
+        const float b = t < 0 ? 0.f : L.dloss[row], a = t >= 0 && L.dlse ? b + L.dlse[row] : b;
+        if (lane == 0) L.coef[row] = make_float4(t < 0 ? 0.f : L.lse_in[row], a, b, __int_as_float(t < 0 ? -1 : (int)t));
+        if (fabsf(a) < INFINITY) most = fabsf(a);
+        if (fabsf(b) < INFINITY) most = fmaxf(most, fabsf(b));
+        if (L.x && a == 0.f && b == 0.f) {
+            // (x is in rows on 16 bytes here)
+            const uint16_t* x = L.x + row * L.ld_x;
+#pragma unroll 4
+            for (int64_t c = lane * 8; c < L.k; c += 256) {
+                float v[8];
+                load8(x + c, !L.f16, (int)min((int64_t)8, L.k - c), v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) bad |= !(fabsf(v[i]) < INFINITY);
+            }
         }
-        if (bad) *L.dirty = 1;
+    }
+    bad = __any_sync(~0u, bad);
+    if (lane == 0) found[warp] = make_float2(most, bad ? 1.f : 0.f);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        float2 all = found[0];
+        for (int i = 1; i < 8; ++i) all.x = fmaxf(all.x, found[i].x), all.y = fmaxf(all.y, found[i].y);
+        L.block[blockIdx.x] = all;
     }
 }
 
-// x without the rows that count for nothing, where one of them is dirty.
-static __global__ void __launch_bounds__(256) loss_clean_kernel(const LossRows L)
+// What the products are told of all rows: for f16 the scale that brings the
+// largest factor to below 2^14 (sums of two below 2^15; f16 then holds what is
+// 2^-38 of it to half a unit), and whether x is to be read without the rows that
+// count for nothing, which is written here where one of them is dirty.
+static __global__ void __launch_bounds__(256) loss_ready_kernel(const LossRows L)
 {
+    __shared__ float2 found[8];
     let_next_in();
     wait_for_previous();
-    if (!*L.dirty) return;
+    float2 all = make_float2(0.f, 0.f);
+    const int64_t blocks = (L.rows + 7) / 8;
+#pragma unroll 8
+    for (int64_t i = threadIdx.x; i < blocks; i += 256) {
+        const float2 b = L.block[i];
+        all.x = fmaxf(all.x, b.x);
+        all.y = fmaxf(all.y, b.y);
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) {
+        all.x = fmaxf(all.x, __shfl_xor_sync(~0u, all.x, d));
+        all.y = fmaxf(all.y, __shfl_xor_sync(~0u, all.y, d));
+    }
+    if ((threadIdx.x & 31) == 0) found[threadIdx.x >> 5] = all;
+    __syncthreads();
+    for (int i = 0; i < 8; ++i) all.x = fmaxf(all.x, found[i].x), all.y = fmaxf(all.y, found[i].y);
+    const bool dirty = all.y != 0.f;
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        int e = 0;
+        if (all.x > 0.f) frexpf(all.x, &e);    // the largest factor < 2^e
+        const int shift = L.f16 && all.x > 0.f ? max(-100, min(100, 14 - e)) : 0;
+        L.scale[0] = ldexpf(1.f, shift);
+        L.scale[1] = ldexpf(1.f, -shift);
+        *L.dirty = dirty;
+    }
+    if (!dirty) return;
     for (int64_t row = blockIdx.x; row < L.rows; row += gridDim.x) {
         const float4 k = L.coef[row];
         const bool dead = k.y == 0.f && k.z == 0.f;
         for (int64_t c = threadIdx.x; c < L.k; c += 256)
             L.clean[row * L.ld_clean + c] = dead ? (uint16_t)0 : L.x[row * L.ld_x + c];
     }
+}
+
+// dx from its parts, which the segments of the vocabulary left, added up in order.
+struct LossSum {
+    const float* sum;
+    uint16_t* dx;
+    int64_t rows, k, ld_sum, bs_sum, ld_dx;
+    int32_t parts, bf;
+};
+static __global__ void __launch_bounds__(256) loss_sum_kernel(const LossSum L)
+{
+    let_next_in();
+    wait_for_previous();
+    // (rows of the parts are on 16 bytes and padded)
+    const int64_t quads = (L.k + 3) / 4, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= L.rows * quads) return;
+    const int64_t row = i / quads, c = (i - row * quads) * 4;
+    const float4* p = reinterpret_cast<const float4*>(L.sum + row * L.ld_sum + c);
+    float4 v = __ldcg(p);
+#pragma unroll 4
+    for (int s = 1; s < L.parts; ++s) {
+        const float4 u = __ldcg(p + s * (L.bs_sum / 4));
+        v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+    }
+    uint16_t* o = L.dx + row * L.ld_dx + c;
+    const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (c + e < L.k) store1(o + e, f[e], L.bf);
 }
 
 }  // namespace tensor

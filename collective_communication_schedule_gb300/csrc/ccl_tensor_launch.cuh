@@ -188,7 +188,7 @@ inline Choices choose(const Product& P, int sms, int max_split = 8)
     if (alt) TRY(encode(dev, &P->mp, *alt, 64, P->a_mn ? kSliceK : kTileM));
     if (sh.split == 1) {
         const int64_t count = P->ragged == RAGGED_ROWS ? 1 : P->groups;
-        P->tma_out = P->out && vectors(P->out, P->ld_out, P->bs_out);
+        P->tma_out = P->out && !P->sum && vectors(P->out, P->ld_out, P->bs_out);
         if (P->tma_out)
             TRY(encode(dev, &P->mo, Matrix{P->out, P->n, P->m, P->ld_out, count, P->bs_out}, 32, kBlockRows,
                        CU_TENSOR_MAP_SWIZZLE_NONE));

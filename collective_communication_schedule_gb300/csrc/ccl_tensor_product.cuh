@@ -88,9 +88,11 @@ struct Scalars {
     const uint16_t *c, *bias;
     const float *alpha_of, *beta_of;   // device factors per batch entry (may be null)
     int64_t ld_out, bs_out, ld_pre, ld_c, bs_c, bs_bias;
-    float* sum;                    // SUM_PAIR: an output that grows over several launches, in 32 bits (may be null)
-    int64_t ld_sum;
-    int32_t sum_first, sum_last;   // nothing in it yet; the rounded result goes to out
+    float* sum;                    // SUM_PAIR: an output in parts that grow over several launches, in 32 bits (may be null)
+    int64_t ld_sum, bs_sum;
+    int32_t sum_first;             // nothing in it yet
+    int32_t segment;               // SUM_PAIR: > 0: group g reduces over [g segment, (g + 1) segment) of the operands' one
+                                   // reduction axis (a multiple of a slice) into the g-th part
     const int32_t* alt;            // device word: not 0 if A is to be read through mp (may be null)
 };
 
@@ -108,17 +110,21 @@ struct Pair {
     Product p[2];
 };
 
-// A product x w^T whose lanes are rows of x, for what is done with a row of
-// its values where they are made, in 32 bits (the values themselves are stored
-// nowhere): STATS its sum of exponentials, SLOPE the derivative of a loss.
+// A product x w^T for what is done with a row of its values where they are
+// made, in 32 bits (the values themselves are stored nowhere): STATS its sum of
+// exponentials, SLOPE the derivative of a loss.  Lanes are rows of x, so that a
+// thread has a row's values to itself; for few rows, which would leave lanes
+// idle, they are rows of w (the _TURNED forms) and a row's values lie across a warp.
 struct Rowwise {
-    Product p;                     // A: rows of x, B: rows of w
+    Product p;                     // A: rows of x, B: rows of w (turned: the other way round)
     const void* target;            // STATS: rows' targets, whose values go to `picked`
     int32_t wide;                  // targets of 64 bits
     float* picked;
     float2* part;                  // STATS: a row's largest value and sum of exp(value - largest), by row tile of B
+                                   // (turned: by 32 rows of A)
     const float4* coef;            // SLOPE: log-sum, a, b, target
-    int32_t first;                 // SLOPE: the number of the first row of B
+    const float* scale;            // SLOPE: of a and b
+    int32_t first;                 // SLOPE: the number of the first row of w
 };
 
 struct TileAt {
@@ -233,6 +239,11 @@ __device__ __forceinline__ TileAt tile_at(const Scalars& P, const Shared* sh, in
             q.n0 = x * P.bn;
         }
         q.za = q.zb = q.g;
+        if (P.segment) {
+            q.k0 = q.g * P.segment;
+            q.klen = min(P.segment, P.k - q.k0);
+            q.za = q.zb = 0;
+        }
         if (P.ragged == RAGGED_REDUCE) {
             group_range(P, q.g, P.k, q.k0, q.klen);
             q.za = q.zb = 0;
@@ -300,9 +311,9 @@ __device__ __forceinline__ void fetch_c(const Scalars& P, uint16_t c[kBlockRows]
 }
 
 // The same of an output's sum so far, 128 neighbouring bytes a row and warp.
-__device__ __forceinline__ void fetch_sum(const Scalars& P, float* v, int64_t row, int nrows, int f)
+__device__ __forceinline__ void fetch_sum(const Scalars& P, float* v, int g, int64_t row, int nrows, int f)
 {
-    const float* p = P.sum + row * P.ld_sum + f;
+    const float* p = P.sum + g * P.bs_sum + row * P.ld_sum + f;
 #pragma unroll
     for (int i = 0; i < kBlockRows; ++i, p += P.ld_sum) v[i] = f < P.m && i < nrows ? __ldcg(p) : 0.f;
 }
@@ -436,9 +447,9 @@ enum { BOTH_K = 0, A_MN = 1, BOTH_MN = 2 };
 
 // MODE: one product, the two of a Pair, those with an output that grows over
 // several launches, or a Rowwise one
-enum { SINGLE = 0, PAIR = 1, SUM_PAIR = 2, STATS = 3, SLOPE = 4 };
+enum { SINGLE = 0, PAIR = 1, SUM_PAIR = 2, STATS = 3, SLOPE = 4, STATS_TURNED = 5, SLOPE_TURNED = 6 };
 __host__ __device__ constexpr bool is_pair(int mode) { return mode == PAIR || mode == SUM_PAIR; }
-__host__ __device__ constexpr bool is_rowwise(int mode) { return mode == STATS || mode == SLOPE; }
+__host__ __device__ constexpr bool is_rowwise(int mode) { return mode >= STATS; }
 
 template <int MODE>
 struct Sequence {
@@ -473,6 +484,10 @@ template <>
 struct Sequence<STATS> : RowwiseSequence {};
 template <>
 struct Sequence<SLOPE> : RowwiseSequence {};
+template <>
+struct Sequence<STATS_TURNED> : RowwiseSequence {};
+template <>
+struct Sequence<SLOPE_TURNED> : RowwiseSequence {};
 
 __device__ __forceinline__ float exp2_fast(float x)      // within 2^-22
 {
@@ -528,14 +543,20 @@ __device__ __forceinline__ float2 stats_blocks(uint32_t from, int first, int liv
 }
 
 // The same walk for dl = a exp(value - log-sum) - b [column = target], rounded
-// to 16 bits: 32 neighbouring bytes of a row a lane.  A row that counts for
-// nothing (a = b = 0) gives 0 whatever its values are.
+// to 16 bits.  A row that counts for nothing (a = b = 0) gives 0 whatever its
+// values are.  All blocks of the tile (at most 4 of a warp) are held before any
+// is stored: the accumulator is handed back in between, and that would wait for
+// the stores.
+constexpr int kMostBlocks = 256 / (kEpilogueWarps / 4 * kBlockRows);
 template <bool BF>
-__device__ __forceinline__ void slope_blocks(uint32_t from, int first, int live, int stride, float4 k, int at, uint16_t* out)
+__device__ __forceinline__ void slope_blocks(uint32_t from, int first, int live, float4 k, int at,
+                                             uint32_t (&w)[kMostBlocks][kBlockRows / 2])
 {
     const bool dead = k.y == 0.f && k.z == 0.f;
-#pragma unroll 1
-    for (int c = first; c < live; c += stride) {
+#pragma unroll
+    for (int j = 0; j < kMostBlocks; ++j) {
+        const int c = first + j * (kEpilogueWarps / 4 * kBlockRows);
+        if (c >= live) break;
         uint32_t u[kBlockRows];
         float v[kBlockRows];
         tmem_load16(from + c, u);
@@ -549,13 +570,67 @@ __device__ __forceinline__ void slope_blocks(uint32_t from, int first, int live,
 #pragma unroll
             for (int i = 0; i < kBlockRows; ++i) v[i] = 0.f;
         }
-        if (out) {
-            uint4* p = reinterpret_cast<uint4*>(out + c);
-            p[0] = make_uint4(pack2<BF>(v[0], v[1]), pack2<BF>(v[2], v[3]), pack2<BF>(v[4], v[5]), pack2<BF>(v[6], v[7]));
-            p[1] = make_uint4(pack2<BF>(v[8], v[9]), pack2<BF>(v[10], v[11]), pack2<BF>(v[12], v[13]), pack2<BF>(v[14], v[15]));
-        }
+#pragma unroll
+        for (int i = 0; i < kBlockRows / 2; ++i) w[j][i] = pack2<BF>(v[2 * i], v[2 * i + 1]);
         __syncwarp();
     }
+}
+// 32 neighbouring bytes of a row a lane and block
+__device__ __forceinline__ void store_slopes(uint16_t* out, int first, int live, const uint32_t (&w)[kMostBlocks][kBlockRows / 2])
+{
+#pragma unroll
+    for (int j = 0; j < kMostBlocks; ++j) {
+        const int c = first + j * (kEpilogueWarps / 4 * kBlockRows);
+        if (c < live)
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out + c), "r"(w[j][0]), "r"(w[j][1]),
+                         "r"(w[j][2]), "r"(w[j][3]), "r"(w[j][4]), "r"(w[j][5]), "r"(w[j][6]), "r"(w[j][7])
+                         : "memory");
+    }
+}
+
+// One step of a sum over the warp: 2 N values a lane become N, one half of the lanes (by lane bit 2 N) keeping each half.
+template <int N>
+__device__ __forceinline__ void half_sums(float (&v)[kBlockRows], int lane)
+{
+    const bool up = lane & (2 * N);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float send = up ? v[i] : v[i + N], keep = up ? v[i + N] : v[i];
+        v[i] = keep + __shfl_xor_sync(~0u, send, 2 * N);
+    }
+}
+
+// Turned: 16 rows of x x 32 rows of w, a row of w a lane.  A row's largest value
+// and its sum of exponentials over the warp; lane i gets those of row i.  at: the
+// targets less the lane's row of w, a row a lane.
+__device__ __forceinline__ float2 turned_stats(const uint32_t (&u)[kBlockRows], bool own, int64_t target, int64_t mine, float* picked,
+                                               int rows, int lane)
+{
+    float2 s = make_float2(-INFINITY, 0.f);
+    float v[kBlockRows], m[kBlockRows];
+#pragma unroll
+    for (int i = 0; i < kBlockRows; ++i) {
+        v[i] = own ? __uint_as_float(u[i]) : -INFINITY;
+        asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m[i]) : "f"(v[i]));
+    }
+#pragma unroll
+    for (int i = 0; i < kBlockRows; ++i) {
+        if (__shfl_sync(~0u, target, i) == mine && own && i < rows) picked[i] = v[i];
+        const float z = m[i] == -INFINITY ? 0.f : m[i];
+        v[i] = exp2_fast((v[i] - z) * kLog2e);
+    }
+    // 16 sums over the warp: halves of the lanes keep halves of the rows
+    half_sums<8>(v, lane);
+    half_sums<4>(v, lane);
+    half_sums<2>(v, lane);
+    half_sums<1>(v, lane);
+    v[0] += __shfl_xor_sync(~0u, v[0], 1);
+    // lane l has the sum of row l / 2
+    s.y = __shfl_sync(~0u, v[0], (lane & 15) * 2);
+#pragma unroll
+    for (int i = 0; i < kBlockRows; ++i)
+        if ((lane & 15) == i) s.x = m[i];
+    return s;
 }
 
 // A threadblock's share of the tiles of a sequence of products.
@@ -708,8 +783,9 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
                             for (int i = 0; i < bn / CG; i += 64)
                                 load(b + i * (kSliceK * 2), &maps.mb, n0 + i, q.k0 + k, q.zb);
                         } else {
-                            load(b, &maps.mb, k, q.row0 + n0, q.zb);
-                            load(b + part_b, &maps.mb, k + 64, q.row0 + n0, q.zb);
+                            const int kb = MODE == SUM_PAIR ? q.k0 + k : k;
+                            load(b, &maps.mb, kb, q.row0 + n0, q.zb);
+                            load(b + part_b, &maps.mb, kb + 64, q.row0 + n0, q.zb);
                         }
                     }
                     if (clear && good) flips ^= 1u << s, used |= 1u << s;
@@ -859,7 +935,7 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
                 const int acc = done & 1;
                 const int feat = q.m0 + (CG == 2 ? rank * kTileM : 0) + quad * 32, nfeat = P.m - feat, f = feat + lane;
                 const int64_t row = (int64_t)q.row0 + q.n0;
-                if constexpr (is_rowwise(MODE)) {
+                if constexpr (MODE == STATS || MODE == SLOPE) {
                     // lanes are rows of x, columns the rows of w
                     const Rowwise& R = *seq.rows;
                     const bool own = f < P.m;
@@ -871,21 +947,21 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
                     }
                     if (own && MODE == SLOPE) {
                         coef = R.coef[f];
+                        coef.y *= *R.scale;
+                        coef.z *= *R.scale;
                         at = __float_as_int(coef.w) - R.first - q.n0;
                     }
                     if (!__all_sync(~0u, bar_wait(smem_addr(&sh.acc_full[acc]), (done >> 1) & 1, failed))) break;
                     fence_after();
                     const uint32_t from = tmem + ((uint32_t)(quad * 32) << 16) + acc * width;
                     float2 part;
-                    if (MODE == STATS) {
+                    uint32_t w[kMostBlocks][kBlockRows / 2];
+                    if (MODE == STATS)
                         part = stats_blocks(from, slot * kBlockRows, q.live, kStride, at, R.picked + f);
-                    } else {
-                        uint16_t* out = own ? P.out + f * P.ld_out + q.n0 : nullptr;
-                        if (P.out_bf)
-                            slope_blocks<true>(from, slot * kBlockRows, q.live, kStride, coef, at, out);
-                        else
-                            slope_blocks<false>(from, slot * kBlockRows, q.live, kStride, coef, at, out);
-                    }
+                    else if (P.out_bf)
+                        slope_blocks<true>(from, slot * kBlockRows, q.live, coef, at, w);
+                    else
+                        slope_blocks<false>(from, slot * kBlockRows, q.live, coef, at, w);
                     fence_before();
                     if (lane == 0) {
                         if (CG == 2)
@@ -904,11 +980,64 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
                             for (int i = 1; i < 4; ++i) part = join(part, parts[i * kTileM]);
                             if (own) R.part[(int64_t)(q.n0 / P.bn) * P.m + f] = part;
                         }
+                    } else if (own) {
+                        store_slopes(P.out + f * P.ld_out + q.n0, slot * kBlockRows, q.live, w);
                     }
                     ++done;
                     continue;
                 }
-                const float alpha = P.alpha * ((kAll || MODE == SUM_PAIR) && P.alpha_of ? P.alpha_of[q.g] : 1.f);
+                if constexpr (MODE == STATS_TURNED || MODE == SLOPE_TURNED) {
+                    // lanes are rows of w, columns the rows of x
+                    const Rowwise& R = *seq.rows;
+                    const bool own = f < P.m;
+                    const float scale = MODE == SLOPE_TURNED ? *R.scale : 0.f;
+                    if (!__all_sync(~0u, bar_wait(smem_addr(&sh.acc_full[acc]), (done >> 1) & 1, failed))) break;
+                    fence_after();
+                    const uint32_t from = tmem + ((uint32_t)(quad * 32) << 16) + acc * width;
+                    for (int c = slot * kBlockRows; c < q.live; c += kStride) {
+                        uint32_t u[kBlockRows];
+                        const int n = q.n0 + c, nrows = q.live - c;
+                        // what a row has of its own, a row a lane
+                        int64_t target = -1;
+                        float4 coef = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (lane < kBlockRows && lane < nrows) {
+                            if (MODE == STATS_TURNED)
+                                target = R.wide ? ((const int64_t*)R.target)[n + lane] : ((const int32_t*)R.target)[n + lane];
+                            else
+                                coef = R.coef[n + lane];
+                        }
+                        tmem_load16(from + c, u);
+                        if (MODE == STATS_TURNED) {
+                            const float2 part = turned_stats(u, own, target, f, R.picked + n, nrows, lane);
+                            if (feat < P.m && lane < kBlockRows && lane < nrows) R.part[(int64_t)(feat / 32) * P.n + n + lane] = part;
+                        } else {
+                            float v[kBlockRows];
+                            uint32_t w[kBlockRows / 2];
+#pragma unroll
+                            for (int i = 0; i < kBlockRows; ++i) {
+                                const float lse = __shfl_sync(~0u, coef.x, i), a = __shfl_sync(~0u, coef.y, i) * scale;
+                                const float b = __shfl_sync(~0u, coef.z, i) * scale;
+                                const int t = __float_as_int(__shfl_sync(~0u, coef.w, i)) - R.first;
+                                const float p = a * exp2_fast((__uint_as_float(u[i]) - lse) * kLog2e);
+                                v[i] = a == 0.f && b == 0.f ? 0.f : p - (t == f ? b : 0.f);
+                            }
+                            pack_block(v, w, P.out_bf);
+                            store_block(&maps.mo, P.out + (int64_t)n * P.ld_out + f, P.ld_out, w, st, P.tma_out, lane, feat, n, 0,
+                                        nrows, nfeat);
+                        }
+                        __syncwarp();
+                    }
+                    fence_before();
+                    if (lane == 0) {
+                        if (CG == 2)
+                            bar_arrive_cluster(release[acc]);
+                        else
+                            bar_arrive(release[acc]);
+                    }
+                    ++done;
+                    continue;
+                }
+                const float alpha = P.alpha * ((kAll || MODE == SUM_PAIR) && P.alpha_of ? P.alpha_of[P.segment ? 0 : q.g] : 1.f);
                 const float beta = P.beta * (P.beta_of ? P.beta_of[q.g] : 1.f);
                 const float bias = kAll && P.bias && f < P.m ? load1(P.bias + q.g * P.bs_bias + f, P.in_bf) : 0.f;
                 const bool whole = P.ragged != RAGGED_ROWS;
@@ -923,7 +1052,7 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
                 // so far, of an output that grows over several launches: read a block ahead too
                 const bool grown = MODE == SUM_PAIR && P.sum && !P.sum_first;
                 float so_far[MODE == SUM_PAIR ? kBlockRows : 1];
-                if (grown) fetch_sum(P, so_far, row + c, q.live - c, f);
+                if (grown) fetch_sum(P, so_far, q.g, row + c, q.live - c, f);
                 if (some) {
                     if (!__all_sync(~0u, bar_wait(smem_addr(&sh.acc_full[acc]), (done >> 1) & 1, failed))) break;
                     fence_after();
@@ -987,15 +1116,13 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
                         if (grown) {
 #pragma unroll
                             for (int i = 0; i < kBlockRows; ++i) v[i] += so_far[MODE == SUM_PAIR ? i : 0];
-                            if (c + kStride < q.live) fetch_sum(P, so_far, row + c + kStride, nrows - kStride, f);
+                            if (c + kStride < q.live) fetch_sum(P, so_far, q.g, row + c + kStride, nrows - kStride, f);
                         }
-                        if (!P.sum_last) {
-                            float* p = P.sum + (row + c) * P.ld_sum + f;
+                        float* p = P.sum + q.g * P.bs_sum + (row + c) * P.ld_sum + f;
 #pragma unroll
-                            for (int i = 0; i < kBlockRows; ++i, p += P.ld_sum)
-                                if (f < P.m && i < nrows) *p = v[i];
-                            continue;
-                        }
+                        for (int i = 0; i < kBlockRows; ++i, p += P.ld_sum)
+                            if (f < P.m && i < nrows) *p = v[i];
+                        continue;
                     }
                     if (kAll && P.pre) {
                         pack_block(v, w, P.in_bf);
@@ -1111,11 +1238,13 @@ __global__ void __launch_bounds__(kThreads, 1) pair_kernel(const __grid_constant
 {
     products<CG, A_MN, PAIR>({{&P}});
 }
+// (a template all the same: one definition in every translation unit that asks for it)
 template <int CG>
-__global__ void __launch_bounds__(kThreads, 1) sum_pair_kernel(const __grid_constant__ Pair P)
+__global__ void __launch_bounds__(kThreads, 1) sum_pairs(const __grid_constant__ Pair P)
 {
     products<CG, A_MN, SUM_PAIR>({{&P}});
 }
+constexpr auto sum_pair_kernel = sum_pairs<2>;
 template <int CG, int MODE>
 __global__ void __launch_bounds__(kThreads, 1) rowwise_kernel(const __grid_constant__ Rowwise R)
 {
