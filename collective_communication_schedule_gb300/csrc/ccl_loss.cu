@@ -39,42 +39,57 @@ static ccl_status_t loss_device(const Device** out)
 // sums depend on the sizes alone.
 constexpr int kShapeSms = 152;
 
-// Up to this many rows, rows of w lie along the lanes: 128 rows of x or less would
-// leave lanes idle and cost the matrix instructions the same.
-constexpr int kTurnedRows = 128;
+// Up to this many rows, rows of w lie along the lanes.  Forward, 32003 x 2048
+// weights, us turned and not: 1 row 25.3 and 41.5 (all tiles read the one row of x),
+// 8 rows 25.6 and 39.9, 32 rows 27.2 and 28.0, 64 rows 31.0 and 28.1.  The whole
+// backward pass: 1 row 101 and 116, 64 rows 101 and 104, 128 rows 107 and 108.
+static bool turns(int mode, int64_t rows) { return rows <= (mode == STATS ? 32 : 128); }
 
 // The product x w^T, in either orientation, and its shape.
-static Product values_of(int64_t rows, int64_t vocab, int64_t k, bool bf, Shape* sh)
+static Product values_of(int mode, int64_t rows, int64_t vocab, int64_t k, bool bf, Shape* sh)
 {
     Product P = {};
-    const bool turned = rows <= kTurnedRows;
+    const bool turned = turns(mode, rows);
     P.m = (int32_t)(turned ? vocab : rows);
     P.n = (int32_t)(turned ? rows : vocab);
     P.k = (int32_t)k;
     P.groups = 1;
     P.alpha = 1.f;
     P.in_bf = P.out_bf = bf;
-    *sh = choose(P, kShapeSms, 1).best;
+    if (turned) {                  // all rows of x in one tile
+        *sh = {1, 32, 1, 0.};
+        while (sh->bn < rows) sh->bn *= 2;
+    } else if (rows <= kTileM) {
+        // one tile of rows: single threadblocks, all SMs busy (128 x 32003 x 2048 28.3 us, 30.6 in pairs)
+        *sh = {1, 128, 1, 0.};
+        while (sh->bn > 32 && (vocab + sh->bn - 1) / sh->bn < kShapeSms) sh->bn /= 2;
+    } else {
+        *sh = choose(P, kShapeSms, 1).best;
+    }
     return P;
 }
-// parts of a row's statistics
-static int64_t parts_of(int64_t rows, int64_t vocab, const Shape& sh)
+// Parts of a row's statistics: by tile, or by cluster (turned: by threadblock)
+// where one tile holds all rows.
+static int64_t parts_of(const Product& P, const Shape& sh, bool turned, int sms, bool* whole)
 {
-    return rows <= kTurnedRows ? (vocab + 31) / 32 : (vocab + sh.bn - 1) / sh.bn;
+    const int64_t across = (P.m + sh.cg * kTileM - 1) / (sh.cg * kTileM), along = (P.n + sh.bn - 1) / sh.bn;
+    *whole = turned || across == 1;
+    if (!*whole) return along;
+    return std::min<int64_t>(across * along, sms / sh.cg) * (turned ? sh.cg : 1);
 }
 
 // mode: STATS or SLOPE
 static ccl_status_t run_rowwise(const Device* dev, int mode, Rowwise* R, const Shape& sh, const Matrix& x, const Matrix& w,
                                 uint16_t* out, int64_t ld_out, cudaStream_t stream)
 {
-    const bool turned = x.rows <= kTurnedRows;
+    const bool turned = turns(mode, x.rows);
     if (turned) set_out(&R->p, out, ld_out, 0, R->p.out_bf);
     TRY(complete(dev, &R->p, sh, turned ? w : x, turned ? x : w));
     R->p.out = out;
     R->p.ld_out = ld_out;
     const int bytes = (kTileM + sh.bn / sh.cg) * kSliceK * 2, fixed = 1024 + kStagingBytes;
     R->p.stages = std::min(kMaxStages, (kSmemBudget - fixed) / bytes);
-    const int clusters = std::min(R->p.total, dev->sms / sh.cg);
+    const int clusters = std::min(R->p.total, std::min(dev->sms, kShapeSms) / sh.cg);
     void (*const kernels[2][2][2])(Rowwise) = {
         {{rowwise_kernel<1, STATS>, rowwise_kernel<2, STATS>}, {rowwise_kernel<1, STATS_TURNED>, rowwise_kernel<2, STATS_TURNED>}},
         {{rowwise_kernel<1, SLOPE>, rowwise_kernel<2, SLOPE>}, {rowwise_kernel<1, SLOPE_TURNED>, rowwise_kernel<2, SLOPE_TURNED>}}};
@@ -114,9 +129,10 @@ static ccl_status_t cross_entropy(const ccl_cross_entropy_t* a, char* base, int6
     Rowwise R = {};
     LossRows L = {};
     Shape sh = {};
+    bool whole = false;
     if (a->rows > 0) {
-        R.p = values_of(a->rows, a->vocab, a->k, a->dtype == CCL_BF16, &sh);
-        L.tiles = parts_of(a->rows, a->vocab, sh);
+        R.p = values_of(STATS, a->rows, a->vocab, a->k, a->dtype == CCL_BF16, &sh);
+        L.tiles = parts_of(R.p, sh, turns(STATS, a->rows), kShapeSms, &whole);
         R.part = ws.take<float2>(L.tiles * a->rows * sizeof(float2));
         R.picked = ws.take<float>(a->rows * 4);
     }
@@ -136,6 +152,8 @@ static ccl_status_t cross_entropy(const ccl_cross_entropy_t* a, char* base, int6
     TRY(loss_device(&dev));
     TRY(loadable(&w, &ws, stream));
     TRY(loadable(&x, &ws, stream));
+    R.whole = whole;
+    L.tiles = parts_of(R.p, sh, turns(STATS, a->rows), std::min(dev->sms, kShapeSms), &whole);
     R.target = L.target = a->target;
     R.wide = L.wide = a->target_bits == 64;
     TRY(run_rowwise(dev, STATS, &R, sh, x, w, nullptr, 0, stream));
@@ -146,7 +164,7 @@ static ccl_status_t cross_entropy(const ccl_cross_entropy_t* a, char* base, int6
     L.picked = R.picked;
     L.loss = a->loss;
     L.lse = a->lse;
-    return launch(loss_kernel, dim3((unsigned)((a->rows + 7) / 8)), 512, 0, stream, L);
+    return launch(loss_kernel, dim3((unsigned)((a->rows + 7) / 8)), 256, 0, stream, L);
 }
 
 // Rows of w whose derivatives are held at a time: what keeps them within 256 MB.
@@ -270,7 +288,7 @@ static ccl_status_t cross_entropy_grad(const ccl_cross_entropy_grad_t* a, char* 
         wp.rows = width;
         Rowwise R = {};
         Shape shape;
-        R.p = values_of(a->rows, width, a->k, bf, &shape);
+        R.p = values_of(SLOPE, a->rows, width, a->k, bf, &shape);
         R.coef = L.coef;
         R.scale = L.scale;
         R.first = (int32_t)first;

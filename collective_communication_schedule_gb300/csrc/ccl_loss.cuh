@@ -41,43 +41,42 @@ __device__ __forceinline__ int64_t target_of(const LossRows& L, int64_t row)
     return t;
 }
 
-// The parts of a row's tiles put together, in an order that the sizes fix:
+// A row's parts put together, in an order that the sizes fix:
 // lse = m + log(sum), loss = log(sum) + (m - the target's value), which keeps
-// the digits of a small loss.  8 rows a threadblock; 64 groups of threads take
-// the tiles in turn.
-static __global__ void __launch_bounds__(512) loss_kernel(const LossRows L)
+// the digits of a small loss.  8 rows a threadblock; 32 groups of threads take
+// the parts in turn, a warp a row puts the groups' together.
+static __global__ void __launch_bounds__(256) loss_kernel(const LossRows L)
 {
-    __shared__ float2 parts[64][8];
+    __shared__ float2 parts[32][9];
     let_next_in();
     wait_for_previous();
-    const int tx = threadIdx.x & 7, ty = threadIdx.x >> 3;
-    const int64_t row = (int64_t)blockIdx.x * 8 + tx;
+    const int tx = threadIdx.x & 7, ty = threadIdx.x >> 3, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t row = (int64_t)blockIdx.x * 8 + tx, mine = (int64_t)blockIdx.x * 8 + warp;
+    const bool live = lane == 0 && mine < L.rows && target_of(L, mine) >= 0;
+    const float picked = live ? L.picked[mine] : 0.f;
     float2 s = make_float2(-INFINITY, 0.f);
     if (row < L.rows) {
-        for (int64_t t = ty; t < L.tiles; t += 512) {
+        for (int64_t t = ty; t < L.tiles; t += 256) {
             float2 p[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                p[i] = t + i * 64 < L.tiles ? __ldcg(L.part + (t + i * 64) * L.rows + row) : make_float2(-INFINITY, 0.f);
+                p[i] = t + i * 32 < L.tiles ? __ldcg(L.part + (t + i * 32) * L.rows + row) : make_float2(-INFINITY, 0.f);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s = join(s, p[i]);
+            for (int n = 4; n; n /= 2)
+#pragma unroll
+                for (int i = 0; i < n; ++i) p[i] = join(p[i], p[i + n]);
+            s = join(s, p[0]);
         }
     }
     parts[ty][tx] = s;
+    __syncthreads();
+    s = parts[lane][warp];
 #pragma unroll
-    for (int n = 32; n; n /= 2) {
-        __syncthreads();
-        if (ty < n) parts[ty][tx] = s = join(s, parts[ty + n][tx]);
-    }
-    if (ty == 0 && row < L.rows) {
-        float loss = 0.f, lse = 0.f;
-        if (target_of(L, row) >= 0) {
-            const float l = logf(s.y);
-            loss = l + (s.x - L.picked[row]);
-            lse = s.x + l;
-        }
-        L.loss[row] = loss;
-        if (L.lse) L.lse[row] = lse;
+    for (int d = 16; d; d /= 2) s = join(s, make_float2(__shfl_xor_sync(~0u, s.x, d), __shfl_xor_sync(~0u, s.y, d)));
+    if (lane == 0 && mine < L.rows) {
+        const float l = logf(s.y);
+        L.loss[mine] = live ? l + (s.x - picked) : 0.f;
+        if (L.lse) L.lse[mine] = live ? s.x + l : 0.f;
     }
 }
 

@@ -121,7 +121,7 @@ struct Rowwise {
     int32_t wide;                  // targets of 64 bits
     float* picked;
     float2* part;                  // STATS: a row's largest value and sum of exp(value - largest), by row tile of B
-                                   // (turned: by 32 rows of A)
+    int32_t whole;                 // STATS: all rows of x lie in one tile: parts are by cluster, over all of its tiles
     const float4* coef;            // SLOPE: log-sum, a, b, target
     const float* scale;            // SLOPE: of a and b
     int32_t first;                 // SLOPE: the number of the first row of w
@@ -505,11 +505,10 @@ __device__ __forceinline__ float2 join(float2 a, float2 b)
 }
 
 // A warp's 32 rows of a tile, 16 columns at a time and every fourth 16 of them:
-// largest value and sum of exponentials so far, and the target's value.  at:
-// the target's column in the tile.
-__device__ __forceinline__ float2 stats_blocks(uint32_t from, int first, int live, int stride, int at, float* picked)
+// largest value and sum of exponentials added to those so far, and the target's
+// value.  at: the target's column in the tile.
+__device__ __forceinline__ float2 stats_blocks(float2 s, uint32_t from, int first, int live, int stride, int at, float* picked)
 {
-    float2 s = make_float2(-INFINITY, 0.f);
 #pragma unroll 1
     for (int c = first; c < live; c += stride) {
         uint32_t u[kBlockRows];
@@ -919,6 +918,9 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
         for (int i = 0; i < 2; ++i)
             release[i] = CG == 2 ? cluster_addr(smem_addr(&sh.acc_empty[i]), 0) : smem_addr(&sh.acc_empty[i]);
         int done = 0, round = 0;
+        // STATS with all rows in one tile: of this thread's row so far (turned: of row `lane` of two blocks)
+        bool good = true;
+        float2 so_far2[2] = {make_float2(-INFINITY, 0.f), make_float2(-INFINITY, 0.f)};
         for (int ph = 0; ph < phases; ++ph) {
             const Product& maps = seq.at(ph);
             const Scalars P = maps;
@@ -951,25 +953,30 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
                         coef.z *= *R.scale;
                         at = __float_as_int(coef.w) - R.first - q.n0;
                     }
-                    if (!__all_sync(~0u, bar_wait(smem_addr(&sh.acc_full[acc]), (done >> 1) & 1, failed))) break;
-                    fence_after();
-                    const uint32_t from = tmem + ((uint32_t)(quad * 32) << 16) + acc * width;
-                    float2 part;
+                    // (the warps of a quadrant meet below: a wait that fails does not change the way there)
+                    if (good) good = __all_sync(~0u, bar_wait(smem_addr(&sh.acc_full[acc]), (done >> 1) & 1, failed));
+                    float2 part = R.whole ? so_far2[0] : make_float2(-INFINITY, 0.f);
                     uint32_t w[kMostBlocks][kBlockRows / 2];
-                    if (MODE == STATS)
-                        part = stats_blocks(from, slot * kBlockRows, q.live, kStride, at, R.picked + f);
-                    else if (P.out_bf)
-                        slope_blocks<true>(from, slot * kBlockRows, q.live, coef, at, w);
-                    else
-                        slope_blocks<false>(from, slot * kBlockRows, q.live, coef, at, w);
-                    fence_before();
-                    if (lane == 0) {
-                        if (CG == 2)
-                            bar_arrive_cluster(release[acc]);
+                    if (good) {
+                        fence_after();
+                        const uint32_t from = tmem + ((uint32_t)(quad * 32) << 16) + acc * width;
+                        if (MODE == STATS)
+                            part = stats_blocks(part, from, slot * kBlockRows, q.live, kStride, at, R.picked + f);
+                        else if (P.out_bf)
+                            slope_blocks<true>(from, slot * kBlockRows, q.live, coef, at, w);
                         else
-                            bar_arrive(release[acc]);
+                            slope_blocks<false>(from, slot * kBlockRows, q.live, coef, at, w);
+                        fence_before();
+                        if (lane == 0) {
+                            if (CG == 2)
+                                bar_arrive_cluster(release[acc]);
+                            else
+                                bar_arrive(release[acc]);
+                        }
                     }
-                    if (MODE == STATS) {
+                    if (MODE == STATS && R.whole && t + clusters < run.end) {
+                        so_far2[0] = part;
+                    } else if (MODE == STATS) {
                         // the four warps of these rows put their parts together (in turn in two places: the next
                         // tile's parts do not meet this one's)
                         float2* parts = reinterpret_cast<float2*>(staging) + acc * (4 * kTileM) + quad * 32 + lane;
@@ -978,9 +985,9 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
                         if (slot == 0) {
 #pragma unroll
                             for (int i = 1; i < 4; ++i) part = join(part, parts[i * kTileM]);
-                            if (own) R.part[(int64_t)(q.n0 / P.bn) * P.m + f] = part;
+                            if (own) R.part[(int64_t)(R.whole ? cluster : q.n0 / P.bn) * P.m + f] = part;
                         }
-                    } else if (own) {
+                    } else if (own && good) {
                         store_slopes(P.out + f * P.ld_out + q.n0, slot * kBlockRows, q.live, w);
                     }
                     ++done;
@@ -991,10 +998,13 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
                     const Rowwise& R = *seq.rows;
                     const bool own = f < P.m;
                     const float scale = MODE == SLOPE_TURNED ? *R.scale : 0.f;
-                    if (!__all_sync(~0u, bar_wait(smem_addr(&sh.acc_full[acc]), (done >> 1) & 1, failed))) break;
+                    if (good) good = __all_sync(~0u, bar_wait(smem_addr(&sh.acc_full[acc]), (done >> 1) & 1, failed));
                     fence_after();
                     const uint32_t from = tmem + ((uint32_t)(quad * 32) << 16) + acc * width;
-                    for (int c = slot * kBlockRows; c < q.live; c += kStride) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {          // (at most 128 rows)
+                        const int c = slot * kBlockRows + j * kStride;
+                        if (!good || c >= q.live) break;
                         uint32_t u[kBlockRows];
                         const int n = q.n0 + c, nrows = q.live - c;
                         // what a row has of its own, a row a lane
@@ -1008,8 +1018,7 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
                         }
                         tmem_load16(from + c, u);
                         if (MODE == STATS_TURNED) {
-                            const float2 part = turned_stats(u, own, target, f, R.picked + n, nrows, lane);
-                            if (feat < P.m && lane < kBlockRows && lane < nrows) R.part[(int64_t)(feat / 32) * P.n + n + lane] = part;
+                            so_far2[j] = join(so_far2[j], turned_stats(u, own, target, f, R.picked + n, nrows, lane));
                         } else {
                             float v[kBlockRows];
                             uint32_t w[kBlockRows / 2];
@@ -1028,11 +1037,30 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
                         __syncwarp();
                     }
                     fence_before();
-                    if (lane == 0) {
+                    if (lane == 0 && good) {
                         if (CG == 2)
                             bar_arrive_cluster(release[acc]);
                         else
                             bar_arrive(release[acc]);
+                    }
+                    if (MODE == STATS_TURNED && t + clusters >= run.end) {
+                        // after the last tile, the warps of the same rows put their parts together, and so do the two
+                        // threadblocks of a pair by writing a part each
+                        float2* parts = reinterpret_cast<float2*>(staging) + slot * kBlockRows + (lane & 15);
+                        if (lane < kBlockRows) {
+                            parts[quad * kTileM] = so_far2[0];
+                            parts[quad * kTileM + kStride] = so_far2[1];
+                        }
+                        named_sync(3 + slot, 128);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const int c = slot * kBlockRows + j * kStride + (lane & 15);
+                            if (quad > 0 || lane >= kBlockRows || c >= q.live) continue;
+                            float2 part = so_far2[j];
+#pragma unroll
+                            for (int i = 1; i < 4; ++i) part = join(part, parts[i * kTileM + j * kStride]);
+                            R.part[(int64_t)(cluster * size + rank) * P.n + c] = part;
+                        }
                     }
                     ++done;
                     continue;
