@@ -119,7 +119,7 @@ struct Choices {
     Shape single, pairs;           // beside another product in one launch: of single threadblocks, of pairs
 };
 
-inline Choices choose(const Product& P, int sms, int max_split = 8)
+inline Choices choose_anew(const Product& P, int sms, int max_split)
 {
     const bool ragged_rows = P.ragged == RAGGED_ROWS, ragged_reduce = P.ragged == RAGGED_REDUCE;
     const int64_t rows = ragged_rows ? std::max(1, P.n / P.groups) : P.n;
@@ -160,6 +160,26 @@ inline Choices choose(const Product& P, int sms, int max_split = 8)
         }
     }
     return c;
+}
+
+// The same, remembered by the sizes that it depends on: an estimate takes about a
+// microsecond, a gradient asks for ten, and calls come again with the same sizes.
+inline Choices choose(const Product& P, int sms, int max_split = 8)
+{
+    struct Entry {
+        int32_t key[10];
+        Choices choices;
+    };
+    static thread_local Entry known[64];
+    const int32_t key[10] = {P.m, P.n, P.k, P.groups, P.ragged, P.symmetric, P.b_mn, sms, max_split, 1};
+    uint32_t h = 0;
+    for (int32_t v : key) h = (h ^ (uint32_t)v) * 0x9e3779b1u, h ^= h >> 15;
+    Entry& e = known[h % 64];
+    if (!std::equal(key, key + 10, e.key)) {
+        e.choices = choose_anew(P, sms, max_split);
+        std::copy(key, key + 10, e.key);
+    }
+    return e.choices;
 }
 
 // Complete a product for a shape: tiles and maps.  alt: A as P->alt's flag has it read.
