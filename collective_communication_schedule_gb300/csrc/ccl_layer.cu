@@ -332,7 +332,7 @@ static ccl_status_t dispatch(const ccl_dispatch_t* a, cudaStream_t stream)
     M.k = a->k;
     const bool vec = by_vectors(a->h, a->dtype, {{a->x, M.ld_x}, {a->out, M.ld_out}});
     dim3 grid;
-    TRY(pieces(who, &M, 64 * (vec ? 16 / es : 1), &grid));
+    TRY(pieces(who, &M, 64 * (vec ? 16 / es : 8), &grid));
     return launch(BY_TYPE(dispatch_kernel, a->dtype, vec), grid, 256, 0, stream, M);
 }
 
@@ -366,7 +366,7 @@ static ccl_status_t combine(const ccl_combine_t* a, cudaStream_t stream)
     M.k = a->k;
     const bool vec = by_vectors(a->h, a->dtype, {{a->r, M.ld_r}, {a->y, M.ld_out}, {a->residual, M.ld_s}});
     dim3 grid;
-    TRY(pieces(who, &M, 32 * (vec ? 16 / es : 1), &grid));
+    TRY(pieces(who, &M, 32 * (vec ? 16 / es : 8), &grid));
     return launch(BY_TYPE(combine_kernel, a->dtype, vec), grid, 256, 0, stream, M);
 }
 
@@ -401,7 +401,7 @@ static ccl_status_t combine_grad(const ccl_combine_grad_t* a, cudaStream_t strea
     M.h = a->h;
     M.k = a->k;
     const bool vec = by_vectors(a->h, a->dtype, {{a->dy, M.ld_x}, {a->dweights ? a->r : nullptr, M.ld_r}, {a->dr, M.ld_out}});
-    return launch(BY_TYPE(combine_grad_kernel, a->dtype, vec), dim3((unsigned)a->rows), 32 * std::min(8, a->k), 0, stream, M);
+    return launch(BY_TYPE(combine_grad_kernel, a->dtype, vec), dim3((unsigned)((a->rows * a->k + 7) / 8)), 256, 0, stream, M);
 }
 
 ccl_status_t take_layer_status()

@@ -38,144 +38,194 @@ __device__ __forceinline__ int64_t place_of(const Moves& M, int64_t row, int j)
     return p;
 }
 
-// out[place[t, j]] = x[t].  A warp takes a piece of 64 loads of one token, two
-// a lane, and writes it k times.  VEC: loads of 16 bytes, else of one element.
+// A lane's pieces of a row: VEC: one of 16 bytes, else 8 elements 32 apart.
+// at: the first one's element, of h.
+template <typename E, bool VEC>
+struct Part {
+    static constexpr int kSize = VEC ? E::kVec : 8;        // elements
+    static constexpr int kWarp = 32 * kSize;               // of a warp
+    uint4 u;
+    typename E::Raw r[VEC ? 1 : 8];
+
+    static __device__ __forceinline__ int first(int lane) { return VEC ? lane * E::kVec : lane; }
+    __device__ __forceinline__ void load(const typename E::Raw* p, int64_t at, int64_t h)
+    {
+        if constexpr (VEC) {
+            if (at < h) u = *reinterpret_cast<const uint4*>(p + at);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (at + i * 32 < h) r[i] = p[at + i * 32];
+        }
+    }
+    // copied as it is
+    __device__ __forceinline__ void store(typename E::Raw* p, int64_t at, int64_t h) const
+    {
+        if constexpr (VEC) {
+            if (at < h) *reinterpret_cast<uint4*>(p + at) = u;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (at + i * 32 < h) p[at + i * 32] = r[i];
+        }
+    }
+    // in 32 bits (0 beyond the row)
+    __device__ __forceinline__ void get(float (&v)[kSize], int64_t at, int64_t h) const
+    {
+        if constexpr (VEC) {
+            if (at < h) {
+                E::unpack(u, v);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kSize; ++i) v[i] = 0.f;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = at + i * 32 < h ? E::load(r + i) : 0.f;
+        }
+    }
+    static __device__ __forceinline__ void put(typename E::Raw* p, const float (&v)[kSize], int64_t at, int64_t h)
+    {
+        if constexpr (VEC) {
+            if (at < h) *reinterpret_cast<uint4*>(p + at) = E::pack(v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (at + i * 32 < h) E::store(p + at + i * 32, v[i]);
+        }
+    }
+};
+
+// out[place[t, j]] = x[t].  A warp takes two parts of a token and writes them k
+// times.
 template <int T, bool VEC>
 __global__ void __launch_bounds__(256) dispatch_kernel(const Moves M)
 {
     typedef Type<T> E;
     typedef typename E::Raw Raw;
-    constexpr int W = VEC ? E::kVec : 1;
+    typedef Part<E, VEC> P;
     let_next_in();
     wait_for_previous();
     const int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     const int64_t t = item / M.chunks;
     if (t >= M.rows) return;
-    const int64_t c = ((item - t * M.chunks) * 64 + lane) * W;
-    const Raw* x = (const Raw*)M.x + t * M.ld_x + c;
-    uint4 v[2];
-    Raw s[2];
+    const int64_t c = (item - t * M.chunks) * (2 * P::kWarp) + P::first(lane);
+    const Raw* x = (const Raw*)M.x + t * M.ld_x;
+    P v[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-        if (c + i * 32 * W < M.h) {
-            if (VEC)
-                v[i] = *reinterpret_cast<const uint4*>(x + i * 32 * W);
-            else
-                s[i] = x[i * 32];
-        }
+    for (int i = 0; i < 2; ++i) v[i].load(x, c + i * P::kWarp, M.h);
+#pragma unroll 4
     for (int j = 0; j < M.k; ++j) {
         const int64_t p = place_of(M, t, j);
         if (p < 0) continue;
-        Raw* o = (Raw*)M.out + p * M.ld_out + c;
+        Raw* o = (Raw*)M.out + p * M.ld_out;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (c + i * 32 * W < M.h) {
-                if (VEC)
-                    *reinterpret_cast<uint4*>(o + i * 32 * W) = v[i];
-                else
-                    o[i * 32] = s[i];
-            }
+        for (int i = 0; i < 2; ++i) v[i].store(o, c + i * P::kWarp, M.h);
     }
 }
 
-// y[t] = sum_j w[t, j] r[place[t, j]] (+ residual[t]), in 32 bits, j ascending.
+// y[t] = sum_j w[t, j] r[place[t, j]] (+ residual[t]), in 32 bits, j ascending.  A
+// warp takes a part of a token, four choices' loads on their way at a time.
 template <int T, bool VEC>
 __global__ void __launch_bounds__(256) combine_kernel(const Moves M)
 {
     typedef Type<T> E;
     typedef typename E::Raw Raw;
-    constexpr int W = VEC ? E::kVec : 1;
+    typedef Part<E, VEC> P;
     let_next_in();
     wait_for_previous();
     const int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     const int64_t t = item / M.chunks;
     if (t >= M.rows) return;
-    const int64_t c = ((item - t * M.chunks) * 32 + lane) * W;
-    const bool in = c < M.h;
-    float acc[W] = {};
+    const int64_t c = (item - t * M.chunks) * P::kWarp + P::first(lane);
+    float acc[P::kSize] = {};
 #pragma unroll 4
     for (int j = 0; j < M.k; ++j) {
         const int64_t p = place_of(M, t, j);
-        if (p < 0 || !in) continue;
+        if (p < 0) continue;
         const float w = M.weights ? M.weights[t * M.k + j] : 1.f;
-        const Raw* r = (const Raw*)M.r + p * M.ld_r + c;
-        float v[W];
-        if (VEC)
-            E::unpack(*reinterpret_cast<const uint4*>(r), v);
-        else
-            v[0] = E::load(r);
+        P part;
+        float v[P::kSize];
+        part.load((const Raw*)M.r + p * M.ld_r, c, M.h);
+        part.get(v, c, M.h);
 #pragma unroll
-        for (int i = 0; i < W; ++i) acc[i] = fmaf(w, v[i], acc[i]);
+        for (int i = 0; i < P::kSize; ++i) acc[i] = fmaf(w, v[i], acc[i]);
     }
-    if (!in) return;
     if (M.residual) {
-        const Raw* r = (const Raw*)M.residual + t * M.ld_s + c;
-        float v[W];
-        if (VEC)
-            E::unpack(*reinterpret_cast<const uint4*>(r), v);
-        else
-            v[0] = E::load(r);
+        P part;
+        float v[P::kSize];
+        part.load((const Raw*)M.residual + t * M.ld_s, c, M.h);
+        part.get(v, c, M.h);
 #pragma unroll
-        for (int i = 0; i < W; ++i) acc[i] += v[i];
+        for (int i = 0; i < P::kSize; ++i) acc[i] += v[i];
     }
-    Raw* o = (Raw*)M.out + t * M.ld_out + c;
-    if (VEC)
-        *reinterpret_cast<uint4*>(o) = E::pack(acc);
-    else
-        E::store(o, acc[0]);
+    P::put((Raw*)M.out + t * M.ld_out, acc, c, M.h);
 }
 
-// dr[place[t, j]] = w[t, j] dy[t],  dweights[t, j] = <dy[t], r[place[t, j]]>.
-// A threadblock takes a token, a warp a choice; dy is read once from memory and
-// by the other warps from L1.  x: dy, out: dr (either output may be null).
+// dr[place[t, j]] = w[t, j] dy[t],  dweights[t, j] = <dy[t], r[place[t, j]]>.  A
+// warp takes a choice; neighbouring warps take choices of one token, whose dy is
+// read once from memory and by the others from L1.  x: dy, out: dr (either output
+// may be null).
 template <int T, bool VEC>
 __global__ void __launch_bounds__(256) combine_grad_kernel(const Moves M)
 {
     typedef Type<T> E;
     typedef typename E::Raw Raw;
-    constexpr int W = VEC ? E::kVec : 1;
     let_next_in();
     wait_for_previous();
     const int lane = threadIdx.x & 31;
-    const int64_t t = blockIdx.x;
-    const Raw* dy = (const Raw*)M.x + t * M.ld_x;
-    for (int j = threadIdx.x >> 5; j < M.k; j += blockDim.x >> 5) {
-        const int64_t p = place_of(M, t, j);
-        float dot = 0.f;
-        if (p >= 0) {
-            const float w = M.weights ? M.weights[t * M.k + j] : 1.f;
-            const Raw* r = (const Raw*)M.r + p * M.ld_r;
-            Raw* o = (Raw*)M.out + p * M.ld_out;
+    const int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (item >= M.rows * M.k) return;
+    const int t = (int)item / M.k, h = (int)M.h;           // (fewer than 2^31 choices)
+    const int64_t p = place_of(M, 0, (int)item);
+    float dot = 0.f;
+    if (p >= 0) {
+        const Raw* dy = (const Raw*)M.x + t * M.ld_x;
+        const float w = M.weights ? M.weights[item] : 1.f;
+        const Raw* r = (const Raw*)M.r + p * M.ld_r;
+        Raw* o = (Raw*)M.out + p * M.ld_out;
+        if constexpr (VEC) {
+            constexpr int W = E::kVec;
 #pragma unroll 4
-            for (int64_t c = lane * W; c < M.h; c += 32 * W) {
+            for (int c = lane * W; c < h; c += 32 * W) {
                 float g[W], v[W];
-                if (VEC) {
-                    E::unpack(*reinterpret_cast<const uint4*>(dy + c), g);
-                    if (M.dweights) E::unpack(*reinterpret_cast<const uint4*>(r + c), v);
-                } else {
-                    g[0] = E::load(dy + c);
-                    if (M.dweights) v[0] = E::load(r + c);
-                }
+                E::unpack(*reinterpret_cast<const uint4*>(dy + c), g);
                 if (M.dweights) {
+                    E::unpack(*reinterpret_cast<const uint4*>(r + c), v);
 #pragma unroll
                     for (int i = 0; i < W; ++i) dot = fmaf(g[i], v[i], dot);
                 }
                 if (M.out) {
 #pragma unroll
                     for (int i = 0; i < W; ++i) g[i] *= w;
-                    if (VEC)
-                        *reinterpret_cast<uint4*>(o + c) = E::pack(g);
-                    else
-                        E::store(o + c, g[0]);
+                    *reinterpret_cast<uint4*>(o + c) = E::pack(g);
                 }
             }
+        } else {
+            // 8 elements a lane on their way at a time
+            for (int c0 = lane; c0 < h; c0 += 8 * 32) {
+                Raw v[8], g[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (c0 + i * 32 < h) {
+                        if (M.dweights) v[i] = r[c0 + i * 32];
+                        g[i] = dy[c0 + i * 32];
+                    }
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (c0 + i * 32 < h) {
+                        const float a = E::load(g + i);
+                        if (M.dweights) dot = fmaf(a, E::load(v + i), dot);
+                        if (M.out) E::store(o + c0 + i * 32, a * w);
+                    }
+            }
         }
-        if (M.dweights) {
-            dot = warp_sum(dot);
-            if (lane == 0) M.dweights[t * M.k + j] = dot;
-        }
+    }
+    if (M.dweights) {
+        dot = warp_sum(dot);
+        if (lane == 0) M.dweights[item] = dot;
     }
 }
 
