@@ -206,7 +206,8 @@ static ccl_status_t expert_order(const ccl_expert_order_t* a, char* base, int64_
     if (a->slots < 0 || a->slots > INT32_MAX) return fail(CCL_ERR_INVALID_ARG, who + "slots out of range");
     Arena ws = {base};
     Route R = {};
-    R.blocks = order_blocks(a->slots, 4 * kOrderThreads);
+    // one threadblock for what takes it no longer than a second launch
+    R.blocks = a->slots <= 4 * kOrderThreads ? 1 : order_blocks(a->slots, 512);
     if (R.blocks > 1) R.hist = ws.take<int32_t>(hist_bytes(R.blocks, a->experts));
     if (need) {
         *need = ws.used;

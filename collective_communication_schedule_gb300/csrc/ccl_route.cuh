@@ -382,9 +382,10 @@ __device__ __forceinline__ void store_row(typename E::Raw* p, int at, int n, boo
 // for neighbours in the order, all that lie within `near` of the k-th are ordered
 // again in 64 bits, about one row in a hundred; where it is so for the groups at
 // the border, or for more than 32 candidates, the whole row is.
-//   sigmoid: 2^(-l log2 e) within 2^-22 and its argument within 2^-24 of itself,
-//     which |l| s (1 - s) < 0.23 turns into 2^-25 of s; a sum and a reciprocal
-//     within 2^-22: less than 2^-21.4 in all, twice that for two of them;
+//   sigmoid, in units of 2^-22: 2^(-l log2 e) within 1 of itself, of which
+//     s (1 - s) <= 1/4 reaches s; its argument within 1/4 of itself, of which
+//     |l| s (1 - s) < 0.23 does; the sum 1/4 and the reciprocal 1/2 of s: less than
+//     1.07 in all, twice that for two of them, so 1.125 x 2^-21;
 //   softmax: the sum is off by up to 37 roundings and scales all scores alike,
 //     the exponential is within 2^-22, and l - max and its product with log2 e
 //     round to 2^-24 |l - max| of a score, at most 2^-24: 2^-18 of the largest
@@ -422,7 +423,7 @@ __device__ __forceinline__ void route_row(const Route& R, int64_t row, double* v
         float v[VPL];
         if (R.scored) {
             const float inv = 1.f / sum;
-            near = softmax ? inv * 0x1p-18f : 0x1p-20f;
+            near = softmax ? inv * 0x1p-18f : 0x1.2p-21f;
             float bias[VPL];
             if (R.bias)
                 load_row<VPL, Type<CCL_F32>>(R.bias, lane * VPL, R.experts, R.vec_b, bias);
