@@ -318,10 +318,10 @@ static ccl_status_t dispatch(const ccl_dispatch_t* a, cudaStream_t stream)
     Moves M = {};
     TRY(stride("x", a->ldx, a->h, &M.ld_x));
     TRY(stride("out", a->ldo, a->h, &M.ld_out));
-    if (a->rows == 0 || a->count == 0) return CCL_OK;
+    if (a->rows == 0) return CCL_OK;
     const int es = element_bytes(a->dtype);
     TRY(array(who, "x", a->x, true, es));
-    TRY(array(who, "out", a->out, true, es));
+    TRY(array(who, "out", a->out, a->count > 0, es));
     TRY(array(who, "place", a->place, true));
     if (same(a->out, {a->x, a->place})) return fail(CCL_ERR_INVALID_ARG, who + "the output is also an operand");
     M.x = a->x;

@@ -435,6 +435,13 @@ def test_places_beyond_the_rows_are_passed_over_and_reported(ccl):
             ccl.tensor_status()
         assert all(torch.equal(a, b) for a, b in zip(got if isinstance(got, tuple) else (got,), want))
         assert bool((held[0] == 5).all()) and bool((held[2] == 5).all())
+    for call in (lambda p: ccl.dispatch(x, p, out=held[1, :0]), lambda p: ccl.combine(r[:0], p, w),
+                 lambda p: ccl.combine_backward(x, r[:0], p, w)):       # no rows to place them in at all
+        call(torch.full_like(good, -1))
+        ccl.tensor_status()
+        call(torch.zeros_like(good))
+        with pytest.raises(ccl.CclError, match="place"):
+            ccl.tensor_status()
     ccl.tensor_status()
 
 

@@ -174,7 +174,7 @@ def test_empty_calls_need_no_device():
     assert code("ccl_route", route(rows=0, logits=None, weights=None, chosen=None)) == 0
     assert code("ccl_route_grad", route_grad(rows=0)) == 0
     assert code("ccl_dispatch", dispatch(rows=0)) == 0
-    assert code("ccl_dispatch", dispatch(count=0)) == 0
+    assert code("ccl_dispatch", dispatch(rows=0, x=None, out=None, place=None)) == 0
     assert code("ccl_combine", combine(rows=0)) == 0
     assert code("ccl_combine_grad", combine_grad(dr=None, dweights=None)) == 0
     assert code("ccl_layer_norm", norm(rows=0)) == 0
