@@ -221,8 +221,9 @@ __device__ __noinline__ int order64(const Route& R, int64_t row, int expert, int
 }
 
 // Which groups are kept, decided in 64 bits: lane g takes the largest values of
-// group g and computes them again.  Says whether it could: not where the second
-// and the third value of a group may be in the wrong order.
+// group g and computes them again.  Says whether it could: not where the third
+// value of a group may in truth be among those that the group's value is made of:
+// its two largest, or the larger of them.
 __device__ __noinline__ bool groups64(const Route& R, int64_t row, int lane, float most, float inv, float near, uint32_t& kept)
 {
     const int size = R.group_size;
@@ -244,8 +245,8 @@ __device__ __noinline__ bool groups64(const Route& R, int64_t row, int lane, flo
                 b = c, at_b = e;
         }
     }
-    const float bound = fmaf(fmaxf(fabsf(b), fabsf(third)), 0x1p-22f, near);
-    const bool unsure = R.bias && R.group_best == 2 && third != -INFINITY && !(b - third >= bound);
+    const float last = R.group_best == 2 ? b : a, bound = fmaf(fmaxf(fabsf(last), fabsf(third)), 0x1p-22f, near);
+    const bool unsure = R.bias && third != -INFINITY && !(last - third >= bound);
     if (__any_sync(~0u, unsure)) return false;
     const double2 s = softmax64(R, row, lane);
     double v = -INFINITY;
@@ -255,7 +256,7 @@ __device__ __noinline__ bool groups64(const Route& R, int64_t row, int lane, flo
     };
     if (at_a >= 0) {
         v = value(at_a);
-        if (R.group_best == 2 && at_b >= 0) v += value(at_b);
+        if (at_b >= 0) v = R.group_best == 2 ? v + value(at_b) : fmax(v, value(at_b));
     }
     bool close = false;
     kept = best_groups(R, v, 0., lane, 0., close);

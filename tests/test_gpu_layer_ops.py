@@ -62,6 +62,8 @@ def route64(logits, k, score, bias, groups, top, best, renorm, scale=1.0):
             v = v + torch.where(s[..., 1] == -INF, 0.0, s[..., 1])
         kept = torch.sort(v, dim=1, descending=True, stable=True).indices[:, :top]
         open_ = torch.zeros_like(v, dtype=torch.bool).scatter_(1, kept, True)
+        if bias is None:   # scores grow with the logits, though two of 64 bits may round to one value
+            c = torch.where(l == -INF, -INF, l)
         c = torch.where(open_.repeat_interleave(e // groups, 1), c, -INF)
     v, at = torch.sort(c, dim=1, descending=True, stable=True)
     chosen = torch.where(v[:, :k] == -INF, -1, at[:, :k])
@@ -153,6 +155,17 @@ def test_route_decides_near_values_in_64_bits(ccl):
         flat = 18 + 8 * torch.rand(40, 64, device="cuda", generator=g)
         check_route(ccl, flat, 6, 1, torch.zeros(64, device="cuda"))
         check_route(ccl, flat, 6, 1, None, groups=8, top=4, best=2)
+
+
+def test_route_groups_by_near_best_values(ccl):
+    """Groups whose largest values lie within a rounding of 32 bits of each other and of others of their own."""
+    for seed in range(6):
+        g = gen(100 + seed)
+        for e, groups in ((1024, 2), (1024, 16), (500, 10), (96, 4), (64, 16)):
+            flat = 18 + 8 * torch.rand(200, e, device="cuda", generator=g)
+            for bias in (torch.zeros(e, device="cuda"), None):
+                for best in (1, 2):
+                    check_route(ccl, flat, 6, 1, bias, groups, max(1, groups // 4, -(-6 * groups // e)), best)
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=IDS)
