@@ -48,6 +48,9 @@ static ccl_status_t norm_device(const NormKernels& k)
         for (const auto& r : form)
             TRY_CUDA(cudaFuncSetAttribute(r.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)grad_smem(r)),
                      "shared memory of a norm's gradient");
+    for (const auto& r : k.forward[1])
+        if (r.blocks)
+            TRY_CUDA(cudaFuncSetAttribute(r.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, r.smem + r.stage), "shared memory of a norm");
     known[d].push_back(&k);
     return CCL_OK;
 }
@@ -103,9 +106,17 @@ static ccl_status_t layer_norm(const ccl_layer_norm_t* a, cudaStream_t stream)
     const int64_t each = a->dtype == CCL_F32 ? 4 : 8;
     const bool vec = a->n % each == 0 && aligned16(a->x) && aligned16(a->y) && aligned16(a->w) && aligned16(a->b) &&
                      N.ld_x % each == 0 && N.ld_y % each == 0;
-    for (const auto& r : k.forward[!vec])
-        if (a->n <= r.width)
-            return launch(r.kernel, dim3((unsigned)((a->rows + r.rows - 1) / r.rows)), r.threads, 0, stream, N);
+    const int64_t es = a->dtype == CCL_F32 ? 4 : 2;
+    N.apart = ((uintptr_t)a->x - (uintptr_t)a->y) % 16 != 0 || (a->rows > 1 && (N.ld_x - N.ld_y) * es % 16 != 0);
+    for (const auto& r : k.forward[!vec]) {
+        if (a->n > r.width) continue;
+        int64_t blocks = (a->rows + r.rows - 1) / r.rows;
+        if (r.blocks) {
+            TRY(norm_device(k));
+            blocks = std::min<int64_t>(blocks, (int64_t)kNormBlocks * r.blocks);
+        }
+        return launch(r.kernel, dim3((unsigned)blocks), r.threads, r.smem + (N.apart ? r.stage : 0), stream, N);
+    }
     return launch(k.forward_long, dim3((unsigned)a->rows), 1024, 0, stream, N);
 }
 

@@ -22,6 +22,7 @@ struct Norm {
     int64_t ld_x, ld_y, ld_dy, ld_dx;
     int32_t blocks;                // of the backward pass
     float eps;
+    int32_t apart;                 // rows of y lie otherwise to 16 bytes than those of x
 };
 
 // Sum over the TPR threads of a row (all of them get it): a warp, or a
@@ -183,6 +184,144 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_kernel_rows(const 
             if (b) o += EW::load(b + c);
             E::store(y + c, o);
         }
+    }
+}
+
+// Rows off 16 bytes: what lies on 16 bytes of each is read and written so, and
+// the up to 2 (W - 1) elements before and behind go to a thread each.  A thread's
+// elements of w and b then lie anywhere, so the threadblock keeps both as W
+// planes in shared memory (element i in plane i mod W), of which neighbouring
+// lanes read neighbouring places whatever the row's distance from 16 bytes.  Where
+// rows of y have another distance they go through shared memory too, and out by
+// elements.  The threadblock's groups of TPR threads take rows in turn.
+//
+// Instructions bound it (1750 a row of 2057, most SM cycles issue one).  Element
+// by element, us, and so: bf16 8191 x 2057 26.3 and 19.8 (3.4 TB/s), 4097 x 4097
+// 48.5 and 23.4, 1000 x 10007 26.9 and 18.6, f16 20000 x 517 29.5 and 12.8, bf16
+// 20000 x 131 10.1 and 9.3, but 8191 x 100 3.6 and 5.2, so up to 128 elements
+// stay one by one, and f32, which has half as many elements in the same bytes: 8191
+// x 2057 27.3 and 37.5.
+constexpr int kShiftedThreads = 256;
+__host__ __device__ constexpr int shifted_blocks(int each) { return each > 24 ? 3 : 4; }    // elements of a thread, which are in registers
+template <int W, int TPR, int V>
+__host__ __device__ constexpr int plane_of() { return V * TPR + 16 / W; }    // pairs (one behind the last; spread over the banks)
+template <int T, int TW, int TPR, int V>
+__global__ void __launch_bounds__(kShiftedThreads, shifted_blocks(V * Type<T>::kVec)) norm_kernel_shifted(const Norm N)
+{
+    typedef Type<T> E;
+    typedef Type<TW> EW;
+    typedef typename E::Raw Raw;
+    constexpr int W = E::kVec, P = plane_of<W, TPR, V>(), kRows = kShiftedThreads / TPR;
+    __shared__ float buf[2][kShiftedThreads / 32];
+    extern __shared__ __align__(16) float2 planes[];       // w and b
+    let_next_in();
+    wait_for_previous();
+    const int tid = threadIdx.x % TPR, group = threadIdx.x / TPR, n = (int)N.n;
+    const typename EW::Raw *w = (const typename EW::Raw*)N.w, *b = (const typename EW::Raw*)N.b;
+    uint4* stage = reinterpret_cast<uint4*>(planes + W * P) + group * (V * TPR);
+    const float inv = 1.f / (float)n;
+    auto sync = [&]() {            // the row's threads
+        if (TPR == 32)
+            __syncwarp();
+        else
+            named_sync(1 + group, TPR);
+    };
+    auto sum = [&](float t, float* at) {
+        t = warp_sum(t);
+        if (TPR == 32) return t;
+        if ((threadIdx.x & 31) == 0) at[threadIdx.x >> 5] = t;
+        sync();
+        t = 0.f;
+#pragma unroll
+        for (int i = 0; i < TPR / 32; ++i) t += at[group * (TPR / 32) + i];
+        return t;
+    };
+    const int64_t step = (int64_t)gridDim.x * kRows;
+    int64_t row = (int64_t)blockIdx.x * kRows + group;
+    uint4 raw[V];
+    Raw one;
+    int head = 0, full = 0, own = n;       // elements before the first 16 bytes, pieces, this thread's element of the rest
+    auto fetch = [&]() {
+        const Raw* x = (const Raw*)N.x + row * N.ld_x;
+        head = min((int)(-(uintptr_t)x & 15) / (int)sizeof(Raw), n);
+        full = (n - head) / W;
+        own = tid < W ? (tid < head ? tid : n) : tid < 2 * W ? head + full * W + tid - W : n;
+        if (own < n) one = x[own];
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (i * TPR + tid < full) raw[i] = *reinterpret_cast<const uint4*>(x + head + (i * TPR + tid) * W);
+    };
+    if (row < N.rows) fetch();
+    for (int i0 = threadIdx.x; i0 < n; i0 += 8 * kShiftedThreads) {
+        float kw[8], kb[8];        // all on their way at a time
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int i = min(i0 + j * kShiftedThreads, n - 1);
+            kw[j] = w ? EW::load(w + i) : 1.f;
+            kb[j] = b ? EW::load(b + i) : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int i = i0 + j * kShiftedThreads;
+            if (i < n) planes[i % W * P + i / W] = make_float2(kw[j], kb[j]);
+        }
+    }
+    __syncthreads();
+    while (row < N.rows) {
+        float v[V][W], z = own < n ? E::load(&one) : 0.f, t = z;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (i * TPR + tid < full) {
+                E::unpack(raw[i], v[i]);
+#pragma unroll
+                for (int e = 0; e < W; ++e) t += v[i][e];
+            }
+        const float mean = sum(t, buf[0]) * inv;
+        z -= mean;
+        t = own < n ? z * z : 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (i * TPR + tid < full) {
+#pragma unroll
+                for (int e = 0; e < W; ++e) {
+                    v[i][e] -= mean;
+                    t = fmaf(v[i][e], v[i][e], t);
+                }
+            }
+        const float rstd = 1.f / sqrtf(sum(t, buf[1]) * inv + N.eps);
+        if (tid == 0) {
+            if (N.mean) N.mean[row] = mean;
+            if (N.rstd) N.rstd[row] = rstd;
+        }
+        Raw* y = (Raw*)N.y + row * N.ld_y;
+        if (own < n) {
+            const float2 k = planes[own % W * P + own / W];
+            E::store(y + own, fmaf(z * rstd, k.x, k.y));
+        }
+        int at[W];                 // its elements of w and b
+#pragma unroll
+        for (int e = 0; e < W; ++e) at[e] = ((e + head) & (W - 1)) * P + tid + (e + head >= W);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (i * TPR + tid < full) {
+#pragma unroll
+                for (int e = 0; e < W; ++e) {
+                    const float2 k = planes[at[e] + i * TPR];
+                    v[i][e] = fmaf(v[i][e] * rstd, k.x, k.y);
+                }
+                if (N.apart)
+                    stage[i * TPR + tid] = E::pack(v[i]);
+                else
+                    *reinterpret_cast<uint4*>(y + head + (i * TPR + tid) * W) = E::pack(v[i]);
+            }
+        if (N.apart) {
+            sync();
+            const Raw* held = reinterpret_cast<const Raw*>(stage);
+            for (int i = tid; i < full * W; i += TPR) y[head + i] = held[i];
+            sync();
+        }
+        row += step;
+        if (row < N.rows) fetch();
     }
 }
 

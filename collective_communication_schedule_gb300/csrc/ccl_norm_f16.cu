@@ -4,8 +4,16 @@
 namespace ccl {
 namespace tensor {
 
-const NormKernels& norm_kernels_f16_f16() { return norm_kernels_of<CCL_F16, CCL_F16>(); }
-const NormKernels& norm_kernels_f16_f32() { return norm_kernels_of<CCL_F16, CCL_F32>(); }
+const NormKernels& norm_kernels_f16_f16()
+{
+    static const NormKernels k = norm_kernels_of<CCL_F16, CCL_F16>();
+    return k;
+}
+const NormKernels& norm_kernels_f16_f32()
+{
+    static const NormKernels k = norm_kernels_of<CCL_F16, CCL_F32>();
+    return k;
+}
 
 }  // namespace tensor
 }  // namespace ccl

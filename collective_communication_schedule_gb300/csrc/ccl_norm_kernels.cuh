@@ -1,6 +1,8 @@
 // The norm's kernels of one pair of types, one translation unit a type.
 #pragma once
 
+#include <vector>
+
 #include "ccl_norm.cuh"
 
 namespace ccl {
@@ -13,6 +15,8 @@ struct NormKernels {
         int64_t width;             // elements of the longest row
         int threads, rows;         // of a threadblock
         void (*kernel)(const Norm);
+        int blocks;                // of an SM, which take rows in turn; 0: as many as the rows need
+        int smem, stage;           // bytes of shared memory, and where rows of y lie apart
     };
     struct Backward {
         int64_t width;
@@ -20,7 +24,7 @@ struct NormKernels {
         int pieces, each;          // of a thread, elements of one
         void (*kernel)(const Norm);
     };
-    Forward forward[2][7];
+    std::vector<Forward> forward[2];
     Backward backward[2][6];
     void (*forward_long)(const Norm);
     void (*backward_long)(const Norm);
@@ -29,17 +33,18 @@ struct NormKernels {
 };
 
 template <int T, int TW>
-const NormKernels& norm_kernels_of()
+NormKernels norm_kernels_of()
 {
     // (f32: half the elements a piece, twice the pieces)
     constexpr int W = Type<T>::kVec, M = 8 / W;
 #define FORWARD(tpr, v, vec) {(tpr) * (v) * ((vec) ? W : 1), (tpr) < 128 ? 128 : (tpr), (tpr) < 128 ? 128 / (tpr) : 1, norm_kernel_rows<T, TW, tpr, v, vec>}
+#define SHIFTED(tpr, v)                                                                                            \
+    {(tpr) * (v) * W - (W - 1), kShiftedThreads, kShiftedThreads / (tpr), norm_kernel_shifted<T, TW, tpr, v>,          \
+     shifted_blocks((v) * W), 8 * W * plane_of<W, tpr, v>(), kShiftedThreads * (v) * 16}
 #define BACKWARD(tpr, v, vec) {(tpr) * (v) * ((vec) ? W : 1), tpr, v, (vec) ? W : 1, norm_grad_kernel_rows<T, TW, tpr, v, vec>}
-    static const NormKernels k = {
+    NormKernels k = {
         {{FORWARD(32, M, true), FORWARD(32, 4 * M, true), FORWARD(128, 2 * M, true), FORWARD(128, 4 * M, true),
-          FORWARD(512, 2 * M, true), FORWARD(512, 4 * M, true), FORWARD(1024, 2 * M, true)},
-         {FORWARD(32, 4, false), FORWARD(32, 16, false), FORWARD(128, 16, false), FORWARD(256, 10, false), FORWARD(256, 16, false),
-          FORWARD(512, 16, false), FORWARD(1024, 16, false)}},
+          FORWARD(512, 2 * M, true), FORWARD(512, 4 * M, true), FORWARD(1024, 2 * M, true)}},
         {{BACKWARD(32, 1, true), BACKWARD(128, 1, true), BACKWARD(256, 1, true), BACKWARD(512, 1, true), BACKWARD(1024, 1, true),
           BACKWARD(1024, 2, true)},
          {BACKWARD(32, 5, false), BACKWARD(128, 5, false), BACKWARD(256, 5, false), BACKWARD(512, 5, false), BACKWARD(1024, 5, false),
@@ -48,7 +53,13 @@ const NormKernels& norm_kernels_of()
         norm_grad_kernel_long<T, TW>,
         norm_sums_kernel_long<T>,
         norm_sums_kernel<TW>};
+    if constexpr (T == CCL_F32)
+        k.forward[1] = {FORWARD(32, 4, false), FORWARD(32, 16, false), FORWARD(128, 16, false), FORWARD(256, 10, false),
+                        FORWARD(256, 16, false), FORWARD(512, 16, false), FORWARD(1024, 16, false)};
+    else
+        k.forward[1] = {FORWARD(32, 4, false), SHIFTED(32, 3), SHIFTED(128, 3), SHIFTED(256, 3), SHIFTED(256, 5), FORWARD(1024, 16, false)};
 #undef FORWARD
+#undef SHIFTED
 #undef BACKWARD
     return k;
 }

@@ -857,7 +857,7 @@ ccl_status_t ccl_orthogonalize(const ccl_ortho_t* a, void* ws, int64_t ws_bytes,
  * allocation, nothing kept between calls, capturable after one call on the
  * device outside capture, strides in elements with 0 = packed, any stride and
  * alignment, sums in 32 bits in an order that the sizes fix and, for the norm and
- * the gradients of weights, whether all rows start on 16 bytes.  Outputs may
+ * the gradients of weights, how rows lie to 16 bytes.  Outputs may
  * overlap neither operands nor each other but where it says so (ones that start
  * at one address are refused).  Vectors and arrays of choices are packed.  Types: CCL_F32, CCL_BF16, CCL_F16.
  * ====================================================================== */
