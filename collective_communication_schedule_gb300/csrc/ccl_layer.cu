@@ -76,8 +76,10 @@ static ccl_status_t layer_device(int* sms)
     return CCL_OK;
 }
 
-// Blocks of a router call whose rows are ordered too, and of an order alone:
-// by the sizes, so that the workspace does not depend on the device.
+// Blocks of a router call whose rows are ordered too, and of an order alone, at
+// least `least` rows or slots each: by the sizes, so that the workspace does not
+// depend on the device.  A block's place in the order costs the same whatever it
+// holds, so small calls take few.
 constexpr int kOrderBlocks = 152;
 static int order_blocks(int64_t items, int least)
 {
@@ -99,8 +101,10 @@ static ccl_status_t check_router(const std::string& who, int64_t rows, int64_t e
     return CCL_OK;
 }
 
-// As many rows go to one threadblock, which orders them as well.
-constexpr int kRowsOfOne = 16;
+// As many rows go to one threadblock, which orders them as well: us in one launch
+// and in two, 64 experts, choose 6: 1 row 4.6 and 7.0, 24 rows 6.3 and 7.3, 32 rows 7.1
+// and 7.4; 256 experts, choose 8: 6.8 and 8.6, 8.6 and 9.3, 10.2 and 9.6.
+constexpr int kRowsOfOne = 24;
 
 static ccl_status_t route(const ccl_route_t* a, char* base, int64_t* need, cudaStream_t stream)
 {
@@ -206,8 +210,9 @@ static ccl_status_t expert_order(const ccl_expert_order_t* a, char* base, int64_
     if (a->slots < 0 || a->slots > INT32_MAX) return fail(CCL_ERR_INVALID_ARG, who + "slots out of range");
     Arena ws = {base};
     Route R = {};
-    // one threadblock for what takes it no longer than a second launch
-    R.blocks = a->slots <= 4 * kOrderThreads ? 1 : order_blocks(a->slots, 512);
+    // one threadblock for what takes it no longer than a second launch (256 experts, us in one and
+    // several: 1024 slots 5.0 and 5.4, 2048 slots 7.2 and 5.5, 8192 slots 19.1 and 5.7)
+    R.blocks = a->slots <= kOrderThreads ? 1 : order_blocks(a->slots, 512);
     if (R.blocks > 1) R.hist = ws.take<int32_t>(hist_bytes(R.blocks, a->experts));
     if (need) {
         *need = ws.used;
@@ -333,7 +338,7 @@ static ccl_status_t dispatch(const ccl_dispatch_t* a, cudaStream_t stream)
     M.k = a->k;
     const bool vec = by_vectors(a->h, a->dtype, {{a->x, M.ld_x}, {a->out, M.ld_out}});
     dim3 grid;
-    TRY(pieces(who, &M, 64 * (vec ? 16 / es : 8), &grid));
+    TRY(pieces(who, &M, 32 * (vec ? 16 / es : 8), &grid));
     return launch(BY_TYPE(dispatch_kernel, a->dtype, vec), grid, 256, 0, stream, M);
 }
 
@@ -402,7 +407,18 @@ static ccl_status_t combine_grad(const ccl_combine_grad_t* a, cudaStream_t strea
     M.h = a->h;
     M.k = a->k;
     const bool vec = by_vectors(a->h, a->dtype, {{a->dy, M.ld_x}, {a->dweights ? a->r : nullptr, M.ld_r}, {a->dr, M.ld_out}});
-    return launch(BY_TYPE(combine_grad_kernel, a->dtype, vec), dim3((unsigned)((a->rows * a->k + 7) / 8)), 256, 0, stream, M);
+    const int64_t all = a->rows * a->k;
+    // four short rows at a time from 16384 choices on, us so and a warp a choice: h = 128 bf16, 8192 choices
+    // 4.2 and 3.0, 16384 4.7 and 4.7, 32768 4.9 and 8.3, 128000 15.6 and 36.3
+    if (vec && a->h * es <= 32 * 16 && all > 16384) {
+        M.chunks = 1;
+        while (M.chunks * 16 < a->h * es) M.chunks *= 2;
+        const int64_t each = 256 / M.chunks * 4;
+        auto kernel = a->dtype == CCL_F32 ? combine_grad_short_kernel<CCL_F32>
+                      : a->dtype == CCL_BF16 ? combine_grad_short_kernel<CCL_BF16> : combine_grad_short_kernel<CCL_F16>;
+        return launch(kernel, dim3((unsigned)((all + each - 1) / each)), 256, 0, stream, M);
+    }
+    return launch(BY_TYPE(combine_grad_kernel, a->dtype, vec), dim3((unsigned)((all + 7) / 8)), 256, 0, stream, M);
 }
 
 ccl_status_t take_layer_status()

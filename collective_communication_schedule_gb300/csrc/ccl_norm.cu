@@ -31,7 +31,7 @@ static const NormKernels& norm_kernels(int t, int tw)
 // the sums of its groups go through.
 static size_t grad_smem(const NormKernels::Backward& r)
 {
-    return std::max<size_t>(r.each > 1 ? (size_t)rows_ahead(r.pieces) * 2 * r.pieces * kGradThreads * 16 : 0, (size_t)kGradThreads * r.each * 4);
+    return std::max<size_t>(r.each > 1 ? (size_t)kRowsAhead * 2 * r.pieces * kGradThreads * 16 : 0, (size_t)kGradThreads * r.each * 4);
 }
 
 // Once per device: the kernels of a pair of types may use that much.

@@ -10,8 +10,9 @@ namespace tensor {
 // that the order of the sums is.
 constexpr int kNormBlocks = 152;
 constexpr int kGradThreads = 1024;
-// rows that the backward pass has on their way, for so many pieces of 16 bytes a thread: what shared memory holds
-__host__ __device__ constexpr int rows_ahead(int pieces) { return pieces == 1 ? 4 : pieces == 2 ? 3 : 1; }
+// Rows that the backward pass has on their way.  us with 1, 2 and 3: bf16 8192 x 4096
+// 60.3, 47.5 and 48.2, 8192 x 8192 124, 91.6 and 94.9, f32 8192 x 4096 110, 72.1 and 71.0.
+constexpr int kRowsAhead = 2;
 
 struct Norm {
     const void *x, *dy, *w, *b;
@@ -412,7 +413,7 @@ __global__ void __launch_bounds__(kGradThreads) norm_grad_kernel_rows(const Norm
     typedef Type<T> E;
     typedef Type<TW> EW;
     typedef typename E::Raw Raw;
-    constexpr int W = VEC ? E::kVec : 1, kAhead = rows_ahead(V);
+    constexpr int W = VEC ? E::kVec : 1, kAhead = kRowsAhead;
     __shared__ float part[2][64];
     extern __shared__ __align__(16) unsigned char dyn[];
     let_next_in();

@@ -96,8 +96,11 @@ struct Part {
     }
 };
 
-// out[place[t, j]] = x[t].  A warp takes two parts of a token and writes them k
-// times.
+// out[place[t, j]] = x[t].  A warp takes a part of a token (16 bytes a lane) and
+// writes it k times; written bytes bound it.  8190 rows of 2048 bf16 to 4 places each:
+// 26 us, 6.4 TB/s; 24 rows to 8 places 2.2 us.  Two parts a warp took as long at
+// the large size, 14.4 us instead of 12.5 for 4096 rows of 1024 to 8 places and 14.7
+// instead of 15.0 for 4097 rows of 1544 to 6.
 template <int T, bool VEC>
 __global__ void __launch_bounds__(256) dispatch_kernel(const Moves M)
 {
@@ -110,23 +113,22 @@ __global__ void __launch_bounds__(256) dispatch_kernel(const Moves M)
     const int lane = threadIdx.x & 31;
     const int64_t t = item / M.chunks;
     if (t >= M.rows) return;
-    const int64_t c = (item - t * M.chunks) * (2 * P::kWarp) + P::first(lane);
-    const Raw* x = (const Raw*)M.x + t * M.ld_x;
-    P v[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) v[i].load(x, c + i * P::kWarp, M.h);
+    const int64_t c = (item - t * M.chunks) * P::kWarp + P::first(lane);
+    P v;
+    v.load((const Raw*)M.x + t * M.ld_x, c, M.h);
 #pragma unroll 4
     for (int j = 0; j < M.k; ++j) {
         const int64_t p = place_of(M, t, j);
         if (p < 0) continue;
-        Raw* o = (Raw*)M.out + p * M.ld_out;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) v[i].store(o, c + i * P::kWarp, M.h);
+        v.store((Raw*)M.out + p * M.ld_out, c, M.h);
     }
 }
 
 // y[t] = sum_j w[t, j] r[place[t, j]] (+ residual[t]), in 32 bits, j ascending.  A
-// warp takes a part of a token, four choices' loads on their way at a time.
+// warp takes a part of a token, four choices' loads on their way at a time (a
+// thread's place and weight come from L1).  Bytes read bound it, 8190 rows of 2048 bf16
+// from 4 places 33 us, 5.1 TB/s; for few rows the chain of place, row and launch
+// does: 24 rows from 8 places 3.6 us.
 template <int T, bool VEC>
 __global__ void __launch_bounds__(256) combine_kernel(const Moves M)
 {
@@ -164,10 +166,64 @@ __global__ void __launch_bounds__(256) combine_kernel(const Moves M)
     P::put((Raw*)M.out + t * M.ld_out, acc, c, M.h);
 }
 
-// dr[place[t, j]] = w[t, j] dy[t],  dweights[t, j] = <dy[t], r[place[t, j]]>.  A
-// warp takes a choice; neighbouring warps take choices of one token, whose dy is
+// dr[place[t, j]] = w[t, j] dy[t],  dweights[t, j] = <dy[t], r[place[t, j]]>, for
+// rows of up to 16 bytes a lane.  `across` lanes (a power of two) lie along a row, and
+// take four choices with all loads on their way at a time: a warp a choice spends its
+// time on the chain of place, row and sum (128000 choices of 128 bf16 15.6 us, 4.4
+// TB/s, instead of 36).
+template <int T>
+__global__ void __launch_bounds__(256) combine_grad_short_kernel(const Moves M)
+{
+    typedef Type<T> E;
+    typedef typename E::Raw Raw;
+    constexpr int W = E::kVec, kEach = 4;
+    let_next_in();
+    wait_for_previous();
+    const int across = M.chunks, lane = threadIdx.x & (across - 1), c = lane * W, h = (int)M.h;
+    const int64_t all = M.rows * M.k, first = ((int64_t)blockIdx.x * 256 + threadIdx.x) / across * kEach;
+    int64_t p[kEach];
+    float w[kEach], dot[kEach];
+    uint4 g[kEach], r[kEach];
+#pragma unroll
+    for (int q = 0; q < kEach; ++q) p[q] = first + q < all ? place_of(M, 0, (int)(first + q)) : -1;
+#pragma unroll
+    for (int q = 0; q < kEach; ++q) {
+        dot[q] = 0.f;
+        if (p[q] < 0) continue;
+        w[q] = M.weights ? M.weights[first + q] : 1.f;
+        if (c >= h) continue;
+        g[q] = *reinterpret_cast<const uint4*>((const Raw*)M.x + (int)(first + q) / M.k * M.ld_x + c);
+        if (M.dweights) r[q] = *reinterpret_cast<const uint4*>((const Raw*)M.r + p[q] * M.ld_r + c);
+    }
+#pragma unroll
+    for (int q = 0; q < kEach; ++q) {
+        if (p[q] < 0 || c >= h) continue;
+        float a[W], b[W];
+        E::unpack(g[q], a);
+        if (M.dweights) {
+            E::unpack(r[q], b);
+#pragma unroll
+            for (int i = 0; i < W; ++i) dot[q] = fmaf(a[i], b[i], dot[q]);
+        }
+        if (M.out) {
+#pragma unroll
+            for (int i = 0; i < W; ++i) a[i] *= w[q];
+            *reinterpret_cast<uint4*>((Raw*)M.out + p[q] * M.ld_out + c) = E::pack(a);
+        }
+    }
+    if (!M.dweights) return;
+#pragma unroll
+    for (int q = 0; q < kEach; ++q) {
+        for (int d = across / 2; d; d /= 2) dot[q] += __shfl_xor_sync(~0u, dot[q], d);
+        if (lane == 0 && first + q < all) M.dweights[first + q] = dot[q];
+    }
+}
+
+// The same for rows of any length.  A warp takes a choice; neighbouring warps take choices of one token, whose dy is
 // read once from memory and by the others from L1.  x: dy, out: dr (either output
-// may be null).
+// may be null).  Bytes bound it: 8190 rows of 2048 bf16 at 4 places 54 us (5.6 TB/s),
+// 4097 rows of 1544 f16 at 6 places, a fifth of them none, 30 us (4.5 TB/s): its rows
+// share lines of 128 bytes with their neighbours.
 template <int T, bool VEC>
 __global__ void __launch_bounds__(256) combine_grad_kernel(const Moves M)
 {
