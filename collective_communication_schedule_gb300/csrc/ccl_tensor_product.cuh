@@ -52,6 +52,10 @@ namespace tensor {
 //     that are only rounded (4096 x 4096 outputs of 64 products each: 15 us),
 //     twice that with an activation or a residual (22 and 24 us); sixteen warps,
 //     since eight took 1.3 times as long.
+//   values that a loss takes where they are made (Rowwise): the matrix
+//     instructions, 8192 x 131072 x 2048 forward 2188 us, 2010 TFLOP/s, after a
+//     pause and 2570 us at the power limit; 37 x 32003 x 2048, turned, 25 us, DRAM
+//     (5.2 TB/s of weights).
 //   between: whole waves of tiles (4096 x 4096 x 4096: 78 us, 1750 TFLOP/s),
 //     rows that start off a cache line (a 128-byte row of a tile then costs
 //     two: 1001 x 5003 takes 30 us at k = 2056, 24 at 2048).
@@ -113,8 +117,10 @@ struct Pair {
 // A product x w^T for what is done with a row of its values where they are
 // made, in 32 bits (the values themselves are stored nowhere): STATS its sum of
 // exponentials, SLOPE the derivative of a loss.  Lanes are rows of x, so that a
-// thread has a row's values to itself; for few rows, which would leave lanes
-// idle, they are rows of w (the _TURNED forms) and a row's values lie across a warp.
+// thread has a row's values to itself (a maximum, exponentials and their sum of 32
+// values at a time as they leave tensor memory, no exchange between threads until the
+// tile's end); for few rows, which would leave lanes idle, they are rows of w (the
+// _TURNED forms) and a row's values lie across a warp.
 struct Rowwise {
     Product p;                     // A: rows of x, B: rows of w (turned: the other way round)
     const void* target;            // STATS: rows' targets, whose values go to `picked`
@@ -241,7 +247,7 @@ __device__ __forceinline__ TileAt tile_at(const Scalars& P, const Shared* sh, in
         q.za = q.zb = q.g;
         if (P.segment) {
             q.k0 = q.g * P.segment;
-            q.klen = min(P.segment, P.k - q.k0);
+            q.klen = min(P.segment, P.k - q.k0);           // (none where a narrower last piece ends before)
             q.za = q.zb = 0;
         }
         if (P.ragged == RAGGED_REDUCE) {
@@ -918,8 +924,8 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
         for (int i = 0; i < 2; ++i)
             release[i] = CG == 2 ? cluster_addr(smem_addr(&sh.acc_empty[i]), 0) : smem_addr(&sh.acc_empty[i]);
         int done = 0, round = 0;
-        // STATS with all rows in one tile: of this thread's row so far (turned: of row `lane` of two blocks)
         bool good = true;
+        // STATS with all rows in one tile: of this thread's row so far (turned: of row `lane` of two blocks)
         float2 so_far2[2] = {make_float2(-INFINITY, 0.f), make_float2(-INFINITY, 0.f)};
         for (int ph = 0; ph < phases; ++ph) {
             const Product& maps = seq.at(ph);
