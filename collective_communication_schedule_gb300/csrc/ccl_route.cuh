@@ -230,14 +230,16 @@ __device__ __noinline__ bool groups64(const Route& R, int64_t row, int lane, flo
     const bool softmax = R.score != CCL_SCORE_SIGMOID;
     float a = -INFINITY, b = -INFINITY, third = -INFINITY;
     int at_a = -1, at_b = -1;
+    auto near_value = [&](int e, float l) {        // (without a bias the logits are in the scores' order)
+        float c = l;
+        if (R.bias && l != -INFINITY) c = (softmax ? exp2_near((l - most) * 1.4426950408889634f) * inv : sigmoid(l)) + __ldg(R.bias + e);
+        return c != c ? -3.402823466e38f : c;
+    };
     if (lane < R.groups) {
 #pragma unroll 4
         for (int i = 0; i < size; ++i) {
             const int e = lane * size + i;
-            const float l = load_as(R.logits, row * R.ld + e, R.type);
-            float c = l;                       // (without a bias the logits are in the scores' order)
-            if (R.bias && l != -INFINITY) c = (softmax ? exp2_near((l - most) * 1.4426950408889634f) * inv : sigmoid(l)) + __ldg(R.bias + e);
-            if (c != c) c = -3.402823466e38f;
+            const float c = near_value(e, load_as(R.logits, row * R.ld + e, R.type));
             third = fmaxf(third, fminf(b, c));
             if (c > a)
                 b = a, at_b = at_a, a = c, at_a = e;
@@ -246,8 +248,21 @@ __device__ __noinline__ bool groups64(const Route& R, int64_t row, int lane, flo
         }
     }
     const float last = R.group_best == 2 ? b : a, bound = fmaf(fmaxf(fabsf(last), fabsf(third)), 0x1p-22f, near);
-    const bool unsure = R.bias && third != -INFINITY && !(last - third >= bound);
-    if (__any_sync(~0u, unsure)) return false;
+    bool unsure = R.bias && third != -INFINITY && !(last - third >= bound);
+    if (__any_sync(~0u, unsure)) {
+        // one with the last one's logit and bias has its value, whichever of them is taken
+        if (unsure) {
+            const int of = R.group_best == 2 ? at_b : at_a;
+            const float l = load_as(R.logits, row * R.ld + of, R.type), b_of = R.bias[of];
+            third = -INFINITY;
+            for (int e = lane * size; e < (lane + 1) * size; ++e) {
+                const float u = load_as(R.logits, row * R.ld + e, R.type);
+                if (e != at_a && e != at_b && !(u == l && R.bias[e] == b_of)) third = fmaxf(third, near_value(e, u));
+            }
+            unsure = third != -INFINITY && !(last - third >= bound);
+        }
+        if (__any_sync(~0u, unsure)) return false;
+    }
     const double2 s = softmax64(R, row, lane);
     double v = -INFINITY;
     auto value = [&](int e) {
@@ -649,13 +664,14 @@ constexpr int route_threads(int vpl) { return vpl < 16 ? 1024 : 512; }
 
 // A warp a row, a threadblock `per_block` consecutive rows.
 //
-// Instructions bound it: a row of 256 experts with bias and groups takes about
-// 1290 (scores 300, groups 250, 8 choices 300, error bounds 150, weights 100), and the
-// schedulers issue in 6 cycles of 10.  8190 rows choose 8 of 256: 20 us, and 2 more
-// with their order; the bytes alone would take 1.4.  A warp a row keeps scores in
-// registers, so that a choice is one maximum over the warp; for one row
-// (64 experts, choose 6, ordered in the same launch: 4.6 us) the chain of these is
-// all there is.
+// Instructions bound it, about 1290 a row of 256 experts with bias and groups, and
+// the schedulers issue in 6 cycles of 10.  8190 rows choose 8 of 256 f32: by logits
+// alone 9.7 us, in groups 11.7, by sigmoids with a bias 12.5, both 16, and with the
+// order of the rows 22; the bytes alone would take 1.4.  A warp a row keeps scores in
+// registers, so that a choice is one maximum over the warp; for one row (64
+// experts, choose 6, ordered in the same launch: 4.6 us) the chain of these is all
+// there is.  Where many values of a row are equal, as bf16 logits without a
+// bias are, more rows are decided again in 64 bits: 23 us instead of 16 before the order.
 template <int VPL>
 __global__ void __launch_bounds__(route_threads(VPL)) route_kernel(const Route R)
 {
