@@ -27,8 +27,6 @@ struct Type<CCL_F32> {
     {
         return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
     }
-    static __device__ __forceinline__ void unpack4(const uint2&, float*) {}       // (16 bytes are four already)
-    static __device__ __forceinline__ uint2 pack4(const float*) { return make_uint2(0, 0); }
 };
 template <bool BF>
 struct Type16 {
@@ -41,12 +39,6 @@ struct Type16 {
     {
         return make_uint4(pack2<BF>(v[0], v[1]), pack2<BF>(v[2], v[3]), pack2<BF>(v[4], v[5]), pack2<BF>(v[6], v[7]));
     }
-    static __device__ __forceinline__ void unpack4(const uint2& u, float* v)
-    {
-        const float2 a = unpack2<BF>(u.x), b = unpack2<BF>(u.y);
-        v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
-    }
-    static __device__ __forceinline__ uint2 pack4(const float* v) { return make_uint2(pack2<BF>(v[0], v[1]), pack2<BF>(v[2], v[3])); }
 };
 template <>
 struct Type<CCL_BF16> : Type16<true> {};

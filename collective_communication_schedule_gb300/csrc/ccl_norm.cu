@@ -31,7 +31,7 @@ static const NormKernels& norm_kernels(int t, int tw)
 // the sums of its groups go through.
 static size_t grad_smem(const NormKernels::Backward& r)
 {
-    return std::max<size_t>(r.each > 1 ? (size_t)kRowsAhead * 2 * r.pieces * kGradThreads * 16 : 0, (size_t)kGradThreads * r.each * 4);
+    return std::max<size_t>(r.each > 1 ? (size_t)kRowsAhead * 2 * r.pieces * r.threads * 16 : 0, (size_t)r.threads * r.each * 4);
 }
 
 // Once per device: the kernels of a pair of types may use that much.
@@ -182,8 +182,8 @@ static ccl_status_t layer_norm_grad(const ccl_layer_norm_grad_t* a, char* base, 
     for (const auto& r : k.backward[!vec])
         if (!fit && a->n <= r.width) fit = &r;
     if (fit) {
-        N.blocks = norm_blocks(a->rows, kGradThreads / fit->across);
-        TRY(launch(fit->kernel, dim3(N.blocks), kGradThreads, grad_smem(*fit), stream, N));
+        N.blocks = norm_blocks(a->rows, fit->threads / fit->across);
+        TRY(launch(fit->kernel, dim3(N.blocks), fit->threads, grad_smem(*fit), stream, N));
     } else {
         if (a->dx) TRY(launch(k.backward_long, dim3((unsigned)a->rows), 1024, 0, stream, N));
         N.blocks = norm_blocks(a->rows, 32);

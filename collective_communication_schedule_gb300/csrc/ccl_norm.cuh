@@ -9,7 +9,6 @@ namespace tensor {
 // Blocks of a backward pass that keep sums of dw and db: by the sizes alone, so
 // that the order of the sums is.
 constexpr int kNormBlocks = 152;
-constexpr int kGradThreads = 1024;
 // Rows that the backward pass has on their way.  us with 1, 2 and 3: bf16 8192 x 4096
 // 60.3, 47.5 and 48.2, 8192 x 8192 124, 91.6 and 94.9, f32 8192 x 4096 110, 72.1 and 71.0.
 constexpr int kRowsAhead = 2;
@@ -51,9 +50,6 @@ __device__ __forceinline__ void read(const typename E::Raw* p, float* v)
 {
     if (VEC && W == 8 && E::kVec == 8) {
         E::unpack(*reinterpret_cast<const uint4*>(p), v);
-    } else if (VEC && W == 4 && E::kVec == 8) {
-        const uint2 u = *reinterpret_cast<const uint2*>(p);
-        E::unpack4(u, v);
     } else if (VEC && E::kVec == 4) {
 #pragma unroll
         for (int i = 0; i < W; i += 4) E::unpack(*reinterpret_cast<const uint4*>(p + i), v + i);
@@ -67,8 +63,6 @@ __device__ __forceinline__ void write(typename E::Raw* p, const float* v)
 {
     if (VEC && W == 8 && E::kVec == 8) {
         *reinterpret_cast<uint4*>(p) = E::pack(v);
-    } else if (VEC && W == 4 && E::kVec == 8) {
-        *reinterpret_cast<uint2*>(p) = E::pack4(v);
     } else if (VEC && E::kVec == 4) {
 #pragma unroll
         for (int i = 0; i < W; i += 4) *reinterpret_cast<uint4*>(p + i) = E::pack(v + i);
@@ -413,10 +407,10 @@ __device__ __forceinline__ float2 group_sums(float2 s, float* part, int group, i
 // schedulers issue in 7 cycles of 10): 8192 x 4096 bf16 47.5 us with dw and db
 // (4.2 TB/s), f32 with half as many elements in the same bytes 72 us (5.6 TB/s).
 // Elements are unpacked twice instead of kept: 1024 threads have 64 registers each, of
-// which w, dw and db take 24.  Rows off 16 bytes: 8191 x 2057 bf16 41 us; columns belong
+// which w, dw and db take 24.  Rows off 16 bytes: 8191 x 2057 bf16 34 us; columns belong
 // to threads, so rows cannot be taken by the pieces of 16 bytes that they touch.
-template <int T, int TW, int ACROSS, int V, bool VEC>
-__global__ void __launch_bounds__(kGradThreads) norm_grad_kernel_rows(const Norm N)
+template <int T, int TW, int THREADS, int ACROSS, int V, bool VEC>
+__global__ void __launch_bounds__(THREADS) norm_grad_kernel_rows(const Norm N)
 {
     typedef Type<T> E;
     typedef Type<TW> EW;
@@ -426,7 +420,7 @@ __global__ void __launch_bounds__(kGradThreads) norm_grad_kernel_rows(const Norm
     extern __shared__ __align__(16) unsigned char dyn[];
     let_next_in();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = (int)N.n;
-    constexpr int across = ACROSS, groups = kGradThreads / ACROSS;
+    constexpr int across = ACROSS, groups = THREADS / ACROSS;
     const int group = threadIdx.x / across, tid = threadIdx.x & (across - 1);
     const float inv = 1.f / (float)n;
     const int step = gridDim.x * groups, row = blockIdx.x * groups + group;
@@ -434,7 +428,7 @@ __global__ void __launch_bounds__(kGradThreads) norm_grad_kernel_rows(const Norm
     // places of this thread: [row ahead][x, dy][piece], 16 bytes each, neighbours for neighbouring threads
     unsigned char* place = dyn + threadIdx.x * 16;
     const uint32_t place0 = smem_addr(place);
-    constexpr int kPlace = kGradThreads * 16;
+    constexpr int kPlace = THREADS * 16;
     bool mine[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) mine[i] = (i * across + tid) * W < n;

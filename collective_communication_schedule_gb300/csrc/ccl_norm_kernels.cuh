@@ -20,7 +20,7 @@ struct NormKernels {
     };
     struct Backward {
         int64_t width;
-        int across;                // threads of a row
+        int threads, across;       // of a threadblock, of a row
         int pieces, each;          // of a thread, elements of one
         void (*kernel)(const Norm);
     };
@@ -45,14 +45,20 @@ NormKernels norm_kernels_of()
 #define SHIFTED(tpr, v)                                                                                            \
     {(tpr) * (v) * W - (W - 1), kShiftedThreads, kShiftedThreads / (tpr), norm_kernel_shifted<T, TW, tpr, v>,          \
      shifted_blocks((v) * W), 8 * W * plane_of<W, tpr, v>(), kShiftedThreads * (v) * 16}
-#define BACKWARD(tpr, v, vec) {(tpr) * (v) * ((vec) ? W : 1), tpr, v, (vec) ? W : 1, norm_grad_kernel_rows<T, TW, tpr, v, vec>}
+    // Backward, likewise.  us: rows of 16-bit elements in 512 threads of 2 or 4 pieces or in
+    // 1024 of half as many, 8192 x 8192 87.6 and 91.5, 8192 x 12288 142 and 208, 8192 x 4096
+    // 47.7 and 47.4, 20000 x 1024 50.2 and 29.0; f32 8192 x 4096 89.4 and 72.0; element by
+    // element, 10 a thread or 5, 8191 x 2057 bf16 34.2 and 40.9, f32 42.2 and 48.9,
+    // 4097 x 4097 37.7 and 48.2.
+    constexpr int D = W == 8 ? 512 : 1024;
+#define BACKWARD(threads, across, v, vec) {(across) * (v) * ((vec) ? W : 1), threads, across, v, (vec) ? W : 1, norm_grad_kernel_rows<T, TW, threads, across, v, vec>}
     NormKernels k = {
         {{FORWARD(32, M, true), FORWARD(32, 4 * M, true), FORWARD(128, 2 * M, true), FORWARD(128, 4 * M, true),
-          FORWARD(256, 4 * M, true), FORWARD(512, 4 * M, true), FORWARD(1024, 2 * M, true)}},
-        {{BACKWARD(32, 1, true), BACKWARD(128, 1, true), BACKWARD(256, 1, true), BACKWARD(512, 1, true), BACKWARD(1024, 1, true),
-          BACKWARD(1024, 2, true)},
-         {BACKWARD(32, 5, false), BACKWARD(128, 5, false), BACKWARD(256, 5, false), BACKWARD(512, 5, false), BACKWARD(1024, 5, false),
-          BACKWARD(1024, 8, false)}},
+          FORWARD(256, 4 * M, true), FORWARD(512, 4 * M, true)}},
+        {{BACKWARD(1024, 32, 1, true), BACKWARD(1024, 128, 1, true), BACKWARD(1024, 256, 1, true), BACKWARD(1024, 512, 1, true),
+          BACKWARD(D, D, 1024 / D, true), BACKWARD(512, 512, 4, true)},
+         {BACKWARD(1024, 32, 5, false), BACKWARD(1024, 128, 5, false), BACKWARD(512, 128, 10, false), BACKWARD(512, 256, 10, false),
+          BACKWARD(512, 512, 10, false), BACKWARD(1024, 1024, 8, false)}},
         norm_kernel_long<T, TW>,
         norm_grad_kernel_long<T, TW>,
         norm_sums_kernel_long<T>,
