@@ -52,27 +52,23 @@ static const RouteKernel& route_kernel_for(int64_t experts)
     return *k;
 }
 
-// once per device: how many SMs it has; kernels that take more than 48 KB of shared memory are told so
-static ccl_status_t layer_device(int* sms)
+// once per device: kernels that take more than 48 KB of shared memory are told so
+static ccl_status_t layer_device()
 {
     static std::mutex mu;
-    static int known[64];
+    static bool known[64];
     int d = 0;
     TRY_CUDA(cudaGetDevice(&d), "cudaGetDevice");
     if (d < 0 || d >= 64) return fail(CCL_ERR_UNSUPPORTED, "device index above 63");
     std::lock_guard<std::mutex> lock(mu);
-    if (!known[d]) {
-        for (const RouteKernel& k : kRoute)
-            TRY_CUDA(cudaFuncSetAttribute(k.route, cudaFuncAttributeMaxDynamicSharedMemorySize, kRouteSmem),
-                     "shared memory of the router");
-        for (auto kernel : {place_kernel<true>, place_kernel<false>})
-            TRY_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRouteSmem),
-                     "shared memory of the row order");
-        int n = 0;
-        TRY_CUDA(cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, d), "SM count");
-        known[d] = n;
-    }
-    *sms = known[d];
+    if (known[d]) return CCL_OK;
+    for (const RouteKernel& k : kRoute)
+        TRY_CUDA(cudaFuncSetAttribute(k.route, cudaFuncAttributeMaxDynamicSharedMemorySize, kRouteSmem),
+                 "shared memory of the router");
+    for (auto kernel : {place_kernel<true>, place_kernel<false>})
+        TRY_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRouteSmem),
+                 "shared memory of the row order");
+    known[d] = true;
     return CCL_OK;
 }
 
@@ -166,8 +162,7 @@ static ccl_status_t route(const ccl_route_t* a, char* base, int64_t* need, cudaS
     R.renormalize = a->renormalize != 0;
     R.scored = a->bias || R.group_best == 2;
     R.scale = a->scale;
-    int sms;
-    TRY(layer_device(&sms));
+    TRY(layer_device());
     const int64_t each = 16 / element_bytes(a->dtype);
     R.vec = aligned16(a->logits) && ld % each == 0 && a->experts % each == 0;
     const RouteKernel& k = route_kernel_for(a->experts);
@@ -233,8 +228,7 @@ static ccl_status_t expert_order(const ccl_expert_order_t* a, char* base, int64_
     R.place = a->place;
     R.slots = a->slots;
     R.experts = a->experts;
-    int sms;
-    TRY(layer_device(&sms));
+    TRY(layer_device());
     R.per_block = (a->slots + R.blocks - 1) / R.blocks;
     if (R.blocks == 1) return launch(place_kernel<true>, dim3(1), kOrderThreads, order_smem(R.experts, kOrderThreads), stream, R);
     R.blocks = (int32_t)((a->slots + R.per_block - 1) / R.per_block);
@@ -272,8 +266,6 @@ static ccl_status_t route_grad(const ccl_route_grad_t* a, cudaStream_t stream)
     R.score = a->score;
     R.renormalize = a->renormalize != 0;
     R.scale = a->scale;
-    int sms;
-    TRY(layer_device(&sms));
     const int64_t each = 16 / es;
     R.vec = aligned16(a->logits) && ld % each == 0 && a->experts % each == 0;
     R.vec_d = aligned16(a->dlogits) && ldd % each == 0 && a->experts % each == 0;

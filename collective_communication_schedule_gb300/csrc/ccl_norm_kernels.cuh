@@ -39,7 +39,8 @@ NormKernels norm_kernels_of()
     // Forward, the narrowest that holds a row, with 2 to 4 pieces of 16 bytes a thread on
     // their way.  bf16, us with the next wider form instead: 20000 x 1024 12.8 and 22.1,
     // 8192 x 2048 11.7 and 13.8, 8192 x 4096 22.1 and 42.2 (in 512 threads of 2
-    // pieces; 8192 columns in them 29.2, in 256 threads of 4 23.0).
+    // pieces; 8192 columns in them 29.2, in 256 threads of 4 23.0), 1000 x 32768 33.9 and,
+    // read three times, 60.8.
     constexpr int W = Type<T>::kVec, M = 8 / W;
 #define FORWARD(tpr, v, vec) {(tpr) * (v) * ((vec) ? W : 1), (tpr) < 128 ? 128 : (tpr), (tpr) < 128 ? 128 / (tpr) : 1, norm_kernel_rows<T, TW, tpr, v, vec>}
 #define SHIFTED(tpr, v)                                                                                            \
@@ -54,7 +55,7 @@ NormKernels norm_kernels_of()
 #define BACKWARD(threads, across, v, vec) {(across) * (v) * ((vec) ? W : 1), threads, across, v, (vec) ? W : 1, norm_grad_kernel_rows<T, TW, threads, across, v, vec>}
     NormKernels k = {
         {{FORWARD(32, M, true), FORWARD(32, 4 * M, true), FORWARD(128, 2 * M, true), FORWARD(128, 4 * M, true),
-          FORWARD(256, 4 * M, true), FORWARD(512, 4 * M, true)}},
+          FORWARD(256, 4 * M, true), FORWARD(512, 4 * M, true), FORWARD(1024, 4 * M, true)}},
         {{BACKWARD(1024, 32, 1, true), BACKWARD(1024, 128, 1, true), BACKWARD(1024, 256, 1, true), BACKWARD(1024, 512, 1, true),
           BACKWARD(D, D, 1024 / D, true), BACKWARD(512, 512, 4, true)},
          {BACKWARD(1024, 32, 5, false), BACKWARD(1024, 128, 5, false), BACKWARD(512, 128, 10, false), BACKWARD(512, 256, 10, false),

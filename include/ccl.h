@@ -1031,8 +1031,8 @@ typedef struct {
  * ccl_linear_grad rounds dz (f16: scaled by a power of two so that the largest
  * |dloss|, |dloss + dlse| of a row is just below 2^14; it keeps what is down to
  * 2^-38 of that).  The vocabulary is taken in pieces whose dl fits 256 MB of the
- * workspace (1024 classes at least); dx is summed over pieces in 32 bits.  dx
- * or dw may be null; neither may overlap the other or an operand.
+ * workspace (1024 classes at least); dx is summed over pieces, and over segments of
+ * one, in 32 bits.  dx or dw may be null; neither may overlap the other or an operand.
  */
 typedef struct {
     int64_t rows, vocab, k;
