@@ -970,7 +970,7 @@ def combine(r, place, weights=None, residual=None, out=None, stream=None):
     device, dtype = r.device, r.dtype
     _graphless(r, weights, residual)
     handle = _handle(device)
-    rows = place.shape[0]
+    rows = place.shape[0] if place.dim() else 0
     where, k = _places(place, rows, device)
     a = Combine(rows, count, h, k, _type_code(dtype))
     a.place = where

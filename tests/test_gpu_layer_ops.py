@@ -420,6 +420,21 @@ def test_moves_without_places_or_rows(ccl):
     assert ccl.dispatch(x[:0], empty).shape == (0, 40) and ccl.combine(out, empty).shape == (0, 40)
 
 
+def test_shapes_that_disagree_are_refused(ccl):
+    x = torch.zeros(4, 8, device="cuda")
+    i, w = torch.zeros(4, 2, device="cuda", dtype=torch.int32), torch.zeros(4, 2, device="cuda")
+    for place in (i[0, 0], i[0], i[:3], i[None], i.long(), i.t().contiguous().t(), i.cpu()):
+        for call in (lambda: ccl.dispatch(x, place), lambda: ccl.combine_backward(x, x, place, w), lambda: ccl.combine(x, place, w)):
+            with pytest.raises(ValueError):
+                call()
+    for call in (lambda: ccl.combine(x, i, w, out=x[:, :7]), lambda: ccl.combine(x, i, w, residual=x[:3]),
+                 lambda: ccl.combine(x, i, w.t().contiguous().t()), lambda: ccl.dispatch(x, i, out=x[:, :7]),
+                 lambda: ccl.route_backward(w[:3], x, i), lambda: ccl.layer_norm(x, w[0]), lambda: ccl.layer_norm(x, out=x[:3]),
+                 lambda: ccl.layer_norm_backward(x, x, None, w[:, 0], w[:, 0]), lambda: ccl.route(x, 2, bias=w[0])):
+        with pytest.raises(ValueError):
+            call()
+
+
 def test_residual_in_place(ccl):
     g = gen(2)
     r, res = rnd(g, 60, 264, dtype=torch.bfloat16), rnd(g, 20, 264, dtype=torch.bfloat16)
