@@ -563,8 +563,13 @@ __global__ void __launch_bounds__(THREADS) norm_grad_kernel_rows(const Norm N)
                 }
             }
             if (c < n) {
+                if constexpr (VEC) {       // (n is a multiple of W)
 #pragma unroll
-                for (int e = 0; e < W; ++e) out[which * n + c + e] = v[e];
+                    for (int e = 0; e < W; e += 4)
+                        *reinterpret_cast<float4*>(out + which * n + c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                } else {
+                    out[which * n + c] = v[0];
+                }
             }
         }
 }
