@@ -10,7 +10,7 @@ namespace tensor {
 // that the order of the sums is.
 constexpr int kNormBlocks = 152;
 // Rows that the backward pass has on their way.  us with 1, 2 and 3: bf16 8192 x 4096
-// 60.3, 47.5 and 48.2, 8192 x 8192 124, 91.6 and 94.9, f32 8192 x 4096 110, 72.1 and 71.0.
+// 57.7, 42.2 and 44.8, 8192 x 8192 126, 81.2 and 81.9, f32 8192 x 4096 110, 71.1 and 70.5.
 constexpr int kRowsAhead = 2;
 
 struct Norm {
@@ -404,10 +404,11 @@ __device__ __forceinline__ float2 group_sums(float2 s, float* part, int group, i
 // one element, read a row ahead.
 //
 // Instructions bound it, about 300 of a warp a row for 8 elements a lane (the
-// schedulers issue in 7 cycles of 10): 8192 x 4096 bf16 47.5 us with dw and db
-// (4.2 TB/s), f32 with half as many elements in the same bytes 72 us (5.6 TB/s).
+// schedulers issue in 7 cycles of 10): 8192 x 4096 bf16 42 us with dw and db
+// (4.8 TB/s), f32 with half as many elements in the same bytes 71 us (5.7 TB/s).
 // Elements are unpacked twice instead of kept: 1024 threads have 64 registers each, of
-// which w, dw and db take 24.  Rows off 16 bytes: 8191 x 2057 bf16 34 us; columns belong
+// which w, dw and db take 24.  Few rows: 85 x 15656 14 us, of which the sums and their
+// way through memory take two thirds (dx alone 4.8).  Rows off 16 bytes: 8191 x 2057 bf16 34 us; columns belong
 // to threads, so rows cannot be taken by the pieces of 16 bytes that they touch.
 template <int T, int TW, int THREADS, int ACROSS, int V, bool VEC>
 __global__ void __launch_bounds__(THREADS) norm_grad_kernel_rows(const Norm N)
@@ -467,12 +468,18 @@ __global__ void __launch_bounds__(THREADS) norm_grad_kernel_rows(const Norm N)
     } else {
         fetch1(left > 0);
     }
-    float w[V][W], dw[V][W], db[V][W];
+    constexpr bool kHeld = !VEC || V * W <= 16;            // w in registers; else read for every row (from L1)
+    float held[kHeld ? V : 1][W], dw[V][W], db[V][W];
+    auto weights = [&](int i, float (&w)[W]) {
+#pragma unroll
+        for (int e = 0; e < W; ++e) w[e] = 1.f;
+        if (N.w && mine[i]) read<EW, VEC, W>((const typename EW::Raw*)N.w + (i * across + tid) * W, w);
+    };
 #pragma unroll
     for (int i = 0; i < V; ++i) {
 #pragma unroll
-        for (int e = 0; e < W; ++e) w[i][e] = 1.f, dw[i][e] = db[i][e] = 0.f;
-        if (N.w && mine[i]) read<EW, VEC, W>((const typename EW::Raw*)N.w + (i * across + tid) * W, w[i]);
+        for (int e = 0; e < W; ++e) dw[i][e] = db[i][e] = 0.f;
+        if (kHeld) weights(i, held[kHeld ? i : 0]);
     }
     const float *pm = N.mean + row, *pr = N.rstd + row;
     float next_mean = left > 0 ? *pm : 0.f, next_rstd = left > 0 ? *pr : 0.f;
@@ -501,12 +508,15 @@ __global__ void __launch_bounds__(THREADS) norm_grad_kernel_rows(const Norm N)
                     read<E, VEC, W>((const Raw*)(at + i * kPlace), xh[i]);
                     read<E, VEC, W>((const Raw*)(at + (V + i) * kPlace), g[i]);
                 }
+                float own[W];
+                if (!kHeld) weights(i, own);
+                const float (&w)[W] = kHeld ? held[kHeld ? i : 0] : own;
 #pragma unroll
                 for (int e = 0; e < W; ++e) {
                     xh[i][e] = (xh[i][e] - mean) * rstd;
                     dw[i][e] = fmaf(g[i][e], xh[i][e], dw[i][e]);
                     db[i][e] += g[i][e];
-                    g[i][e] *= w[i][e];
+                    g[i][e] *= w[e];
                     s.x += g[i][e];
                     s.y = fmaf(g[i][e], xh[i][e], s.y);
                 }
@@ -522,8 +532,11 @@ __global__ void __launch_bounds__(THREADS) norm_grad_kernel_rows(const Norm N)
                         asm volatile("" ::: "memory");
                         read<E, VEC, W>((const Raw*)(at + i * kPlace), xh[i]);
                         read<E, VEC, W>((const Raw*)(at + (V + i) * kPlace), g[i]);
+                        float own[W];
+                        if (!kHeld) weights(i, own);
+                        const float (&w)[W] = kHeld ? held[kHeld ? i : 0] : own;
 #pragma unroll
-                        for (int e = 0; e < W; ++e) xh[i][e] = (xh[i][e] - mean) * rstd, g[i][e] *= w[i][e];
+                        for (int e = 0; e < W; ++e) xh[i][e] = (xh[i][e] - mean) * rstd, g[i][e] *= w[e];
                     }
 #pragma unroll
                     for (int e = 0; e < W; ++e) g[i][e] = fmaf(xh[i][e], kb, fmaf(g[i][e], rstd, ka));

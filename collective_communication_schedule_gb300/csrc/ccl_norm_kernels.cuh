@@ -47,8 +47,8 @@ NormKernels norm_kernels_of()
     {(tpr) * (v) * W - (W - 1), kShiftedThreads, kShiftedThreads / (tpr), norm_kernel_shifted<T, TW, tpr, v>,          \
      shifted_blocks((v) * W), 8 * W * plane_of<W, tpr, v>(), kShiftedThreads * (v) * 16}
     // Backward, likewise.  us: rows of 16-bit elements in 512 threads of 2 or 4 pieces or in
-    // 1024 of half as many, 8192 x 8192 87.6 and 91.5, 8192 x 12288 142 and 208, 8192 x 4096
-    // 47.7 and 47.4, 20000 x 1024 50.2 and 29.0; f32 8192 x 4096 89.4 and 72.0; element by
+    // 1024 of half as many, 8192 x 8192 81.2 and 84.6, 8192 x 12288 133 and 248, 8192 x 4096
+    // 43.0 and 42.2, 20000 x 1024 28.8 and 27.7; f32 8192 x 4096 89.4 and 71.1; element by
     // element, 10 a thread or 5, 8191 x 2057 bf16 34.2 and 40.9, f32 42.2 and 48.9,
     // 4097 x 4097 37.7 and 48.2.
     constexpr int D = W == 8 ? 512 : 1024;
