@@ -125,8 +125,9 @@ __device__ __forceinline__ uint32_t keep_groups(const Route& R, const float (&v)
             }
         __syncwarp();
     }
+    // (a sum of open values stays above -inf, which marks a closed group: NaN stands as the lowest finite number)
     float from = fabsf(a);
-    if (R.group_best == 2 && b != -INFINITY) from += fabsf(b), a += b;
+    if (R.group_best == 2 && b != -INFINITY) from += fabsf(b), a = fmaxf(a + b, -3.402823466e38f);
     if (lane >= R.groups) a = -INFINITY;
     return best_groups(R, a, R.scored ? from : 0.f, lane, near, close);
 }
@@ -271,7 +272,7 @@ __device__ __noinline__ bool groups64(const Route& R, int64_t row, int lane, flo
     };
     if (at_a >= 0) {
         v = value(at_a);
-        if (at_b >= 0) v = R.group_best == 2 ? v + value(at_b) : fmax(v, value(at_b));
+        if (at_b >= 0) v = R.group_best == 2 ? fmax(v + value(at_b), -1.7976931348623157e308) : fmax(v, value(at_b));
     }
     bool close = false;
     kept = best_groups(R, v, 0., lane, 0., close);
@@ -305,7 +306,7 @@ __device__ __noinline__ int choose64(const Route& R, int64_t row, double* val, i
                 b = fmax(b, fmin(a, u));
                 a = fmax(a, u);
             }
-        if (R.group_best == 2 && b != -INFINITY) a += b;
+        if (R.group_best == 2 && b != -INFINITY) a = fmax(a + b, -1.7976931348623157e308);
         bool close = false;
         const uint32_t kept = best_groups(R, a, 0., lane, 0., close);
         __syncwarp();

@@ -871,15 +871,17 @@ ccl_status_t ccl_orthogonalize(const ccl_ortho_t* a, void* ws, int64_t ws_bytes,
  *   c = s + bias                      (bias: balance; it does not enter the weights)
  *   with groups > 1 (at most 32 of equal size): experts of one group are
  *     neighbours, a group's value is its largest c (group_best = 1) or the sum
- *     of its two largest (2), and only the top_groups best groups stay open
+ *     of its two largest (2; of a single open expert its c alone), and only the
+ *     top_groups best groups stay open
  *   chosen = the k largest c of open experts, descending
  *   weights = scale * s[chosen], or with renormalize scale * s / sum over the chosen of s
  * Ties go to the lower expert (and group).  The order is that of the exact c:
  * values that lie nearer to each other than 32 bits can tell are computed in 64.
  * An expert whose logit (or bias) is -Inf is closed; where fewer than k are
  * open, the choices that are left are -1 with weight 0 (a row of -Inf: all of
- * them).  A NaN ranks behind every number; with softmax it makes the row's
- * weights NaN.
+ * them).  A NaN ranks behind every number (without a bias beside a logit of the
+ * lowest f32) and in front of what is closed, and so does a group whose sum holds
+ * one; with softmax it makes the row's scores and weights NaN.
  * offsets and place (both or neither) are those of ccl_expert_order.
  */
 typedef struct {

@@ -232,6 +232,63 @@ def test_route_keeps_choices_sound_with_nan_and_inf(ccl):
     check_route(ccl, low, 4, 0, renorm=True)
 
 
+def choices_with_nan(l, k, score, bias, groups, top):
+    """Choices in 64 bits by groups of two largest values, a NaN being the lowest finite number, and so a sum below it."""
+    low = torch.finfo(torch.float64).min
+    l = l.double()
+    rows, e = l.shape
+    p = torch.sigmoid(l) if score else torch.softmax(l, 1)
+    c = p + bias.double() if bias is not None else p
+    c = torch.where(l == -INF, -INF, torch.where(c.isnan(), low, c))
+    s = c.view(rows, groups, e // groups).sort(2, descending=True).values
+    v = s[..., 0] + torch.where(s[..., 1] == -INF, 0.0, s[..., 1])
+    v = torch.where(s[..., 0] == -INF, -INF, v.clamp(min=low))
+    kept = torch.sort(v, dim=1, descending=True, stable=True).indices[:, :top]
+    open_ = torch.zeros_like(v, dtype=torch.bool).scatter_(1, kept, True).repeat_interleave(e // groups, 1)
+    if bias is None:
+        c = torch.where(l == -INF, -INF, torch.where(l.isnan(), low, l))
+    v, at = torch.sort(torch.where(open_, c, -INF), dim=1, descending=True, stable=True)
+    return torch.where(v[:, :k] == -INF, -1, at[:, :k])
+
+
+@pytest.mark.parametrize("score", [0, 1], ids=["softmax", "sigmoid"])
+@pytest.mark.parametrize("e,groups", [(64, 8), (60, 4), (256, 8), (96, 32), (1024, 16)])
+def test_route_groups_of_nan_or_lowest_values_stay_open(ccl, e, groups, score):
+    """A group whose two best are NaN, or as low as a type goes, is behind the others but in front of a closed one."""
+    g = gen(e)
+    size = e // groups
+    k = min(4, 2 * size)
+    logits = rnd(g, 60, e)
+    for row in range(60):
+        own = logits[row].view(groups, size)
+        if row % 5 == 1:
+            own[groups - 1, 0] = math.nan                                  # one: with softmax all scores are NaN
+        elif row % 5 == 2:
+            own[1:] = math.nan
+        elif row % 5 == 3:
+            own[1:, 1:] = math.nan                                         # one number a group
+        elif row % 5 == 4:
+            own[2:] = math.nan                                             # one group of numbers
+        own[0] = -INF
+        if row % 2:
+            own[groups - 1, -1] = -INF
+    lowest = torch.full((e,), -3.4028234663852886e38, device="cuda")
+    some = rnd(g, e, scale=0.1)
+    some[size:2 * size] = lowest[0]
+    for bias in (None, rnd(g, e, scale=0.1), some, lowest):
+        for top in (1, 2, groups - 1):
+            if top * size < k:
+                continue
+            want = choices_with_nan(logits, k, score, bias, groups, top)
+            w, chosen, offsets, place = ccl.route(logits, k, score=score, bias=bias, groups=groups, top_groups=top, group_best=2,
+                                                  order=True)
+            assert torch.equal(chosen.long(), want)
+            assert bool((chosen[chosen >= 0] >= size).all()) and bool((chosen[:, 0] >= 0).all())
+            assert bool((w[chosen < 0] == 0).all())
+            at, where = order64(want, e)
+            assert torch.equal(offsets.cpu().long(), at) and torch.equal(place.cpu().long(), where)
+
+
 @pytest.mark.parametrize("dtype", TYPES, ids=IDS)
 @pytest.mark.parametrize("score", [0, 1], ids=["softmax", "sigmoid"])
 @pytest.mark.parametrize("renorm", [False, True], ids=["as they are", "renormalised"])
