@@ -463,6 +463,68 @@ def test_rows_of_any_stride(ccl, lead, pitch, dtype):
     check_moves(ccl, 50, 3, 264, dtype, lead=lead, pitch=pitch)
 
 
+def check_many_choices(ccl, rows, k, h, dtype, lead=0, pitch=0):
+    """Gradients of more choices of short rows than are taken a warp each.  A lane has 8 products at most, then up to 5
+    additions over the lanes of a row."""
+    g = gen(rows + h)
+    count = rows * k + 5
+    place = some_places(g, rows, k, count, 0.2)
+    dy = rnd(g, rows, h + lead + pitch, dtype=dtype)[:, lead:lead + h]
+    r = rnd(g, count, h + lead + pitch, dtype=dtype)[:, lead:lead + h]
+    live = place >= 0
+    at = place[live].long()
+    named = torch.zeros(count, dtype=torch.bool, device="cuda")
+    named[at] = True
+    r[~named] = math.nan
+    weights = rnd(g, rows, k)
+    held = torch.full((count + 2, h + lead + pitch), 9.0, dtype=dtype, device="cuda")
+    dr = held[1:-1, lead:lead + h]
+    out, dw = ccl.combine_backward(dy, r, place, weights, out=dr)
+    assert out is dr
+    want = torch.full((count, h), 9.0, dtype=torch.float64, device="cuda")
+    want[at] = (weights.double()[..., None] * dy.double()[:, None])[live]
+    close(dr, want, 2.0 ** -24 * want.abs())
+    assert bool((dr[~named] == 9).all())
+    terms = torch.where(live[..., None], r.double()[place.clamp(min=0).long()], 0.0) * dy.double()[:, None]
+    close(dw, terms.sum(2), 13 * 2.0 ** -24 * terms.abs().sum(2))
+    assert not dw[~live].any()
+    only = ccl.combine_backward(dy, r, place, weights, need_dr=False)
+    assert only[0] is None and torch.equal(only[1], dw)
+    only = ccl.combine_backward(dy, r, place, None, need_dweights=False)
+    assert only[1] is None and torch.equal(only[0][at], dy[:, None].expand(rows, k, h)[live])
+    only = ccl.combine_backward(dy, r, place, weights, need_dweights=False)
+    assert only[1] is None and torch.equal(only[0][at], dr[at])
+    dr.fill_(9)
+    assert bool((held == 9).all())
+    ccl.tensor_status()
+    # places out of range do as much as none, and are reported
+    bad, none = place.clone(), place.clone()
+    for t, j, p in ((0, 0, count), (rows // 2, k - 1, 2 ** 31 - 1), (rows - 1, k - 1, count + 1)):
+        bad[t, j], none[t, j] = p, -1
+    want = ccl.combine_backward(dy, r, none, weights, out=torch.full_like(want, 9.0, dtype=dtype))
+    ccl.tensor_status()
+    got = ccl.combine_backward(dy, r, bad, weights, out=dr)
+    with pytest.raises(ccl.CclError, match="place"):
+        ccl.tensor_status()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("rows,k,h", [(2731, 7, 8), (5501, 3, 24), (16387, 1, 40), (1030, 16, 128), (2731, 7, 128), (520, 32, 256),
+                                      (5501, 3, 256), (2731, 7, 136)])
+def test_gradients_of_many_short_rows(ccl, rows, k, h, dtype):
+    """1 to 32 lanes a row, some of them beyond its end, and last groups of one to four choices."""
+    if h * torch.finfo(dtype).bits // 8 > 512:
+        h = 128
+    check_many_choices(ccl, rows, k, h, dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("lead,pitch", [(0, 8), (8, 8), (1, 0), (3, 5)])
+def test_gradients_of_many_short_rows_of_any_stride(ccl, lead, pitch, dtype):
+    check_many_choices(ccl, 2731, 7, 72, dtype, lead, pitch)
+
+
 def test_moves_without_places_or_rows(ccl):
     x = rnd(gen(1), 6, 40, dtype=torch.bfloat16)
     none = torch.full((6, 2), -1, dtype=torch.int32, device="cuda")
