@@ -698,6 +698,29 @@ def test_layer_norm_strides_and_in_place(ccl, t):
         assert bool((held == 7).all())
 
 
+SHIFTED = [(15000, 131), (15000, 517), (3700, 2057), (1900, 4097), (1400, 9001)]
+
+
+@pytest.mark.parametrize("t,tw", NORM_TYPES[1:], ids=NORM_IDS[1:])
+@pytest.mark.parametrize("rows,n", SHIFTED)
+def test_layer_norm_of_more_rows_off_16_bytes_than_are_taken_at_once(ccl, rows, n, t, tw):
+    """Three turns of every group of threads, each with another distance to 16 bytes, y at the distance of x or not."""
+    g = gen(n)
+    x = rnd(g, rows, n, dtype=t) + rnd(g, rows, 1, dtype=t)
+    w, b = rnd(g, n, dtype=tw), rnd(g, n, dtype=tw)
+    y = check_norm(ccl, x, w, b)[0]
+    for lead, pitch in ((1, 0), (0, 4), (5, 3)):
+        held = torch.full((rows + 2, n + lead + pitch), 7.0, dtype=t, device="cuda")
+        out = held[1:-1, lead:lead + n]
+        assert ccl.layer_norm(x, w, b, out=out) is out and torch.equal(out, y)
+        out.copy_(x)
+        want = check_norm(ccl, out, w, b)[0]
+        ccl.layer_norm(out, w, b, out=out)
+        assert torch.equal(out, want)
+        out.fill_(7.0)
+        assert bool((held == 7).all())
+
+
 def check_norm_grad(ccl, dy, x, w, mean, rstd, tw, bias=True):
     rows, n = x.shape
     got = ccl.layer_norm_backward(dy, x, w, mean, rstd, bias=bias)
@@ -736,6 +759,24 @@ def test_layer_norm_backward(ccl, rows, n, t, tw):
     assert only[0] is None and only[1] is None and torch.equal(only[2], got[2])
     alone = ccl.layer_norm_backward(dy, x, w, mean, rstd, need_dw=False)
     assert torch.equal(alone[0], got[0]) and alone[1] is None
+
+
+@pytest.mark.parametrize("t,tw", NORM_TYPES, ids=NORM_IDS)
+@pytest.mark.parametrize("rows,n", [(15000, 64), (15000, 131), (3700, 517), (3700, 1000), (1900, 1101), (1900, 2000),
+                                    (1000, 2057), (500, 4097), (470, 7001), (470, 8192), (470, 12288), (470, 16384)])
+def test_layer_norm_backward_of_more_rows_than_are_taken_at_once(ccl, rows, n, t, tw):
+    """Three turns and a part of one of every group of threads, by elements and by 16 bytes."""
+    g = gen(n)
+    for lead in (0, 3) if n % 8 == 0 and n < 5000 else (0,):
+        x, dy = (rnd(g, rows, n + lead, dtype=t)[:, lead:] for _ in range(2))
+        w = rnd(g, n, dtype=tw)
+        mean, rstd, _, _ = norm64(x, w, None, 1e-5)
+        mean, rstd = mean[:, 0].float(), rstd[:, 0].float()
+        got = check_norm_grad(ccl, dy, x, w, mean, rstd, tw)
+        alone = ccl.layer_norm_backward(dy, x, w, mean, rstd, need_dw=False)
+        assert torch.equal(alone[0], got[0])
+        sums = ccl.layer_norm_backward(dy, x, w, mean, rstd, bias=True, need_dx=False)
+        assert torch.equal(sums[1], got[1]) and torch.equal(sums[2], got[2])
 
 
 def test_layer_norm_backward_of_views(ccl):
