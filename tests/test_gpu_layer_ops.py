@@ -232,6 +232,19 @@ def test_route_keeps_choices_sound_with_nan_and_inf(ccl):
     check_route(ccl, low, 4, 0, renorm=True)
 
 
+@pytest.mark.parametrize("dtype", TYPES[:2], ids=IDS[:2])
+@pytest.mark.parametrize("rows,e,k,groups,top", [(11000, 64, 6, 1, 1), (11000, 256, 8, 8, 4), (11000, 384, 3, 1, 1), (6000, 512, 8, 16, 4),
+                                                 (6000, 1000, 5, 1, 1)])
+def test_route_more_rows_than_warps(ccl, rows, e, k, groups, top, dtype):
+    """With the order, a warp takes a second row and more, and its choices count with those of the block."""
+    g = gen(rows + e)
+    logits = rnd(g, rows, e, dtype=dtype, scale=1.5)
+    for score, bias in ((0, None), (1, rnd(g, e, scale=0.05))):
+        w, chosen, _, _ = check_route(ccl, logits, k, score, bias, groups, top, min(2, groups))
+        alone = ccl.route(logits, k, score=score, bias=bias, groups=groups, top_groups=top, group_best=min(2, groups))
+        assert torch.equal(alone[0], w) and torch.equal(alone[1], chosen)
+
+
 def choices_with_nan(l, k, score, bias, groups, top):
     """Choices in 64 bits by groups of two largest values, a NaN being the lowest finite number, and so a sum below it."""
     low = torch.finfo(torch.float64).min
