@@ -116,6 +116,21 @@ def test_loss(ccl, rows, vocab, k, dtype):
 
 
 @pytest.mark.parametrize("dtype", DT, ids=IDS)
+@pytest.mark.parametrize("rows,vocab,k", [(1, 40001, 8), (32, 40001, 72), (33, 40001, 72), (100, 40000, 40), (128, 45001, 64),
+                                          (129, 40001, 72), (200, 60000, 40), (256, 60001, 136)])
+def test_loss_of_few_rows_over_several_tiles(ccl, rows, vocab, k, dtype):
+    """More tiles than SMs, all rows in each of them: statistics are carried from one tile to the next."""
+    g = gen(rows + vocab)
+    x, w, t = make(g, rows, vocab, k, dtype)
+    t[0] = vocab - 1
+    t[-1] = 0 if rows > 1 else vocab - 1
+    loss, lse = check_loss(ccl, x, w, t)
+    other = check_loss(ccl, x, w, t.int())
+    assert torch.equal(other[0], loss) and torch.equal(other[1], lse)
+    check_grad(ccl, x, w, t, rnd(g, rows) / rows, rnd(g, rows) / rows, lse)
+
+
+@pytest.mark.parametrize("dtype", DT, ids=IDS)
 @pytest.mark.parametrize("rows,vocab,k", SIZES)
 def test_loss_backward(ccl, rows, vocab, k, dtype):
     g = gen(rows + vocab)
