@@ -23,7 +23,7 @@ SOURCES = ["ccl_runtime.cu", "ccl_static.cu", "ccl_tensor.cu", "ccl_layer.cu", "
 # device headers the run-time compiler of generated kernels receives as text
 EMBEDDED = ["ccl_layout.h", "ccl_core.cuh"]
 HEADERS = ["ccl_internal.h", "ccl_plan.h", "ccl_layout.h", "ccl_core.cuh", "ccl_tensor.cuh", "ccl_tensor_ortho.cuh",
-           "ccl_tensor_passes.cuh", "ccl_tensor_product.cuh", "ccl_tensor_host.h", "ccl_tensor_launch.cuh",
+           "ccl_tensor_passes.cuh", "ccl_tensor_grad.cuh", "ccl_tensor_product.cuh", "ccl_tensor_host.h", "ccl_tensor_launch.cuh",
            "ccl_layer_common.cuh", "ccl_route.cuh", "ccl_rows.cuh", "ccl_norm.cuh", "ccl_norm_kernels.cuh", "ccl_loss.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -23,11 +23,10 @@ static ccl_status_t loss_device(const Device** out)
     if (!all[d].ready) {
         TRY(look_up(&all[d], d));
         for (auto kernel : {rowwise_kernel<1, STATS>, rowwise_kernel<2, STATS>, rowwise_kernel<1, SLOPE>, rowwise_kernel<2, SLOPE>,
-                            rowwise_kernel<1, STATS_TURNED>, rowwise_kernel<2, STATS_TURNED>, rowwise_kernel<1, SLOPE_TURNED>,
-                            rowwise_kernel<2, SLOPE_TURNED>})
+                            rowwise_kernel<1, STATS_TURNED>, rowwise_kernel<1, SLOPE_TURNED>})
             TRY_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBudget),
                      "shared memory of the rowwise kernel");
-        TRY_CUDA(cudaFuncSetAttribute(sum_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBudget),
+        TRY_CUDA(cudaFuncSetAttribute(sum_pairs<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBudget),
                  "shared memory of the pair kernel");
         all[d].ready = true;
     }
@@ -68,14 +67,13 @@ static Product values_of(int mode, int64_t rows, int64_t vocab, int64_t k, bool 
     }
     return P;
 }
-// Parts of a row's statistics: by tile, or by cluster (turned: by threadblock)
-// where one tile holds all rows.
+// Parts of a row's statistics: by tile, or by cluster where one tile holds all rows.
 static int64_t parts_of(const Product& P, const Shape& sh, bool turned, int sms, bool* whole)
 {
     const int64_t across = (P.m + sh.cg * kTileM - 1) / (sh.cg * kTileM), along = (P.n + sh.bn - 1) / sh.bn;
     *whole = turned || across == 1;
     if (!*whole) return along;
-    return std::min<int64_t>(across * along, sms / sh.cg) * (turned ? sh.cg : 1);
+    return std::min<int64_t>(across * along, sms / sh.cg);
 }
 
 // mode: STATS or SLOPE
@@ -90,10 +88,10 @@ static ccl_status_t run_rowwise(const Device* dev, int mode, Rowwise* R, const S
     const int bytes = (kTileM + sh.bn / sh.cg) * kSliceK * 2, fixed = 1024 + kStagingBytes;
     R->p.stages = std::min(kMaxStages, (kSmemBudget - fixed) / bytes);
     const int clusters = std::min(R->p.total, std::min(dev->sms, kShapeSms) / sh.cg);
-    void (*const kernels[2][2][2])(Rowwise) = {
-        {{rowwise_kernel<1, STATS>, rowwise_kernel<2, STATS>}, {rowwise_kernel<1, STATS_TURNED>, rowwise_kernel<2, STATS_TURNED>}},
-        {{rowwise_kernel<1, SLOPE>, rowwise_kernel<2, SLOPE>}, {rowwise_kernel<1, SLOPE_TURNED>, rowwise_kernel<2, SLOPE_TURNED>}}};
-    return launch(kernels[mode == SLOPE][turned][sh.cg - 1], dim3((unsigned)(clusters * sh.cg)), kThreads,
+    // lanes along x: single threadblocks or pairs; turned: single ones
+    void (*const kernels[2][3])(Rowwise) = {{rowwise_kernel<1, STATS>, rowwise_kernel<2, STATS>, rowwise_kernel<1, STATS_TURNED>},
+                                            {rowwise_kernel<1, SLOPE>, rowwise_kernel<2, SLOPE>, rowwise_kernel<1, SLOPE_TURNED>}};
+    return launch(kernels[mode == SLOPE][turned ? 2 : sh.cg - 1], dim3((unsigned)(clusters * sh.cg)), kThreads,
                   fixed + (size_t)R->p.stages * bytes, stream, *R, sh.cg);
 }
 
@@ -350,7 +348,7 @@ static ccl_status_t cross_entropy_grad(const ccl_cross_entropy_grad_t* a, char* 
         const int bytes = (kTileM + S.width / 2) * kSliceK * 2, fixed = 1024 + kStagingBytes;
         S.stages = std::min(kMaxStages, (kSmemBudget - fixed) / bytes);
         const int clusters = (int)std::min<int64_t>(most, dev->sms / 2);
-        TRY(launch(sum_pair_kernel, dim3((unsigned)(clusters * 2)), kThreads, fixed + (size_t)S.stages * bytes, stream, S, 2));
+        TRY(launch(sum_pairs<2>, dim3((unsigned)(clusters * 2)), kThreads, fixed + (size_t)S.stages * bytes, stream, S, 2));
     }
     if (sum) {
         LossSum Q = {sum, (uint16_t*)a->dx, a->rows, a->k, ld_sum, a->rows * ld_sum, lddx, dxs.parts, bf};

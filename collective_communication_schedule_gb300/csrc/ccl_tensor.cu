@@ -8,6 +8,7 @@
 
 #include <cuda_runtime.h>
 
+#include "ccl_tensor_grad.cuh"
 #include "ccl_tensor_launch.cuh"
 #include "ccl_tensor_ortho.cuh"
 

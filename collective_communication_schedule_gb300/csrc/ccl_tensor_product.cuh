@@ -1001,6 +1001,7 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
                 }
                 if constexpr (MODE == STATS_TURNED || MODE == SLOPE_TURNED) {
                     // lanes are rows of w, columns the rows of x
+                    static_assert(CG == 1, "few rows want single threadblocks");
                     const Rowwise& R = *seq.rows;
                     const bool own = f < P.m;
                     const float scale = MODE == SLOPE_TURNED ? *R.scale : 0.f;
@@ -1043,15 +1044,9 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
                         __syncwarp();
                     }
                     fence_before();
-                    if (lane == 0 && good) {
-                        if (CG == 2)
-                            bar_arrive_cluster(release[acc]);
-                        else
-                            bar_arrive(release[acc]);
-                    }
+                    if (lane == 0 && good) bar_arrive(release[acc]);
                     if (MODE == STATS_TURNED && t + clusters >= run.end) {
-                        // after the last tile, the warps of the same rows put their parts together, and so do the two
-                        // threadblocks of a pair by writing a part each
+                        // after the last tile, the warps of the same rows put their parts together
                         float2* parts = reinterpret_cast<float2*>(staging) + slot * kBlockRows + (lane & 15);
                         if (lane < kBlockRows) {
                             parts[quad * kTileM] = so_far2[0];
@@ -1065,7 +1060,7 @@ __device__ __forceinline__ void products(const Sequence<MODE> seq)
                             float2 part = so_far2[j];
 #pragma unroll
                             for (int i = 1; i < 4; ++i) part = join(part, parts[i * kTileM + j * kStride]);
-                            R.part[(int64_t)(cluster * size + rank) * P.n + c] = part;
+                            R.part[(int64_t)cluster * P.n + c] = part;
                         }
                     }
                     ++done;
@@ -1272,13 +1267,12 @@ __global__ void __launch_bounds__(kThreads, 1) pair_kernel(const __grid_constant
 {
     products<CG, A_MN, PAIR>({{&P}});
 }
-// (a template all the same: one definition in every translation unit that asks for it)
+// (a template, as the rest: compiled where it is launched)
 template <int CG>
 __global__ void __launch_bounds__(kThreads, 1) sum_pairs(const __grid_constant__ Pair P)
 {
     products<CG, A_MN, SUM_PAIR>({{&P}});
 }
-constexpr auto sum_pair_kernel = sum_pairs<2>;
 template <int CG, int MODE>
 __global__ void __launch_bounds__(kThreads, 1) rowwise_kernel(const __grid_constant__ Rowwise R)
 {
