@@ -15,7 +15,7 @@ struct NormKernels {
         int64_t width;             // elements of the longest row
         int threads, rows;         // of a threadblock
         void (*kernel)(const Norm);
-        int blocks;                // of an SM, which take rows in turn; 0: as many as the rows need
+        int blocks;                // an SM in the grid, which take rows in turn; 0: as many as the rows need
         int smem, stage;           // bytes of shared memory, and where rows of y lie apart
     };
     struct Backward {
@@ -50,7 +50,11 @@ NormKernels norm_kernels_of()
     // 1024 of half as many, 8192 x 8192 81.2 and 84.6, 8192 x 12288 133 and 248, 8192 x 4096
     // 43.0 and 42.2, 20000 x 1024 28.8 and 27.7; f32 8192 x 4096 89.4 and 71.1; element by
     // element, 10 a thread or 5, 8191 x 2057 bf16 34.2 and 40.9, f32 42.2 and 48.9,
-    // 4097 x 4097 37.7 and 48.2.
+    // 4097 x 4097 37.7 and 48.2.  The last form of single elements, 8 for each of 1024
+    // threads with 64 registers, spills 290 bytes a thread (4097 x 7001 bf16 123 us, 1.4
+    // TB/s), those of 5 for 1024 threads 40 to 48.  Wider rows, f32 and single elements
+    // from 8193 columns on and 16-bit ones from 16385, are read three times by
+    // elements: f32 4096 x 8192 65 us (6.2 TB/s), 4096 x 8196 151 (2.7), 2048 x 16384 147.
     constexpr int D = W == 8 ? 512 : 1024;
 #define BACKWARD(threads, across, v, vec) {(across) * (v) * ((vec) ? W : 1), threads, across, v, (vec) ? W : 1, norm_grad_kernel_rows<T, TW, threads, across, v, vec>}
     NormKernels k = {

@@ -280,8 +280,8 @@ __device__ __noinline__ bool groups64(const Route& R, int64_t row, int lane, flo
 }
 
 // A row's choices all in 64 bits, for values of a group or more candidates than
-// lanes too near to each other (rare: values in shared memory, so that the
-// common way keeps its registers).
+// lanes too near to each other (rare: a call, with the row's values in shared
+// memory).
 __device__ __noinline__ int choose64(const Route& R, int64_t row, double* val, int lane)
 {
     const int E = R.experts;
@@ -397,8 +397,9 @@ __device__ __forceinline__ void store_row(typename E::Raw* p, int at, int n, boo
 // for groups by the sum of two) values are computed in 32 bits with an error
 // bound: two values nearer than `near` may be in the wrong order.  Where that is so
 // for neighbours in the order, all that lie within `near` of the k-th are ordered
-// again in 64 bits, about one row in a hundred; where it is so for the groups at
-// the border, or for more than 32 candidates, the whole row is.
+// again in 64 bits, about one row in a thousand (6 to 9 of 8190 rows of 256 experts
+// with a bias); where it is so for the groups at the border, their values are, and
+// where that cannot decide, or for more than 32 candidates, the whole row.
 //   sigmoid, in units of 2^-22: 2^(-l log2 e) within 1 of itself, of which
 //     s (1 - s) <= 1/4 reaches s; its argument within 1/4 of itself, of which
 //     |l| s (1 - s) < 0.23 does; the sum 1/4 and the reciprocal 1/2 of s: less than
@@ -522,7 +523,7 @@ __device__ __forceinline__ void route_row(const Route& R, int64_t row, double* v
     const bool on = expert >= 0;
     float w;
     if (!R.renormalize) {
-        w = !softmax ? sigmoid32(own) : expf(own - most) / sum;
+        w = !softmax ? sigmoid32(own) : expf(own - most) / sum;       // (the sum, of exponentials within 2^-22, is within 2^-18)
     } else if (softmax) {
         const float top = warp_max(on ? own : -INFINITY);
         w = on ? expf(own - top) : 0.f;
@@ -659,14 +660,16 @@ __device__ __forceinline__ void leave_counts(const Route& R, const int32_t* coun
         R.hist[(int64_t)blockIdx.x * width + e] = e < R.experts ? counts[e] : 0;
 }
 
-// Threads that a block of the router may have: more than 64 registers a thread
-// are needed from 16 experts a lane on.
+// Threads that a block of the router may have.  With 1024 of them, 64 registers
+// each, the kernels spill from 3 experts a lane on: 4 to 36 bytes a thread up to 6, 88
+// for 8 and 196 for 12; with 512, 148 for 32.
 constexpr int route_threads(int vpl) { return vpl < 16 ? 1024 : 512; }
 
 // A warp a row, a threadblock `per_block` consecutive rows.
 //
-// Instructions bound it, about 1290 a row of 256 experts with bias and groups, and
-// the schedulers issue in 6 cycles of 10.  8190 rows choose 8 of 256 f32: by logits
+// Instructions bound it, about 1290 a row of 256 experts with bias and groups, some
+// of them spills and next to none of them rows in 64 bits, and the schedulers issue in
+// 6 cycles of 10.  8190 rows choose 8 of 256 f32: by logits
 // alone 9.7 us, in groups 11.7, by sigmoids with a bias 12.5, both 16, and with the
 // order of the rows 22; the bytes alone would take 1.4.  A warp a row keeps scores in
 // registers, so that a choice is one maximum over the warp; for one row (64

@@ -125,10 +125,11 @@ __global__ void __launch_bounds__(256) dispatch_kernel(const Moves M)
 }
 
 // y[t] = sum_j w[t, j] r[place[t, j]] (+ residual[t]), in 32 bits, j ascending.  A
-// warp takes a part of a token, four choices' loads on their way at a time (a
-// thread's place and weight come from L1).  Bytes read bound it, 8190 rows of 2048 bf16
-// from 4 places 33 us, 5.1 TB/s; for few rows the chain of place, row and launch
-// does: 24 rows from 8 places 3.6 us.
+// warp takes a part of a token, its choices one after another (places and weights
+// come from L1): the 32 registers of a thread do not hold the loads of four choices,
+// and a choice without a place is a branch between two of them.  8190 rows of 2048 bf16
+// from 4 places 33 us, 5.1 TB/s, where dispatch writes at 6.4: too few loads on their way.
+// Few rows are bound by the chain of place, row and launch: 24 rows from 8 places 3.6 us.
 template <int T, bool VEC>
 __global__ void __launch_bounds__(256) combine_kernel(const Moves M)
 {
@@ -221,9 +222,11 @@ __global__ void __launch_bounds__(256) combine_grad_short_kernel(const Moves M)
 
 // The same for rows of any length.  A warp takes a choice; neighbouring warps take choices of one token, whose dy is
 // read once from memory and by the others from L1.  x: dy, out: dr (either output
-// may be null).  Bytes bound it: 8190 rows of 2048 bf16 at 4 places 54 us (5.6 TB/s),
-// 4097 rows of 1544 f16 at 6 places, a fifth of them none, 30 us (4.5 TB/s): its rows
-// share lines of 128 bytes with their neighbours.
+// may be null).  8190 rows of 2048 bf16 at 4 places 54 us (5.6 TB/s).  dr may lie
+// anywhere, so a step's loads wait for the stores of the step before, and with a step
+// for less than a warp or choices without a place there is less on its way: f16, 4097
+// rows at 6 places, 1536 wide (6 steps) 32.5 us (5.0 TB/s), 1544 (a seventh for one lane)
+// 34.6 (4.8), and with a fifth of the places none 28.9 (4.6) and 30.8 (4.4).
 template <int T, bool VEC>
 __global__ void __launch_bounds__(256) combine_grad_kernel(const Moves M)
 {

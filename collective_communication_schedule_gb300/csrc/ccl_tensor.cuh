@@ -358,7 +358,7 @@ __device__ __forceinline__ void store8(uint16_t* p, bool bf, int n, const float 
 // u = sqrt(2/pi) (z + 0.044715 z^3); silu is z sigmoid(z).  In 32 bits.
 enum { ACT_NONE = 0, ACT_RELU = 1, ACT_GELU = 2, ACT_SILU = 3 };
 
-// 1 / (1 + 2^(-x log2 e)): two approximate instructions, each within 2^-22
+// 1 / (1 + 2^(-x log2 e)): two approximate instructions, the exponential within 2^-22 and the reciprocal within 2^-23
 __device__ __forceinline__ float sigmoid(float x)
 {
     float e, r;

@@ -547,9 +547,14 @@ __device__ __forceinline__ float2 stats_blocks(float2 s, uint32_t from, int firs
     return s;
 }
 
-// The same walk for dl = a exp(value - log-sum) - b [column = target], rounded
-// to 16 bits.  A row that counts for nothing (a = b = 0) gives 0 whatever its
-// values are.  All blocks of the tile (at most 4 of a warp) are held before any
+// The same walk for dl = a exp(value - log-sum) - b [column = target], in 32 bits
+// and rounded to the element type: dl is an operand of two products, and the matrix
+// instructions take no 32-bit operands (tf32, at half the rate, has the digits of
+// f16).  That rounding is all that dx and dw lose against 32 bits throughout: they
+// lie 2.0e-3 from 64 bits instead of 1.7e-3 (relative, root of mean squares; bf16,
+// 4096 x 65536 x 4096) and 3.1e-4 instead of 2.1e-4 (f16, 777 x 32003 x 1032); 1.7e-3
+// and 2.1e-4 are the rounding of the results.  A row that counts for nothing
+// (a = b = 0) gives 0 whatever its values are.  All blocks of the tile (at most 4 of a warp) are held before any
 // is stored: the accumulator is handed back in between, and that would wait for
 // the stores.
 constexpr int kMostBlocks = 256 / (kEpilogueWarps / 4 * kBlockRows);
