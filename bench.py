@@ -1098,6 +1098,26 @@ def run_hier_allgather(args):
         print(json.dumps(rec), flush=True)
 
 
+# What the record holds beside the benchmark's line, by its part of the record.
+DETAILS = {None: ("per_collective", "sweep", "codegen"), "roofline": ("kernels", "traffic_unit", "traffic_basis"),
+           "e2e": ("host_link_before_gbs",), "cpu_baseline": ("sample",)}
+
+
+def report(out):
+    """The benchmark's one line, short enough for a log's tail, on stdout; all
+    that was measured beside it as a line on stderr."""
+    line, details = dict(out), {}
+    for part, names in DETAILS.items():
+        held = line if part is None else dict(line.get(part) or {})
+        found = {n: held.pop(n) for n in names if n in held}
+        if part is None:
+            details.update(found)
+        elif found:
+            line[part], details[part] = held, found
+    print(json.dumps({"details": details}), file=sys.stderr, flush=True)
+    print(json.dumps(line), flush=True)
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--gpus", type=int, default=1)
@@ -1161,12 +1181,12 @@ def main():
         dist.init_process_group("nccl")
         res = combine_replicas(run_gpu(args), world, device="cuda")
         if rank == 0:
-            print(json.dumps(res))
+            report(res)
         dist.destroy_process_group()
         return
     import torch
     torch.cuda.set_device(0)
-    print(json.dumps(run_gpu(args)))
+    report(run_gpu(args))
 
 
 if __name__ == "__main__":

@@ -111,3 +111,27 @@ def test_committed_sweep_tables_plan_on_their_schedules(kind):
             o.channels = ch
             st = s.check(ce, 1, opts=o)
             assert st.nthreadblocks <= 2 * 152
+
+
+def test_the_line_is_short_and_whole(capsys):
+    """What goes to stdout is one JSON line without the tables, which go to stderr; nothing is lost on the way."""
+    import json
+    out = {"metric": "m", "value": 1.5, "unit": "GB/s", "config": {"workload": "w" * 300}, "clocks": {"sm_mhz": 2070.0},
+           "gpu_launches": 160, "collective_min_bytes_gbs": 4288.8, "per_collective": [{"us": 1.0}] * 100,
+           "sweep": {"rows": [{"us": 2.0}] * 900}, "codegen": [{"row": "ag_3m"}] * 9,
+           "roofline": {"frac": 0.9, "kernels": ["k"] * 40, "traffic": 5, "traffic_unit": "u", "traffic_basis": "b" * 300},
+           "e2e": {"value": 3.0, "h2d_bytes_per_step": 7, "d2h_bytes_per_step": 8, "host_link_before_gbs": {"h2d": 1}},
+           "cpu_baseline": {"value": 3.0, "sample": "s" * 300}}
+    want = json.loads(json.dumps(out))
+    bench.report(out)
+    assert out == want
+    got = capsys.readouterr()
+    assert got.out.count("\n") == 1 and len(got.out) < 2000
+    line, rest = json.loads(got.out), json.loads(got.err)["details"]
+    assert line["value"] == 1.5 and line["e2e"]["d2h_bytes_per_step"] == 8 and line["roofline"]["frac"] == 0.9
+    for part in list(rest):
+        if isinstance(rest[part], dict) and part in line:
+            line[part].update(rest.pop(part))
+    assert line | rest == want
+    bench.report({"value": 1.0, "metric": "m"})                    # a run without the tables
+    assert json.loads(capsys.readouterr().out) == {"value": 1.0, "metric": "m"}
